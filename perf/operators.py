@@ -409,11 +409,13 @@ def _run_own(s, c, kind):
                 "dx": fb.dispatch_tokens_bwd(s["drows_in"], s["slot_row"])}
     if kind == "norm_fwd":
         return list(fb.norm_fwd(s["x"], s["y"], s["w_post"], s["w_pre"], gate=s["gate"],
+                                gate_kind=None if s["gate"] is None else c["gate"],
                                 sigmoid=s["sigmoid"], residual_scale=s["residual_scale"],
                                 branch_scale=s["branch_scale"], eps=EPS))
     if kind == "norm_bwd":
         return list(fb.norm_bwd(s["dr"], s["dh"], s["r"], s["y"], s["w_post"], s["w_pre"],
                                 s["rstd_post"], s["rstd_pre"], gate=s["gate"],
+                                gate_kind=None if s["gate"] is None else c["gate"],
                                 sigmoid=s["sigmoid"], residual_scale=s["residual_scale"],
                                 branch_scale=s["branch_scale"]))
     if kind == "mxfp4":
