@@ -28,10 +28,14 @@ OP_GMM_DLHS_FP8 = 3
 OP_TGMM_DRHS_QUANT = 4
 OP_GMM_BF16_FWD = 5
 OP_GMM_FP8_FWD_BLOCK = 7
+OP_GMM_MXFP4_FWD = 8
+OP_GMM_SILU_MXFP4_FWD = 9
+OP_NORM_BWD = 10
 
 STATUS_NEGATIVE_GROUP = 0x1
 STATUS_GROUPS_EXCEED_M = 0x2
 STATUS_WAIT_TIMEOUT = 0x4
+STATUS_BAD_EXPERT = 0x10
 
 # every symbol include/fp8moe.h declares
 EXPORTS = [
@@ -43,7 +47,10 @@ EXPORTS = [
     "fp8moe_gmm_dlhs_dswiglu_fp8", "fp8moe_gmm_dlhs_dswiglu_fp8_path",
     "fp8moe_tgmm_drhs_quant_fmt", "fp8moe_tgmm_quantize_tiles_fmt",
     "fp8moe_gmm_fp8_fwd_block", "fp8moe_quantize_rows_block", "fp8moe_selftest_wait_timeout",
-    "fp8moe_selftest_cast_f32",
+    "fp8moe_selftest_cast_f32", "fp8moe_sort_tokens", "fp8moe_dispatch_tokens",
+    "fp8moe_combine_tokens", "fp8moe_combine_tokens_bwd", "fp8moe_norm_fwd", "fp8moe_norm_bwd",
+    "fp8moe_mxfp4_quantize_rows", "fp8moe_mxfp4_quantize_weights", "fp8moe_mxfp4_dequantize",
+    "fp8moe_gmm_mxfp4_fwd", "fp8moe_gmm_silu_mxfp4_fwd",
 ]
 
 FMT = {"e4m3": 0, "e5m2": 1}
@@ -73,6 +80,7 @@ def load(build_if_missing: bool = True):
             _build.build()
         L = ctypes.CDLL(path)
         P, I64, I32, SZ = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int32, ctypes.c_size_t
+        F32 = ctypes.c_float
         sig = {
             "fp8moe_workspace_size": ([I32, I64, I64, I64, I32], SZ),
             "fp8moe_gmm_fp8_fwd": ([P, I64, I64, P, P, I32, I64, P, P, P, SZ, P], I32),
@@ -100,6 +108,19 @@ def load(build_if_missing: bool = True):
             "fp8moe_quantize_rows_block": ([P, I64, I64, P, I32, I32, P, P, P], I32),
             "fp8moe_selftest_wait_timeout": ([ctypes.c_uint32, P], I32),
             "fp8moe_selftest_cast_f32": ([P, I64, I32, P, P], I32),
+            "fp8moe_sort_tokens": ([P, I64, I32, I32, I64, P, P, P, P], I32),
+            "fp8moe_dispatch_tokens": ([P, P, I64, I32, I64, I32, I32, I64, P, P, P, P, P], I32),
+            "fp8moe_combine_tokens": ([P, I64, I64, I32, P, P, I64, I32, P, P], I32),
+            "fp8moe_combine_tokens_bwd": ([P, P, I64, I64, I32, P, P, I64, I32, P, P, P], I32),
+            "fp8moe_norm_fwd": ([P, P, I64, I64, I32, P, P, P, I32, I32, F32, F32, F32, P, P, P, P,
+                                 P], I32),
+            "fp8moe_norm_bwd": ([P, P, P, P, I64, I64, I32, P, P, P, P, P, I32, I32, F32, F32, P, P,
+                                 P, P, P, P, SZ, P], I32),
+            "fp8moe_mxfp4_quantize_rows": ([P, I64, I64, P, I32, P, P, P], I32),
+            "fp8moe_mxfp4_quantize_weights": ([P, I32, I64, I64, P, P, P], I32),
+            "fp8moe_mxfp4_dequantize": ([P, P, I32, I64, I64, P, P], I32),
+            "fp8moe_gmm_mxfp4_fwd": ([P, I64, I64, P, P, I32, I64, P, P, P, SZ, P], I32),
+            "fp8moe_gmm_silu_mxfp4_fwd": ([P, I64, I64, P, P, I32, I64, P, P, P, SZ, P], I32),
         }
         for name, (args, res) in sig.items():
             fn = getattr(L, name)
@@ -425,6 +446,308 @@ def selftest_cast_f32(x, fmt: str = "e4m3", codes=None):
     _check(load().fp8moe_selftest_cast_f32(_ptr(x), x.numel(), FMT[fmt], _ptr(codes),
                                            _stream(x.device)), "fp8moe_selftest_cast_f32")
     return codes
+
+
+TYPES = {torch.bfloat16: 0, torch.float32: 1}
+GATES = {"token": 1, "channel": 2, "full": 3}
+
+
+def _rows_type(t: torch.Tensor, name: str) -> int:
+    if isinstance(t, torch.Tensor) and t.dtype not in TYPES:
+        raise TypeError(f"{name} must be torch.bfloat16 or torch.float32, got {t.dtype}")
+    return TYPES[t.dtype] if isinstance(t, torch.Tensor) else 0
+
+
+def _like(out, shape, dtype, device, name: str):
+    """A given output, checked, or a new one."""
+    if out is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    _req(out, dtype, name, len(shape))
+    if tuple(out.shape) != tuple(shape):
+        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(out.shape)}")
+    return out
+
+
+def _sort_outputs(ids, num_experts: int, M: int):
+    T, k = ids.shape
+    i32, dev = torch.int32, ids.device
+    return (torch.empty(num_experts, dtype=i32, device=dev),
+            torch.empty(T, k, dtype=i32, device=dev), torch.empty(M, dtype=i32, device=dev))
+
+
+def sort_tokens(ids, num_experts: int, M: Optional[int] = None):
+    """The router's choices ids int32 [T, topk] sorted by expert: (group_sizes [E],
+    slot_row [T, topk], row_slot [M]), all int32 (see fp8moe_sort_tokens). M: rows
+    of the sorted buffer, T * topk by default."""
+    L = load()
+    _req(ids, torch.int32, "ids", 2)
+    T, k = ids.shape
+    M = T * k if M is None else int(M)
+    gs, slot_row, row_slot = _sort_outputs(ids, num_experts, M)
+    _check(L.fp8moe_sort_tokens(_ptr(ids), T, k, num_experts, M, _ptr(gs), _ptr(slot_row),
+                                _ptr(row_slot), _stream(ids.device)), "fp8moe_sort_tokens")
+    return gs, slot_row, row_slot
+
+
+def dispatch_tokens(x, ids, num_experts: int, M: Optional[int] = None, out=None):
+    """x [T, H] (bf16 or f32) copied to its tokens' rows, sorted by expert:
+    (rows [M, H], group_sizes, slot_row, row_slot) (see fp8moe_dispatch_tokens).
+    Rows past the last group's are not written."""
+    L = load()
+    ty = _rows_type(x, "x")
+    _req(x, x.dtype if isinstance(x, torch.Tensor) else None, "x", 2)
+    _req(ids, torch.int32, "ids", 2)
+    T, H = x.shape
+    if ids.shape[0] != T:
+        raise ValueError("shape mismatch")
+    k = ids.shape[1]
+    M = T * k if M is None else int(M)
+    out = _like(out, (M, H), x.dtype, x.device, "out")
+    gs, slot_row, row_slot = _sort_outputs(ids, num_experts, M)
+    _check(L.fp8moe_dispatch_tokens(_ptr(x), _ptr(ids), T, k, H, ty, num_experts, M, _ptr(out),
+                                    _ptr(gs), _ptr(slot_row), _ptr(row_slot), _stream(x.device)),
+           "fp8moe_dispatch_tokens")
+    return out, gs, slot_row, row_slot
+
+
+def combine_tokens(rows, slot_row, weights=None, out=None):
+    """out [T, H] = sum_j weights[t, j] * rows[slot_row[t, j]] in f32, weights f32
+    [T, topk] or None for ones (see fp8moe_combine_tokens)."""
+    L = load()
+    ty = _rows_type(rows, "rows")
+    _req(rows, rows.dtype if isinstance(rows, torch.Tensor) else None, "rows", 2)
+    _req(slot_row, torch.int32, "slot_row", 2)
+    M, H = rows.shape
+    T, k = slot_row.shape
+    if weights is not None:
+        _req(weights, torch.float32, "weights", 2)
+        if weights.shape != slot_row.shape:
+            raise ValueError("shape mismatch")
+    out = _like(out, (T, H), rows.dtype, rows.device, "out")
+    _check(L.fp8moe_combine_tokens(_ptr(rows), M, H, ty, _ptr(slot_row), _ptr(weights), T, k,
+                                   _ptr(out), _stream(rows.device)), "fp8moe_combine_tokens")
+    return out
+
+
+def dispatch_tokens_bwd(drows, slot_row, out=None):
+    """Gradient of dispatch_tokens with respect to x [T, H]: the sum of a token's
+    rows' gradients."""
+    return combine_tokens(drows, slot_row, None, out)
+
+
+def combine_tokens_bwd(dout, rows, slot_row, weights, out=None):
+    """Gradient of combine_tokens: (drows [M, H], dweights f32 [T, topk]) (see
+    fp8moe_combine_tokens_bwd). Rows of drows that no slot names are not written."""
+    L = load()
+    ty = _rows_type(rows, "rows")
+    _req(rows, rows.dtype if isinstance(rows, torch.Tensor) else None, "rows", 2)
+    _req(dout, rows.dtype, "dout", 2)
+    _req(slot_row, torch.int32, "slot_row", 2)
+    _req(weights, torch.float32, "weights", 2)
+    M, H = rows.shape
+    T, k = slot_row.shape
+    if dout.shape != (T, H) or weights.shape != slot_row.shape:
+        raise ValueError("shape mismatch")
+    out = _like(out, (M, H), rows.dtype, rows.device, "out")
+    dweights = torch.empty(T, k, dtype=torch.float32, device=rows.device)
+    _check(L.fp8moe_combine_tokens_bwd(_ptr(dout), _ptr(rows), M, H, ty, _ptr(slot_row),
+                                       _ptr(weights), T, k, _ptr(out), _ptr(dweights),
+                                       _stream(rows.device)), "fp8moe_combine_tokens_bwd")
+    return out, dweights
+
+
+def _gate(gate, kind: Optional[str], T: int, H: int, dtype):
+    """The gate's kind number and the shape and type that it (and its gradient) has."""
+    if (gate is None) != (kind is None):
+        raise ValueError("gate and gate_kind go together")
+    if gate is None:
+        return 0, None, None
+    if kind not in GATES:
+        raise ValueError(f"gate_kind must be one of {sorted(GATES)}, got {kind!r}")
+    shape = {"token": (T,), "channel": (H,), "full": (T, H)}[kind]
+    ty = dtype if kind == "full" else torch.float32
+    _req(gate, ty, "gate", len(shape))
+    if tuple(gate.shape) != shape:
+        raise ValueError(f"a gate per {kind} must have shape {shape}, got {tuple(gate.shape)}")
+    return GATES[kind], shape, ty
+
+
+def _norm_weight(w, H: int, name: str):
+    if w is not None:
+        _req(w, torch.float32, name, 1)
+        if w.shape[0] != H:
+            raise ValueError(f"{name} must have shape ({H},), got {tuple(w.shape)}")
+
+
+def norm_fwd(x, y=None, w_post=None, w_pre=None, gate=None, gate_kind: Optional[str] = None,
+             sigmoid: bool = False, residual_scale: float = 1.0, branch_scale: float = 1.0,
+             eps: float = 1e-6):
+    """The norms after and before a block with its gate and the scaled residual sum:
+        r = residual_scale * x + branch_scale * g * (w_post * rmsnorm(y))
+        h = w_pre * rmsnorm(r)
+    Returns (r, h, rstd_post, rstd_pre); without y and w_post r is x and returned as
+    None, without w_pre h and rstd_pre are None. gate_kind: "token" (f32 [T]),
+    "channel" (f32 [H]) or "full" ([T, H] of x's type); sigmoid passes the gate
+    through one (see fp8moe_norm_fwd)."""
+    L = load()
+    ty = _rows_type(x, "x")
+    _req(x, x.dtype if isinstance(x, torch.Tensor) else None, "x", 2)
+    T, H = x.shape
+    post, pre = w_post is not None, w_pre is not None
+    if (y is not None) != post:
+        raise ValueError("y and w_post go together")
+    if not post and (gate is not None or residual_scale != 1.0 or branch_scale != 1.0):
+        raise ValueError("a gate or a scale needs y and w_post")
+    if post:
+        _req(y, x.dtype, "y", 2)
+        if y.shape != x.shape:
+            raise ValueError("shape mismatch")
+    _norm_weight(w_post, H, "w_post")
+    _norm_weight(w_pre, H, "w_pre")
+    kind, _, _ = _gate(gate, gate_kind, T, H, x.dtype)
+    f32 = torch.float32
+    r = torch.empty_like(x) if post else None
+    h = torch.empty_like(x) if pre else None
+    rstd_post = torch.empty(T, dtype=f32, device=x.device) if post else None
+    rstd_pre = torch.empty(T, dtype=f32, device=x.device) if pre else None
+    _check(L.fp8moe_norm_fwd(_ptr(x), _ptr(y), T, H, ty, _ptr(w_post), _ptr(w_pre), _ptr(gate),
+                             kind, int(bool(sigmoid)), residual_scale, branch_scale, eps, _ptr(r),
+                             _ptr(h), _ptr(rstd_post), _ptr(rstd_pre), _stream(x.device)),
+           "fp8moe_norm_fwd")
+    return r, h, rstd_post, rstd_pre
+
+
+def norm_bwd(dr, dh, r, y=None, w_post=None, w_pre=None, rstd_post=None, rstd_pre=None, gate=None,
+             gate_kind: Optional[str] = None, sigmoid: bool = False, residual_scale: float = 1.0,
+             branch_scale: float = 1.0, workspace=None):
+    """Gradient of norm_fwd: (dx, dy, dw_post, dw_pre, dgate), None for what the
+    forward did not have. dr: the residual stream's gradient of r (None: zero); dh:
+    of h; r: the forward's r, or its x when it had no y (see fp8moe_norm_bwd)."""
+    L = load()
+    like = dr if dr is not None else dh
+    if like is None:
+        raise ValueError("dr or dh must be given")
+    ty = _rows_type(like, "dr" if dr is not None else "dh")
+    _req(like, like.dtype if isinstance(like, torch.Tensor) else None,
+         "dr" if dr is not None else "dh", 2)
+    T, H = like.shape
+    dt, dev, f32 = like.dtype, like.device, torch.float32
+    post, pre = w_post is not None, w_pre is not None
+    if (y is not None) != post or (rstd_post is not None) != post:
+        raise ValueError("y, w_post and rstd_post go together")
+    if (dh is not None) != pre or (rstd_pre is not None) != pre or (pre and r is None):
+        raise ValueError("dh, w_pre, rstd_pre and r go together")
+    if not post and (gate is not None or residual_scale != 1.0 or branch_scale != 1.0):
+        raise ValueError("a gate or a scale needs y and w_post")
+    for t, name in ((dr, "dr"), (dh, "dh"), (r if pre else None, "r"), (y, "y")):
+        if t is not None:
+            _req(t, dt, name, 2)
+            if t.shape != (T, H):
+                raise ValueError(f"{name} must have shape {(T, H)}, got {tuple(t.shape)}")
+    for t, name in ((rstd_post, "rstd_post"), (rstd_pre, "rstd_pre")):
+        if t is not None:
+            _req(t, f32, name, 1)
+            if t.shape[0] != T:
+                raise ValueError(f"{name} must have shape ({T},), got {tuple(t.shape)}")
+    _norm_weight(w_post, H, "w_post")
+    _norm_weight(w_pre, H, "w_pre")
+    kind, gshape, gtype = _gate(gate, gate_kind, T, H, dt)
+    dx = torch.empty(T, H, dtype=dt, device=dev)
+    dy = torch.empty(T, H, dtype=dt, device=dev) if post else None
+    dw_post = torch.empty(H, dtype=f32, device=dev) if post else None
+    dw_pre = torch.empty(H, dtype=f32, device=dev) if pre else None
+    dgate = torch.empty(gshape, dtype=gtype, device=dev) if kind else None
+    ws, wsb = _workspace(OP_NORM_BWD, T, H, 0, 0, dev, workspace)
+    _check(L.fp8moe_norm_bwd(_ptr(dr), _ptr(dh), _ptr(r) if pre else None, _ptr(y), T, H, ty,
+                             _ptr(w_post), _ptr(w_pre), _ptr(rstd_post), _ptr(rstd_pre),
+                             _ptr(gate), kind, int(bool(sigmoid)), residual_scale, branch_scale,
+                             _ptr(dx), _ptr(dy), _ptr(dw_post), _ptr(dw_pre), _ptr(dgate), _ptr(ws),
+                             wsb, _stream(dev)), "fp8moe_norm_bwd")
+    return dx, dy, dw_post, dw_pre, dgate
+
+
+def mxfp4_words(K: int) -> int:
+    """32-bit scale words of a row: one for every 128 values along K."""
+    return (K + 127) // 128
+
+
+def mxfp4_quantize_rows(lhs, group_sizes):
+    """Parity export of the 4-bit products' activation quantization: codes u8
+    [M, K/2] and scales u8 [ceil(K/128), M, 4] for rows < T (others zero)."""
+    L = load()
+    _req(lhs, torch.bfloat16, "lhs", 2)
+    _req(group_sizes, torch.int32, "group_sizes", 1)
+    M, K = lhs.shape
+    codes = torch.zeros(M, K // 2, dtype=torch.uint8, device=lhs.device)
+    scales = torch.zeros(mxfp4_words(K), M, 4, dtype=torch.uint8, device=lhs.device)
+    _check(L.fp8moe_mxfp4_quantize_rows(_ptr(lhs), M, K, _ptr(group_sizes), group_sizes.numel(),
+                                        _ptr(codes), _ptr(scales), _stream(lhs.device)),
+           "fp8moe_mxfp4_quantize_rows")
+    return codes, scales
+
+
+def mxfp4_quantize_weights(w):
+    """Expert weights bf16 [E, K, N] as MXFP4 with blocks along K: codes u8
+    [E, N, K/2] and scales u8 [E, ceil(K/128), N, 4] (see
+    fp8moe_mxfp4_quantize_weights)."""
+    L = load()
+    _req(w, torch.bfloat16, "w", 3)
+    E, K, N = w.shape
+    codes = torch.empty(E, N, K // 2, dtype=torch.uint8, device=w.device)
+    scales = torch.empty(E, mxfp4_words(K), N, 4, dtype=torch.uint8, device=w.device)
+    _check(L.fp8moe_mxfp4_quantize_weights(_ptr(w), E, K, N, _ptr(codes), _ptr(scales),
+                                           _stream(w.device)), "fp8moe_mxfp4_quantize_weights")
+    return codes, scales
+
+
+def _mxfp4_weight(codes, scales):
+    _req(codes, torch.uint8, "codes", 3)
+    _req(scales, torch.uint8, "scales", 4)
+    E, N, half = codes.shape
+    K = 2 * half
+    if tuple(scales.shape) != (E, mxfp4_words(K), N, 4):
+        raise ValueError("shape mismatch")
+    return E, K, N
+
+
+def mxfp4_dequantize(codes, scales, out=None):
+    """bf16 [E, N, K] of MXFP4 weights: K contiguous, so that as the weight of
+    gmm_bf16_fwd it gives a product's activation gradient (see
+    fp8moe_mxfp4_dequantize)."""
+    L = load()
+    E, K, N = _mxfp4_weight(codes, scales)
+    out = _like(out, (E, N, K), torch.bfloat16, codes.device, "out")
+    _check(L.fp8moe_mxfp4_dequantize(_ptr(codes), _ptr(scales), E, N, K, _ptr(out),
+                                     _stream(codes.device)), "fp8moe_mxfp4_dequantize")
+    return out
+
+
+def _mxfp4_fwd(lhs, codes, scales, group_sizes, out, workspace, silu: bool):
+    L = load()
+    _req(lhs, torch.bfloat16, "lhs", 2)
+    _req(group_sizes, torch.int32, "group_sizes", 1)
+    E, K, N = _mxfp4_weight(codes, scales)
+    M, K2 = lhs.shape
+    if K2 != K or group_sizes.numel() != E:
+        raise ValueError("shape mismatch")
+    out = _like(out, (M, N // 2 if silu else N), torch.bfloat16, lhs.device, "out")
+    op = OP_GMM_SILU_MXFP4_FWD if silu else OP_GMM_MXFP4_FWD
+    ws, wsb = _workspace(op, M, K, N, E, lhs.device, workspace)
+    fn = L.fp8moe_gmm_silu_mxfp4_fwd if silu else L.fp8moe_gmm_mxfp4_fwd
+    _check(fn(_ptr(lhs), M, K, _ptr(codes), _ptr(scales), E, N, _ptr(group_sizes), _ptr(out),
+              _ptr(ws), wsb, _stream(lhs.device)), fn.__name__)
+    return out
+
+
+def gmm_mxfp4_fwd(lhs, codes, scales, group_sizes, out=None, workspace=None):
+    """Grouped product of 4-bit weights with the rows quantised to 4 bits: bf16
+    [M, N] (see fp8moe_gmm_mxfp4_fwd)."""
+    return _mxfp4_fwd(lhs, codes, scales, group_sizes, out, workspace, silu=False)
+
+
+def gmm_silu_mxfp4_fwd(lhs, codes, scales, group_sizes, out=None, workspace=None):
+    """The same with fused SwiGLU: bf16 [M, N/2] (see fp8moe_gmm_silu_mxfp4_fwd)."""
+    return _mxfp4_fwd(lhs, codes, scales, group_sizes, out, workspace, silu=True)
 
 
 def read_status(device=None) -> int:

@@ -71,14 +71,14 @@ size_t round_up(size_t x, size_t a) { return (x + a - 1) / a * a; }
 
 int64_t segment_bound(int64_t M, int32_t E) { return (M + 127) / 128 + E; }
 
-// rank-2 or rank-3 tiled tensor map; dims[0] is the contiguous one.
+// rank-2 to rank-5 tiled tensor map; dims[0] is the contiguous one.
 int make_tmap(CUtensorMap* m, CUtensorMapDataType dt, int rank, const void* base,
               const uint64_t* dims, const uint64_t* strides_bytes, const uint32_t* box,
               CUtensorMapSwizzle sw) {
-  cuuint64_t gd[3];
-  cuuint64_t gs[2];
-  cuuint32_t bx[3];
-  cuuint32_t es[3] = {1, 1, 1};
+  cuuint64_t gd[5];
+  cuuint64_t gs[4];
+  cuuint32_t bx[5];
+  cuuint32_t es[5] = {1, 1, 1, 1, 1};
   for (int i = 0; i < rank; ++i) {
     gd[i] = dims[i];
     bx[i] = box[i];
@@ -260,6 +260,133 @@ int tgmm_quantize_impl(const void* lhs, const void* dout, int64_t M, int64_t K, 
   return FP8MOE_OK;
 }
 
+// ---- tokens sorted by expert, norms around the block, MXFP4
+
+bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
+
+// Bytes per element of a row type, 0 if it is not one.
+int type_bytes(int32_t type) {
+  return type == FP8MOE_TYPE_BF16 ? 2 : type == FP8MOE_TYPE_F32 ? 4 : 0;
+}
+
+int check_route(int64_t T, int32_t topk, int64_t M) {
+  if (T < 0 || M < 0 || M >= (int64_t(1) << 31)) return FP8MOE_EINVAL;
+  if (topk < 1 || topk > 32 || T >= (int64_t(1) << 31) / topk) return FP8MOE_EINVAL;
+  return FP8MOE_OK;
+}
+
+// Row length and type; *nvec receives the 16-byte vectors of a row.
+int check_row(int64_t H, int32_t type, int* nvec) {
+  const int b = type_bytes(type);
+  if (!b || H <= 0 || H >= (int64_t(1) << 31)) return FP8MOE_EINVAL;
+  if (H * b % 16 != 0) return FP8MOE_EALIGN;
+  *nvec = (int)(H * b / 16);
+  return FP8MOE_OK;
+}
+
+int sort_impl(const int32_t* ids, int64_t T, int32_t topk, int32_t E, int64_t M,
+              int32_t* group_sizes, int32_t* slot_row, int32_t* row_slot, cudaStream_t stream,
+              int* sms) {
+  int rc = check_route(T, topk, M);
+  if (rc) return rc;
+  if (E < 1 || E > 1024 || !group_sizes || (T > 0 && (!ids || !slot_row))) return FP8MOE_EINVAL;
+  if (!aligned4(ids) || !aligned4(group_sizes) || !aligned4(slot_row) || !aligned4(row_slot))
+    return FP8MOE_EALIGN;
+  rc = device_init(sms);
+  if (rc) return rc;
+  cudaError_t e = fp8moe_launch_sort_tokens(ids, T * topk, E, M, group_sizes, slot_row, row_slot,
+                                            stream);
+  return e == cudaSuccess ? FP8MOE_OK : cuda_fail(e);
+}
+
+int check_norm(int64_t T, int64_t H, int32_t type, int32_t gate_kind, int32_t sigmoid) {
+  int nvec = 0;
+  if (T < 0 || T >= (int64_t(1) << 31)) return FP8MOE_EINVAL;
+  int rc = check_row(H, type, &nvec);
+  if (rc) return rc;
+  if (nvec > 2048) return FP8MOE_EINVAL;     // H * element size <= 32768
+  if (gate_kind < FP8MOE_GATE_NONE || gate_kind > FP8MOE_GATE_FULL) return FP8MOE_EINVAL;
+  if (sigmoid != 0 && sigmoid != 1) return FP8MOE_EINVAL;
+  return FP8MOE_OK;
+}
+
+size_t norm_bwd_ws_bytes(int64_t T, int64_t H) {
+  return (size_t)3 * (size_t)fp8moe_norm_bwd_ctas(T) * (size_t)H * sizeof(float);
+}
+
+int64_t mxfp4_words(int64_t K) { return (K + 127) / 128; }
+
+size_t mxfp4_ws_bytes(int64_t M, int64_t K) {
+  return round_up((size_t)M * (size_t)(K / 2), 256) +
+         round_up((size_t)M * (size_t)mxfp4_words(K) * 4, 256);
+}
+
+int check_mxfp4(int64_t M, int64_t K, int64_t N, int32_t E) {
+  int rc = check_common(M, K, N, E);
+  if (rc) return rc;
+  return K % 32 != 0 ? FP8MOE_EALIGN : FP8MOE_OK;
+}
+
+int gmm_mxfp4_impl(const void* lhs, int64_t M, int64_t K, const uint8_t* codes,
+                   const uint8_t* scales, int32_t E, int64_t N, const int32_t* gs, void* out,
+                   void* ws, size_t ws_bytes, cudaStream_t stream, int swiglu) {
+  int rc = check_mxfp4(M, K, N, E);
+  if (rc) return rc;
+  if (swiglu && N % 32 != 0) return FP8MOE_EALIGN;
+  if (M == 0) return FP8MOE_OK;
+  if (!lhs || !codes || !scales || !gs || !out) return FP8MOE_EINVAL;
+  if (!ws) return FP8MOE_EWORKSPACE;
+  if (!aligned16(lhs) || !aligned16(codes) || !aligned16(scales) || !aligned16(out) ||
+      (reinterpret_cast<uintptr_t>(ws) & 255u) || !aligned4(gs))
+    return FP8MOE_EALIGN;
+  if (ws_bytes < mxfp4_ws_bytes(M, K)) return FP8MOE_EWORKSPACE;
+  int sms = 0;
+  rc = device_init(&sms);
+  if (rc) return rc;
+  uint8_t* const qx = static_cast<uint8_t*>(ws);
+  uint8_t* const sx = qx + round_up((size_t)M * (size_t)(K / 2), 256);
+  const uint64_t kb = (uint64_t)K / 2;
+  GmmMxfp4Args a;
+  if (swiglu) {
+    const uint64_t F = (uint64_t)N / 2;
+    const uint64_t dims[5] = {kb, 16, 2, F / 16, (uint64_t)E};
+    const uint64_t st[4] = {kb, F * kb, 16 * kb, (uint64_t)N * kb};
+    const uint32_t box[5] = {128, 16, 2, 4, 1};
+    rc = make_tmap(&a.tmW, CU_TENSOR_MAP_DATA_TYPE_UINT8, 5, codes, dims, st, box,
+                   CU_TENSOR_MAP_SWIZZLE_128B);
+  } else {
+    const uint64_t dims[3] = {kb, (uint64_t)N, (uint64_t)E};
+    const uint64_t st[2] = {kb, (uint64_t)N * kb};
+    const uint32_t box[3] = {128, 128, 1};
+    rc = make_tmap(&a.tmW, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, codes, dims, st, box,
+                   CU_TENSOR_MAP_SWIZZLE_128B);
+  }
+  if (rc) return rc;
+  int rows[3];
+  fp8moe_gmm_mxfp4_boxes(rows);
+  for (int i = 0; i < 3; ++i) {
+    const uint64_t dims[2] = {kb, (uint64_t)M};
+    const uint64_t st[1] = {kb};
+    const uint32_t box[2] = {128, (uint32_t)rows[i]};
+    rc = make_tmap(&a.tmX[i], CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, qx, dims, st, box,
+                   CU_TENSOR_MAP_SWIZZLE_128B);
+    if (rc) return rc;
+  }
+  a.sw = scales;
+  a.sx = sx;
+  a.gs = gs;
+  a.out = out;
+  a.M = M;
+  a.K = (int)K;
+  a.N = (int)N;
+  a.E = E;
+  a.swiglu = swiglu;
+  cudaError_t e = fp8moe_launch_mxfp4_quantize_rows(lhs, M, (int)K, gs, E, qx, sx, sms, 1, stream);
+  if (e != cudaSuccess) return cuda_fail(e);
+  e = fp8moe_launch_gmm_mxfp4(a, sms, stream);
+  return e == cudaSuccess ? FP8MOE_OK : cuda_fail(e);
+}
+
 }  // namespace
 
 extern "C" {
@@ -274,6 +401,11 @@ size_t fp8moe_workspace_size(int op, int64_t M, int64_t K, int64_t N, int32_t E)
       return tgmm_ws_bytes(M, K, N, E);
     case FP8MOE_OP_GMM_FP8_FWD_BLOCK:
       return fwd_block_ws_bytes(M, K);
+    case FP8MOE_OP_GMM_MXFP4_FWD:
+    case FP8MOE_OP_GMM_SILU_MXFP4_FWD:
+      return mxfp4_ws_bytes(M, K);
+    case FP8MOE_OP_NORM_BWD:
+      return norm_bwd_ws_bytes(M, K);
     default:
       return 0;
   }
@@ -623,13 +755,204 @@ int fp8moe_selftest_cast_f32(const float* x, int64_t n, int32_t fmt, uint8_t* co
   return FP8MOE_OK;
 }
 
+int fp8moe_sort_tokens(const int32_t* ids, int64_t T, int32_t topk, int32_t E, int64_t M,
+                       int32_t* group_sizes, int32_t* slot_row, int32_t* row_slot,
+                       fp8moe_stream_t stream) {
+  int sms = 0;
+  return sort_impl(ids, T, topk, E, M, group_sizes, slot_row, row_slot, stream, &sms);
+}
+
+int fp8moe_dispatch_tokens(const void* x, const int32_t* ids, int64_t T, int32_t topk, int64_t H,
+                           int32_t type, int32_t E, int64_t M, void* rows, int32_t* group_sizes,
+                           int32_t* slot_row, int32_t* row_slot, fp8moe_stream_t stream) {
+  int nvec = 0, sms = 0;
+  int rc = check_route(T, topk, M);
+  if (rc) return rc;
+  rc = check_row(H, type, &nvec);
+  if (rc) return rc;
+  if (T > 0 && M > 0 && (!x || !rows)) return FP8MOE_EINVAL;
+  if (!aligned16(x) || !aligned16(rows)) return FP8MOE_EALIGN;
+  rc = sort_impl(ids, T, topk, E, M, group_sizes, slot_row, row_slot, stream, &sms);
+  if (rc) return rc;
+  if (T == 0 || M == 0) return FP8MOE_OK;
+  cudaError_t e = fp8moe_launch_dispatch(x, T, topk, nvec, slot_row, M, rows, sms, stream);
+  return e == cudaSuccess ? FP8MOE_OK : cuda_fail(e);
+}
+
+int fp8moe_combine_tokens(const void* rows, int64_t M, int64_t H, int32_t type,
+                          const int32_t* slot_row, const float* weights, int64_t T, int32_t topk,
+                          void* out, fp8moe_stream_t stream) {
+  int nvec = 0, sms = 0;
+  int rc = check_route(T, topk, M);
+  if (rc) return rc;
+  rc = check_row(H, type, &nvec);
+  if (rc) return rc;
+  if (T == 0) return FP8MOE_OK;
+  if (!slot_row || !out || (M > 0 && !rows)) return FP8MOE_EINVAL;
+  if (!aligned16(rows) || !aligned16(out) || !aligned4(slot_row) || !aligned4(weights))
+    return FP8MOE_EALIGN;
+  rc = device_init(&sms);
+  if (rc) return rc;
+  cudaError_t e = fp8moe_launch_combine(rows, T, topk, nvec, type == FP8MOE_TYPE_F32, slot_row, M,
+                                        weights, out, sms, stream);
+  return e == cudaSuccess ? FP8MOE_OK : cuda_fail(e);
+}
+
+int fp8moe_combine_tokens_bwd(const void* dout, const void* rows, int64_t M, int64_t H,
+                              int32_t type, const int32_t* slot_row, const float* weights,
+                              int64_t T, int32_t topk, void* drows, float* dweights,
+                              fp8moe_stream_t stream) {
+  int nvec = 0, sms = 0;
+  int rc = check_route(T, topk, M);
+  if (rc) return rc;
+  rc = check_row(H, type, &nvec);
+  if (rc) return rc;
+  if (T == 0) return FP8MOE_OK;
+  if (!dout || !slot_row || !weights || !dweights || (M > 0 && (!rows || !drows)))
+    return FP8MOE_EINVAL;
+  if (!aligned16(dout) || !aligned16(rows) || !aligned16(drows) || !aligned4(slot_row) ||
+      !aligned4(weights) || !aligned4(dweights))
+    return FP8MOE_EALIGN;
+  rc = device_init(&sms);
+  if (rc) return rc;
+  cudaError_t e = fp8moe_launch_combine_bwd(dout, rows, T, topk, nvec, type == FP8MOE_TYPE_F32,
+                                            slot_row, M, weights, drows, dweights, stream);
+  return e == cudaSuccess ? FP8MOE_OK : cuda_fail(e);
+}
+
+int fp8moe_norm_fwd(const void* x, const void* y, int64_t T, int64_t H, int32_t type,
+                    const float* w_post, const float* w_pre, const void* gate, int32_t gate_kind,
+                    int32_t sigmoid, float residual_scale, float branch_scale, float eps, void* r,
+                    void* h, float* rstd_post, float* rstd_pre, fp8moe_stream_t stream) {
+  int rc = check_norm(T, H, type, gate_kind, sigmoid);
+  if (rc) return rc;
+  const bool post = w_post != nullptr, pre = w_pre != nullptr;
+  if (!post && !pre) return FP8MOE_EINVAL;
+  if (!post && (y || gate_kind != FP8MOE_GATE_NONE)) return FP8MOE_EINVAL;
+  if (T == 0) return FP8MOE_OK;
+  if (!x || (post && (!y || !r || !rstd_post)) || (pre && (!h || !rstd_pre))) return FP8MOE_EINVAL;
+  if ((gate_kind != FP8MOE_GATE_NONE) != (gate != nullptr)) return FP8MOE_EINVAL;
+  // a token's gate is read value by value, the other kinds by 16 bytes
+  if (!aligned16(x) || !aligned16(y) || !aligned16(w_post) || !aligned16(w_pre) ||
+      !aligned16(r) || !aligned16(h) || !aligned4(rstd_post) || !aligned4(rstd_pre) ||
+      (gate_kind == FP8MOE_GATE_TOKEN ? !aligned4(gate) : !aligned16(gate)))
+    return FP8MOE_EALIGN;
+  int sms = 0;
+  rc = device_init(&sms);
+  if (rc) return rc;
+  NormFwdArgs a = {x, y, w_post, w_pre, gate, gate_kind, sigmoid, residual_scale, branch_scale,
+                   eps, T, (int)H, type == FP8MOE_TYPE_F32, r, h, rstd_post, rstd_pre};
+  cudaError_t e = fp8moe_launch_norm_fwd(a, sms, stream);
+  return e == cudaSuccess ? FP8MOE_OK : cuda_fail(e);
+}
+
+int fp8moe_norm_bwd(const void* dr, const void* dh, const void* r, const void* y, int64_t T,
+                    int64_t H, int32_t type, const float* w_post, const float* w_pre,
+                    const float* rstd_post, const float* rstd_pre, const void* gate,
+                    int32_t gate_kind, int32_t sigmoid, float residual_scale, float branch_scale,
+                    void* dx, void* dy, float* dw_post, float* dw_pre, void* dgate,
+                    void* workspace, size_t workspace_bytes, fp8moe_stream_t stream) {
+  int rc = check_norm(T, H, type, gate_kind, sigmoid);
+  if (rc) return rc;
+  const bool post = w_post != nullptr, pre = w_pre != nullptr;
+  if (!post && !pre) return FP8MOE_EINVAL;
+  if (!post && (y || gate_kind != FP8MOE_GATE_NONE)) return FP8MOE_EINVAL;
+  if (!pre && dh) return FP8MOE_EINVAL;
+  if ((post && !dw_post) || (pre && !dw_pre)) return FP8MOE_EINVAL;
+  if (T > 0 && (gate_kind != FP8MOE_GATE_NONE) != (gate != nullptr)) return FP8MOE_EINVAL;
+  if (gate_kind != FP8MOE_GATE_NONE && !dgate && (T > 0 || gate_kind == FP8MOE_GATE_CHANNEL))
+    return FP8MOE_EINVAL;
+  if (T > 0) {
+    if (!dx || (!dr && !pre)) return FP8MOE_EINVAL;
+    if (post && (!y || !rstd_post || !dy)) return FP8MOE_EINVAL;
+    if (pre && (!dh || !r || !rstd_pre)) return FP8MOE_EINVAL;
+    if (!workspace) return FP8MOE_EWORKSPACE;
+  }
+  if (!aligned16(dr) || !aligned16(dh) || !aligned16(r) || !aligned16(y) || !aligned16(w_post) ||
+      !aligned16(w_pre) || !aligned4(rstd_post) || !aligned4(rstd_pre) || !aligned16(dx) ||
+      !aligned16(dy) || !aligned4(dw_post) || !aligned4(dw_pre) ||
+      (reinterpret_cast<uintptr_t>(workspace) & 255u) ||
+      (gate_kind == FP8MOE_GATE_TOKEN ? !aligned4(gate) || !aligned4(dgate)
+                                    : !aligned16(gate) || !aligned16(dgate)))
+    return FP8MOE_EALIGN;
+  if (T > 0 && workspace_bytes < norm_bwd_ws_bytes(T, H)) return FP8MOE_EWORKSPACE;
+  int sms = 0;
+  rc = device_init(&sms);
+  if (rc) return rc;
+  NormBwdArgs a = {dr, dh, r, y, w_post, w_pre, rstd_post, rstd_pre, gate, gate_kind, sigmoid,
+                   residual_scale, branch_scale, T, (int)H, type == FP8MOE_TYPE_F32, dx, dy,
+                   dw_post, dw_pre, dgate, static_cast<float*>(workspace)};
+  cudaError_t e = fp8moe_launch_norm_bwd(a, sms, stream);
+  return e == cudaSuccess ? FP8MOE_OK : cuda_fail(e);
+}
+
+int fp8moe_mxfp4_quantize_rows(const void* lhs, int64_t M, int64_t K, const int32_t* group_sizes,
+                               int32_t E, uint8_t* codes, uint8_t* scales, fp8moe_stream_t stream) {
+  int rc = check_mxfp4(M, K, 16, E);
+  if (rc) return rc;
+  if (M == 0) return FP8MOE_OK;
+  if (!lhs || !group_sizes || !codes || !scales) return FP8MOE_EINVAL;
+  if (!aligned16(lhs) || !aligned16(codes) || !aligned16(scales) || !aligned4(group_sizes))
+    return FP8MOE_EALIGN;
+  int sms = 0;
+  rc = device_init(&sms);
+  if (rc) return rc;
+  cudaError_t e = fp8moe_launch_mxfp4_quantize_rows(lhs, M, (int)K, group_sizes, E, codes, scales,
+                                                    sms, 1, stream);
+  return e == cudaSuccess ? FP8MOE_OK : cuda_fail(e);
+}
+
+int fp8moe_mxfp4_quantize_weights(const void* w, int32_t E, int64_t K, int64_t N, uint8_t* codes,
+                                  uint8_t* scales, fp8moe_stream_t stream) {
+  int rc = check_mxfp4(0, K, N, E);
+  if (rc) return rc;
+  if (!w || !codes || !scales) return FP8MOE_EINVAL;
+  if (!aligned16(w) || !aligned16(codes) || !aligned16(scales)) return FP8MOE_EALIGN;
+  int sms = 0;
+  rc = device_init(&sms);
+  if (rc) return rc;
+  cudaError_t e = fp8moe_launch_mxfp4_quantize_weights(w, E, (int)K, (int)N, codes, scales, stream);
+  return e == cudaSuccess ? FP8MOE_OK : cuda_fail(e);
+}
+
+int fp8moe_mxfp4_dequantize(const uint8_t* codes, const uint8_t* scales, int32_t E, int64_t N,
+                            int64_t K, void* out, fp8moe_stream_t stream) {
+  int rc = check_mxfp4(0, K, N, E);
+  if (rc) return rc;
+  if (!codes || !scales || !out) return FP8MOE_EINVAL;
+  if (!aligned16(codes) || !aligned16(scales) || !aligned16(out)) return FP8MOE_EALIGN;
+  int sms = 0;
+  rc = device_init(&sms);
+  if (rc) return rc;
+  cudaError_t e = fp8moe_launch_mxfp4_dequantize(codes, scales, E, (int)N, (int)K, out, sms, stream);
+  return e == cudaSuccess ? FP8MOE_OK : cuda_fail(e);
+}
+
+int fp8moe_gmm_mxfp4_fwd(const void* lhs, int64_t M, int64_t K, const uint8_t* codes,
+                         const uint8_t* scales, int32_t E, int64_t N, const int32_t* group_sizes,
+                         void* out, void* workspace, size_t workspace_bytes,
+                         fp8moe_stream_t stream) {
+  return gmm_mxfp4_impl(lhs, M, K, codes, scales, E, N, group_sizes, out, workspace,
+                        workspace_bytes, stream, 0);
+}
+
+int fp8moe_gmm_silu_mxfp4_fwd(const void* lhs, int64_t M, int64_t K, const uint8_t* codes,
+                              const uint8_t* scales, int32_t E, int64_t N,
+                              const int32_t* group_sizes, void* out, void* workspace,
+                              size_t workspace_bytes, fp8moe_stream_t stream) {
+  return gmm_mxfp4_impl(lhs, M, K, codes, scales, E, N, group_sizes, out, workspace,
+                        workspace_bytes, stream, 1);
+}
+
 int fp8moe_read_status(fp8moe_stream_t stream, uint32_t* flags) {
   if (!flags) return FP8MOE_EINVAL;
   uint32_t v = 0;
   uint32_t (*takes[])(cudaStream_t) = {fp8moe_status_take_quant, fp8moe_status_take_dequant,
                                        fp8moe_status_take_gmm_fwd, fp8moe_status_take_dlhs,
                                        fp8moe_status_take_dlhs_pair, fp8moe_status_take_tgmm,
-                                       fp8moe_status_take_selftest};
+                                       fp8moe_status_take_selftest, fp8moe_status_take_route,
+                                       fp8moe_status_take_norm, fp8moe_status_take_mxfp4,
+                                       fp8moe_status_take_gmm_mxfp4};
   for (auto take : takes) {
     uint32_t x = take(stream);
     if (x == 0xFFFFFFFFu) return cuda_fail(cudaGetLastError());

@@ -14,6 +14,7 @@ constexpr uint32_t kStatusNegativeGroup = 1u << 0;
 constexpr uint32_t kStatusGroupsExceedM = 1u << 1;
 constexpr uint32_t kStatusWaitTimeout = 1u << 2;
 constexpr uint32_t kStatusTooManySegments = 1u << 3;
+constexpr uint32_t kStatusBadExpert = 1u << 4;
 // bits [8, 16) name the wait that timed out
 constexpr uint32_t kWhereProducer = 1u << 8;
 constexpr uint32_t kWhereMma = 2u << 8;

@@ -1,0 +1,452 @@
+// gmm_mxfp4.cu -- the ragged grouped product of microscaled 4-bit operands,
+//   y[m, n] = sum_blocks 2^(ex[m, b] + ew[e(m), n, b]) * sum_{k in b} qx[m, k] * qw[e(m), n, k]
+// (f32 accumulation), out = bf16(y), or with SwiGLU bf16(silu(y[m, f]) * y[m, F + f]).
+//
+// The product is computed transposed, D[n, m]: the weight rows are the MMA's M side
+// and the tokens its N side, whose size an instruction can choose in steps of 16.
+// An expert's rows are cut into equal tiles of at most 208 tokens (a group of 1024
+// into five of 208, not four of 208 and one of 192; a group of one token into one
+// tile of 16), so few tokens cost few tensor cycles and the weight's bytes bound.
+//
+// CTA pairs, tcgen05.mma.cta_group::2 kind::mxf4: M = 256 weight rows (128 per CTA),
+// N = the token tile (half of its rows in each CTA's shared memory), K = 64. Roles:
+//   warp 0       TMA: 256 k per stage: this CTA's 128 weight rows (16 KB) and its half
+//                of the token rows, 128-byte swizzle, 7 stages, counted on the even
+//                CTA's barrier. Three token boxes (16, 48, 104 rows): a small tile
+//                does not fetch rows that it does not multiply.
+//   warp 1       TMEM; in the even CTA the MMA-issuing thread.
+//   warps 2, 3   idle.
+//   warps 4..11  scales: two groups of four that take every other stage. The scale
+//                words of a stage (2 words of each of 128 weight rows and up to 208
+//                token rows) go from global memory through registers into tensor
+//                memory (tcgen05.st), one warp per lane quarter, the same data in all
+//                four. They are fetched two stages ahead. Storing them this way and
+//                not from shared memory lets a token tile start at any row.
+//   warps 12..19 epilogue: two warps per lane quarter, alternating 16-token chunks of
+//                one of two accumulators.
+// TMEM (512 columns): two accumulators of 208, four scale slots of 24.
+//
+// SwiGLU: a CTA's 128 weight rows are 4 x (16 gate rows, 16 up rows), fetched by one
+// five-dimensional box, so each warp's 32 lanes hold the gate and up rows of the same
+// 16 columns and one shuffle per token pair brings them together.
+//
+// Bound: tensor issue for many tokens per expert, the weight's bytes for few.
+#include <cstdint>
+#include <cuda.h>
+#include <cuda_runtime.h>
+#include <cuda_bf16.h>
+
+#include "groups.cuh"
+#include "kernels.h"
+#include "mxfp4.cuh"
+#include "ptx.cuh"
+
+namespace fp8moe {
+namespace mxgmm {
+
+constexpr int kBK = 256;                     // k per stage: 128 bytes of codes
+constexpr int kKBytes = kBK / 2;
+constexpr int kRowsA = 128;                  // weight rows per CTA
+constexpr int kUnitN = 2 * kRowsA;           // weight rows per unit = MMA M
+constexpr int kMaxTok = 208;                 // token rows per unit = largest MMA N
+// token rows per CTA of the three TMA boxes
+constexpr int kBox0 = 16, kBox1 = 48, kBox2 = 104;
+constexpr int kABytes = kRowsA * kKBytes;    // 16 KB
+constexpr int kBBytes = kBox2 * kKBytes;
+constexpr int kStageBytes = kABytes + kBBytes;
+constexpr int kStages = 7;
+constexpr int kSlots = 4;
+constexpr int kSfA = 8, kSfB = 16;           // TMEM columns of a stage's scales
+constexpr int kSfCols = kSfA + kSfB;
+constexpr int kDCols = kMaxTok;
+constexpr int kSfBase = 2 * kDCols;
+static_assert(kSfBase + kSlots * kSfCols <= 512, "TMEM budget");
+static_assert(kBBytes % 1024 == 0, "swizzle atoms start on 1024-byte boundaries");
+constexpr int kTokWords = (kMaxTok + 31) / 32;   // scale columns of the token rows per 128 k
+constexpr int kSfGroups = 2;
+constexpr int kFirstSf = 4, kFirstEpi = kFirstSf + 4 * kSfGroups;
+constexpr int kEpiWarps = 8;
+constexpr int kThreads = (kFirstEpi + kEpiWarps) * 32;   // 640
+
+struct Smem {
+  uint64_t full[kStages];      // even CTA: all four boxes of the stage landed
+  uint64_t empty[kStages];     // the MMAs reading the stage completed
+  uint64_t sfull[kSlots];      // even CTA: both CTAs' scales of the slot are in TMEM
+  uint64_t sempty[kSlots];     // the MMAs reading the slot completed
+  uint64_t tfull[2];           // accumulator complete
+  uint64_t tempty[2];          // even CTA: both CTAs' epilogues loaded it
+  uint64_t drain;
+  uint32_t tmem_base;
+  int32_t T;
+  int32_t total_units;
+  int32_t begin[kMaxExperts];
+  int32_t end[kMaxExperts];
+  int32_t prefix[kMaxExperts + 1];
+};
+constexpr size_t kSmemBytes = 1024 + (size_t)kStages * kStageBytes + sizeof(Smem);
+static_assert(kSmemBytes <= 232448, "shared memory per CTA exceeds 227 KB");
+
+struct Unit {
+  int e, m0, rows, tok, w0;    // rows: valid token rows; tok: MMA N; w0: first weight tile index
+};
+
+__device__ __forceinline__ int token_tiles(int rows) { return (rows + kMaxTok - 1) / kMaxTok; }
+
+// Units: expert by expert, token tiles, weight tiles fastest (their shared token
+// tile stays in L2). Tiles of equal size: with t = ceil(rows / 208) tiles of
+// ceil(rows / t) rounded up to 16, which is <= 208, the last one is never empty.
+__device__ __forceinline__ Unit decode_unit(const Smem& s, int E, int wt, int u) {
+  Unit r;
+  r.e = find_bucket(s.prefix, E, u);
+  const int local = u - s.prefix[r.e];
+  const int mi = local / wt;
+  r.w0 = local - mi * wt;
+  const int rows = s.end[r.e] - s.begin[r.e];
+  const int tiles = token_tiles(rows);
+  r.tok = ((rows + tiles - 1) / tiles + 15) & ~15;
+  r.m0 = s.begin[r.e] + mi * r.tok;
+  r.rows = min(r.tok, s.end[r.e] - r.m0);
+  return r;
+}
+
+// The smallest box that holds half of a tile.
+__device__ __forceinline__ int box_rows(int tok) {
+  return tok <= 2 * kBox0 ? kBox0 : tok <= 2 * kBox1 ? kBox1 : kBox2;
+}
+
+// A position in the sequence of (unit, stage) steps of this pair.
+struct Cursor {
+  int u, kb;
+  Unit t;
+};
+
+template <bool SWIGLU>
+__global__ void __launch_bounds__(kThreads, 1)
+gmm_mxfp4_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmX0,
+                 const __grid_constant__ CUtensorMap tmX1, const __grid_constant__ CUtensorMap tmX2,
+                 const uint32_t* __restrict__ sw, const uint32_t* __restrict__ sx,
+                 const int32_t* __restrict__ gs, __nv_bfloat16* __restrict__ out, int64_t M, int K,
+                 int N, int E) {
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* tiles = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                              ~uintptr_t(1023));
+  Smem& s = *reinterpret_cast<Smem*>(tiles + (size_t)kStages * kStageBytes);
+  auto a_tile = [&](int i) -> uint8_t* { return tiles + i * kStageBytes; };
+  auto b_tile = [&](int i) -> uint8_t* { return tiles + i * kStageBytes + kABytes; };
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int rank = (int)cluster_ctarank();
+  const int cluster = blockIdx.x >> 1, nclusters = gridDim.x >> 1;
+  const int F = N / 2;                                  // SwiGLU: gate and up rows
+  const int wt = SWIGLU ? (F + kRowsA - 1) / kRowsA : (N + kUnitN - 1) / kUnitN;
+  const int nkb = (K + kBK - 1) / kBK;
+
+  if (warp == 0) {
+    load_groups_warp0(gs, E, M, s.begin, s.end, &s.T, blockIdx.x == 0);
+    __syncwarp();
+    int32_t carry = 0;
+    for (int base = 0; base < E; base += 32) {
+      const int e = base + lane;
+      int32_t n = 0;
+      if (e < E) n = token_tiles(s.end[e] - s.begin[e]) * wt;
+      int32_t incl = n;
+#pragma unroll
+      for (int d = 1; d < 32; d <<= 1) {
+        const int32_t o = __shfl_up_sync(0xffffffffu, incl, d);
+        if (lane >= d) incl += o;
+      }
+      if (e < E) s.prefix[e] = carry + incl - n;
+      carry += __shfl_sync(0xffffffffu, incl, 31);
+    }
+    if (lane == 0) {
+      s.prefix[E] = carry;
+      s.total_units = carry;
+      prefetch_tmap(&tmW);
+      prefetch_tmap(&tmX0);
+      prefetch_tmap(&tmX1);
+      prefetch_tmap(&tmX2);
+    }
+  } else if (warp == 1) {
+    if (lane == 0) {
+      for (int i = 0; i < kStages; ++i) {
+        mbar_init(&s.full[i], 1);
+        mbar_init(&s.empty[i], 1);
+      }
+      for (int i = 0; i < kSlots; ++i) {
+        mbar_init(&s.sfull[i], 8);       // one group of four warps of each CTA
+        mbar_init(&s.sempty[i], 1);
+      }
+      for (int i = 0; i < 2; ++i) {
+        mbar_init(&s.tfull[i], 1);
+        mbar_init(&s.tempty[i], 2 * kEpiWarps);
+      }
+      mbar_init(&s.drain, 1);
+      fence_mbar_init();
+    }
+    __syncwarp();
+    tmem_alloc_pair(&s.tmem_base, 512);
+    tmem_relinquish_pair();
+    tc_fence_before();
+  }
+  __syncthreads();
+  cluster_sync();      // the peer's barriers exist before anyone signals them
+  tc_fence_after();
+  const int total = s.total_units;
+  const uint32_t tmem = s.tmem_base;
+
+  if (warp == 0) {
+    // ============================ TMA producer ============================
+    if (lane == 0) {
+      int st = 0;
+      uint32_t ph = 0;
+      int64_t issued = 0;
+      bool ok = true;
+      for (int u = cluster; u < total && ok; u += nclusters) {
+        const Unit t = decode_unit(s, E, wt, u);
+        const int box = box_rows(t.tok);
+        const CUtensorMap* tmX = box == kBox0 ? &tmX0 : box == kBox1 ? &tmX1 : &tmX2;
+        const uint32_t bytes = 2u * (uint32_t)(kABytes + box * kKBytes);
+        const int m = t.m0 + rank * (t.tok / 2);
+        for (int kb = 0; kb < nkb; ++kb) {
+          if (!mbar_wait_cluster(&s.empty[st], ph ^ 1, kWhereProducer)) { ok = false; break; }
+          if (rank == 0) mbar_arrive_expect_tx(&s.full[st], bytes);
+          const uint32_t bar = mapa_shared(smem_u32(&s.full[st]), 0);
+          if (SWIGLU)
+            tma_load_5d_pair(a_tile(st), &tmW, bar, kb * kKBytes, 0, 0,
+                             t.w0 * (kRowsA / 16) + rank * 4, t.e);
+          else
+            tma_load_3d_pair(a_tile(st), &tmW, bar, kb * kKBytes, t.w0 * kUnitN + rank * kRowsA,
+                             t.e);
+          tma_load_2d_pair(b_tile(st), tmX, bar, kb * kKBytes, m);
+          ++issued;
+          if (++st == kStages) { st = 0; ph ^= 1; }
+        }
+      }
+      // drain: every copy landed before either CTA may exit
+      if (rank == 0) {
+        const int64_t n_last = issued < kStages ? issued : kStages;
+        for (int64_t i = 1; i <= n_last; ++i) {
+          const int64_t idx = issued - i;
+          mbar_wait_cluster(&s.full[idx % kStages], (uint32_t)((idx / kStages) & 1), kWhereDrain);
+        }
+      }
+    }
+  } else if (warp == 1) {
+    // ============================== MMA issuer ============================
+    if (lane == 0 && rank == 0) {
+      int st = 0, sl = 0, ab = 0;
+      uint32_t ph = 0, sph = 0, tph = 0;
+      bool ok = true;
+      for (int u = cluster; u < total && ok; u += nclusters) {
+        const Unit t = decode_unit(s, E, wt, u);
+        const uint32_t idesc0 = make_idesc_mxf4(kUnitN, t.tok, 0);
+        const uint32_t idesc2 = make_idesc_mxf4(kUnitN, t.tok, 2);
+        const uint32_t d = tmem + (uint32_t)(ab * kDCols);
+        if (!mbar_wait_cluster(&s.tempty[ab], tph ^ 1, kWhereMma)) { ok = false; break; }
+        tc_fence_after();
+        for (int kb = 0; kb < nkb; ++kb) {
+          if (!mbar_wait_cluster(&s.full[st], ph, kWhereMma)) { ok = false; break; }
+          if (!mbar_wait_cluster(&s.sfull[sl], sph, kWhereMma)) { ok = false; break; }
+          tc_fence_after();
+          const uint32_t a_addr = smem_u32(a_tile(st)), b_addr = smem_u32(b_tile(st));
+          const uint32_t sf = tmem + (uint32_t)(kSfBase + sl * kSfCols);
+          const int steps = min(4, (K - kb * kBK + 63) / 64);
+          for (int kk = 0; kk < steps; ++kk) {
+            const uint64_t ad = make_desc(a_addr + kk * 32, 16, 1024, kSwizzle128B);
+            const uint64_t bd = make_desc(b_addr + kk * 32, 16, 1024, kSwizzle128B);
+            mma_mxf4_pair(d, ad, bd, (kk & 1) ? idesc2 : idesc0, sf + (kk >> 1) * (kSfA / 2),
+                          sf + kSfA + (kk >> 1) * (kSfB / 2), (kb | kk) != 0);
+          }
+          mma_commit_pair(&s.empty[st]);
+          mma_commit_pair(&s.sempty[sl]);
+          if (++st == kStages) { st = 0; ph ^= 1; }
+          if (++sl == kSlots) { sl = 0; sph ^= 1; }
+        }
+        if (!ok) break;
+        mma_commit_pair(&s.tfull[ab]);
+        if (++ab == 2) { ab = 0; tph ^= 1; }
+      }
+      // all MMAs complete (in both CTAs' TMEM) before TMEM may be released
+      mma_commit_pair(&s.drain);
+    }
+    if (lane == 0) mbar_wait_cluster(&s.drain, 0, kWhereDrain);
+  } else if (warp < kFirstSf) {
+    // idle
+  } else if (warp < kFirstEpi) {
+    // =============================== scales ===============================
+    const int quarter = warp & 3;
+    const int group = (warp - kFirstSf) >> 2;
+    const uint32_t tq = tmem + ((uint32_t)(quarter * 32) << 16) + (uint32_t)kSfBase;
+    const uint32_t even_sfull = mapa_shared(smem_u32(&s.sfull[0]), 0);
+    const int words = (K + kMxWord - 1) / kMxWord;
+    const int last_blocks = (K - (words - 1) * kMxWord) / kMxBlock;     // of the last word: 1..4
+    const uint32_t last_mask = last_blocks == 4 ? 0xFFFFFFFFu : (1u << (8 * last_blocks)) - 1u;
+    auto next = [&](Cursor& c, int by) {       // false past the last step
+      c.kb += by;
+      while (c.kb >= nkb) {
+        c.kb -= nkb;
+        c.u += nclusters;
+        if (c.u >= total) return false;
+        c.t = decode_unit(s, E, wt, c.u);
+      }
+      return true;
+    };
+    auto fetch = [&](const Cursor& c, uint32_t (&wa)[8], uint32_t (&wb)[16]) {
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const int word = 2 * c.kb + h;
+        const uint32_t mask = word >= words ? 0u : word == words - 1 ? last_mask : 0xFFFFFFFFu;
+        const uint32_t* pa = sw + ((int64_t)c.t.e * words + word) * N;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          int n;
+          bool in;
+          if (SWIGLU) {
+            const int f = c.t.w0 * kRowsA + rank * 64 + j * 16 + (lane & 15);
+            n = (lane >> 4) * F + f;
+            in = f < F;
+          } else {
+            n = c.t.w0 * kUnitN + rank * kRowsA + j * 32 + lane;
+            in = n < N;
+          }
+          wa[h * 4 + j] = (in && mask) ? __ldg(pa + n) & mask : 0u;
+        }
+        const uint32_t* pb = sx + (int64_t)word * M + c.t.m0;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          const int m = j * 32 + lane;
+          wb[h * 8 + j] = (j < kTokWords && m < c.t.rows && mask) ? __ldg(pb + m) & mask : 0u;
+        }
+      }
+    };
+    Cursor c;
+    c.u = cluster;
+    c.kb = 0;
+    bool more = cluster < total;
+    if (more) {
+      c.t = decode_unit(s, E, wt, c.u);
+      if (group) more = next(c, group);
+    }
+    uint32_t wa[8], wb[16];
+    if (more) fetch(c, wa, wb);
+    for (uint32_t i = (uint32_t)group; more; i += kSfGroups) {
+      const int sl = (int)(i % kSlots);
+      const uint32_t sph = (i / kSlots) & 1;
+      uint32_t na[8], nb[16];
+      const bool again = next(c, kSfGroups);
+      if (again) fetch(c, na, nb);
+      if (!mbar_wait_warp_cluster(&s.sempty[sl], sph ^ 1, kWhereDequant)) break;
+      tc_fence_after();
+      tmem_st8(tq + (uint32_t)(sl * kSfCols), wa);
+      tmem_st16(tq + (uint32_t)(sl * kSfCols + kSfA), wb);
+      tmem_st_wait();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive_cluster_relaxed(even_sfull + (uint32_t)(sl * sizeof(uint64_t)));
+#pragma unroll
+      for (int j = 0; j < 8; ++j) wa[j] = na[j];
+#pragma unroll
+      for (int j = 0; j < 16; ++j) wb[j] = nb[j];
+      more = again;
+    }
+  } else {
+    // =============================== epilogue =============================
+    const int quarter = warp & 3;
+    const int half = (warp - kFirstEpi) >> 2;
+    const uint32_t tq = tmem + ((uint32_t)(quarter * 32) << 16);
+    const uint32_t even_tempty = mapa_shared(smem_u32(&s.tempty[0]), 0);
+    int ab = 0;
+    uint32_t tph = 0;
+    uint16_t* const o16 = reinterpret_cast<uint16_t*>(out);
+    for (int u = cluster; u < total; u += nclusters) {
+      const Unit t = decode_unit(s, E, wt, u);
+      if (!mbar_wait_warp_cluster(&s.tfull[ab], tph, kWhereEpilogue)) break;
+      tc_fence_after();
+      for (int c0 = half * 16; c0 < t.tok; c0 += 32) {
+        uint32_t w[16];
+        tmem_ld16(tq + (uint32_t)(ab * kDCols + c0), w);
+        tmem_ld_wait();
+        const int64_t row0 = (int64_t)t.m0 + c0;
+        if (SWIGLU) {
+          const bool up = lane >= 16;
+          const int f = t.w0 * kRowsA + rank * 64 + quarter * 16 + (lane & 15);
+#pragma unroll
+          for (int j = 0; j < 16; j += 2) {
+            // lanes 0..15 take token j, lanes 16..31 token j + 1
+            const float send = __uint_as_float(up ? w[j] : w[j + 1]);
+            const float got = __shfl_xor_sync(0xffffffffu, send, 16);
+            const float g = up ? got : __uint_as_float(w[j]);
+            const float v = up ? __uint_as_float(w[j + 1]) : got;
+            const float h = __fmul_rn(__fdiv_rn(g, __fadd_rn(1.0f, expf(-g))), v);
+            const int jj = j + (up ? 1 : 0);
+            if (f < F && c0 + jj < t.rows)
+              o16[(row0 + jj) * F + f] = (uint16_t)(f32x2_to_bf16x2(h, 0.0f) & 0xFFFFu);
+          }
+        } else {
+          const int n = t.w0 * kUnitN + rank * kRowsA + quarter * 32 + lane;
+          if (n < N) {
+#pragma unroll
+            for (int j = 0; j < 16; ++j)
+              if (c0 + j < t.rows)
+                o16[(row0 + j) * N + n] =
+                    (uint16_t)(f32x2_to_bf16x2(__uint_as_float(w[j]), 0.0f) & 0xFFFFu);
+          }
+        }
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive_cluster_relaxed(even_tempty + (uint32_t)(ab * sizeof(uint64_t)));
+      if (++ab == 2) { ab = 0; tph ^= 1; }
+    }
+  }
+
+  __syncthreads();
+  cluster_sync();      // both CTAs done with TMEM, shared memory and barriers
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc_pair(tmem, 512);
+  }
+}
+
+template <bool SWIGLU>
+cudaError_t launch(const GmmMxfp4Args& a, int num_sms, cudaStream_t s) {
+  auto kern = gmm_mxfp4_kernel<SWIGLU>;
+  cudaError_t err =
+      cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmemBytes);
+  if (err != cudaSuccess) return err;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)(num_sms & ~1), 1, 1);   // whole CTA pairs, one CTA per SM
+  cfg.blockDim = dim3(kThreads, 1, 1);
+  cfg.dynamicSmemBytes = kSmemBytes;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = 2;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  err = cudaLaunchKernelEx(&cfg, kern, a.tmW, a.tmX[0], a.tmX[1], a.tmX[2],
+                           reinterpret_cast<const uint32_t*>(a.sw),
+                           reinterpret_cast<const uint32_t*>(a.sx), a.gs,
+                           static_cast<__nv_bfloat16*>(a.out), a.M, a.K, a.N, a.E);
+  if (err != cudaSuccess) return err;
+  return cudaGetLastError();
+}
+
+}  // namespace mxgmm
+}  // namespace fp8moe
+
+FP8MOE_DEFINE_STATUS_TAKE(fp8moe_status_take_gmm_mxfp4)
+
+void fp8moe_gmm_mxfp4_boxes(int rows[3]) {
+  using namespace fp8moe::mxgmm;
+  rows[0] = kBox0;
+  rows[1] = kBox1;
+  rows[2] = kBox2;
+}
+
+cudaError_t fp8moe_launch_gmm_mxfp4(const GmmMxfp4Args& a, int num_sms, cudaStream_t s) {
+  using namespace fp8moe::mxgmm;
+  return a.swiglu ? launch<true>(a, num_sms, s) : launch<false>(a, num_sms, s);
+}

@@ -92,3 +92,89 @@ cudaError_t fp8moe_launch_selftest_wait(uint64_t limit_ns, cudaStream_t s);
 // cast (selftest.cu).
 cudaError_t fp8moe_launch_selftest_cast(const float* x, int64_t n, int fmt, uint8_t* out,
                                         int num_sms, cudaStream_t s);
+
+// Tokens sorted by expert and back (route.cu). n = T * topk slots; nvec = 16-byte
+// vectors of a row; f32: rows hold f32 instead of bf16.
+uint32_t fp8moe_status_take_route(cudaStream_t s);
+cudaError_t fp8moe_launch_sort_tokens(const int32_t* ids, int64_t n, int E, int64_t M,
+                                      int32_t* group_sizes, int32_t* slot_row, int32_t* row_slot,
+                                      cudaStream_t s);
+cudaError_t fp8moe_launch_dispatch(const void* x, int64_t T, int topk, int nvec,
+                                   const int32_t* slot_row, int64_t M, void* rows, int num_sms,
+                                   cudaStream_t s);
+cudaError_t fp8moe_launch_combine(const void* rows, int64_t T, int topk, int nvec, int f32,
+                                  const int32_t* slot_row, int64_t M, const float* weights,
+                                  void* out, int num_sms, cudaStream_t s);
+cudaError_t fp8moe_launch_combine_bwd(const void* dout, const void* rows, int64_t T, int topk,
+                                      int nvec, int f32, const int32_t* slot_row, int64_t M,
+                                      const float* weights, void* drows, float* dweights,
+                                      cudaStream_t s);
+
+// Norms around a block (norm.cu). gate_kind: 0 none, 1 per row, 2 per column, 3 per element.
+struct NormFwdArgs {
+  const void* x;
+  const void* y;          // null: no block output, only h = norm(x)
+  const float* w_post;    // with y
+  const float* w_pre;     // null: no h
+  const void* gate;
+  int gate_kind, sigmoid;
+  float residual_scale, branch_scale, eps;
+  int64_t T;
+  int H, f32;
+  void* r;
+  void* h;
+  float* rstd_post;
+  float* rstd_pre;
+};
+cudaError_t fp8moe_launch_norm_fwd(const NormFwdArgs& a, int num_sms, cudaStream_t s);
+
+struct NormBwdArgs {
+  const void* dr;         // may be null (with dh)
+  const void* dh;         // null: no pre norm
+  const void* r;
+  const void* y;          // null: no post norm
+  const float* w_post;
+  const float* w_pre;
+  const float* rstd_post;
+  const float* rstd_pre;
+  const void* gate;
+  int gate_kind, sigmoid;
+  float residual_scale, branch_scale;
+  int64_t T;
+  int H, f32;
+  void* dx;
+  void* dy;
+  float* dw_post;
+  float* dw_pre;
+  void* dgate;
+  float* part;            // 3 * fp8moe_norm_bwd_ctas(T) * H
+};
+int fp8moe_norm_bwd_ctas(int64_t T);
+cudaError_t fp8moe_launch_norm_bwd(const NormBwdArgs& a, int num_sms, cudaStream_t s);
+uint32_t fp8moe_status_take_norm(cudaStream_t s);
+
+// Microscaled 4-bit quantisation (mxfp4.cu).
+cudaError_t fp8moe_launch_mxfp4_quantize_rows(const void* x, int64_t M, int K, const int32_t* gs,
+                                              int E, uint8_t* codes, uint8_t* scales, int num_sms,
+                                              int report, cudaStream_t s);
+cudaError_t fp8moe_launch_mxfp4_quantize_weights(const void* w, int E, int K, int N, uint8_t* codes,
+                                                 uint8_t* scales, cudaStream_t s);
+cudaError_t fp8moe_launch_mxfp4_dequantize(const uint8_t* codes, const uint8_t* scales, int E,
+                                           int N, int K, void* out, int num_sms, cudaStream_t s);
+uint32_t fp8moe_status_take_mxfp4(cudaStream_t s);
+
+// Grouped product of MXFP4 operands (gmm_mxfp4.cu).
+struct GmmMxfp4Args {
+  CUtensorMap tmW;          // weight codes: [E, N, K/2] boxes of 128 rows, or with SwiGLU
+                            // [E, F/16, 2, 16, K/2] boxes of 4 x 2 x 16 rows
+  CUtensorMap tmX[3];       // activation codes [M, K/2], boxes of fp8moe_gmm_mxfp4_boxes() rows
+  const uint8_t* sw;        // [E, ceil(K/128), N, 4]
+  const uint8_t* sx;        // [ceil(K/128), M, 4]
+  const int32_t* gs;
+  void* out;                // bf16 [M, N] or [M, N/2]
+  int64_t M;
+  int K, N, E, swiglu;
+};
+void fp8moe_gmm_mxfp4_boxes(int rows[3]);
+cudaError_t fp8moe_launch_gmm_mxfp4(const GmmMxfp4Args& a, int num_sms, cudaStream_t s);
+uint32_t fp8moe_status_take_gmm_mxfp4(cudaStream_t s);

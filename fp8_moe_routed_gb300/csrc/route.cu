@@ -1,0 +1,388 @@
+// route.cu -- tokens sorted by expert and back: the stable counting sort of the
+// router's choices, the copy of each token to its rows (dispatch), the weighted
+// sum of a token's rows (combine), and their gradients.
+//
+// A slot s = t * topk + j is token t's j-th choice. With key(s) its expert id
+// (a slot whose id is outside [0, E) has no row):
+//   row(s) = #{s': key(s') < key(s)} + #{s' < s: key(s') = key(s)},  dropped if >= M
+//   rows[row(t, j)]  = x[t]                                   (dispatch)
+//   out[t]           = sum_j w[t, j] * rows[row(t, j)]        (combine; w = 1: dispatch's gradient)
+//   drows[row(t, j)] = w[t, j] * dout[t],  dw[t, j] = <dout[t], rows[row(t, j)]>
+// Everything but the sort is bound by HBM: each kernel reads and writes every row
+// once. Work is laid out by token, so a token's vector is read once for its topk
+// rows, and no two threads ever write (or add to) the same element: no atomics,
+// the sums run in the order of j and the results do not depend on scheduling.
+#include <cstdint>
+#include <cooperative_groups.h>
+#include <cuda_runtime.h>
+#include <cuda_bf16.h>
+
+#include "fp8moe_status.cuh"
+#include "groups.cuh"
+#include "kernels.h"
+#include "vec16.cuh"
+
+namespace cg = cooperative_groups;
+
+namespace fp8moe {
+namespace route {
+
+__device__ __forceinline__ int warp_incl_scan(int v, int lane) {
+#pragma unroll
+  for (int d = 1; d < 32; d <<= 1) {
+    const int o = __shfl_up_sync(0xffffffffu, v, d);
+    if (lane >= d) v += o;
+  }
+  return v;
+}
+
+// ------------------------------------------------------------------------ sort
+// One cluster of kSortCtas CTAs (one CTA when there are few slots). The slots are
+// cut into one contiguous run per warp. First pass: every warp counts its run per
+// expert in its own shared-memory counters, 32 slots at a time (match_any gives
+// the lanes that share an expert, their lowest lane adds their number). Then each
+// counter becomes the first row of that (warp, expert): an exclusive scan over the
+// warps of a CTA, over the CTAs (their totals read through distributed shared
+// memory) and over the experts. Second pass: a slot's row is its warp's counter
+// plus the number of lower lanes with the same expert. Bound by the two passes'
+// issue rate on eight SMs; the dispatch that follows moves H / 2 times the bytes.
+constexpr int kSortCtas = 8;
+constexpr int kSortThreads = 1024;
+constexpr int kSortWarps = kSortThreads / 32;
+
+__global__ void __launch_bounds__(kSortThreads, 1)
+sort_kernel(const int32_t* __restrict__ ids, int64_t n, int E, int64_t M,
+            int32_t* __restrict__ group_sizes, int32_t* __restrict__ slot_row,
+            int32_t* __restrict__ row_slot) {
+  extern __shared__ int32_t sm[];
+  int32_t* const counts = sm;                           // [kSortWarps][E]
+  int32_t* const cta_total = sm + (size_t)kSortWarps * E;   // [E], read by the other CTAs
+  __shared__ int32_t s_warp[kSortWarps];
+  __shared__ int64_t s_rows;
+  cg::cluster_group cluster = cg::this_cluster();
+  const int ctas = (int)cluster.num_blocks(), rank = (int)cluster.block_rank();
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+
+  for (int i = threadIdx.x; i < kSortWarps * E; i += kSortThreads) counts[i] = 0;
+  __syncthreads();
+
+  const int64_t batches = (n + 31) / 32;
+  const int64_t per = (batches + ctas * kSortWarps - 1) / (ctas * kSortWarps);
+  const int64_t b0 = (int64_t)(rank * kSortWarps + warp) * per;
+  const int64_t b1 = b0 + per < batches ? b0 + per : batches;
+  int32_t* const mine = counts + (size_t)warp * E;
+  bool bad = false;
+  for (int64_t b = b0; b < b1; ++b) {
+    const int64_t s = b * 32 + lane;
+    const int32_t e = s < n ? __ldg(ids + s) : -1;
+    bad |= e >= E;
+    const int32_t key = (e >= 0 && e < E) ? e : -1;
+    const uint32_t same = __match_any_sync(0xffffffffu, key);
+    if (key >= 0 && lane == __ffs(same) - 1) mine[key] += __popc(same);
+    __syncwarp();
+  }
+  __syncthreads();
+  // thread e: exclusive scan of expert e over this CTA's warps
+  for (int e = threadIdx.x; e < E; e += kSortThreads) {
+    int32_t run = 0;
+#pragma unroll 8
+    for (int w = 0; w < kSortWarps; ++w) {
+      const int32_t c = counts[(size_t)w * E + e];
+      counts[(size_t)w * E + e] = run;
+      run += c;
+    }
+    cta_total[e] = run;
+  }
+  cluster.sync();
+  // experts: E <= 1024 = one per thread
+  {
+    const int e = threadIdx.x;
+    int32_t before = 0, total = 0;
+    if (e < E) {
+      for (int c = 0; c < ctas; ++c) {
+        const int32_t v = cluster.map_shared_rank(cta_total, c)[e];
+        if (c < rank) before += v;
+        total += v;
+      }
+    }
+    const int32_t incl = warp_incl_scan(total, lane);
+    if (lane == 31) s_warp[warp] = incl;
+    __syncthreads();
+    int32_t base = 0;
+    for (int w = 0; w < warp; ++w) base += s_warp[w];
+    const int32_t start = base + incl - total;
+    if (e < E) {
+      for (int w = 0; w < kSortWarps; ++w) counts[(size_t)w * E + e] += start + before;
+      if (rank == 0) {
+        const int64_t lo = start < M ? start : M;
+        const int64_t hi = (int64_t)start + total < M ? (int64_t)start + total : M;
+        group_sizes[e] = (int32_t)(hi - lo);
+      }
+    }
+    if (threadIdx.x == kSortThreads - 1) {
+      s_rows = (int64_t)base + incl;
+      if (rank == 0 && s_rows > M) status_set(kStatusGroupsExceedM);
+    }
+  }
+  __syncthreads();
+  for (int64_t b = b0; b < b1; ++b) {
+    const int64_t s = b * 32 + lane;
+    const int32_t e = s < n ? __ldg(ids + s) : -1;
+    const int32_t key = (e >= 0 && e < E) ? e : -1;
+    const uint32_t same = __match_any_sync(0xffffffffu, key);
+    int32_t row = -1;
+    if (key >= 0) row = mine[key] + __popc(same & ((1u << lane) - 1u));
+    __syncwarp();
+    if (key >= 0 && lane == __ffs(same) - 1) mine[key] += __popc(same);
+    __syncwarp();
+    if (row >= M) row = -1;
+    if (s < n) {
+      slot_row[s] = row;
+      if (row >= 0 && row_slot) row_slot[row] = (int32_t)s;
+    }
+  }
+  if (row_slot) {
+    for (int64_t r = s_rows + (int64_t)rank * kSortThreads + threadIdx.x; r < M;
+         r += (int64_t)ctas * kSortThreads)
+      row_slot[r] = -1;
+  }
+  if (__any_sync(0xffffffffu, bad) && lane == 0) status_set(kStatusBadExpert);
+  cluster.sync();   // no CTA leaves while another may still read its totals
+}
+
+// The row of a slot, -1 for none. A caller's entry past the buffer (a slot_row
+// made for a larger one) counts as none: it is never followed out of bounds.
+__device__ __forceinline__ int32_t row_of(const int32_t* slot_row, int64_t s, int64_t M) {
+  const int32_t r = __ldg(slot_row + s);
+  return r < M ? r : -1;
+}
+
+// -------------------------------------------------------------------- dispatch
+// A warp moves 128 16-byte vectors of one token: four loads in flight per lane,
+// then the stores to each of the token's rows (512 contiguous bytes per store).
+constexpr int kMoveVecs = 4;
+constexpr int kMoveThreads = 256;
+
+__global__ void __launch_bounds__(kMoveThreads)
+dispatch_kernel(const uint4* __restrict__ x, int64_t T, int topk, int nvec, int chunks,
+                const int32_t* __restrict__ slot_row, int64_t M, uint4* __restrict__ rows) {
+  const int lane = threadIdx.x & 31;
+  const int64_t items = T * chunks;
+  const int64_t step = (int64_t)gridDim.x * (kMoveThreads / 32);
+  for (int64_t it = (int64_t)blockIdx.x * (kMoveThreads / 32) + (threadIdx.x >> 5); it < items;
+       it += step) {
+    const int64_t t = it / chunks;
+    const int v0 = (int)(it - t * chunks) * (32 * kMoveVecs) + lane;
+    const int32_t r = lane < topk ? row_of(slot_row, t * topk + lane, M) : -1;
+    uint4 v[kMoveVecs];
+#pragma unroll
+    for (int i = 0; i < kMoveVecs; ++i)
+      if (v0 + 32 * i < nvec) v[i] = __ldg(x + t * nvec + v0 + 32 * i);
+    for (int j = 0; j < topk; ++j) {
+      const int32_t row = __shfl_sync(0xffffffffu, r, j);
+      if (row < 0) continue;
+      uint4* d = rows + (int64_t)row * nvec + v0;
+#pragma unroll
+      for (int i = 0; i < kMoveVecs; ++i)
+        if (v0 + 32 * i < nvec) d[32 * i] = v[i];
+    }
+  }
+}
+
+// --------------------------------------------------------------------- combine
+// A warp sums 32 vectors of one token over its rows; up to eight row loads are in
+// flight per lane. A slot without a row adds nothing: its vector is not read, so
+// what lies there (or a NaN weight) cannot reach the sum.
+constexpr int kSumBatch = 8;
+
+template <typename T, bool WEIGHTED>
+__global__ void __launch_bounds__(kMoveThreads)
+combine_kernel(const uint4* __restrict__ rows, int64_t tokens, int topk, int nvec, int chunks,
+               const int32_t* __restrict__ slot_row, int64_t M, const float* __restrict__ weights,
+               uint4* __restrict__ out) {
+  constexpr int N = Vec<T>::kN;
+  const int lane = threadIdx.x & 31;
+  const int64_t items = tokens * chunks;
+  const int64_t step = (int64_t)gridDim.x * (kMoveThreads / 32);
+  for (int64_t it = (int64_t)blockIdx.x * (kMoveThreads / 32) + (threadIdx.x >> 5); it < items;
+       it += step) {
+    const int64_t t = it / chunks;
+    const int v0 = (int)(it - t * chunks) * 32 + lane;
+    int32_t r = -1;
+    float w = 1.0f;
+    if (lane < topk) {
+      r = row_of(slot_row, t * topk + lane, M);
+      if (WEIGHTED) w = __ldg(weights + t * topk + lane);
+    }
+    float acc[N];
+#pragma unroll
+    for (int i = 0; i < N; ++i) acc[i] = 0.0f;
+    for (int j0 = 0; j0 < topk; j0 += kSumBatch) {
+      uint4 v[kSumBatch];
+      int32_t row[kSumBatch];
+#pragma unroll
+      for (int j = 0; j < kSumBatch; ++j) {
+        row[j] = __shfl_sync(0xffffffffu, r, (j0 + j) & 31);
+        if (j0 + j >= topk) row[j] = -1;
+        if (row[j] >= 0 && v0 < nvec) v[j] = __ldg(rows + (int64_t)row[j] * nvec + v0);
+      }
+#pragma unroll
+      for (int j = 0; j < kSumBatch; ++j) {
+        const float wj = WEIGHTED ? __shfl_sync(0xffffffffu, w, (j0 + j) & 31) : 1.0f;
+        if (row[j] < 0) continue;
+        float f[N];
+        Vec<T>::unpack(v[j], f);
+#pragma unroll
+        for (int i = 0; i < N; ++i) acc[i] = WEIGHTED ? fmaf(wj, f[i], acc[i]) : acc[i] + f[i];
+      }
+    }
+    if (v0 < nvec) out[t * nvec + v0] = Vec<T>::pack(acc);
+  }
+}
+
+// ---------------------------------------------------------- combine's gradient
+// A CTA takes a token: every thread walks its share of the token's vectors, reads
+// dout once and each row once (eight at a time), writes the row's gradient and
+// keeps the partial dot products; one block reduction per eight rows ends it.
+constexpr int kBwdThreads = 256;
+
+template <typename T>
+__global__ void __launch_bounds__(kBwdThreads)
+combine_bwd_kernel(const uint4* __restrict__ dout, const uint4* __restrict__ rows, int topk,
+                   int nvec, const int32_t* __restrict__ slot_row, int64_t M,
+                   const float* __restrict__ weights, uint4* __restrict__ drows,
+                   float* __restrict__ dweights) {
+  constexpr int N = Vec<T>::kN;
+  __shared__ float s_part[kBwdThreads / 32][kSumBatch];
+  const int64_t t = blockIdx.x;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  for (int j0 = 0; j0 < topk; j0 += kSumBatch) {
+    int32_t row[kSumBatch];
+    float w[kSumBatch], dot[kSumBatch];
+#pragma unroll
+    for (int j = 0; j < kSumBatch; ++j) {
+      row[j] = j0 + j < topk ? row_of(slot_row, t * topk + j0 + j, M) : -1;
+      w[j] = j0 + j < topk ? __ldg(weights + t * topk + j0 + j) : 0.0f;
+      dot[j] = 0.0f;
+    }
+    for (int v = threadIdx.x; v < nvec; v += kBwdThreads) {
+      const uint4 dv = __ldg(dout + t * nvec + v);
+      uint4 y[kSumBatch];
+#pragma unroll
+      for (int j = 0; j < kSumBatch; ++j)
+        if (row[j] >= 0) y[j] = __ldg(rows + (int64_t)row[j] * nvec + v);
+      float d[N];
+      Vec<T>::unpack(dv, d);
+#pragma unroll
+      for (int j = 0; j < kSumBatch; ++j) {
+        if (row[j] < 0) continue;
+        float f[N], o[N];
+        Vec<T>::unpack(y[j], f);
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+          dot[j] = fmaf(d[i], f[i], dot[j]);
+          o[i] = w[j] * d[i];
+        }
+        drows[(int64_t)row[j] * nvec + v] = Vec<T>::pack(o);
+      }
+    }
+#pragma unroll
+    for (int j = 0; j < kSumBatch; ++j) {
+#pragma unroll
+      for (int d = 16; d > 0; d >>= 1) dot[j] += __shfl_xor_sync(0xffffffffu, dot[j], d);
+      if (lane == 0) s_part[warp][j] = dot[j];
+    }
+    __syncthreads();
+    if (threadIdx.x < kSumBatch && j0 + (int)threadIdx.x < topk) {
+      float sum = 0.0f;
+#pragma unroll
+      for (int k = 0; k < kBwdThreads / 32; ++k) sum += s_part[k][threadIdx.x];
+      dweights[t * topk + j0 + threadIdx.x] = sum;   // 0 where the slot has no row
+    }
+    __syncthreads();
+  }
+}
+
+int grid_for(int64_t items, int per_cta, int num_sms, int ctas_per_sm) {
+  const int64_t want = (items + per_cta - 1) / per_cta;
+  const int64_t most = (int64_t)num_sms * ctas_per_sm;
+  return (int)(want < most ? want : most);
+}
+
+}  // namespace route
+}  // namespace fp8moe
+
+FP8MOE_DEFINE_STATUS_TAKE(fp8moe_status_take_route)
+
+cudaError_t fp8moe_launch_sort_tokens(const int32_t* ids, int64_t n, int E, int64_t M,
+                                      int32_t* group_sizes, int32_t* slot_row, int32_t* row_slot,
+                                      cudaStream_t s) {
+  using namespace fp8moe::route;
+  const size_t smem = (size_t)(kSortWarps + 1) * E * sizeof(int32_t);
+  cudaError_t err = cudaFuncSetAttribute(sort_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                         (int)smem);
+  if (err != cudaSuccess) return err;
+  cudaLaunchConfig_t cfg = {};
+  // below 8192 slots one CTA has at most eight 32-slot batches per warp
+  const unsigned ctas = n <= 8192 ? 1 : kSortCtas;
+  cfg.gridDim = dim3(ctas, 1, 1);
+  cfg.blockDim = dim3(kSortThreads, 1, 1);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = ctas;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  err = cudaLaunchKernelEx(&cfg, sort_kernel, ids, n, E, M, group_sizes, slot_row, row_slot);
+  if (err != cudaSuccess) return err;
+  return cudaGetLastError();
+}
+
+cudaError_t fp8moe_launch_dispatch(const void* x, int64_t T, int topk, int nvec,
+                                   const int32_t* slot_row, int64_t M, void* rows, int num_sms,
+                                   cudaStream_t s) {
+  using namespace fp8moe::route;
+  const int chunks = (nvec + 32 * kMoveVecs - 1) / (32 * kMoveVecs);
+  const int grid = grid_for(T * chunks, kMoveThreads / 32, num_sms, 8);
+  dispatch_kernel<<<grid, kMoveThreads, 0, s>>>(static_cast<const uint4*>(x), T, topk, nvec, chunks,
+                                                slot_row, M, static_cast<uint4*>(rows));
+  return cudaGetLastError();
+}
+
+cudaError_t fp8moe_launch_combine(const void* rows, int64_t T, int topk, int nvec, int f32,
+                                  const int32_t* slot_row, int64_t M, const float* weights,
+                                  void* out, int num_sms, cudaStream_t s) {
+  using namespace fp8moe::route;
+  const int chunks = (nvec + 31) / 32;
+  const int grid = grid_for(T * chunks, kMoveThreads / 32, num_sms, 8);
+  auto run = [&](auto kern) {
+    kern<<<grid, kMoveThreads, 0, s>>>(static_cast<const uint4*>(rows), T, topk, nvec, chunks,
+                                       slot_row, M, weights, static_cast<uint4*>(out));
+  };
+  if (f32) {
+    if (weights) run(combine_kernel<float, true>);
+    else run(combine_kernel<float, false>);
+  } else {
+    if (weights) run(combine_kernel<__nv_bfloat16, true>);
+    else run(combine_kernel<__nv_bfloat16, false>);
+  }
+  return cudaGetLastError();
+}
+
+cudaError_t fp8moe_launch_combine_bwd(const void* dout, const void* rows, int64_t T, int topk,
+                                      int nvec, int f32, const int32_t* slot_row, int64_t M,
+                                      const float* weights, void* drows, float* dweights,
+                                      cudaStream_t s) {
+  using namespace fp8moe::route;
+  auto run = [&](auto kern) {
+    kern<<<(unsigned)T, kBwdThreads, 0, s>>>(static_cast<const uint4*>(dout),
+                                             static_cast<const uint4*>(rows), topk, nvec, slot_row,
+                                             M, weights, static_cast<uint4*>(drows), dweights);
+  };
+  if (f32) run(combine_bwd_kernel<float>);
+  else run(combine_bwd_kernel<__nv_bfloat16>);
+  return cudaGetLastError();
+}

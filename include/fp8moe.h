@@ -62,7 +62,24 @@ enum {
   FP8MOE_OP_TGMM_DRHS_QUANT = 4,
   FP8MOE_OP_GMM_BF16_FWD = 5,
   FP8MOE_OP_DEQUANTIZE = 6,
-  FP8MOE_OP_GMM_FP8_FWD_BLOCK = 7
+  FP8MOE_OP_GMM_FP8_FWD_BLOCK = 7,
+  FP8MOE_OP_GMM_MXFP4_FWD = 8,
+  FP8MOE_OP_GMM_SILU_MXFP4_FWD = 9,
+  FP8MOE_OP_NORM_BWD = 10        /* M = T rows, K = H columns; N and E unused */
+};
+
+/* Element types of the rows that the token and norm operators move. */
+enum {
+  FP8MOE_TYPE_BF16 = 0,
+  FP8MOE_TYPE_F32 = 1
+};
+
+/* What a block's gate is shared by (fp8moe_norm_fwd). */
+enum {
+  FP8MOE_GATE_NONE = 0,  /* no gate (1) */
+  FP8MOE_GATE_TOKEN = 1,   /* f32 [T], one value per token */
+  FP8MOE_GATE_CHANNEL = 2, /* f32 [H], one value per column */
+  FP8MOE_GATE_FULL = 3     /* [T, H] of the rows' type */
 };
 
 /* fp8 formats of the tgmm's dout (gradient) operand -- [DQ] What: the
@@ -77,6 +94,7 @@ enum {
 #define FP8MOE_STATUS_GROUPS_EXCEED_M 0x2u   /* sum(group_sizes) > M (clipped at M) */
 #define FP8MOE_STATUS_WAIT_TIMEOUT 0x4u      /* a kernel pipeline wait gave up; bits 8..15 say where */
 #define FP8MOE_STATUS_TOO_MANY_SEGMENTS 0x8u /* internal: segment bound exceeded */
+#define FP8MOE_STATUS_BAD_EXPERT 0x10u       /* an expert id >= E (its slot was dropped) */
 
 /* Workspace bytes the operation needs for these sizes (0 if none); the
  * workspace pointer must be 256-byte aligned.  Depends on M, K, N, E only. */
@@ -284,6 +302,128 @@ int fp8moe_gmm_silu_fp8_fwd_noalloc(const void* lhs, int64_t M, int64_t K, const
                                     const float* scale, int32_t E, int64_t N,
                                     const int32_t* group_sizes, void* out,
                                     fp8moe_stream_t stream);
+
+/* ---- Tokens sorted by expert and back (no counterpart on the pages: the layer
+ * around the routed experts that the ragged buffer above belongs to).
+ *
+ * ids int32 [T, topk]: the experts that a router chose for each token, 1 <= topk
+ * <= 32, T * topk < 2^31.  Slot s = t * topk + j is token t's j-th choice.  A slot
+ * whose id is negative has no row (an expert of another rank, a padding token); so
+ * has one whose id is >= E, which also sets FP8MOE_STATUS_BAD_EXPERT.  The rows of
+ * the other slots are sorted by expert and, inside an expert, by slot: the order
+ * does not depend on scheduling.  Rows that would be at or past M are dropped,
+ * group_sizes is clipped accordingly and FP8MOE_STATUS_GROUPS_EXCEED_M set.
+ *   group_sizes int32 [E]        rows of each expert (what the grouped products take)
+ *   slot_row    int32 [T, topk]  the row of a slot, -1 for none
+ *   row_slot    int32 [M]        the slot of a row, -1 past the last (NULL: not written)
+ * All three are fully written, also when T = 0.  4-byte aligned. */
+int fp8moe_sort_tokens(const int32_t* ids, int64_t T, int32_t topk, int32_t E, int64_t M,
+                       int32_t* group_sizes, int32_t* slot_row, int32_t* row_slot,
+                       fp8moe_stream_t stream);
+
+/* fp8moe_sort_tokens, and the copy of each token to its rows:
+ *   rows[slot_row[t, j]] = x[t].   x: [T, H] of `type` (FP8MOE_TYPE_*), rows: [M, H];
+ * rows past the last are not written.  H * element size must be a multiple of 16
+ * (FP8MOE_EALIGN). */
+int fp8moe_dispatch_tokens(const void* x, const int32_t* ids, int64_t T, int32_t topk, int64_t H,
+                           int32_t type, int32_t E, int64_t M, void* rows, int32_t* group_sizes,
+                           int32_t* slot_row, int32_t* row_slot, fp8moe_stream_t stream);
+
+/* The weighted sum of a token's rows, f32 in the order of j, rounded once:
+ *   out[t] = sum_j weights[t, j] * rows[slot_row[t, j]]       (weights f32 [T, topk])
+ * weights NULL: all 1, which is also the gradient of fp8moe_dispatch_tokens (rows:
+ * the rows' gradient, out: x's).  A slot without a row, or with one outside
+ * [0, M), adds nothing, whatever its weight; a token without rows gives 0.  No other
+ * row is read. */
+int fp8moe_combine_tokens(const void* rows, int64_t M, int64_t H, int32_t type,
+                          const int32_t* slot_row, const float* weights, int64_t T, int32_t topk,
+                          void* out, fp8moe_stream_t stream);
+
+/* Gradient of fp8moe_combine_tokens:
+ *   drows[slot_row[t, j]] = weights[t, j] * dout[t]
+ *   dweights[t, j]        = sum_h dout[t, h] * rows[slot_row[t, j], h]   (f32; 0 without a row)
+ * Rows that no slot names are not written. */
+int fp8moe_combine_tokens_bwd(const void* dout, const void* rows, int64_t M, int64_t H,
+                              int32_t type, const int32_t* slot_row, const float* weights,
+                              int64_t T, int32_t topk, void* drows, float* dweights,
+                              fp8moe_stream_t stream);
+
+/* ---- Norms after and before a block, with the block's gate and the scaled
+ * residual sum (no counterpart on the pages).  x (residual stream), y (block
+ * output), r, h: [T, H] of `type`; norm weights f32 [H]; rstd f32 [T].
+ *   rstd(z) = 1 / sqrt(mean_h z^2 + eps)
+ *   r = residual_scale * x + branch_scale * g * (w_post * y * rstd(y))
+ *   h = w_pre * r * rstd(r)                 (of r before it is rounded to `type`)
+ * g: 1, or `gate` by gate_kind (FP8MOE_GATE_*), through 1 / (1 + exp(-gate)) with
+ * sigmoid = 1.  w_post NULL: no block output (y NULL, no gate); r is x, is not
+ * written, and only h is.  w_pre NULL: no h.  At least one of them is given.
+ * rstd_post and rstd_pre are what the gradient takes.  H * element size: a multiple
+ * of 16 (FP8MOE_EALIGN), at most 32768 (FP8MOE_EINVAL).  All sums are f32. */
+int fp8moe_norm_fwd(const void* x, const void* y, int64_t T, int64_t H, int32_t type,
+                    const float* w_post, const float* w_pre, const void* gate, int32_t gate_kind,
+                    int32_t sigmoid, float residual_scale, float branch_scale, float eps, void* r,
+                    void* h, float* rstd_post, float* rstd_pre, fp8moe_stream_t stream);
+
+/* Gradient of fp8moe_norm_fwd.  dr: the gradient of r from the residual stream (NULL:
+ * 0, only with w_pre); dh: of h (with w_pre); r: the forward's r (without w_post: x).
+ *   D  = dr + rstd_pre * (w_pre dh - rh * mean(w_pre dh rh)),      rh = r rstd_pre
+ *   dx = residual_scale * D,   dn = branch_scale * D * g,          yh = y rstd_post
+ *   dy = rstd_post * (w_post dn - yh * mean(w_post dn yh))
+ *   dw_pre = sum_t dh rh,   dw_post = sum_t dn yh                  (f32 [H])
+ *   dgate = branch_scale * D * w_post * yh, summed over what shares a gate value, times
+ *   g (1 - g) with sigmoid = 1: f32 [T], f32 [H] or [T, H] of `type`, by gate_kind
+ * Without w_post dx = D (r is x, unscaled).  Column sums are joined in a fixed order.
+ * T = 0 writes zeros to dw_post, dw_pre and a per-channel dgate.  Workspace: FP8MOE_OP_NORM_BWD with M = T, K = H. */
+int fp8moe_norm_bwd(const void* dr, const void* dh, const void* r, const void* y, int64_t T,
+                    int64_t H, int32_t type, const float* w_post, const float* w_pre,
+                    const float* rstd_post, const float* rstd_pre, const void* gate,
+                    int32_t gate_kind, int32_t sigmoid, float residual_scale, float branch_scale,
+                    void* dx, void* dy, float* dw_post, float* dw_pre, void* dgate,
+                    void* workspace, size_t workspace_bytes, fp8moe_stream_t stream);
+
+/* ---- Microscaled 4-bit floating point (OCP MXFP4; no counterpart on the pages):
+ * e2m1 elements (0, .5, 1, 1.5, 2, 3, 4, 6 and their negatives) in blocks of 32
+ * along K, each block with a power-of-two scale X:
+ *   X = 2^(floor(log2 max|v|) - 2), at least 2^-127;  scale byte = log2 X + 127
+ *   code = e2m1(v / X), round to nearest even, saturating
+ * A block with an infinity or a NaN gets scale byte 0xFF (NaN) and codes 0: what is
+ * computed from it is NaN.  K must be a multiple of 32, N of 16 (FP8MOE_EALIGN).
+ *   codes of weights      u8 [E, N, K/2], two a byte along K, even k in the low half
+ *   scales of weights     u8 [E, ceil(K/128), N, 4]: four consecutive blocks of a row
+ *                         together; bytes past K/32 mean nothing and are never used
+ *   codes, scales of rows u8 [M, K/2], u8 [ceil(K/128), M, 4] */
+
+/* Rows < T of lhs bf16 [M, K] (what the products do with their activations);
+ * codes and scales of rows >= T untouched. */
+int fp8moe_mxfp4_quantize_rows(const void* lhs, int64_t M, int64_t K, const int32_t* group_sizes,
+                               int32_t E, uint8_t* codes, uint8_t* scales, fp8moe_stream_t stream);
+
+/* Expert weights w bf16 [E, K, N] (N contiguous, as every weight of this library). */
+int fp8moe_mxfp4_quantize_weights(const void* w, int32_t E, int64_t K, int64_t N, uint8_t* codes,
+                                  uint8_t* scales, fp8moe_stream_t stream);
+
+/* out bf16 [E, N, K] = code * X (exact wherever bf16 can hold it).  As the weight of
+ * fp8moe_gmm_bf16_fwd, with its K and N exchanged, it gives the gradient of a
+ * product's activations taken as if they were not rounded (straight through). */
+int fp8moe_mxfp4_dequantize(const uint8_t* codes, const uint8_t* scales, int32_t E, int64_t N,
+                            int64_t K, void* out, fp8moe_stream_t stream);
+
+/* The grouped product on 4-bit weights: the activation rows are quantised as above
+ * (into the workspace), then for row m of expert e
+ *   out[m, n] = bf16( sum_k (qx Xx)[m, k] * (qw Xw)[e, n, k] )        (f32 accumulation)
+ * lhs: bf16 [M, K]; out: bf16 [M, N]; rows >= T untouched.  Any number of rows per
+ * expert, from none to all.  Workspace: FP8MOE_OP_GMM_MXFP4_FWD. */
+int fp8moe_gmm_mxfp4_fwd(const void* lhs, int64_t M, int64_t K, const uint8_t* codes,
+                         const uint8_t* scales, int32_t E, int64_t N, const int32_t* group_sizes,
+                         void* out, void* workspace, size_t workspace_bytes,
+                         fp8moe_stream_t stream);
+
+/* The same with the SwiGLU of fp8moe_gmm_silu_fp8_fwd (gate | up halves of N, N a
+ * multiple of 32): out bf16 [M, N/2].  Workspace: FP8MOE_OP_GMM_SILU_MXFP4_FWD. */
+int fp8moe_gmm_silu_mxfp4_fwd(const void* lhs, int64_t M, int64_t K, const uint8_t* codes,
+                              const uint8_t* scales, int32_t E, int64_t N,
+                              const int32_t* group_sizes, void* out, void* workspace,
+                              size_t workspace_bytes, fp8moe_stream_t stream);
 
 /* Text for a return code. */
 const char* fp8moe_status_string(int code);
