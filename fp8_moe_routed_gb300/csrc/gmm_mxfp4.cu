@@ -39,7 +39,7 @@
 #include "groups.cuh"
 #include "kernels.h"
 #include "mxfp4.cuh"
-#include "ptx.cuh"
+#include "ptx_mx.cuh"
 
 namespace fp8moe {
 namespace mxgmm {

@@ -516,53 +516,3 @@ __device__ __forceinline__ void mma_commit_pair(uint64_t* bar) {
 }
 
 }  // namespace fp8moe
-
-// ======================================================= microscaled FP4 products
-namespace fp8moe {
-
-__device__ __forceinline__ void tma_load_5d_pair(void* dst, const void* tmap,
-                                                 uint32_t bar_cluster_addr, int32_t c0, int32_t c1,
-                                                 int32_t c2, int32_t c3, int32_t c4) {
-  asm volatile(
-      "cp.async.bulk.tensor.5d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes"
-      " [%0], [%1, {%3, %4, %5, %6, %7}], [%2];"
-      ::"r"(smem_u32(dst)), "l"(tmap), "r"(bar_cluster_addr), "r"(c0), "r"(c1), "r"(c2), "r"(c3),
-        "r"(c4) : "memory");
-}
-
-// 32 lanes x 8 consecutive 32-bit columns from registers.
-__device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t (&r)[8]) {
-  asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};"
-      ::"r"(taddr), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]),
-        "r"(r[7]) : "memory");
-}
-
-// Instruction descriptor of kind::mxf4 with e8m0 scales, both operands e2m1 and
-// K-major, K = 64: scale-factor id of B in [4,6), A format in [7,10), B format in
-// [10,12) (1 = e2m1), N >> 3 in [17,23), scale format bit 23 (1 = e8m0), M >> 4 in
-// [24,29), scale-factor id of A in [29,31). The id picks the two bytes of a 32-bit
-// scale column that an instruction uses: 0 the lower, 2 the upper ones.
-__host__ __device__ constexpr uint32_t make_idesc_mxf4(uint32_t M, uint32_t N, uint32_t sf_id) {
-  return (sf_id << 4) | (1u << 7) | (1u << 10) | ((N >> 3) << 17) | (1u << 23) |
-         ((M >> 4) << 24) | (sf_id << 29);
-}
-
-// D[tmem] (+)= (A x scale_A) x (B x scale_B) over the pair, e2m1 operands in shared
-// memory, e8m0 scales of 32-value blocks in tensor memory: lane i (mod 32) and
-// column j of the scale area hold the four bytes of operand row 32 j + i, the same
-// in all four lane quarters. Each CTA holds its own 128 rows of A's scales and all
-// N rows of B's.
-__device__ __forceinline__ void mma_mxf4_pair(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc,
-                                              uint32_t idesc, uint32_t sfa, uint32_t sfb,
-                                              uint32_t accumulate) {
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "setp.ne.b32 p, %6, 0;\n\t"
-      "tcgen05.mma.cta_group::2.kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%4], [%5],"
-      " p;\n\t}"
-      ::"r"(d_tmem), "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate)
-      : "memory");
-}
-
-}  // namespace fp8moe
