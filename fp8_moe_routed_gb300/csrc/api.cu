@@ -316,9 +316,12 @@ size_t norm_bwd_ws_bytes(int64_t T, int64_t H) {
 
 int64_t mxfp4_words(int64_t K) { return (K + 127) / 128; }
 
+// The products' scale words of 128 k start on 16 bytes (a TMA stride).
+int64_t mxfp4_scale_stride(int64_t M) { return (M + 3) / 4 * 4; }
+
 size_t mxfp4_ws_bytes(int64_t M, int64_t K) {
   return round_up((size_t)M * (size_t)(K / 2), 256) +
-         round_up((size_t)M * (size_t)mxfp4_words(K) * 4, 256);
+         round_up((size_t)mxfp4_scale_stride(M) * (size_t)mxfp4_words(K) * 4, 256);
 }
 
 int check_mxfp4(int64_t M, int64_t K, int64_t N, int32_t E) {
@@ -362,8 +365,32 @@ int gmm_mxfp4_impl(const void* lhs, int64_t M, int64_t K, const uint8_t* codes,
                    CU_TENSOR_MAP_SWIZZLE_128B);
   }
   if (rc) return rc;
-  int rows[3];
-  fp8moe_gmm_mxfp4_boxes(rows);
+  const uint64_t words = (uint64_t)mxfp4_words(K), stride = (uint64_t)mxfp4_scale_stride(M);
+  int rows[3], scale_rows = 0;
+  fp8moe_gmm_mxfp4_boxes(rows, &scale_rows);
+  if (swiglu) {
+    const uint64_t F = (uint64_t)N / 2;
+    const uint64_t dims[5] = {16, 2, F / 16, words, (uint64_t)E};
+    const uint64_t st[4] = {F * 4, 64, (uint64_t)N * 4, words * (uint64_t)N * 4};
+    const uint32_t box[5] = {16, 2, 4, 2, 1};
+    rc = make_tmap(&a.tmSw, CU_TENSOR_MAP_DATA_TYPE_UINT32, 5, scales, dims, st, box,
+                   CU_TENSOR_MAP_SWIZZLE_NONE);
+  } else {
+    const uint64_t dims[3] = {(uint64_t)N, words, (uint64_t)E};
+    const uint64_t st[2] = {(uint64_t)N * 4, words * (uint64_t)N * 4};
+    const uint32_t box[3] = {128, 2, 1};
+    rc = make_tmap(&a.tmSw, CU_TENSOR_MAP_DATA_TYPE_UINT32, 3, scales, dims, st, box,
+                   CU_TENSOR_MAP_SWIZZLE_NONE);
+  }
+  if (rc) return rc;
+  {
+    const uint64_t dims[2] = {stride, words};
+    const uint64_t st[1] = {stride * 4};
+    const uint32_t box[2] = {(uint32_t)scale_rows, 2};
+    rc = make_tmap(&a.tmSx, CU_TENSOR_MAP_DATA_TYPE_UINT32, 2, sx, dims, st, box,
+                   CU_TENSOR_MAP_SWIZZLE_NONE);
+    if (rc) return rc;
+  }
   for (int i = 0; i < 3; ++i) {
     const uint64_t dims[2] = {kb, (uint64_t)M};
     const uint64_t st[1] = {kb};
@@ -372,8 +399,6 @@ int gmm_mxfp4_impl(const void* lhs, int64_t M, int64_t K, const uint8_t* codes,
                    CU_TENSOR_MAP_SWIZZLE_128B);
     if (rc) return rc;
   }
-  a.sw = scales;
-  a.sx = sx;
   a.gs = gs;
   a.out = out;
   a.M = M;
@@ -381,7 +406,8 @@ int gmm_mxfp4_impl(const void* lhs, int64_t M, int64_t K, const uint8_t* codes,
   a.N = (int)N;
   a.E = E;
   a.swiglu = swiglu;
-  cudaError_t e = fp8moe_launch_mxfp4_quantize_rows(lhs, M, (int)K, gs, E, qx, sx, sms, 1, stream);
+  cudaError_t e = fp8moe_launch_mxfp4_quantize_rows(lhs, M, (int)K, gs, E, qx, sx,
+                                                    (int64_t)stride, sms, 1, stream);
   if (e != cudaSuccess) return cuda_fail(e);
   e = fp8moe_launch_gmm_mxfp4(a, sms, stream);
   return e == cudaSuccess ? FP8MOE_OK : cuda_fail(e);
@@ -898,7 +924,7 @@ int fp8moe_mxfp4_quantize_rows(const void* lhs, int64_t M, int64_t K, const int3
   rc = device_init(&sms);
   if (rc) return rc;
   cudaError_t e = fp8moe_launch_mxfp4_quantize_rows(lhs, M, (int)K, group_sizes, E, codes, scales,
-                                                    sms, 1, stream);
+                                                    M, sms, 1, stream);
   return e == cudaSuccess ? FP8MOE_OK : cuda_fail(e);
 }
 

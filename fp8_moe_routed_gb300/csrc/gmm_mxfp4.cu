@@ -11,19 +11,23 @@
 // CTA pairs, tcgen05.mma.cta_group::2 kind::mxf4: M = 256 weight rows (128 per CTA),
 // N = the token tile (half of its rows in each CTA's shared memory), K = 64. Roles:
 //   warp 0       TMA: 256 k per stage: this CTA's 128 weight rows (16 KB) and its half
-//                of the token rows, 128-byte swizzle, 7 stages, counted on the even
+//                of the token rows, 128-byte swizzle, 6 stages, counted on the even
 //                CTA's barrier. Three token boxes (16, 48, 104 rows): a small tile
 //                does not fetch rows that it does not multiply.
 //   warp 1       TMEM; in the even CTA the MMA-issuing thread.
-//   warps 2, 3   idle.
-//   warps 4..11  scales: two groups of four that take every other stage. The scale
-//                words of a stage (2 words of each of 128 weight rows and up to 208
-//                token rows) go from global memory through registers into tensor
-//                memory (tcgen05.st), one warp per lane quarter, the same data in all
-//                four. They are fetched two stages ahead. Storing them this way and
-//                not from shared memory lets a token tile start at any row.
-//   warps 12..19 epilogue: two warps per lane quarter, alternating 16-token chunks of
-//                one of two accumulators.
+//   warp 2       TMA: the scale words of the stages (8 stages of their own, counted on
+//                this CTA's barriers).
+//   warp 3       idle.
+//   warps 4..19  scales: four groups of four that take every fourth stage. The words of a
+//                stage (2 words of each of 128 weight rows and up to 208 token rows) go
+//                from shared memory through registers into tensor memory (tcgen05.st),
+//                one warp per lane quarter, the same data in all four. Passing them
+//                through registers lets a token tile start at any row: the box starts at
+//                the next lower multiple of four (a copy starts on 16 bytes) and the
+//                warps read from the remainder on. A group's chain per stage (two waits,
+//                the TMEM store's round trip) takes about 900 cycles, a stage of MMAs 416.
+//   warps 20..27 epilogue: two groups of four (one warp per lane quarter) alternate over
+//                16-token chunks of one of two accumulators.
 // TMEM (512 columns): two accumulators of 208, four scale slots of 24.
 //
 // SwiGLU: a CTA's 128 weight rows are 4 x (16 gate rows, 16 up rows), fetched by one
@@ -53,8 +57,13 @@ constexpr int kMaxTok = 208;                 // token rows per unit = largest MM
 constexpr int kBox0 = 16, kBox1 = 48, kBox2 = 104;
 constexpr int kABytes = kRowsA * kKBytes;    // 16 KB
 constexpr int kBBytes = kBox2 * kKBytes;
-constexpr int kStageBytes = kABytes + kBBytes;
-constexpr int kStages = 7;
+constexpr int kSaBytes = 2 * kRowsA * 4;     // scale words of a stage: weight rows
+constexpr int kSbWords = kMaxTok + 4;        // token rows, from a multiple of four on
+constexpr int kSbBytes = 2 * kSbWords * 4;
+constexpr int kScaleBytes = (kSaBytes + kSbBytes + 127) / 128 * 128;
+constexpr int kCodeBytes = kABytes + kBBytes;
+constexpr int kStages = 6;                   // code stages
+constexpr int kWords = 8;                    // scale-word stages
 constexpr int kSlots = 4;
 constexpr int kSfA = 8, kSfB = 16;           // TMEM columns of a stage's scales
 constexpr int kSfCols = kSfA + kSfB;
@@ -62,15 +71,22 @@ constexpr int kDCols = kMaxTok;
 constexpr int kSfBase = 2 * kDCols;
 static_assert(kSfBase + kSlots * kSfCols <= 512, "TMEM budget");
 static_assert(kBBytes % 1024 == 0, "swizzle atoms start on 1024-byte boundaries");
+// A parity wait tells a phase from the one before it, not from the one before that: a
+// scale group has to take part in every use of its stages and slots.
+constexpr int kSfGroups = 4;
+static_assert(kWords % kSfGroups == 0 && kSlots % kSfGroups == 0, "groups own words and slots");
 constexpr int kTokWords = (kMaxTok + 31) / 32;   // scale columns of the token rows per 128 k
-constexpr int kSfGroups = 2;
 constexpr int kFirstSf = 4, kFirstEpi = kFirstSf + 4 * kSfGroups;
 constexpr int kEpiWarps = 8;
-constexpr int kThreads = (kFirstEpi + kEpiWarps) * 32;   // 640
+constexpr int kThreads = (kFirstEpi + kEpiWarps) * 32;   // 896
+constexpr int kChunk = 16;                   // token rows that four epilogue warps turn at a time
+constexpr int kTurnBytes = kChunk * kRowsA * 2;
 
 struct Smem {
-  uint64_t full[kStages];      // even CTA: all four boxes of the stage landed
+  uint64_t full[kStages];      // even CTA: all four code boxes of the stage landed
   uint64_t empty[kStages];     // the MMAs reading the stage completed
+  uint64_t words[kWords];      // this CTA's scale words landed
+  uint64_t wempty[kWords];     // and were read
   uint64_t sfull[kSlots];      // even CTA: both CTAs' scales of the slot are in TMEM
   uint64_t sempty[kSlots];     // the MMAs reading the slot completed
   uint64_t tfull[2];           // accumulator complete
@@ -83,7 +99,7 @@ struct Smem {
   int32_t end[kMaxExperts];
   int32_t prefix[kMaxExperts + 1];
 };
-constexpr size_t kSmemBytes = 1024 + (size_t)kStages * kStageBytes + sizeof(Smem);
+constexpr size_t kSmemBytes = 1024 + (size_t)kStages * kCodeBytes + (size_t)kWords * kScaleBytes + 4 * kTurnBytes + sizeof(Smem);
 static_assert(kSmemBytes <= 232448, "shared memory per CTA exceeds 227 KB");
 
 struct Unit {
@@ -114,25 +130,23 @@ __device__ __forceinline__ int box_rows(int tok) {
   return tok <= 2 * kBox0 ? kBox0 : tok <= 2 * kBox1 ? kBox1 : kBox2;
 }
 
-// A position in the sequence of (unit, stage) steps of this pair.
-struct Cursor {
-  int u, kb;
-  Unit t;
-};
-
 template <bool SWIGLU>
 __global__ void __launch_bounds__(kThreads, 1)
 gmm_mxfp4_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmX0,
                  const __grid_constant__ CUtensorMap tmX1, const __grid_constant__ CUtensorMap tmX2,
-                 const uint32_t* __restrict__ sw, const uint32_t* __restrict__ sx,
+                 const __grid_constant__ CUtensorMap tmSw, const __grid_constant__ CUtensorMap tmSx,
                  const int32_t* __restrict__ gs, __nv_bfloat16* __restrict__ out, int64_t M, int K,
                  int N, int E) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t* tiles = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                               ~uintptr_t(1023));
-  Smem& s = *reinterpret_cast<Smem*>(tiles + (size_t)kStages * kStageBytes);
-  auto a_tile = [&](int i) -> uint8_t* { return tiles + i * kStageBytes; };
-  auto b_tile = [&](int i) -> uint8_t* { return tiles + i * kStageBytes + kABytes; };
+  uint8_t* const scales = tiles + (size_t)kStages * kCodeBytes;
+  uint8_t* const turn = scales + (size_t)kWords * kScaleBytes;
+  Smem& s = *reinterpret_cast<Smem*>(turn + 4 * kTurnBytes);
+  auto a_tile = [&](int i) -> uint8_t* { return tiles + i * kCodeBytes; };
+  auto b_tile = [&](int i) -> uint8_t* { return tiles + i * kCodeBytes + kABytes; };
+  auto sa_tile = [&](int i) -> uint8_t* { return scales + i * kScaleBytes; };
+  auto sb_tile = [&](int i) -> uint8_t* { return scales + i * kScaleBytes + kSaBytes; };
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int rank = (int)cluster_ctarank();
@@ -165,12 +179,18 @@ gmm_mxfp4_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant_
       prefetch_tmap(&tmX0);
       prefetch_tmap(&tmX1);
       prefetch_tmap(&tmX2);
+      prefetch_tmap(&tmSw);
+      prefetch_tmap(&tmSx);
     }
   } else if (warp == 1) {
     if (lane == 0) {
       for (int i = 0; i < kStages; ++i) {
         mbar_init(&s.full[i], 1);
         mbar_init(&s.empty[i], 1);
+      }
+      for (int i = 0; i < kWords; ++i) {
+        mbar_init(&s.words[i], 1);
+        mbar_init(&s.wempty[i], 4);      // one group of scale warps
       }
       for (int i = 0; i < kSlots; ++i) {
         mbar_init(&s.sfull[i], 8);       // one group of four warps of each CTA
@@ -195,20 +215,22 @@ gmm_mxfp4_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant_
   const uint32_t tmem = s.tmem_base;
 
   if (warp == 0) {
-    // ============================ TMA producer ============================
-    if (lane == 0) {
-      int st = 0;
-      uint32_t ph = 0;
-      int64_t issued = 0;
-      bool ok = true;
-      for (int u = cluster; u < total && ok; u += nclusters) {
-        const Unit t = decode_unit(s, E, wt, u);
-        const int box = box_rows(t.tok);
-        const CUtensorMap* tmX = box == kBox0 ? &tmX0 : box == kBox1 ? &tmX1 : &tmX2;
-        const uint32_t bytes = 2u * (uint32_t)(kABytes + box * kKBytes);
-        const int m = t.m0 + rank * (t.tok / 2);
-        for (int kb = 0; kb < nkb; ++kb) {
-          if (!mbar_wait_cluster(&s.empty[st], ph ^ 1, kWhereProducer)) { ok = false; break; }
+    // ========================= TMA producer: codes ========================
+    // Like the MMA warp: the whole warp walks the steps, one thread issues.
+    const bool leader = elect_one();
+    int st = 0;
+    uint32_t ph = 0;
+    int64_t issued = 0;
+    bool ok = true;
+    for (int u = cluster; u < total && ok; u += nclusters) {
+      const Unit t = decode_unit(s, E, wt, u);
+      const int box = box_rows(t.tok);
+      const CUtensorMap* tmX = box == kBox0 ? &tmX0 : box == kBox1 ? &tmX1 : &tmX2;
+      const uint32_t bytes = 2u * (uint32_t)(kABytes + box * kKBytes);
+      const int m = t.m0 + rank * (t.tok / 2);
+      for (int kb = 0; kb < nkb; ++kb) {
+        if (!mbar_wait_warp_cluster(&s.empty[st], ph ^ 1, kWhereProducer)) { ok = false; break; }
+        if (leader) {
           if (rank == 0) mbar_arrive_expect_tx(&s.full[st], bytes);
           const uint32_t bar = mapa_shared(smem_u32(&s.full[st]), 0);
           if (SWIGLU)
@@ -218,58 +240,103 @@ gmm_mxfp4_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant_
             tma_load_3d_pair(a_tile(st), &tmW, bar, kb * kKBytes, t.w0 * kUnitN + rank * kRowsA,
                              t.e);
           tma_load_2d_pair(b_tile(st), tmX, bar, kb * kKBytes, m);
-          ++issued;
-          if (++st == kStages) { st = 0; ph ^= 1; }
         }
+        __syncwarp();
+        ++issued;
+        if (++st == kStages) { st = 0; ph ^= 1; }
       }
-      // drain: every copy landed before either CTA may exit
-      if (rank == 0) {
-        const int64_t n_last = issued < kStages ? issued : kStages;
-        for (int64_t i = 1; i <= n_last; ++i) {
-          const int64_t idx = issued - i;
-          mbar_wait_cluster(&s.full[idx % kStages], (uint32_t)((idx / kStages) & 1), kWhereDrain);
-        }
+    }
+    // drain: every copy landed before either CTA may exit
+    if (lane == 0 && rank == 0) {
+      const int64_t n_last = issued < kStages ? issued : kStages;
+      for (int64_t i = 1; i <= n_last; ++i) {
+        const int64_t idx = issued - i;
+        mbar_wait_cluster(&s.full[idx % kStages], (uint32_t)((idx / kStages) & 1), kWhereDrain);
       }
     }
   } else if (warp == 1) {
     // ============================== MMA issuer ============================
-    if (lane == 0 && rank == 0) {
+    // The whole warp walks the steps (so that descriptors and addresses are computed
+    // in uniform registers) and one elected thread issues.
+    if (rank == 0) {
       int st = 0, sl = 0, ab = 0;
       uint32_t ph = 0, sph = 0, tph = 0;
       bool ok = true;
+      const bool leader = elect_one();
       for (int u = cluster; u < total && ok; u += nclusters) {
         const Unit t = decode_unit(s, E, wt, u);
         const uint32_t idesc0 = make_idesc_mxf4(kUnitN, t.tok, 0);
         const uint32_t idesc2 = make_idesc_mxf4(kUnitN, t.tok, 2);
         const uint32_t d = tmem + (uint32_t)(ab * kDCols);
-        if (!mbar_wait_cluster(&s.tempty[ab], tph ^ 1, kWhereMma)) { ok = false; break; }
+        if (!mbar_wait_warp_cluster(&s.tempty[ab], tph ^ 1, kWhereMma)) { ok = false; break; }
         tc_fence_after();
         for (int kb = 0; kb < nkb; ++kb) {
-          if (!mbar_wait_cluster(&s.full[st], ph, kWhereMma)) { ok = false; break; }
-          if (!mbar_wait_cluster(&s.sfull[sl], sph, kWhereMma)) { ok = false; break; }
+          if (!mbar_wait_warp_cluster(&s.full[st], ph, kWhereMma)) { ok = false; break; }
+          if (!mbar_wait_warp_cluster(&s.sfull[sl], sph, kWhereMma)) { ok = false; break; }
           tc_fence_after();
-          const uint32_t a_addr = smem_u32(a_tile(st)), b_addr = smem_u32(b_tile(st));
+          const uint64_t ad = make_desc(smem_u32(a_tile(st)), 16, 1024, kSwizzle128B);
+          const uint64_t bd = make_desc(smem_u32(b_tile(st)), 16, 1024, kSwizzle128B);
           const uint32_t sf = tmem + (uint32_t)(kSfBase + sl * kSfCols);
-          const int steps = min(4, (K - kb * kBK + 63) / 64);
-          for (int kk = 0; kk < steps; ++kk) {
-            const uint64_t ad = make_desc(a_addr + kk * 32, 16, 1024, kSwizzle128B);
-            const uint64_t bd = make_desc(b_addr + kk * 32, 16, 1024, kSwizzle128B);
-            mma_mxf4_pair(d, ad, bd, (kk & 1) ? idesc2 : idesc0, sf + (kk >> 1) * (kSfA / 2),
-                          sf + kSfA + (kk >> 1) * (kSfB / 2), (kb | kk) != 0);
+          const int steps = (K - kb * kBK + 63) / 64;
+          if (leader) {
+#pragma unroll
+            for (int kk = 0; kk < 4; ++kk) {
+              // the descriptors' address field counts 16 bytes: 64 values are two
+              if (kk < steps)
+                mma_mxf4_pair(d, ad + 2 * kk, bd + 2 * kk, (kk & 1) ? idesc2 : idesc0,
+                              sf + (kk >> 1) * (kSfA / 2), sf + kSfA + (kk >> 1) * (kSfB / 2),
+                              (kb | kk) != 0);
+            }
+            mma_commit_pair(&s.empty[st]);
+            mma_commit_pair(&s.sempty[sl]);
           }
-          mma_commit_pair(&s.empty[st]);
-          mma_commit_pair(&s.sempty[sl]);
+          __syncwarp();
           if (++st == kStages) { st = 0; ph ^= 1; }
           if (++sl == kSlots) { sl = 0; sph ^= 1; }
         }
         if (!ok) break;
-        mma_commit_pair(&s.tfull[ab]);
+        if (leader) mma_commit_pair(&s.tfull[ab]);
+        __syncwarp();
         if (++ab == 2) { ab = 0; tph ^= 1; }
       }
       // all MMAs complete (in both CTAs' TMEM) before TMEM may be released
-      mma_commit_pair(&s.drain);
+      if (leader) mma_commit_pair(&s.drain);
+      __syncwarp();
     }
     if (lane == 0) mbar_wait_cluster(&s.drain, 0, kWhereDrain);
+  } else if (warp == 2) {
+    // ===================== TMA producer: scale words ======================
+    const bool leader = elect_one();
+    int st = 0;
+    uint32_t ph = 0;
+    int64_t issued = 0;
+    bool ok = true;
+    for (int u = cluster; u < total && ok; u += nclusters) {
+      const Unit t = decode_unit(s, E, wt, u);
+      for (int kb = 0; kb < nkb; ++kb) {
+        if (!mbar_wait_warp(&s.wempty[st], ph ^ 1, kWhereProducer)) { ok = false; break; }
+        if (leader) {
+          mbar_arrive_expect_tx(&s.words[st], kSaBytes + kSbBytes);
+          if (SWIGLU)
+            tma_load_5d(sa_tile(st), &tmSw, &s.words[st], 0, 0, t.w0 * (kRowsA / 16) + rank * 4,
+                        2 * kb, t.e);
+          else
+            tma_load_3d(sa_tile(st), &tmSw, &s.words[st], t.w0 * kUnitN + rank * kRowsA, 2 * kb,
+                        t.e);
+          tma_load_2d(sb_tile(st), &tmSx, &s.words[st], t.m0 & ~3, 2 * kb);
+        }
+        __syncwarp();
+        ++issued;
+        if (++st == kWords) { st = 0; ph ^= 1; }
+      }
+    }
+    if (lane == 0) {
+      const int64_t n_last = issued < kWords ? issued : kWords;
+      for (int64_t i = 1; i <= n_last; ++i) {
+        const int64_t idx = issued - i;
+        mbar_wait(&s.words[idx % kWords], (uint32_t)((idx / kWords) & 1), kWhereDrain);
+      }
+    }
   } else if (warp < kFirstSf) {
     // idle
   } else if (warp < kFirstEpi) {
@@ -281,73 +348,43 @@ gmm_mxfp4_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant_
     const int words = (K + kMxWord - 1) / kMxWord;
     const int last_blocks = (K - (words - 1) * kMxWord) / kMxBlock;     // of the last word: 1..4
     const uint32_t last_mask = last_blocks == 4 ? 0xFFFFFFFFu : (1u << (8 * last_blocks)) - 1u;
-    auto next = [&](Cursor& c, int by) {       // false past the last step
-      c.kb += by;
-      while (c.kb >= nkb) {
-        c.kb -= nkb;
-        c.u += nclusters;
-        if (c.u >= total) return false;
-        c.t = decode_unit(s, E, wt, c.u);
-      }
-      return true;
-    };
-    auto fetch = [&](const Cursor& c, uint32_t (&wa)[8], uint32_t (&wb)[16]) {
+    uint32_t i = 0;                                // global step index (word stages and slots)
+    bool ok = true;
+    for (int u = cluster; u < total && ok; u += nclusters) {
+      const Unit t = decode_unit(s, E, wt, u);
+      const int shift = t.m0 & 3;
+      for (int kb = 0; kb < nkb; ++kb, ++i) {
+        if ((int)(i % kSfGroups) != group) continue;
+        const int st = (int)(i % kWords), sl = (int)(i % kSlots);
+        if (!mbar_wait_warp(&s.words[st], (i / kWords) & 1, kWhereDequant)) { ok = false; break; }
+        const uint32_t* const pa = reinterpret_cast<const uint32_t*>(sa_tile(st)) + lane;
+        const uint32_t* const pb = reinterpret_cast<const uint32_t*>(sb_tile(st)) + shift + lane;
+        uint32_t wa[8], wb[16];
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const int word = 2 * c.kb + h;
-        const uint32_t mask = word >= words ? 0u : word == words - 1 ? last_mask : 0xFFFFFFFFu;
-        const uint32_t* pa = sw + ((int64_t)c.t.e * words + word) * N;
+        for (int h = 0; h < 2; ++h) {
+          // past the last word the boxes are filled with zeros
+          const uint32_t mask = 2 * kb + h == words - 1 ? last_mask : 0xFFFFFFFFu;
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          int n;
-          bool in;
-          if (SWIGLU) {
-            const int f = c.t.w0 * kRowsA + rank * 64 + j * 16 + (lane & 15);
-            n = (lane >> 4) * F + f;
-            in = f < F;
-          } else {
-            n = c.t.w0 * kUnitN + rank * kRowsA + j * 32 + lane;
-            in = n < N;
-          }
-          wa[h * 4 + j] = (in && mask) ? __ldg(pa + n) & mask : 0u;
+          for (int j = 0; j < 4; ++j) wa[h * 4 + j] = pa[h * kRowsA + j * 32] & mask;
+#pragma unroll
+          for (int j = 0; j < 8; ++j)
+            wb[h * 8 + j] = j < kTokWords && j * 32 + lane < kMaxTok
+                                ? pb[h * kSbWords + j * 32] & mask : 0u;
         }
-        const uint32_t* pb = sx + (int64_t)word * M + c.t.m0;
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          const int m = j * 32 + lane;
-          wb[h * 8 + j] = (j < kTokWords && m < c.t.rows && mask) ? __ldg(pb + m) & mask : 0u;
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&s.wempty[st]);     // words read
+        if (!mbar_wait_warp_cluster(&s.sempty[sl], ((i / kSlots) & 1) ^ 1, kWhereDequant)) {
+          ok = false;
+          break;
         }
+        tc_fence_after();
+        tmem_st8(tq + (uint32_t)(sl * kSfCols), wa);
+        tmem_st16(tq + (uint32_t)(sl * kSfCols + kSfA), wb);
+        tmem_st_wait();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive_cluster_relaxed(even_sfull + (uint32_t)(sl * sizeof(uint64_t)));
       }
-    };
-    Cursor c;
-    c.u = cluster;
-    c.kb = 0;
-    bool more = cluster < total;
-    if (more) {
-      c.t = decode_unit(s, E, wt, c.u);
-      if (group) more = next(c, group);
-    }
-    uint32_t wa[8], wb[16];
-    if (more) fetch(c, wa, wb);
-    for (uint32_t i = (uint32_t)group; more; i += kSfGroups) {
-      const int sl = (int)(i % kSlots);
-      const uint32_t sph = (i / kSlots) & 1;
-      uint32_t na[8], nb[16];
-      const bool again = next(c, kSfGroups);
-      if (again) fetch(c, na, nb);
-      if (!mbar_wait_warp_cluster(&s.sempty[sl], sph ^ 1, kWhereDequant)) break;
-      tc_fence_after();
-      tmem_st8(tq + (uint32_t)(sl * kSfCols), wa);
-      tmem_st16(tq + (uint32_t)(sl * kSfCols + kSfA), wb);
-      tmem_st_wait();
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive_cluster_relaxed(even_sfull + (uint32_t)(sl * sizeof(uint64_t)));
-#pragma unroll
-      for (int j = 0; j < 8; ++j) wa[j] = na[j];
-#pragma unroll
-      for (int j = 0; j < 16; ++j) wb[j] = nb[j];
-      more = again;
     }
   } else {
     // =============================== epilogue =============================
@@ -355,43 +392,58 @@ gmm_mxfp4_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant_
     const int half = (warp - kFirstEpi) >> 2;
     const uint32_t tq = tmem + ((uint32_t)(quarter * 32) << 16);
     const uint32_t even_tempty = mapa_shared(smem_u32(&s.tempty[0]), 0);
-    int ab = 0;
+    // The accumulator has a column per token; the output wants whole rows. Four warps turn
+    // 16 tokens x their 128 weight rows through shared memory and store 16 bytes a lane,
+    // 256 (SwiGLU: 128) contiguous bytes of a token.
+    constexpr int kCols = SWIGLU ? kRowsA / 2 : kRowsA;     // outputs of a token in this CTA
+    constexpr int kPieces = kCols / 8;
+    const int width = SWIGLU ? F : N;
+    int ab = 0, buf = 0;
     uint32_t tph = 0;
     uint16_t* const o16 = reinterpret_cast<uint16_t*>(out);
     for (int u = cluster; u < total; u += nclusters) {
       const Unit t = decode_unit(s, E, wt, u);
-      if (!mbar_wait_warp_cluster(&s.tfull[ab], tph, kWhereEpilogue)) break;
+      // the four warps leave together: a named barrier's wait has no limit
+      if (!named_bar_all(1 + half, 128, mbar_wait_warp_cluster(&s.tfull[ab], tph, kWhereEpilogue)))
+        break;
       tc_fence_after();
-      for (int c0 = half * 16; c0 < t.tok; c0 += 32) {
-        uint32_t w[16];
+      const int col0 = SWIGLU ? t.w0 * kRowsA + rank * 64 : t.w0 * kUnitN + rank * kRowsA;
+      for (int c0 = half * kChunk; c0 < t.tok; c0 += 2 * kChunk) {
+        uint32_t w[kChunk];
         tmem_ld16(tq + (uint32_t)(ab * kDCols + c0), w);
         tmem_ld_wait();
-        const int64_t row0 = (int64_t)t.m0 + c0;
+        uint16_t* const mine = reinterpret_cast<uint16_t*>(turn + (2 * half + buf) * kTurnBytes);
         if (SWIGLU) {
           const bool up = lane >= 16;
-          const int f = t.w0 * kRowsA + rank * 64 + quarter * 16 + (lane & 15);
+          uint16_t* const p = mine + (up ? kCols : 0) + quarter * 16 + (lane & 15);
 #pragma unroll
-          for (int j = 0; j < 16; j += 2) {
+          for (int j = 0; j < kChunk; j += 2) {
             // lanes 0..15 take token j, lanes 16..31 token j + 1
             const float send = __uint_as_float(up ? w[j] : w[j + 1]);
             const float got = __shfl_xor_sync(0xffffffffu, send, 16);
             const float g = up ? got : __uint_as_float(w[j]);
             const float v = up ? __uint_as_float(w[j + 1]) : got;
             const float h = __fmul_rn(__fdiv_rn(g, __fadd_rn(1.0f, expf(-g))), v);
-            const int jj = j + (up ? 1 : 0);
-            if (f < F && c0 + jj < t.rows)
-              o16[(row0 + jj) * F + f] = (uint16_t)(f32x2_to_bf16x2(h, 0.0f) & 0xFFFFu);
+            p[j * kCols] = (uint16_t)(f32x2_to_bf16x2(h, 0.0f) & 0xFFFFu);
           }
         } else {
-          const int n = t.w0 * kUnitN + rank * kRowsA + quarter * 32 + lane;
-          if (n < N) {
+          uint16_t* const p = mine + quarter * 32 + lane;
 #pragma unroll
-            for (int j = 0; j < 16; ++j)
-              if (c0 + j < t.rows)
-                o16[(row0 + j) * N + n] =
-                    (uint16_t)(f32x2_to_bf16x2(__uint_as_float(w[j]), 0.0f) & 0xFFFFu);
-          }
+          for (int j = 0; j < kChunk; ++j)
+            p[j * kCols] = (uint16_t)(f32x2_to_bf16x2(__uint_as_float(w[j]), 0.0f) & 0xFFFFu);
         }
+        // the barrier also orders this turn's writes after the reads of the one before
+        // the last, which had the same buffer
+        named_bar_sync(1 + half, 128);
+        const uint4* const src = reinterpret_cast<const uint4*>(mine);
+#pragma unroll
+        for (int i = 0; i < kChunk * kPieces / 128; ++i) {
+          const int q = i * 128 + quarter * 32 + lane;
+          const int j = q / kPieces, col = col0 + (q % kPieces) * 8;
+          if (c0 + j < t.rows && col < width)
+            *reinterpret_cast<uint4*>(o16 + ((int64_t)t.m0 + c0 + j) * width + col) = src[q];
+        }
+        buf ^= 1;
       }
       tc_fence_before();
       __syncwarp();
@@ -426,9 +478,8 @@ cudaError_t launch(const GmmMxfp4Args& a, int num_sms, cudaStream_t s) {
   attr[0].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  err = cudaLaunchKernelEx(&cfg, kern, a.tmW, a.tmX[0], a.tmX[1], a.tmX[2],
-                           reinterpret_cast<const uint32_t*>(a.sw),
-                           reinterpret_cast<const uint32_t*>(a.sx), a.gs,
+  err = cudaLaunchKernelEx(&cfg, kern, a.tmW, a.tmX[0], a.tmX[1], a.tmX[2], a.tmSw,
+                           a.tmSx, a.gs,
                            static_cast<__nv_bfloat16*>(a.out), a.M, a.K, a.N, a.E);
   if (err != cudaSuccess) return err;
   return cudaGetLastError();
@@ -439,11 +490,12 @@ cudaError_t launch(const GmmMxfp4Args& a, int num_sms, cudaStream_t s) {
 
 FP8MOE_DEFINE_STATUS_TAKE(fp8moe_status_take_gmm_mxfp4)
 
-void fp8moe_gmm_mxfp4_boxes(int rows[3]) {
+void fp8moe_gmm_mxfp4_boxes(int rows[3], int* scale_rows) {
   using namespace fp8moe::mxgmm;
   rows[0] = kBox0;
   rows[1] = kBox1;
   rows[2] = kBox2;
+  *scale_rows = kSbWords;
 }
 
 cudaError_t fp8moe_launch_gmm_mxfp4(const GmmMxfp4Args& a, int num_sms, cudaStream_t s) {

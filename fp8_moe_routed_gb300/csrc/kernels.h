@@ -154,9 +154,11 @@ cudaError_t fp8moe_launch_norm_bwd(const NormBwdArgs& a, int num_sms, cudaStream
 uint32_t fp8moe_status_take_norm(cudaStream_t s);
 
 // Microscaled 4-bit quantisation (mxfp4.cu).
+// scale_stride: words between the scale words of consecutive 128 k (>= M).
 cudaError_t fp8moe_launch_mxfp4_quantize_rows(const void* x, int64_t M, int K, const int32_t* gs,
-                                              int E, uint8_t* codes, uint8_t* scales, int num_sms,
-                                              int report, cudaStream_t s);
+                                              int E, uint8_t* codes, uint8_t* scales,
+                                              int64_t scale_stride, int num_sms, int report,
+                                              cudaStream_t s);
 cudaError_t fp8moe_launch_mxfp4_quantize_weights(const void* w, int E, int K, int N, uint8_t* codes,
                                                  uint8_t* scales, cudaStream_t s);
 cudaError_t fp8moe_launch_mxfp4_dequantize(const uint8_t* codes, const uint8_t* scales, int E,
@@ -168,13 +170,14 @@ struct GmmMxfp4Args {
   CUtensorMap tmW;          // weight codes: [E, N, K/2] boxes of 128 rows, or with SwiGLU
                             // [E, F/16, 2, 16, K/2] boxes of 4 x 2 x 16 rows
   CUtensorMap tmX[3];       // activation codes [M, K/2], boxes of fp8moe_gmm_mxfp4_boxes() rows
-  const uint8_t* sw;        // [E, ceil(K/128), N, 4]
-  const uint8_t* sx;        // [ceil(K/128), M, 4]
+  CUtensorMap tmSw;         // weight scale words [E, ceil(K/128), N], boxes of 2 x 128, or with
+                            // SwiGLU [E, ceil(K/128), F/16, 2, 16], boxes of 2 x 4 x 2 x 16
+  CUtensorMap tmSx;         // activation scale words [ceil(K/128), M], boxes of 2 x scale_rows
   const int32_t* gs;
   void* out;                // bf16 [M, N] or [M, N/2]
   int64_t M;
   int K, N, E, swiglu;
 };
-void fp8moe_gmm_mxfp4_boxes(int rows[3]);
+void fp8moe_gmm_mxfp4_boxes(int rows[3], int* scale_rows);
 cudaError_t fp8moe_launch_gmm_mxfp4(const GmmMxfp4Args& a, int num_sms, cudaStream_t s);
 uint32_t fp8moe_status_take_gmm_mxfp4(cudaStream_t s);

@@ -49,7 +49,7 @@ constexpr int kRowsUnroll = 4;
 __global__ void __launch_bounds__(kRowsThreads)
 mx_quantize_rows_kernel(const uint4* __restrict__ x, int64_t M, int K,
                         const int32_t* __restrict__ gs, int E, uint32_t* __restrict__ codes,
-                        uint32_t* __restrict__ scales, int report) {
+                        uint32_t* __restrict__ scales, int64_t scale_stride, int report) {
   __shared__ int32_t s_lo, s_hi;
   group_row_range_warp0(gs, E, M, 0, E, &s_lo, &s_hi, report && blockIdx.x == 0);
   __syncthreads();
@@ -78,7 +78,7 @@ mx_quantize_rows_kernel(const uint4* __restrict__ x, int64_t M, int K,
       uint32_t word = byte << (8 * ((lane >> 2) & 3));
       word |= __shfl_xor_sync(0xffffffffu, word, 4);
       word |= __shfl_xor_sync(0xffffffffu, word, 8);
-      if ((lane & 15) == 0 && vi < nvec) scales[(int64_t)(vi / 16) * M + row] = word;
+      if ((lane & 15) == 0 && vi < nvec) scales[(vi / 16) * scale_stride + row] = word;
     }
   }
 }
@@ -208,13 +208,14 @@ int grid_for(int64_t items, int num_sms) {
 FP8MOE_DEFINE_STATUS_TAKE(fp8moe_status_take_mxfp4)
 
 cudaError_t fp8moe_launch_mxfp4_quantize_rows(const void* x, int64_t M, int K, const int32_t* gs,
-                                              int E, uint8_t* codes, uint8_t* scales, int num_sms,
-                                              int report, cudaStream_t s) {
+                                              int E, uint8_t* codes, uint8_t* scales,
+                                              int64_t scale_stride, int num_sms, int report,
+                                              cudaStream_t s) {
   using namespace fp8moe::mx;
   const int chunks = (K / 8 + 32 * kRowsUnroll - 1) / (32 * kRowsUnroll);
   mx_quantize_rows_kernel<<<grid_for(M * chunks, num_sms), kRowsThreads, 0, s>>>(
       static_cast<const uint4*>(x), M, K, gs, E, reinterpret_cast<uint32_t*>(codes),
-      reinterpret_cast<uint32_t*>(scales), report);
+      reinterpret_cast<uint32_t*>(scales), scale_stride, report);
   return cudaGetLastError();
 }
 
