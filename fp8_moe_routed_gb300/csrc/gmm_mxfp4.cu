@@ -83,21 +83,20 @@ constexpr int kChunk = 16;                   // token rows that four epilogue wa
 constexpr int kTurnBytes = kChunk * kRowsA * 2;
 
 struct Smem {
-  uint64_t full[kStages];      // even CTA: all four code boxes of the stage landed
-  uint64_t empty[kStages];     // the MMAs reading the stage completed
+  uint64_t full[kStages];      // even CTA: the stage's four code boxes landed and both CTAs'
+                               // scales are in TMEM
+  uint64_t empty[kStages];     // the MMAs of the stage completed (and of its scale slot)
   uint64_t words[kWords];      // this CTA's scale words landed
   uint64_t wempty[kWords];     // and were read
-  uint64_t sfull[kSlots];      // even CTA: both CTAs' scales of the slot are in TMEM
-  uint64_t sempty[kSlots];     // the MMAs reading the slot completed
   uint64_t tfull[2];           // accumulator complete
   uint64_t tempty[2];          // even CTA: both CTAs' epilogues loaded it
   uint64_t drain;
   uint32_t tmem_base;
   int32_t T;
   int32_t total_units;
-  int32_t begin[kMaxExperts];
-  int32_t end[kMaxExperts];
-  int32_t prefix[kMaxExperts + 1];
+  int32_t begin[kMaxExperts + 1];    // [e + 1] is also where expert e ends
+  int32_t prefix[kMaxExperts + 1];   // units before expert e
+  uint8_t tok[kMaxExperts];          // token rows of its tiles
 };
 constexpr size_t kSmemBytes = 1024 + (size_t)kStages * kCodeBytes + (size_t)kWords * kScaleBytes + 4 * kTurnBytes + sizeof(Smem);
 static_assert(kSmemBytes <= 232448, "shared memory per CTA exceeds 227 KB");
@@ -108,20 +107,28 @@ struct Unit {
 
 __device__ __forceinline__ int token_tiles(int rows) { return (rows + kMaxTok - 1) / kMaxTok; }
 
-// Units: expert by expert, token tiles, weight tiles fastest (their shared token
-// tile stays in L2). Tiles of equal size: with t = ceil(rows / 208) tiles of
-// ceil(rows / t) rounded up to 16, which is <= 208, the last one is never empty.
-__device__ __forceinline__ Unit decode_unit(const Smem& s, int E, int wt, int u) {
+// Token rows of an expert's tiles: equal tiles, t = ceil(rows / 208) of ceil(rows / t)
+// rounded up to 16. That is <= 208, so the last of the t tiles is never empty.
+__device__ __forceinline__ int tile_rows(int rows) {
+  const int t = max(1, token_tiles(rows));
+  return ((rows + t - 1) / t + 15) & ~15;
+}
+
+// Units: expert by expert, token tiles, weight tiles fastest (their shared token tile
+// stays in L2). `e`: the expert of an earlier unit of the caller, 0 at first.
+__device__ __forceinline__ int expert_of(const Smem& s, int u, int e) {
+  while (u >= s.prefix[e + 1]) ++e;
+  return e;
+}
+__device__ __forceinline__ Unit decode_unit(const Smem& s, int wt, int u, int e) {
   Unit r;
-  r.e = find_bucket(s.prefix, E, u);
+  r.e = expert_of(s, u, e);
   const int local = u - s.prefix[r.e];
   const int mi = local / wt;
   r.w0 = local - mi * wt;
-  const int rows = s.end[r.e] - s.begin[r.e];
-  const int tiles = token_tiles(rows);
-  r.tok = ((rows + tiles - 1) / tiles + 15) & ~15;
+  r.tok = s.tok[r.e];
   r.m0 = s.begin[r.e] + mi * r.tok;
-  r.rows = min(r.tok, s.end[r.e] - r.m0);
+  r.rows = min(r.tok, s.begin[r.e + 1] - r.m0);
   return r;
 }
 
@@ -156,13 +163,17 @@ gmm_mxfp4_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant_
   const int nkb = (K + kBK - 1) / kBK;
 
   if (warp == 0) {
-    load_groups_warp0(gs, E, M, s.begin, s.end, &s.T, blockIdx.x == 0);
+    load_groups_warp0(gs, E, M, s.begin, s.begin + 1, &s.T, blockIdx.x == 0);
     __syncwarp();
     int32_t carry = 0;
     for (int base = 0; base < E; base += 32) {
       const int e = base + lane;
       int32_t n = 0;
-      if (e < E) n = token_tiles(s.end[e] - s.begin[e]) * wt;
+      if (e < E) {
+        const int rows = s.begin[e + 1] - s.begin[e];
+        n = token_tiles(rows) * wt;
+        s.tok[e] = (uint8_t)tile_rows(rows);
+      }
       int32_t incl = n;
 #pragma unroll
       for (int d = 1; d < 32; d <<= 1) {
@@ -185,16 +196,12 @@ gmm_mxfp4_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant_
   } else if (warp == 1) {
     if (lane == 0) {
       for (int i = 0; i < kStages; ++i) {
-        mbar_init(&s.full[i], 1);
+        mbar_init(&s.full[i], 1 + 8);    // the producer's bytes + a group of scale warps per CTA
         mbar_init(&s.empty[i], 1);
       }
       for (int i = 0; i < kWords; ++i) {
         mbar_init(&s.words[i], 1);
         mbar_init(&s.wempty[i], 4);      // one group of scale warps
-      }
-      for (int i = 0; i < kSlots; ++i) {
-        mbar_init(&s.sfull[i], 8);       // one group of four warps of each CTA
-        mbar_init(&s.sempty[i], 1);
       }
       for (int i = 0; i < 2; ++i) {
         mbar_init(&s.tfull[i], 1);
@@ -218,18 +225,19 @@ gmm_mxfp4_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant_
     // ========================= TMA producer: codes ========================
     // Like the MMA warp: the whole warp walks the steps, one thread issues.
     const bool leader = elect_one();
-    int st = 0;
+    int st = 0, e = 0;
     uint32_t ph = 0;
     int64_t issued = 0;
     bool ok = true;
     for (int u = cluster; u < total && ok; u += nclusters) {
-      const Unit t = decode_unit(s, E, wt, u);
+      const Unit t = decode_unit(s, wt, u, e);
+      e = t.e;
       const int box = box_rows(t.tok);
       const CUtensorMap* tmX = box == kBox0 ? &tmX0 : box == kBox1 ? &tmX1 : &tmX2;
       const uint32_t bytes = 2u * (uint32_t)(kABytes + box * kKBytes);
       const int m = t.m0 + rank * (t.tok / 2);
       for (int kb = 0; kb < nkb; ++kb) {
-        if (!mbar_wait_warp_cluster(&s.empty[st], ph ^ 1, kWhereProducer)) { ok = false; break; }
+        if (!mbar_wait_warp(&s.empty[st], ph ^ 1, kWhereProducer)) { ok = false; break; }
         if (leader) {
           if (rank == 0) mbar_arrive_expect_tx(&s.full[st], bytes);
           const uint32_t bar = mapa_shared(smem_u32(&s.full[st]), 0);
@@ -251,68 +259,67 @@ gmm_mxfp4_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant_
       const int64_t n_last = issued < kStages ? issued : kStages;
       for (int64_t i = 1; i <= n_last; ++i) {
         const int64_t idx = issued - i;
-        mbar_wait_cluster(&s.full[idx % kStages], (uint32_t)((idx / kStages) & 1), kWhereDrain);
+        mbar_wait(&s.full[idx % kStages], (uint32_t)((idx / kStages) & 1), kWhereDrain);
       }
     }
   } else if (warp == 1) {
     // ============================== MMA issuer ============================
-    // The whole warp walks the steps (so that descriptors and addresses are computed
-    // in uniform registers) and one elected thread issues.
-    if (rank == 0) {
-      int st = 0, sl = 0, ab = 0;
-      uint32_t ph = 0, sph = 0, tph = 0;
-      bool ok = true;
-      const bool leader = elect_one();
+    // One elected thread walks the steps: a branch on elect.sync (unlike one on the lane
+    // number) tells the compiler that a single thread runs it, so that descriptors and
+    // addresses go to uniform registers without a loop over the warp's values.
+    if (rank == 0 && elect_one()) {
+      int st = 0, sl = 0, ab = 0, e = 0;
+      uint32_t ph = 0, tph = 0;
+      bool ok = true, ready = false;
       for (int u = cluster; u < total && ok; u += nclusters) {
-        const Unit t = decode_unit(s, E, wt, u);
-        const uint32_t idesc0 = make_idesc_mxf4(kUnitN, t.tok, 0);
-        const uint32_t idesc2 = make_idesc_mxf4(kUnitN, t.tok, 2);
+        e = expert_of(s, u, e);
+        const uint32_t idesc0 = make_idesc_mxf4(kUnitN, s.tok[e], 0);
+        const uint32_t idesc2 = make_idesc_mxf4(kUnitN, s.tok[e], 2);
         const uint32_t d = tmem + (uint32_t)(ab * kDCols);
-        if (!mbar_wait_warp_cluster(&s.tempty[ab], tph ^ 1, kWhereMma)) { ok = false; break; }
+        if (!mbar_wait(&s.tempty[ab], tph ^ 1, kWhereMma)) { ok = false; break; }
         tc_fence_after();
         for (int kb = 0; kb < nkb; ++kb) {
-          if (!mbar_wait_warp_cluster(&s.full[st], ph, kWhereMma)) { ok = false; break; }
-          if (!mbar_wait_warp_cluster(&s.sfull[sl], sph, kWhereMma)) { ok = false; break; }
+          // a wait costs its latency even when there is nothing to wait for, so the next
+          // step's barrier is tested before this step's products are issued
+          if (!ready && !mbar_wait(&s.full[st], ph, kWhereMma)) { ok = false; break; }
           tc_fence_after();
           const uint64_t ad = make_desc(smem_u32(a_tile(st)), 16, 1024, kSwizzle128B);
           const uint64_t bd = make_desc(smem_u32(b_tile(st)), 16, 1024, kSwizzle128B);
           const uint32_t sf = tmem + (uint32_t)(kSfBase + sl * kSfCols);
           const int steps = (K - kb * kBK + 63) / 64;
-          if (leader) {
-#pragma unroll
-            for (int kk = 0; kk < 4; ++kk) {
-              // the descriptors' address field counts 16 bytes: 64 values are two
-              if (kk < steps)
-                mma_mxf4_pair(d, ad + 2 * kk, bd + 2 * kk, (kk & 1) ? idesc2 : idesc0,
-                              sf + (kk >> 1) * (kSfA / 2), sf + kSfA + (kk >> 1) * (kSfB / 2),
-                              (kb | kk) != 0);
-            }
-            mma_commit_pair(&s.empty[st]);
-            mma_commit_pair(&s.sempty[sl]);
-          }
-          __syncwarp();
+          uint64_t* const done = &s.empty[st];
           if (++st == kStages) { st = 0; ph ^= 1; }
-          if (++sl == kSlots) { sl = 0; sph ^= 1; }
+          if (++sl == kSlots) sl = 0;
+          ready = mbar_test(&s.full[st], ph);
+#pragma unroll
+          for (int kk = 0; kk < 4; ++kk) {
+            // the descriptors' address field counts 16 bytes: 64 values are two
+            if (kk < steps)
+              mma_mxf4_pair(d, ad + 2 * kk, bd + 2 * kk, (kk & 1) ? idesc2 : idesc0,
+                            sf + (kk >> 1) * (kSfA / 2), sf + kSfA + (kk >> 1) * (kSfB / 2),
+                            (kb | kk) != 0);
+          }
+          mma_commit_pair(done);
         }
         if (!ok) break;
-        if (leader) mma_commit_pair(&s.tfull[ab]);
-        __syncwarp();
+        mma_commit_pair(&s.tfull[ab]);
         if (++ab == 2) { ab = 0; tph ^= 1; }
       }
       // all MMAs complete (in both CTAs' TMEM) before TMEM may be released
-      if (leader) mma_commit_pair(&s.drain);
-      __syncwarp();
+      mma_commit_pair(&s.drain);
     }
-    if (lane == 0) mbar_wait_cluster(&s.drain, 0, kWhereDrain);
+    __syncwarp();
+    if (lane == 0) mbar_wait(&s.drain, 0, kWhereDrain);
   } else if (warp == 2) {
     // ===================== TMA producer: scale words ======================
     const bool leader = elect_one();
-    int st = 0;
+    int st = 0, e = 0;
     uint32_t ph = 0;
     int64_t issued = 0;
     bool ok = true;
     for (int u = cluster; u < total && ok; u += nclusters) {
-      const Unit t = decode_unit(s, E, wt, u);
+      const Unit t = decode_unit(s, wt, u, e);
+      e = t.e;
       for (int kb = 0; kb < nkb; ++kb) {
         if (!mbar_wait_warp(&s.wempty[st], ph ^ 1, kWhereProducer)) { ok = false; break; }
         if (leader) {
@@ -344,14 +351,16 @@ gmm_mxfp4_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant_
     const int quarter = warp & 3;
     const int group = (warp - kFirstSf) >> 2;
     const uint32_t tq = tmem + ((uint32_t)(quarter * 32) << 16) + (uint32_t)kSfBase;
-    const uint32_t even_sfull = mapa_shared(smem_u32(&s.sfull[0]), 0);
+    const uint32_t even_full = mapa_shared(smem_u32(&s.full[0]), 0);
     const int words = (K + kMxWord - 1) / kMxWord;
     const int last_blocks = (K - (words - 1) * kMxWord) / kMxBlock;     // of the last word: 1..4
     const uint32_t last_mask = last_blocks == 4 ? 0xFFFFFFFFu : (1u << (8 * last_blocks)) - 1u;
+    int e = 0;
     uint32_t i = 0;                                // global step index (word stages and slots)
     bool ok = true;
     for (int u = cluster; u < total && ok; u += nclusters) {
-      const Unit t = decode_unit(s, E, wt, u);
+      const Unit t = decode_unit(s, wt, u, e);
+      e = t.e;
       const int shift = t.m0 & 3;
       for (int kb = 0; kb < nkb; ++kb, ++i) {
         if ((int)(i % kSfGroups) != group) continue;
@@ -373,9 +382,15 @@ gmm_mxfp4_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant_
         }
         __syncwarp();
         if (lane == 0) mbar_arrive(&s.wempty[st]);     // words read
-        if (!mbar_wait_warp_cluster(&s.sempty[sl], ((i / kSlots) & 1) ^ 1, kWhereDequant)) {
-          ok = false;
-          break;
+        // The slot was last read by the products of step i - kSlots: their stage's
+        // barrier tells. The phase it may be mistaken for, step i - kSlots - 2 kStages's,
+        // is past: this group has waited for step i - 2 kSlots, in order, before.
+        if (i >= kSlots) {
+          const uint32_t j = i - kSlots;
+          if (!mbar_wait_warp(&s.empty[j % kStages], (j / kStages) & 1, kWhereDequant)) {
+            ok = false;
+            break;
+          }
         }
         tc_fence_after();
         tmem_st8(tq + (uint32_t)(sl * kSfCols), wa);
@@ -383,7 +398,7 @@ gmm_mxfp4_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant_
         tmem_st_wait();
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive_cluster_relaxed(even_sfull + (uint32_t)(sl * sizeof(uint64_t)));
+        if (lane == 0) mbar_arrive_cluster_relaxed(even_full + (uint32_t)((i % kStages) * sizeof(uint64_t)));
       }
     }
   } else {
@@ -398,13 +413,14 @@ gmm_mxfp4_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant_
     constexpr int kCols = SWIGLU ? kRowsA / 2 : kRowsA;     // outputs of a token in this CTA
     constexpr int kPieces = kCols / 8;
     const int width = SWIGLU ? F : N;
-    int ab = 0, buf = 0;
+    int ab = 0, buf = 0, e = 0;
     uint32_t tph = 0;
     uint16_t* const o16 = reinterpret_cast<uint16_t*>(out);
     for (int u = cluster; u < total; u += nclusters) {
-      const Unit t = decode_unit(s, E, wt, u);
+      const Unit t = decode_unit(s, wt, u, e);
+      e = t.e;
       // the four warps leave together: a named barrier's wait has no limit
-      if (!named_bar_all(1 + half, 128, mbar_wait_warp_cluster(&s.tfull[ab], tph, kWhereEpilogue)))
+      if (!named_bar_all(1 + half, 128, mbar_wait_warp(&s.tfull[ab], tph, kWhereEpilogue)))
         break;
       tc_fence_after();
       const int col0 = SWIGLU ? t.w0 * kRowsA + rank * 64 : t.w0 * kUnitN + rank * kRowsA;
