@@ -820,7 +820,7 @@ int fp8moe_combine_tokens(const void* rows, int64_t M, int64_t H, int32_t type,
   rc = device_init(&sms);
   if (rc) return rc;
   cudaError_t e = fp8moe_launch_combine(rows, T, topk, nvec, type == FP8MOE_TYPE_F32, slot_row, M,
-                                        weights, out, sms, stream);
+                                        weights, out, stream);
   return e == cudaSuccess ? FP8MOE_OK : cuda_fail(e);
 }
 

@@ -104,7 +104,7 @@ cudaError_t fp8moe_launch_dispatch(const void* x, int64_t T, int topk, int nvec,
                                    cudaStream_t s);
 cudaError_t fp8moe_launch_combine(const void* rows, int64_t T, int topk, int nvec, int f32,
                                   const int32_t* slot_row, int64_t M, const float* weights,
-                                  void* out, int num_sms, cudaStream_t s);
+                                  void* out, cudaStream_t s);
 cudaError_t fp8moe_launch_combine_bwd(const void* dout, const void* rows, int64_t T, int topk,
                                       int nvec, int f32, const int32_t* slot_row, int64_t M,
                                       const float* weights, void* drows, float* dweights,

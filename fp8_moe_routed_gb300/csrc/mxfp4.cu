@@ -30,10 +30,10 @@ __device__ __forceinline__ uint32_t max_bits(const uint4& v) {
 }
 
 __device__ __forceinline__ uint32_t quantize8(const uint4& v, float inv) {
-  float f[8];
+  float2 f[4];
   Vec<__nv_bfloat16>::unpack(v, f);
 #pragma unroll
-  for (int i = 0; i < 8; ++i) f[i] = inv == 0.0f ? 0.0f : f[i] * inv;
+  for (int i = 0; i < 4; ++i) f[i] = inv == 0.0f ? both(0.0f) : mul2(f[i], both(inv));
   return f32x8_to_e2m1x8(f);
 }
 
@@ -120,11 +120,13 @@ mx_quantize_weights_kernel(const uint32_t* __restrict__ w, int K, int N, int k_t
     uint32_t q[4];
 #pragma unroll
     for (int g = 0; g < 4; ++g) {
-      float f[8];
+      float2 f[4];
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const float x = c ? bf16hi_to_f32(v[8 * g + i]) : bf16lo_to_f32(v[8 * g + i]);
-        f[i] = inv == 0.0f ? 0.0f : x * inv;
+      for (int i = 0; i < 4; ++i) {
+        const uint32_t a = v[8 * g + 2 * i], b = v[8 * g + 2 * i + 1];
+        const float2 x = c ? make_float2(bf16hi_to_f32(a), bf16hi_to_f32(b))
+                           : make_float2(bf16lo_to_f32(a), bf16lo_to_f32(b));
+        f[i] = inv == 0.0f ? both(0.0f) : mul2(x, both(inv));
       }
       q[g] = f32x8_to_e2m1x8(f);
     }
@@ -186,11 +188,12 @@ mx_dequantize_kernel(const uint32_t* __restrict__ codes, const uint8_t* __restri
       const float s = mx_scale(b[i]);
       uint32_t h[4];
       e2m1x8_to_f16x2x4(c[i], h);
-      float f[8];
+      float2 f[4];
 #pragma unroll
-      for (int k = 0; k < 4; ++k) half2_to_f32(h[k], f[2 * k], f[2 * k + 1]);
-#pragma unroll
-      for (int k = 0; k < 8; ++k) f[k] *= s;
+      for (int k = 0; k < 4; ++k) {
+        half2_to_f32(h[k], f[k].x, f[k].y);
+        f[k] = mul2(f[k], both(s));
+      }
       out[row * nvec + vi] = Vec<__nv_bfloat16>::pack(f);
     }
   }

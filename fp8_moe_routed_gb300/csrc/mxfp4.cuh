@@ -37,7 +37,7 @@ __device__ __forceinline__ float mx_scale(uint32_t byte) {
 }
 
 // Eight f32 -> eight e2m1 codes, the first in the lowest four bits.
-__device__ __forceinline__ uint32_t f32x8_to_e2m1x8(const float (&f)[8]) {
+__device__ __forceinline__ uint32_t f32x8_to_e2m1x8(const float2 (&f)[4]) {
   uint32_t r;
   asm("{\n\t.reg .b8 a, b, c, d;\n\t"
       "cvt.rn.satfinite.e2m1x2.f32 a, %2, %1;\n\t"
@@ -45,8 +45,8 @@ __device__ __forceinline__ uint32_t f32x8_to_e2m1x8(const float (&f)[8]) {
       "cvt.rn.satfinite.e2m1x2.f32 c, %6, %5;\n\t"
       "cvt.rn.satfinite.e2m1x2.f32 d, %8, %7;\n\t"
       "mov.b32 %0, {a, b, c, d};\n\t}"
-      : "=r"(r) : "f"(f[0]), "f"(f[1]), "f"(f[2]), "f"(f[3]), "f"(f[4]), "f"(f[5]), "f"(f[6]),
-        "f"(f[7]));
+      : "=r"(r) : "f"(f[0].x), "f"(f[0].y), "f"(f[1].x), "f"(f[1].y), "f"(f[2].x), "f"(f[2].y),
+        "f"(f[3].x), "f"(f[3].y));
   return r;
 }
 

@@ -50,63 +50,99 @@ struct Shape {
   uint32_t row_bytes;
 };
 
-// Which tensor of a stage a pointer is: the inputs that are there, in order.
+// The inputs of a stage that are there, in order.
 struct Loads {
   const uint8_t* p[kMaxTensors];
 };
 
-__device__ __forceinline__ float sigmoid(float z) { return 1.0f / (1.0f + expf(-z)); }
+// exp and reciprocal by the fast units: a relative error of a few 2^-23, that of one or
+// two of the f32 operations that follow.
+__device__ __forceinline__ float sigmoid(float z) {
+  return __fdividef(1.0f, 1.0f + __expf(-z));
+}
+__device__ __forceinline__ float2 sigmoid2(float2 z) { return make_float2(sigmoid(z.x), sigmoid(z.y)); }
 
-template <typename T>
+// A ring of stages in shared memory, a stage the rows of one item.
 struct Ring {
   uint8_t* base;
   uint64_t* full;
-  const Shape& sh;
-  __device__ __forceinline__ uint8_t* at(int stage, int tensor) const {
-    return base + ((size_t)stage * sh.tensors + tensor) * ((size_t)sh.teams * sh.row_bytes);
+  __device__ __forceinline__ const uint4* row(const Shape& sh, int stage, int tensor, int team) const {
+    return reinterpret_cast<const uint4*>(
+        base + ((size_t)(stage * sh.tensors + tensor) * sh.teams + team) * sh.row_bytes);
   }
   // one thread: the rows of item `it` into `stage`
-  __device__ __forceinline__ void fill(const Loads& in, int64_t it, int stage) const {
+  __device__ __forceinline__ void fill(const Shape& sh, const Loads& in, int64_t it, int stage) const {
     const int64_t r0 = it * sh.teams;
     const int64_t left = sh.T - r0;
     const uint32_t bytes = (uint32_t)(left < sh.teams ? left : sh.teams) * sh.row_bytes;
     mbar_arrive_expect_tx(&full[stage], bytes * sh.tensors);
-    for (int i = 0; i < sh.tensors; ++i)
-      bulk_load(at(stage, i), in.p[i] + r0 * sh.row_bytes, bytes, &full[stage]);
+#pragma unroll
+    for (int i = 0; i < kMaxTensors; ++i)
+      if (i < sh.tensors)
+        bulk_load(const_cast<uint4*>(row(sh, stage, i, 0)), in.p[i] + r0 * sh.row_bytes, bytes,
+                  &full[stage]);
   }
 };
 
-// Sums of NV values over a team's warps, for every thread of the team. `buf`
+// Sums of NS values over a team's warps, for every thread of the team. `buf`
 // alternates between two areas: a slow reader of one call's sums is past them
 // before the call after the next writes there again.
-template <int NV>
-__device__ __forceinline__ void team_sum(float (&v)[NV], float* s_red, int buf, int warp,
+template <int NS>
+__device__ __forceinline__ void team_sum(float (&v)[NS], float* s_red, int buf, int warp,
                                          int team_warp0, int team_warps) {
 #pragma unroll
-  for (int i = 0; i < NV; ++i)
+  for (int d = 16; d > 0; d >>= 1)
 #pragma unroll
-    for (int d = 16; d > 0; d >>= 1) v[i] += __shfl_xor_sync(0xffffffffu, v[i], d);
-  float* const area = s_red + buf * (32 * 3);
-  if ((threadIdx.x & 31) == 0) {
-#pragma unroll
-    for (int i = 0; i < NV; ++i) area[warp * 3 + i] = v[i];
-  }
+    for (int i = 0; i < NS; ++i) v[i] += __shfl_xor_sync(0xffffffffu, v[i], d);
+  float4* const area = reinterpret_cast<float4*>(s_red) + buf * 32;
+  if ((threadIdx.x & 31) == 0)
+    area[warp] = make_float4(v[0], NS > 1 ? v[NS > 1 ? 1 : 0] : 0.0f, NS > 2 ? v[NS - 1] : 0.0f, 0.0f);
   __syncthreads();
 #pragma unroll
-  for (int i = 0; i < NV; ++i) v[i] = 0.0f;
-  for (int w = 0; w < team_warps; ++w)
-#pragma unroll
-    for (int i = 0; i < NV; ++i) v[i] += area[(team_warp0 + w) * 3 + i];
-}
-
-template <int N>
-__device__ __forceinline__ void load_f32(const float* __restrict__ p, float (&f)[N]) {
-#pragma unroll
-  for (int i = 0; i < N / 4; ++i) {
-    const float4 v = __ldg(reinterpret_cast<const float4*>(p) + i);
-    f[4 * i] = v.x; f[4 * i + 1] = v.y; f[4 * i + 2] = v.z; f[4 * i + 3] = v.w;
+  for (int i = 0; i < NS; ++i) v[i] = 0.0f;
+#pragma unroll 4
+  for (int w = 0; w < team_warps; ++w) {
+    const float4 p = area[team_warp0 + w];
+    v[0] += p.x;
+    if (NS > 1) v[NS > 1 ? 1 : 0] += p.y;
+    if (NS > 2) v[NS - 1] += p.z;
   }
 }
+
+template <int P>
+__device__ __forceinline__ void load_f32(const float* __restrict__ p, float2 (&f)[P]) {
+#pragma unroll
+  for (int i = 0; i < P / 2; ++i) {
+    const float4 v = __ldg(reinterpret_cast<const float4*>(p) + i);
+    f[2 * i] = make_float2(v.x, v.y);
+    f[2 * i + 1] = make_float2(v.z, v.w);
+  }
+}
+
+// A per-column parameter: in registers for all rows of a thread (HOIST), or, when rows
+// are so long that a CTA needs more than 512 threads, loaded for every row.
+template <typename T, bool HOIST>
+struct Param {
+  static constexpr int P = Vec<T>::kP, NV = kCols / Vec<T>::kN;
+  float2 v[HOIST ? NV : 1][P];
+  const float* p;
+  __device__ __forceinline__ void init(const float* src, int tt, int stride, int nvec) {
+    p = src;
+    if (HOIST && src) {
+#pragma unroll
+      for (int i = 0; i < NV; ++i)
+        if (tt + i * stride < nvec) load_f32<P>(src + (size_t)(tt + i * stride) * Vec<T>::kN, v[i]);
+    }
+  }
+  __device__ __forceinline__ void get(int i, int vec, float2 (&o)[P]) const {
+    if (HOIST) {
+#pragma unroll
+      for (int k = 0; k < P; ++k) o[k] = v[HOIST ? i : 0][k];
+    } else {
+      load_f32<P>(p + (size_t)vec * Vec<T>::kN, o);
+    }
+  }
+};
 
 struct FwdArgs {
   Loads in;                    // x, y, gate (each only if it is there)
@@ -121,16 +157,19 @@ struct FwdArgs {
   float* rstd_pre;
 };
 
-template <typename T, int MAXT>
-__global__ void __launch_bounds__(MAXT, 1) norm_fwd_kernel(const FwdArgs a, const Shape sh) {
-  constexpr int N = Vec<T>::kN, NV = kCols / N;
+// COL: a gate per column (its registers are not spent otherwise).
+template <typename T, int MAXT, bool COL>
+__global__ void __launch_bounds__(MAXT, 1)
+norm_fwd_kernel(const __grid_constant__ FwdArgs a, const __grid_constant__ Shape sh) {
+  constexpr int P = Vec<T>::kP, NV = kCols / Vec<T>::kN;
+  constexpr bool HOIST = MAXT <= kTeamThreads;
   extern __shared__ __align__(128) uint8_t ring_mem[];
   __shared__ uint64_t s_full[kMaxStages];
-  __shared__ float s_red[2 * 32 * 3];
-  const Ring<T> ring{ring_mem, s_full, sh};
+  __shared__ __align__(16) float s_red[2 * 32 * 4];
+  const Ring ring{ring_mem, s_full};
   const int warp = threadIdx.x >> 5;
   const int team = warp / sh.warps, team_warp0 = team * sh.warps;
-  const int tt = threadIdx.x - team_warp0 * 32;
+  const int tt = threadIdx.x - team_warp0 * 32, stride = sh.warps * 32;
   const int64_t items = (sh.T + sh.teams - 1) / sh.teams;
   const bool post = a.w_post != nullptr, pre = a.w_pre != nullptr;
   if (threadIdx.x == 0) {
@@ -138,9 +177,13 @@ __global__ void __launch_bounds__(MAXT, 1) norm_fwd_kernel(const FwdArgs a, cons
     fence_mbar_init();
     for (int i = 0; i < sh.stages; ++i) {
       const int64_t it = blockIdx.x + (int64_t)i * gridDim.x;
-      if (it < items) ring.fill(a.in, it, i);
+      if (it < items) ring.fill(sh, a.in, it, i);
     }
   }
+  Param<T, HOIST> w_post, w_pre, gate;
+  w_post.init(a.w_post, tt, stride, sh.nvec);
+  w_pre.init(a.w_pre, tt, stride, sh.nvec);
+  if (COL) gate.init(a.gate, tt, stride, sh.nvec);
   __syncthreads();
   const float inv_h = 1.0f / (float)sh.H;
   int stage = 0, buf = 0;
@@ -149,80 +192,82 @@ __global__ void __launch_bounds__(MAXT, 1) norm_fwd_kernel(const FwdArgs a, cons
   for (int64_t it = blockIdx.x; it < items; it += gridDim.x) {
     const int64_t row = it * sh.teams + team;
     const bool live = row < sh.T;
-    ok = ok && mbar_wait(&s_full[stage], phase, kWhereEpilogue);
-    const uint4* xs = reinterpret_cast<const uint4*>(ring.at(stage, 0) + (size_t)team * sh.row_bytes);
-    const uint4* ys = reinterpret_cast<const uint4*>(ring.at(stage, 1) + (size_t)team * sh.row_bytes);
-    const uint4* gs = reinterpret_cast<const uint4*>(ring.at(stage, 2) + (size_t)team * sh.row_bytes);
-    float r[NV][N];
-    float rp = 0.0f;
-    if (post) {
-      float ss[1] = {0.0f};
-#pragma unroll
-      for (int i = 0; i < NV; ++i) {
-        const int v = tt + i * sh.warps * 32;
-        if (!live || v >= sh.nvec) continue;
-        float y[N];
-        Vec<T>::unpack(ys[v], y);
-#pragma unroll
-        for (int k = 0; k < N; ++k) ss[0] = fmaf(y[k], y[k], ss[0]);
-      }
-      team_sum<1>(ss, s_red, buf, warp, team_warp0, sh.warps);
-      buf ^= 1;
-      rp = 1.0f / sqrtf(ss[0] * inv_h + a.eps);
-    }
-    float ss[1] = {0.0f};
     float grow = 1.0f;
     if (post && a.gate_kind == kGateRow && live) {
       grow = __ldg(a.gate + row);
       if (a.sigmoid) grow = sigmoid(grow);
     }
+    ok = ok && mbar_wait(&s_full[stage], phase, kWhereEpilogue);
+    const uint4* const xs = ring.row(sh, stage, 0, team);
+    const uint4* const ys = ring.row(sh, stage, 1, team);
+    const uint4* const gs = ring.row(sh, stage, 2, team);
+    float rp = 0.0f;
+    if (post) {
+      float2 s2 = both(0.0f);
+#pragma unroll
+      for (int i = 0; i < NV; ++i) {
+        const int v = tt + i * stride;
+        if (!live || v >= sh.nvec) continue;
+        float2 y[P];
+        Vec<T>::unpack(ys[v], y);
+#pragma unroll
+        for (int k = 0; k < P; ++k) s2 = fma2(y[k], y[k], s2);
+      }
+      float ss[1] = {s2.x + s2.y};
+      team_sum<1>(ss, s_red, buf, warp, team_warp0, sh.warps);
+      buf ^= 1;
+      rp = 1.0f / sqrtf(ss[0] * inv_h + a.eps);
+    }
+    float2 r[NV][P];
+    float2 s2 = both(0.0f);
+    const float2 scale = both(a.branch_scale * grow), rs = both(a.residual_scale);
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-      const int v = tt + i * sh.warps * 32;
+      const int v = tt + i * stride;
 #pragma unroll
-      for (int k = 0; k < N; ++k) r[i][k] = 0.0f;
+      for (int k = 0; k < P; ++k) r[i][k] = both(0.0f);
       if (!live || v >= sh.nvec) continue;
-      float x[N];
+      float2 x[P];
       Vec<T>::unpack(xs[v], x);
       if (post) {
-        float y[N], w[N], g[N];
+        float2 y[P], w[P], g[P];
         Vec<T>::unpack(ys[v], y);
-        load_f32<N>(a.w_post + (size_t)v * N, w);
-        if (a.gate_kind == kGateCol) load_f32<N>(a.gate + (size_t)v * N, g);
+        w_post.get(i, v, w);
+        if (COL) gate.get(i, v, g);
         else if (a.gate_kind == kGateFull) Vec<T>::unpack(gs[v], g);
 #pragma unroll
-        for (int k = 0; k < N; ++k) {
-          float b = y[k] * rp * w[k];
-          if (a.gate_kind >= kGateCol) b *= a.sigmoid ? sigmoid(g[k]) : g[k];
-          else b *= grow;
-          r[i][k] = fmaf(a.residual_scale, x[k], a.branch_scale * b);
+        for (int k = 0; k < P; ++k) {
+          float2 b = mul2(mul2(y[k], both(rp)), w[k]);
+          if (COL || a.gate_kind == kGateFull) b = mul2(b, a.sigmoid ? sigmoid2(g[k]) : g[k]);
+          r[i][k] = fma2(b, scale, mul2(rs, x[k]));
         }
         reinterpret_cast<uint4*>(a.r)[row * sh.nvec + v] = Vec<T>::pack(r[i]);
       } else {
 #pragma unroll
-        for (int k = 0; k < N; ++k) r[i][k] = x[k];
+        for (int k = 0; k < P; ++k) r[i][k] = x[k];
       }
 #pragma unroll
-      for (int k = 0; k < N; ++k) ss[0] = fmaf(r[i][k], r[i][k], ss[0]);
+      for (int k = 0; k < P; ++k) s2 = fma2(r[i][k], r[i][k], s2);
     }
     if (post && tt == 0 && live) a.rstd_post[row] = rp;
     // the barrier of this sum also says that every thread has read the stage
+    float ss[1] = {s2.x + s2.y};
     team_sum<1>(ss, s_red, buf, warp, team_warp0, sh.warps);
     buf ^= 1;
     if (threadIdx.x == 0) {
       const int64_t next = it + (int64_t)sh.stages * gridDim.x;
-      if (next < items) ring.fill(a.in, next, stage);
+      if (next < items) ring.fill(sh, a.in, next, stage);
     }
     if (pre) {
       const float rq = 1.0f / sqrtf(ss[0] * inv_h + a.eps);
 #pragma unroll
       for (int i = 0; i < NV; ++i) {
-        const int v = tt + i * sh.warps * 32;
+        const int v = tt + i * stride;
         if (!live || v >= sh.nvec) continue;
-        float w[N], h[N];
-        load_f32<N>(a.w_pre + (size_t)v * N, w);
+        float2 w[P], h[P];
+        w_pre.get(i, v, w);
 #pragma unroll
-        for (int k = 0; k < N; ++k) h[k] = r[i][k] * rq * w[k];
+        for (int k = 0; k < P; ++k) h[k] = mul2(mul2(r[i][k], both(rq)), w[k]);
         reinterpret_cast<uint4*>(a.h)[row * sh.nvec + v] = Vec<T>::pack(h);
       }
       if (tt == 0 && live) a.rstd_pre[row] = rq;
@@ -251,34 +296,41 @@ struct BwdArgs {
   float* part;                 // [3][gridDim.x][H]: dw_pre, dw_post, dgate per column
 };
 
-template <typename T, int MAXT>
-__global__ void __launch_bounds__(MAXT, 1) norm_bwd_kernel(const BwdArgs a, const Shape sh) {
-  constexpr int N = Vec<T>::kN, NV = kCols / N;
+template <typename T, int MAXT, bool COL>
+__global__ void __launch_bounds__(MAXT, 1)
+norm_bwd_kernel(const __grid_constant__ BwdArgs a, const __grid_constant__ Shape sh) {
+  constexpr int N = Vec<T>::kN, P = Vec<T>::kP, NV = kCols / N;
+  constexpr bool HOIST = MAXT <= kTeamThreads && !COL;   // else too many registers
   extern __shared__ __align__(128) uint8_t ring_mem[];
   __shared__ uint64_t s_full[kMaxStages];
-  __shared__ float s_red[2 * 32 * 3];
-  const Ring<T> ring{ring_mem, s_full, sh};
+  __shared__ __align__(16) float s_red[2 * 32 * 4];
+  const Ring ring{ring_mem, s_full};
   const int warp = threadIdx.x >> 5;
   const int team = warp / sh.warps, team_warp0 = team * sh.warps;
-  const int tt = threadIdx.x - team_warp0 * 32;
+  const int tt = threadIdx.x - team_warp0 * 32, stride = sh.warps * 32;
   const int64_t items = (sh.T + sh.teams - 1) / sh.teams;
   const bool post = a.w_post != nullptr, pre = a.w_pre != nullptr;
-  const bool col = a.gate_kind == kGateCol;
+  const bool full = !COL && a.gate_kind == kGateFull;
   if (threadIdx.x == 0) {
     for (int i = 0; i < sh.stages; ++i) mbar_init(&s_full[i], 1);
     fence_mbar_init();
     for (int i = 0; i < sh.stages; ++i) {
       const int64_t it = blockIdx.x + (int64_t)i * gridDim.x;
-      if (it < items) ring.fill(a.in, it, i);
+      if (it < items) ring.fill(sh, a.in, it, i);
     }
   }
+  Param<T, HOIST> w_post, w_pre;
+  Param<T, false> gate;
+  w_post.init(a.w_post, tt, stride, sh.nvec);
+  w_pre.init(a.w_pre, tt, stride, sh.nvec);
+  gate.init(a.gate, tt, stride, sh.nvec);
   __syncthreads();
   const float inv_h = 1.0f / (float)sh.H;
-  float acc_pre[NV][N], acc_post[NV][N], acc_gate[NV][N];
+  float2 acc_pre[NV][P], acc_post[NV][P], acc_gate[COL ? NV : 1][P];
 #pragma unroll
   for (int i = 0; i < NV; ++i)
 #pragma unroll
-    for (int k = 0; k < N; ++k) acc_pre[i][k] = acc_post[i][k] = acc_gate[i][k] = 0.0f;
+    for (int k = 0; k < P; ++k) acc_pre[i][k] = acc_post[i][k] = acc_gate[COL ? i : 0][k] = both(0.0f);
   int stage = 0, buf = 0;
   uint32_t phase = 0;
   bool ok = true;
@@ -298,113 +350,128 @@ __global__ void __launch_bounds__(MAXT, 1) norm_bwd_kernel(const BwdArgs a, cons
       }
     }
     ok = ok && mbar_wait(&s_full[stage], phase, kWhereEpilogue);
-    auto tensor = [&](int i) {
-      return reinterpret_cast<const uint4*>(ring.at(stage, i < 0 ? 0 : i) +
-                                            (size_t)team * sh.row_bytes);
-    };
+    auto tensor = [&](int i) { return ring.row(sh, stage, i < 0 ? 0 : i, team); };
     const uint4* const drs = tensor(a.i_dr);
     const uint4* const dhs = tensor(a.i_dh);
     const uint4* const rs = tensor(a.i_r);
     const uint4* const ys = tensor(a.i_y);
     const uint4* const gs = tensor(a.i_gate);
+    // the branch factor q = b g w_post yh of a vector, with g as far as it is per element
+    auto gate_of = [&](int i, int v, float2 (&g)[P]) {
+      if (COL) gate.get(i, v, g);
+      else Vec<T>::unpack(gs[v], g);
+      if (a.sigmoid) {
+#pragma unroll
+        for (int k = 0; k < P; ++k) g[k] = sigmoid2(g[k]);
+      }
+    };
     // first pass: sum u rh, sum q (dr + rq u), sum q rh
-    float s3[3] = {0.0f, 0.0f, 0.0f};
+    float2 s0 = both(0.0f), s1 = both(0.0f), s2 = both(0.0f);
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-      const int v = tt + i * sh.warps * 32;
+      const int v = tt + i * stride;
       if (!live || v >= sh.nvec) continue;
-      float d[N], u[N], rh[N];
+      float2 d[P], rh[P];
 #pragma unroll
-      for (int k = 0; k < N; ++k) d[k] = u[k] = rh[k] = 0.0f;
+      for (int k = 0; k < P; ++k) d[k] = rh[k] = both(0.0f);
       if (a.i_dr >= 0) Vec<T>::unpack(drs[v], d);
       if (pre) {
-        float w[N];
+        float2 u[P], w[P];
         Vec<T>::unpack(dhs[v], u);
         Vec<T>::unpack(rs[v], rh);
-        load_f32<N>(a.w_pre + (size_t)v * N, w);
+        w_pre.get(i, v, w);
 #pragma unroll
-        for (int k = 0; k < N; ++k) {
-          u[k] *= w[k];
-          rh[k] *= rq;
-          s3[0] = fmaf(u[k], rh[k], s3[0]);
+        for (int k = 0; k < P; ++k) {
+          u[k] = mul2(u[k], w[k]);
+          rh[k] = mul2(rh[k], both(rq));
+          s0 = fma2(u[k], rh[k], s0);
+          d[k] = fma2(both(rq), u[k], d[k]);
         }
       }
       if (post) {
-        float y[N], w[N], g[N];
+        float2 y[P], w[P];
         Vec<T>::unpack(ys[v], y);
-        load_f32<N>(a.w_post + (size_t)v * N, w);
-        if (col) load_f32<N>(a.gate + (size_t)v * N, g);
-        else if (a.gate_kind == kGateFull) Vec<T>::unpack(gs[v], g);
+        w_post.get(i, v, w);
 #pragma unroll
-        for (int k = 0; k < N; ++k) {
-          float q = a.branch_scale * w[k] * (y[k] * rp);
-          if (a.gate_kind >= kGateCol) q *= a.sigmoid ? sigmoid(g[k]) : g[k];
-          s3[1] = fmaf(q, fmaf(rq, u[k], d[k]), s3[1]);
-          s3[2] = fmaf(q, rh[k], s3[2]);
+        for (int k = 0; k < P; ++k) y[k] = mul2(mul2(y[k], both(rp)), w[k]);
+        if (COL || full) {
+          float2 g[P];
+          gate_of(i, v, g);
+#pragma unroll
+          for (int k = 0; k < P; ++k) y[k] = mul2(y[k], g[k]);
+        }
+#pragma unroll
+        for (int k = 0; k < P; ++k) {
+          s1 = fma2(y[k], d[k], s1);
+          s2 = fma2(y[k], rh[k], s2);
         }
       }
     }
+    float s3[3] = {s0.x + s0.y, s1.x + s1.y, s2.x + s2.y};
     team_sum<3>(s3, s_red, buf, warp, team_warp0, sh.warps);
     buf ^= 1;
+    // Past this barrier every thread has finished with the stage of the item before.
+    if (threadIdx.x == 0 && it >= gridDim.x && sh.stages > 1) {
+      const int64_t next = it + (int64_t)(sh.stages - 1) * gridDim.x;
+      if (next < items) ring.fill(sh, a.in, next, stage == 0 ? sh.stages - 1 : stage - 1);
+    }
     const float c1 = s3[0] * inv_h;
-    const float qd = s3[1] - c1 * rq * s3[2];
+    const float qd = a.branch_scale * (s3[1] - c1 * rq * s3[2]);
     const float c2 = qd * grow * inv_h;
     if (a.gate_kind == kGateRow && tt == 0 && live) a.dgate_row[row] = qd * slope_row;
     // second pass: the outputs and the column sums
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-      const int v = tt + i * sh.warps * 32;
+      const int v = tt + i * stride;
       if (!live || v >= sh.nvec) continue;
-      float d[N];
+      float2 d[P], o[P];
 #pragma unroll
-      for (int k = 0; k < N; ++k) d[k] = 0.0f;
+      for (int k = 0; k < P; ++k) d[k] = both(0.0f);
       if (a.i_dr >= 0) Vec<T>::unpack(drs[v], d);
       if (pre) {
-        float dh[N], rh[N], w[N];
+        float2 dh[P], rh[P], w[P];
         Vec<T>::unpack(dhs[v], dh);
         Vec<T>::unpack(rs[v], rh);
-        load_f32<N>(a.w_pre + (size_t)v * N, w);
+        w_pre.get(i, v, w);
 #pragma unroll
-        for (int k = 0; k < N; ++k) {
-          rh[k] *= rq;
-          acc_pre[i][k] = fmaf(dh[k], rh[k], acc_pre[i][k]);
-          d[k] = fmaf(rq, fmaf(-rh[k], c1, dh[k] * w[k]), d[k]);
+        for (int k = 0; k < P; ++k) {
+          rh[k] = mul2(rh[k], both(rq));
+          acc_pre[i][k] = fma2(dh[k], rh[k], acc_pre[i][k]);
+          d[k] = fma2(both(rq), fma2(rh[k], both(-c1), mul2(dh[k], w[k])), d[k]);
         }
       }
-      float o[N];
 #pragma unroll
-      for (int k = 0; k < N; ++k) o[k] = a.residual_scale * d[k];
+      for (int k = 0; k < P; ++k) o[k] = mul2(both(a.residual_scale), d[k]);
       reinterpret_cast<uint4*>(a.dx)[row * sh.nvec + v] = Vec<T>::pack(o);
       if (post) {
-        float y[N], w[N], g[N];
+        float2 y[P], w[P], g[P];
         Vec<T>::unpack(ys[v], y);
-        load_f32<N>(a.w_post + (size_t)v * N, w);
-        if (col) load_f32<N>(a.gate + (size_t)v * N, g);
-        else if (a.gate_kind == kGateFull) Vec<T>::unpack(gs[v], g);
+        w_post.get(i, v, w);
+        if (COL || full) gate_of(i, v, g);
 #pragma unroll
-        for (int k = 0; k < N; ++k) {
-          const float yh = y[k] * rp;
-          const float db = a.branch_scale * d[k];
-          float gk = grow;
-          if (a.gate_kind >= kGateCol) {
-            gk = a.sigmoid ? sigmoid(g[k]) : g[k];
-            const float dg = db * w[k] * yh;
-            if (col) acc_gate[i][k] += dg;
-            else g[k] = a.sigmoid ? dg * (gk * (1.0f - gk)) : dg;
+        for (int k = 0; k < P; ++k) {
+          const float2 yh = mul2(y[k], both(rp));
+          float2 dn = mul2(both(a.branch_scale), d[k]);
+          if (COL || full) {
+            const float2 dg = mul2(mul2(dn, w[k]), yh);
+            dn = mul2(dn, g[k]);
+            if (COL) acc_gate[COL ? i : 0][k] = add2(acc_gate[COL ? i : 0][k], dg);
+            else if (a.sigmoid) g[k] = mul2(dg, fma2(mul2(g[k], both(-1.0f)), g[k], g[k]));
+            else g[k] = dg;
+          } else {
+            dn = mul2(dn, both(grow));
           }
-          const float dn = db * gk;
-          acc_post[i][k] = fmaf(dn, yh, acc_post[i][k]);
-          o[k] = rp * fmaf(-yh, c2, w[k] * dn);
+          acc_post[i][k] = fma2(dn, yh, acc_post[i][k]);
+          o[k] = mul2(both(rp), fma2(yh, both(-c2), mul2(w[k], dn)));
         }
         reinterpret_cast<uint4*>(a.dy)[row * sh.nvec + v] = Vec<T>::pack(o);
-        if (a.gate_kind == kGateFull)
-          reinterpret_cast<uint4*>(a.dgate_full)[row * sh.nvec + v] = Vec<T>::pack(g);
+        if (full) reinterpret_cast<uint4*>(a.dgate_full)[row * sh.nvec + v] = Vec<T>::pack(g);
       }
     }
-    __syncthreads();   // every thread has read the stage
-    if (threadIdx.x == 0) {
-      const int64_t next = it + (int64_t)sh.stages * gridDim.x;
-      if (next < items) ring.fill(a.in, next, stage);
+    if (sh.stages == 1) {      // the longest rows: this item's stage is also the next one's
+      __syncthreads();
+      const int64_t next = it + gridDim.x;
+      if (threadIdx.x == 0 && next < items) ring.fill(sh, a.in, next, 0);
     }
     if (++stage == sh.stages) {
       stage = 0;
@@ -413,16 +480,17 @@ __global__ void __launch_bounds__(MAXT, 1) norm_bwd_kernel(const BwdArgs a, cons
   }
   // the column sums of this CTA: its teams' are joined in shared memory (the ring
   // is idle: every stage that was filled has been read)
-  auto join = [&](float (&acc)[NV][N], int which) {
+  auto join = [&](float2 (&acc)[NV][P], int which) {
     float* const out = a.part + ((size_t)which * gridDim.x + blockIdx.x) * sh.H;
     float* const s = reinterpret_cast<float*>(ring_mem);
     __syncthreads();
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-      const int v = tt + i * sh.warps * 32;
+      const int v = tt + i * stride;
       if (v >= sh.nvec) continue;
 #pragma unroll
-      for (int k = 0; k < N; ++k) s[(size_t)team * sh.H + v * N + k] = acc[i][k];
+      for (int k = 0; k < P; ++k)
+        *reinterpret_cast<float2*>(s + (size_t)team * sh.H + v * N + 2 * k) = acc[i][k];
     }
     __syncthreads();
     for (int c = threadIdx.x; c < sh.H; c += blockDim.x) {
@@ -433,7 +501,7 @@ __global__ void __launch_bounds__(MAXT, 1) norm_bwd_kernel(const BwdArgs a, cons
   };
   if (pre) join(acc_pre, 0);
   if (post) join(acc_post, 1);
-  if (col) join(acc_gate, 2);
+  if constexpr (COL) join(acc_gate, 2);
 }
 
 // Joins the CTAs' column sums: 16 threads per column take every 16th CTA.
@@ -526,10 +594,18 @@ cudaError_t fp8moe_launch_norm_fwd(const NormFwdArgs& p, int num_sms, cudaStream
     return cudaGetLastError();
   };
   // rows past 8192 columns need more than 512 threads, which halves the registers
-  if (sh.teams * sh.warps * 32 <= kTeamThreads)
-    return p.f32 ? run(norm_fwd_kernel<float, kTeamThreads>)
-                 : run(norm_fwd_kernel<__nv_bfloat16, kTeamThreads>);
-  return p.f32 ? run(norm_fwd_kernel<float, 1024>) : run(norm_fwd_kernel<__nv_bfloat16, 1024>);
+  const bool small = sh.teams * sh.warps * 32 <= kTeamThreads;
+  const bool col = p.gate_kind == kGateCol;
+  using bf16 = __nv_bfloat16;
+  if (p.f32)
+    return small ? (col ? run(norm_fwd_kernel<float, kTeamThreads, true>)
+                        : run(norm_fwd_kernel<float, kTeamThreads, false>))
+                 : (col ? run(norm_fwd_kernel<float, 1024, true>)
+                        : run(norm_fwd_kernel<float, 1024, false>));
+  return small ? (col ? run(norm_fwd_kernel<bf16, kTeamThreads, true>)
+                      : run(norm_fwd_kernel<bf16, kTeamThreads, false>))
+               : (col ? run(norm_fwd_kernel<bf16, 1024, true>)
+                      : run(norm_fwd_kernel<bf16, 1024, false>));
 }
 
 int fp8moe_norm_bwd_ctas(int64_t T) {
@@ -581,10 +657,19 @@ cudaError_t fp8moe_launch_norm_bwd(const NormBwdArgs& p, int num_sms, cudaStream
       return cudaGetLastError();
     };
     const bool small = sh.teams * sh.warps * 32 <= kTeamThreads;
-    const cudaError_t e =
-        p.f32 ? (small ? run(norm_bwd_kernel<float, kTeamThreads>) : run(norm_bwd_kernel<float, 1024>))
-              : (small ? run(norm_bwd_kernel<__nv_bfloat16, kTeamThreads>)
-                       : run(norm_bwd_kernel<__nv_bfloat16, 1024>));
+    const bool col = p.gate_kind == kGateCol;
+    using bf16 = __nv_bfloat16;
+    cudaError_t e;
+    if (p.f32)
+      e = small ? (col ? run(norm_bwd_kernel<float, kTeamThreads, true>)
+                       : run(norm_bwd_kernel<float, kTeamThreads, false>))
+                : (col ? run(norm_bwd_kernel<float, 1024, true>)
+                       : run(norm_bwd_kernel<float, 1024, false>));
+    else
+      e = small ? (col ? run(norm_bwd_kernel<bf16, kTeamThreads, true>)
+                       : run(norm_bwd_kernel<bf16, kTeamThreads, false>))
+                : (col ? run(norm_bwd_kernel<bf16, 1024, true>)
+                       : run(norm_bwd_kernel<bf16, 1024, false>));
     if (e != cudaSuccess) return e;
   }
   const dim3 jg((unsigned)((p.H + kJoinCols - 1) / kJoinCols), 3, 1);

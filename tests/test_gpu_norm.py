@@ -63,7 +63,8 @@ CASES = [  # T, H, type, parts, gate, sigmoid
     (321, 2056, F32, "both", None, False), (450, 1032, BF16, "pre", None, False),
     (33, 7168, F32, "pre", None, False), (450, 1032, BF16, "post", "token", False),
     (160, 776, F32, "post", "channel", True), (3, 4104, BF16, "post", None, False),
-    (600, 2048, F32, "both", "token", True),
+    (600, 2048, F32, "both", "token", True), (400, 16384, BF16, "both", "full", True),
+    (330, 8192, F32, "both", "full", False), (310, 16384, BF16, "both", "channel", False),
 ]
 
 
