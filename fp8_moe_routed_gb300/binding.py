@@ -586,7 +586,8 @@ def norm_fwd(x, y=None, w_post=None, w_pre=None, gate=None, gate_kind: Optional[
         r = residual_scale * x + branch_scale * g * (w_post * rmsnorm(y))
         h = w_pre * rmsnorm(r)
     Returns (r, h, rstd_post, rstd_pre); without y and w_post r is x and returned as
-    None, without w_pre h and rstd_pre are None. gate_kind: "token" (f32 [T]),
+    None (the scales belong to the sum and are not used), without w_pre h and rstd_pre
+    are None. gate_kind: "token" (f32 [T]),
     "channel" (f32 [H]) or "full" ([T, H] of x's type); sigmoid passes the gate
     through one (see fp8moe_norm_fwd)."""
     L = load()
@@ -596,8 +597,8 @@ def norm_fwd(x, y=None, w_post=None, w_pre=None, gate=None, gate_kind: Optional[
     post, pre = w_post is not None, w_pre is not None
     if (y is not None) != post:
         raise ValueError("y and w_post go together")
-    if not post and (gate is not None or residual_scale != 1.0 or branch_scale != 1.0):
-        raise ValueError("a gate or a scale needs y and w_post")
+    if not post and gate is not None:
+        raise ValueError("a gate needs y and w_post")
     if post:
         _req(y, x.dtype, "y", 2)
         if y.shape != x.shape:
@@ -637,8 +638,8 @@ def norm_bwd(dr, dh, r, y=None, w_post=None, w_pre=None, rstd_post=None, rstd_pr
         raise ValueError("y, w_post and rstd_post go together")
     if (dh is not None) != pre or (rstd_pre is not None) != pre or (pre and r is None):
         raise ValueError("dh, w_pre, rstd_pre and r go together")
-    if not post and (gate is not None or residual_scale != 1.0 or branch_scale != 1.0):
-        raise ValueError("a gate or a scale needs y and w_post")
+    if not post and gate is not None:
+        raise ValueError("a gate needs y and w_post")
     for t, name in ((dr, "dr"), (dh, "dh"), (r if pre else None, "r"), (y, "y")):
         if t is not None:
             _req(t, dt, name, 2)

@@ -311,7 +311,7 @@ int check_norm(int64_t T, int64_t H, int32_t type, int32_t gate_kind, int32_t si
 }
 
 size_t norm_bwd_ws_bytes(int64_t T, int64_t H) {
-  return (size_t)3 * (size_t)fp8moe_norm_bwd_ctas(T) * (size_t)H * sizeof(float);
+  return (size_t)2 * (size_t)fp8moe_norm_bwd_ctas(T) * (size_t)H * sizeof(float);
 }
 
 int64_t mxfp4_words(int64_t K) { return (K + 127) / 128; }

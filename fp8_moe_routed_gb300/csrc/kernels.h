@@ -147,7 +147,7 @@ struct NormBwdArgs {
   float* dw_post;
   float* dw_pre;
   void* dgate;
-  float* part;            // 3 * fp8moe_norm_bwd_ctas(T) * H
+  float* part;            // 2 * fp8moe_norm_bwd_ctas(T) * H
 };
 int fp8moe_norm_bwd_ctas(int64_t T);
 cudaError_t fp8moe_launch_norm_bwd(const NormBwdArgs& a, int num_sms, cudaStream_t s);

@@ -33,10 +33,16 @@
 namespace fp8moe {
 namespace norm {
 
-constexpr int kCols = 16;            // columns a thread holds: 2 vectors of bf16 or 4 of f32
-constexpr int kTeamThreads = 512;    // threads of a CTA when rows are short (several teams)
+// A thread holds 16 columns of a row, a row of up to 8192 columns takes at most 512
+// threads, whose 128 registers hold the weights and the column sums as well. Rows past
+// that take up to 1024 threads, whose 64 registers do not. (8 columns a thread and
+// twice the warps measured slower, 54 against 44 us forward and 110 against 96 us
+// backward for 4096 x 7168 bf16: the reductions' share grows with the warps.)
+constexpr int kCols = 16;
+constexpr int kShort = 512, kLong = 1024;
 constexpr int kRingBytes = 200 * 1024;
-constexpr int kMaxStages = 4;
+constexpr int kMaxStages = 4;       // of a team
+constexpr int kMaxTeams = 16;
 constexpr int kMaxTensors = 5;
 
 enum { kGateNone = 0, kGateRow = 1, kGateCol = 2, kGateFull = 3 };
@@ -45,12 +51,14 @@ struct Shape {
   int64_t T;
   int H, nvec;
   int warps;       // of a team: one row per team
-  int teams;       // rows of a stage
-  int stages, tensors;
+  int teams;       // of a CTA, each at its own pace
+  int stages;      // rows that a team has in shared memory, in use or on their way
+  int tensors;
   uint32_t row_bytes;
+  bool is_long;
 };
 
-// The inputs of a stage that are there, in order.
+// The inputs of a row that are there, in order.
 struct Loads {
   const uint8_t* p[kMaxTensors];
 };
@@ -62,51 +70,74 @@ __device__ __forceinline__ float sigmoid(float z) {
 }
 __device__ __forceinline__ float2 sigmoid2(float2 z) { return make_float2(sigmoid(z.x), sigmoid(z.y)); }
 
-// A ring of stages in shared memory, a stage the rows of one item.
+// A team's ring of rows in shared memory, by 32-bit shared addresses.
 struct Ring {
-  uint8_t* base;
+  uint32_t base, row_bytes;
   uint64_t* full;
-  __device__ __forceinline__ const uint4* row(const Shape& sh, int stage, int tensor, int team) const {
-    return reinterpret_cast<const uint4*>(
-        base + ((size_t)(stage * sh.tensors + tensor) * sh.teams + team) * sh.row_bytes);
+  int tensors;
+  __device__ __forceinline__ Ring(const Shape& sh, const uint8_t* mem, uint64_t* bars, int team)
+      : base(smem_u32(mem) + (uint32_t)(team * sh.stages * sh.tensors) * sh.row_bytes),
+        row_bytes(sh.row_bytes), full(bars + team * kMaxStages), tensors(sh.tensors) {}
+  __device__ __forceinline__ uint32_t at(int stage, int tensor) const {
+    return base + (uint32_t)(stage * tensors + tensor) * row_bytes;
   }
-  // one thread: the rows of item `it` into `stage`
-  __device__ __forceinline__ void fill(const Shape& sh, const Loads& in, int64_t it, int stage) const {
-    const int64_t r0 = it * sh.teams;
-    const int64_t left = sh.T - r0;
-    const uint32_t bytes = (uint32_t)(left < sh.teams ? left : sh.teams) * sh.row_bytes;
-    mbar_arrive_expect_tx(&full[stage], bytes * sh.tensors);
+  // one thread: row `row` into `stage`
+  __device__ __forceinline__ void fill(const Loads& in, uint32_t row, int stage) const {
+    mbar_arrive_expect_tx(&full[stage], row_bytes * tensors);
 #pragma unroll
     for (int i = 0; i < kMaxTensors; ++i)
-      if (i < sh.tensors)
-        bulk_load(const_cast<uint4*>(row(sh, stage, i, 0)), in.p[i] + r0 * sh.row_bytes, bytes,
-                  &full[stage]);
+      if (i < tensors)
+        asm volatile(
+            "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];"
+            ::"r"(at(stage, i)), "l"(in.p[i] + (size_t)row * row_bytes), "r"(row_bytes),
+              "r"(smem_u32(&full[stage])) : "memory");
   }
 };
 
-// Sums of NS values over a team's warps, for every thread of the team. `buf`
-// alternates between two areas: a slow reader of one call's sums is past them
-// before the call after the next writes there again.
+// Vector v of a row, zeros past its end.
+__device__ __forceinline__ uint4 row_vec(uint32_t row, int v, bool in) {
+  uint4 x = make_uint4(0, 0, 0, 0);
+  if (in)
+    asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(x.x), "=r"(x.y), "=r"(x.z), "=r"(x.w) : "r"(row + 16u * (uint32_t)v));
+  return x;
+}
+
+// Barrier of a team's warps.
+__device__ __forceinline__ void team_sync(int team, int warps) {
+  if (warps == 1) __syncwarp();
+  else named_bar_sync(1 + team, warps * 32);
+}
+
+// Sums of NS values over a team's warps, for every thread of the team. The warps' sums
+// lie in groups of four (zeros behind a team's last), `buf` alternates between two
+// areas: a slow reader of one call's sums is past them before the call after the next
+// writes there again.
+constexpr int kRedTeam = 64;         // most words of all teams: teams * (warps rounded up to 4)
+constexpr int kRedWords = 2 * 3 * kRedTeam;
+
 template <int NS>
-__device__ __forceinline__ void team_sum(float (&v)[NS], float* s_red, int buf, int warp,
-                                         int team_warp0, int team_warps) {
+__device__ __forceinline__ void team_sum(float (&v)[NS], float* s_red, int buf, int slot, int first,
+                                         int quads, int team, int warps) {
 #pragma unroll
   for (int d = 16; d > 0; d >>= 1)
 #pragma unroll
     for (int i = 0; i < NS; ++i) v[i] += __shfl_xor_sync(0xffffffffu, v[i], d);
-  float4* const area = reinterpret_cast<float4*>(s_red) + buf * 32;
-  if ((threadIdx.x & 31) == 0)
-    area[warp] = make_float4(v[0], NS > 1 ? v[NS > 1 ? 1 : 0] : 0.0f, NS > 2 ? v[NS - 1] : 0.0f, 0.0f);
-  __syncthreads();
+  float* const area = s_red + buf * (3 * kRedTeam);
+  if ((threadIdx.x & 31) == 0) {
+#pragma unroll
+    for (int i = 0; i < NS; ++i) area[i * kRedTeam + slot] = v[i];
+  }
+  team_sync(team, warps);
 #pragma unroll
   for (int i = 0; i < NS; ++i) v[i] = 0.0f;
 #pragma unroll 4
-  for (int w = 0; w < team_warps; ++w) {
-    const float4 p = area[team_warp0 + w];
-    v[0] += p.x;
-    if (NS > 1) v[NS > 1 ? 1 : 0] += p.y;
-    if (NS > 2) v[NS - 1] += p.z;
-  }
+  for (int q = 0; q < quads; ++q)
+#pragma unroll
+    for (int i = 0; i < NS; ++i) {
+      const float4 p = reinterpret_cast<const float4*>(area + i * kRedTeam + first)[q];
+      v[i] += (p.x + p.y) + (p.z + p.w);
+    }
 }
 
 template <int P>
@@ -119,19 +150,37 @@ __device__ __forceinline__ void load_f32(const float* __restrict__ p, float2 (&f
   }
 }
 
-// A per-column parameter: in registers for all rows of a thread (HOIST), or, when rows
-// are so long that a CTA needs more than 512 threads, loaded for every row.
+// A norm's weight, times the block's gate where that is one per column: in registers for
+// all rows of a thread (HOIST), or loaded for every row.
 template <typename T, bool HOIST>
 struct Param {
   static constexpr int P = Vec<T>::kP, NV = kCols / Vec<T>::kN;
   float2 v[HOIST ? NV : 1][P];
-  const float* p;
-  __device__ __forceinline__ void init(const float* src, int tt, int stride, int nvec) {
-    p = src;
-    if (HOIST && src) {
+  const float* w;
+  const float* g;      // null: no gate
+  int sig, nvec;
+  // zeros past the row
+  __device__ __forceinline__ void load(int vec, float2 (&o)[P]) const {
 #pragma unroll
-      for (int i = 0; i < NV; ++i)
-        if (tt + i * stride < nvec) load_f32<P>(src + (size_t)(tt + i * stride) * Vec<T>::kN, v[i]);
+    for (int k = 0; k < P; ++k) o[k] = both(0.0f);
+    if (vec >= nvec) return;
+    load_f32<P>(w + (size_t)vec * Vec<T>::kN, o);
+    if (g) {
+      float2 z[P];
+      load_f32<P>(g + (size_t)vec * Vec<T>::kN, z);
+#pragma unroll
+      for (int k = 0; k < P; ++k) o[k] = mul2(o[k], sig ? sigmoid2(z[k]) : z[k]);
+    }
+  }
+  __device__ __forceinline__ void init(const float* weight, const float* gate, int sigmoid, int tt,
+                                       int stride, int n) {
+    w = weight;
+    g = gate;
+    sig = sigmoid;
+    nvec = n;
+    if (HOIST) {
+#pragma unroll
+      for (int i = 0; i < NV; ++i) load(tt + i * stride, v[HOIST ? i : 0]);
     }
   }
   __device__ __forceinline__ void get(int i, int vec, float2 (&o)[P]) const {
@@ -139,7 +188,7 @@ struct Param {
 #pragma unroll
       for (int k = 0; k < P; ++k) o[k] = v[HOIST ? i : 0][k];
     } else {
-      load_f32<P>(p + (size_t)vec * Vec<T>::kN, o);
+      load(vec, o);
     }
   }
 };
@@ -157,120 +206,120 @@ struct FwdArgs {
   float* rstd_pre;
 };
 
-// COL: a gate per column (its registers are not spent otherwise).
-template <typename T, int MAXT, bool COL>
+// What a kernel variant does: the norm after the block, the one before it, a gate value
+// per element (the other gates are a factor of the row's or of the weight's).
+template <typename T, int MAXT, bool POST, bool PRE, bool FULL>
 __global__ void __launch_bounds__(MAXT, 1)
 norm_fwd_kernel(const __grid_constant__ FwdArgs a, const __grid_constant__ Shape sh) {
   constexpr int P = Vec<T>::kP, NV = kCols / Vec<T>::kN;
-  constexpr bool HOIST = MAXT <= kTeamThreads;
+  constexpr bool HOIST = MAXT == kShort;
   extern __shared__ __align__(128) uint8_t ring_mem[];
-  __shared__ uint64_t s_full[kMaxStages];
-  __shared__ __align__(16) float s_red[2 * 32 * 4];
-  const Ring ring{ring_mem, s_full};
+  __shared__ uint64_t s_full[kMaxTeams * kMaxStages];
+  __shared__ __align__(16) float s_red[kRedWords];
   const int warp = threadIdx.x >> 5;
-  const int team = warp / sh.warps, team_warp0 = team * sh.warps;
-  const int tt = threadIdx.x - team_warp0 * 32, stride = sh.warps * 32;
-  const int64_t items = (sh.T + sh.teams - 1) / sh.teams;
-  const bool post = a.w_post != nullptr, pre = a.w_pre != nullptr;
-  if (threadIdx.x == 0) {
-    for (int i = 0; i < sh.stages; ++i) mbar_init(&s_full[i], 1);
+  const int team = warp / sh.warps;
+  const Ring ring(sh, ring_mem, s_full, team);
+  const int tt = threadIdx.x - team * sh.warps * 32, stride = sh.warps * 32;
+  const int quads = (sh.warps + 3) / 4, first = team * quads * 4;
+  const int slot = first + warp - team * sh.warps;
+  // the team's first row, and on to its next (T < 2^31: the sums stay below 2^32)
+  const uint32_t row0 = blockIdx.x * sh.teams + team, step = gridDim.x * sh.teams;
+  const uint32_t rows = (uint32_t)sh.T;
+  if (tt == 0) {
+    for (int i = 0; i < sh.stages; ++i) mbar_init(&ring.full[i], 1);
     fence_mbar_init();
-    for (int i = 0; i < sh.stages; ++i) {
-      const int64_t it = blockIdx.x + (int64_t)i * gridDim.x;
-      if (it < items) ring.fill(sh, a.in, it, i);
-    }
+    for (int i = 0; i < sh.stages; ++i)
+      if (row0 + i * step < rows) ring.fill(a.in, row0 + i * step, i);
   }
-  Param<T, HOIST> w_post, w_pre, gate;
-  w_post.init(a.w_post, tt, stride, sh.nvec);
-  w_pre.init(a.w_pre, tt, stride, sh.nvec);
-  if (COL) gate.init(a.gate, tt, stride, sh.nvec);
+  for (int i = threadIdx.x; i < kRedWords; i += blockDim.x) s_red[i] = 0.0f;
+  Param<T, HOIST> w_post, w_pre;
+  if (POST)
+    w_post.init(a.w_post, a.gate_kind == kGateCol ? a.gate : nullptr, a.sigmoid, tt, stride, sh.nvec);
+  if (PRE) w_pre.init(a.w_pre, nullptr, 0, tt, stride, sh.nvec);
   __syncthreads();
   const float inv_h = 1.0f / (float)sh.H;
   int stage = 0, buf = 0;
   uint32_t phase = 0;
   bool ok = true;
-  for (int64_t it = blockIdx.x; it < items; it += gridDim.x) {
-    const int64_t row = it * sh.teams + team;
-    const bool live = row < sh.T;
-    float grow = 1.0f;
-    if (post && a.gate_kind == kGateRow && live) {
-      grow = __ldg(a.gate + row);
-      if (a.sigmoid) grow = sigmoid(grow);
-    }
-    ok = ok && mbar_wait(&s_full[stage], phase, kWhereEpilogue);
-    const uint4* const xs = ring.row(sh, stage, 0, team);
-    const uint4* const ys = ring.row(sh, stage, 1, team);
-    const uint4* const gs = ring.row(sh, stage, 2, team);
+  const bool row_gate = POST && a.gate_kind == kGateRow;
+  float next_g = 1.0f;                     // the next item's gate, fetched an item ahead
+  auto fetch = [&](uint32_t row) {
+    if (row_gate && row < rows) next_g = __ldg(a.gate + row);
+  };
+  fetch(row0);
+  for (uint32_t row = row0; row < rows; row += step) {
+    float grow = next_g;
+    fetch(row + step);
+    ok = ok && mbar_wait(&ring.full[stage], phase, kWhereEpilogue);
+    const uint32_t xs = ring.at(stage, 0);
+    const uint32_t ys = ring.at(stage, 1);
+    const uint32_t gs = ring.at(stage, 2);
+    float2 r[NV][P];
     float rp = 0.0f;
-    if (post) {
+    if (POST) {
       float2 s2 = both(0.0f);
 #pragma unroll
       for (int i = 0; i < NV; ++i) {
         const int v = tt + i * stride;
-        if (!live || v >= sh.nvec) continue;
-        float2 y[P];
-        Vec<T>::unpack(ys[v], y);
+        Vec<T>::unpack(row_vec(ys, v, v < sh.nvec), r[i]);
 #pragma unroll
-        for (int k = 0; k < P; ++k) s2 = fma2(y[k], y[k], s2);
+        for (int k = 0; k < P; ++k) s2 = fma2(r[i][k], r[i][k], s2);
       }
       float ss[1] = {s2.x + s2.y};
-      team_sum<1>(ss, s_red, buf, warp, team_warp0, sh.warps);
+      team_sum<1>(ss, s_red, buf, slot, first, quads, team, sh.warps);
       buf ^= 1;
-      rp = 1.0f / sqrtf(ss[0] * inv_h + a.eps);
+      rp = rsqrtf(fmaf(ss[0], inv_h, a.eps));
     }
-    float2 r[NV][P];
+    if (row_gate && a.sigmoid) grow = sigmoid(grow);
     float2 s2 = both(0.0f);
-    const float2 scale = both(a.branch_scale * grow), rs = both(a.residual_scale);
+    const float2 scale = both(a.branch_scale * grow * rp), rs = both(a.residual_scale);
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
       const int v = tt + i * stride;
-#pragma unroll
-      for (int k = 0; k < P; ++k) r[i][k] = both(0.0f);
-      if (!live || v >= sh.nvec) continue;
+      const bool in = v < sh.nvec;
       float2 x[P];
-      Vec<T>::unpack(xs[v], x);
-      if (post) {
-        float2 y[P], w[P], g[P];
-        Vec<T>::unpack(ys[v], y);
+      Vec<T>::unpack(row_vec(xs, v, in), x);
+      if (POST) {
+        float2 w[P], g[P];
         w_post.get(i, v, w);
-        if (COL) gate.get(i, v, g);
-        else if (a.gate_kind == kGateFull) Vec<T>::unpack(gs[v], g);
+        if (FULL) Vec<T>::unpack(row_vec(gs, v, in), g);
 #pragma unroll
         for (int k = 0; k < P; ++k) {
-          float2 b = mul2(mul2(y[k], both(rp)), w[k]);
-          if (COL || a.gate_kind == kGateFull) b = mul2(b, a.sigmoid ? sigmoid2(g[k]) : g[k]);
+          float2 b = mul2(r[i][k], w[k]);
+          if (FULL) b = mul2(b, a.sigmoid ? sigmoid2(g[k]) : g[k]);
           r[i][k] = fma2(b, scale, mul2(rs, x[k]));
         }
-        reinterpret_cast<uint4*>(a.r)[row * sh.nvec + v] = Vec<T>::pack(r[i]);
+        if (in) reinterpret_cast<uint4*>(a.r)[(size_t)row * sh.nvec + v] = Vec<T>::pack(r[i]);
       } else {
 #pragma unroll
         for (int k = 0; k < P; ++k) r[i][k] = x[k];
       }
+      // columns past the row are zeros, so they add nothing
 #pragma unroll
       for (int k = 0; k < P; ++k) s2 = fma2(r[i][k], r[i][k], s2);
     }
-    if (post && tt == 0 && live) a.rstd_post[row] = rp;
-    // the barrier of this sum also says that every thread has read the stage
+    if (POST && tt == 0) a.rstd_post[row] = rp;
     float ss[1] = {s2.x + s2.y};
-    team_sum<1>(ss, s_red, buf, warp, team_warp0, sh.warps);
-    buf ^= 1;
-    if (threadIdx.x == 0) {
-      const int64_t next = it + (int64_t)sh.stages * gridDim.x;
-      if (next < items) ring.fill(sh, a.in, next, stage);
+    if (PRE) {
+      team_sum<1>(ss, s_red, buf, slot, first, quads, team, sh.warps);
+      buf ^= 1;
+    } else {
+      team_sync(team, sh.warps);
     }
-    if (pre) {
-      const float rq = 1.0f / sqrtf(ss[0] * inv_h + a.eps);
+    // past that barrier every thread has read the stage
+    if (tt == 0 && row + sh.stages * step < rows) ring.fill(a.in, row + sh.stages * step, stage);
+    if (PRE) {
+      const float rq = rsqrtf(fmaf(ss[0], inv_h, a.eps));
 #pragma unroll
       for (int i = 0; i < NV; ++i) {
         const int v = tt + i * stride;
-        if (!live || v >= sh.nvec) continue;
         float2 w[P], h[P];
         w_pre.get(i, v, w);
 #pragma unroll
         for (int k = 0; k < P; ++k) h[k] = mul2(mul2(r[i][k], both(rq)), w[k]);
-        reinterpret_cast<uint4*>(a.h)[row * sh.nvec + v] = Vec<T>::pack(h);
+        if (v < sh.nvec) reinterpret_cast<uint4*>(a.h)[(size_t)row * sh.nvec + v] = Vec<T>::pack(h);
       }
-      if (tt == 0 && live) a.rstd_pre[row] = rq;
+      if (tt == 0) a.rstd_pre[row] = rq;
     }
     if (++stage == sh.stages) {
       stage = 0;
@@ -281,7 +330,7 @@ norm_fwd_kernel(const __grid_constant__ FwdArgs a, const __grid_constant__ Shape
 
 struct BwdArgs {
   Loads in;                    // dr, dh, r, y, gate (each only if it is there)
-  int i_dr, i_dh, i_r, i_y, i_gate;   // their places in a stage, -1 if absent
+  int i_dr, i_dh, i_y;         // places in a stage (-1: absent); r follows dh, the gate y
   const float* w_post;
   const float* w_pre;
   const float* rstd_post;
@@ -293,185 +342,169 @@ struct BwdArgs {
   void* dy;
   float* dgate_row;
   void* dgate_full;
-  float* part;                 // [3][gridDim.x][H]: dw_pre, dw_post, dgate per column
+  float* part;                 // [2][gridDim.x][H]: the sums of dh rh, and of b D g yh (g without a
+                               // gate per column)
 };
 
-template <typename T, int MAXT, bool COL>
+template <typename T, int MAXT, bool POST, bool PRE, bool FULL>
 __global__ void __launch_bounds__(MAXT, 1)
 norm_bwd_kernel(const __grid_constant__ BwdArgs a, const __grid_constant__ Shape sh) {
   constexpr int N = Vec<T>::kN, P = Vec<T>::kP, NV = kCols / N;
-  constexpr bool HOIST = MAXT <= kTeamThreads && !COL;   // else too many registers
+  constexpr bool HOIST = MAXT == kShort;
   extern __shared__ __align__(128) uint8_t ring_mem[];
-  __shared__ uint64_t s_full[kMaxStages];
-  __shared__ __align__(16) float s_red[2 * 32 * 4];
-  const Ring ring{ring_mem, s_full};
+  __shared__ uint64_t s_full[kMaxTeams * kMaxStages];
+  __shared__ __align__(16) float s_red[kRedWords];
   const int warp = threadIdx.x >> 5;
-  const int team = warp / sh.warps, team_warp0 = team * sh.warps;
-  const int tt = threadIdx.x - team_warp0 * 32, stride = sh.warps * 32;
-  const int64_t items = (sh.T + sh.teams - 1) / sh.teams;
-  const bool post = a.w_post != nullptr, pre = a.w_pre != nullptr;
-  const bool full = !COL && a.gate_kind == kGateFull;
-  if (threadIdx.x == 0) {
-    for (int i = 0; i < sh.stages; ++i) mbar_init(&s_full[i], 1);
+  const int team = warp / sh.warps;
+  const Ring ring(sh, ring_mem, s_full, team);
+  const int tt = threadIdx.x - team * sh.warps * 32, stride = sh.warps * 32;
+  const int quads = (sh.warps + 3) / 4, first = team * quads * 4;
+  const int slot = first + warp - team * sh.warps;
+  // the team's first row, and on to its next (T < 2^31: the sums stay below 2^32)
+  const uint32_t row0 = blockIdx.x * sh.teams + team, step = gridDim.x * sh.teams;
+  const uint32_t rows = (uint32_t)sh.T;
+  if (tt == 0) {
+    for (int i = 0; i < sh.stages; ++i) mbar_init(&ring.full[i], 1);
     fence_mbar_init();
-    for (int i = 0; i < sh.stages; ++i) {
-      const int64_t it = blockIdx.x + (int64_t)i * gridDim.x;
-      if (it < items) ring.fill(sh, a.in, it, i);
-    }
+    for (int i = 0; i < sh.stages; ++i)
+      if (row0 + i * step < rows) ring.fill(a.in, row0 + i * step, i);
   }
+  for (int i = threadIdx.x; i < kRedWords; i += blockDim.x) s_red[i] = 0.0f;
   Param<T, HOIST> w_post, w_pre;
-  Param<T, false> gate;
-  w_post.init(a.w_post, tt, stride, sh.nvec);
-  w_pre.init(a.w_pre, tt, stride, sh.nvec);
-  gate.init(a.gate, tt, stride, sh.nvec);
+  if (POST)
+    w_post.init(a.w_post, a.gate_kind == kGateCol ? a.gate : nullptr, a.sigmoid, tt, stride, sh.nvec);
+  if (PRE) w_pre.init(a.w_pre, nullptr, 0, tt, stride, sh.nvec);
   __syncthreads();
   const float inv_h = 1.0f / (float)sh.H;
-  float2 acc_pre[NV][P], acc_post[NV][P], acc_gate[COL ? NV : 1][P];
+  const bool row_gate = POST && a.gate_kind == kGateRow;
+  float2 acc_pre[PRE ? NV : 1][P], acc_post[POST ? NV : 1][P];
 #pragma unroll
   for (int i = 0; i < NV; ++i)
 #pragma unroll
-    for (int k = 0; k < P; ++k) acc_pre[i][k] = acc_post[i][k] = acc_gate[COL ? i : 0][k] = both(0.0f);
+    for (int k = 0; k < P; ++k) acc_pre[PRE ? i : 0][k] = acc_post[POST ? i : 0][k] = both(0.0f);
+  float next_p = 0.0f, next_q = 0.0f, next_g = 1.0f;   // the next item's, fetched an item ahead
+  auto fetch = [&](uint32_t row) {
+    if (row < rows) {
+      if (POST) next_p = __ldg(a.rstd_post + row);
+      if (PRE) next_q = __ldg(a.rstd_pre + row);
+      if (row_gate) next_g = __ldg(a.gate + row);
+    }
+  };
+  fetch(row0);
   int stage = 0, buf = 0;
   uint32_t phase = 0;
   bool ok = true;
-  for (int64_t it = blockIdx.x; it < items; it += gridDim.x) {
-    const int64_t row = it * sh.teams + team;
-    const bool live = row < sh.T;
-    float rp = 0.0f, rq = 0.0f, grow = 1.0f, slope_row = 1.0f;
-    if (live) {
-      if (post) rp = __ldg(a.rstd_post + row);
-      if (pre) rq = __ldg(a.rstd_pre + row);
-      if (a.gate_kind == kGateRow) {
-        grow = __ldg(a.gate + row);
-        if (a.sigmoid) {
-          grow = sigmoid(grow);
-          slope_row = grow * (1.0f - grow);
-        }
-      }
+  for (uint32_t row = row0; row < rows; row += step) {
+    const float rp = next_p, rq = next_q;
+    float grow = next_g, slope_row = 1.0f;
+    fetch(row + step);
+    ok = ok && mbar_wait(&ring.full[stage], phase, kWhereEpilogue);
+    const uint32_t drs = ring.at(stage, 0);
+    const uint32_t dhs = ring.at(stage, PRE ? a.i_dh : 0);
+    const uint32_t rs = ring.at(stage, PRE ? a.i_dh + 1 : 0);
+    const uint32_t ys = ring.at(stage, POST ? a.i_y : 0);
+    const uint32_t gs = ring.at(stage, FULL ? a.i_y + 1 : 0);
+    if (row_gate && a.sigmoid) {
+      grow = sigmoid(grow);
+      slope_row = grow * (1.0f - grow);
     }
-    ok = ok && mbar_wait(&s_full[stage], phase, kWhereEpilogue);
-    auto tensor = [&](int i) { return ring.row(sh, stage, i < 0 ? 0 : i, team); };
-    const uint4* const drs = tensor(a.i_dr);
-    const uint4* const dhs = tensor(a.i_dh);
-    const uint4* const rs = tensor(a.i_r);
-    const uint4* const ys = tensor(a.i_y);
-    const uint4* const gs = tensor(a.i_gate);
-    // the branch factor q = b g w_post yh of a vector, with g as far as it is per element
-    auto gate_of = [&](int i, int v, float2 (&g)[P]) {
-      if (COL) gate.get(i, v, g);
-      else Vec<T>::unpack(gs[v], g);
-      if (a.sigmoid) {
-#pragma unroll
-        for (int k = 0; k < P; ++k) g[k] = sigmoid2(g[k]);
-      }
-    };
-    // first pass: sum u rh, sum q (dr + rq u), sum q rh
+    // With u = w_pre dh and p = w_post y (times a gate per column or element):
+    // sum u r, sum p (dr + rq u), sum p r. The row's factors come in afterwards.
     float2 s0 = both(0.0f), s1 = both(0.0f), s2 = both(0.0f);
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
       const int v = tt + i * stride;
-      if (!live || v >= sh.nvec) continue;
-      float2 d[P], rh[P];
-#pragma unroll
-      for (int k = 0; k < P; ++k) d[k] = rh[k] = both(0.0f);
-      if (a.i_dr >= 0) Vec<T>::unpack(drs[v], d);
-      if (pre) {
-        float2 u[P], w[P];
-        Vec<T>::unpack(dhs[v], u);
-        Vec<T>::unpack(rs[v], rh);
+      const bool in = v < sh.nvec;
+      float2 d[P], r[P], w[P];
+      Vec<T>::unpack(row_vec(drs, v, in && a.i_dr >= 0), d);
+      if (PRE) {
+        float2 u[P];
+        Vec<T>::unpack(row_vec(dhs, v, in), u);
+        Vec<T>::unpack(row_vec(rs, v, in), r);
         w_pre.get(i, v, w);
 #pragma unroll
         for (int k = 0; k < P; ++k) {
           u[k] = mul2(u[k], w[k]);
-          rh[k] = mul2(rh[k], both(rq));
-          s0 = fma2(u[k], rh[k], s0);
+          s0 = fma2(u[k], r[k], s0);
           d[k] = fma2(both(rq), u[k], d[k]);
         }
       }
-      if (post) {
-        float2 y[P], w[P];
-        Vec<T>::unpack(ys[v], y);
+      if (POST) {
+        float2 y[P];
+        Vec<T>::unpack(row_vec(ys, v, in), y);
         w_post.get(i, v, w);
 #pragma unroll
-        for (int k = 0; k < P; ++k) y[k] = mul2(mul2(y[k], both(rp)), w[k]);
-        if (COL || full) {
+        for (int k = 0; k < P; ++k) y[k] = mul2(y[k], w[k]);
+        if (FULL) {
           float2 g[P];
-          gate_of(i, v, g);
+          Vec<T>::unpack(row_vec(gs, v, in), g);
 #pragma unroll
-          for (int k = 0; k < P; ++k) y[k] = mul2(y[k], g[k]);
+          for (int k = 0; k < P; ++k) y[k] = mul2(y[k], a.sigmoid ? sigmoid2(g[k]) : g[k]);
         }
 #pragma unroll
         for (int k = 0; k < P; ++k) {
           s1 = fma2(y[k], d[k], s1);
-          s2 = fma2(y[k], rh[k], s2);
+          if (PRE) s2 = fma2(y[k], r[k], s2);
         }
       }
     }
     float s3[3] = {s0.x + s0.y, s1.x + s1.y, s2.x + s2.y};
-    team_sum<3>(s3, s_red, buf, warp, team_warp0, sh.warps);
+    team_sum<3>(s3, s_red, buf, slot, first, quads, team, sh.warps);
     buf ^= 1;
-    // Past this barrier every thread has finished with the stage of the item before.
-    if (threadIdx.x == 0 && it >= gridDim.x && sh.stages > 1) {
-      const int64_t next = it + (int64_t)(sh.stages - 1) * gridDim.x;
-      if (next < items) ring.fill(sh, a.in, next, stage == 0 ? sh.stages - 1 : stage - 1);
-    }
-    const float c1 = s3[0] * inv_h;
-    const float qd = a.branch_scale * (s3[1] - c1 * rq * s3[2]);
-    const float c2 = qd * grow * inv_h;
-    if (a.gate_kind == kGateRow && tt == 0 && live) a.dgate_row[row] = qd * slope_row;
-    // second pass: the outputs and the column sums
+    // Past this barrier every thread has finished with the stage of the row before.
+    if (tt == 0 && sh.stages > 2 && row != row0 && row + (sh.stages - 1) * step < rows)
+      ring.fill(a.in, row + (sh.stages - 1) * step, stage == 0 ? sh.stages - 1 : stage - 1);
+    // D = dr + rq u - k1 r;  dy = k2 (w_post g D) - k3 y
+    const float k1 = rq * rq * rq * s3[0] * inv_h;
+    const float qd = a.branch_scale * rp * (s3[1] - k1 * s3[2]);     // sum q D without the row's gate
+    const float k2 = a.branch_scale * grow * rp;
+    const float k3 = rp * rp * grow * qd * inv_h;
+    if (row_gate && tt == 0) a.dgate_row[row] = qd * slope_row;
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
       const int v = tt + i * stride;
-      if (!live || v >= sh.nvec) continue;
-      float2 d[P], o[P];
-#pragma unroll
-      for (int k = 0; k < P; ++k) d[k] = both(0.0f);
-      if (a.i_dr >= 0) Vec<T>::unpack(drs[v], d);
-      if (pre) {
-        float2 dh[P], rh[P], w[P];
-        Vec<T>::unpack(dhs[v], dh);
-        Vec<T>::unpack(rs[v], rh);
+      const bool in = v < sh.nvec;
+      float2 d[P], o[P], w[P];
+      Vec<T>::unpack(row_vec(drs, v, in && a.i_dr >= 0), d);
+      if (PRE) {
+        float2 dh[P], r[P];
+        Vec<T>::unpack(row_vec(dhs, v, in), dh);
+        Vec<T>::unpack(row_vec(rs, v, in), r);
         w_pre.get(i, v, w);
 #pragma unroll
         for (int k = 0; k < P; ++k) {
-          rh[k] = mul2(rh[k], both(rq));
-          acc_pre[i][k] = fma2(dh[k], rh[k], acc_pre[i][k]);
-          d[k] = fma2(both(rq), fma2(rh[k], both(-c1), mul2(dh[k], w[k])), d[k]);
+          d[k] = fma2(r[k], both(-k1), fma2(both(rq), mul2(dh[k], w[k]), d[k]));
+          acc_pre[PRE ? i : 0][k] = fma2(dh[k], mul2(r[k], both(rq)), acc_pre[PRE ? i : 0][k]);
         }
       }
 #pragma unroll
       for (int k = 0; k < P; ++k) o[k] = mul2(both(a.residual_scale), d[k]);
-      reinterpret_cast<uint4*>(a.dx)[row * sh.nvec + v] = Vec<T>::pack(o);
-      if (post) {
-        float2 y[P], w[P], g[P];
-        Vec<T>::unpack(ys[v], y);
+      if (in) reinterpret_cast<uint4*>(a.dx)[(size_t)row * sh.nvec + v] = Vec<T>::pack(o);
+      if (POST) {
+        float2 y[P], g[P];
+        Vec<T>::unpack(row_vec(ys, v, in), y);
         w_post.get(i, v, w);
-        if (COL || full) gate_of(i, v, g);
+        if (FULL) Vec<T>::unpack(row_vec(gs, v, in), g);
 #pragma unroll
         for (int k = 0; k < P; ++k) {
-          const float2 yh = mul2(y[k], both(rp));
-          float2 dn = mul2(both(a.branch_scale), d[k]);
-          if (COL || full) {
-            const float2 dg = mul2(mul2(dn, w[k]), yh);
-            dn = mul2(dn, g[k]);
-            if (COL) acc_gate[COL ? i : 0][k] = add2(acc_gate[COL ? i : 0][k], dg);
-            else if (a.sigmoid) g[k] = mul2(dg, fma2(mul2(g[k], both(-1.0f)), g[k], g[k]));
-            else g[k] = dg;
-          } else {
-            dn = mul2(dn, both(grow));
+          float2 dy = mul2(d[k], y[k]), wd = mul2(w[k], d[k]);
+          if (FULL) {
+            const float2 s = a.sigmoid ? sigmoid2(g[k]) : g[k];
+            const float2 dg = mul2(mul2(dy, w[k]), both(k2));
+            g[k] = a.sigmoid ? mul2(dg, fma2(mul2(s, both(-1.0f)), s, s)) : dg;
+            dy = mul2(dy, s);
+            wd = mul2(wd, s);
           }
-          acc_post[i][k] = fma2(dn, yh, acc_post[i][k]);
-          o[k] = mul2(both(rp), fma2(yh, both(-c2), mul2(w[k], dn)));
+          acc_post[POST ? i : 0][k] = fma2(dy, both(k2), acc_post[POST ? i : 0][k]);
+          o[k] = fma2(wd, both(k2), mul2(y[k], both(-k3)));
         }
-        reinterpret_cast<uint4*>(a.dy)[row * sh.nvec + v] = Vec<T>::pack(o);
-        if (full) reinterpret_cast<uint4*>(a.dgate_full)[row * sh.nvec + v] = Vec<T>::pack(g);
+        if (in) reinterpret_cast<uint4*>(a.dy)[(size_t)row * sh.nvec + v] = Vec<T>::pack(o);
+        if (FULL && in) reinterpret_cast<uint4*>(a.dgate_full)[(size_t)row * sh.nvec + v] = Vec<T>::pack(g);
       }
     }
-    if (sh.stages == 1) {      // the longest rows: this item's stage is also the next one's
-      __syncthreads();
-      const int64_t next = it + gridDim.x;
-      if (threadIdx.x == 0 && next < items) ring.fill(sh, a.in, next, 0);
+    if (sh.stages <= 2) {      // long rows: a stage is too dear to wait for the next barrier
+      team_sync(team, sh.warps);
+      if (tt == 0 && row + sh.stages * step < rows) ring.fill(a.in, row + sh.stages * step, stage);
     }
     if (++stage == sh.stages) {
       stage = 0;
@@ -480,7 +513,7 @@ norm_bwd_kernel(const __grid_constant__ BwdArgs a, const __grid_constant__ Shape
   }
   // the column sums of this CTA: its teams' are joined in shared memory (the ring
   // is idle: every stage that was filled has been read)
-  auto join = [&](float2 (&acc)[NV][P], int which) {
+  auto join = [&](const auto& acc, int which) {
     float* const out = a.part + ((size_t)which * gridDim.x + blockIdx.x) * sh.H;
     float* const s = reinterpret_cast<float*>(ring_mem);
     __syncthreads();
@@ -499,21 +532,21 @@ norm_bwd_kernel(const __grid_constant__ BwdArgs a, const __grid_constant__ Shape
       out[c] = sum;
     }
   };
-  if (pre) join(acc_pre, 0);
-  if (post) join(acc_post, 1);
-  if constexpr (COL) join(acc_gate, 2);
+  if constexpr (PRE) join(acc_pre, 0);
+  if constexpr (POST) join(acc_post, 1);
 }
 
-// Joins the CTAs' column sums: 16 threads per column take every 16th CTA.
+// Joins the CTAs' column sums: 16 threads per column take every 16th CTA. A gate per
+// column shares its sum with the weight: with S = sum b D yh, dw_post = g S and
+// dgate = w_post S (times g (1 - g) behind a sigmoid).
 constexpr int kJoinCols = 32, kJoinRows = 16;
 
 __global__ void __launch_bounds__(kJoinCols * kJoinRows)
 norm_join_kernel(const float* __restrict__ part, int ctas, int H, const float* __restrict__ gate,
-                 int sigmoid_gate, float* __restrict__ dw_pre, float* __restrict__ dw_post,
-                 float* __restrict__ dgate) {
+                 const float* __restrict__ w_post, int sigmoid_gate, float* __restrict__ dw_pre,
+                 float* __restrict__ dw_post, float* __restrict__ dgate) {
   __shared__ float s[kJoinRows][kJoinCols + 1];
-  float* const out = blockIdx.y == 0 ? dw_pre : blockIdx.y == 1 ? dw_post : dgate;
-  if (!out) return;
+  if (!(blockIdx.y == 0 ? dw_pre : dw_post)) return;
   const int cx = threadIdx.x % kJoinCols, ry = threadIdx.x / kJoinCols;
   const int c = blockIdx.x * kJoinCols + cx;
   const float* p = part + (size_t)blockIdx.y * ctas * H;
@@ -524,15 +557,18 @@ norm_join_kernel(const float* __restrict__ part, int ctas, int H, const float* _
   }
   s[ry][cx] = sum;
   __syncthreads();
-  if (ry == 0 && c < H) {
-    float t = 0.0f;
+  if (ry != 0 || c >= H) return;
+  float t = 0.0f;
 #pragma unroll
-    for (int i = 0; i < kJoinRows; ++i) t += s[i][cx];
-    if (blockIdx.y == 2 && sigmoid_gate) {
-      const float g = sigmoid(__ldg(gate + c));
-      t *= g * (1.0f - g);
-    }
-    out[c] = t;
+  for (int i = 0; i < kJoinRows; ++i) t += s[i][cx];
+  if (blockIdx.y == 0) {
+    dw_pre[c] = t;
+  } else if (gate) {
+    const float z = __ldg(gate + c), g = sigmoid_gate ? sigmoid(z) : z;
+    dw_post[c] = t * g;
+    dgate[c] = t * __ldg(w_post + c) * (sigmoid_gate ? g * (1.0f - g) : 1.0f);
+  } else {
+    dw_post[c] = t;
   }
 }
 
@@ -544,13 +580,38 @@ Shape make_shape(int64_t T, int H, int f32, int tensors) {
   s.row_bytes = (uint32_t)H * (f32 ? 4 : 2);
   const int per_warp = 32 * (kCols / (f32 ? 4 : 8));
   s.warps = (s.nvec + per_warp - 1) / per_warp;
-  s.teams = kTeamThreads / (32 * s.warps);
-  if (s.teams < 1) s.teams = 1;
+  s.is_long = s.warps * 32 > kShort;
+  // rows that fit into shared memory: two at least for a team if there is more than one
+  const int64_t rows = kRingBytes / ((int64_t)s.row_bytes * tensors);
+  s.teams = s.is_long ? 1 : kShort / (32 * s.warps);
+  if (s.teams > rows / 2) s.teams = rows < 4 ? 1 : (int)(rows / 2);
   s.tensors = tensors;
-  const int64_t stage = (int64_t)s.teams * s.row_bytes * tensors;
-  s.stages = (int)(kRingBytes / stage);
+  s.stages = (int)(rows / s.teams);
   if (s.stages > kMaxStages) s.stages = kMaxStages;
   return s;      // H * element size <= 32768 leaves at least one stage
+}
+
+// A kernel variant as a type, and the choice of one.
+template <typename TT, int MAXT, bool POST, bool PRE, bool FULL>
+struct Variant {
+  using T = TT;
+  static constexpr int kMaxT = MAXT;
+  static constexpr bool kPost = POST, kPre = PRE, kFull = FULL;
+};
+template <typename T, int MAXT, typename F>
+cudaError_t pick_parts(bool post, bool pre, int gate, F f) {
+  if (!post) return f(Variant<T, MAXT, false, true, false>());
+  if (gate == kGateFull)
+    return pre ? f(Variant<T, MAXT, true, true, true>()) : f(Variant<T, MAXT, true, false, true>());
+  return pre ? f(Variant<T, MAXT, true, true, false>()) : f(Variant<T, MAXT, true, false, false>());
+}
+template <typename F>
+cudaError_t pick_norm(bool f32, const Shape& sh, bool post, bool pre, int gate, F f) {
+  if (f32)
+    return sh.is_long ? pick_parts<float, kLong>(post, pre, gate, f)
+                      : pick_parts<float, kShort>(post, pre, gate, f);
+  return sh.is_long ? pick_parts<__nv_bfloat16, kLong>(post, pre, gate, f)
+                    : pick_parts<__nv_bfloat16, kShort>(post, pre, gate, f);
 }
 
 size_t ring_bytes(const Shape& s) {
@@ -586,6 +647,7 @@ cudaError_t fp8moe_launch_norm_fwd(const NormFwdArgs& p, int num_sms, cudaStream
   const Shape sh = make_shape(p.T, p.H, p.f32, n);
   const int64_t items = (sh.T + sh.teams - 1) / sh.teams;
   const int grid = (int)(items < num_sms ? items : num_sms);
+  const bool post = p.w_post != nullptr, pre = p.w_pre != nullptr;
   const size_t smem = ring_bytes(sh);
   auto run = [&](auto kern) {
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
@@ -593,19 +655,10 @@ cudaError_t fp8moe_launch_norm_fwd(const NormFwdArgs& p, int num_sms, cudaStream
     kern<<<grid, sh.teams * sh.warps * 32, smem, s>>>(a, sh);
     return cudaGetLastError();
   };
-  // rows past 8192 columns need more than 512 threads, which halves the registers
-  const bool small = sh.teams * sh.warps * 32 <= kTeamThreads;
-  const bool col = p.gate_kind == kGateCol;
-  using bf16 = __nv_bfloat16;
-  if (p.f32)
-    return small ? (col ? run(norm_fwd_kernel<float, kTeamThreads, true>)
-                        : run(norm_fwd_kernel<float, kTeamThreads, false>))
-                 : (col ? run(norm_fwd_kernel<float, 1024, true>)
-                        : run(norm_fwd_kernel<float, 1024, false>));
-  return small ? (col ? run(norm_fwd_kernel<bf16, kTeamThreads, true>)
-                      : run(norm_fwd_kernel<bf16, kTeamThreads, false>))
-               : (col ? run(norm_fwd_kernel<bf16, 1024, true>)
-                      : run(norm_fwd_kernel<bf16, 1024, false>));
+  return pick_norm(p.f32, sh, post, pre, p.gate_kind, [&](auto v) {
+    using V = decltype(v);
+    return run(norm_fwd_kernel<typename V::T, V::kMaxT, V::kPost, V::kPre, V::kFull>);
+  });
 }
 
 int fp8moe_norm_bwd_ctas(int64_t T) {
@@ -626,9 +679,9 @@ cudaError_t fp8moe_launch_norm_bwd(const NormBwdArgs& p, int num_sms, cudaStream
   const bool post = p.w_post != nullptr, pre = p.w_pre != nullptr;
   a.i_dr = add(p.dr);
   a.i_dh = add(p.dh);
-  a.i_r = add(pre ? p.r : nullptr);
+  add(pre ? p.r : nullptr);
   a.i_y = add(p.y);
-  a.i_gate = add(post && p.gate_kind == kGateFull ? p.gate : nullptr);
+  add(post && p.gate_kind == kGateFull ? p.gate : nullptr);
   a.w_post = p.w_post;
   a.w_pre = p.w_pre;
   a.rstd_post = p.rstd_post;
@@ -636,7 +689,7 @@ cudaError_t fp8moe_launch_norm_bwd(const NormBwdArgs& p, int num_sms, cudaStream
   a.gate = static_cast<const float*>(p.gate);
   a.gate_kind = p.gate_kind;
   a.sigmoid = p.sigmoid;
-  a.residual_scale = p.residual_scale;
+  a.residual_scale = post ? p.residual_scale : 1.0f;
   a.branch_scale = p.branch_scale;
   a.dx = p.dx;
   a.dy = p.dy;
@@ -656,25 +709,15 @@ cudaError_t fp8moe_launch_norm_bwd(const NormBwdArgs& p, int num_sms, cudaStream
       kern<<<grid, sh.teams * sh.warps * 32, smem, s>>>(a, sh);
       return cudaGetLastError();
     };
-    const bool small = sh.teams * sh.warps * 32 <= kTeamThreads;
-    const bool col = p.gate_kind == kGateCol;
-    using bf16 = __nv_bfloat16;
-    cudaError_t e;
-    if (p.f32)
-      e = small ? (col ? run(norm_bwd_kernel<float, kTeamThreads, true>)
-                       : run(norm_bwd_kernel<float, kTeamThreads, false>))
-                : (col ? run(norm_bwd_kernel<float, 1024, true>)
-                       : run(norm_bwd_kernel<float, 1024, false>));
-    else
-      e = small ? (col ? run(norm_bwd_kernel<bf16, kTeamThreads, true>)
-                       : run(norm_bwd_kernel<bf16, kTeamThreads, false>))
-                : (col ? run(norm_bwd_kernel<bf16, 1024, true>)
-                       : run(norm_bwd_kernel<bf16, 1024, false>));
+    const cudaError_t e = pick_norm(p.f32, sh, post, pre, p.gate_kind, [&](auto v) {
+      using V = decltype(v);
+      return run(norm_bwd_kernel<typename V::T, V::kMaxT, V::kPost, V::kPre, V::kFull>);
+    });
     if (e != cudaSuccess) return e;
   }
-  const dim3 jg((unsigned)((p.H + kJoinCols - 1) / kJoinCols), 3, 1);
+  const dim3 jg((unsigned)((p.H + kJoinCols - 1) / kJoinCols), 2, 1);
   norm_join_kernel<<<jg, kJoinCols * kJoinRows, 0, s>>>(
-      p.part, grid, p.H, p.gate_kind == kGateCol ? a.gate : nullptr, p.sigmoid,
+      p.part, grid, p.H, p.gate_kind == kGateCol ? a.gate : nullptr, p.w_post, p.sigmoid,
       pre ? p.dw_pre : nullptr, post ? p.dw_post : nullptr,
       p.gate_kind == kGateCol ? static_cast<float*>(p.dgate) : nullptr);
   return cudaGetLastError();

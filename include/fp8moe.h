@@ -355,8 +355,8 @@ int fp8moe_combine_tokens_bwd(const void* dout, const void* rows, int64_t M, int
  *   r = residual_scale * x + branch_scale * g * (w_post * y * rstd(y))
  *   h = w_pre * r * rstd(r)                 (of r before it is rounded to `type`)
  * g: 1, or `gate` by gate_kind (FP8MOE_GATE_*), through 1 / (1 + exp(-gate)) with
- * sigmoid = 1.  w_post NULL: no block output (y NULL, no gate); r is x, is not
- * written, and only h is.  w_pre NULL: no h.  At least one of them is given.
+ * sigmoid = 1.  w_post NULL: no block output (y NULL, no gate, the scales are not
+ * used); r is x, is not written, and only h is.  w_pre NULL: no h.  At least one of them is given.
  * rstd_post and rstd_pre are what the gradient takes.  H * element size: a multiple
  * of 16 (FP8MOE_EALIGN), at most 32768 (FP8MOE_EINVAL).  All sums are f32. */
 int fp8moe_norm_fwd(const void* x, const void* y, int64_t T, int64_t H, int32_t type,
@@ -372,7 +372,7 @@ int fp8moe_norm_fwd(const void* x, const void* y, int64_t T, int64_t H, int32_t 
  *   dw_pre = sum_t dh rh,   dw_post = sum_t dn yh                  (f32 [H])
  *   dgate = branch_scale * D * w_post * yh, summed over what shares a gate value, times
  *   g (1 - g) with sigmoid = 1: f32 [T], f32 [H] or [T, H] of `type`, by gate_kind
- * Without w_post dx = D (r is x, unscaled).  Column sums are joined in a fixed order.
+ * Without w_post dx = D (r is x; the scales are not used).  Column sums are joined in a fixed order.
  * T = 0 writes zeros to dw_post, dw_pre and a per-channel dgate.  Workspace: FP8MOE_OP_NORM_BWD with M = T, K = H. */
 int fp8moe_norm_bwd(const void* dr, const void* dh, const void* r, const void* y, int64_t T,
                     int64_t H, int32_t type, const float* w_post, const float* w_pre,

@@ -18,8 +18,8 @@ def test_workspace_sizes():
     for op in (fb.OP_GMM_MXFP4_FWD, fb.OP_GMM_SILU_MXFP4_FWD):
         assert fb.workspace_size(op, M, K, 4096, 32) == M * K // 2 + words
     assert fb.workspace_size(fb.OP_GMM_MXFP4_FWD, 3, 32, 16, 1) == 256 + 256
-    assert fb.workspace_size(fb.OP_NORM_BWD, 4096, K, 0, 0) == 3 * 256 * K * 4
-    assert fb.workspace_size(fb.OP_NORM_BWD, 5, K, 0, 0) == 3 * 5 * K * 4
+    assert fb.workspace_size(fb.OP_NORM_BWD, 4096, K, 0, 0) == 2 * 256 * K * 4
+    assert fb.workspace_size(fb.OP_NORM_BWD, 5, K, 0, 0) == 2 * 5 * K * 4
     assert fb.workspace_size(fb.OP_NORM_BWD, 0, K, 0, 0) == 0
 
 
