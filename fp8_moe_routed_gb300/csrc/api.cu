@@ -284,19 +284,14 @@ int check_row(int64_t H, int32_t type, int* nvec) {
   return FP8MOE_OK;
 }
 
-int sort_impl(const int32_t* ids, int64_t T, int32_t topk, int32_t E, int64_t M,
-              int32_t* group_sizes, int32_t* slot_row, int32_t* row_slot, cudaStream_t stream,
-              int* sms) {
+int check_sort(const int32_t* ids, int64_t T, int32_t topk, int32_t E, int64_t M,
+               const int32_t* group_sizes, const int32_t* slot_row, const int32_t* row_slot) {
   int rc = check_route(T, topk, M);
   if (rc) return rc;
   if (E < 1 || E > 1024 || !group_sizes || (T > 0 && (!ids || !slot_row))) return FP8MOE_EINVAL;
   if (!aligned4(ids) || !aligned4(group_sizes) || !aligned4(slot_row) || !aligned4(row_slot))
     return FP8MOE_EALIGN;
-  rc = device_init(sms);
-  if (rc) return rc;
-  cudaError_t e = fp8moe_launch_sort_tokens(ids, T * topk, E, M, group_sizes, slot_row, row_slot,
-                                            stream);
-  return e == cudaSuccess ? FP8MOE_OK : cuda_fail(e);
+  return FP8MOE_OK;
 }
 
 int check_norm(int64_t T, int64_t H, int32_t type, int32_t gate_kind, int32_t sigmoid) {
@@ -784,24 +779,30 @@ int fp8moe_selftest_cast_f32(const float* x, int64_t n, int32_t fmt, uint8_t* co
 int fp8moe_sort_tokens(const int32_t* ids, int64_t T, int32_t topk, int32_t E, int64_t M,
                        int32_t* group_sizes, int32_t* slot_row, int32_t* row_slot,
                        fp8moe_stream_t stream) {
+  int rc = check_sort(ids, T, topk, E, M, group_sizes, slot_row, row_slot);
+  if (rc) return rc;
   int sms = 0;
-  return sort_impl(ids, T, topk, E, M, group_sizes, slot_row, row_slot, stream, &sms);
+  rc = device_init(&sms);
+  if (rc) return rc;
+  cudaError_t e = fp8moe_launch_sort_tokens(ids, T * topk, E, M, group_sizes, slot_row, row_slot,
+                                            stream);
+  return e == cudaSuccess ? FP8MOE_OK : cuda_fail(e);
 }
 
 int fp8moe_dispatch_tokens(const void* x, const int32_t* ids, int64_t T, int32_t topk, int64_t H,
                            int32_t type, int32_t E, int64_t M, void* rows, int32_t* group_sizes,
                            int32_t* slot_row, int32_t* row_slot, fp8moe_stream_t stream) {
   int nvec = 0, sms = 0;
-  int rc = check_route(T, topk, M);
+  int rc = check_sort(ids, T, topk, E, M, group_sizes, slot_row, row_slot);
   if (rc) return rc;
   rc = check_row(H, type, &nvec);
   if (rc) return rc;
-  if (T > 0 && M > 0 && (!x || !rows)) return FP8MOE_EINVAL;
+  if (T > 0 && (!x || (M > 0 && !rows))) return FP8MOE_EINVAL;
   if (!aligned16(x) || !aligned16(rows)) return FP8MOE_EALIGN;
-  rc = sort_impl(ids, T, topk, E, M, group_sizes, slot_row, row_slot, stream, &sms);
+  rc = device_init(&sms);
   if (rc) return rc;
-  if (T == 0 || M == 0) return FP8MOE_OK;
-  cudaError_t e = fp8moe_launch_dispatch(x, T, topk, nvec, slot_row, M, rows, sms, stream);
+  cudaError_t e = fp8moe_launch_dispatch(x, ids, T, topk, E, M, nvec, rows, group_sizes, slot_row,
+                                         row_slot, sms, stream);
   return e == cudaSuccess ? FP8MOE_OK : cuda_fail(e);
 }
 

@@ -43,6 +43,7 @@
 #include "groups.cuh"
 #include "kernels.h"
 #include "mxfp4.cuh"
+#include "pdl.cuh"
 #include "ptx_mx.cuh"
 
 namespace fp8moe {
@@ -223,6 +224,7 @@ gmm_mxfp4_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant_
 
   if (warp == 0) {
     // ========================= TMA producer: codes ========================
+    pdl_wait();        // the activations' codes and scales are the quantiser's
     // Like the MMA warp: the whole warp walks the steps, one thread issues.
     const bool leader = elect_one();
     int st = 0, e = 0;
@@ -312,6 +314,7 @@ gmm_mxfp4_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant_
     if (lane == 0) mbar_wait(&s.drain, 0, kWhereDrain);
   } else if (warp == 2) {
     // ===================== TMA producer: scale words ======================
+    pdl_wait();
     const bool leader = elect_one();
     int st = 0, e = 0;
     uint32_t ph = 0;
@@ -487,13 +490,14 @@ cudaError_t launch(const GmmMxfp4Args& a, int num_sms, cudaStream_t s) {
   cfg.blockDim = dim3(kThreads, 1, 1);
   cfg.dynamicSmemBytes = kSmemBytes;
   cfg.stream = s;
-  cudaLaunchAttribute attr[1];
+  cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeClusterDimension;
   attr[0].val.clusterDim.x = 2;
   attr[0].val.clusterDim.y = 1;
   attr[0].val.clusterDim.z = 1;
+  pdl_attribute(attr[1]);
   cfg.attrs = attr;
-  cfg.numAttrs = 1;
+  cfg.numAttrs = 2;
   err = cudaLaunchKernelEx(&cfg, kern, a.tmW, a.tmX[0], a.tmX[1], a.tmX[2], a.tmSw,
                            a.tmSx, a.gs,
                            static_cast<__nv_bfloat16*>(a.out), a.M, a.K, a.N, a.E);

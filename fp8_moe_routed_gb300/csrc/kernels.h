@@ -99,8 +99,10 @@ uint32_t fp8moe_status_take_route(cudaStream_t s);
 cudaError_t fp8moe_launch_sort_tokens(const int32_t* ids, int64_t n, int E, int64_t M,
                                       int32_t* group_sizes, int32_t* slot_row, int32_t* row_slot,
                                       cudaStream_t s);
-cudaError_t fp8moe_launch_dispatch(const void* x, int64_t T, int topk, int nvec,
-                                   const int32_t* slot_row, int64_t M, void* rows, int num_sms,
+// The sort and the copy; rows is not touched when M == 0.
+cudaError_t fp8moe_launch_dispatch(const void* x, const int32_t* ids, int64_t T, int topk, int E,
+                                   int64_t M, int nvec, void* rows, int32_t* group_sizes,
+                                   int32_t* slot_row, int32_t* row_slot, int num_sms,
                                    cudaStream_t s);
 cudaError_t fp8moe_launch_combine(const void* rows, int64_t T, int topk, int nvec, int f32,
                                   const int32_t* slot_row, int64_t M, const float* weights,

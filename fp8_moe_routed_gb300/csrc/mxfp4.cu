@@ -13,6 +13,7 @@
 #include "groups.cuh"
 #include "kernels.h"
 #include "mxfp4.cuh"
+#include "pdl.cuh"
 #include "vec16.cuh"
 
 namespace fp8moe {
@@ -51,6 +52,7 @@ mx_quantize_rows_kernel(const uint4* __restrict__ x, int64_t M, int K,
                         const int32_t* __restrict__ gs, int E, uint32_t* __restrict__ codes,
                         uint32_t* __restrict__ scales, int64_t scale_stride, int report) {
   __shared__ int32_t s_lo, s_hi;
+  pdl_launch_dependents();
   group_row_range_warp0(gs, E, M, 0, E, &s_lo, &s_hi, report && blockIdx.x == 0);
   __syncthreads();
   const int64_t T = s_hi;

@@ -28,6 +28,7 @@
 
 #include "fp8moe_status.cuh"
 #include "kernels.h"
+#include "pdl.cuh"
 #include "vec16.cuh"
 
 namespace fp8moe {
@@ -363,6 +364,7 @@ norm_bwd_kernel(const __grid_constant__ BwdArgs a, const __grid_constant__ Shape
   // the team's first row, and on to its next (T < 2^31: the sums stay below 2^32)
   const uint32_t row0 = blockIdx.x * sh.teams + team, step = gridDim.x * sh.teams;
   const uint32_t rows = (uint32_t)sh.T;
+  pdl_launch_dependents();
   if (tt == 0) {
     for (int i = 0; i < sh.stages; ++i) mbar_init(&ring.full[i], 1);
     fence_mbar_init();
@@ -550,10 +552,13 @@ norm_join_kernel(const float* __restrict__ part, int ctas, int H, const float* _
   const int cx = threadIdx.x % kJoinCols, ry = threadIdx.x / kJoinCols;
   const int c = blockIdx.x * kJoinCols + cx;
   const float* p = part + (size_t)blockIdx.y * ctas * H;
+  pdl_wait();          // the sums are the backward kernel's
   float sum = 0.0f;
   if (c < H) {
+    // plain loads: the kernel that writes them may still run when this one starts
 #pragma unroll 4
-    for (int i = ry; i < ctas; i += kJoinRows) sum += __ldg(p + (size_t)i * H + c);
+    for (int i = ry; i < ctas; i += kJoinRows)
+      sum += *static_cast<const volatile float*>(p + (size_t)i * H + c);
   }
   s[ry][cx] = sum;
   __syncthreads();
@@ -716,9 +721,19 @@ cudaError_t fp8moe_launch_norm_bwd(const NormBwdArgs& p, int num_sms, cudaStream
     if (e != cudaSuccess) return e;
   }
   const dim3 jg((unsigned)((p.H + kJoinCols - 1) / kJoinCols), 2, 1);
-  norm_join_kernel<<<jg, kJoinCols * kJoinRows, 0, s>>>(
-      p.part, grid, p.H, p.gate_kind == kGateCol ? a.gate : nullptr, p.w_post, p.sigmoid,
-      pre ? p.dw_pre : nullptr, post ? p.dw_post : nullptr,
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = jg;
+  cfg.blockDim = dim3(kJoinCols * kJoinRows, 1, 1);
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  fp8moe::pdl_attribute(attr[0]);
+  cfg.attrs = attr;
+  cfg.numAttrs = grid > 0 ? 1 : 0;
+  const cudaError_t e = cudaLaunchKernelEx(
+      &cfg, norm_join_kernel, static_cast<const float*>(p.part), grid, p.H,
+      p.gate_kind == kGateCol ? a.gate : nullptr, p.w_post, p.sigmoid, pre ? p.dw_pre : nullptr,
+      post ? p.dw_post : nullptr,
       p.gate_kind == kGateCol ? static_cast<float*>(p.dgate) : nullptr);
+  if (e != cudaSuccess) return e;
   return cudaGetLastError();
 }

@@ -20,6 +20,7 @@
 #include "fp8moe_status.cuh"
 #include "groups.cuh"
 #include "kernels.h"
+#include "pdl.cuh"
 #include "vec16.cuh"
 
 namespace cg = cooperative_groups;
@@ -63,6 +64,7 @@ sort_kernel(const int32_t* __restrict__ ids, int64_t n, int E, int64_t M,
   const int ctas = (int)cluster.num_blocks(), rank = (int)cluster.block_rank();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
+  pdl_launch_dependents();
   for (int i = threadIdx.x; i < kSortWarps * E; i += kSortThreads) counts[i] = 0;
   __syncthreads();
 
@@ -153,7 +155,8 @@ sort_kernel(const int32_t* __restrict__ ids, int64_t n, int E, int64_t M,
 // The row of a slot, -1 for none. A caller's entry past the buffer (a slot_row
 // made for a larger one) counts as none: it is never followed out of bounds.
 __device__ __forceinline__ int32_t row_of(const int32_t* slot_row, int64_t s, int64_t M) {
-  const int32_t r = __ldg(slot_row + s);
+  // a plain load: the kernel that writes slot_row may still run when this one starts
+  const int32_t r = *static_cast<const volatile int32_t*>(slot_row + s);
   return r < M ? r : -1;
 }
 
@@ -173,11 +176,12 @@ dispatch_kernel(const uint4* __restrict__ x, int64_t T, int topk, int nvec, int 
        it += step) {
     const int64_t t = it / chunks;
     const int v0 = (int)(it - t * chunks) * (32 * kMoveVecs) + lane;
-    const int32_t r = lane < topk ? row_of(slot_row, t * topk + lane, M) : -1;
     uint4 v[kMoveVecs];
 #pragma unroll
     for (int i = 0; i < kMoveVecs; ++i)
       if (v0 + 32 * i < nvec) v[i] = __ldg(x + t * nvec + v0 + 32 * i);
+    pdl_wait();            // the row numbers are the sort's
+    const int32_t r = lane < topk ? row_of(slot_row, t * topk + lane, M) : -1;
     for (int j = 0; j < topk; ++j) {
       const int32_t row = __shfl_sync(0xffffffffu, r, j);
       if (row < 0) continue;
@@ -187,6 +191,84 @@ dispatch_kernel(const uint4* __restrict__ x, int64_t T, int topk, int nvec, int 
         if (v0 + 32 * i < nvec) d[32 * i] = v[i];
     }
   }
+}
+
+// --------------------------------------------------------- dispatch of few slots
+// Up to 1024 slots sort and copy in one launch: every CTA holds all keys in shared
+// memory and counts the rows of its own token's slots, row(s) = #{key < key(s)} +
+// #{s' < s: key = key(s)}, a warp per slot, 32 keys at a time. A CTA copies 256 vectors
+// of one token; the first of a token also writes its row numbers, one more CTA the group
+// sizes and the empty tail of row_slot. (One token to eight experts: 4 us against 10 us
+// for the two launches.)
+constexpr int kFewSlots = 1024;
+
+__global__ void __launch_bounds__(kMoveThreads)
+dispatch_few_kernel(const uint4* __restrict__ x, const int32_t* __restrict__ ids, int T, int topk,
+                    int E, int64_t M, int nvec, int chunks, uint4* __restrict__ rows,
+                    int32_t* __restrict__ group_sizes, int32_t* __restrict__ slot_row,
+                    int32_t* __restrict__ row_slot) {
+  __shared__ int32_t s_key[kFewSlots];
+  __shared__ int32_t s_row[32];
+  __shared__ int32_t s_count[kMaxExperts];
+  const int n = T * topk;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int t = blockIdx.x / chunks, chunk = blockIdx.x - t * chunks;
+  const int vec = chunk * kMoveThreads + threadIdx.x;
+  const bool copies = t < T && vec < nvec;
+  uint4 v;
+  if (copies) v = __ldg(x + (int64_t)t * nvec + vec);
+  bool bad = false;
+  for (int i = threadIdx.x; i < n; i += kMoveThreads) {
+    const int32_t e = __ldg(ids + i);
+    bad |= e >= E;
+    s_key[i] = e >= 0 && e < E ? e : E;
+  }
+  if (t < T) {
+    __syncthreads();
+    for (int j = warp; j < topk; j += kMoveThreads / 32) {
+      const int s = t * topk + j, key = s_key[s];
+      int before = 0;
+      for (int i = lane; i < n; i += 32) before += s_key[i] < key || (s_key[i] == key && i < s);
+      int row = __reduce_add_sync(0xffffffffu, before);
+      if (key == E || row >= M) row = -1;
+      if (lane == 0) {
+        s_row[j] = row;
+        if (chunk == 0) {
+          slot_row[s] = row;
+          if (row >= 0 && row_slot) row_slot[row] = s;
+        }
+      }
+    }
+    __syncthreads();
+    if (!copies) return;
+    for (int j = 0; j < topk; ++j)
+      if (s_row[j] >= 0) rows[(int64_t)s_row[j] * nvec + vec] = v;
+    return;
+  }
+  for (int e = threadIdx.x; e < E; e += kMoveThreads) s_count[e] = 0;
+  __syncthreads();
+  for (int i = threadIdx.x; i < n; i += kMoveThreads)
+    if (s_key[i] < E) atomicAdd(&s_count[s_key[i]], 1);
+  const bool any_bad = __syncthreads_or(bad);
+  if (warp == 0) {
+    int carry = 0;
+    for (int base = 0; base < E; base += 32) {
+      const int e = base + lane;
+      const int c = e < E ? s_count[e] : 0;
+      const int incl = warp_incl_scan(c, lane);
+      const int64_t lo = carry + incl - c, hi = carry + incl;
+      if (e < E) group_sizes[e] = (int32_t)((hi < M ? hi : M) - (lo < M ? lo : M));
+      carry += __shfl_sync(0xffffffffu, incl, 31);
+    }
+    if (lane == 0) {
+      s_row[0] = carry;
+      if (carry > M) status_set(kStatusGroupsExceedM);
+      if (any_bad) status_set(kStatusBadExpert);
+    }
+  }
+  __syncthreads();
+  if (row_slot)
+    for (int64_t r = s_row[0] + (int64_t)threadIdx.x; r < M; r += kMoveThreads) row_slot[r] = -1;
 }
 
 // --------------------------------------------------------------------- combine
@@ -335,14 +417,32 @@ cudaError_t fp8moe_launch_sort_tokens(const int32_t* ids, int64_t n, int E, int6
   return cudaGetLastError();
 }
 
-cudaError_t fp8moe_launch_dispatch(const void* x, int64_t T, int topk, int nvec,
-                                   const int32_t* slot_row, int64_t M, void* rows, int num_sms,
+cudaError_t fp8moe_launch_dispatch(const void* x, const int32_t* ids, int64_t T, int topk, int E,
+                                   int64_t M, int nvec, void* rows, int32_t* group_sizes,
+                                   int32_t* slot_row, int32_t* row_slot, int num_sms,
                                    cudaStream_t s) {
   using namespace fp8moe::route;
+  if (T * topk <= kFewSlots) {
+    const int chunks = (nvec + kMoveThreads - 1) / kMoveThreads;
+    dispatch_few_kernel<<<(unsigned)(T * chunks + 1), kMoveThreads, 0, s>>>(
+        static_cast<const uint4*>(x), ids, (int)T, topk, E, M, nvec, chunks,
+        static_cast<uint4*>(rows), group_sizes, slot_row, row_slot);
+    return cudaGetLastError();
+  }
+  cudaError_t err = fp8moe_launch_sort_tokens(ids, T * topk, E, M, group_sizes, slot_row, row_slot, s);
+  if (err != cudaSuccess || M == 0) return err;
   const int chunks = (nvec + 32 * kMoveVecs - 1) / (32 * kMoveVecs);
-  const int grid = grid_for(T * chunks, kMoveThreads / 32, num_sms, 8);
-  dispatch_kernel<<<grid, kMoveThreads, 0, s>>>(static_cast<const uint4*>(x), T, topk, nvec, chunks,
-                                                slot_row, M, static_cast<uint4*>(rows));
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)grid_for(T * chunks, kMoveThreads / 32, num_sms, 8), 1, 1);
+  cfg.blockDim = dim3(kMoveThreads, 1, 1);
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  fp8moe::pdl_attribute(attr[0]);
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  err = cudaLaunchKernelEx(&cfg, dispatch_kernel, static_cast<const uint4*>(x), T, topk, nvec, chunks,
+                           static_cast<const int32_t*>(slot_row), M, static_cast<uint4*>(rows));
+  if (err != cudaSuccess) return err;
   return cudaGetLastError();
 }
 
