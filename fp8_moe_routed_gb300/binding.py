@@ -572,7 +572,7 @@ def _gate(gate, kind: Optional[str], T: int, H: int, dtype):
         return 0, None, None
     if kind not in GATES:
         raise ValueError(f"gate_kind must be one of {sorted(GATES)}, got {kind!r}")
-    shape = {"token": (T,), "channel": (H,), "full": (T, H)}[kind]
+    shape = (T,) if kind == "token" else (H,) if kind == "channel" else (T, H)
     ty = dtype if kind == "full" else torch.float32
     _req(gate, ty, "gate", len(shape))
     if tuple(gate.shape) != shape:

@@ -19,23 +19,23 @@
 namespace fp8moe {
 namespace mx {
 
-__device__ __forceinline__ uint32_t max_bits(const uint4& v) {
-  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-  uint32_t m = 0;
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    m = max(m, w[i] & 0x7FFFu);
-    m = max(m, (w[i] >> 16) & 0x7FFFu);
-  }
-  return m;
+// The larger magnitudes' bf16 bits, in both halves.
+__device__ __forceinline__ uint32_t max_abs2(uint32_t a, uint32_t b) {
+  return __vmaxu2(a, b & 0x7FFF7FFFu);
+}
+__device__ __forceinline__ uint32_t max_bits2(const uint4& v) {
+  return max_abs2(max_abs2(max_abs2(v.x & 0x7FFF7FFFu, v.y), v.z), v.w);
 }
 
-__device__ __forceinline__ uint32_t quantize8(const uint4& v, float inv) {
+// Eight values times inv as codes; the codes of a NaN block (whatever the conversion
+// made of it) are zeros.
+__device__ __forceinline__ uint32_t quantize8(const uint4& v, uint32_t byte, float inv) {
   float2 f[4];
   Vec<__nv_bfloat16>::unpack(v, f);
 #pragma unroll
-  for (int i = 0; i < 4; ++i) f[i] = inv == 0.0f ? both(0.0f) : mul2(f[i], both(inv));
-  return f32x8_to_e2m1x8(f);
+  for (int i = 0; i < 4; ++i) f[i] = mul2(f[i], both(inv));
+  const uint32_t q = f32x8_to_e2m1x8(f);
+  return byte == kMxNan ? 0u : q;
 }
 
 // ------------------------------------------------------------ activation rows
@@ -71,12 +71,12 @@ mx_quantize_rows_kernel(const uint4* __restrict__ x, int64_t M, int K,
       v[i] = v0 + 32 * i < nvec ? __ldg(x + row * nvec + v0 + 32 * i) : make_uint4(0, 0, 0, 0);
 #pragma unroll
     for (int i = 0; i < kRowsUnroll; ++i) {
-      uint32_t m = max_bits(v[i]);
-      m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
-      m = max(m, __shfl_xor_sync(0xffffffffu, m, 2));
-      const uint32_t byte = mx_scale_byte(m);
+      uint32_t m = max_bits2(v[i]);
+      m = __vmaxu2(m, __shfl_xor_sync(0xffffffffu, m, 1));
+      m = __vmaxu2(m, __shfl_xor_sync(0xffffffffu, m, 2));
+      const uint32_t byte = mx_scale_byte(max(m & 0xFFFFu, m >> 16));
       const int vi = v0 + 32 * i;
-      if (vi < nvec) codes[row * nvec + vi] = quantize8(v[i], mx_inv_scale(byte));
+      if (vi < nvec) codes[row * nvec + vi] = quantize8(v[i], byte, mx_inv_scale(byte));
       uint32_t word = byte << (8 * ((lane >> 2) & 3));
       word |= __shfl_xor_sync(0xffffffffu, word, 4);
       word |= __shfl_xor_sync(0xffffffffu, word, 8);
@@ -112,25 +112,23 @@ mx_quantize_weights_kernel(const uint32_t* __restrict__ w, int K, int N, int k_t
   const uint32_t* src = w + ((e * K + k0) * (int64_t)N + n) / 2;
 #pragma unroll
   for (int i = 0; i < kMxBlock; ++i) v[i] = in ? __ldg(src + (int64_t)i * (N / 2)) : 0u;
+  uint32_t m = 0;
+#pragma unroll
+  for (int i = 0; i < kMxBlock; ++i) m = max_abs2(m, v[i]);
 #pragma unroll
   for (int c = 0; c < 2; ++c) {
-    uint32_t m = 0;
-#pragma unroll
-    for (int i = 0; i < kMxBlock; ++i) m = max(m, (v[i] >> (16 * c)) & 0x7FFFu);
-    const uint32_t byte = mx_scale_byte(m);
+    const uint32_t byte = mx_scale_byte(c ? m >> 16 : m & 0xFFFFu);
     const float inv = mx_inv_scale(byte);
     uint32_t q[4];
 #pragma unroll
     for (int g = 0; g < 4; ++g) {
-      float2 f[4];
+      // this column's eight values of the group, two a word
+      uint4 x;
+      uint32_t* const p = &x.x;
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const uint32_t a = v[8 * g + 2 * i], b = v[8 * g + 2 * i + 1];
-        const float2 x = c ? make_float2(bf16hi_to_f32(a), bf16hi_to_f32(b))
-                           : make_float2(bf16lo_to_f32(a), bf16lo_to_f32(b));
-        f[i] = inv == 0.0f ? both(0.0f) : mul2(x, both(inv));
-      }
-      q[g] = f32x8_to_e2m1x8(f);
+      for (int i = 0; i < 4; ++i)
+        p[i] = __byte_perm(v[8 * g + 2 * i], v[8 * g + 2 * i + 1], c ? 0x7632 : 0x5410);
+      q[g] = quantize8(x, byte, inv);
     }
     s_code[2 * lane + c][warp] = make_uint4(q[0], q[1], q[2], q[3]);
     s_scale[warp >> 2][2 * lane + c][warp & 3] = (uint8_t)byte;

@@ -24,10 +24,10 @@ __device__ __forceinline__ uint32_t mx_scale_byte(uint32_t amax_bits) {
   return e == 0xFFu ? kMxNan : e > 2u ? e - 2u : 0u;
 }
 
-// 1 / X for a scale byte (<= 252 when not NaN): 2^(127 - byte), a normal number.
-// A NaN block's codes are zeros.
+// 1 / X for a scale byte (<= 252 when not NaN): 2^(127 - byte), a normal number. A NaN
+// byte gives some number: the caller does not use the codes.
 __device__ __forceinline__ float mx_inv_scale(uint32_t byte) {
-  return byte == kMxNan ? 0.0f : __uint_as_float((254u - byte) << 23);
+  return __uint_as_float((254u - byte) << 23);
 }
 
 // X itself: 2^(byte - 127); byte 0 is the subnormal 2^-127, 0xFF is NaN.

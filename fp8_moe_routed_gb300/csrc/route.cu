@@ -50,6 +50,7 @@ __device__ __forceinline__ int warp_incl_scan(int v, int lane) {
 constexpr int kSortCtas = 8;
 constexpr int kSortThreads = 1024;
 constexpr int kSortWarps = kSortThreads / 32;
+constexpr int kSortHeld = 8;      // batches of a warp kept in registers between the passes
 
 __global__ void __launch_bounds__(kSortThreads, 1)
 sort_kernel(const int32_t* __restrict__ ids, int64_t n, int E, int64_t M,
@@ -59,6 +60,7 @@ sort_kernel(const int32_t* __restrict__ ids, int64_t n, int E, int64_t M,
   int32_t* const counts = sm;                           // [kSortWarps][E]
   int32_t* const cta_total = sm + (size_t)kSortWarps * E;   // [E], read by the other CTAs
   __shared__ int32_t s_warp[kSortWarps];
+  __shared__ int32_t s_base[kMaxExperts];    // first row of this CTA's slots of an expert
   __shared__ int64_t s_rows;
   cg::cluster_group cluster = cg::this_cluster();
   const int ctas = (int)cluster.num_blocks(), rank = (int)cluster.block_rank();
@@ -74,20 +76,29 @@ sort_kernel(const int32_t* __restrict__ ids, int64_t n, int E, int64_t M,
   const int64_t b1 = b0 + per < batches ? b0 + per : batches;
   int32_t* const mine = counts + (size_t)warp * E;
   bool bad = false;
-  for (int64_t b = b0; b < b1; ++b) {
+  auto fetch = [&](int64_t b) -> int32_t {
     const int64_t s = b * 32 + lane;
-    const int32_t e = s < n ? __ldg(ids + s) : -1;
+    const int32_t e = b < b1 && s < n ? __ldg(ids + s) : -1;
     bad |= e >= E;
-    const int32_t key = (e >= 0 && e < E) ? e : -1;
+    return e >= 0 && e < E ? e : -1;
+  };
+  auto count = [&](int32_t key) {
     const uint32_t same = __match_any_sync(0xffffffffu, key);
     if (key >= 0 && lane == __ffs(same) - 1) mine[key] += __popc(same);
     __syncwarp();
-  }
+  };
+  int32_t held[kSortHeld];       // the first batches' keys, all loads in flight at once
+#pragma unroll
+  for (int i = 0; i < kSortHeld; ++i) held[i] = fetch(b0 + i);
+#pragma unroll
+  for (int i = 0; i < kSortHeld; ++i)
+    if (b0 + i < b1) count(held[i]);
+  for (int64_t b = b0 + kSortHeld; b < b1; ++b) count(fetch(b));
   __syncthreads();
   // thread e: exclusive scan of expert e over this CTA's warps
   for (int e = threadIdx.x; e < E; e += kSortThreads) {
     int32_t run = 0;
-#pragma unroll 8
+#pragma unroll
     for (int w = 0; w < kSortWarps; ++w) {
       const int32_t c = counts[(size_t)w * E + e];
       counts[(size_t)w * E + e] = run;
@@ -114,7 +125,7 @@ sort_kernel(const int32_t* __restrict__ ids, int64_t n, int E, int64_t M,
     for (int w = 0; w < warp; ++w) base += s_warp[w];
     const int32_t start = base + incl - total;
     if (e < E) {
-      for (int w = 0; w < kSortWarps; ++w) counts[(size_t)w * E + e] += start + before;
+      s_base[e] = start + before;
       if (rank == 0) {
         const int64_t lo = start < M ? start : M;
         const int64_t hi = (int64_t)start + total < M ? (int64_t)start + total : M;
@@ -127,13 +138,11 @@ sort_kernel(const int32_t* __restrict__ ids, int64_t n, int E, int64_t M,
     }
   }
   __syncthreads();
-  for (int64_t b = b0; b < b1; ++b) {
+  auto place = [&](int64_t b, int32_t key) {
     const int64_t s = b * 32 + lane;
-    const int32_t e = s < n ? __ldg(ids + s) : -1;
-    const int32_t key = (e >= 0 && e < E) ? e : -1;
     const uint32_t same = __match_any_sync(0xffffffffu, key);
     int32_t row = -1;
-    if (key >= 0) row = mine[key] + __popc(same & ((1u << lane) - 1u));
+    if (key >= 0) row = s_base[key] + mine[key] + __popc(same & ((1u << lane) - 1u));
     __syncwarp();
     if (key >= 0 && lane == __ffs(same) - 1) mine[key] += __popc(same);
     __syncwarp();
@@ -142,7 +151,11 @@ sort_kernel(const int32_t* __restrict__ ids, int64_t n, int E, int64_t M,
       slot_row[s] = row;
       if (row >= 0 && row_slot) row_slot[row] = (int32_t)s;
     }
-  }
+  };
+#pragma unroll
+  for (int i = 0; i < kSortHeld; ++i)
+    if (b0 + i < b1) place(b0 + i, held[i]);
+  for (int64_t b = b0 + kSortHeld; b < b1; ++b) place(b, fetch(b));
   if (row_slot) {
     for (int64_t r = s_rows + (int64_t)rank * kSortThreads + threadIdx.x; r < M;
          r += (int64_t)ctas * kSortThreads)
@@ -155,8 +168,7 @@ sort_kernel(const int32_t* __restrict__ ids, int64_t n, int E, int64_t M,
 // The row of a slot, -1 for none. A caller's entry past the buffer (a slot_row
 // made for a larger one) counts as none: it is never followed out of bounds.
 __device__ __forceinline__ int32_t row_of(const int32_t* slot_row, int64_t s, int64_t M) {
-  // a plain load: the kernel that writes slot_row may still run when this one starts
-  const int32_t r = *static_cast<const volatile int32_t*>(slot_row + s);
+  const int32_t r = __ldg(slot_row + s);
   return r < M ? r : -1;
 }
 
@@ -181,7 +193,9 @@ dispatch_kernel(const uint4* __restrict__ x, int64_t T, int topk, int nvec, int 
     for (int i = 0; i < kMoveVecs; ++i)
       if (v0 + 32 * i < nvec) v[i] = __ldg(x + t * nvec + v0 + 32 * i);
     pdl_wait();            // the row numbers are the sort's
-    const int32_t r = lane < topk ? row_of(slot_row, t * topk + lane, M) : -1;
+    // (not by row_of: its load may use a cache that does not see a kernel still running)
+    int32_t r = lane < topk ? __ldcg(slot_row + t * topk + lane) : -1;
+    if (r >= M) r = -1;
     for (int j = 0; j < topk; ++j) {
       const int32_t row = __shfl_sync(0xffffffffu, r, j);
       if (row < 0) continue;
