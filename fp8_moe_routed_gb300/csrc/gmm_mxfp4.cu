@@ -81,7 +81,7 @@ constexpr int kFirstSf = 4, kFirstEpi = kFirstSf + 4 * kSfGroups;
 constexpr int kEpiWarps = 8;
 constexpr int kThreads = (kFirstEpi + kEpiWarps) * 32;   // 896
 constexpr int kChunk = 16;                   // token rows that four epilogue warps turn at a time
-constexpr int kTurnBytes = kChunk * kRowsA * 2;
+constexpr int kTurnBytes = kChunk * (kRowsA * 2 + 16);
 
 struct Smem {
   uint64_t full[kStages];      // even CTA: the stage's four code boxes landed and both CTAs'
@@ -273,10 +273,15 @@ gmm_mxfp4_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant_
       int st = 0, sl = 0, ab = 0, e = 0;
       uint32_t ph = 0, tph = 0;
       bool ok = true, ready = false;
+      if (cluster < total) e = expert_of(s, cluster, 0);
+      uint32_t tok = s.tok[e];
       for (int u = cluster; u < total && ok; u += nclusters) {
-        e = expert_of(s, u, e);
-        const uint32_t idesc0 = make_idesc_mxf4(kUnitN, s.tok[e], 0);
-        const uint32_t idesc2 = make_idesc_mxf4(kUnitN, s.tok[e], 2);
+        const uint32_t idesc0 = make_idesc_mxf4(kUnitN, tok, 0);
+        const uint32_t idesc2 = make_idesc_mxf4(kUnitN, tok, 2);
+        if (u + nclusters < total) {       // the next unit's, while this one runs
+          e = expert_of(s, u + nclusters, e);
+          tok = s.tok[e];
+        }
         const uint32_t d = tmem + (uint32_t)(ab * kDCols);
         if (!mbar_wait(&s.tempty[ab], tph ^ 1, kWhereMma)) { ok = false; break; }
         tc_fence_after();
@@ -415,6 +420,12 @@ gmm_mxfp4_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant_
     // 256 (SwiGLU: 128) contiguous bytes of a token.
     constexpr int kCols = SWIGLU ? kRowsA / 2 : kRowsA;     // outputs of a token in this CTA
     constexpr int kPieces = kCols / 8;
+    constexpr uint32_t kPitch = kCols * 2 + 16;             // rows of 16 bytes fall into all banks
+    const uint32_t turn_addr = smem_u32(turn);
+    // this lane's row of the four 8 x 8 pieces: pieces (tokens 0..7, rows 0..7), (0..7, 8..15),
+    // (8..15, 0..7), (8..15, 8..15)
+    const uint32_t st_row = (uint32_t)((lane >> 4) * 8 + (lane & 7));
+    const uint32_t st_col = (uint32_t)(((lane >> 3) & 1) * 16);
     const int width = SWIGLU ? F : N;
     int ab = 0, buf = 0, e = 0;
     uint32_t tph = 0;
@@ -428,39 +439,48 @@ gmm_mxfp4_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant_
       tc_fence_after();
       const int col0 = SWIGLU ? t.w0 * kRowsA + rank * 64 : t.w0 * kUnitN + rank * kRowsA;
       for (int c0 = half * kChunk; c0 < t.tok; c0 += 2 * kChunk) {
-        uint32_t w[kChunk];
-        tmem_ld16(tq + (uint32_t)(ab * kDCols + c0), w);
+        // rows 0..15 and 16..31 of the quarter: a thread holds, of row (lane / 4) and the row
+        // 8 below it, tokens 2 (lane % 4), + 1 and the same 8 further on. The transposing
+        // matrix store turns 8 x 8 pieces of such pairs into 16 bytes of a token's row.
+        uint32_t lo[8], hi[8];
+        tmem_ld_16x256b_x2(tq + (uint32_t)(ab * kDCols + c0), lo);
+        tmem_ld_16x256b_x2(tq + (16u << 16) + (uint32_t)(ab * kDCols + c0), hi);
         tmem_ld_wait();
-        uint16_t* const mine = reinterpret_cast<uint16_t*>(turn + (2 * half + buf) * kTurnBytes);
+        const uint32_t mine = turn_addr + (uint32_t)((2 * half + buf) * kTurnBytes);
+        uint32_t pk[4];
         if (SWIGLU) {
-          const bool up = lane >= 16;
-          uint16_t* const p = mine + (up ? kCols : 0) + quarter * 16 + (lane & 15);
+          // gate rows and the up rows of the same columns
 #pragma unroll
-          for (int j = 0; j < kChunk; j += 2) {
-            // lanes 0..15 take token j, lanes 16..31 token j + 1
-            const float send = __uint_as_float(up ? w[j] : w[j + 1]);
-            const float got = __shfl_xor_sync(0xffffffffu, send, 16);
-            const float g = up ? got : __uint_as_float(w[j]);
-            const float v = up ? __uint_as_float(w[j + 1]) : got;
-            const float h = __fmul_rn(__fdiv_rn(g, __fadd_rn(1.0f, expf(-g))), v);
-            p[j * kCols] = (uint16_t)(f32x2_to_bf16x2(h, 0.0f) & 0xFFFFu);
+          for (int j = 0; j < 8; j += 2) {
+            float h[2];
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+              const float g = __uint_as_float(lo[j + i]), v = __uint_as_float(hi[j + i]);
+              h[i] = __fmul_rn(__fdiv_rn(g, __fadd_rn(1.0f, expf(-g))), v);
+            }
+            pk[j / 2] = f32x2_to_bf16x2(h[0], h[1]);
           }
+          stmatrix_x4_trans(mine + st_row * kPitch + (uint32_t)(quarter * 32) + st_col, pk);
         } else {
-          uint16_t* const p = mine + quarter * 32 + lane;
 #pragma unroll
-          for (int j = 0; j < kChunk; ++j)
-            p[j * kCols] = (uint16_t)(f32x2_to_bf16x2(__uint_as_float(w[j]), 0.0f) & 0xFFFFu);
+          for (int j = 0; j < 8; j += 2)
+            pk[j / 2] = f32x2_to_bf16x2(__uint_as_float(lo[j]), __uint_as_float(lo[j + 1]));
+          stmatrix_x4_trans(mine + st_row * kPitch + (uint32_t)(quarter * 64) + st_col, pk);
+#pragma unroll
+          for (int j = 0; j < 8; j += 2)
+            pk[j / 2] = f32x2_to_bf16x2(__uint_as_float(hi[j]), __uint_as_float(hi[j + 1]));
+          stmatrix_x4_trans(mine + st_row * kPitch + (uint32_t)(quarter * 64) + 32u + st_col, pk);
         }
         // the barrier also orders this turn's writes after the reads of the one before
         // the last, which had the same buffer
         named_bar_sync(1 + half, 128);
-        const uint4* const src = reinterpret_cast<const uint4*>(mine);
 #pragma unroll
         for (int i = 0; i < kChunk * kPieces / 128; ++i) {
           const int q = i * 128 + quarter * 32 + lane;
           const int j = q / kPieces, col = col0 + (q % kPieces) * 8;
           if (c0 + j < t.rows && col < width)
-            *reinterpret_cast<uint4*>(o16 + ((int64_t)t.m0 + c0 + j) * width + col) = src[q];
+            *reinterpret_cast<uint4*>(o16 + ((int64_t)t.m0 + c0 + j) * width + col) =
+                ld_shared_16B(mine + (uint32_t)(j * kPitch + (q % kPieces) * 16));
         }
         buf ^= 1;
       }

@@ -67,6 +67,32 @@ __device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t (&r)[8])
         "r"(r[7]) : "memory");
 }
 
+// 16 lanes x 16 consecutive 32-bit columns: thread t gets, of lane t / 4, columns
+// 2 (t % 4) and + 1 in r[0], r[1], of lane t / 4 + 8 the same in r[2], r[3], and both
+// 8 columns further on in r[4..7].
+__device__ __forceinline__ void tmem_ld_16x256b_x2(uint32_t taddr, uint32_t (&r)[8]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.16x256b.x2.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+        "=r"(r[7])
+      : "r"(taddr));
+}
+
+// Four 8 x 8 matrices of 16-bit values, stored transposed: thread t's pair of register i
+// goes to rows 2 (t % 4), + 1 and column t / 4 of matrix i; lane 8 i + j gives the
+// address of row j of matrix i (16 bytes).
+__device__ __forceinline__ void stmatrix_x4_trans(uint32_t addr, const uint32_t (&r)[4]) {
+  asm volatile("stmatrix.sync.aligned.m8n8.x4.trans.shared.b16 [%0], {%1, %2, %3, %4};"
+               ::"r"(addr), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]) : "memory");
+}
+
+__device__ __forceinline__ uint4 ld_shared_16B(uint32_t addr) {
+  uint4 v;
+  asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr) : "memory");
+  return v;
+}
+
 // Instruction descriptor of kind::mxf4 with e8m0 scales, both operands e2m1 and
 // K-major, K = 64: scale-factor id of B in [4,6), A format in [7,10), B format in
 // [10,12) (1 = e2m1), N >> 3 in [17,23), scale format bit 23 (1 = e8m0), M >> 4 in
