@@ -62,8 +62,12 @@ constexpr int kSaBytes = 2 * kRowsA * 4;     // scale words of a stage: weight r
 constexpr int kSbWords = kMaxTok + 4;        // token rows, from a multiple of four on
 constexpr int kSbBytes = 2 * kSbWords * 4;
 constexpr int kScaleBytes = (kSaBytes + kSbBytes + 127) / 128 * 128;
-constexpr int kCodeBytes = kABytes + kBBytes;
-constexpr int kStages = 6;                   // code stages
+// The code stages share this much memory: 6 stages when a tile of the call has more than
+// 96 token rows, 7 or 9 when every tile is small. A few tokens are bound by how many
+// weight bytes are in flight: with 6 stages a pair got 84 GB/s.
+constexpr int kCodeBytes = 6 * (kABytes + kBBytes);
+constexpr int kMaxStages = 9;
+static_assert(kCodeBytes / (kABytes + kBox0 * kKBytes) == kMaxStages, "barriers for every stage");
 constexpr int kWords = 8;                    // scale-word stages
 constexpr int kSlots = 4;
 constexpr int kSfA = 8, kSfB = 16;           // TMEM columns of a stage's scales
@@ -75,7 +79,7 @@ static_assert(kBBytes % 1024 == 0, "swizzle atoms start on 1024-byte boundaries"
 // A parity wait tells a phase from the one before it, not from the one before that: a
 // scale group has to take part in every use of its stages and slots.
 constexpr int kSfGroups = 4;
-static_assert(kWords % kSfGroups == 0 && kSlots % kSfGroups == 0, "groups own words and slots");
+static_assert(kWords % kSfGroups == 0 && kSlots == kSfGroups, "a group owns a slot and its words");
 constexpr int kTokWords = (kMaxTok + 31) / 32;   // scale columns of the token rows per 128 k
 constexpr int kFirstSf = 4, kFirstEpi = kFirstSf + 4 * kSfGroups;
 constexpr int kEpiWarps = 8;
@@ -84,9 +88,9 @@ constexpr int kChunk = 16;                   // token rows that four epilogue wa
 constexpr int kTurnBytes = kChunk * (kRowsA * 2 + 16);
 
 struct Smem {
-  uint64_t full[kStages];      // even CTA: the stage's four code boxes landed and both CTAs'
+  uint64_t full[kMaxStages];      // even CTA: the stage's four code boxes landed and both CTAs'
                                // scales are in TMEM
-  uint64_t empty[kStages];     // the MMAs of the stage completed (and of its scale slot)
+  uint64_t empty[kMaxStages];     // the MMAs of the stage completed (and of its scale slot)
   uint64_t words[kWords];      // this CTA's scale words landed
   uint64_t wempty[kWords];     // and were read
   uint64_t tfull[2];           // accumulator complete
@@ -95,11 +99,12 @@ struct Smem {
   uint32_t tmem_base;
   int32_t T;
   int32_t total_units;
+  int32_t stage_bytes, stages;
   int32_t begin[kMaxExperts + 1];    // [e + 1] is also where expert e ends
   int32_t prefix[kMaxExperts + 1];   // units before expert e
   uint8_t tok[kMaxExperts];          // token rows of its tiles
 };
-constexpr size_t kSmemBytes = 1024 + (size_t)kStages * kCodeBytes + (size_t)kWords * kScaleBytes + 4 * kTurnBytes + sizeof(Smem);
+constexpr size_t kSmemBytes = 1024 + (size_t)kCodeBytes + (size_t)kWords * kScaleBytes + 4 * kTurnBytes + sizeof(Smem);
 static_assert(kSmemBytes <= 232448, "shared memory per CTA exceeds 227 KB");
 
 struct Unit {
@@ -148,11 +153,9 @@ gmm_mxfp4_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant_
   extern __shared__ uint8_t smem_raw[];
   uint8_t* tiles = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                               ~uintptr_t(1023));
-  uint8_t* const scales = tiles + (size_t)kStages * kCodeBytes;
+  uint8_t* const scales = tiles + kCodeBytes;
   uint8_t* const turn = scales + (size_t)kWords * kScaleBytes;
   Smem& s = *reinterpret_cast<Smem*>(turn + 4 * kTurnBytes);
-  auto a_tile = [&](int i) -> uint8_t* { return tiles + i * kCodeBytes; };
-  auto b_tile = [&](int i) -> uint8_t* { return tiles + i * kCodeBytes + kABytes; };
   auto sa_tile = [&](int i) -> uint8_t* { return scales + i * kScaleBytes; };
   auto sb_tile = [&](int i) -> uint8_t* { return scales + i * kScaleBytes + kSaBytes; };
 
@@ -166,14 +169,15 @@ gmm_mxfp4_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant_
   if (warp == 0) {
     load_groups_warp0(gs, E, M, s.begin, s.begin + 1, &s.T, blockIdx.x == 0);
     __syncwarp();
-    int32_t carry = 0;
+    int32_t carry = 0, most = 16;
     for (int base = 0; base < E; base += 32) {
       const int e = base + lane;
       int32_t n = 0;
       if (e < E) {
-        const int rows = s.begin[e + 1] - s.begin[e];
+        const int rows = s.begin[e + 1] - s.begin[e], tok = tile_rows(rows);
         n = token_tiles(rows) * wt;
-        s.tok[e] = (uint8_t)tile_rows(rows);
+        s.tok[e] = (uint8_t)tok;
+        most = max(most, tok);
       }
       int32_t incl = n;
 #pragma unroll
@@ -184,7 +188,10 @@ gmm_mxfp4_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant_
       if (e < E) s.prefix[e] = carry + incl - n;
       carry += __shfl_sync(0xffffffffu, incl, 31);
     }
+    most = __reduce_max_sync(0xffffffffu, most);
     if (lane == 0) {
+      s.stage_bytes = kABytes + box_rows(most) * kKBytes;
+      s.stages = kCodeBytes / s.stage_bytes;
       s.prefix[E] = carry;
       s.total_units = carry;
       prefetch_tmap(&tmW);
@@ -196,7 +203,7 @@ gmm_mxfp4_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant_
     }
   } else if (warp == 1) {
     if (lane == 0) {
-      for (int i = 0; i < kStages; ++i) {
+      for (int i = 0; i < kMaxStages; ++i) {
         mbar_init(&s.full[i], 1 + 8);    // the producer's bytes + a group of scale warps per CTA
         mbar_init(&s.empty[i], 1);
       }
@@ -221,6 +228,9 @@ gmm_mxfp4_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant_
   tc_fence_after();
   const int total = s.total_units;
   const uint32_t tmem = s.tmem_base;
+  const int stages = s.stages, stage_bytes = s.stage_bytes;
+  auto a_tile = [&](int i) -> uint8_t* { return tiles + i * stage_bytes; };
+  auto b_tile = [&](int i) -> uint8_t* { return tiles + i * stage_bytes + kABytes; };
 
   if (warp == 0) {
     // ========================= TMA producer: codes ========================
@@ -253,15 +263,15 @@ gmm_mxfp4_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant_
         }
         __syncwarp();
         ++issued;
-        if (++st == kStages) { st = 0; ph ^= 1; }
+        if (++st == stages) { st = 0; ph ^= 1; }
       }
     }
     // drain: every copy landed before either CTA may exit
     if (lane == 0 && rank == 0) {
-      const int64_t n_last = issued < kStages ? issued : kStages;
+      const int64_t n_last = issued < stages ? issued : stages;
       for (int64_t i = 1; i <= n_last; ++i) {
         const int64_t idx = issued - i;
-        mbar_wait(&s.full[idx % kStages], (uint32_t)((idx / kStages) & 1), kWhereDrain);
+        mbar_wait(&s.full[idx % stages], (uint32_t)((idx / stages) & 1), kWhereDrain);
       }
     }
   } else if (warp == 1) {
@@ -294,7 +304,7 @@ gmm_mxfp4_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant_
           const uint64_t bd = make_desc(smem_u32(b_tile(st)), 16, 1024, kSwizzle128B);
           const uint32_t sf = tmem + (uint32_t)(kSfBase + sl * kSfCols);
           uint64_t* const done = &s.empty[st];
-          if (++st == kStages) { st = 0; ph ^= 1; }
+          if (++st == stages) { st = 0; ph ^= 1; }
           if (++sl == kSlots) sl = 0;
           ready = mbar_test(&s.full[st], ph);
 #pragma unroll
@@ -365,6 +375,9 @@ gmm_mxfp4_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant_
     const uint32_t last_mask = last_blocks == 4 ? 0xFFFFFFFFu : (1u << (8 * last_blocks)) - 1u;
     int e = 0;
     uint32_t i = 0;                                // global step index (word stages and slots)
+    // the code stage of this group's step and of its step before, which had the same slot
+    int cs = group, before = 0;
+    uint32_t cph = 0, before_ph = 0;
     bool ok = true;
     for (int u = cluster; u < total && ok; u += nclusters) {
       const Unit t = decode_unit(s, wt, u, e);
@@ -390,15 +403,12 @@ gmm_mxfp4_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant_
         }
         __syncwarp();
         if (lane == 0) mbar_arrive(&s.wempty[st]);     // words read
-        // The slot was last read by the products of step i - kSlots: their stage's
-        // barrier tells. The phase it may be mistaken for, step i - kSlots - 2 kStages's,
-        // is past: this group has waited for step i - 2 kSlots, in order, before.
-        if (i >= kSlots) {
-          const uint32_t j = i - kSlots;
-          if (!mbar_wait_warp(&s.empty[j % kStages], (j / kStages) & 1, kWhereDequant)) {
-            ok = false;
-            break;
-          }
+        // The slot was last read by the products of step i - kSlots, this group's step
+        // before: their stage's barrier tells when they are done. (The phase that it could
+        // be mistaken for, two uses of the stage earlier, was waited for in its turn.)
+        if (i >= kSlots && !mbar_wait_warp(&s.empty[before], before_ph, kWhereDequant)) {
+          ok = false;
+          break;
         }
         tc_fence_after();
         tmem_st8(tq + (uint32_t)(sl * kSfCols), wa);
@@ -406,7 +416,11 @@ gmm_mxfp4_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant_
         tmem_st_wait();
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive_cluster_relaxed(even_full + (uint32_t)((i % kStages) * sizeof(uint64_t)));
+        if (lane == 0) mbar_arrive_cluster_relaxed(even_full + (uint32_t)(cs * sizeof(uint64_t)));
+        before = cs;
+        before_ph = cph;
+        cs += kSfGroups;
+        if (cs >= stages) { cs -= stages; cph ^= 1; }
       }
     }
   } else {
