@@ -157,6 +157,9 @@ def _stream(device) -> int:
 
 
 def _req(t: torch.Tensor, dtype, name: str, ndim: int):
+    if isinstance(t, torch.Tensor) and t.is_cuda and t.dtype == dtype and t.dim() == ndim \
+            and t.is_contiguous():
+        return
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a tensor")
     if t.device.type != "cuda":
@@ -460,10 +463,15 @@ TYPES = {torch.bfloat16: 0, torch.float32: 1}
 GATES = {"token": 1, "channel": 2, "full": 3}
 
 
-def _rows_type(t: torch.Tensor, name: str) -> int:
-    if isinstance(t, torch.Tensor) and t.dtype not in TYPES:
+def _req_rows(t: torch.Tensor, name: str) -> int:
+    """Checks a contiguous [rows, H] CUDA tensor of a row type; the type's number."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a tensor")
+    ty = TYPES.get(t.dtype)
+    if ty is None:
         raise TypeError(f"{name} must be torch.bfloat16 or torch.float32, got {t.dtype}")
-    return TYPES[t.dtype] if isinstance(t, torch.Tensor) else 0
+    _req(t, t.dtype, name, 2)
+    return ty
 
 
 def _like(out, shape, dtype, device, name: str):
@@ -502,8 +510,7 @@ def dispatch_tokens(x, ids, num_experts: int, M: Optional[int] = None, out=None)
     (rows [M, H], group_sizes, slot_row, row_slot) (see fp8moe_dispatch_tokens).
     Rows past the last group's are not written."""
     L = load()
-    ty = _rows_type(x, "x")
-    _req(x, x.dtype if isinstance(x, torch.Tensor) else None, "x", 2)
+    ty = _req_rows(x, "x")
     _req(ids, torch.int32, "ids", 2)
     T, H = x.shape
     if ids.shape[0] != T:
@@ -522,8 +529,7 @@ def combine_tokens(rows, slot_row, weights=None, out=None):
     """out [T, H] = sum_j weights[t, j] * rows[slot_row[t, j]] in f32, weights f32
     [T, topk] or None for ones (see fp8moe_combine_tokens)."""
     L = load()
-    ty = _rows_type(rows, "rows")
-    _req(rows, rows.dtype if isinstance(rows, torch.Tensor) else None, "rows", 2)
+    ty = _req_rows(rows, "rows")
     _req(slot_row, torch.int32, "slot_row", 2)
     M, H = rows.shape
     T, k = slot_row.shape
@@ -547,8 +553,7 @@ def combine_tokens_bwd(dout, rows, slot_row, weights, out=None):
     """Gradient of combine_tokens: (drows [M, H], dweights f32 [T, topk]) (see
     fp8moe_combine_tokens_bwd). Rows of drows that no slot names are not written."""
     L = load()
-    ty = _rows_type(rows, "rows")
-    _req(rows, rows.dtype if isinstance(rows, torch.Tensor) else None, "rows", 2)
+    ty = _req_rows(rows, "rows")
     _req(dout, rows.dtype, "dout", 2)
     _req(slot_row, torch.int32, "slot_row", 2)
     _req(weights, torch.float32, "weights", 2)
@@ -599,8 +604,7 @@ def norm_fwd(x, y=None, w_post=None, w_pre=None, gate=None, gate_kind: Optional[
     "channel" (f32 [H]) or "full" ([T, H] of x's type); sigmoid passes the gate
     through one (see fp8moe_norm_fwd)."""
     L = load()
-    ty = _rows_type(x, "x")
-    _req(x, x.dtype if isinstance(x, torch.Tensor) else None, "x", 2)
+    ty = _req_rows(x, "x")
     T, H = x.shape
     post, pre = w_post is not None, w_pre is not None
     if (y is not None) != post:
@@ -636,9 +640,7 @@ def norm_bwd(dr, dh, r, y=None, w_post=None, w_pre=None, rstd_post=None, rstd_pr
     like = dr if dr is not None else dh
     if like is None:
         raise ValueError("dr or dh must be given")
-    ty = _rows_type(like, "dr" if dr is not None else "dh")
-    _req(like, like.dtype if isinstance(like, torch.Tensor) else None,
-         "dr" if dr is not None else "dh", 2)
+    ty = _req_rows(like, "dr" if dr is not None else "dh")
     T, H = like.shape
     dt, dev, f32 = like.dtype, like.device, torch.float32
     post, pre = w_post is not None, w_pre is not None
