@@ -13,6 +13,7 @@
 // rows, and no two threads ever write (or add to) the same element: no atomics,
 // the sums run in the order of j and the results do not depend on scheduling.
 #include <cstdint>
+#include <type_traits>
 #include <cooperative_groups.h>
 #include <cuda_runtime.h>
 #include <cuda_bf16.h>
@@ -286,36 +287,46 @@ dispatch_few_kernel(const uint4* __restrict__ x, const int32_t* __restrict__ ids
 }
 
 // --------------------------------------------------------------------- combine
-// A CTA sums one token's rows, a thread 16 bytes at a time with up to eight row loads
-// in flight; four CTAs of 256 threads on an SM keep 128 KB in flight, and the token's
-// row numbers are read once. (Warps that walked 512-byte pieces of all tokens waited
-// for row numbers and rows in turn: 69 us against ... for 4093 x 8 x 4096 bf16.) A slot
-// without a row adds nothing: its vector is not read, so what lies there (or a NaN
+// A CTA sums one token's rows (several tokens' when rows are short), a thread 16 bytes at
+// a time with up to eight row loads in flight; four CTAs of 256 threads on an SM keep
+// 128 KB in flight, and the token's row numbers are read once. (Warps that walked
+// 512-byte pieces of all tokens waited for row numbers and rows in turn: 72 us against
+// 45 for 4093 x 8 x 4096 bf16; 128 or 512 threads a CTA measured the same or slower.) A
+// slot without a row adds nothing: its vector is not read, so what lies there (or a NaN
 // weight) cannot reach the sum.
-constexpr int kSumBatch = 8;
 
-template <typename T, bool WEIGHTED>
+// BATCH row loads in flight (the rows of up to four or eight choices at once); SHORT: rows
+// of at most 128 vectors, per_token threads each, else a token has the whole CTA.
+template <typename T, bool WEIGHTED, int BATCH, bool SHORT>
 __global__ void __launch_bounds__(kMoveThreads, 4)
-combine_kernel(const uint4* __restrict__ rows, int topk, int nvec,
+combine_kernel(const uint4* __restrict__ rows, int64_t tokens, int topk, int nvec, int per_token,
                const int32_t* __restrict__ slot_row, int64_t M, const float* __restrict__ weights,
                uint4* __restrict__ out) {
   constexpr int P = Vec<T>::kP;
-  const int64_t t = blockIdx.x;
+  int64_t t = blockIdx.x;
+  int v = threadIdx.x, step = blockDim.x;
+  if (SHORT) {
+    const int group = threadIdx.x / per_token;
+    t = t * (kMoveThreads / per_token) + group;
+    v -= group * per_token;
+    step = per_token;
+    if (t >= tokens) return;
+  }
   const int32_t* const sr = slot_row + t * topk;
-  for (int v = threadIdx.x; v < nvec; v += blockDim.x) {
+  for (; v < nvec; v += step) {
     float2 acc[P];
 #pragma unroll
     for (int i = 0; i < P; ++i) acc[i] = both(0.0f);
-    for (int j0 = 0; j0 < topk; j0 += kSumBatch) {
-      uint4 x[kSumBatch];
-      int32_t row[kSumBatch];
+    for (int j0 = 0; j0 < topk; j0 += BATCH) {
+      uint4 x[BATCH];
+      int32_t row[BATCH];
 #pragma unroll
-      for (int j = 0; j < kSumBatch; ++j) {
+      for (int j = 0; j < BATCH; ++j) {
         row[j] = j0 + j < topk ? row_of(sr, j0 + j, M) : -1;
         if (row[j] >= 0) x[j] = __ldg(rows + (int64_t)row[j] * nvec + v);
       }
 #pragma unroll
-      for (int j = 0; j < kSumBatch; ++j) {
+      for (int j = 0; j < BATCH; ++j) {
         if (row[j] < 0) continue;
         float2 f[P];
         Vec<T>::unpack(x[j], f);
@@ -329,41 +340,45 @@ combine_kernel(const uint4* __restrict__ rows, int topk, int nvec,
 }
 
 // ---------------------------------------------------------- combine's gradient
-// A CTA takes a token: every thread walks its share of the token's vectors, reads
-// dout once and each row once (eight at a time), writes the row's gradient and
-// keeps the partial dot products; one block reduction per eight rows ends it.
+// A CTA takes a token (several when rows are short): every thread walks its share of the
+// token's vectors, reads
+// dout once and each row once (BATCH at a time), writes the row's gradient and
+// keeps the partial dot products; one reduction per BATCH rows ends it.
 constexpr int kBwdThreads = 256;
 
-template <typename T>
-__global__ void __launch_bounds__(kBwdThreads, 2)
-combine_bwd_kernel(const uint4* __restrict__ dout, const uint4* __restrict__ rows, int topk,
-                   int nvec, const int32_t* __restrict__ slot_row, int64_t M,
+template <typename T, int BATCH>
+__global__ void __launch_bounds__(kBwdThreads, BATCH == 8 ? 2 : 4)
+combine_bwd_kernel(const uint4* __restrict__ dout, const uint4* __restrict__ rows, int64_t tokens,
+                   int topk, int nvec, int per_token, const int32_t* __restrict__ slot_row, int64_t M,
                    const float* __restrict__ weights, uint4* __restrict__ drows,
                    float* __restrict__ dweights) {
   constexpr int P = Vec<T>::kP;
-  __shared__ float s_part[kBwdThreads / 32][kSumBatch];
-  const int64_t t = blockIdx.x;
+  __shared__ float s_part[kBwdThreads / 32][BATCH];
+  const int group = threadIdx.x / per_token, tid = threadIdx.x - group * per_token;
+  const int64_t t = (int64_t)blockIdx.x * (kBwdThreads / per_token) + group;
+  const bool live = t < tokens;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  for (int j0 = 0; j0 < topk; j0 += kSumBatch) {
-    int32_t row[kSumBatch];
-    float w[kSumBatch];
-    float2 dot[kSumBatch];
+  for (int j0 = 0; j0 < topk; j0 += BATCH) {
+    int32_t row[BATCH];
+    float w[BATCH];
+    float2 dot[BATCH];
 #pragma unroll
-    for (int j = 0; j < kSumBatch; ++j) {
-      row[j] = j0 + j < topk ? row_of(slot_row, t * topk + j0 + j, M) : -1;
-      w[j] = j0 + j < topk ? __ldg(weights + t * topk + j0 + j) : 0.0f;
+    for (int j = 0; j < BATCH; ++j) {
+      const bool have = live && j0 + j < topk;
+      row[j] = have ? row_of(slot_row, t * topk + j0 + j, M) : -1;
+      w[j] = have ? __ldg(weights + t * topk + j0 + j) : 0.0f;
       dot[j] = both(0.0f);
     }
-    for (int v = threadIdx.x; v < nvec; v += kBwdThreads) {
+    for (int v = live ? tid : nvec; v < nvec; v += per_token) {
       const uint4 dv = __ldg(dout + t * nvec + v);
-      uint4 y[kSumBatch];
+      uint4 y[BATCH];
 #pragma unroll
-      for (int j = 0; j < kSumBatch; ++j)
+      for (int j = 0; j < BATCH; ++j)
         if (row[j] >= 0) y[j] = __ldg(rows + (int64_t)row[j] * nvec + v);
       float2 d[P];
       Vec<T>::unpack(dv, d);
 #pragma unroll
-      for (int j = 0; j < kSumBatch; ++j) {
+      for (int j = 0; j < BATCH; ++j) {
         if (row[j] < 0) continue;
         float2 f[P], o[P];
         Vec<T>::unpack(y[j], f);
@@ -376,21 +391,27 @@ combine_bwd_kernel(const uint4* __restrict__ dout, const uint4* __restrict__ row
       }
     }
 #pragma unroll
-    for (int j = 0; j < kSumBatch; ++j) {
+    for (int j = 0; j < BATCH; ++j) {
       float sum = dot[j].x + dot[j].y;
 #pragma unroll
       for (int d = 16; d > 0; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
       if (lane == 0) s_part[warp][j] = sum;
     }
     __syncthreads();
-    if (threadIdx.x < kSumBatch && j0 + (int)threadIdx.x < topk) {
+    if (live && tid < BATCH && j0 + tid < topk) {
       float sum = 0.0f;
-#pragma unroll
-      for (int k = 0; k < kBwdThreads / 32; ++k) sum += s_part[k][threadIdx.x];
-      dweights[t * topk + j0 + threadIdx.x] = sum;   // 0 where the slot has no row
+      for (int k = 0; k < per_token / 32; ++k) sum += s_part[group * (per_token / 32) + k][tid];
+      dweights[t * topk + j0 + tid] = sum;   // 0 where the slot has no row
     }
     __syncthreads();
   }
+}
+
+// Threads of a 256-thread CTA that share a token: a power of two of warps.
+int threads_per_token(int nvec) {
+  int n = 32;
+  while (n < 256 && n < nvec) n *= 2;
+  return n;
 }
 
 int grid_for(int64_t items, int per_cta, int num_sms, int ctas_per_sm) {
@@ -464,18 +485,22 @@ cudaError_t fp8moe_launch_combine(const void* rows, int64_t T, int topk, int nve
                                   const int32_t* slot_row, int64_t M, const float* weights,
                                   void* out, cudaStream_t s) {
   using namespace fp8moe::route;
-  const int threads = nvec < kMoveThreads ? (nvec + 31) / 32 * 32 : kMoveThreads;
+  const bool is_short = nvec <= 128;
+  const int per_token = is_short ? threads_per_token(nvec) : kMoveThreads;
+  const int tokens = kMoveThreads / per_token;
   auto run = [&](auto kern) {
-    kern<<<(unsigned)T, threads, 0, s>>>(static_cast<const uint4*>(rows), topk, nvec, slot_row, M,
-                                         weights, static_cast<uint4*>(out));
+    kern<<<(unsigned)((T + tokens - 1) / tokens), kMoveThreads, 0, s>>>(
+        static_cast<const uint4*>(rows), T, topk, nvec, per_token, slot_row, M, weights,
+        static_cast<uint4*>(out));
   };
-  if (f32) {
-    if (weights) run(combine_kernel<float, true>);
-    else run(combine_kernel<float, false>);
-  } else {
-    if (weights) run(combine_kernel<__nv_bfloat16, true>);
-    else run(combine_kernel<__nv_bfloat16, false>);
-  }
+  auto pick = [&](auto type, auto weighted) {
+    using R = decltype(type);
+    constexpr bool W = decltype(weighted)::value;
+    if (topk <= 4) is_short ? run(combine_kernel<R, W, 4, true>) : run(combine_kernel<R, W, 4, false>);
+    else is_short ? run(combine_kernel<R, W, 8, true>) : run(combine_kernel<R, W, 8, false>);
+  };
+  if (f32) weights ? pick(float(), std::true_type()) : pick(float(), std::false_type());
+  else weights ? pick(__nv_bfloat16(), std::true_type()) : pick(__nv_bfloat16(), std::false_type());
   return cudaGetLastError();
 }
 
@@ -484,12 +509,13 @@ cudaError_t fp8moe_launch_combine_bwd(const void* dout, const void* rows, int64_
                                       const float* weights, void* drows, float* dweights,
                                       cudaStream_t s) {
   using namespace fp8moe::route;
+  const int per_token = threads_per_token(nvec), tokens = kBwdThreads / per_token;
   auto run = [&](auto kern) {
-    kern<<<(unsigned)T, kBwdThreads, 0, s>>>(static_cast<const uint4*>(dout),
-                                             static_cast<const uint4*>(rows), topk, nvec, slot_row,
-                                             M, weights, static_cast<uint4*>(drows), dweights);
+    kern<<<(unsigned)((T + tokens - 1) / tokens), kBwdThreads, 0, s>>>(
+        static_cast<const uint4*>(dout), static_cast<const uint4*>(rows), T, topk, nvec, per_token,
+        slot_row, M, weights, static_cast<uint4*>(drows), dweights);
   };
-  if (f32) run(combine_bwd_kernel<float>);
-  else run(combine_bwd_kernel<__nv_bfloat16>);
+  if (f32) topk <= 4 ? run(combine_bwd_kernel<float, 4>) : run(combine_bwd_kernel<float, 8>);
+  else topk <= 4 ? run(combine_bwd_kernel<__nv_bfloat16, 4>) : run(combine_bwd_kernel<__nv_bfloat16, 8>);
   return cudaGetLastError();
 }
