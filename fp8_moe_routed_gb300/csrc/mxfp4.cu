@@ -199,9 +199,9 @@ mx_dequantize_kernel(const uint32_t* __restrict__ codes, const uint8_t* __restri
   }
 }
 
-int grid_for(int64_t items, int num_sms) {
+int grid_for(int64_t items, int num_sms, int ctas_per_sm) {
   const int64_t want = (items + kRowsThreads / 32 - 1) / (kRowsThreads / 32);
-  const int64_t most = (int64_t)num_sms * 8;
+  const int64_t most = (int64_t)num_sms * ctas_per_sm;
   return (int)(want < most ? want : most);
 }
 
@@ -216,7 +216,8 @@ cudaError_t fp8moe_launch_mxfp4_quantize_rows(const void* x, int64_t M, int K, c
                                               cudaStream_t s) {
   using namespace fp8moe::mx;
   const int chunks = (K / 8 + 32 * kRowsUnroll - 1) / (32 * kRowsUnroll);
-  mx_quantize_rows_kernel<<<grid_for(M * chunks, num_sms), kRowsThreads, 0, s>>>(
+  // the resident CTAs (45 registers a thread): every one reads the group sizes once
+  mx_quantize_rows_kernel<<<grid_for(M * chunks, num_sms, 5), kRowsThreads, 0, s>>>(
       static_cast<const uint4*>(x), M, K, gs, E, reinterpret_cast<uint32_t*>(codes),
       reinterpret_cast<uint32_t*>(scales), scale_stride, report);
   return cudaGetLastError();
@@ -239,7 +240,8 @@ cudaError_t fp8moe_launch_mxfp4_dequantize(const uint8_t* codes, const uint8_t* 
   using namespace fp8moe::mx;
   const int64_t rows = (int64_t)E * N;
   const int chunks = (K / 8 + 32 * kDqUnroll - 1) / (32 * kDqUnroll);
-  mx_dequantize_kernel<<<grid_for(rows * chunks, num_sms), kRowsThreads, 0, s>>>(
+  // many short CTAs: an even end (7168 x 4096 x 8: 90 us against 106 with 8 per SM)
+  mx_dequantize_kernel<<<grid_for(rows * chunks, num_sms, 64), kRowsThreads, 0, s>>>(
       reinterpret_cast<const uint32_t*>(codes), scales, rows, N, K, static_cast<uint4*>(out));
   return cudaGetLastError();
 }

@@ -41,20 +41,20 @@ __device__ __forceinline__ int warp_incl_scan(int v, int lane) {
 // ------------------------------------------------------------------------ sort
 // One cluster of kSortCtas CTAs (one CTA when there are few slots). The slots are
 // cut into one contiguous run per warp. First pass: every warp counts its run per
-// expert in its own shared-memory counters, 32 slots at a time (match_any gives
-// the lanes that share an expert, their lowest lane adds their number). Then each
+// expert in its own shared-memory counters, 32 slots at a time (votes on the keys' bits
+// give the lanes that share an expert, their lowest lane adds their number). Then each
 // counter becomes the first row of that (warp, expert): an exclusive scan over the
 // warps of a CTA, over the CTAs (their totals read through distributed shared
 // memory) and over the experts. Second pass: a slot's row is its warp's counter
-// plus the number of lower lanes with the same expert. Bound by the two passes'
-// issue rate on eight SMs; the dispatch that follows moves H / 2 times the bytes.
+// plus the number of lower lanes with the same expert. Bound by latency and by the
+// passes' issue rate on eight SMs; the dispatch that follows moves H / 2 times the bytes.
 constexpr int kSortCtas = 8;
 constexpr int kSortThreads = 1024;
 constexpr int kSortWarps = kSortThreads / 32;
 constexpr int kSortHeld = 8;      // batches of a warp kept in registers between the passes
 
 __global__ void __launch_bounds__(kSortThreads, 1)
-sort_kernel(const int32_t* __restrict__ ids, int64_t n, int E, int64_t M,
+sort_kernel(const int32_t* __restrict__ ids, uint32_t n, int E, int32_t M,
             int32_t* __restrict__ group_sizes, int32_t* __restrict__ slot_row,
             int32_t* __restrict__ row_slot) {
   extern __shared__ int32_t sm[];
@@ -71,30 +71,45 @@ sort_kernel(const int32_t* __restrict__ ids, int64_t n, int E, int64_t M,
   for (int i = threadIdx.x; i < kSortWarps * E; i += kSortThreads) counts[i] = 0;
   __syncthreads();
 
-  const int64_t batches = (n + 31) / 32;
-  const int64_t per = (batches + ctas * kSortWarps - 1) / (ctas * kSortWarps);
-  const int64_t b0 = (int64_t)(rank * kSortWarps + warp) * per;
-  const int64_t b1 = b0 + per < batches ? b0 + per : batches;
+  // (n < 2^31: slots and batches past the end stay below 2^32)
+  const uint32_t batches = (n + 31) / 32;
+  const uint32_t per = (batches + ctas * kSortWarps - 1) / (ctas * kSortWarps);
+  const uint32_t b0 = (rank * kSortWarps + warp) * per;
+  const uint32_t b1 = min(b0 + per, batches);
   int32_t* const mine = counts + (size_t)warp * E;
+  const int bits = 32 - __clz(E - 1);        // of a key; 0 for one expert
   bool bad = false;
-  auto fetch = [&](int64_t b) -> int32_t {
-    const int64_t s = b * 32 + lane;
+  auto fetch = [&](uint32_t b) -> int32_t {
+    const uint32_t s = b * 32 + lane;
     const int32_t e = b < b1 && s < n ? __ldg(ids + s) : -1;
     bad |= e >= E;
     return e >= 0 && e < E ? e : -1;
   };
-  auto count = [&](int32_t key) {
-    const uint32_t same = __match_any_sync(0xffffffffu, key);
-    if (key >= 0 && lane == __ffs(same) - 1) mine[key] += __popc(same);
+  // key, the lower lanes with the same one and, for the lowest of them, their number: a
+  // vote per bit of the key (match_any takes a step per different key, 45 cycles a batch
+  // on an SM, and twice as long in all)
+  auto ranked = [&](int32_t key) -> int32_t {
+    uint32_t same = __ballot_sync(0xffffffffu, key >= 0);
+    for (int i = 0; i < bits; ++i) {
+      const bool one = (key >> i) & 1;
+      const uint32_t ones = __ballot_sync(0xffffffffu, one);
+      same &= one ? ones : ~ones;
+    }
+    if (key < 0) return -1;
+    const int below = __popc(same & ((1u << lane) - 1u));
+    return key | below << 10 | (below ? 0 : __popc(same)) << 15;
+  };
+  auto advance = [&](int32_t packed) {
+    if (packed >= 0 && packed >> 15) mine[packed & 1023] += packed >> 15;
     __syncwarp();
   };
-  int32_t held[kSortHeld];       // the first batches' keys, all loads in flight at once
+  int32_t held[kSortHeld];       // of the first batches, all loads in flight at once
 #pragma unroll
   for (int i = 0; i < kSortHeld; ++i) held[i] = fetch(b0 + i);
 #pragma unroll
   for (int i = 0; i < kSortHeld; ++i)
-    if (b0 + i < b1) count(held[i]);
-  for (int64_t b = b0 + kSortHeld; b < b1; ++b) count(fetch(b));
+    if (b0 + i < b1) advance(held[i] = ranked(held[i]));
+  for (uint32_t b = b0 + kSortHeld; b < b1; ++b) advance(ranked(fetch(b)));
   __syncthreads();
   // thread e: exclusive scan of expert e over this CTA's warps
   for (int e = threadIdx.x; e < E; e += kSortThreads) {
@@ -139,14 +154,15 @@ sort_kernel(const int32_t* __restrict__ ids, int64_t n, int E, int64_t M,
     }
   }
   __syncthreads();
-  auto place = [&](int64_t b, int32_t key) {
-    const int64_t s = b * 32 + lane;
-    const uint32_t same = __match_any_sync(0xffffffffu, key);
+  auto place = [&](uint32_t b, int32_t packed) {
+    const uint32_t s = b * 32 + lane;
     int32_t row = -1;
-    if (key >= 0) row = s_base[key] + mine[key] + __popc(same & ((1u << lane) - 1u));
+    if (packed >= 0) {
+      const int key = packed & 1023;
+      row = s_base[key] + mine[key] + (packed >> 10 & 31);
+    }
     __syncwarp();
-    if (key >= 0 && lane == __ffs(same) - 1) mine[key] += __popc(same);
-    __syncwarp();
+    advance(packed);
     if (row >= M) row = -1;
     if (s < n) {
       slot_row[s] = row;
@@ -156,7 +172,7 @@ sort_kernel(const int32_t* __restrict__ ids, int64_t n, int E, int64_t M,
 #pragma unroll
   for (int i = 0; i < kSortHeld; ++i)
     if (b0 + i < b1) place(b0 + i, held[i]);
-  for (int64_t b = b0 + kSortHeld; b < b1; ++b) place(b, fetch(b));
+  for (uint32_t b = b0 + kSortHeld; b < b1; ++b) place(b, ranked(fetch(b)));
   if (row_slot) {
     for (int64_t r = s_rows + (int64_t)rank * kSortThreads + threadIdx.x; r < M;
          r += (int64_t)ctas * kSortThreads)
@@ -434,8 +450,9 @@ cudaError_t fp8moe_launch_sort_tokens(const int32_t* ids, int64_t n, int E, int6
                                          (int)smem);
   if (err != cudaSuccess) return err;
   cudaLaunchConfig_t cfg = {};
-  // below 8192 slots one CTA has at most eight 32-slot batches per warp
-  const unsigned ctas = n <= 8192 ? 1 : kSortCtas;
+  // up to 2048 slots one CTA has at most two 32-slot batches per warp (8192 slots: 11.5 us
+  // on one CTA, 32768 slots 8.2 us on eight)
+  const unsigned ctas = n <= 2048 ? 1 : kSortCtas;
   cfg.gridDim = dim3(ctas, 1, 1);
   cfg.blockDim = dim3(kSortThreads, 1, 1);
   cfg.dynamicSmemBytes = smem;
@@ -447,7 +464,8 @@ cudaError_t fp8moe_launch_sort_tokens(const int32_t* ids, int64_t n, int E, int6
   attr[0].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  err = cudaLaunchKernelEx(&cfg, sort_kernel, ids, n, E, M, group_sizes, slot_row, row_slot);
+  err = cudaLaunchKernelEx(&cfg, sort_kernel, ids, (uint32_t)n, E, (int32_t)M, group_sizes, slot_row,
+                           row_slot);
   if (err != cudaSuccess) return err;
   return cudaGetLastError();
 }

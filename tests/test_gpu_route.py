@@ -23,7 +23,8 @@ def draw_ids(T, k, E, seed, drop=0.0, skew=0.0):
 # T, topk, E, rows of the buffer past (or short of) the kept slots, share dropped
 SORTS = [
     (1, 1, 1, 0, 0.0), (1, 8, 32, 0, 0.0), (3, 5, 7, 9, 0.3), (33, 2, 1024, 0, 0.0),
-    (127, 32, 61, 100, 0.1), (1024, 8, 32, 0, 0.0),            # the last size of one CTA
+    (127, 32, 61, 100, 0.1), (1024, 8, 32, 0, 0.0),
+    (256, 8, 32, 0, 0.0), (257, 8, 32, 7, 0.1),                # the last size of one CTA, and more
     (1025, 8, 32, 0, 0.5), (4096, 8, 256, 1000, 0.0), (9001, 7, 1024, 0, 0.02),
     (2000, 8, 16, -3000, 0.0), (64, 4, 8, -255, 0.0), (5, 3, 4, 0, 1.0),
 ]
