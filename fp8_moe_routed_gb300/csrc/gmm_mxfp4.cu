@@ -98,10 +98,10 @@ struct Smem {
   uint64_t drain;
   uint32_t tmem_base;
   int32_t T;
-  int32_t total_units;
+  int32_t tiles;               // token tiles of all experts
   int32_t stage_bytes, stages;
   int32_t begin[kMaxExperts + 1];    // [e + 1] is also where expert e ends
-  int32_t prefix[kMaxExperts + 1];   // units before expert e
+  int32_t prefix[kMaxExperts + 1];   // token tiles before expert e
   uint8_t tok[kMaxExperts];          // token rows of its tiles
 };
 constexpr size_t kSmemBytes = 1024 + (size_t)kCodeBytes + (size_t)kWords * kScaleBytes + 4 * kTurnBytes + sizeof(Smem);
@@ -121,22 +121,32 @@ __device__ __forceinline__ int tile_rows(int rows) {
 }
 
 // Units: expert by expert, token tiles, weight tiles fastest (their shared token tile
-// stays in L2). `e`: the expert of an earlier unit of the caller, 0 at first.
-__device__ __forceinline__ int expert_of(const Smem& s, int u, int e) {
-  while (u >= s.prefix[e + 1]) ++e;
-  return e;
-}
-__device__ __forceinline__ Unit decode_unit(const Smem& s, int wt, int u, int e) {
-  Unit r;
-  r.e = expert_of(s, u, e);
-  const int local = u - s.prefix[r.e];
-  const int mi = local / wt;
-  r.w0 = local - mi * wt;
-  r.tok = s.tok[r.e];
-  r.m0 = s.begin[r.e] + mi * r.tok;
-  r.rows = min(r.tok, s.begin[r.e + 1] - r.m0);
-  return r;
-}
+// stays in L2). A pair walks units cluster, cluster + nclusters, ...: `tile` counts token
+// tiles over all experts, w0 the weight tile; steps and wraps, no division per unit.
+struct Walk {
+  int tile, w0, e, step_t, step_w, wt;
+  __device__ __forceinline__ Walk(int first, int step, int weight_tiles)
+      : tile(first / weight_tiles), w0(first % weight_tiles), e(0), step_t(step / weight_tiles),
+        step_w(step % weight_tiles), wt(weight_tiles) {}
+  __device__ __forceinline__ void next() {
+    tile += step_t;
+    w0 += step_w;
+    if (w0 >= wt) { w0 -= wt; ++tile; }
+  }
+  __device__ __forceinline__ int expert(const Smem& s) {
+    while (tile >= s.prefix[e + 1]) ++e;
+    return e;
+  }
+  __device__ __forceinline__ Unit unit(const Smem& s) {
+    Unit r;
+    r.e = expert(s);
+    r.w0 = w0;
+    r.tok = s.tok[r.e];
+    r.m0 = s.begin[r.e] + (tile - s.prefix[r.e]) * r.tok;
+    r.rows = min(r.tok, s.begin[r.e + 1] - r.m0);
+    return r;
+  }
+};
 
 // The smallest box that holds half of a tile.
 __device__ __forceinline__ int box_rows(int tok) {
@@ -151,9 +161,9 @@ gmm_mxfp4_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant_
                  const int32_t* __restrict__ gs, __nv_bfloat16* __restrict__ out, int64_t M, int K,
                  int N, int E) {
   extern __shared__ uint8_t smem_raw[];
-  uint8_t* tiles = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+  uint8_t* const ring = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                               ~uintptr_t(1023));
-  uint8_t* const scales = tiles + kCodeBytes;
+  uint8_t* const scales = ring + kCodeBytes;
   uint8_t* const turn = scales + (size_t)kWords * kScaleBytes;
   Smem& s = *reinterpret_cast<Smem*>(turn + 4 * kTurnBytes);
   auto sa_tile = [&](int i) -> uint8_t* { return scales + i * kScaleBytes; };
@@ -175,7 +185,7 @@ gmm_mxfp4_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant_
       int32_t n = 0;
       if (e < E) {
         const int rows = s.begin[e + 1] - s.begin[e], tok = tile_rows(rows);
-        n = token_tiles(rows) * wt;
+        n = token_tiles(rows);
         s.tok[e] = (uint8_t)tok;
         most = max(most, tok);
       }
@@ -193,7 +203,7 @@ gmm_mxfp4_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant_
       s.stage_bytes = kABytes + box_rows(most) * kKBytes;
       s.stages = kCodeBytes / s.stage_bytes;
       s.prefix[E] = carry;
-      s.total_units = carry;
+      s.tiles = carry;
       prefetch_tmap(&tmW);
       prefetch_tmap(&tmX0);
       prefetch_tmap(&tmX1);
@@ -226,24 +236,23 @@ gmm_mxfp4_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant_
   __syncthreads();
   cluster_sync();      // the peer's barriers exist before anyone signals them
   tc_fence_after();
-  const int total = s.total_units;
+  const int tiles = s.tiles;
   const uint32_t tmem = s.tmem_base;
   const int stages = s.stages, stage_bytes = s.stage_bytes;
-  auto a_tile = [&](int i) -> uint8_t* { return tiles + i * stage_bytes; };
-  auto b_tile = [&](int i) -> uint8_t* { return tiles + i * stage_bytes + kABytes; };
+  auto a_tile = [&](int i) -> uint8_t* { return ring + i * stage_bytes; };
+  auto b_tile = [&](int i) -> uint8_t* { return ring + i * stage_bytes + kABytes; };
 
   if (warp == 0) {
     // ========================= TMA producer: codes ========================
     pdl_wait();        // the activations' codes and scales are the quantiser's
     // Like the MMA warp: the whole warp walks the steps, one thread issues.
     const bool leader = elect_one();
-    int st = 0, e = 0;
+    int st = 0;
     uint32_t ph = 0;
     int64_t issued = 0;
     bool ok = true;
-    for (int u = cluster; u < total && ok; u += nclusters) {
-      const Unit t = decode_unit(s, wt, u, e);
-      e = t.e;
+    for (Walk at(cluster, nclusters, wt); at.tile < tiles && ok; at.next()) {
+      const Unit t = at.unit(s);
       const int box = box_rows(t.tok);
       const CUtensorMap* tmX = box == kBox0 ? &tmX0 : box == kBox1 ? &tmX1 : &tmX2;
       const uint32_t bytes = 2u * (uint32_t)(kABytes + box * kKBytes);
@@ -280,18 +289,14 @@ gmm_mxfp4_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant_
     // number) tells the compiler that a single thread runs it, so that descriptors and
     // addresses go to uniform registers without a loop over the warp's values.
     if (rank == 0 && elect_one()) {
-      int st = 0, sl = 0, ab = 0, e = 0;
+      int st = 0, sl = 0, ab = 0;
       uint32_t ph = 0, tph = 0;
       bool ok = true, ready = false;
-      if (cluster < total) e = expert_of(s, cluster, 0);
-      uint32_t tok = s.tok[e];
-      for (int u = cluster; u < total && ok; u += nclusters) {
+      Walk at(cluster, nclusters, wt);
+      uint32_t tok = at.tile < tiles ? s.tok[at.expert(s)] : 16u;
+      while (at.tile < tiles && ok) {
         const uint32_t idesc0 = make_idesc_mxf4(kUnitN, tok, 0);
         const uint32_t idesc2 = make_idesc_mxf4(kUnitN, tok, 2);
-        if (u + nclusters < total) {       // the next unit's, while this one runs
-          e = expert_of(s, u + nclusters, e);
-          tok = s.tok[e];
-        }
         const uint32_t d = tmem + (uint32_t)(ab * kDCols);
         if (!mbar_wait(&s.tempty[ab], tph ^ 1, kWhereMma)) { ok = false; break; }
         tc_fence_after();
@@ -317,6 +322,10 @@ gmm_mxfp4_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant_
                             (kb | kk) != 0);
           }
           mma_commit_pair(done);
+          if (kb == 0) {                     // the next unit's tile size, while this one runs
+            at.next();
+            if (at.tile < tiles) tok = s.tok[at.expert(s)];
+          }
         }
         if (!ok) break;
         mma_commit_pair(&s.tfull[ab]);
@@ -331,13 +340,12 @@ gmm_mxfp4_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant_
     // ===================== TMA producer: scale words ======================
     pdl_wait();
     const bool leader = elect_one();
-    int st = 0, e = 0;
+    int st = 0;
     uint32_t ph = 0;
     int64_t issued = 0;
     bool ok = true;
-    for (int u = cluster; u < total && ok; u += nclusters) {
-      const Unit t = decode_unit(s, wt, u, e);
-      e = t.e;
+    for (Walk at(cluster, nclusters, wt); at.tile < tiles && ok; at.next()) {
+      const Unit t = at.unit(s);
       for (int kb = 0; kb < nkb; ++kb) {
         if (!mbar_wait_warp(&s.wempty[st], ph ^ 1, kWhereProducer)) { ok = false; break; }
         if (leader) {
@@ -373,15 +381,13 @@ gmm_mxfp4_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant_
     const int words = (K + kMxWord - 1) / kMxWord;
     const int last_blocks = (K - (words - 1) * kMxWord) / kMxBlock;     // of the last word: 1..4
     const uint32_t last_mask = last_blocks == 4 ? 0xFFFFFFFFu : (1u << (8 * last_blocks)) - 1u;
-    int e = 0;
     uint32_t i = 0;                                // global step index (word stages and slots)
     // the code stage of this group's step and of its step before, which had the same slot
     int cs = group, before = 0;
     uint32_t cph = 0, before_ph = 0;
     bool ok = true;
-    for (int u = cluster; u < total && ok; u += nclusters) {
-      const Unit t = decode_unit(s, wt, u, e);
-      e = t.e;
+    for (Walk at(cluster, nclusters, wt); at.tile < tiles && ok; at.next()) {
+      const Unit t = at.unit(s);
       const int shift = t.m0 & 3;
       for (int kb = 0; kb < nkb; ++kb, ++i) {
         if ((int)(i % kSfGroups) != group) continue;
@@ -441,12 +447,11 @@ gmm_mxfp4_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant_
     const uint32_t st_row = (uint32_t)((lane >> 4) * 8 + (lane & 7));
     const uint32_t st_col = (uint32_t)(((lane >> 3) & 1) * 16);
     const int width = SWIGLU ? F : N;
-    int ab = 0, buf = 0, e = 0;
+    int ab = 0, buf = 0;
     uint32_t tph = 0;
     uint16_t* const o16 = reinterpret_cast<uint16_t*>(out);
-    for (int u = cluster; u < total; u += nclusters) {
-      const Unit t = decode_unit(s, wt, u, e);
-      e = t.e;
+    for (Walk at(cluster, nclusters, wt); at.tile < tiles; at.next()) {
+      const Unit t = at.unit(s);
       // the four warps leave together: a named barrier's wait has no limit
       if (!named_bar_all(1 + half, 128, mbar_wait_warp(&s.tfull[ab], tph, kWhereEpilogue)))
         break;
