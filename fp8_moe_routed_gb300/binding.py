@@ -143,7 +143,7 @@ def _check(rc: int, what: str):
 
 
 def _ptr(t: Optional[torch.Tensor]):
-    return None if t is None else t.data_ptr()
+    return t.data_ptr() if t is not None else None
 
 
 # the stream's handle without a Stream object around it, where torch offers that
@@ -182,6 +182,8 @@ def _workspace(op, M, K, N, E, device, workspace):
         if need == 0:
             return None, 0
         workspace = torch.empty(need, dtype=torch.uint8, device=device)
+    elif not workspace.is_cuda or not workspace.is_contiguous():
+        raise ValueError("workspace must be a contiguous CUDA tensor")
     return workspace, workspace.numel() * workspace.element_size()
 
 
@@ -474,13 +476,20 @@ def _req_rows(t: torch.Tensor, name: str) -> int:
     return ty
 
 
+def _shaped(t, dtype, name: str, shape: tuple):
+    """_req with the whole shape."""
+    if isinstance(t, torch.Tensor) and t.is_cuda and t.dtype == dtype and t.shape == shape \
+            and t.is_contiguous():
+        return
+    _req(t, dtype, name, len(shape))
+    raise ValueError(f"{name} must have shape {shape}, got {tuple(t.shape)}")
+
+
 def _like(out, shape, dtype, device, name: str):
     """A given output, checked, or a new one."""
     if out is None:
         return torch.empty(shape, dtype=dtype, device=device)
-    _req(out, dtype, name, len(shape))
-    if tuple(out.shape) != tuple(shape):
-        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(out.shape)}")
+    _shaped(out, dtype, name, shape)
     return out
 
 
@@ -534,9 +543,7 @@ def combine_tokens(rows, slot_row, weights=None, out=None):
     M, H = rows.shape
     T, k = slot_row.shape
     if weights is not None:
-        _req(weights, torch.float32, "weights", 2)
-        if weights.shape != slot_row.shape:
-            raise ValueError("shape mismatch")
+        _shaped(weights, torch.float32, "weights", (T, k))
     out = _like(out, (T, H), rows.dtype, rows.device, "out")
     _check(L.fp8moe_combine_tokens(_ptr(rows), M, H, ty, _ptr(slot_row), _ptr(weights), T, k,
                                    _ptr(out), _stream(rows.device)), "fp8moe_combine_tokens")
@@ -554,13 +561,11 @@ def combine_tokens_bwd(dout, rows, slot_row, weights, out=None):
     fp8moe_combine_tokens_bwd). Rows of drows that no slot names are not written."""
     L = load()
     ty = _req_rows(rows, "rows")
-    _req(dout, rows.dtype, "dout", 2)
     _req(slot_row, torch.int32, "slot_row", 2)
-    _req(weights, torch.float32, "weights", 2)
     M, H = rows.shape
     T, k = slot_row.shape
-    if dout.shape != (T, H) or weights.shape != slot_row.shape:
-        raise ValueError("shape mismatch")
+    _shaped(dout, rows.dtype, "dout", (T, H))
+    _shaped(weights, torch.float32, "weights", (T, k))
     out = _like(out, (M, H), rows.dtype, rows.device, "out")
     dweights = torch.empty(T, k, dtype=torch.float32, device=rows.device)
     _check(L.fp8moe_combine_tokens_bwd(_ptr(dout), _ptr(rows), M, H, ty, _ptr(slot_row),
@@ -579,17 +584,8 @@ def _gate(gate, kind: Optional[str], T: int, H: int, dtype):
         raise ValueError(f"gate_kind must be one of {sorted(GATES)}, got {kind!r}")
     shape = (T,) if kind == "token" else (H,) if kind == "channel" else (T, H)
     ty = dtype if kind == "full" else torch.float32
-    _req(gate, ty, "gate", len(shape))
-    if tuple(gate.shape) != shape:
-        raise ValueError(f"a gate per {kind} must have shape {shape}, got {tuple(gate.shape)}")
+    _shaped(gate, ty, f"a gate per {kind}", shape)
     return GATES[kind], shape, ty
-
-
-def _norm_weight(w, H: int, name: str):
-    if w is not None:
-        _req(w, torch.float32, name, 1)
-        if w.shape[0] != H:
-            raise ValueError(f"{name} must have shape ({H},), got {tuple(w.shape)}")
 
 
 def norm_fwd(x, y=None, w_post=None, w_pre=None, gate=None, gate_kind: Optional[str] = None,
@@ -611,21 +607,21 @@ def norm_fwd(x, y=None, w_post=None, w_pre=None, gate=None, gate_kind: Optional[
         raise ValueError("y and w_post go together")
     if not post and gate is not None:
         raise ValueError("a gate needs y and w_post")
+    f32, dev = torch.float32, x.device
+    kind = _gate(gate, gate_kind, T, H, x.dtype)[0] if gate is not None or gate_kind is not None else 0
+    r = h = rstd_post = rstd_pre = None
     if post:
-        _req(y, x.dtype, "y", 2)
-        if y.shape != x.shape:
-            raise ValueError("shape mismatch")
-    _norm_weight(w_post, H, "w_post")
-    _norm_weight(w_pre, H, "w_pre")
-    kind, _, _ = _gate(gate, gate_kind, T, H, x.dtype)
-    f32 = torch.float32
-    r = torch.empty_like(x) if post else None
-    h = torch.empty_like(x) if pre else None
-    rstd_post = torch.empty(T, dtype=f32, device=x.device) if post else None
-    rstd_pre = torch.empty(T, dtype=f32, device=x.device) if pre else None
+        _shaped(y, x.dtype, "y", (T, H))
+        _shaped(w_post, f32, "w_post", (H,))
+        r = torch.empty_like(x)
+        rstd_post = torch.empty(T, dtype=f32, device=dev)
+    if pre:
+        _shaped(w_pre, f32, "w_pre", (H,))
+        h = torch.empty_like(x)
+        rstd_pre = torch.empty(T, dtype=f32, device=dev)
     _check(L.fp8moe_norm_fwd(_ptr(x), _ptr(y), T, H, ty, _ptr(w_post), _ptr(w_pre), _ptr(gate),
                              kind, int(bool(sigmoid)), residual_scale, branch_scale, eps, _ptr(r),
-                             _ptr(h), _ptr(rstd_post), _ptr(rstd_pre), _stream(x.device)),
+                             _ptr(h), _ptr(rstd_post), _ptr(rstd_pre), _stream(dev)),
            "fp8moe_norm_fwd")
     return r, h, rstd_post, rstd_pre
 
@@ -650,18 +646,17 @@ def norm_bwd(dr, dh, r, y=None, w_post=None, w_pre=None, rstd_post=None, rstd_pr
         raise ValueError("dh, w_pre, rstd_pre and r go together")
     if not post and gate is not None:
         raise ValueError("a gate needs y and w_post")
-    for t, name in ((dr, "dr"), (dh, "dh"), (r if pre else None, "r"), (y, "y")):
-        if t is not None:
-            _req(t, dt, name, 2)
-            if t.shape != (T, H):
-                raise ValueError(f"{name} must have shape {(T, H)}, got {tuple(t.shape)}")
-    for t, name in ((rstd_post, "rstd_post"), (rstd_pre, "rstd_pre")):
-        if t is not None:
-            _req(t, f32, name, 1)
-            if t.shape[0] != T:
-                raise ValueError(f"{name} must have shape ({T},), got {tuple(t.shape)}")
-    _norm_weight(w_post, H, "w_post")
-    _norm_weight(w_pre, H, "w_pre")
+    rows = (T, H)
+    if dh is not None and like is not dh:
+        _shaped(dh, dt, "dh", rows)
+    if pre:
+        _shaped(r, dt, "r", rows)
+        _shaped(w_pre, f32, "w_pre", (H,))
+        _shaped(rstd_pre, f32, "rstd_pre", (T,))
+    if post:
+        _shaped(y, dt, "y", rows)
+        _shaped(w_post, f32, "w_post", (H,))
+        _shaped(rstd_post, f32, "rstd_post", (T,))
     kind, gshape, gtype = _gate(gate, gate_kind, T, H, dt)
     dx = torch.empty(T, H, dtype=dt, device=dev)
     dy = torch.empty(T, H, dtype=dt, device=dev) if post else None
@@ -713,11 +708,9 @@ def mxfp4_quantize_weights(w):
 
 def _mxfp4_weight(codes, scales):
     _req(codes, torch.uint8, "codes", 3)
-    _req(scales, torch.uint8, "scales", 4)
     E, N, half = codes.shape
     K = 2 * half
-    if tuple(scales.shape) != (E, mxfp4_words(K), N, 4):
-        raise ValueError("shape mismatch")
+    _shaped(scales, torch.uint8, "scales", (E, mxfp4_words(K), N, 4))
     return E, K, N
 
 

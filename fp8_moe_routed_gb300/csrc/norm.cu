@@ -16,12 +16,15 @@
 // and every row needs one reduction (three sums), not two in a row.
 //
 // Bound by HBM: 4 (forward) or 6 (backward) row vectors per row, each moved once. A
-// persistent CTA per SM streams rows through a ring of shared-memory stages filled
-// by bulk copies, which keeps two stages (57 KB each at H = 7168) in flight without
-// holding registers; rows are contiguous, so one copy per tensor fills a stage. All
-// sums and the column sums of the weight gradients are f32; the latter stay in
-// registers over all rows of a CTA and are joined by a second small kernel in a
-// fixed order, so results do not change from run to run.
+// persistent CTA per SM streams rows through rings of shared-memory stages filled by
+// bulk copies (one per tensor and row), which keeps 100 to 150 KB on their way without
+// holding registers. A row belongs to a team of warps; short rows get several teams,
+// each with a ring of its own and at its own pace. All sums and the column sums of the
+// weight gradients are f32; the latter stay in registers over all rows of a CTA and are
+// joined by a second small kernel in a fixed order, so results do not change from run
+// to run. 4096 x 7168 bf16: forward 41 us (5.7 TB/s), backward 66 us (5.3 TB/s) and the
+// join 4 us; what is left is the latency of a row's chain (copy, reduction, stores),
+// which 14 to 16 warps do not hide completely.
 #include <cstdint>
 #include <cuda_runtime.h>
 #include <cuda_bf16.h>

@@ -342,7 +342,8 @@ int fp8moe_combine_tokens(const void* rows, int64_t M, int64_t H, int32_t type,
 /* Gradient of fp8moe_combine_tokens:
  *   drows[slot_row[t, j]] = weights[t, j] * dout[t]
  *   dweights[t, j]        = sum_h dout[t, h] * rows[slot_row[t, j], h]   (f32; 0 without a row)
- * Rows that no slot names are not written. */
+ * A row belongs to one slot at most (as fp8moe_sort_tokens makes it); rows that no slot
+ * names are not written. */
 int fp8moe_combine_tokens_bwd(const void* dout, const void* rows, int64_t M, int64_t H,
                               int32_t type, const int32_t* slot_row, const float* weights,
                               int64_t T, int32_t topk, void* drows, float* dweights,
