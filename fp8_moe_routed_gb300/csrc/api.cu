@@ -856,6 +856,7 @@ int fp8moe_norm_fwd(const void* x, const void* y, int64_t T, int64_t H, int32_t 
   const bool post = w_post != nullptr, pre = w_pre != nullptr;
   if (!post && !pre) return FP8MOE_EINVAL;
   if (!post && (y || gate_kind != FP8MOE_GATE_NONE)) return FP8MOE_EINVAL;
+  if (!(eps >= 0.0f)) return FP8MOE_EINVAL;
   if (T == 0) return FP8MOE_OK;
   if (!x || (post && (!y || !r || !rstd_post)) || (pre && (!h || !rstd_pre))) return FP8MOE_EINVAL;
   if ((gate_kind != FP8MOE_GATE_NONE) != (gate != nullptr)) return FP8MOE_EINVAL;

@@ -212,7 +212,9 @@ struct FwdArgs {
 
 // What a kernel variant does: the norm after the block, the one before it, a gate value
 // per element (the other gates are a factor of the row's or of the weight's).
-template <typename T, int MAXT, bool POST, bool PRE, bool FULL>
+// EXACT: a row is as long as its threads' 16 columns each, so no column is out of range
+// (the common lengths, multiples of 512 up to 8192).
+template <typename T, int MAXT, bool POST, bool PRE, bool FULL, bool EXACT>
 __global__ void __launch_bounds__(MAXT, 1)
 norm_fwd_kernel(const __grid_constant__ FwdArgs a, const __grid_constant__ Shape sh) {
   constexpr int P = Vec<T>::kP, NV = kCols / Vec<T>::kN;
@@ -265,7 +267,7 @@ norm_fwd_kernel(const __grid_constant__ FwdArgs a, const __grid_constant__ Shape
 #pragma unroll
       for (int i = 0; i < NV; ++i) {
         const int v = tt + i * stride;
-        Vec<T>::unpack(row_vec(ys, v, v < sh.nvec), r[i]);
+        Vec<T>::unpack(row_vec(ys, v, EXACT || v < sh.nvec), r[i]);
 #pragma unroll
         for (int k = 0; k < P; ++k) s2 = fma2(r[i][k], r[i][k], s2);
       }
@@ -280,7 +282,7 @@ norm_fwd_kernel(const __grid_constant__ FwdArgs a, const __grid_constant__ Shape
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
       const int v = tt + i * stride;
-      const bool in = v < sh.nvec;
+      const bool in = EXACT || v < sh.nvec;
       float2 x[P];
       Vec<T>::unpack(row_vec(xs, v, in), x);
       if (POST) {
@@ -321,7 +323,7 @@ norm_fwd_kernel(const __grid_constant__ FwdArgs a, const __grid_constant__ Shape
         w_pre.get(i, v, w);
 #pragma unroll
         for (int k = 0; k < P; ++k) h[k] = mul2(mul2(r[i][k], both(rq)), w[k]);
-        if (v < sh.nvec) reinterpret_cast<uint4*>(a.h)[(size_t)row * sh.nvec + v] = Vec<T>::pack(h);
+        if (EXACT || v < sh.nvec) reinterpret_cast<uint4*>(a.h)[(size_t)row * sh.nvec + v] = Vec<T>::pack(h);
       }
       if (tt == 0) a.rstd_pre[row] = rq;
     }
@@ -350,7 +352,7 @@ struct BwdArgs {
                                // gate per column)
 };
 
-template <typename T, int MAXT, bool POST, bool PRE, bool FULL>
+template <typename T, int MAXT, bool POST, bool PRE, bool FULL, bool EXACT>
 __global__ void __launch_bounds__(MAXT, 1)
 norm_bwd_kernel(const __grid_constant__ BwdArgs a, const __grid_constant__ Shape sh) {
   constexpr int N = Vec<T>::kN, P = Vec<T>::kP, NV = kCols / N;
@@ -419,7 +421,7 @@ norm_bwd_kernel(const __grid_constant__ BwdArgs a, const __grid_constant__ Shape
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
       const int v = tt + i * stride;
-      const bool in = v < sh.nvec;
+      const bool in = EXACT || v < sh.nvec;
       float2 d[P], r[P], w[P];
       Vec<T>::unpack(row_vec(drs, v, in && a.i_dr >= 0), d);
       if (PRE) {
@@ -468,7 +470,7 @@ norm_bwd_kernel(const __grid_constant__ BwdArgs a, const __grid_constant__ Shape
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
       const int v = tt + i * stride;
-      const bool in = v < sh.nvec;
+      const bool in = EXACT || v < sh.nvec;
       float2 d[P], o[P], w[P];
       Vec<T>::unpack(row_vec(drs, v, in && a.i_dr >= 0), d);
       if (PRE) {
@@ -600,26 +602,32 @@ Shape make_shape(int64_t T, int H, int f32, int tensors) {
 }
 
 // A kernel variant as a type, and the choice of one.
-template <typename TT, int MAXT, bool POST, bool PRE, bool FULL>
+template <typename TT, int MAXT, bool POST, bool PRE, bool FULL, bool EXACT>
 struct Variant {
   using T = TT;
   static constexpr int kMaxT = MAXT;
-  static constexpr bool kPost = POST, kPre = PRE, kFull = FULL;
+  static constexpr bool kPost = POST, kPre = PRE, kFull = FULL, kExact = EXACT;
 };
-template <typename T, int MAXT, typename F>
+template <typename T, int MAXT, bool EXACT, typename F>
 cudaError_t pick_parts(bool post, bool pre, int gate, F f) {
-  if (!post) return f(Variant<T, MAXT, false, true, false>());
+  if (!post) return f(Variant<T, MAXT, false, true, false, EXACT>());
   if (gate == kGateFull)
-    return pre ? f(Variant<T, MAXT, true, true, true>()) : f(Variant<T, MAXT, true, false, true>());
-  return pre ? f(Variant<T, MAXT, true, true, false>()) : f(Variant<T, MAXT, true, false, false>());
+    return pre ? f(Variant<T, MAXT, true, true, true, EXACT>())
+               : f(Variant<T, MAXT, true, false, true, EXACT>());
+  return pre ? f(Variant<T, MAXT, true, true, false, EXACT>())
+             : f(Variant<T, MAXT, true, false, false, EXACT>());
+}
+template <typename T, typename F>
+cudaError_t pick_length(const Shape& sh, bool post, bool pre, int gate, F f) {
+  if (sh.is_long) return pick_parts<T, kLong, false>(post, pre, gate, f);
+  const bool exact = sh.nvec * Vec<T>::kN == sh.warps * 32 * kCols;
+  return exact ? pick_parts<T, kShort, true>(post, pre, gate, f)
+               : pick_parts<T, kShort, false>(post, pre, gate, f);
 }
 template <typename F>
 cudaError_t pick_norm(bool f32, const Shape& sh, bool post, bool pre, int gate, F f) {
-  if (f32)
-    return sh.is_long ? pick_parts<float, kLong>(post, pre, gate, f)
-                      : pick_parts<float, kShort>(post, pre, gate, f);
-  return sh.is_long ? pick_parts<__nv_bfloat16, kLong>(post, pre, gate, f)
-                    : pick_parts<__nv_bfloat16, kShort>(post, pre, gate, f);
+  return f32 ? pick_length<float>(sh, post, pre, gate, f)
+             : pick_length<__nv_bfloat16>(sh, post, pre, gate, f);
 }
 
 size_t ring_bytes(const Shape& s) {
@@ -665,7 +673,7 @@ cudaError_t fp8moe_launch_norm_fwd(const NormFwdArgs& p, int num_sms, cudaStream
   };
   return pick_norm(p.f32, sh, post, pre, p.gate_kind, [&](auto v) {
     using V = decltype(v);
-    return run(norm_fwd_kernel<typename V::T, V::kMaxT, V::kPost, V::kPre, V::kFull>);
+    return run(norm_fwd_kernel<typename V::T, V::kMaxT, V::kPost, V::kPre, V::kFull, V::kExact>);
   });
 }
 
@@ -719,7 +727,7 @@ cudaError_t fp8moe_launch_norm_bwd(const NormBwdArgs& p, int num_sms, cudaStream
     };
     const cudaError_t e = pick_norm(p.f32, sh, post, pre, p.gate_kind, [&](auto v) {
       using V = decltype(v);
-      return run(norm_bwd_kernel<typename V::T, V::kMaxT, V::kPost, V::kPre, V::kFull>);
+      return run(norm_bwd_kernel<typename V::T, V::kMaxT, V::kPost, V::kPre, V::kFull, V::kExact>);
     });
     if (e != cudaSuccess) return e;
   }

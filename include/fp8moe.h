@@ -358,8 +358,9 @@ int fp8moe_combine_tokens_bwd(const void* dout, const void* rows, int64_t M, int
  * g: 1, or `gate` by gate_kind (FP8MOE_GATE_*), through 1 / (1 + exp(-gate)) with
  * sigmoid = 1.  w_post NULL: no block output (y NULL, no gate, the scales are not
  * used); r is x, is not written, and only h is.  w_pre NULL: no h.  At least one of them is given.
- * rstd_post and rstd_pre are what the gradient takes.  H * element size: a multiple
- * of 16 (FP8MOE_EALIGN), at most 32768 (FP8MOE_EINVAL).  All sums are f32. */
+ * rstd_post and rstd_pre are what the gradient takes.  eps >= 0 (FP8MOE_EINVAL; with 0 a
+ * row of zeros gives NaN).  H * element size: a multiple of 16 (FP8MOE_EALIGN), at most
+ * 32768 (FP8MOE_EINVAL).  All sums are f32. */
 int fp8moe_norm_fwd(const void* x, const void* y, int64_t T, int64_t H, int32_t type,
                     const float* w_post, const float* w_pre, const void* gate, int32_t gate_kind,
                     int32_t sigmoid, float residual_scale, float branch_scale, float eps, void* r,

@@ -89,6 +89,7 @@ PRODUCTS = [  # group sizes, rows past them, K, N, SwiGLU
     ([700, 0, 0, 12], 0, 1056, 160, True), ([64] * 9, 0, 768, 1024, False),
     ([0, 0], 5, 128, 128, False), ([1] * 8 + [0] * 24, 0, 2048, 512, True),
     ([833, 100], 3, 96, 2080, False), ([3] * 130, 0, 352, 80, False),
+    ([0] * 700 + [2, 0, 300] + [0] * 321, 5, 64, 48, False),
 ]
 
 

@@ -225,6 +225,9 @@ def test_refusals():
         fb.norm_fwd(x, None, None, w, gate=t, gate_kind="token")
     with pytest.raises(fb.Fp8MoeError, match="EINVAL"):
         fb.norm_fwd(x)                                     # nothing to do
+    for eps in (-1e-6, float("nan")):
+        with pytest.raises(fb.Fp8MoeError, match="EINVAL"):
+            fb.norm_fwd(x, None, None, w, eps=eps)
     with pytest.raises(fb.Fp8MoeError, match="EALIGN"):
         fb.norm_fwd(torch.zeros(4, 12, dtype=BF16, device="cuda"), None, None,
                     torch.ones(12, device="cuda"))
