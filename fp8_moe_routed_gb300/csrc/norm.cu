@@ -636,6 +636,13 @@ size_t ring_bytes(const Shape& s) {
   return b > join ? b : join;
 }
 
+// The same limit for every call: another thread's call or a captured graph of the same
+// kernel may need more than this one does. (A join takes at most 64 KB.)
+template <typename K>
+cudaError_t allow_ring(K kern) {
+  return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kRingBytes);
+}
+
 }  // namespace norm
 }  // namespace fp8moe
 
@@ -666,7 +673,7 @@ cudaError_t fp8moe_launch_norm_fwd(const NormFwdArgs& p, int num_sms, cudaStream
   const bool post = p.w_post != nullptr, pre = p.w_pre != nullptr;
   const size_t smem = ring_bytes(sh);
   auto run = [&](auto kern) {
-    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    cudaError_t e = allow_ring(kern);
     if (e != cudaSuccess) return e;
     kern<<<grid, sh.teams * sh.warps * 32, smem, s>>>(a, sh);
     return cudaGetLastError();
@@ -719,8 +726,7 @@ cudaError_t fp8moe_launch_norm_bwd(const NormBwdArgs& p, int num_sms, cudaStream
   if (grid > 0) {
     const size_t smem = ring_bytes(sh);
     auto run = [&](auto kern) {
-      cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                           (int)smem);
+      cudaError_t e = allow_ring(kern);
       if (e != cudaSuccess) return e;
       kern<<<grid, sh.teams * sh.warps * 32, smem, s>>>(a, sh);
       return cudaGetLastError();

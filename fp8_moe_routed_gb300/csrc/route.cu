@@ -449,8 +449,11 @@ cudaError_t fp8moe_launch_sort_tokens(const int32_t* ids, int64_t n, int E, int6
                                       cudaStream_t s) {
   using namespace fp8moe::route;
   const size_t smem = (size_t)(kSortWarps + 1) * E * sizeof(int32_t);
+  // the limit is the same for every call: another thread's call or a captured graph may
+  // need more than this one does
+  constexpr size_t most = (size_t)(kSortWarps + 1) * fp8moe::kMaxExperts * sizeof(int32_t);
   cudaError_t err = cudaFuncSetAttribute(sort_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                         (int)smem);
+                                         (int)most);
   if (err != cudaSuccess) return err;
   cudaLaunchConfig_t cfg = {};
   // up to 2048 slots one CTA has at most two 32-slot batches per warp (8192 slots: 11.5 us
