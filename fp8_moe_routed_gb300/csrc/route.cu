@@ -308,11 +308,13 @@ dispatch_few_kernel(const uint4* __restrict__ x, const int32_t* __restrict__ ids
 // --------------------------------------------------------------------- combine
 // A CTA sums one token's rows (several tokens' when rows are short), a thread 16 bytes at
 // a time with up to eight row loads in flight; four CTAs of 256 threads on an SM keep
-// 128 KB in flight, and the token's row numbers are read once. (Warps that walked
-// 512-byte pieces of all tokens waited for row numbers and rows in turn: 72 us against
-// 45 for 4093 x 8 x 4096 bf16; 128 or 512 threads a CTA measured the same or slower.) A
-// slot without a row adds nothing: its vector is not read, so what lies there (or a NaN
-// weight) cannot reach the sum.
+// 128 KB in flight, and the token's row numbers are read once. A slot without a row adds
+// nothing: neither its vector nor its weight is read (zeros stand for them), so what lies
+// there, or a NaN weight, cannot reach the sum. Bound by HBM: 4093 x 8 x 4096 bf16 with a
+// quarter of the slots dropped 37 us = 6.3 TB/s. (Warps that walked 512-byte pieces of
+// all tokens waited for row numbers and rows in turn: 72 us; weights read beside their
+// row's sum, which is skipped without a row: 42.6, two waits where one does; 128 or 512
+// threads a CTA measured the same or slower.)
 
 // BATCH row loads in flight (the rows of up to four or eight choices at once); SHORT: rows
 // of at most 128 vectors, per_token threads each, else a token has the whole CTA.
@@ -338,20 +340,24 @@ combine_kernel(const uint4* __restrict__ rows, int64_t tokens, int topk, int nve
     for (int i = 0; i < P; ++i) acc[i] = both(0.0f);
     for (int j0 = 0; j0 < topk; j0 += BATCH) {
       uint4 x[BATCH];
-      int32_t row[BATCH];
+      float w[BATCH];
 #pragma unroll
       for (int j = 0; j < BATCH; ++j) {
-        row[j] = j0 + j < topk ? row_of(sr, j0 + j, M) : -1;
-        if (row[j] >= 0) x[j] = __ldg(rows + (int64_t)row[j] * nvec + v);
+        const int32_t row = j0 + j < topk ? row_of(sr, j0 + j, M) : -1;
+        x[j] = make_uint4(0, 0, 0, 0);
+        w[j] = 0.0f;
+        if (row >= 0) {
+          if (WEIGHTED) w[j] = __ldg(weights + t * topk + j0 + j);
+          x[j] = __ldg(rows + (int64_t)row * nvec + v);
+        }
       }
 #pragma unroll
       for (int j = 0; j < BATCH; ++j) {
-        if (row[j] < 0) continue;
         float2 f[P];
         Vec<T>::unpack(x[j], f);
-        const float w = WEIGHTED ? __ldg(weights + t * topk + j0 + j) : 1.0f;
 #pragma unroll
-        for (int i = 0; i < P; ++i) acc[i] = WEIGHTED ? fma2(both(w), f[i], acc[i]) : add2(acc[i], f[i]);
+        for (int i = 0; i < P; ++i)
+          acc[i] = WEIGHTED ? fma2(both(w[j]), f[i], acc[i]) : add2(acc[i], f[i]);
       }
     }
     out[t * nvec + v] = Vec<T>::pack(acc);
