@@ -461,11 +461,12 @@ norm_bwd_kernel(const __grid_constant__ BwdArgs a, const __grid_constant__ Shape
     // Past this barrier every thread has finished with the stage of the row before.
     if (tt == 0 && sh.stages > 2 && row != row0 && row + (sh.stages - 1) * step < rows)
       ring.fill(a.in, row + (sh.stages - 1) * step, stage == 0 ? sh.stages - 1 : stage - 1);
-    // D = dr + rq u - k1 r;  dy = k2 (w_post g D) - k3 y
-    const float k1 = rq * rq * rq * s3[0] * inv_h;
-    const float qd = a.branch_scale * rp * (s3[1] - k1 * s3[2]);     // sum q D without the row's gate
-    const float k2 = a.branch_scale * grow * rp;
-    const float k3 = rp * rp * grow * qd * inv_h;
+    // D = dr + rq u - k1 rh;  dn = bg g D;  dy = k2 (w_post g D) - k3 yh. No factor is a higher
+    // power of rstd than the result: rows of 1e15, or of 1e-15, keep their precision.
+    const float k1 = rq * (rq * s3[0] * inv_h);
+    const float qd = a.branch_scale * rp * (s3[1] - k1 * (rq * s3[2]));   // sum q D without the row's gate
+    const float bg = a.branch_scale * grow, k2 = bg * rp;
+    const float k3 = rp * (grow * qd * inv_h);
     if (row_gate && tt == 0) a.dgate_row[row] = qd * slope_row;
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
@@ -480,8 +481,9 @@ norm_bwd_kernel(const __grid_constant__ BwdArgs a, const __grid_constant__ Shape
         w_pre.get(i, v, w);
 #pragma unroll
         for (int k = 0; k < P; ++k) {
+          r[k] = mul2(r[k], both(rq));
           d[k] = fma2(r[k], both(-k1), fma2(both(rq), mul2(dh[k], w[k]), d[k]));
-          acc_pre[PRE ? i : 0][k] = fma2(dh[k], mul2(r[k], both(rq)), acc_pre[PRE ? i : 0][k]);
+          acc_pre[PRE ? i : 0][k] = fma2(dh[k], r[k], acc_pre[PRE ? i : 0][k]);
         }
       }
 #pragma unroll
@@ -494,15 +496,16 @@ norm_bwd_kernel(const __grid_constant__ BwdArgs a, const __grid_constant__ Shape
         if (FULL) Vec<T>::unpack(row_vec(gs, v, in), g);
 #pragma unroll
         for (int k = 0; k < P; ++k) {
+          y[k] = mul2(y[k], both(rp));
           float2 dy = mul2(d[k], y[k]), wd = mul2(w[k], d[k]);
           if (FULL) {
             const float2 s = a.sigmoid ? sigmoid2(g[k]) : g[k];
-            const float2 dg = mul2(mul2(dy, w[k]), both(k2));
+            const float2 dg = mul2(mul2(dy, w[k]), both(bg));
             g[k] = a.sigmoid ? mul2(dg, fma2(mul2(s, both(-1.0f)), s, s)) : dg;
             dy = mul2(dy, s);
             wd = mul2(wd, s);
           }
-          acc_post[POST ? i : 0][k] = fma2(dy, both(k2), acc_post[POST ? i : 0][k]);
+          acc_post[POST ? i : 0][k] = fma2(dy, both(bg), acc_post[POST ? i : 0][k]);
           o[k] = fma2(wd, both(k2), mul2(y[k], both(-k3)));
         }
         if (in) reinterpret_cast<uint4*>(a.dy)[(size_t)row * sh.nvec + v] = Vec<T>::pack(o);
