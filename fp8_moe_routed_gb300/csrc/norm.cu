@@ -97,10 +97,22 @@ __device__ __forceinline__ float2 one_over_one_plus2(float2 t) {
   return d;
 }
 
-// 1 / (1 + exp(-z)) by t = exp(-|z|), which cannot overflow.
-__device__ __forceinline__ float2 sigmoid2(float2 z) {
+// g = 1 / (1 + exp(-z)) by t = exp(-|z|), which cannot overflow, and its slope g (1 - g) =
+// t / (1 + t)^2, which unlike that product does not cancel where g is near one.
+__device__ __forceinline__ float2 sigmoid2(float2 z, float2& slope) {
   const float2 t = exp_minus_abs2(z), d = one_over_one_plus2(t), td = mul2(t, d);
+  slope = mul2(td, d);
   return make_float2(z.x >= 0.0f ? d.x : td.x, z.y >= 0.0f ? d.y : td.y);
+}
+__device__ __forceinline__ float2 sigmoid2(float2 z) {
+  float2 slope;
+  return sigmoid2(z, slope);
+}
+__device__ __forceinline__ float sigmoid(float z, float& slope) {
+  float2 slopes;
+  const float g = sigmoid2(both(z), slopes).x;
+  slope = slopes.x;
+  return g;
 }
 __device__ __forceinline__ float sigmoid(float z) { return sigmoid2(both(z)).x; }
 
@@ -434,10 +446,6 @@ norm_bwd_kernel(const __grid_constant__ BwdArgs a, const __grid_constant__ Shape
   for (uint32_t row = row0; row < rows; row += step) {
     const float rp = next_p, rq = next_q;
     float grow = next_g, slope_row = 1.0f;
-    if (row_gate && a.sigmoid) {
-      grow = sigmoid(grow);
-      slope_row = grow * (1.0f - grow);
-    }
     fetch(row + step);
     ok = ok && mbar_wait(&ring.full[stage], phase, kWhereEpilogue);
     const uint32_t drs = ring.at(stage, 0);
@@ -486,6 +494,7 @@ norm_bwd_kernel(const __grid_constant__ BwdArgs a, const __grid_constant__ Shape
       }
     }
     float s3[3] = {s0.x + s0.y, s1.x + s1.y, s2.x + s2.y};
+    if (row_gate && a.sigmoid) grow = sigmoid(grow, slope_row);
     team_sum<3>(s3, s_red, buf, slot, first, quads, team, sh.warps);
     buf ^= 1;
     // Past this barrier every thread has finished with the stage of the row before.
@@ -529,9 +538,9 @@ norm_bwd_kernel(const __grid_constant__ BwdArgs a, const __grid_constant__ Shape
           y[k] = mul2(y[k], both(rp));
           float2 dy = mul2(d[k], y[k]), wd = mul2(w[k], d[k]);
           if (FULL) {
-            const float2 s = a.sigmoid ? sigmoid2(g[k]) : g[k];
-            const float2 dg = mul2(mul2(dy, w[k]), both(bg));
-            g[k] = a.sigmoid ? mul2(dg, fma2(mul2(s, both(-1.0f)), s, s)) : dg;
+            float2 slope = both(1.0f);
+            const float2 s = a.sigmoid ? sigmoid2(g[k], slope) : g[k];
+            g[k] = mul2(mul2(mul2(dy, w[k]), both(bg)), slope);
             dy = mul2(dy, s);
             wd = mul2(wd, s);
           }
@@ -607,9 +616,10 @@ norm_join_kernel(const float* __restrict__ part, int ctas, int H, const float* _
   if (blockIdx.y == 0) {
     dw_pre[c] = t;
   } else if (gate) {
-    const float z = __ldg(gate + c), g = sigmoid_gate ? sigmoid(z) : z;
+    float slope = 1.0f;
+    const float z = __ldg(gate + c), g = sigmoid_gate ? sigmoid(z, slope) : z;
     dw_post[c] = t * g;
-    dgate[c] = t * __ldg(w_post + c) * (sigmoid_gate ? g * (1.0f - g) : 1.0f);
+    dgate[c] = t * __ldg(w_post + c) * slope;
   } else {
     dw_post[c] = t;
   }

@@ -65,3 +65,31 @@ def test_value_at_the_ends(kind):
     assert (r[0] == 1).all() and (r[1] == 0).all() and (r[2] == 1).all() and (r[3] == 0).all()
     assert torch.isnan(r[4]).all() and (r[7] == 0.5).all()
     assert ((r[5] > 8e-39) & (r[5] < 9e-39)).all() and (r[6] < 1e-44).all()
+
+
+@pytest.mark.parametrize("kind,dtype", KINDS)
+def test_slope(kind, dtype):
+    """dgate = b dr w yh g (1 - g), summed over what shares a logit. The steps of test_value
+    with 3 more for the slope's second factor, and up to 16 for the sum: 48, or 2.9e-6; 3e-6
+    is asked.
+    bf16 for a gate per element alone, the other gates and their gradients are f32."""
+    y, dr, w, yh, z, t, kw = make(kind, dtype)
+    rp = fb.norm_fwd(torch.zeros_like(y).cuda(), y.cuda(), w.cuda(), None, eps=0.0, **kw)[2]
+    dgate = fb.norm_bwd(dr.cuda(), None, None, y.cuda(), w.cuda(), None, rp, None, **kw)[4]
+    want = B * dr.double() * w.double() * yh * t / (1 + t) ** 2
+    want = {"token": want.sum(1), "channel": want.sum(0), "full": want}[kind]
+    off = worst(dgate, want)
+    assert off <= (2.0 ** -8 if dgate.dtype == BF16 else 3e-6), off
+
+
+@pytest.mark.parametrize("kind", ["token", "full"])
+def test_slope_at_the_ends(kind):
+    z, full = ends()
+    dr, y, w = torch.ones(8, H), torch.ones(8, H), torch.ones(H)
+    gate = (full if kind == "full" else z).cuda()
+    dgate = fb.norm_bwd(dr.cuda(), None, None, y.cuda(), w.cuda(), None, torch.ones(8, device="cuda"),
+                        None, gate=gate, gate_kind=kind, sigmoid=True)[4].cpu()
+    n = H if kind == "token" else 1
+    assert (dgate[:4] == 0).all() and torch.isnan(dgate[4]).all()
+    assert ((dgate[5] > n * 8e-39) & (dgate[5] < n * 9e-39)).all() and (dgate[6] < n * 1e-44).all()
+    assert (dgate[7] == n * 0.25).all()
