@@ -26,6 +26,7 @@
 // join 4 us; what is left is the latency of a row's chain (copy, reduction, stores),
 // which 14 to 16 warps do not hide completely.
 #include <cstdint>
+#include <initializer_list>
 #include <cuda_runtime.h>
 #include <cuda_bf16.h>
 
@@ -735,6 +736,16 @@ int fp8moe_norm_bwd_ctas(int64_t T) {
 
 cudaError_t fp8moe_launch_norm_bwd(const NormBwdArgs& p, int num_sms, cudaStream_t s) {
   using namespace fp8moe::norm;
+  if (p.T == 0) {
+    // No rows: no kernel shape either (empty tensors have no address, so nothing to stream).
+    // Sums over nothing are zeros, whatever the weights and the gate hold.
+    for (float* sum : {p.w_pre ? p.dw_pre : nullptr, p.w_post ? p.dw_post : nullptr,
+                       p.gate_kind == kGateCol ? static_cast<float*>(p.dgate) : nullptr}) {
+      const cudaError_t e = sum ? cudaMemsetAsync(sum, 0, (size_t)p.H * sizeof(float), s) : cudaSuccess;
+      if (e != cudaSuccess) return e;
+    }
+    return cudaSuccess;
+  }
   BwdArgs a = {};
   int n = 0;
   auto add = [&](const void* t) {
@@ -766,20 +777,18 @@ cudaError_t fp8moe_launch_norm_bwd(const NormBwdArgs& p, int num_sms, cudaStream
   const int64_t items = (sh.T + sh.teams - 1) / sh.teams;
   int grid = (int)(items < num_sms ? items : num_sms);
   if (grid > fp8moe_norm_bwd_ctas(p.T)) grid = fp8moe_norm_bwd_ctas(p.T);
-  if (grid > 0) {
-    const size_t smem = ring_bytes(sh);
-    auto run = [&](auto kern) {
-      cudaError_t e = allow_ring(kern);
-      if (e != cudaSuccess) return e;
-      kern<<<grid, sh.teams * sh.warps * 32, smem, s>>>(a, sh);
-      return cudaGetLastError();
-    };
-    const cudaError_t e = pick_norm(p.f32, sh, post, pre, p.gate_kind, [&](auto v) {
-      using V = decltype(v);
-      return run(norm_bwd_kernel<typename V::T, V::kMaxT, V::kPost, V::kPre, V::kFull, V::kExact>);
-    });
+  const size_t smem = ring_bytes(sh);
+  auto run = [&](auto kern) {
+    cudaError_t e = allow_ring(kern);
     if (e != cudaSuccess) return e;
-  }
+    kern<<<grid, sh.teams * sh.warps * 32, smem, s>>>(a, sh);
+    return cudaGetLastError();
+  };
+  cudaError_t e = pick_norm(p.f32, sh, post, pre, p.gate_kind, [&](auto v) {
+    using V = decltype(v);
+    return run(norm_bwd_kernel<typename V::T, V::kMaxT, V::kPost, V::kPre, V::kFull, V::kExact>);
+  });
+  if (e != cudaSuccess) return e;
   const dim3 jg((unsigned)((p.H + kJoinCols - 1) / kJoinCols), 2, 1);
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = jg;
@@ -788,8 +797,8 @@ cudaError_t fp8moe_launch_norm_bwd(const NormBwdArgs& p, int num_sms, cudaStream
   cudaLaunchAttribute attr[1];
   fp8moe::pdl_attribute(attr[0]);
   cfg.attrs = attr;
-  cfg.numAttrs = grid > 0 ? 1 : 0;
-  const cudaError_t e = cudaLaunchKernelEx(
+  cfg.numAttrs = 1;
+  e = cudaLaunchKernelEx(
       &cfg, norm_join_kernel, static_cast<const float*>(p.part), grid, p.H,
       p.gate_kind == kGateCol ? a.gate : nullptr, p.w_post, p.sigmoid, pre ? p.dw_pre : nullptr,
       post ? p.dw_post : nullptr,
