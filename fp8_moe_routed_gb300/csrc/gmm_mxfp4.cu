@@ -28,6 +28,8 @@
 //                the TMEM store's round trip) takes about 900 cycles, a stage of MMAs 416.
 //   warps 20..27 epilogue: two groups of four (one warp per lane quarter) alternate over
 //                16-token chunks of one of two accumulators.
+// The peer's threads, copies or commits arrive on full, empty, tfull, tempty and drain:
+// these are waited for at cluster scope (no difference in time to CTA scope).
 // TMEM (512 columns): two accumulators of 208, four scale slots of 24.
 //
 // SwiGLU: a CTA's 128 weight rows are 4 x (16 gate rows, 16 up rows), fetched by one
@@ -266,7 +268,7 @@ gmm_mxfp4_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant_
       const uint32_t bytes = 2u * (uint32_t)(kABytes + box * kKBytes);
       const int m = t.m0 + rank * (t.tok / 2);
       for (int kb = 0; kb < nkb; ++kb) {
-        if (!mbar_wait_warp(&s.empty[st], ph ^ 1, kWhereProducer)) { ok = false; break; }
+        if (!mbar_wait_warp_cluster(&s.empty[st], ph ^ 1, kWhereProducer)) { ok = false; break; }
         if (leader) {
           if (rank == 0) mbar_arrive_expect_tx(&s.full[st], bytes);
           const uint32_t bar = mapa_shared(smem_u32(&s.full[st]), 0);
@@ -288,7 +290,7 @@ gmm_mxfp4_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant_
       const int64_t n_last = issued < stages ? issued : stages;
       for (int64_t i = 1; i <= n_last; ++i) {
         const int64_t idx = issued - i;
-        mbar_wait(&s.full[idx % stages], (uint32_t)((idx / stages) & 1), kWhereDrain);
+        mbar_wait_cluster(&s.full[idx % stages], (uint32_t)((idx / stages) & 1), kWhereDrain);
       }
     }
   } else if (warp == 1) {
@@ -306,12 +308,12 @@ gmm_mxfp4_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant_
         const uint32_t idesc0 = make_idesc_mxf4(kUnitN, tok, 0);
         const uint32_t idesc2 = make_idesc_mxf4(kUnitN, tok, 2);
         const uint32_t d = tmem + (uint32_t)(ab * kDCols);
-        if (!mbar_wait(&s.tempty[ab], tph ^ 1, kWhereMma)) { ok = false; break; }
+        if (!mbar_wait_cluster(&s.tempty[ab], tph ^ 1, kWhereMma)) { ok = false; break; }
         tc_fence_after();
         for (int kb = 0; kb < nkb; ++kb) {
           // a wait costs its latency even when there is nothing to wait for, so the next
           // step's barrier is tested before this step's products are issued
-          if (!ready && !mbar_wait(&s.full[st], ph, kWhereMma)) { ok = false; break; }
+          if (!ready && !mbar_wait_cluster(&s.full[st], ph, kWhereMma)) { ok = false; break; }
           tc_fence_after();
           const uint64_t ad = make_desc(smem_u32(a_tile(st)), 16, 1024, kSwizzle128B);
           const uint64_t bd = make_desc(smem_u32(b_tile(st)), 16, 1024, kSwizzle128B);
@@ -319,7 +321,7 @@ gmm_mxfp4_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant_
           uint64_t* const done = &s.empty[st];
           if (++st == stages) { st = 0; ph ^= 1; }
           if (++sl == kSlots) sl = 0;
-          ready = mbar_test(&s.full[st], ph);
+          ready = mbar_test_cluster(&s.full[st], ph);
 #pragma unroll
           for (int kk = 0; kk < 4; ++kk) {
             // the descriptors' address field counts 16 bytes: 64 values are two. Past K
@@ -343,7 +345,7 @@ gmm_mxfp4_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant_
       mma_commit_pair(&s.drain);
     }
     __syncwarp();
-    if (lane == 0) mbar_wait(&s.drain, 0, kWhereDrain);
+    if (lane == 0) mbar_wait_cluster(&s.drain, 0, kWhereDrain);
   } else if (warp == 2) {
     // ===================== TMA producer: scale words ======================
     pdl_wait();
@@ -420,7 +422,7 @@ gmm_mxfp4_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant_
         // The slot was last read by the products of step i - kSlots, this group's step
         // before: their stage's barrier tells when they are done. (The phase that it could
         // be mistaken for, two uses of the stage earlier, was waited for in its turn.)
-        if (i >= kSlots && !mbar_wait_warp(&s.empty[before], before_ph, kWhereDequant)) {
+        if (i >= kSlots && !mbar_wait_warp_cluster(&s.empty[before], before_ph, kWhereDequant)) {
           ok = false;
           break;
         }
@@ -430,6 +432,9 @@ gmm_mxfp4_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant_
         tmem_st_wait();
         tc_fence_before();
         __syncwarp();
+        // Relaxed: what the product reads is in tensor memory, ordered by the store's wait and the
+        // fences on both sides of the barrier, not by a release (which would also wait for
+        // every earlier access of this thread: balanced wi 552 against 418 us).
         if (lane == 0) mbar_arrive_cluster_relaxed(even_full + (uint32_t)(cs * sizeof(uint64_t)));
         before = cs;
         before_ph = cph;
@@ -461,7 +466,7 @@ gmm_mxfp4_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant_
     for (Walk at(cluster, nclusters, wt); at.tile < tiles; at.next()) {
       const Unit t = at.unit(s);
       // the four warps leave together: a named barrier's wait has no limit
-      if (!named_bar_all(1 + half, 128, mbar_wait_warp(&s.tfull[ab], tph, kWhereEpilogue)))
+      if (!named_bar_all(1 + half, 128, mbar_wait_warp_cluster(&s.tfull[ab], tph, kWhereEpilogue)))
         break;
       tc_fence_after();
       const int col0 = SWIGLU ? t.w0 * kRowsA + rank * 64 : t.w0 * kUnitN + rank * kRowsA;

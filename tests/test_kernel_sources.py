@@ -1,0 +1,27 @@
+"""Rules of the kernels that no result shows, checked on their sources: what breaks them
+breaks a run only now and then."""
+import glob
+import os
+import re
+
+import pytest
+
+CSRC = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))),
+                    "fp8_moe_routed_gb300", "csrc")
+SOURCES = sorted(glob.glob(os.path.join(CSRC, "*.cu")))
+
+
+def code(path):
+    with open(path) as f:
+        text = f.read()
+    return re.sub(r"//[^\n]*|/\*.*?\*/", "", text, flags=re.S)
+
+
+@pytest.mark.parametrize("path", SOURCES, ids=os.path.basename)
+def test_barriers_of_the_peer_cta_are_waited_for_at_cluster_scope(path):
+    """A barrier that is addressed through mapa (threads or copies of the peer CTA arrive on
+    it) is waited for and tested with an acquire at cluster scope."""
+    text = code(path)
+    shared = set(re.findall(r"mapa_shared\(smem_u32\(&s\.(\w+)", text))
+    for wait, name in re.findall(r"(mbar_(?:try_)?(?:wait|test)\w*)\(&s\.(\w+)", text):
+        assert name not in shared or wait.endswith("_cluster"), (wait, name)
