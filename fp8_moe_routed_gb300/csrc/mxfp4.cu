@@ -100,7 +100,7 @@ mx_quantize_weights_kernel(const uint32_t* __restrict__ w, int K, int N, int k_t
                            uint8_t* __restrict__ codes, uint32_t* __restrict__ scales) {
   // 36-word rows: 16-byte aligned, and eight consecutive rows fall into different banks
   __shared__ uint4 s_code[kWtN][kWtK / 32 + 1];
-  __shared__ uint8_t s_scale[kWtK / kMxWord][kWtN][4];
+  __shared__ uint32_t s_scale[kWtK / kMxWord][kWtN];    // written by bytes, read by words
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int64_t tile = blockIdx.x;
   const int kt = (int)(tile % k_tiles);
@@ -132,7 +132,7 @@ mx_quantize_weights_kernel(const uint32_t* __restrict__ w, int K, int N, int k_t
       q[g] = quantize8(x, byte, inv);
     }
     s_code[2 * lane + c][warp] = make_uint4(q[0], q[1], q[2], q[3]);
-    s_scale[warp >> 2][2 * lane + c][warp & 3] = (uint8_t)byte;
+    reinterpret_cast<uint8_t*>(&s_scale[warp >> 2][2 * lane + c])[warp & 3] = (uint8_t)byte;
   }
   __syncthreads();
   const int64_t row_bytes = K / 2;
@@ -148,7 +148,7 @@ mx_quantize_weights_kernel(const uint32_t* __restrict__ w, int K, int N, int k_t
     const int g = threadIdx.x / kWtN, r = threadIdx.x % kWtN;
     const int word = kt * (kWtK / kMxWord) + g;
     if (word < words && n0 + r < N)
-      scales[(e * words + word) * N + n0 + r] = *reinterpret_cast<const uint32_t*>(s_scale[g][r]);
+      scales[(e * words + word) * N + n0 + r] = s_scale[g][r];
   }
 }
 

@@ -25,3 +25,11 @@ def test_barriers_of_the_peer_cta_are_waited_for_at_cluster_scope(path):
     shared = set(re.findall(r"mapa_shared\(smem_u32\(&s\.(\w+)", text))
     for wait, name in re.findall(r"(mbar_(?:try_)?(?:wait|test)\w*)\(&s\.(\w+)", text):
         assert name not in shared or wait.endswith("_cluster"), (wait, name)
+
+
+@pytest.mark.parametrize("path", SOURCES, ids=os.path.basename)
+def test_shared_byte_arrays_are_aligned_for_the_words_read_from_them(path):
+    """Arrays of a kernel's own (dynamic shared memory is aligned by where it starts)."""
+    text = code(path)
+    for name in re.findall(r"(?<!extern )__shared__\s+uint8_t\s+(\w+)\s*\[", text):
+        assert not re.search(r"reinterpret_cast<[^>]*\*>\(\s*&?%s\b" % name, text), name
