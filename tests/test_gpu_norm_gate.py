@@ -93,3 +93,28 @@ def test_slope_at_the_ends(kind):
     assert (dgate[:4] == 0).all() and torch.isnan(dgate[4]).all()
     assert ((dgate[5] > n * 8e-39) & (dgate[5] < n * 9e-39)).all() and (dgate[6] < n * 1e-44).all()
     assert (dgate[7] == n * 0.25).all()
+
+
+@pytest.mark.parametrize("kind", ["token", "channel", "full"])
+def test_bf16_rows_at_the_ends(kind):
+    """The same in bf16 rows, whose gates per element and channel take the fast exponential:
+    beyond f32's smallest normal value a gate may be zero, but nothing is infinite or NaN."""
+    z, full = ends()
+    n = H // 8
+    gate = {"token": z, "channel": z.repeat_interleave(n), "full": full.to(BF16)}[kind].cuda()
+    T = 8 if kind == "token" else 3 if kind == "channel" else 8
+    y, dr = (torch.ones(T, H, dtype=BF16) for _ in range(2))
+    w = torch.ones(H)
+    kw = dict(gate=gate, gate_kind=kind, sigmoid=True)
+    r = fb.norm_fwd(torch.zeros_like(y).cuda(), y.cuda(), w.cuda(), None, eps=0.0, **kw)[0].cpu().float()
+    dgate = fb.norm_bwd(dr.cuda(), None, None, y.cuda(), w.cuda(), None, torch.ones(T, device="cuda"),
+                        None, **kw)[4].cpu().float()
+    if kind == "channel":
+        r, dgate = r[0].reshape(8, n), dgate.reshape(8, n)
+    terms = {"token": H, "channel": T, "full": 1}[kind]
+    for i, want in enumerate([1.0, 0.0, 1.0, 0.0]):
+        assert (r[i] == want).all() and (dgate[i] == 0).all()
+    assert torch.isnan(r[4]).all() and torch.isnan(dgate[4]).all()
+    assert ((r[5:7] >= 0) & (r[5:7] < 1e-38)).all() and (r[7] == 0.5).all()
+    assert ((dgate[5:7] >= 0) & (dgate[5:7] < terms * 1e-38)).all()
+    assert (dgate[7] == terms * 0.25).all()
