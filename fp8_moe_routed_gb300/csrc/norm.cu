@@ -155,6 +155,17 @@ struct Ring {
   }
 };
 
+// What a thread knows of its ring, in one word: bit 0 the parity of its stage's barrier, above
+// it the waits that have run out (each sets the status word). After the first of them the
+// thread that fills the ring fetches no row any more, but goes on waiting, as every thread
+// does until it has given up on as many as there are stages: so whatever was on its way to
+// the ring has been waited for, with the same limit, before the CTA leaves its shared memory.
+constexpr uint32_t kOneLost = 2, kAllLost = kOneLost * kMaxStages;
+
+__device__ __forceinline__ void wait_row(const Ring& ring, int stage, uint32_t& state) {
+  if (state < kAllLost && !mbar_wait(&ring.full[stage], state & 1, kWhereEpilogue)) state += kOneLost;
+}
+
 // Vector v of a row, zeros past its end.
 __device__ __forceinline__ uint4 row_vec(uint32_t row, int v, bool in) {
   uint4 x = make_uint4(0, 0, 0, 0);
@@ -303,8 +314,7 @@ norm_fwd_kernel(const __grid_constant__ FwdArgs a, const __grid_constant__ Shape
   __syncthreads();
   const float inv_h = 1.0f / (float)sh.H;
   int stage = 0, buf = 0;
-  uint32_t phase = 0;
-  bool ok = true;
+  uint32_t state = 0;
   const bool row_gate = POST && a.gate_kind == kGateRow;
   float next_g = 1.0f;                     // the next item's gate, fetched an item ahead
   auto fetch = [&](uint32_t row) {
@@ -315,7 +325,7 @@ norm_fwd_kernel(const __grid_constant__ FwdArgs a, const __grid_constant__ Shape
     float grow = next_g;
     if (row_gate && a.sigmoid) grow = sigmoid(grow);
     fetch(row + step);
-    ok = ok && mbar_wait(&ring.full[stage], phase, kWhereEpilogue);
+    wait_row(ring, stage, state);
     const uint32_t xs = ring.at(stage, 0);
     const uint32_t ys = ring.at(stage, 1);
     const uint32_t gs = ring.at(stage, 2);
@@ -371,7 +381,7 @@ norm_fwd_kernel(const __grid_constant__ FwdArgs a, const __grid_constant__ Shape
       team_sync(team, sh.warps);
     }
     // past that barrier every thread has read the stage
-    if (tt == 0 && row + sh.stages * step < rows) ring.fill(a.in, row + sh.stages * step, stage);
+    if (tt == 0 && state < kOneLost && row + sh.stages * step < rows) ring.fill(a.in, row + sh.stages * step, stage);
     if (PRE) {
       const float rq = rsqrtf(fmaf(ss[0], inv_h, a.eps));
 #pragma unroll
@@ -387,7 +397,7 @@ norm_fwd_kernel(const __grid_constant__ FwdArgs a, const __grid_constant__ Shape
     }
     if (++stage == sh.stages) {
       stage = 0;
-      phase ^= 1;
+      state ^= 1;
     }
   }
 }
@@ -457,13 +467,12 @@ norm_bwd_kernel(const __grid_constant__ BwdArgs a, const __grid_constant__ Shape
   };
   fetch(row0);
   int stage = 0, buf = 0;
-  uint32_t phase = 0;
-  bool ok = true;
+  uint32_t state = 0;
   for (uint32_t row = row0; row < rows; row += step) {
     const float rp = next_p, rq = next_q;
     float grow = next_g, slope_row = 1.0f;
     fetch(row + step);
-    ok = ok && mbar_wait(&ring.full[stage], phase, kWhereEpilogue);
+    wait_row(ring, stage, state);
     const uint32_t drs = ring.at(stage, 0);
     const uint32_t dhs = ring.at(stage, PRE ? a.i_dh : 0);
     const uint32_t rs = ring.at(stage, PRE ? a.i_dh + 1 : 0);
@@ -514,7 +523,8 @@ norm_bwd_kernel(const __grid_constant__ BwdArgs a, const __grid_constant__ Shape
     team_sum<3>(s3, s_red, buf, slot, first, quads, team, sh.warps);
     buf ^= 1;
     // Past this barrier every thread has finished with the stage of the row before.
-    if (tt == 0 && sh.stages > 2 && row != row0 && row + (sh.stages - 1) * step < rows)
+    if (tt == 0 && state < kOneLost && sh.stages > 2 && row != row0 &&
+        row + (sh.stages - 1) * step < rows)
       ring.fill(a.in, row + (sh.stages - 1) * step, stage == 0 ? sh.stages - 1 : stage - 1);
     // D = dr + rq u - k1 rh;  dn = bg g D;  dy = k2 (w_post g D) - k3 yh. No factor is a higher
     // power of rstd than the result: rows of 1e15, or of 1e-15, keep their precision.
@@ -569,11 +579,11 @@ norm_bwd_kernel(const __grid_constant__ BwdArgs a, const __grid_constant__ Shape
     }
     if (sh.stages <= 2) {      // long rows: a stage is too dear to wait for the next barrier
       team_sync(team, sh.warps);
-      if (tt == 0 && row + sh.stages * step < rows) ring.fill(a.in, row + sh.stages * step, stage);
+      if (tt == 0 && state < kOneLost && row + sh.stages * step < rows) ring.fill(a.in, row + sh.stages * step, stage);
     }
     if (++stage == sh.stages) {
       stage = 0;
-      phase ^= 1;
+      state ^= 1;
     }
   }
   // the column sums of this CTA: its teams' are joined in shared memory (the ring

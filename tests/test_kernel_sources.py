@@ -33,3 +33,19 @@ def test_shared_byte_arrays_are_aligned_for_the_words_read_from_them(path):
     text = code(path)
     for name in re.findall(r"(?<!extern )__shared__\s+uint8_t\s+(\w+)\s*\[", text):
         assert not re.search(r"reinterpret_cast<[^>]*\*>\(\s*&?%s\b" % name, text), name
+
+
+def test_the_norms_leave_no_copy_in_flight_behind_a_failed_wait():
+    """A wait for a row that runs out ends the filling of the ring, but not the waits for the
+    rows that were on their way: a CTA gives up on as many as it has stages."""
+    text = code(os.path.join(CSRC, "norm.cu"))
+    assert re.search(r"kAllLost = kOneLost \* kMaxStages;", text)
+    assert re.search(r"if \(state < kAllLost && !mbar_wait\(.*?\)\) state \+= kOneLost;", text)
+    kernels = [k for k in re.split(r"__global__", text)[1:] if "ring.fill" in k]
+    assert len(kernels) == 2
+    for k in kernels:
+        body = k[k.index("for (uint32_t row = row0"):]
+        assert body.count("wait_row(ring, stage, state);") == 1 and "mbar_wait" not in body
+        fills = re.findall(r"if \(([^;{]*?)\)\s*ring\.fill", body)
+        assert len(fills) == body.count("ring.fill") > 0
+        assert all("state < kOneLost" in f for f in fills), fills
