@@ -19,7 +19,7 @@ LIB = os.path.join(OUT_DIR, "libfp8moe.so")
 
 SOURCES = ["api.cu", "quant.cu", "dequant.cu", "gmm_fwd.cu", "gmm_dlhs.cu", "gmm_dlhs_pair.cu",
            "tgmm.cu", "noalloc.cu", "selftest.cu", "route.cu", "norm.cu", "mxfp4.cu",
-           "gmm_mxfp4.cu"]
+           "gmm_mxfp4.cu", "status.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "-Xptxas", "-v",
               "--expt-relaxed-constexpr", f"-I{INCLUDE}", f"-I{CSRC}"]

@@ -975,17 +975,8 @@ int fp8moe_gmm_silu_mxfp4_fwd(const void* lhs, int64_t M, int64_t K, const uint8
 int fp8moe_read_status(fp8moe_stream_t stream, uint32_t* flags) {
   if (!flags) return FP8MOE_EINVAL;
   uint32_t v = 0;
-  uint32_t (*takes[])(cudaStream_t) = {fp8moe_status_take_quant, fp8moe_status_take_dequant,
-                                       fp8moe_status_take_gmm_fwd, fp8moe_status_take_dlhs,
-                                       fp8moe_status_take_dlhs_pair, fp8moe_status_take_tgmm,
-                                       fp8moe_status_take_selftest, fp8moe_status_take_route,
-                                       fp8moe_status_take_norm, fp8moe_status_take_mxfp4,
-                                       fp8moe_status_take_gmm_mxfp4};
-  for (auto take : takes) {
-    uint32_t x = take(stream);
-    if (x == 0xFFFFFFFFu) return cuda_fail(cudaGetLastError());
-    v |= x;
-  }
+  const cudaError_t e = fp8moe_collect_status(&v, stream);
+  if (e != cudaSuccess) return cuda_fail(e);
   *flags = v;
   return FP8MOE_OK;
 }

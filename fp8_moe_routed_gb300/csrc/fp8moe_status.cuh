@@ -29,18 +29,9 @@ __device__ __forceinline__ void status_set(uint32_t bits) { atomicOr(&g_status_w
 
 }  // namespace fp8moe
 
-// Defines `uint32_t <fn>(cudaStream_t)`: waits for the stream, returns this
-// translation unit's status word and clears it.
-#define FP8MOE_DEFINE_STATUS_TAKE(fn)                                              \
-  uint32_t fn(cudaStream_t s) {                                                    \
-    uint32_t v = 0, z = 0;                                                         \
-    if (cudaMemcpyFromSymbolAsync(&v, fp8moe::g_status_word, 4, 0,                 \
-                                  cudaMemcpyDeviceToHost, s) != cudaSuccess)       \
-      return 0xFFFFFFFFu;                                                          \
-    if (cudaStreamSynchronize(s) != cudaSuccess) return 0xFFFFFFFFu;               \
-    if (cudaMemcpyToSymbolAsync(fp8moe::g_status_word, &z, 4, 0,                   \
-                                cudaMemcpyHostToDevice, s) != cudaSuccess)         \
-      return 0xFFFFFFFFu;                                                          \
-    if (cudaStreamSynchronize(s) != cudaSuccess) return 0xFFFFFFFFu;               \
-    return v;                                                                      \
+// Defines `cudaError_t <fn>(uint32_t** word)`: where to take this translation unit's status
+// word from on the current device.
+#define FP8MOE_DEFINE_STATUS_TAKE(fn)                                                    \
+  cudaError_t fn(uint32_t** word) {                                                      \
+    return cudaGetSymbolAddress(reinterpret_cast<void**>(word), fp8moe::g_status_word);  \
   }

@@ -77,13 +77,17 @@ extern "C" int fp8moe_internal_check_fwd_args(const void* lhs, int64_t M, int64_
                                               int64_t N, const int32_t* gs, const void* out,
                                               int swiglu, int* empty);
 
-uint32_t fp8moe_status_take_quant(cudaStream_t s);
-uint32_t fp8moe_status_take_dequant(cudaStream_t s);
-uint32_t fp8moe_status_take_gmm_fwd(cudaStream_t s);
-uint32_t fp8moe_status_take_dlhs(cudaStream_t s);
-uint32_t fp8moe_status_take_dlhs_pair(cudaStream_t s);
-uint32_t fp8moe_status_take_tgmm(cudaStream_t s);
-uint32_t fp8moe_status_take_selftest(cudaStream_t s);
+// Waits for the stream; *flags receives the OR of all status words, which are cleared
+// (status.cu).
+cudaError_t fp8moe_collect_status(uint32_t* flags, cudaStream_t s);
+// Addresses of the translation units' status words on the current device.
+cudaError_t fp8moe_status_take_quant(uint32_t** word);
+cudaError_t fp8moe_status_take_dequant(uint32_t** word);
+cudaError_t fp8moe_status_take_gmm_fwd(uint32_t** word);
+cudaError_t fp8moe_status_take_dlhs(uint32_t** word);
+cudaError_t fp8moe_status_take_dlhs_pair(uint32_t** word);
+cudaError_t fp8moe_status_take_tgmm(uint32_t** word);
+cudaError_t fp8moe_status_take_selftest(uint32_t** word);
 
 // One thread waits on an mbarrier that nothing completes for limit_ns, then
 // records a wait timeout (selftest.cu).
@@ -95,7 +99,7 @@ cudaError_t fp8moe_launch_selftest_cast(const float* x, int64_t n, int fmt, uint
 
 // Tokens sorted by expert and back (route.cu). n = T * topk slots; nvec = 16-byte
 // vectors of a row; f32: rows hold f32 instead of bf16.
-uint32_t fp8moe_status_take_route(cudaStream_t s);
+cudaError_t fp8moe_status_take_route(uint32_t** word);
 cudaError_t fp8moe_launch_sort_tokens(const int32_t* ids, int64_t n, int E, int64_t M,
                                       int32_t* group_sizes, int32_t* slot_row, int32_t* row_slot,
                                       cudaStream_t s);
@@ -153,7 +157,7 @@ struct NormBwdArgs {
 };
 int fp8moe_norm_bwd_ctas(int64_t T);
 cudaError_t fp8moe_launch_norm_bwd(const NormBwdArgs& a, int num_sms, cudaStream_t s);
-uint32_t fp8moe_status_take_norm(cudaStream_t s);
+cudaError_t fp8moe_status_take_norm(uint32_t** word);
 
 // Microscaled 4-bit quantisation (mxfp4.cu).
 // scale_stride: words between the scale words of consecutive 128 k (>= M).
@@ -165,7 +169,7 @@ cudaError_t fp8moe_launch_mxfp4_quantize_weights(const void* w, int E, int K, in
                                                  uint8_t* scales, cudaStream_t s);
 cudaError_t fp8moe_launch_mxfp4_dequantize(const uint8_t* codes, const uint8_t* scales, int E,
                                            int N, int K, void* out, int num_sms, cudaStream_t s);
-uint32_t fp8moe_status_take_mxfp4(cudaStream_t s);
+cudaError_t fp8moe_status_take_mxfp4(uint32_t** word);
 
 // Grouped product of MXFP4 operands (gmm_mxfp4.cu).
 struct GmmMxfp4Args {
@@ -182,4 +186,4 @@ struct GmmMxfp4Args {
 };
 void fp8moe_gmm_mxfp4_boxes(int rows[3], int* scale_rows);
 cudaError_t fp8moe_launch_gmm_mxfp4(const GmmMxfp4Args& a, int num_sms, cudaStream_t s);
-uint32_t fp8moe_status_take_gmm_mxfp4(cudaStream_t s);
+cudaError_t fp8moe_status_take_gmm_mxfp4(uint32_t** word);
