@@ -688,7 +688,9 @@ cudaError_t pick_parts(bool post, bool pre, int gate, F f) {
 }
 template <typename T, typename F>
 cudaError_t pick_length(const Shape& sh, bool post, bool pre, int gate, F f) {
-  if (sh.is_long) return pick_parts<T, kLong, false>(post, pre, gate, f);
+  // rows of at most 32768 bytes: only bf16 ones are longer than kShort threads' columns
+  if constexpr (32768 / sizeof(T) > kShort * kCols)
+    if (sh.is_long) return pick_parts<T, kLong, false>(post, pre, gate, f);
   const bool exact = sh.nvec * Vec<T>::kN == sh.warps * 32 * kCols;
   return exact ? pick_parts<T, kShort, true>(post, pre, gate, f)
                : pick_parts<T, kShort, false>(post, pre, gate, f);

@@ -49,3 +49,14 @@ def test_the_norms_leave_no_copy_in_flight_behind_a_failed_wait():
         fills = re.findall(r"if \(([^;{]*?)\)\s*ring\.fill", body)
         assert len(fills) == body.count("ring.fill") > 0
         assert all("state < kOneLost" in f for f in fills), fills
+
+
+def test_no_norm_variant_is_built_that_no_row_reaches():
+    """f32 rows hold at most 8192 values, which 512 threads take: the variants of 1024 threads
+    are bf16's alone. By the compiler's report of the build at hand."""
+    report = os.path.join(os.path.dirname(CSRC), "_build", "norm.cu.ptxas.txt")
+    if not os.path.exists(report):
+        pytest.skip("not built here")
+    with open(report) as f:
+        built = set(re.findall(r"norm_(?:fwd|bwd)_kernelI(\w+?)Li(\d+)E", f.read()))
+    assert built == {("13__nv_bfloat16", "512"), ("13__nv_bfloat16", "1024"), ("f", "512")}
