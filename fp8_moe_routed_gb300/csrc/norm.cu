@@ -22,9 +22,9 @@
 // each with a ring of its own and at its own pace. All sums and the column sums of the
 // weight gradients are f32; the latter stay in registers over all rows of a CTA and are
 // joined by a second small kernel in a fixed order, so results do not change from run
-// to run. 4096 x 7168 bf16: forward 41 us (5.7 TB/s), backward 66 us (5.3 TB/s) and the
-// join 4 us; what is left is the latency of a row's chain (copy, reduction, stores),
-// which 14 to 16 warps do not hide completely.
+// to run. 4096 x 7168 bf16, a gate per token: forward 42 us (5.6 TB/s), backward with the
+// join's 4 us 68 us (5.2 TB/s); what is left is the latency of a row's chain (copy,
+// reduction, stores), which 14 to 16 warps do not hide completely.
 #include <cstdint>
 #include <initializer_list>
 #include <cuda_runtime.h>
@@ -72,7 +72,7 @@ struct Loads {
 //   exp(x) = (2^h)^2 exp(r) = (2^h)^2 (1 + r),  r = x - h 2 ln 2  (under 1e-5: r^2 is nothing)
 // with 2^h by the exponential unit (measured 2.4 steps) and r by two exact fused products.
 // A plain fast exponential leaves r out and is off by 1.2 |z| units in the last place; the
-// library's is exact to one, but its branches and registers cost 63.5 us where this takes 47.6
+// library's is exact to one, but its branches and registers cost 63.5 us where this takes 48
 // (5003 x 1544 f32, a gate per element). The square keeps results below 2^-126 from being
 // flushed. NaN stays NaN.
 __device__ __forceinline__ float2 exp_minus_abs2(float2 z) {

@@ -1,6 +1,8 @@
 // vec16.cuh -- 16 bytes of bf16 or f32 values as pairs of f32 registers and back, and
-// the packed f32 arithmetic on such pairs (one instruction for two values, each
-// rounded like the scalar operation).
+// the packed f32 arithmetic on such pairs (one instruction for two values). Each is rounded
+// like the scalar operation, but a product whose sum follows may be joined with it into one
+// rounding, although both ask for their own: where that rounding matters, the product is
+// taken by a scalar operation, which is never joined.
 #pragma once
 #include <cstdint>
 #include <cuda_runtime.h>

@@ -279,7 +279,8 @@ int fp8moe_selftest_cast_f32(const float* x, int64_t n, int32_t fmt, uint8_t* co
                              fp8moe_stream_t stream);
 
 /* Waits for `stream`, returns in *flags the OR of the FP8MOE_STATUS_* bits set
- * since the last call, and clears them. */
+ * since the last call, and clears them.  A bit that is set meanwhile, by work on
+ * another stream, is in this call's flags or in a later one's, never lost. */
 int fp8moe_read_status(fp8moe_stream_t stream, uint32_t* flags);
 
 /* The wi forward of fp8moe_gmm_silu_fp8_fwd for callers that cannot allocate
@@ -360,7 +361,8 @@ int fp8moe_combine_tokens_bwd(const void* dout, const void* rows, int64_t M, int
  * used); r is x, is not written, and only h is.  w_pre NULL: no h.  At least one of them is given.
  * rstd_post and rstd_pre are what the gradient takes.  eps >= 0 (FP8MOE_EINVAL; with 0 a
  * row of zeros gives NaN).  H * element size: a multiple of 16 (FP8MOE_EALIGN), at most
- * 32768 (FP8MOE_EINVAL).  All sums are f32. */
+ * 32768 (FP8MOE_EINVAL).  All sums are f32: a row keeps f32's relative precision, in
+ * both directions, while its sum of squares is a normal f32 number (or eps holds it up). */
 int fp8moe_norm_fwd(const void* x, const void* y, int64_t T, int64_t H, int32_t type,
                     const float* w_post, const float* w_pre, const void* gate, int32_t gate_kind,
                     int32_t sigmoid, float residual_scale, float branch_scale, float eps, void* r,
@@ -375,7 +377,8 @@ int fp8moe_norm_fwd(const void* x, const void* y, int64_t T, int64_t H, int32_t 
  *   dgate = branch_scale * D * w_post * yh, summed over what shares a gate value, times
  *   g (1 - g) with sigmoid = 1: f32 [T], f32 [H] or [T, H] of `type`, by gate_kind
  * Without w_post dx = D (r is x; the scales are not used).  Column sums are joined in a fixed order.
- * T = 0 writes zeros to dw_post, dw_pre and a per-channel dgate.  Workspace: FP8MOE_OP_NORM_BWD with M = T, K = H. */
+ * T = 0 writes zeros to dw_post, dw_pre and a per-channel dgate, whatever the weights and
+ * the gate hold.  Workspace: FP8MOE_OP_NORM_BWD with M = T, K = H. */
 int fp8moe_norm_bwd(const void* dr, const void* dh, const void* r, const void* y, int64_t T,
                     int64_t H, int32_t type, const float* w_post, const float* w_pre,
                     const float* rstd_post, const float* rstd_pre, const void* gate,
