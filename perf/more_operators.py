@@ -271,10 +271,10 @@ def _router_bwd_plain(s, c):
 # ---------------------------------------------------- plain forms: the optimiser
 def _random(at, which, step, seed):
     """32 random bits of a value, from its place: multiplications by the odd numbers next to
-    the fractions of the golden ratio, of sqrt(3) and of sqrt(2), with shifts between them."""
+    the fractions of the golden ratio and of the roots of 2, 3 and 5, with shifts between them."""
     mask = 0xFFFFFFFF
-    key = (seed + 0x9E3779B9 * step + 0xBB67AE85 * which) & mask
-    x = ((at & mask) * 0x9E3779B9 + (at >> 32) * 0x6A09E667 + key) & mask
+    key = (seed + 0x6A09E667 * step + 0xBB67AE85 * which) & mask
+    x = ((at & mask) * 0x9E3779B9 + (at >> 32) * 0x3C6EF373 + key) & mask
     x = ((x ^ (x >> 16)) * 0xBB67AE85) & mask
     x = ((x ^ (x >> 15)) * 0x6A09E667) & mask
     return x ^ (x >> 16)
