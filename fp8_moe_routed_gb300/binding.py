@@ -31,11 +31,13 @@ OP_GMM_FP8_FWD_BLOCK = 7
 OP_GMM_MXFP4_FWD = 8
 OP_GMM_SILU_MXFP4_FWD = 9
 OP_NORM_BWD = 10
+OP_BALANCE = 11
 
 STATUS_NEGATIVE_GROUP = 0x1
 STATUS_GROUPS_EXCEED_M = 0x2
 STATUS_WAIT_TIMEOUT = 0x4
 STATUS_BAD_EXPERT = 0x10
+STATUS_BAD_OFFSETS = 0x20
 
 # every symbol include/fp8moe.h declares
 EXPORTS = [
@@ -51,6 +53,8 @@ EXPORTS = [
     "fp8moe_combine_tokens", "fp8moe_combine_tokens_bwd", "fp8moe_norm_fwd", "fp8moe_norm_bwd",
     "fp8moe_mxfp4_quantize_rows", "fp8moe_mxfp4_quantize_weights", "fp8moe_mxfp4_dequantize",
     "fp8moe_gmm_mxfp4_fwd", "fp8moe_gmm_silu_mxfp4_fwd",
+    "fp8moe_router_fwd", "fp8moe_balance_fwd", "fp8moe_router_bwd", "fp8moe_adamw_workspace_size",
+    "fp8moe_adamw_step",
 ]
 
 FMT = {"e4m3": 0, "e5m2": 1}
@@ -82,7 +86,7 @@ def load(build_if_missing: bool = True):
             _build.build()
         L = ctypes.CDLL(path)
         P, I64, I32, SZ = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int32, ctypes.c_size_t
-        F32 = ctypes.c_float
+        F32, F64, U32 = ctypes.c_float, ctypes.c_double, ctypes.c_uint32
         sig = {
             "fp8moe_workspace_size": ([I32, I64, I64, I64, I32], SZ),
             "fp8moe_gmm_fp8_fwd": ([P, I64, I64, P, P, I32, I64, P, P, P, SZ, P], I32),
@@ -123,6 +127,13 @@ def load(build_if_missing: bool = True):
             "fp8moe_mxfp4_dequantize": ([P, P, I32, I64, I64, P, P], I32),
             "fp8moe_gmm_mxfp4_fwd": ([P, I64, I64, P, P, I32, I64, P, P, P, SZ, P], I32),
             "fp8moe_gmm_silu_mxfp4_fwd": ([P, I64, I64, P, P, I32, I64, P, P, P, SZ, P], I32),
+            "fp8moe_router_fwd": ([P, I64, I32, I32, I32, P, I32, I32, F32, P, I32, P, P, P, P, P, P,
+                                   SZ, P], I32),
+            "fp8moe_balance_fwd": ([P, P, I64, I32, I32, I32, I32, P, I32, P, P, P, P, SZ, P], I32),
+            "fp8moe_router_bwd": ([P, P, P, I64, I32, I32, I32, I32, I32, F32, P, P, P, I32, P, P],
+                                  I32),
+            "fp8moe_adamw_workspace_size": ([P, I32, I32], SZ),
+            "fp8moe_adamw_step": ([P, I32, I64, P, F64, P, F64, F64, F64, P, U32, P, SZ, P], I32),
         }
         for name, (args, res) in sig.items():
             fn = getattr(L, name)
@@ -752,6 +763,273 @@ def gmm_mxfp4_fwd(lhs, codes, scales, group_sizes, out=None, workspace=None):
 def gmm_silu_mxfp4_fwd(lhs, codes, scales, group_sizes, out=None, workspace=None):
     """The same with fused SwiGLU: bf16 [M, N/2] (see fp8moe_gmm_silu_mxfp4_fwd)."""
     return _mxfp4_fwd(lhs, codes, scales, group_sizes, out, workspace, silu=True)
+
+
+SCORES = {"softmax": 0, "sigmoid": 1}
+
+
+def _router(logits, score: str, topk: int, seq_offsets):
+    """Checks what the router's calls share: (type number, score number, B)."""
+    ty = _req_rows(logits, "logits")
+    if score not in SCORES:
+        raise ValueError(f"score must be one of {sorted(SCORES)}, got {score!r}")
+    B = 1
+    if seq_offsets is not None:
+        _req(seq_offsets, torch.int32, "seq_offsets", 1)
+        B = seq_offsets.numel() - 1
+        if B < 1:
+            raise ValueError("seq_offsets must hold at least one sequence (two offsets)")
+    return ty, SCORES[score], B
+
+
+def _one_device(device, **tensors):
+    """Every tensor of a call lies on the current device."""
+    if device.index != torch.cuda.current_device():
+        raise ValueError(f"tensors must be on the current device, got {device}")
+    for name, t in tensors.items():
+        if t is not None and t.device != device:
+            raise ValueError(f"{name} must be on {device}, got {t.device}")
+
+
+def _balance_outputs(B: int, E: int, device):
+    return (torch.empty(B, E, dtype=torch.int32, device=device),
+            torch.empty(B, dtype=torch.float32, device=device),
+            torch.empty(B, E, dtype=torch.float32, device=device))
+
+
+def router_fwd(logits, topk: int, score: str = "softmax", bias=None, normalize: bool = True,
+               weight_scale: float = 1.0, balance: bool = False, seq_offsets=None, workspace=None):
+    """The router's choice for logits [T, E] (bf16 or f32): (ids int32 [T, topk], weights f32
+    [T, topk], counts, loss, slope), the last three None unless balance (see
+    fp8moe_router_fwd and balance_fwd). score: "softmax" or "sigmoid"; bias f32 [E] takes part in
+    the choice alone; normalize: a token's weights add up to weight_scale. seq_offsets int32
+    [B + 1]: where the sequences of the batch begin and end; tokens outside get no expert (-1)."""
+    L = load()
+    ty, sc, B = _router(logits, score, topk, seq_offsets)
+    T, E = logits.shape
+    dev = logits.device
+    if bias is not None:
+        _shaped(bias, torch.float32, "bias", (E,))
+    _one_device(dev, bias=bias, seq_offsets=seq_offsets, workspace=workspace)
+    if topk < 1:
+        raise ValueError("topk must be positive")
+    ids = torch.empty(T, topk, dtype=torch.int32, device=dev)
+    weights = torch.empty(T, topk, dtype=torch.float32, device=dev)
+    counts = loss = slope = None
+    ws, wsb = None, 0
+    if balance:
+        counts, loss, slope = _balance_outputs(B, E, dev)
+        ws, wsb = _workspace(OP_BALANCE, T, 0, B, E, dev, workspace)
+    _check(L.fp8moe_router_fwd(_ptr(logits), T, E, ty, sc, _ptr(bias), topk, int(bool(normalize)),
+                               weight_scale, _ptr(seq_offsets), B, _ptr(ids), _ptr(weights),
+                               _ptr(counts), _ptr(loss), _ptr(slope), _ptr(ws), wsb, _stream(dev)),
+           "fp8moe_router_fwd")
+    return ids, weights, counts, loss, slope
+
+
+def balance_fwd(logits, ids, score: str = "softmax", seq_offsets=None, workspace=None):
+    """The balance loss of given choices ids int32 [T, topk]: (counts int32 [B, E], loss f32 [B],
+    slope f32 [B, E]) for each sequence (see fp8moe_balance_fwd): loss = sum_i slope_i * sum of the
+    tokens' shares of expert i, slope_i = E counts_i / (choices * tokens). router_fwd gives the
+    same in its pass over the logits."""
+    L = load()
+    _req(ids, torch.int32, "ids", 2)
+    T, k = ids.shape
+    ty, sc, B = _router(logits, score, k, seq_offsets)
+    if logits.shape[0] != T:
+        raise ValueError("shape mismatch")
+    E, dev = logits.shape[1], logits.device
+    _one_device(dev, ids=ids, seq_offsets=seq_offsets, workspace=workspace)
+    counts, loss, slope = _balance_outputs(B, E, dev)
+    ws, wsb = _workspace(OP_BALANCE, T, 0, B, E, dev, workspace)
+    _check(L.fp8moe_balance_fwd(_ptr(logits), _ptr(ids), T, E, ty, sc, k, _ptr(seq_offsets), B,
+                                _ptr(counts), _ptr(loss), _ptr(slope), _ptr(ws), wsb, _stream(dev)),
+           "fp8moe_balance_fwd")
+    return counts, loss, slope
+
+
+def router_bwd(dweights, logits, ids, score: str = "softmax", normalize: bool = True,
+               weight_scale: float = 1.0, dloss=None, slope=None, seq_offsets=None, out=None):
+    """Gradient into the logits [T, E], of their type: of the weights (dweights f32 [T, topk], or
+    None) and of the balance losses (dloss f32 [B] with the forward's slope, or None) (see
+    fp8moe_router_bwd). ids and the options: the forward's."""
+    L = load()
+    _req(ids, torch.int32, "ids", 2)
+    T, k = ids.shape
+    ty, sc, B = _router(logits, score, k, seq_offsets)
+    if logits.shape[0] != T:
+        raise ValueError("shape mismatch")
+    E, dev, f32 = logits.shape[1], logits.device, torch.float32
+    if (dloss is None) != (slope is None):
+        raise ValueError("dloss and slope go together")
+    if dweights is not None:
+        _shaped(dweights, f32, "dweights", (T, k))
+    if dloss is not None:
+        _shaped(dloss, f32, "dloss", (B,))
+        _shaped(slope, f32, "slope", (B, E))
+    _one_device(dev, ids=ids, dweights=dweights, dloss=dloss, slope=slope, seq_offsets=seq_offsets,
+                out=out)
+    out = _like(out, (T, E), logits.dtype, dev, "out")
+    _check(L.fp8moe_router_bwd(_ptr(dweights), _ptr(logits), _ptr(ids), T, E, ty, sc, k,
+                               int(bool(normalize)), weight_scale, _ptr(dloss), _ptr(slope),
+                               _ptr(seq_offsets), B, _ptr(out), _stream(dev)), "fp8moe_router_bwd")
+    return out
+
+
+class _AdamwTensor(ctypes.Structure):
+    """fp8moe_adamw_tensor."""
+    _fields_ = ([(n, ctypes.c_uint64) for n in ("p", "g", "m", "v", "m_scale", "v_scale", "copy",
+                                                "codes", "code_scale")] +
+                [(n, ctypes.c_int64) for n in ("n", "K", "N")] +
+                [("weight_decay", ctypes.c_double), ("g_type", ctypes.c_int32),
+                 ("state_bits", ctypes.c_int32)])
+
+
+ADAMW_BLOCK = 128  # consecutive values of an 8-bit moment that share a scale
+
+
+def adamw_blocks(n: int) -> int:
+    """Scales of an 8-bit moment of n values."""
+    return -(-n // ADAMW_BLOCK)
+
+
+class AdamwPlan:
+    """The tensors of adamw_step, checked once: f32 params with their moments, in 32 bits (f32
+    of the same shape) or, where m_scales and v_scales are given, in 8 (u8 codes of the same
+    shape, f32 [ceil(n / 128)] scales; zeros to begin with). copies: bf16 copies of the new
+    params; codes and code_scales: u8 [E, K, N] and f32 [E, N], the 8-bit weights of params
+    [E, K, N]. Each is a list as long as params, with None where a param has none, or None.
+    weight_decay: a number or one for each param. The plan keeps the tensors' memory: a param
+    whose storage is replaced needs a new plan (adamw_step refuses it)."""
+
+    def __init__(self, params, m, v, m_scales=None, v_scales=None, copies=None, codes=None,
+                 code_scales=None, weight_decay=0.0):
+        count = len(params)
+        none = [None] * count
+
+        def listed(x, name):
+            if x is None:
+                return none
+            if len(x) != count:
+                raise ValueError(f"{name} must have one entry for each of the {count} params")
+            return list(x)
+
+        m, v = listed(m, "m"), listed(v, "v")
+        m_scales, v_scales = listed(m_scales, "m_scales"), listed(v_scales, "v_scales")
+        copies, codes = listed(copies, "copies"), listed(codes, "codes")
+        code_scales = listed(code_scales, "code_scales")
+        decay = list(weight_decay) if isinstance(weight_decay, (list, tuple)) \
+            else [float(weight_decay)] * count
+        listed(decay, "weight_decay")
+        self.params, self._kept, self._shapes = list(params), [], []
+        self.device = None
+        self._table = (_AdamwTensor * max(1, count))()
+        f32, u8 = torch.float32, torch.uint8
+        spans = []
+        for i, p in enumerate(self.params):
+            if not isinstance(p, torch.Tensor):
+                raise TypeError(f"param {i} must be a tensor")
+            shape, n = tuple(p.shape), p.numel()
+            _req(p, f32, f"param {i}", p.dim())
+            eight = m_scales[i] is not None
+            if eight != (v_scales[i] is not None):
+                raise ValueError(f"m_scale and v_scale of param {i} go together")
+            state = u8 if eight else f32
+            _shaped(m[i], state, f"m of param {i}", shape)
+            _shaped(v[i], state, f"v of param {i}", shape)
+            if eight:
+                _shaped(m_scales[i], f32, f"m_scale of param {i}", (adamw_blocks(n),))
+                _shaped(v_scales[i], f32, f"v_scale of param {i}", (adamw_blocks(n),))
+            if copies[i] is not None:
+                _shaped(copies[i], torch.bfloat16, f"copy of param {i}", shape)
+            if (codes[i] is None) != (code_scales[i] is None):
+                raise ValueError(f"codes and code_scale of param {i} go together")
+            e = self._table[i]
+            if codes[i] is not None:
+                if len(shape) != 3:
+                    raise ValueError(f"param {i} must be [E, K, N] to have codes, got {shape}")
+                _shaped(codes[i], u8, f"codes of param {i}", shape)
+                _shaped(code_scales[i], f32, f"code_scale of param {i}", (shape[0], shape[2]))
+                e.K, e.N = shape[1], shape[2]
+            own = [p, m[i], v[i], m_scales[i], v_scales[i], copies[i], codes[i], code_scales[i]]
+            for t, field in zip(own, ("p", "m", "v", "m_scale", "v_scale", "copy", "codes",
+                                      "code_scale")):
+                if t is None:
+                    continue
+                if self.device is None:
+                    self.device = t.device
+                if t.device != self.device:
+                    raise ValueError(f"param {i} and its states must be on {self.device}")
+                setattr(e, field, t.data_ptr())
+                spans.append((t.data_ptr(), t.data_ptr() + t.numel() * t.element_size(), i))
+                self._kept.append(t.detach())
+            e.n, e.weight_decay, e.state_bits = n, float(decay[i]), 8 if eight else 32
+            self._shapes.append(p.shape)
+        spans = sorted(s for s in spans if s[0] < s[1])
+        for a, b in zip(spans, spans[1:]):
+            if b[0] < a[1]:
+                raise ValueError(f"params {a[2]} and {b[2]} or their states overlap")
+        self._addresses = [p.data_ptr() for p in self.params]
+
+    def _enter(self, grads):
+        """Writes the gradients' addresses and types into the table."""
+        count = len(self.params)
+        if len(grads) != count:
+            raise ValueError(f"grads must have one entry for each of the {count} params")
+        if [p.data_ptr() for p in self.params] != self._addresses:
+            raise ValueError("a param's storage was replaced: make a new plan")
+        table, dev = self._table, self.device
+        for i, g in enumerate(grads):
+            e = table[i]
+            if g is None:                       # no gradient: the param is left as it is
+                e.n = 0
+                continue
+            ty = TYPES.get(g.dtype) if isinstance(g, torch.Tensor) else None
+            if ty is None or g.shape != self._shapes[i] or g.device != dev \
+                    or not g.is_contiguous():
+                if not isinstance(g, torch.Tensor):
+                    raise TypeError(f"gradient {i} must be a tensor")
+                if ty is None:
+                    raise TypeError(f"gradient {i} must be torch.bfloat16 or torch.float32, got "
+                                    f"{g.dtype}")
+                _shaped(g, g.dtype, f"gradient {i}", tuple(self._shapes[i]))
+                raise ValueError(f"gradient {i} must be on {dev}, got {g.device}")
+            e.g, e.g_type, e.n = g.data_ptr(), ty, g.numel()
+        return table, count
+
+
+def adamw_step(plan: AdamwPlan, grads, step, lr, beta1: float = 0.9, beta2: float = 0.999,
+               eps: float = 1e-8, grad_scale=None, seed: int = 0, workspace=None) -> None:
+    """One AdamW step on the plan's tensors, in place, for grads (bf16 or f32, one for each param;
+    None leaves the param and its states as they are) (see fp8moe_adamw_step). step: the number
+    of this step, from 1, or an int64 CUDA tensor [1]; lr: a number or an f32 CUDA tensor [1] (what
+    a captured step reads when it is replayed). grad_scale: f32 CUDA tensor [1] that every gradient
+    is multiplied by, or None. seed: of the rounding of 8-bit moments."""
+    L = load()
+    table, count = plan._enter(grads)
+    if count == 0:
+        return
+    dev = plan.device
+    step_dev = lr_dev = None
+    if isinstance(step, torch.Tensor):
+        _shaped(step, torch.int64, "step", (1,))
+        step, step_dev = 0, step
+    if isinstance(lr, torch.Tensor):
+        _shaped(lr, torch.float32, "lr", (1,))
+        lr, lr_dev = 0.0, lr
+    if grad_scale is not None:
+        _shaped(grad_scale, torch.float32, "grad_scale", (1,))
+    _one_device(dev, step=step_dev, lr=lr_dev, grad_scale=grad_scale, workspace=workspace)
+    need = int(L.fp8moe_adamw_workspace_size(table, count,
+                                             step_dev is not None or lr_dev is not None))
+    if workspace is None and need:
+        workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+    elif workspace is not None and not (workspace.is_cuda and workspace.is_contiguous()):
+        raise ValueError("workspace must be a contiguous CUDA tensor")
+    wsb = workspace.numel() * workspace.element_size() if workspace is not None else 0
+    _check(L.fp8moe_adamw_step(table, count, int(step), _ptr(step_dev), float(lr), _ptr(lr_dev),
+                               beta1, beta2, eps, _ptr(grad_scale), seed & 0xFFFFFFFF,
+                               _ptr(workspace), wsb, _stream(dev)), "fp8moe_adamw_step")
 
 
 def read_status(device=None) -> int:

@@ -1,6 +1,7 @@
 // api.cu -- the C ABI of libfp8moe.so (declared in include/fp8moe.h): argument
 // checks, workspace carving, TMA tensor maps and kernel launches.  Every step of
 // the path runs in the kernels of this library; there is no host fallback.
+#include <cmath>
 #include <cstdint>
 #include <cstdio>
 #include <cstring>
@@ -408,6 +409,84 @@ int gmm_mxfp4_impl(const void* lhs, int64_t M, int64_t K, const uint8_t* codes,
   return e == cudaSuccess ? FP8MOE_OK : cuda_fail(e);
 }
 
+int check_router(int64_t T, int32_t E, int32_t type, int32_t score, int32_t topk,
+                 const int32_t* offsets, int32_t B) {
+  if (E < 1 || E > 1024 || topk < 1 || topk > 32 || topk > E || B < 1) return FP8MOE_EINVAL;
+  if (T < 0 || T >= ((int64_t)1 << 31) || T * topk >= ((int64_t)1 << 31)) return FP8MOE_EINVAL;
+  if (!type_bytes(type)) return FP8MOE_EINVAL;
+  if (score != FP8MOE_SCORE_SOFTMAX && score != FP8MOE_SCORE_SIGMOID) return FP8MOE_EINVAL;
+  if (!offsets && B != 1) return FP8MOE_EINVAL;
+  return aligned4(offsets) ? FP8MOE_OK : FP8MOE_EALIGN;
+}
+
+// Parts of the balance sums: one for each chunk of tokens and sequence that has a part in it.
+int64_t balance_slots(int64_t T, int64_t B) {
+  const int64_t chunk = fp8moe_balance_chunk(T);
+  return (T + chunk - 1) / chunk + B;
+}
+
+size_t balance_ws_bytes(int64_t T, int64_t B, int32_t E) {
+  const size_t slots = (size_t)balance_slots(T, B);
+  return 2 * round_up(slots * (size_t)E * 4, 256) + round_up(slots * 4, 256);
+}
+
+// Checks the balance loss's outputs and workspace and enters them into `a`.
+int set_balance(RouterArgs& a, int32_t* counts, float* loss, float* slope, void* ws,
+                size_t ws_bytes) {
+  if (!counts || !loss || !slope) return FP8MOE_EINVAL;
+  if (!ws) return FP8MOE_EWORKSPACE;
+  if (!aligned4(counts) || !aligned4(loss) || !aligned4(slope) ||
+      (reinterpret_cast<uintptr_t>(ws) & 255u))
+    return FP8MOE_EALIGN;
+  if (ws_bytes < balance_ws_bytes(a.T, a.B, a.E)) return FP8MOE_EWORKSPACE;
+  const size_t slots = (size_t)balance_slots(a.T, a.B);
+  uint8_t* w = static_cast<uint8_t*>(ws);
+  a.part_share = reinterpret_cast<float*>(w);
+  a.part_count = reinterpret_cast<int32_t*>(w + round_up(slots * (size_t)a.E * 4, 256));
+  a.part_tokens = reinterpret_cast<int32_t*>(w + 2 * round_up(slots * (size_t)a.E * 4, 256));
+  a.counts = counts;
+  a.loss = loss;
+  a.slope = slope;
+  return FP8MOE_OK;
+}
+
+bool aligned2(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 1u) == 0; }
+
+int check_adamw(const fp8moe_adamw_tensor& d) {
+  if (d.n < 0 || d.n > ((int64_t)1 << 42)) return FP8MOE_EINVAL;
+  if (d.n == 0) return FP8MOE_OK;
+  if (!type_bytes(d.g_type) || (d.state_bits != 32 && d.state_bits != 8)) return FP8MOE_EINVAL;
+  if (!d.p || !d.g || !d.m || !d.v) return FP8MOE_EINVAL;
+  const bool eight = d.state_bits == 8;
+  if ((d.m_scale != nullptr) != eight || (d.v_scale != nullptr) != eight) return FP8MOE_EINVAL;
+  if ((d.codes != nullptr) != (d.code_scale != nullptr)) return FP8MOE_EINVAL;
+  if (!(d.weight_decay == d.weight_decay)) return FP8MOE_EINVAL;
+  if (!aligned4(d.p) || !aligned4(d.m_scale) || !aligned4(d.v_scale) || !aligned4(d.code_scale) ||
+      !aligned2(d.copy) || (d.g_type == FP8MOE_TYPE_F32 ? !aligned4(d.g) : !aligned2(d.g)) ||
+      (!eight && (!aligned4(d.m) || !aligned4(d.v))))
+    return FP8MOE_EALIGN;
+  if (d.codes) {
+    if (d.K < 1 || d.N < 1 || d.K > (1 << 22) || d.N > (1 << 22)) return FP8MOE_EINVAL;
+    if (d.n % (d.K * d.N) != 0 || d.n / (d.K * d.N) > 1024) return FP8MOE_EINVAL;
+    if (d.K % 16 != 0 || d.N % 16 != 0) return FP8MOE_EALIGN;
+  }
+  return FP8MOE_OK;
+}
+
+int64_t adamw_columns(const fp8moe_adamw_tensor& d) {
+  return d.n > 0 && d.codes && d.K > 0 ? d.n / d.K : 0;
+}
+
+// The rates of a step on the device lie in front of the columns' largest magnitudes.
+constexpr size_t kAdamwRatesBytes = 256;
+static_assert(sizeof(AdamwRates) <= kAdamwRatesBytes, "the columns' words begin behind");
+
+size_t adamw_ws_bytes(const fp8moe_adamw_tensor* tensors, int32_t count, bool on_device) {
+  size_t columns = 0;
+  for (int32_t i = 0; i < count; ++i) columns += (size_t)adamw_columns(tensors[i]);
+  return columns || on_device ? kAdamwRatesBytes + round_up(columns * 4, 256) : 0;
+}
+
 }  // namespace
 
 extern "C" {
@@ -427,6 +506,8 @@ size_t fp8moe_workspace_size(int op, int64_t M, int64_t K, int64_t N, int32_t E)
       return mxfp4_ws_bytes(M, K);
     case FP8MOE_OP_NORM_BWD:
       return norm_bwd_ws_bytes(M, K);
+    case FP8MOE_OP_BALANCE:
+      return balance_ws_bytes(M, N, E);
     default:
       return 0;
   }
@@ -970,6 +1051,183 @@ int fp8moe_gmm_silu_mxfp4_fwd(const void* lhs, int64_t M, int64_t K, const uint8
                               size_t workspace_bytes, fp8moe_stream_t stream) {
   return gmm_mxfp4_impl(lhs, M, K, codes, scales, E, N, group_sizes, out, workspace,
                         workspace_bytes, stream, 1);
+}
+
+int fp8moe_router_fwd(const void* logits, int64_t T, int32_t E, int32_t type, int32_t score,
+                      const float* bias, int32_t topk, int32_t normalize, float scale,
+                      const int32_t* seq_offsets, int32_t B, int32_t* ids, float* weights,
+                      int32_t* counts, float* loss, float* slope, void* workspace,
+                      size_t workspace_bytes, fp8moe_stream_t stream) {
+  int rc = check_router(T, E, type, score, topk, seq_offsets, B);
+  if (rc) return rc;
+  if (normalize != 0 && normalize != 1) return FP8MOE_EINVAL;
+  if (T > 0 && (!logits || !ids || !weights)) return FP8MOE_EINVAL;
+  if (!aligned16(logits) || !aligned4(bias) || !aligned4(ids) || !aligned4(weights))
+    return FP8MOE_EALIGN;
+  RouterArgs a = {};
+  a.logits = logits, a.bias = bias, a.ids = ids, a.weights = weights, a.offsets = seq_offsets;
+  a.T = T, a.E = E, a.k = topk, a.B = B, a.f32 = type == FP8MOE_TYPE_F32;
+  a.sig = score == FP8MOE_SCORE_SIGMOID, a.normalize = normalize, a.scale = scale;
+  if (counts || loss || slope) {
+    rc = set_balance(a, counts, loss, slope, workspace, workspace_bytes);
+    if (rc) return rc;
+  } else if (T == 0) {
+    return FP8MOE_OK;
+  }
+  int sms = 0;
+  rc = device_init(&sms);
+  if (rc) return rc;
+  const cudaError_t e = fp8moe_launch_router(a, stream);
+  return e == cudaSuccess ? FP8MOE_OK : cuda_fail(e);
+}
+
+int fp8moe_balance_fwd(const void* logits, const int32_t* ids, int64_t T, int32_t E, int32_t type,
+                       int32_t score, int32_t topk, const int32_t* seq_offsets, int32_t B,
+                       int32_t* counts, float* loss, float* slope, void* workspace,
+                       size_t workspace_bytes, fp8moe_stream_t stream) {
+  int rc = check_router(T, E, type, score, topk, seq_offsets, B);
+  if (rc) return rc;
+  if (T > 0 && (!logits || !ids)) return FP8MOE_EINVAL;
+  if (!aligned16(logits) || !aligned4(ids)) return FP8MOE_EALIGN;
+  RouterArgs a = {};
+  a.logits = logits, a.given = ids, a.offsets = seq_offsets;
+  a.T = T, a.E = E, a.k = topk, a.B = B, a.f32 = type == FP8MOE_TYPE_F32;
+  a.sig = score == FP8MOE_SCORE_SIGMOID;
+  rc = set_balance(a, counts, loss, slope, workspace, workspace_bytes);
+  if (rc) return rc;
+  int sms = 0;
+  rc = device_init(&sms);
+  if (rc) return rc;
+  const cudaError_t e = fp8moe_launch_router(a, stream);
+  return e == cudaSuccess ? FP8MOE_OK : cuda_fail(e);
+}
+
+int fp8moe_router_bwd(const float* dweights, const void* logits, const int32_t* ids, int64_t T,
+                      int32_t E, int32_t type, int32_t score, int32_t topk, int32_t normalize,
+                      float scale, const float* dloss, const float* slope,
+                      const int32_t* seq_offsets, int32_t B, void* dlogits,
+                      fp8moe_stream_t stream) {
+  int rc = check_router(T, E, type, score, topk, seq_offsets, B);
+  if (rc) return rc;
+  if (normalize != 0 && normalize != 1) return FP8MOE_EINVAL;
+  if ((dloss != nullptr) != (slope != nullptr)) return FP8MOE_EINVAL;
+  if (T == 0) return FP8MOE_OK;
+  if (!logits || !ids || !dlogits) return FP8MOE_EINVAL;
+  if (!aligned16(logits) || !aligned16(dlogits) || !aligned16(slope) || !aligned4(ids) ||
+      !aligned4(dweights) || !aligned4(dloss))
+    return FP8MOE_EALIGN;
+  int sms = 0;
+  rc = device_init(&sms);
+  if (rc) return rc;
+  RouterBwdArgs a = {logits, ids, dweights, seq_offsets, dloss, slope, dlogits, T, E, topk, B,
+                     type == FP8MOE_TYPE_F32, score == FP8MOE_SCORE_SIGMOID, normalize, scale};
+  const cudaError_t e = fp8moe_launch_router_bwd(a, stream);
+  return e == cudaSuccess ? FP8MOE_OK : cuda_fail(e);
+}
+
+size_t fp8moe_adamw_workspace_size(const fp8moe_adamw_tensor* tensors, int32_t count,
+                                   int32_t on_device) {
+  return tensors && count > 0 ? adamw_ws_bytes(tensors, count, on_device != 0) : 0;
+}
+
+int fp8moe_adamw_step(const fp8moe_adamw_tensor* tensors, int32_t count, int64_t step,
+                      const int64_t* step_dev, double lr, const float* lr_dev, double beta1,
+                      double beta2, double eps, const float* grad_scale, uint32_t seed,
+                      void* workspace, size_t workspace_bytes, fp8moe_stream_t stream) {
+  if (count < 0 || (count > 0 && !tensors)) return FP8MOE_EINVAL;
+  if (!step_dev && step < 1) return FP8MOE_EINVAL;
+  if (!(beta1 >= 0.0 && beta1 < 1.0 && beta2 >= 0.0 && beta2 < 1.0 && eps >= 0.0) ||
+      (!lr_dev && !(lr == lr)))
+    return FP8MOE_EINVAL;
+  if (!aligned4(grad_scale) || !aligned4(lr_dev) || (reinterpret_cast<uintptr_t>(step_dev) & 7u))
+    return FP8MOE_EALIGN;
+  bool any = false;
+  for (int32_t i = 0; i < count; ++i) {
+    const int rc = check_adamw(tensors[i]);
+    if (rc) return rc;
+    any |= tensors[i].n > 0;
+  }
+  if (!any) return FP8MOE_OK;
+  const bool on_device = step_dev || lr_dev;
+  const size_t need = adamw_ws_bytes(tensors, count, on_device);
+  if (need) {
+    if (!workspace) return FP8MOE_EWORKSPACE;
+    if (reinterpret_cast<uintptr_t>(workspace) & 255u) return FP8MOE_EALIGN;
+    if (workspace_bytes < need) return FP8MOE_EWORKSPACE;
+  }
+  int sms = 0;
+  int rc = device_init(&sms);
+  if (rc) return rc;
+
+  AdamwRates* rates = on_device ? static_cast<AdamwRates*>(workspace) : nullptr;
+  uint32_t* most = need ? reinterpret_cast<uint32_t*>(static_cast<uint8_t*>(workspace) +
+                                                      kAdamwRatesBytes)
+                        : nullptr;
+  cudaError_t e = cudaSuccess;
+  if (need) {
+    e = fp8moe_launch_adamw_prepare(rates, step_dev, step, lr_dev, lr, beta1, beta2, seed, most,
+                                    (int64_t)((need - kAdamwRatesBytes) / 4), stream);
+    if (e != cudaSuccess) return cuda_fail(e);
+  }
+  AdamwCommon c = {};
+  c.rates = rates;
+  c.grad_scale = grad_scale;
+  if (!on_device) {
+    c.rate = (float)(lr / (1.0 - pow(beta1, (double)step)));
+    c.root = (float)(1.0 / sqrt(1.0 - pow(beta2, (double)step)));
+    c.key = seed + 0x6A09E667u * (uint32_t)step;
+  }
+  c.b1 = (float)beta1, c.c1 = (float)(1.0 - beta1);
+  c.b2 = (float)beta2, c.c2 = (float)(1.0 - beta2);
+  c.eps = (float)eps;
+
+  // as many launches as tables: 256 tensors or 2^30 units each
+  AdamwEntry at[kAdamwEntries];
+  int n = 0;
+  uint64_t units = 0;
+  uint32_t* columns = most;
+  for (int32_t i = 0; i < count; ++i) {
+    const fp8moe_adamw_tensor& d = tensors[i];
+    if (d.n == 0) continue;
+    AdamwEntry w = {};
+    w.p = d.p, w.g = d.g, w.m = d.m, w.v = d.v, w.m_scale = d.m_scale, w.v_scale = d.v_scale;
+    w.copy = d.copy, w.n = d.n, w.weight_decay = d.weight_decay;
+    w.keep = (float)(1.0 - lr * d.weight_decay);
+    w.which = (uint32_t)i;
+    w.g_bf16 = d.g_type == FP8MOE_TYPE_BF16, w.bits = (uint8_t)d.state_bits;
+    w.vec = aligned16(d.p) && aligned16(d.g) && aligned16(d.m) && aligned16(d.v) &&
+            aligned16(d.copy);
+    // a block of an 8-bit moment has to lie in one row of a tile
+    w.tiles = d.codes && w.vec && (d.state_bits == 32 || d.N % 128 == 0);
+    if (d.codes) {
+      w.K = (int32_t)d.K, w.N = (int32_t)d.N;
+      w.most = columns;
+      columns += adamw_columns(d);
+    }
+    const uint64_t more = fp8moe_adamw_units(w);
+    if (n == kAdamwEntries || (n > 0 && units + more > (1u << 30))) {
+      e = fp8moe_launch_adamw(c, at, n, stream);
+      if (e != cudaSuccess) return cuda_fail(e);
+      n = 0, units = 0;
+    }
+    at[n++] = w;
+    units += more;
+  }
+  e = fp8moe_launch_adamw(c, at, n, stream);
+  if (e != cudaSuccess) return cuda_fail(e);
+  columns = most;
+  for (int32_t i = 0; i < count; ++i) {
+    const fp8moe_adamw_tensor& d = tensors[i];
+    if (d.n == 0 || !d.codes) continue;
+    const bool vec = aligned16(d.p) && aligned16(d.codes);
+    const bool tiles = aligned16(d.p) && aligned16(d.g) && aligned16(d.m) && aligned16(d.v) &&
+                       aligned16(d.copy) && (d.state_bits == 32 || d.N % 128 == 0);
+    e = fp8moe_launch_weight_codes(d.p, (int)(d.n / (d.K * d.N)), (int)d.K, (int)d.N, vec, tiles,
+                                   columns, d.codes, d.code_scale, stream);
+    if (e != cudaSuccess) return cuda_fail(e);
+    columns += adamw_columns(d);
+  }
+  return FP8MOE_OK;
 }
 
 int fp8moe_read_status(fp8moe_stream_t stream, uint32_t* flags) {

@@ -15,6 +15,7 @@ constexpr uint32_t kStatusGroupsExceedM = 1u << 1;
 constexpr uint32_t kStatusWaitTimeout = 1u << 2;
 constexpr uint32_t kStatusTooManySegments = 1u << 3;
 constexpr uint32_t kStatusBadExpert = 1u << 4;
+constexpr uint32_t kStatusBadOffsets = 1u << 5;
 // bits [8, 16) name the wait that timed out
 constexpr uint32_t kWhereProducer = 1u << 8;
 constexpr uint32_t kWhereMma = 2u << 8;

@@ -187,3 +187,85 @@ struct GmmMxfp4Args {
 void fp8moe_gmm_mxfp4_boxes(int rows[3], int* scale_rows);
 cudaError_t fp8moe_launch_gmm_mxfp4(const GmmMxfp4Args& a, int num_sms, cudaStream_t s);
 cudaError_t fp8moe_status_take_gmm_mxfp4(uint32_t** word);
+
+// The router (router.cu). given: the choices, made elsewhere (null: chosen here, into ids and
+// weights). part_*: the parts of the balance sums, (chunks + B) rows (null: no balance).
+struct RouterArgs {
+  const void* logits;
+  const int32_t* given;
+  const float* bias;
+  int32_t* ids;
+  float* weights;
+  const int32_t* offsets;   // [B + 1], or null: one sequence
+  float* part_share;
+  int32_t* part_count;
+  int32_t* part_tokens;
+  int32_t* counts;
+  float* loss;
+  float* slope;
+  int64_t T;
+  int E, k, B, f32, sig, normalize;
+  float scale;
+  int chunk;                // set by the launcher
+};
+// Tokens of a CTA, whose balance sums are one part for each sequence among them.
+int fp8moe_balance_chunk(int64_t T);
+cudaError_t fp8moe_launch_router(const RouterArgs& a, cudaStream_t s);
+
+struct RouterBwdArgs {
+  const void* logits;
+  const int32_t* ids;
+  const float* dweights;    // null: only the balance loss
+  const int32_t* offsets;
+  const float* dloss;       // null: only the weights
+  const float* slope;
+  void* dlogits;
+  int64_t T;
+  int E, k, B, f32, sig, normalize;
+  float scale;
+};
+cudaError_t fp8moe_launch_router_bwd(const RouterBwdArgs& a, cudaStream_t s);
+cudaError_t fp8moe_status_take_router(uint32_t** word);
+
+// AdamW (adamw.cu): a tensor in a launch's table.
+struct AdamwEntry {
+  float* p;
+  const void* g;
+  void* m;
+  void* v;
+  float* m_scale;
+  float* v_scale;
+  void* copy;               // bf16, or null
+  uint32_t* most;           // tiles: [E, N], the columns' largest magnitudes (by atomicMax)
+  int64_t n;
+  double weight_decay;
+  float keep;               // 1 - lr * weight_decay, unless the rates are on the device
+  uint32_t first_unit;      // set by the launcher
+  uint32_t which;           // the tensor's number in the call
+  int32_t K, N;             // tiles: weights [E, K, N]
+  uint8_t g_bf16, bits, vec, tiles;
+};
+struct AdamwRates {         // from a step or a rate on the device
+  double lr;
+  float rate, root;
+  uint32_t key;
+};
+struct AdamwCommon {
+  const AdamwRates* rates;  // null: the values below
+  const float* grad_scale;
+  float rate, root, b1, c1, b2, c2, eps;
+  uint32_t key;
+  int count;
+};
+constexpr int kAdamwEntries = 256;
+uint64_t fp8moe_adamw_units(const AdamwEntry& d);
+cudaError_t fp8moe_launch_adamw(const AdamwCommon& common, AdamwEntry* at, int count,
+                                cudaStream_t s);
+cudaError_t fp8moe_launch_adamw_prepare(AdamwRates* rates, const int64_t* step, int64_t host_step,
+                                        const float* lr, double host_lr, double beta1,
+                                        double beta2, uint32_t seed, uint32_t* most, int64_t count,
+                                        cudaStream_t s);
+// have_most: the step has left the columns' largest magnitudes; else they are taken here.
+cudaError_t fp8moe_launch_weight_codes(const float* p, int E, int K, int N, bool vec, bool have_most,
+                                       uint32_t* most, uint8_t* codes, float* scale,
+                                       cudaStream_t s);

@@ -1,0 +1,553 @@
+// router.cu -- the router's choice of experts with its weights, the balance loss with the
+// experts' counts, and the gradient of both into the logits.
+//
+//   s = softmax(x) or sigmoid(x) over a token's E logits;  chosen: the topk largest of x, or,
+//   with a bias b, of s + b;  weight: scale * s / (sum of the chosen s), or scale * s
+//   share p_i = s_i / sum s;  for a sequence of n tokens with C choices, c_i of them expert i:
+//   loss = sum_i slope_i * sum_t p_ti,  slope_i = E c_i / (C n)
+//
+// A warp takes a token: lane l holds experts [l V, l V + V) in registers, so that one pass over
+// the logits gives the maximum, the sum, the choice and the shares.
+#include <cmath>
+#include <cstdint>
+#include <type_traits>
+#include <cuda_runtime.h>
+#include <cuda_bf16.h>
+
+#include "fp8moe_status.cuh"
+#include "kernels.h"
+#include "pdl.cuh"
+#include "ptx.cuh"
+#include "router.cuh"
+
+namespace fp8moe {
+namespace {
+
+constexpr int kWarps = 8;
+constexpr int kThreads = 32 * kWarps;
+constexpr int kJoinThreads = 1024;
+
+// Ascending with the value; a NaN is the largest, -inf is no candidate (0).
+__device__ __forceinline__ uint32_t order_key(float v) {
+  if (v != v) return 0xffffffffu;
+  const uint32_t u = __float_as_uint(v + 0.0f);              // -0 is 0
+  if (u == 0xff800000u) return 0u;
+  return u ^ ((uint32_t)((int32_t)u >> 31) | 0x80000000u);
+}
+
+// What decides the choice, in f32: the logit, or score + bias (-inf stays out either way).
+__device__ __forceinline__ float choice_value(float x, float b, bool has_bias, bool sig, float top,
+                                              float inv_sum) {
+  if (!has_bias) return x;
+  if (x == -INFINITY) return x;
+  return __fadd_rn(sig ? sigmoid(x) : __fmul_rn(expf(x - top), inv_sum), b);
+}
+__device__ __forceinline__ double choice_value_64(float x, float b, bool has_bias, bool sig,
+                                                  float top, double sum) {
+  if (!has_bias) return (double)x;
+  const double s = sig ? 1.0 / (1.0 + exp(-(double)x)) : exp((double)x - (double)top) / sum;
+  return s + (double)b;
+}
+
+// The choice in 64 bits, among the experts whose f32 value is at least `cut`: lane j's j-th
+// expert (-1 for none). For the few tokens on which 32 bits leave the order open.
+template <typename T>
+__device__ __noinline__ int choose_exactly(const T* row, const float* bias, int E, int k, bool sig,
+                                           float top, float inv_sum, float cut, uint16_t* list) {
+  const int lane = threadIdx.x & 31;
+  const bool has_bias = bias != nullptr;
+  double sum = 0.0;
+  int n = 0;
+  for (int base = 0; base < E; base += 32) {
+    const int e = base + lane;
+    const float x = e < E ? load_f32(row + e) : -INFINITY;
+    const float b = has_bias && e < E ? bias[e] : 0.0f;
+    if (has_bias && !sig && e < E) sum += exp((double)x - (double)top);
+    const float c = choice_value(x, b, has_bias, sig, top, inv_sum);
+    const bool in = e < E && order_key(c) != 0u && !(c < cut);
+    const uint32_t who = __ballot_sync(kAllLanes, in);
+    if (in) list[n + __popc(who & ((1u << lane) - 1u))] = (uint16_t)e;
+    n += __popc(who);
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(kAllLanes, sum, o);
+  __syncwarp();
+  constexpr int kTaken = 0xffff;
+  // a NaN counts as the largest, as in order_key
+  auto value = [&](int e) {
+    const double v = choice_value_64(load_f32(row + e), has_bias ? bias[e] : 0.0f, has_bias, sig,
+                                     top, sum);
+    return v != v ? (double)INFINITY : v;
+  };
+  const double first = lane < n ? value(list[lane]) : -(double)INFINITY;
+  int mine = -1;
+  for (int j = 0; j < k; ++j) {
+    double best = -(double)INFINITY;
+    int expert = kTaken, place = -1;
+    for (int i = lane; i < n; i += 32) {
+      const int e = list[i];
+      if (e == kTaken) continue;
+      const double v = i == lane ? first : value(e);
+      if (place < 0 || v > best) best = v, expert = e, place = i;
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+      const double v = __shfl_xor_sync(kAllLanes, best, o);
+      const int e = __shfl_xor_sync(kAllLanes, expert, o);
+      const int at = __shfl_xor_sync(kAllLanes, place, o);
+      if (at >= 0 && (place < 0 || v > best || (v == best && e < expert)))
+        best = v, expert = e, place = at;
+    }
+    if (place < 0) break;
+    if (lane == j) mine = expert;
+    if (lane == 0) list[place] = kTaken;
+    __syncwarp();
+  }
+  return mine;
+}
+
+template <typename T, int V, bool VECT, bool GIVEN>
+__global__ void __launch_bounds__(kThreads) router_kernel(const __grid_constant__ RouterArgs a) {
+  extern __shared__ float s_mem[];
+  float* s_share = s_mem;                                           // [kWarps][32 V]
+  int32_t* s_count = reinterpret_cast<int32_t*>(s_mem + kWarps * 32 * V);   // [32 V]
+  __shared__ int32_t s_tokens[kWarps];
+  pdl_launch_dependents();
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int E = a.E, k = a.k;
+  const bool sig = a.sig, has_bias = !GIVEN && a.bias != nullptr;
+  const T* logits = static_cast<const T*>(a.logits);
+  const bool balance = a.part_share != nullptr;
+  uint16_t* list = reinterpret_cast<uint16_t*>(s_mem) + warp * 32 * V;
+
+  float acc[V];
+  int tokens = 0;
+
+  auto token = [&](int64_t t) {
+    const T* row = logits + t * E;
+    float x[V];
+    load_row<T, V, VECT>(row, E, lane, -INFINITY, x);
+    int id = -1;
+    if (GIVEN && lane < k) id = a.given[t * k + lane];
+    float largest = x[0];
+#pragma unroll
+    for (int j = 1; j < V; ++j) largest = max_nan(largest, x[j]);
+    largest = warp_max(largest);
+    const float top = scale_top(largest, sig);
+    const bool none = largest == -INFINITY;
+
+    // the scores, where shares, unnormalised weights or a bias ask for them
+    float n[V], sum = 0.0f;
+    if (balance || (!GIVEN && !sig && (has_bias || !a.normalize))) {
+#pragma unroll
+      for (int j = 0; j < V; ++j) {
+        n[j] = none ? 0.0f : scaled_score(x[j], top, sig);
+        sum += n[j];
+      }
+      sum = warp_sum(sum);
+    }
+    const float inv_sum = none ? 0.0f : __frcp_rn(sum);
+
+    if constexpr (!GIVEN) {
+      // keys: the value's upper 22 bits of order, then the expert, the lowest first; they
+      // differ from each other, so that the largest of a warp names its expert
+      uint32_t key[V];
+      float c[V];
+#pragma unroll
+      for (int j = 0; j < V; ++j) {
+        const int e = lane * V + j;
+        const float b = has_bias && e < E ? a.bias[e] : 0.0f;
+        c[j] = choice_value(x[j], b, has_bias, sig, top, inv_sum);
+        const uint32_t o = order_key(c[j]);
+        key[j] = o == 0u ? 0u : (o & ~1023u) | (uint32_t)(1023 - e);
+      }
+      uint32_t mine = 0;
+      int chosen = 0;
+      for (; chosen < k; ++chosen) {
+        uint32_t m = key[0];
+#pragma unroll
+        for (int j = 1; j < V; ++j) m = max(m, key[j]);
+        m = __reduce_max_sync(kAllLanes, m);
+        if (m == 0u) break;
+#pragma unroll
+        for (int j = 0; j < V; ++j) key[j] = key[j] == m ? 0u : key[j];
+        if (lane == chosen) mine = m;
+      }
+      if (mine) id = 1023 - (int)(mine & 1023u);
+      float xc = id >= 0 ? load_f32(row + id) : -INFINITY;
+
+      // Is the order settled? Values whose upper bits agree, and with a bias those within twice
+      // the error of a score, may stand in the wrong order, or out of place behind the last one.
+      // (With a bias: 8 * 2^-24 of a sigmoid at most 1; of a softmax score the argument's
+      // rounding, at most .4 of the largest score, and the sum's of 37 terms; the sum with
+      // the bias adds half a unit.)
+      const float b = has_bias && id >= 0 ? a.bias[id] : 0.0f;
+      const float cc = id >= 0 ? choice_value(xc, b, has_bias, sig, top, inv_sum) : INFINITY;
+      const float largest_c = fabsf(__shfl_sync(kAllLanes, cc, 0));
+      float least = cc;
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) least = fminf(least, __shfl_xor_sync(kAllLanes, least, o));
+      const float slack = !has_bias ? 0.0f
+          : (sig ? 0x1p-20f : 0x1p-17f * inv_sum) + 0x1p-22f * fmaxf(largest_c, fabsf(least));
+      const float next_c = __shfl_down_sync(kAllLanes, cc, 1);
+      const float next_x = __shfl_down_sync(kAllLanes, xc, 1);
+      const float next_b = __shfl_down_sync(kAllLanes, b, 1);
+      bool open = lane + 1 < chosen &&
+                  (has_bias ? !(cc - next_c > slack) && !(xc == next_x && b == next_b)
+                            : cc < next_c);
+      const float cut = least - slack;
+      const int last = __ffs(__ballot_sync(kAllLanes, cc == least)) - 1;   // -1: all NaN
+      const float last_x = __shfl_sync(kAllLanes, xc, last & 31);
+      const float last_b = __shfl_sync(kAllLanes, b, last & 31);
+#pragma unroll
+      for (int j = 0; j < V; ++j) {
+        if (key[j] == 0u) continue;
+        if (!has_bias) open |= c[j] > least;
+        else if (c[j] >= cut) open |= x[j] != last_x || a.bias[lane * V + j] != last_b;
+      }
+      if (__any_sync(kAllLanes, open)) {
+        id = choose_exactly(row, a.bias, E, k, sig, top, inv_sum, cut, list);
+        xc = id >= 0 ? load_f32(row + id) : -INFINITY;
+        __syncwarp();
+      }
+
+      float w = 0.0f;
+      if (a.normalize) {
+        const float most = warp_max(xc);
+        const float nc = id >= 0 ? scaled_score(xc, scale_top(most, sig), sig) : 0.0f;
+        w = nc / warp_sum(nc);
+      } else if (id >= 0) {
+        w = sig ? sigmoid(xc) : expf(xc - top) * inv_sum;
+      }
+      if (largest != largest) w = largest;       // a NaN among the logits, chosen or not
+      if (lane < k) {
+        a.ids[t * k + lane] = id;
+        a.weights[t * k + lane] = id >= 0 ? a.scale * w : 0.0f;
+      }
+    }
+    if (!balance) return;
+    if (GIVEN && id >= E) {
+      status_set(kStatusBadExpert);
+      id = -1;
+    }
+    if (!__any_sync(kAllLanes, id >= 0)) return;
+    if (id >= 0) atomicAdd(&s_count[id], 1);
+    ++tokens;
+#pragma unroll
+    for (int j = 0; j < V; ++j) acc[j] += n[j] * inv_sum;
+  };
+  auto clear = [&]() {
+    tokens = 0;
+#pragma unroll
+    for (int j = 0; j < V; ++j) acc[j] = 0.0f;
+    if (balance) {
+      for (int i = threadIdx.x; i < 32 * V; i += kThreads) s_count[i] = 0;
+      __syncthreads();
+    }
+  };
+  // the sums of this CTA's tokens of one sequence, added up in the order of the warps
+  auto flush = [&](int64_t slot) {
+    if (!balance) return;
+    __syncthreads();
+#pragma unroll
+    for (int j = 0; j < V; ++j) s_share[warp * 32 * V + j * 32 + lane] = acc[j];
+    if (lane == 0) s_tokens[warp] = tokens;
+    __syncthreads();
+    for (int i = threadIdx.x; i < 32 * V; i += kThreads) {
+      const int e = (i & 31) * V + (i >> 5);
+      if (e >= E) continue;
+      float sum = 0.0f;
+#pragma unroll
+      for (int w = 0; w < kWarps; ++w) sum += s_share[w * 32 * V + i];
+      a.part_share[slot * E + e] = sum;
+      a.part_count[slot * E + e] = s_count[e];
+    }
+    if (threadIdx.x == 0) {
+      int n = 0;
+      for (int w = 0; w < kWarps; ++w) n += s_tokens[w];
+      a.part_tokens[slot] = n;
+    }
+    __syncthreads();
+  };
+  auto padding = [&](int64_t from, int64_t to) {
+    if constexpr (!GIVEN) {
+      for (int64_t i = from * k + threadIdx.x; i < to * k; i += kThreads) {
+        a.ids[i] = -1;
+        a.weights[i] = 0.0f;
+      }
+    }
+  };
+
+  const int64_t begin = (int64_t)blockIdx.x * a.chunk;
+  const int64_t end = begin + a.chunk < a.T ? begin + a.chunk : a.T;
+  if (a.offsets == nullptr) {
+    clear();
+    for (int64_t t = begin + warp; t < end; t += kWarps) token(t);
+    flush(blockIdx.x);
+    return;
+  }
+  int64_t at = max(begin, min((int64_t)a.offsets[0], end));
+  padding(begin, at);
+  // one run of tokens after the other: of each sequence that has a part in this chunk
+  int b = at < end ? max(0, find_sequence(a.offsets, a.B, at)) : a.B;
+  for (; at < end && b < a.B; ++b) {
+    const int64_t stop = min((int64_t)a.offsets[b + 1], end);
+    if (stop <= at) continue;
+    clear();
+    for (int64_t t = at + warp; t < stop; t += kWarps) token(t);
+    flush((int64_t)blockIdx.x + b);
+    at = stop;
+  }
+  padding(at, end);
+}
+
+// Adds up a sequence's parts in a fixed order: counts, slope and loss. One CTA a sequence;
+// thread t has column t % width and every (1024 / width)-th part.
+__global__ void __launch_bounds__(kJoinThreads) balance_join_kernel(const int32_t* offsets, int64_t T,
+                                                         int B, int E, int width, int chunk,
+                                                         const float* part_share,
+                                                         const int32_t* part_count,
+                                                         const int32_t* part_tokens,
+                                                         int32_t* counts, float* loss,
+                                                         float* slope) {
+  __shared__ float s_share[kJoinThreads];
+  __shared__ int32_t s_count[kJoinThreads];
+  __shared__ int32_t s_chosen[32], s_tokens[32];
+  __shared__ float s_loss[32];
+  const int b = blockIdx.x, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int e = tid % width, groups = kJoinThreads / width;
+  int64_t first = 0, last = T;
+  if (offsets != nullptr) {
+    const int64_t o0 = offsets[b], o1 = offsets[b + 1];
+    if (tid == 0 && (o0 < 0 || o1 < o0 || o1 > T)) status_set(kStatusBadOffsets);
+    first = min(max(o0, (int64_t)0), T);
+    last = min(max(o1, first), T);
+  }
+  const int64_t s0 = first / chunk + b, s1 = last > first ? (last - 1) / chunk + b + 1 : s0;
+  pdl_wait();
+  float share = 0.0f;
+  int32_t count = 0, tokens = 0;
+  if (e < E) {
+#pragma unroll 4
+    for (int64_t s = s0 + tid / width; s < s1; s += groups) {
+      share += part_share[s * E + e];
+      count += part_count[s * E + e];
+    }
+  }
+  for (int64_t s = s0 + tid; s < s1; s += kJoinThreads) tokens += part_tokens[s];
+  s_share[tid] = share;
+  s_count[tid] = count;
+  const int32_t chosen = __reduce_add_sync(kAllLanes, count);
+  tokens = __reduce_add_sync(kAllLanes, tokens);
+  if (lane == 0) s_chosen[warp] = chosen, s_tokens[warp] = tokens;
+  __syncthreads();
+  const float C = (float)__reduce_add_sync(kAllLanes, s_chosen[lane]);
+  const float n = (float)__reduce_add_sync(kAllLanes, s_tokens[lane]);
+  float part = 0.0f;
+  if (tid < width && e < E) {
+    for (int g = 1; g < groups; ++g) {
+      share += s_share[g * width + e];
+      count += s_count[g * width + e];
+    }
+    const float d = C > 0.0f ? (float)count * (float)E / C / n : 0.0f;
+    counts[(int64_t)b * E + e] = count;
+    slope[(int64_t)b * E + e] = d;
+    part = d * share;
+  }
+  part = warp_sum(part);
+  if (lane == 0) s_loss[warp] = part;
+  __syncthreads();
+  if (warp == 0) {
+    const float all = warp_sum(s_loss[lane]);
+    if (lane == 0) loss[b] = all;
+  }
+}
+
+// dx = q * (w (dw - sum dw w) + p (D - sum D p)),  q = 1 (softmax) or sigmoid(-x),
+// D = dloss * slope. Weights that are not normalised: of softmax scores their gradient joins
+// D, of sigmoid scores it is dw s.
+template <typename T, int V, bool VECT>
+__global__ void __launch_bounds__(kThreads) router_bwd_kernel(
+    const __grid_constant__ RouterBwdArgs a) {
+  extern __shared__ float s_mem[];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  float* s_row = s_mem + warp * 32 * V;
+  const int E = a.E, k = a.k;
+  const bool sig = a.sig;
+  const int64_t t = (int64_t)blockIdx.x * kWarps + warp;
+  if (t >= a.T) return;
+  const T* row = static_cast<const T*>(a.logits) + t * E;
+  T* out = static_cast<T*>(a.dlogits) + t * E;
+  float x[V], dx[V];
+  load_row<T, V, VECT>(row, E, lane, -INFINITY, x);
+  int id = lane < k ? a.ids[t * k + lane] : -1;
+  if (id >= E) {
+    status_set(kStatusBadExpert);
+    id = -1;
+  }
+  const float dw = a.dweights != nullptr && id >= 0 ? a.scale * a.dweights[t * k + lane] : 0.0f;
+  int b = 0;
+  if (a.offsets != nullptr) b = find_sequence(a.offsets, a.B, t);
+  float largest = x[0];
+#pragma unroll
+  for (int j = 1; j < V; ++j) largest = max_nan(largest, x[j]);
+  largest = warp_max(largest);
+  // nothing was chosen for this token: padding, or no expert was left
+  if (b < 0 || b >= a.B || largest == -INFINITY || !__any_sync(kAllLanes, id >= 0)) {
+#pragma unroll
+    for (int j = 0; j < V; ++j) dx[j] = 0.0f;
+    store_row<T, V, VECT>(out, E, lane, dx);
+    return;
+  }
+  const float xc = id >= 0 ? load_f32(row + id) : -INFINITY;
+  const float top = scale_top(largest, sig);
+#pragma unroll
+  for (int j = 0; j < V; ++j) s_row[j * 32 + lane] = 0.0f;
+  __syncwarp();
+
+  // each choice's part, put to its expert
+  float part = 0.0f;
+  const bool joins = !a.normalize && !sig;
+  if (a.normalize) {
+    const float most = warp_max(xc);
+    const float nc = id >= 0 && xc != -INFINITY ? scaled_score(xc, scale_top(most, sig), sig) : 0.0f;
+    const float total = largest != largest ? largest : warp_sum(nc);
+    const float w = total > 0.0f || total != total ? nc / total : 0.0f;
+    part = w * (dw - warp_sum(dw * w));
+  } else {
+    part = joins ? dw : dw * sigmoid(xc);
+  }
+  const int place = id >= 0 ? (id % V) * 32 + id / V : -1 - lane;
+  const bool alone = __match_any_sync(kAllLanes, place) == (1u << lane);
+  if (__all_sync(kAllLanes, alone)) {
+    if (id >= 0) s_row[place] = part;
+  } else {                                    // an expert twice: in the order of the choices
+    for (int j = 0; j < k; ++j) {
+      if (lane == j && id >= 0) s_row[place] += part;
+      __syncwarp();
+    }
+  }
+  __syncwarp();
+
+  float p[V], sum = 0.0f;
+#pragma unroll
+  for (int j = 0; j < V; ++j) {
+    dx[j] = s_row[j * 32 + lane];
+    p[j] = scaled_score(x[j], top, sig);
+    sum += p[j];
+  }
+  if (a.dloss != nullptr || joins) {
+    const float inv_sum = __frcp_rn(warp_sum(sum));
+    float D[V], dot = 0.0f;
+    if (a.dloss != nullptr) {
+      load_row<float, V, VECT>(a.slope + (int64_t)b * E, E, lane, 0.0f, D);
+      const float dl = a.dloss[b];
+#pragma unroll
+      for (int j = 0; j < V; ++j) D[j] *= dl;
+    } else {
+#pragma unroll
+      for (int j = 0; j < V; ++j) D[j] = 0.0f;
+    }
+#pragma unroll
+    for (int j = 0; j < V; ++j) {
+      if (joins) D[j] += dx[j], dx[j] = 0.0f;
+      p[j] *= inv_sum;
+      dot += D[j] * p[j];
+    }
+    dot = warp_sum(dot);
+#pragma unroll
+    for (int j = 0; j < V; ++j) dx[j] += p[j] * (D[j] - dot);
+  }
+  if (sig) {
+#pragma unroll
+    for (int j = 0; j < V; ++j) dx[j] *= sigmoid(-x[j]);
+  }
+  store_row<T, V, VECT>(out, E, lane, dx);
+}
+
+// Rows of whole pieces for 16-byte accesses (load_row); V: experts of a lane.
+template <typename T>
+bool whole_pieces(int E, int V) {
+  const int values = (V * (int)sizeof(T) < 16 ? V * (int)sizeof(T) : 16) / (int)sizeof(T);
+  return E % values == 0;
+}
+
+template <typename F>
+cudaError_t with_width(int E, F f) {
+  if (E <= 64) return f(std::integral_constant<int, 2>());
+  if (E <= 128) return f(std::integral_constant<int, 4>());
+  if (E <= 256) return f(std::integral_constant<int, 8>());
+  if (E <= 512) return f(std::integral_constant<int, 16>());
+  return f(std::integral_constant<int, 32>());
+}
+
+template <typename T, bool GIVEN>
+cudaError_t launch_router(const RouterArgs& a, cudaStream_t s) {
+  const int64_t grid = (a.T + a.chunk - 1) / a.chunk;
+  return with_width(a.E, [&](auto width) {
+    constexpr int V = decltype(width)::value;
+    const size_t smem = (size_t)(kWarps + 1) * 32 * V * sizeof(float);
+    if (whole_pieces<T>(a.E, V))
+      router_kernel<T, V, true, GIVEN><<<(unsigned)grid, kThreads, smem, s>>>(a);
+    else
+      router_kernel<T, V, false, GIVEN><<<(unsigned)grid, kThreads, smem, s>>>(a);
+    return cudaGetLastError();
+  });
+}
+
+}  // namespace
+}  // namespace fp8moe
+
+using namespace fp8moe;
+
+FP8MOE_DEFINE_STATUS_TAKE(fp8moe_status_take_router)
+
+int fp8moe_balance_chunk(int64_t T) {
+  const int64_t c = (T / 304 + kWarps - 1) / kWarps * kWarps;
+  return (int)(c < kWarps ? kWarps : c > 128 ? 128 : c);
+}
+
+cudaError_t fp8moe_launch_router(const RouterArgs& args, cudaStream_t s) {
+  RouterArgs a = args;
+  const bool balance = a.part_share != nullptr;
+  a.chunk = balance ? fp8moe_balance_chunk(a.T) : kWarps;
+  cudaError_t e = cudaSuccess;
+  if (a.T > 0) {
+    if (a.given != nullptr)
+      e = a.f32 ? launch_router<float, true>(a, s) : launch_router<__nv_bfloat16, true>(a, s);
+    else
+      e = a.f32 ? launch_router<float, false>(a, s) : launch_router<__nv_bfloat16, false>(a, s);
+  }
+  if (e != cudaSuccess || !balance) return e;
+  int width = 32;
+  while (width < a.E) width *= 2;
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute attr[1];
+  pdl_attribute(attr[0]);
+  cfg.gridDim = dim3((unsigned)a.B);
+  cfg.blockDim = dim3(kJoinThreads);
+  cfg.stream = s;
+  cfg.attrs = attr;
+  cfg.numAttrs = a.T > 0 ? 1 : 0;
+  return cudaLaunchKernelEx(&cfg, balance_join_kernel, a.offsets, a.T, a.B, a.E, width, a.chunk,
+                            (const float*)a.part_share, (const int32_t*)a.part_count,
+                            (const int32_t*)a.part_tokens, a.counts, a.loss, a.slope);
+}
+
+cudaError_t fp8moe_launch_router_bwd(const RouterBwdArgs& a, cudaStream_t s) {
+  const int64_t grid = (a.T + kWarps - 1) / kWarps;
+  auto launch = [&](auto type) {
+    using T = decltype(type);
+    return with_width(a.E, [&](auto width) {
+      constexpr int V = decltype(width)::value;
+      const size_t smem = (size_t)kWarps * 32 * V * sizeof(float);
+      // slope rows are f32: their pieces have to be whole, too
+      if (whole_pieces<T>(a.E, V) && whole_pieces<float>(a.E, V))
+        router_bwd_kernel<T, V, true><<<(unsigned)grid, kThreads, smem, s>>>(a);
+      else
+        router_bwd_kernel<T, V, false><<<(unsigned)grid, kThreads, smem, s>>>(a);
+      return cudaGetLastError();
+    });
+  };
+  return a.f32 ? launch(float()) : launch(__nv_bfloat16());
+}

@@ -1,0 +1,140 @@
+// router.cuh -- what the router's choice and its gradient share: a token's logits in a
+// warp's registers, and the experts' scores on a scale on which they cannot all vanish.
+#pragma once
+#include <cstdint>
+#include <cuda_runtime.h>
+#include <cuda_bf16.h>
+
+#include "ptx.cuh"
+
+namespace fp8moe {
+
+constexpr uint32_t kAllLanes = 0xffffffffu;
+
+__device__ __forceinline__ float load_f32(const float* p) { return *p; }
+__device__ __forceinline__ float load_f32(const __nv_bfloat16* p) { return __bfloat162float(*p); }
+
+// Lane l holds experts [l * V, l * V + V): the lowest expert is in the lowest lane. VECT: rows
+// of whole 16-byte pieces (or of whole lanes, where a lane has less). Past E: `fill`.
+template <typename T, int V, bool VECT>
+__device__ __forceinline__ void load_row(const T* row, int E, int lane, float fill, float (&x)[V]) {
+  const int e0 = lane * V;
+  if constexpr (!VECT) {
+#pragma unroll
+    for (int j = 0; j < V; ++j) x[j] = e0 + j < E ? load_f32(row + e0 + j) : fill;
+  } else {
+    constexpr int kWords = V * (int)sizeof(T) / 4;          // 32-bit words of a lane
+    constexpr int kPiece = kWords < 4 ? kWords : 4;         // of one load
+    constexpr int kValues = kPiece * 4 / (int)sizeof(T);
+#pragma unroll
+    for (int i = 0; i < kWords / kPiece; ++i) {
+      uint32_t w[kPiece];
+      const bool in = e0 + i * kValues < E;
+      const T* p = row + e0 + i * kValues;
+      if constexpr (kPiece == 4) {
+        const uint4 v = in ? *reinterpret_cast<const uint4*>(p) : make_uint4(0, 0, 0, 0);
+        w[0] = v.x, w[1] = v.y, w[2] = v.z, w[3] = v.w;
+      } else if constexpr (kPiece == 2) {
+        const uint2 v = in ? *reinterpret_cast<const uint2*>(p) : make_uint2(0, 0);
+        w[0] = v.x, w[1] = v.y;
+      } else {
+        w[0] = in ? *reinterpret_cast<const uint32_t*>(p) : 0;
+      }
+#pragma unroll
+      for (int j = 0; j < kPiece; ++j) {
+        if constexpr (sizeof(T) == 4) {
+          x[i * kValues + j] = in ? __uint_as_float(w[j]) : fill;
+        } else {
+          x[i * kValues + 2 * j] = in ? bf16lo_to_f32(w[j]) : fill;
+          x[i * kValues + 2 * j + 1] = in ? bf16hi_to_f32(w[j]) : fill;
+        }
+      }
+    }
+  }
+}
+
+template <typename T, int V, bool VECT>
+__device__ __forceinline__ void store_row(T* row, int E, int lane, const float (&x)[V]) {
+  const int e0 = lane * V;
+  if constexpr (!VECT) {
+#pragma unroll
+    for (int j = 0; j < V; ++j)
+      if (e0 + j < E) row[e0 + j] = T(x[j]);
+  } else {
+    constexpr int kWords = V * (int)sizeof(T) / 4;
+    constexpr int kPiece = kWords < 4 ? kWords : 4;
+    constexpr int kValues = kPiece * 4 / (int)sizeof(T);
+#pragma unroll
+    for (int i = 0; i < kWords / kPiece; ++i) {
+      uint32_t w[kPiece];
+#pragma unroll
+      for (int j = 0; j < kPiece; ++j) {
+        if constexpr (sizeof(T) == 4) w[j] = __float_as_uint(x[i * kValues + j]);
+        else w[j] = f32x2_to_bf16x2(x[i * kValues + 2 * j], x[i * kValues + 2 * j + 1]);
+      }
+      if (e0 + i * kValues >= E) continue;
+      T* p = row + e0 + i * kValues;
+      if constexpr (kPiece == 4) *reinterpret_cast<uint4*>(p) = make_uint4(w[0], w[1], w[2], w[3]);
+      else if constexpr (kPiece == 2) *reinterpret_cast<uint2*>(p) = make_uint2(w[0], w[1]);
+      else *reinterpret_cast<uint32_t*>(p) = w[0];
+    }
+  }
+}
+
+__device__ __forceinline__ float warp_sum(float v) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(kAllLanes, v, o);
+  return v;
+}
+// A NaN anywhere gives NaN.
+__device__ __forceinline__ float warp_max(float v) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) {
+    const float w = __shfl_xor_sync(kAllLanes, v, o);
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(v) : "f"(v), "f"(w));
+  }
+  return v;
+}
+__device__ __forceinline__ float max_nan(float a, float b) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
+}
+
+// sigmoid(x) without cancellation, by t = exp(-|x|): 1 / (1 + t) or t / (1 + t). Within
+// 4 * 2^-24 of it (expf 2 units, the sum, the reciprocal and the product half a unit each).
+__device__ __forceinline__ float sigmoid(float x) {
+  const float t = expf(-fabsf(x));
+  const float r = __frcp_rn(__fadd_rn(1.0f, t));
+  return x >= 0.0f ? r : x < 0.0f ? __fmul_rn(t, r) : x + r;   // NaN stays NaN
+}
+
+// A score on the row's scale, n(x) = score(x) * exp(-top): top = the largest logit, or, with
+// sigmoid scores, the largest one below zero (0 if there is one above). The scores themselves may
+// all round to zero (sigmoid below -104); their ratios, which is what weights and shares are,
+// do not depend on the scale, and the largest n is at least 1/2. Experts at -inf have 0.
+__device__ __forceinline__ float scaled_score(float x, float top, bool sig) {
+  if (!sig) return expf(x - top);
+  const float t = expf(-fabsf(x));
+  const float r = __frcp_rn(1.0f + t);
+  if (top == 0.0f) return x >= 0.0f ? r : x < 0.0f ? t * r : x + r;
+  return expf(x - top) * r;                  // top < 0, so every x is
+}
+__device__ __forceinline__ float scale_top(float largest, bool sig) {
+  return sig && largest > 0.0f ? 0.0f : largest;
+}
+
+// The sequence that token t belongs to, with offsets[b] <= t < offsets[b + 1] (the first b
+// with offsets[b + 1] > t); B behind the last one, -1 before the first.
+__device__ __forceinline__ int find_sequence(const int32_t* offsets, int B, int64_t t) {
+  if (t < offsets[0]) return -1;
+  int lo = 0, hi = B;
+  while (lo < hi) {
+    const int mid = (lo + hi) >> 1;
+    if (offsets[mid + 1] > t) hi = mid;
+    else lo = mid + 1;
+  }
+  return lo;
+}
+
+}  // namespace fp8moe

@@ -65,13 +65,20 @@ enum {
   FP8MOE_OP_GMM_FP8_FWD_BLOCK = 7,
   FP8MOE_OP_GMM_MXFP4_FWD = 8,
   FP8MOE_OP_GMM_SILU_MXFP4_FWD = 9,
-  FP8MOE_OP_NORM_BWD = 10        /* M = T rows, K = H columns; N and E unused */
+  FP8MOE_OP_NORM_BWD = 10,       /* M = T rows, K = H columns; N and E unused */
+  FP8MOE_OP_BALANCE = 11         /* M = T tokens, N = B sequences, E experts; K unused */
 };
 
 /* Element types of the rows that the token and norm operators move. */
 enum {
   FP8MOE_TYPE_BF16 = 0,
   FP8MOE_TYPE_F32 = 1
+};
+
+/* A router's scores (fp8moe_router_fwd). */
+enum {
+  FP8MOE_SCORE_SOFTMAX = 0,
+  FP8MOE_SCORE_SIGMOID = 1
 };
 
 /* What a block's gate is shared by (fp8moe_norm_fwd). */
@@ -95,6 +102,7 @@ enum {
 #define FP8MOE_STATUS_WAIT_TIMEOUT 0x4u      /* a kernel pipeline wait gave up; bits 8..15 say where */
 #define FP8MOE_STATUS_TOO_MANY_SEGMENTS 0x8u /* internal: segment bound exceeded */
 #define FP8MOE_STATUS_BAD_EXPERT 0x10u       /* an expert id >= E (its slot was dropped) */
+#define FP8MOE_STATUS_BAD_OFFSETS 0x20u      /* sequence offsets below 0, falling, or past T */
 
 /* Workspace bytes the operation needs for these sizes (0 if none); the
  * workspace pointer must be 256-byte aligned.  Depends on M, K, N, E only. */
@@ -429,6 +437,112 @@ int fp8moe_gmm_silu_mxfp4_fwd(const void* lhs, int64_t M, int64_t K, const uint8
                               const uint8_t* scales, int32_t E, int64_t N,
                               const int32_t* group_sizes, void* out, void* workspace,
                               size_t workspace_bytes, fp8moe_stream_t stream);
+
+/* ---- The router in front of the experts (no counterpart on the pages): the choice of experts
+ * with its weights, the balance loss with the experts' counts, and the gradient of both.
+ *
+ * logits: [T, E] of `type` (FP8MOE_TYPE_*), 1 <= E <= 1024, 1 <= topk <= min(32, E).
+ *   s      = softmax over the token's E logits, or sigmoid of each (`score`, FP8MOE_SCORE_*)
+ *   chosen = the topk experts with the largest logit, or, with bias f32 [E], with the largest
+ *            s + bias; equal ones by number. Values that f32 cannot tell apart are compared in
+ *            64 bits. An expert whose logit (or bias) is -inf is never chosen.
+ *   weights[t, j] = scale * s_j / (sum of the chosen s), or scale * s_j with normalize = 0
+ * The bias takes part in the choice alone. Slots without an expert have id -1 and weight 0, as
+ * have all slots of a token that belongs to no sequence; a NaN logit ranks first and spoils the
+ * token's weights.
+ *
+ * seq_offsets: int32 [B + 1], where the batch's B sequences begin and end (token t belongs to
+ * sequence b if seq_offsets[b] <= t < seq_offsets[b + 1]; what lies before the first and behind
+ * the last is padding), or NULL with B = 1: all tokens are one sequence. Offsets below 0, falling
+ * or past T are clipped, what depends on them is unspecified, and FP8MOE_STATUS_BAD_OFFSETS is
+ * set where the balance loss is computed.
+ *
+ * Balance loss of each sequence, over the n tokens with a choice and their C choices:
+ *   p_i = s_i / sum s (a token's share of expert i);  counts_i = choices of expert i
+ *   slope_i = E * counts_i / (C * n),   loss = sum_i slope_i * sum_t p_ti
+ * which is 1 when choices or shares are even. counts int32 [B, E], loss f32 [B], slope f32 [B, E]
+ * (the loss's derivative by a token's share; what the gradient takes); zeros for a sequence without
+ * choices. Sums are f32 and added up in a fixed order.
+ *
+ * fp8moe_router_fwd: ids int32 [T, topk], weights f32 [T, topk], and, unless counts, loss and
+ * slope are NULL, the balance loss. Workspace: FP8MOE_OP_BALANCE with M = T, N = B (with the
+ * balance loss; else NULL, 0). */
+int fp8moe_router_fwd(const void* logits, int64_t T, int32_t E, int32_t type, int32_t score,
+                      const float* bias, int32_t topk, int32_t normalize, float scale,
+                      const int32_t* seq_offsets, int32_t B, int32_t* ids, float* weights,
+                      int32_t* counts, float* loss, float* slope, void* workspace,
+                      size_t workspace_bytes, fp8moe_stream_t stream);
+
+/* The balance loss of choices that were made elsewhere: ids int32 [T, topk]. A negative id is
+ * no choice; one >= E is none either and sets FP8MOE_STATUS_BAD_EXPERT. */
+int fp8moe_balance_fwd(const void* logits, const int32_t* ids, int64_t T, int32_t E, int32_t type,
+                       int32_t score, int32_t topk, const int32_t* seq_offsets, int32_t B,
+                       int32_t* counts, float* loss, float* slope, void* workspace,
+                       size_t workspace_bytes, fp8moe_stream_t stream);
+
+/* Gradient of the weights (dweights f32 [T, topk]; NULL: 0) and of the balance losses (dloss
+ * f32 [B], with the forward's slope; both NULL: 0) into the logits, dlogits [T, E] of `type`:
+ *   dx_i = q_i * (scale w_i (dw_i - sum dw w) + p_i (D_i - sum D p)),   D = dloss_b * slope_b,
+ *   w: the normalised weights without `scale`, q = 1 (softmax) or sigmoid(-x_i)
+ * (normalize = 0: of softmax scores scale * dw joins D, of sigmoid scores the first term is
+ * scale * dw_i * s_i). ids: the forward's, or given ones (one that occurs twice counts twice).
+ * The choice and the bias have no gradient. dlogits is fully written: zeros for a token without
+ * a choice or outside the sequences. No workspace. */
+int fp8moe_router_bwd(const float* dweights, const void* logits, const int32_t* ids, int64_t T,
+                      int32_t E, int32_t type, int32_t score, int32_t topk, int32_t normalize,
+                      float scale, const float* dloss, const float* slope,
+                      const int32_t* seq_offsets, int32_t B, void* dlogits,
+                      fp8moe_stream_t stream);
+
+/* ---- AdamW over many tensors at once (no counterpart on the pages): what turns the gradients
+ * into the next step's weights. For each value, g = grad_scale * g (where one is given):
+ *   m = beta1 m + (1 - beta1) g,   v = beta2 v + (1 - beta2) g^2
+ *   p = p (1 - lr weight_decay) - lr / (1 - beta1^t) * m / (sqrt(v) / sqrt(1 - beta2^t) + eps)
+ * p is f32 (master weights), g bf16 or f32. Every operation is rounded to f32 by itself: a step
+ * has one right result, which does not depend on what else is in the call.
+ *
+ * Moments are f32 (state_bits = 32), or (8) e4m3 codes of m and of sqrt(v) with an f32 scale for
+ * each 128 consecutive values (the last block may be shorter): scale = largest magnitude / 448,
+ * or 0 where that is below 2^-126; code * scale is the value. A value between two codes takes
+ * the upper one with the probability that keeps the mean, by 16 bits of a hash of its place, of
+ * the tensor's number in the call, t and seed: the same inputs give the same result. The code of
+ * a second moment above zero is never zero. Codes and scales of zero are moments of zero.
+ * A NaN or an infinity in a block's moments makes the block NaN or infinite in the next step.
+ *
+ * copy (may be NULL): bf16 of the new p. codes with code_scale (may be NULL): p is expert weights
+ * [E, K, N], n = E K N, K and N multiples of 16, and the new weights come as the forward takes
+ * them, code_scale f32 [E, N] = max(max_k |p|, 1e-12) / 448, codes u8 [E, K, N] = e4m3(p /
+ * code_scale), round to nearest even. */
+typedef struct fp8moe_adamw_tensor {
+  float* p;
+  const void* g;
+  void* m;               /* f32 or u8 [n] */
+  void* v;
+  float* m_scale;        /* f32 [ceil(n / 128)] with 8 bits, else NULL */
+  float* v_scale;
+  void* copy;            /* bf16 [n] or NULL */
+  uint8_t* codes;        /* u8 [n] or NULL */
+  float* code_scale;     /* f32 [E, N] with codes */
+  int64_t n;             /* values; 0: skipped, no pointer is looked at */
+  int64_t K, N;          /* with codes */
+  double weight_decay;
+  int32_t g_type;        /* FP8MOE_TYPE_* */
+  int32_t state_bits;    /* 32 or 8 */
+} fp8moe_adamw_tensor;
+
+/* `tensors` is a HOST array of `count` entries, read during the call (its pointers are device
+ * pointers); no two entries may overlap. Values need the alignment of their type only; tensors
+ * whose pointers are all 16-byte aligned take wider accesses. t: `step` >= 1, or *step_dev (int64
+ * on the device, NULL: `step`); the rate: `lr`, or *lr_dev (f32 on the device, NULL: `lr`): a
+ * captured step follows what they hold when it is replayed. grad_scale: f32 on the device or
+ * NULL. 0 <= beta < 1, eps >= 0. Workspace: fp8moe_adamw_workspace_size (256-byte aligned), with
+ * on_device = 1 if step_dev or lr_dev is given. */
+size_t fp8moe_adamw_workspace_size(const fp8moe_adamw_tensor* tensors, int32_t count,
+                                   int32_t on_device);
+int fp8moe_adamw_step(const fp8moe_adamw_tensor* tensors, int32_t count, int64_t step,
+                      const int64_t* step_dev, double lr, const float* lr_dev, double beta1,
+                      double beta2, double eps, const float* grad_scale, uint32_t seed,
+                      void* workspace, size_t workspace_bytes, fp8moe_stream_t stream);
 
 /* Text for a return code. */
 const char* fp8moe_status_string(int code);
