@@ -21,25 +21,45 @@
 namespace fp8moe {
 namespace {
 
-constexpr int kWarps = 8;
-constexpr int kThreads = 32 * kWarps;
-constexpr int kSteps = 4;                        // quads of values that a lane has in flight
-constexpr int kUnit = kWarps * kSteps * 128;     // values of a unit (a CTA's share)
-constexpr int kTileRows = 128, kTileCols = 128;  // a unit of a tensor with codes
+constexpr int kWarps = 8;                        // that work; one more fetches
+constexpr int kThreads = 32 * (kWarps + 1);
+constexpr int kStage = 2048;                     // values of a stage: 16 blocks of 128
+constexpr int kBlocks = kStage / 128;
+constexpr int kUnit = 4 * kStage;                // values of a linear unit
+constexpr int kTileRows = 128, kTileCols = 128;  // a unit of weights with codes
+constexpr int kSlabTiles = 608;                  // tiles of a slab, at least
+constexpr int kPer32 = 2, kPer8 = 3;             // CTAs on an SM
 constexpr uint32_t kAll = 0xffffffffu;
+
+// A stage in shared memory: the blocks of each array as they lie in memory (with up to 15 bytes
+// in front, where that is not on a boundary of 16), then 8-bit moments' scales. 100 KB or 63 KB
+// for a CTA's ring, so that an SM has about 200 KB on their way.
+constexpr int kRoomWide = kStage * 4 + 128, kRoomCodes = kStage + 128;
+template <int BITS> struct Layout {
+  static constexpr int kStages = 3;
+  static constexpr int kG = kRoomWide, kM = 2 * kRoomWide;
+  static constexpr int kV = kM + (BITS == 32 ? kRoomWide : kRoomCodes);
+  static constexpr int kScales = kV + (BITS == 32 ? kRoomWide : kRoomCodes);
+  static constexpr int kBytes = kScales + (BITS == 32 ? 0 : 2 * kBlocks * 4);
+  static constexpr int kAll = kStages * kBytes;
+  static_assert(kBytes % 128 == 0, "every stage begins on a boundary that copies may have");
+};
 
 // 32 bits for the value at `i` of a tensor, from a key of the seed, the step and the tensor:
 // products with the odd numbers next to 2^32 times the fractions of the golden ratio and of the
 // roots of 5, 3 and 2, and shifts between them. (Means, correlations between neighbours, steps
-// and halves within the noise of 2^20 draws.)
-__device__ __forceinline__ uint32_t random_bits(uint64_t i, uint32_t key) {
-  uint32_t x = (uint32_t)i * 0x9E3779B9u + (uint32_t)(i >> 32) * 0x3C6EF373u + key;
+// and halves within the noise of 2^20 draws.) random_place() is the part that is linear in i.
+constexpr uint32_t kPlace = 0x9E3779B9u;
+__device__ __forceinline__ uint32_t random_place(uint64_t i, uint32_t key) {
+  return (uint32_t)i * kPlace + (uint32_t)(i >> 32) * 0x3C6EF373u + key;
+}
+__device__ __forceinline__ uint32_t random_bits(uint32_t x) {
   x = (x ^ (x >> 16)) * 0xBB67AE85u;
   x = (x ^ (x >> 15)) * 0x6A09E667u;
   return x ^ (x >> 16);
 }
 
-// Four values of a lane.
+// Four values of a lane: following each other (wide), or 32 apart.
 struct Quad {
   float p[4], g[4], m[4], v[4];
   uint32_t mc, vc;               // 8-bit moments: codes
@@ -48,72 +68,206 @@ struct Quad {
 
 struct Rates {
   float keep, rate, root, b1, c1, b2, c2, eps, grad;
-  bool scaled;
   uint32_t key;
+  double lr;
 };
 
-// VEC: the four values follow each other, on the boundary of four; else they are 32 apart.
-template <bool VEC>
-__device__ __forceinline__ int64_t place(int64_t i0, int lane, int j) {
-  return VEC ? i0 + lane * 4 + j : i0 + j * 32 + lane;
+// What a stage holds.
+enum Kind : uint32_t {
+  kEnd,      // nothing: the last one
+  kWide,     // values that lie on boundaries of 16 bytes in every array
+  kNarrow,   // values that do not
+  kDirect,   // nothing: read from memory value by value (a tensor's ends)
+  kTile,     // 16 rows of a tile
+  kCodes     // the new weights of 16 rows of a tile
+};
+struct Desc {
+  int64_t base;              // the first value's place in the tensor
+  Kind kind;
+  uint32_t entry;            // the tensor
+  uint32_t left;             // kDirect: values; kTile, kCodes: rows
+  uint32_t strip, tile_k;    // kTile, kCodes
+  uint32_t edge;             // 1: a tile's first stage, 2: its last
+};
+
+struct Ring {
+  uint64_t *full, *empty;
+  Desc* desc;
+  uint8_t* data;
+};
+
+__device__ __forceinline__ void cp_async4(void* dst, const void* src) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(smem_u32(dst)), "l"(src) : "memory");
 }
 
-__device__ __forceinline__ void load4(const float* a, float (&x)[4]) {
-  const float4 v = __ldcs(reinterpret_cast<const float4*>(a));
-  x[0] = v.x, x[1] = v.y, x[2] = v.z, x[3] = v.w;
-}
-__device__ __forceinline__ void store4(float* a, const float (&x)[4]) {
-  __stcs(reinterpret_cast<float4*>(a), make_float4(x[0], x[1], x[2], x[3]));
-}
+// The fetching warp: stages in the order in which it is told, each when its place is free.
+template <int BITS>
+struct Fetcher {
+  using L = Layout<BITS>;
+  Ring ring;
+  uint32_t count = 0;
 
-template <int BITS, bool GB, bool VEC>
-__device__ __forceinline__ void load_quad(const AdamwEntry& d, int64_t i0, int lane, bool ok,
-                                          Quad& q) {
-  if constexpr (VEC) {
-    if (!ok) {
-      q = Quad{};
-      return;
-    }
-    const int64_t i = i0 + lane * 4;
-    load4(d.p + i, q.p);
-    if constexpr (GB) {
-      const uint2 w = __ldcs(reinterpret_cast<const uint2*>(
-          static_cast<const __nv_bfloat16*>(d.g) + i));
-      q.g[0] = bf16lo_to_f32(w.x), q.g[1] = bf16hi_to_f32(w.x);
-      q.g[2] = bf16lo_to_f32(w.y), q.g[3] = bf16hi_to_f32(w.y);
-    } else {
-      load4(static_cast<const float*>(d.g) + i, q.g);
-    }
-    if constexpr (BITS == 32) {
-      load4(static_cast<const float*>(d.m) + i, q.m);
-      load4(static_cast<const float*>(d.v) + i, q.v);
-    } else {
-      q.mc = __ldcs(reinterpret_cast<const uint32_t*>(static_cast<const uint8_t*>(d.m) + i));
-      q.vc = __ldcs(reinterpret_cast<const uint32_t*>(static_cast<const uint8_t*>(d.v) + i));
-    }
-  } else {
-    q.mc = q.vc = 0;
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const int64_t i = place<VEC>(i0, lane, j);
-      const bool in = ok && i < d.n;
-      q.p[j] = in ? d.p[i] : 0.0f;
-      if constexpr (GB)
-        q.g[j] = in ? __bfloat162float(static_cast<const __nv_bfloat16*>(d.g)[i]) : 0.0f;
-      else
-        q.g[j] = in ? static_cast<const float*>(d.g)[i] : 0.0f;
-      if constexpr (BITS == 32) {
-        q.m[j] = in ? static_cast<const float*>(d.m)[i] : 0.0f;
-        q.v[j] = in ? static_cast<const float*>(d.v)[i] : 0.0f;
-      } else if (in) {
-        q.mc |= (uint32_t)static_cast<const uint8_t*>(d.m)[i] << (8 * j);
-        q.vc |= (uint32_t)static_cast<const uint8_t*>(d.v)[i] << (8 * j);
+  // room() is waited for; then lane 0 names the bytes that will come, and every lane enters a
+  // scale, or that it has none
+  __device__ __forceinline__ bool room() {
+    const uint32_t round = count / L::kStages;
+    return round == 0 ||
+           mbar_wait_warp(&ring.empty[count % L::kStages], (round - 1) & 1, kWhereProducer);
+  }
+  __device__ __forceinline__ uint32_t at() const { return count % L::kStages; }
+  __device__ __forceinline__ uint8_t* data() const { return ring.data + at() * L::kBytes; }
+  __device__ __forceinline__ uint64_t* full() const { return &ring.full[at()]; }
+  __device__ __forceinline__ void begin(const Desc& d, uint32_t bytes) {
+    ring.desc[at()] = d;
+    if (bytes) mbar_arrive_expect_tx(full(), bytes);
+    else mbar_arrive(full());
+  }
+  __device__ __forceinline__ void end(const float* scale) {
+    if constexpr (BITS == 8) {
+      if (scale != nullptr) {
+        cp_async4(data() + L::kScales + (threadIdx.x & 31) * 4, scale);
+        cp_async_mbar_arrive(full());
+      } else {
+        mbar_arrive(full());
       }
     }
+    ++count;
   }
+  __device__ __forceinline__ bool empty_stage(const Desc& d) {
+    if (!room()) return false;
+    if ((threadIdx.x & 31) == 0) begin(d, 0);
+    end(nullptr);
+    return true;
+  }
+  // kWide or kNarrow: kStage values from d.base on, whole blocks, all inside of the tensor
+  // together with what the copies' boundaries take in around them
+  __device__ __forceinline__ bool values(const AdamwEntry& e, const Desc& d) {
+    if (!room()) return false;
+    const int lane = threadIdx.x & 31;
+    if (lane == 0) {
+      const uint8_t* src[4] = {reinterpret_cast<const uint8_t*>(e.p + d.base),
+                               static_cast<const uint8_t*>(e.g) + d.base * (e.g_bf16 ? 2 : 4),
+                               static_cast<const uint8_t*>(e.m) + d.base * (BITS / 8),
+                               static_cast<const uint8_t*>(e.v) + d.base * (BITS / 8)};
+      const uint32_t size[4] = {kStage * 4, kStage * (e.g_bf16 ? 2u : 4u), kStage * (BITS / 8),
+                                kStage * (BITS / 8)};
+      const uint32_t to[4] = {0, L::kG, L::kM, L::kV};
+      uint32_t shift[4], bytes[4], all = 0;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        shift[i] = (uint32_t)(reinterpret_cast<uintptr_t>(src[i]) & 15u);
+        bytes[i] = (shift[i] + size[i] + 15u) & ~15u;
+        all += bytes[i];
+      }
+      begin(d, all);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) bulk_load(data() + to[i], src[i] - shift[i], bytes[i], full());
+    }
+    __syncwarp();
+    if constexpr (BITS == 8)
+      end((lane < kBlocks ? e.m_scale : e.v_scale) + (d.base >> 7) + lane % kBlocks);
+    else
+      end(nullptr);
+    return true;
+  }
+  // what was on its way when a wait ran out is waited for, so that no copy outlives the CTA
+  __device__ __forceinline__ void drain() {
+    for (uint32_t i = 0; i < L::kStages && i < count; ++i) {
+      const uint32_t c = count - 1 - i;
+      mbar_wait_warp(&ring.full[c % L::kStages], (c / L::kStages) & 1, kWhereDrain);
+    }
+  }
+};
+
+template <int BITS>
+__device__ __forceinline__ void ring_init(const Ring& r) {
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < Layout<BITS>::kStages; ++i) {
+      mbar_init(&r.full[i], BITS == 8 ? 33 : 1);
+      mbar_init(&r.empty[i], kWarps);
+    }
+    fence_mbar_init();
+  }
+}
+
+// Four values that follow each other, or are 32 apart, of a block in shared memory.
+template <bool WIDE>
+__device__ __forceinline__ void lds_f32(const uint8_t* s, float (&x)[4]) {
+  const int lane = threadIdx.x & 31;
+  if constexpr (WIDE) {
+    const float4 v = reinterpret_cast<const float4*>(s)[lane];
+    x[0] = v.x, x[1] = v.y, x[2] = v.z, x[3] = v.w;
+  } else {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) x[j] = reinterpret_cast<const float*>(s)[j * 32 + lane];
+  }
+}
+template <bool WIDE>
+__device__ __forceinline__ void lds_bf16(const uint8_t* s, float (&x)[4]) {
+  const int lane = threadIdx.x & 31;
+  if constexpr (WIDE) {
+    const uint2 w = reinterpret_cast<const uint2*>(s)[lane];
+    x[0] = bf16lo_to_f32(w.x), x[1] = bf16hi_to_f32(w.x);
+    x[2] = bf16lo_to_f32(w.y), x[3] = bf16hi_to_f32(w.y);
+  } else {
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      x[j] = __bfloat162float(reinterpret_cast<const __nv_bfloat16*>(s)[j * 32 + lane]);
+  }
+}
+template <bool WIDE>
+__device__ __forceinline__ uint32_t lds_codes(const uint8_t* s) {
+  const int lane = threadIdx.x & 31;
+  if constexpr (WIDE) return reinterpret_cast<const uint32_t*>(s)[lane];
+  uint32_t c = 0;
+#pragma unroll
+  for (int j = 0; j < 4; ++j) c |= (uint32_t)s[j * 32 + lane] << (8 * j);
+  return c;
+}
+
+// shift: bytes in front of the first value, of p, g, m and v.
+template <int BITS, bool WIDE>
+__device__ __forceinline__ void take_quad(const uint8_t* stage, int block, bool g_bf16,
+                                          const uint32_t (&shift)[4], Quad& q) {
+  using L = Layout<BITS>;
+  lds_f32<WIDE>(stage + block * 512 + shift[0], q.p);
+  if (g_bf16) lds_bf16<WIDE>(stage + L::kG + block * 256 + shift[1], q.g);
+  else lds_f32<WIDE>(stage + L::kG + block * 512 + shift[1], q.g);
+  if constexpr (BITS == 32) {
+    lds_f32<WIDE>(stage + L::kM + block * 512 + shift[2], q.m);
+    lds_f32<WIDE>(stage + L::kV + block * 512 + shift[3], q.v);
+  } else {
+    q.mc = lds_codes<WIDE>(stage + L::kM + block * 128 + shift[2]);
+    q.vc = lds_codes<WIDE>(stage + L::kV + block * 128 + shift[3]);
+    const float* scales = reinterpret_cast<const float*>(stage + L::kScales);
+    q.ms = scales[block], q.vs = scales[kBlocks + block];
+  }
+}
+
+// The same straight from memory, value by value: those of a block at `i` of the tensor that exist.
+template <int BITS>
+__device__ __forceinline__ void load_quad(const AdamwEntry& d, int64_t i, uint32_t left, Quad& q) {
+  const uint32_t lane = threadIdx.x & 31;
   if constexpr (BITS == 8) {
-    q.ms = ok ? d.m_scale[i0 >> 7] : 0.0f;
-    q.vs = ok ? d.v_scale[i0 >> 7] : 0.0f;
+    q.mc = q.vc = 0;
+    q.ms = d.m_scale[i >> 7], q.vs = d.v_scale[i >> 7];
+  }
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const bool in = j * 32 + lane < left;
+    const int64_t at = i + j * 32 + lane;
+    q.p[j] = in ? d.p[at] : 0.0f;
+    if (d.g_bf16)
+      q.g[j] = in ? __bfloat162float(static_cast<const __nv_bfloat16*>(d.g)[at]) : 0.0f;
+    else
+      q.g[j] = in ? static_cast<const float*>(d.g)[at] : 0.0f;
+    if constexpr (BITS == 32) {
+      q.m[j] = in ? static_cast<const float*>(d.m)[at] : 0.0f;
+      q.v[j] = in ? static_cast<const float*>(d.v)[at] : 0.0f;
+    } else if (in) {
+      q.mc |= (uint32_t)static_cast<const uint8_t*>(d.m)[at] << (8 * j);
+      q.vc |= (uint32_t)static_cast<const uint8_t*>(d.v)[at] << (8 * j);
+    }
   }
 }
 
@@ -132,17 +286,29 @@ __device__ __forceinline__ float block_scale(uint32_t most) {
   return s < 0x1p-126f ? 0.0f : s;
 }
 
-// |x| as an e4m3 code by chance: |x| / scale * 2^-120 has the code's bits on top of its own
-// (both formats' subnormals included), and 16 random bits decide about the 20 below. The largest
-// of a block has the code 0x7E (448) exactly; 0x7F would be the code of a NaN.
-__device__ __forceinline__ uint32_t encode(float x, float inverse, uint32_t random16) {
+// |x| as an e4m3 code by chance, in the top byte: |x| / scale * 2^-120 has the code's bits on
+// top of its own (both formats' subnormals included), and the random ones, 16 bits and a one
+// behind them for the middle of their step, decide about the 20 below. The largest of a block is
+// 448 to within 4 units (its scale, the inverse and two products are rounded), where the random
+// bits reach the next code only from 8 units on: 0x7F, a NaN's code, is for spoilt blocks alone.
+__device__ __forceinline__ uint32_t encode(float x, float inverse, uint32_t random24) {
   const float y = __fmul_rn(__fmul_rn(fabsf(x), inverse), 0x1p-120f);
-  return min((__float_as_uint(y) + (random16 << 4) + 8u) >> 20, 0x7Eu);
+  return __float_as_uint(y) * 16u + random24;
+}
+__device__ __forceinline__ uint32_t top_bytes(uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+  return __byte_perm(__byte_perm(a, b, 0x0073), __byte_perm(c, d, 0x0073), 0x5410);
 }
 
-template <int BITS, bool VEC>
-__device__ __forceinline__ void step_quad(const AdamwEntry& d, const Rates& r, int64_t i0, int lane,
-                                          bool ok, Quad& q) {
+// The larger magnitude; a NaN stays.
+__device__ __forceinline__ float max_abs(float a, float b, float c) {
+  float r;
+  asm("max.NaN.abs.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
+
+// place: of the lane's first value in the tensor; apart: between two of its values.
+template <int BITS>
+__device__ __forceinline__ void step_quad(const Rates& r, uint64_t place, uint32_t apart, Quad& q) {
   float root[4];
   if constexpr (BITS == 8) {
     decode4(q.mc, q.ms, q.m);
@@ -150,7 +316,7 @@ __device__ __forceinline__ void step_quad(const AdamwEntry& d, const Rates& r, i
   }
 #pragma unroll
   for (int j = 0; j < 4; ++j) {
-    const float g = r.scaled ? __fmul_rn(q.g[j], r.grad) : q.g[j];
+    const float g = __fmul_rn(q.g[j], r.grad);
     const float v = BITS == 8 ? __fmul_rn(q.v[j], q.v[j]) : q.v[j];
     q.m[j] = __fadd_rn(__fmul_rn(q.m[j], r.b1), __fmul_rn(g, r.c1));
     q.v[j] = __fadd_rn(__fmul_rn(v, r.b2), __fmul_rn(__fmul_rn(g, r.c2), g));
@@ -159,134 +325,133 @@ __device__ __forceinline__ void step_quad(const AdamwEntry& d, const Rates& r, i
     q.p[j] = __fsub_rn(__fmul_rn(q.p[j], r.keep), __fmul_rn(step, r.rate));
   }
   if constexpr (BITS == 8) {
-    uint32_t mm = 0, vm = 0;
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const bool in = ok && (VEC || place<VEC>(i0, lane, j) < d.n);
-      mm = max(mm, in ? __float_as_uint(q.m[j]) & 0x7fffffffu : 0u);
-      vm = max(vm, in ? __float_as_uint(root[j]) & 0x7fffffffu : 0u);
-    }
-    q.ms = block_scale(__reduce_max_sync(kAll, mm));
-    q.vs = block_scale(__reduce_max_sync(kAll, vm));
+    // (values that do not exist are zeros, and so are their moments)
+    const float mm = max_abs(max_abs(q.m[0], q.m[1], q.m[2]), q.m[3], 0.0f);
+    const float vm = max_abs(max_abs(root[0], root[1], root[2]), root[3], 0.0f);
+    q.ms = block_scale(__reduce_max_sync(kAll, __float_as_uint(mm)));
+    q.vs = block_scale(__reduce_max_sync(kAll, __float_as_uint(vm)));
     const float mi = q.ms != 0.0f ? __frcp_rn(q.ms) : 0.0f;
     const float vi = q.vs != 0.0f ? __frcp_rn(q.vs) : 0.0f;
-    q.mc = q.vc = 0;
+    const uint32_t least = q.vs != 0.0f ? 0x01000000u : 0u;
+    // a block lies on one side of 2^32, as its first place is a multiple of 128
+    const uint32_t base = random_place(place, r.key);
+    uint32_t mc[4], vc[4];
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-      const uint32_t bits = random_bits((uint64_t)place<VEC>(i0, lane, j), r.key);
-      const uint32_t mc = encode(q.m[j], mi, bits & 0xffffu) |
-                          (__float_as_uint(q.m[j]) >> 31) << 7;
-      // a second moment that is not zero never becomes zero: m / eps would follow
-      uint32_t vc = encode(root[j], vi, bits >> 16);
-      if (vc == 0u && root[j] > 0.0f && q.vs > 0.0f) vc = 1u;
-      q.mc |= mc << (8 * j);
-      q.vc |= vc << (8 * j);
+      const uint32_t bits = random_bits(base + j * apart * kPlace);
+      mc[j] = (__float_as_uint(q.m[j]) & 0x80000000u) |
+              (encode(q.m[j], mi, __byte_perm(bits, 0x80u, 0x7104)) & 0x7fffffffu);
+      // a second moment that is not zero (its root then is at least 2^-75) never becomes zero:
+      // m / eps would follow
+      vc[j] = max(encode(root[j], vi, __byte_perm(bits, 0x80u, 0x7324)),
+                  min(__float_as_uint(root[j]), least));
     }
+    q.mc = top_bytes(mc[0], mc[1], mc[2], mc[3]);
+    q.vc = top_bytes(vc[0], vc[1], vc[2], vc[3]);
   }
 }
 
-template <int BITS, bool VEC>
-__device__ __forceinline__ void store_quad(const AdamwEntry& d, int64_t i0, int lane, bool ok,
+// i: of the block's first value in the tensor. WIDE: the lane's four follow each other.
+template <int BITS, bool WIDE>
+__device__ __forceinline__ void store_quad(const AdamwEntry& d, int64_t i, uint32_t left,
                                            const Quad& q) {
-  if (!ok) return;
-  if constexpr (VEC) {
-    const int64_t i = i0 + lane * 4;
-    store4(d.p + i, q.p);
+  const uint32_t lane = threadIdx.x & 31;
+  float* p = d.p + i;
+  uint8_t* m = static_cast<uint8_t*>(d.m) + i * (BITS / 8);
+  uint8_t* v = static_cast<uint8_t*>(d.v) + i * (BITS / 8);
+  __nv_bfloat16* copy = d.copy ? static_cast<__nv_bfloat16*>(d.copy) + i : nullptr;
+  if constexpr (WIDE) {
+    // p stays in the L2, where its codes are made from it
+    reinterpret_cast<float4*>(p)[lane] = make_float4(q.p[0], q.p[1], q.p[2], q.p[3]);
     if constexpr (BITS == 32) {
-      store4(static_cast<float*>(d.m) + i, q.m);
-      store4(static_cast<float*>(d.v) + i, q.v);
+      __stcs(reinterpret_cast<float4*>(m) + lane, make_float4(q.m[0], q.m[1], q.m[2], q.m[3]));
+      __stcs(reinterpret_cast<float4*>(v) + lane, make_float4(q.v[0], q.v[1], q.v[2], q.v[3]));
     } else {
-      __stcs(reinterpret_cast<uint32_t*>(static_cast<uint8_t*>(d.m) + i), q.mc);
-      __stcs(reinterpret_cast<uint32_t*>(static_cast<uint8_t*>(d.v) + i), q.vc);
+      __stcs(reinterpret_cast<uint32_t*>(m) + lane, q.mc);
+      __stcs(reinterpret_cast<uint32_t*>(v) + lane, q.vc);
     }
-    if (d.copy)
-      __stcs(reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(d.copy) + i),
+    if (copy)
+      __stcs(reinterpret_cast<uint2*>(copy) + lane,
              make_uint2(f32x2_to_bf16x2(q.p[0], q.p[1]), f32x2_to_bf16x2(q.p[2], q.p[3])));
   } else {
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-      const int64_t i = place<VEC>(i0, lane, j);
-      if (i >= d.n) continue;
-      d.p[i] = q.p[j];
+      const uint32_t k = j * 32 + lane;
+      if (k >= left) continue;
+      p[k] = q.p[j];
       if constexpr (BITS == 32) {
-        static_cast<float*>(d.m)[i] = q.m[j];
-        static_cast<float*>(d.v)[i] = q.v[j];
+        reinterpret_cast<float*>(m)[k] = q.m[j];
+        reinterpret_cast<float*>(v)[k] = q.v[j];
       } else {
-        static_cast<uint8_t*>(d.m)[i] = (uint8_t)(q.mc >> (8 * j));
-        static_cast<uint8_t*>(d.v)[i] = (uint8_t)(q.vc >> (8 * j));
+        m[k] = (uint8_t)(q.mc >> (8 * j));
+        v[k] = (uint8_t)(q.vc >> (8 * j));
       }
-      if (d.copy) static_cast<__nv_bfloat16*>(d.copy)[i] = __float2bfloat16_rn(q.p[j]);
+      if (copy) copy[k] = __float2bfloat16_rn(q.p[j]);
     }
   }
   if constexpr (BITS == 8) {
     if (lane == 0) {
-      d.m_scale[i0 >> 7] = q.ms;
-      d.v_scale[i0 >> 7] = q.vs;
+      d.m_scale[i >> 7] = q.ms;
+      d.v_scale[i >> 7] = q.vs;
     }
   }
 }
 
-// kUnit values in order.
-template <int BITS, bool GB, bool VEC>
-__device__ __forceinline__ void linear_unit(const AdamwEntry& d, const Rates& r, int64_t base) {
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  Quad q[kSteps];
-#pragma unroll
-  for (int s = 0; s < kSteps; ++s) {
-    const int64_t i0 = base + (s * kWarps + warp) * 128;
-    load_quad<BITS, GB, VEC>(d, i0, lane, i0 < d.n, q[s]);
+// One of the working warps' blocks of a stage of a linear unit.
+template <int BITS>
+__device__ __forceinline__ void linear_stage(const AdamwEntry& d, const Rates& r, const Desc& a,
+                                             const uint8_t* stage) {
+  const uint32_t lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const uint32_t none[4] = {0, 0, 0, 0};
+  uint32_t shift[4] = {0, 0, 0, 0};
+  if (a.kind == kNarrow) {
+    auto low = [](const void* p, int64_t bytes) {
+      return (uint32_t)((reinterpret_cast<uintptr_t>(p) + (uint64_t)bytes) & 15u);
+    };
+    shift[0] = low(d.p, a.base * 4), shift[1] = low(d.g, a.base * (d.g_bf16 ? 2 : 4));
+    shift[2] = low(d.m, a.base * (BITS / 8)), shift[3] = low(d.v, a.base * (BITS / 8));
   }
-#pragma unroll
-  for (int s = 0; s < kSteps; ++s) {
-    const int64_t i0 = base + (s * kWarps + warp) * 128;
-    const bool ok = i0 < d.n;
-    step_quad<BITS, VEC>(d, r, i0, lane, ok, q[s]);
-    store_quad<BITS, VEC>(d, i0, lane, ok, q[s]);
+#pragma unroll 1
+  for (uint32_t block = warp; block < kBlocks; block += kWarps) {
+    const int64_t i = a.base + block * 128;
+    Quad q;
+    if (a.kind == kWide) {
+      take_quad<BITS, true>(stage, block, d.g_bf16, none, q);
+      step_quad<BITS>(r, i + lane * 4, 1, q);
+      store_quad<BITS, true>(d, i, 128, q);
+    } else {
+      uint32_t left = 128;
+      if (a.kind == kNarrow) {
+        take_quad<BITS, false>(stage, block, d.g_bf16, shift, q);
+      } else {
+        if (block * 128 >= a.left) break;
+        left = a.left - block * 128;
+        load_quad<BITS>(d, i, left, q);
+      }
+      step_quad<BITS>(r, i + lane, 32, q);
+      store_quad<BITS, false>(d, i, left, q);
+    }
   }
 }
 
-// kTileRows x kTileCols weights of an expert [K, N]: also the largest magnitude of each column.
-template <int BITS, bool GB>
-__device__ __forceinline__ void tile_unit(const AdamwEntry& d, const Rates& r, uint32_t unit,
-                                          uint32_t* s_most) {
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const uint32_t tiles_n = (d.N + kTileCols - 1) / kTileCols;
-  const uint32_t tiles_k = (d.K + kTileRows - 1) / kTileRows;
-  const uint32_t tile_n = unit % tiles_n, rest = unit / tiles_n;
-  const uint32_t tile_k = rest % tiles_k, e = rest / tiles_k;
-  const int col = tile_n * kTileCols;
-  const bool ok_col = col + lane * 4 < d.N;      // N is a multiple of 16
-  const int64_t expert = (int64_t)e * d.K * d.N;
-  uint32_t most[4] = {0, 0, 0, 0};
-  for (int k0 = tile_k * kTileRows; k0 < d.K && k0 < (int)(tile_k + 1) * kTileRows;
-       k0 += kWarps * kSteps) {
-    Quad q[kSteps];
-#pragma unroll
-    for (int s = 0; s < kSteps; ++s) {
-      const int k = k0 + s * kWarps + warp;
-      load_quad<BITS, GB, true>(d, expert + (int64_t)k * d.N + col, lane, k < d.K && ok_col, q[s]);
-    }
-#pragma unroll
-    for (int s = 0; s < kSteps; ++s) {
-      const int k = k0 + s * kWarps + warp;
-      const int64_t i0 = expert + (int64_t)k * d.N + col;
-      const bool ok = k < d.K && ok_col;
-      step_quad<BITS, true>(d, r, i0, lane, ok, q[s]);
-      store_quad<BITS, true>(d, i0, lane, ok, q[s]);
-#pragma unroll
-      for (int j = 0; j < 4; ++j)
-        if (ok) most[j] = max(most[j], __float_as_uint(q[s].p[j]) & 0x7fffffffu);
-    }
+// What a call's tensors share, and what is a tensor's own.
+__device__ __forceinline__ Rates rates_of(const AdamwCommon& c) {
+  Rates r;
+  r.b1 = c.b1, r.c1 = c.c1, r.b2 = c.b2, r.c2 = c.c2, r.eps = c.eps;
+  r.grad = c.grad_scale != nullptr ? *c.grad_scale : 1.0f;
+  r.rate = c.rate, r.root = c.root, r.key = c.key, r.lr = 0.0;
+  if (c.rates != nullptr) {                      // step or rate on the device
+    r.rate = c.rates->rate, r.root = c.rates->root, r.key = c.rates->key, r.lr = c.rates->lr;
   }
-#pragma unroll
-  for (int j = 0; j < 4; ++j) s_most[warp * kTileCols + lane * 4 + j] = most[j];
-  __syncthreads();
-  for (int c = threadIdx.x; c < kTileCols && col + c < d.N; c += kThreads) {
-    uint32_t m = 0;
-#pragma unroll
-    for (int w = 0; w < kWarps; ++w) m = max(m, s_most[w * kTileCols + c]);
-    atomicMax(d.most + (int64_t)e * d.N + col + c, m);
-  }
+  r.keep = 1.0f;
+  return r;
+}
+__device__ __forceinline__ Rates rates_for(const Rates& all, const AdamwCommon& c,
+                                           const AdamwEntry& d) {
+  Rates r = all;
+  r.keep = c.rates != nullptr ? (float)(1.0 - all.lr * d.weight_decay) : d.keep;
+  r.key += 0xBB67AE85u * d.which;
+  return r;
 }
 
 template <int kCapacity>
@@ -295,43 +460,56 @@ struct AdamwTable {
   AdamwEntry at[kCapacity];
 };
 
-template <int kCapacity>
-__global__ void __launch_bounds__(kThreads, 2) adamw_kernel(
+template <int BITS, int kCapacity>
+__global__ void __launch_bounds__(kThreads, BITS == 32 ? kPer32 : kPer8) adamw_kernel(
     const __grid_constant__ AdamwTable<kCapacity> table) {
-  __shared__ uint32_t s_most[kWarps * kTileCols];
+  using L = Layout<BITS>;
+  extern __shared__ __align__(128) uint8_t s_data[];
+  __shared__ uint64_t s_full[L::kStages], s_empty[L::kStages];
+  __shared__ Desc s_desc[L::kStages];
+  const Ring ring = {s_full, s_empty, s_desc, s_data};
+  ring_init<BITS>(ring);
+  __syncthreads();
   const AdamwCommon& c = table.c;
-  int lo = 0, hi = c.count - 1;                  // the last entry whose units begin at or before
-  while (lo < hi) {
-    const int mid = (lo + hi + 1) >> 1;
-    if (table.at[mid].first_unit <= blockIdx.x) lo = mid;
-    else hi = mid - 1;
+
+  if (threadIdx.x >= 32 * kWarps) {
+    Fetcher<BITS> f = {ring};
+    bool going = true;
+    uint32_t entry = 0;
+    for (uint32_t unit = blockIdx.x; going && unit < c.units; unit += gridDim.x) {
+      while ((int)entry + 1 < c.count && table.at[entry + 1].first_unit <= unit) ++entry;
+      const AdamwEntry& d = table.at[entry];
+      Desc a = {};
+      a.entry = entry;
+      const uint32_t number = unit - d.first_unit;
+      if (number == 0 && d.head > 0) {             // in front of the first boundary
+        a.kind = kDirect, a.base = 0;
+        a.left = (uint32_t)min(d.n, (int64_t)d.head);
+        going = f.empty_stage(a);
+      }
+      a.base = d.head + (int64_t)number * kUnit;
+      for (int i = 0; going && i < kUnit / kStage && a.base < d.n; ++i, a.base += kStage) {
+        const int64_t behind = d.n - a.base - kStage;
+        a.left = (uint32_t)min((int64_t)kStage, d.n - a.base);
+        a.kind = d.vec && behind >= 0 ? kWide
+                 : !d.vec && behind >= 16 && a.base >= 16 ? kNarrow : kDirect;
+        going = a.kind == kDirect ? f.empty_stage(a) : f.values(d, a);
+      }
+    }
+    if (going) going = f.empty_stage(Desc{});      // kEnd
+    if (!going) f.drain();
+    return;
   }
-  const AdamwEntry& d = table.at[lo];
-  const uint32_t unit = blockIdx.x - d.first_unit;
-  Rates r;
-  r.b1 = c.b1, r.c1 = c.c1, r.b2 = c.b2, r.c2 = c.c2, r.eps = c.eps;
-  r.scaled = c.grad_scale != nullptr;
-  r.grad = r.scaled ? *c.grad_scale : 1.0f;
-  if (c.rates != nullptr) {                      // step or rate on the device
-    r.keep = (float)(1.0 - c.rates->lr * d.weight_decay);
-    r.rate = c.rates->rate, r.root = c.rates->root;
-    r.key = c.rates->key;
-  } else {
-    r.keep = d.keep, r.rate = c.rate, r.root = c.root;
-    r.key = c.key;
-  }
-  r.key += 0xBB67AE85u * d.which;
-  const int64_t base = (int64_t)unit * kUnit;
-  const bool gb = d.g_bf16;
-  if (d.tiles) {
-    if (d.bits == 32) gb ? tile_unit<32, true>(d, r, unit, s_most) : tile_unit<32, false>(d, r, unit, s_most);
-    else gb ? tile_unit<8, true>(d, r, unit, s_most) : tile_unit<8, false>(d, r, unit, s_most);
-  } else if (d.vec && base + kUnit <= d.n) {
-    if (d.bits == 32) gb ? linear_unit<32, true, true>(d, r, base) : linear_unit<32, false, true>(d, r, base);
-    else gb ? linear_unit<8, true, true>(d, r, base) : linear_unit<8, false, true>(d, r, base);
-  } else {
-    if (d.bits == 32) gb ? linear_unit<32, true, false>(d, r, base) : linear_unit<32, false, false>(d, r, base);
-    else gb ? linear_unit<8, true, false>(d, r, base) : linear_unit<8, false, false>(d, r, base);
+  const Rates all = rates_of(c);
+  for (uint32_t n = 0;; ++n) {
+    const uint32_t at = n % L::kStages;
+    if (!mbar_wait_warp(&s_full[at], (n / L::kStages) & 1, kWhereEpilogue)) return;
+    const Desc a = s_desc[at];
+    if (a.kind == kEnd) return;
+    const AdamwEntry& d = table.at[a.entry];
+    linear_stage<BITS>(d, rates_for(all, c, d), a, s_data + at * L::kBytes);
+    __syncwarp();
+    if ((threadIdx.x & 31) == 0) mbar_arrive(&s_empty[at]);
   }
 }
 
@@ -353,7 +531,7 @@ __global__ void adamw_prepare_kernel(AdamwRates* rates, const int64_t* step, int
 }
 
 // The columns' largest magnitudes of weights [E, K, N], where the step's units are not tiles.
-__global__ void __launch_bounds__(kThreads) column_max_kernel(const float* p, int K, int N,
+__global__ void __launch_bounds__(32 * kWarps) column_max_kernel(const float* p, int K, int N,
                                                               uint32_t* most) {
   __shared__ uint32_t s_most[kWarps * kTileCols];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -370,7 +548,7 @@ __global__ void __launch_bounds__(kThreads) column_max_kernel(const float* p, in
 #pragma unroll
   for (int j = 0; j < 4; ++j) s_most[warp * kTileCols + j * 32 + lane] = m[j];
   __syncthreads();
-  for (int c = threadIdx.x; c < kTileCols && col + c < N; c += kThreads) {
+  for (int c = threadIdx.x; c < kTileCols && col + c < N; c += 32 * kWarps) {
     uint32_t v = 0;
 #pragma unroll
     for (int w = 0; w < kWarps; ++w) v = max(v, s_most[w * kTileCols + c]);
@@ -379,57 +557,275 @@ __global__ void __launch_bounds__(kThreads) column_max_kernel(const float* p, in
 }
 
 // codes = e4m3(p / scale), scale = max(column's largest, 1e-12) / 448, both as the library's
-// other quantisers have them (quantize.cuh).
-template <bool VEC>
-__global__ void __launch_bounds__(kThreads) weight_codes_kernel(const float* p, int K, int N,
-                                                                const uint32_t* most,
-                                                                uint8_t* codes, float* scale) {
+// other quantisers have them (quantize.cuh). A lane's four columns follow each other (WIDE) or are
+// 32 apart.
+struct Columns {
+  float s[4], rl[4], rh[4];
+};
+template <bool WIDE>
+__device__ __forceinline__ void columns_of(const uint32_t* most, float* scale, int64_t e, int col,
+                                           int N, bool first, Columns& x) {
+  const int lane = threadIdx.x & 31;
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const int c = col + (WIDE ? lane * 4 + j : j * 32 + lane);
+    float a = c < N ? __uint_as_float(__ldcg(most + e * N + c)) : 1.0f;
+    a = a < kEps ? kEps : a;                     // a NaN stays
+    x.s[j] = __fdiv_rn(a, kE4m3Max);
+    bracket(x.s[j], x.rl[j], x.rh[j]);
+    if (first && c < N) scale[e * N + c] = x.s[j];
+  }
+}
+__device__ __forceinline__ uint32_t codes_of(const float (&v)[4], const Columns& x) {
+  const uint16_t lo =
+      quotient_x2<false>(v[0], v[1], x.s[0], x.s[1], x.rl[0], x.rl[1], x.rh[0], x.rh[1]);
+  const uint16_t hi =
+      quotient_x2<false>(v[2], v[3], x.s[2], x.s[3], x.rl[2], x.rl[3], x.rh[2], x.rh[3]);
+  return (uint32_t)lo | (uint32_t)hi << 16;
+}
+
+// For weights that the step went through in order.
+__global__ void __launch_bounds__(32 * kWarps) weight_codes_kernel(const float* p, int K, int N,
+                                                                   const uint32_t* most,
+                                                                   uint8_t* codes, float* scale) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int col = blockIdx.x * kTileCols, k0 = blockIdx.y * kTileRows;
   const int64_t e = blockIdx.z;
-  float s[4], rl[4], rh[4];
+  Columns x;
+  columns_of<false>(most, scale, e, col, N, k0 == 0 && warp == 0, x);
+  const int64_t base = (e * K + k0) * N + col;
+  for (int row = warp; row < kTileRows && k0 + row < K; row += kWarps) {
+    float v[4];
 #pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    const int c = col + (VEC ? lane * 4 + j : j * 32 + lane);
-    float a = c < N ? __uint_as_float(most[e * N + c]) : 1.0f;
-    a = a < kEps ? kEps : a;                     // a NaN stays
-    s[j] = __fdiv_rn(a, kE4m3Max);
-    bracket(s[j], rl[j], rh[j]);
-    if (blockIdx.y == 0 && warp == 0 && c < N) scale[e * N + c] = s[j];
-  }
-  const int64_t expert = e * K * N;
-  for (int k = k0 + warp; k < K && k < k0 + kTileRows; k += kWarps) {
-    const int64_t i0 = expert + (int64_t)k * N + col;
-    float x[4];
-    if constexpr (VEC) {
-      if (col + lane * 4 >= N) continue;
-      load4(p + i0 + lane * 4, x);
-    } else {
+    for (int j = 0; j < 4; ++j)
+      v[j] = col + j * 32 + lane < N ? p[base + (int64_t)row * N + j * 32 + lane] : 0.0f;
+    const uint32_t w = codes_of(v, x);
 #pragma unroll
-      for (int j = 0; j < 4; ++j) x[j] = col + j * 32 + lane < N ? p[i0 + j * 32 + lane] : 0.0f;
-    }
-    const uint16_t lo = quotient_x2<false>(x[0], x[1], s[0], s[1], rl[0], rl[1], rh[0], rh[1]);
-    const uint16_t hi = quotient_x2<false>(x[2], x[3], s[2], s[3], rl[2], rl[3], rh[2], rh[3]);
-    const uint32_t w = (uint32_t)lo | (uint32_t)hi << 16;
-    if constexpr (VEC) {
-      *reinterpret_cast<uint32_t*>(codes + i0 + lane * 4) = w;
-    } else {
-#pragma unroll
-      for (int j = 0; j < 4; ++j)
-        if (col + j * 32 + lane < N) codes[i0 + j * 32 + lane] = (uint8_t)(w >> (8 * j));
-    }
+    for (int j = 0; j < 4; ++j)
+      if (col + j * 32 + lane < N)
+        codes[base + (int64_t)row * N + j * 32 + lane] = (uint8_t)(w >> (8 * j));
   }
 }
 
-template <int kCapacity>
-cudaError_t launch_table(const AdamwCommon& c, const AdamwEntry* at, int count, uint32_t units,
-                         cudaStream_t s) {
-  static thread_local AdamwTable<kCapacity> t;   // up to 27 KB: not on the stack
+// Weights with codes. A strip is 128 columns of an expert, a slab some strips over all their rows.
+// The units, in order: the tiles of slab 0, then of slab i followed by the codes of slab i - 1,
+// whose weights are still in the L2: they are read from there and not from memory (a value's 33
+// bytes of traffic become 29). CTAs take units in this order from a counter. Codes wait until
+// their slab's tiles are done; those have been taken before, by CTAs that wait for nothing or for
+// earlier tiles still, so that the wait ends whatever else runs, and as a slab has as many tiles as
+// there are CTAs it hardly ever begins.
+// Waits until a slab's tiles are done; false (and a status bit) after two seconds.
+__device__ __forceinline__ bool wait_slab(const uint32_t* done, uint32_t tiles) {
+  const uint64_t began = globaltimer_ns();
+  for (;;) {
+    uint32_t v;
+    asm volatile("ld.acquire.gpu.global.u32 %0, [%1];" : "=r"(v) : "l"(done) : "memory");
+    if (v >= tiles) break;
+    if (globaltimer_ns() - began > kWaitLimitNs) {
+      status_set(kStatusWaitTimeout | kWhereDrain);
+      return false;
+    }
+    __nanosleep(200);
+  }
+  // the tiles were written by ordinary stores; the copies that follow read them another way
+  asm volatile("fence.proxy.async.global;" ::: "memory");
+  return true;
+}
+
+struct UnitOf {
+  uint32_t slab, strip, tile_k, tiles;           // tiles: 1, codes: 0
+};
+// What the unit with this number is; `units` has the order.
+__device__ __forceinline__ UnitOf unit_of(const AdamwSlabArgs& a, uint32_t unit, uint32_t tiles_k) {
+  const uint32_t whole = a.per_slab * tiles_k;   // units of a slab but the last
+  const uint32_t last = a.slabs - 1, last_strips = a.strips - last * a.per_slab;
+  const uint32_t first = last == 0 ? last_strips * tiles_k : whole;
+  UnitOf u = {0, 0, 0, 1};
+  if (unit >= first) {
+    unit -= first;
+    if (last != 0) {
+      u.slab = min(1 + unit / (2 * whole), last);
+      unit -= (u.slab - 1) * 2 * whole;
+    }
+    const uint32_t n = last == 0 ? 0 : u.slab < last ? whole : last_strips * tiles_k;
+    if (unit >= n) {
+      unit -= n, u.tiles = 0;
+      if (unit < whole && last != 0) --u.slab;
+      else if (last != 0) unit -= whole;
+    }
+  }
+  const uint32_t strips = u.slab == last ? last_strips : a.per_slab;
+  u.strip = u.slab * a.per_slab + unit % strips;
+  u.tile_k = unit / strips;
+  return u;
+}
+
+template <int BITS>
+__global__ void __launch_bounds__(kThreads, BITS == 32 ? kPer32 : kPer8) adamw_slab_kernel(
+    const __grid_constant__ AdamwSlabArgs a) {
+  using L = Layout<BITS>;
+  extern __shared__ __align__(128) uint8_t s_data[];
+  __shared__ uint64_t s_full[L::kStages], s_empty[L::kStages], s_join[2];
+  __shared__ Desc s_desc[L::kStages];
+  __shared__ float s_most[kWarps * kTileCols];
+  const Ring ring = {s_full, s_empty, s_desc, s_data};
+  if (threadIdx.x == 0) {
+    mbar_init(&s_join[0], kWarps);
+    mbar_init(&s_join[1], kWarps);
+  }
+  ring_init<BITS>(ring);
+  __syncthreads();
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int K = a.d.K, N = a.d.N;
+  const uint32_t tiles_k = (K + kTileRows - 1) / kTileRows;
+  const uint32_t tiles_n = (N + kTileCols - 1) / kTileCols;
+  constexpr int kRows = kStage / kTileCols;      // of a stage
+
+  if (warp == kWarps) {
+    Fetcher<BITS> f = {ring};
+    bool going = true;
+    uint32_t next = lane == 0 ? atomicAdd(a.counters, 1u) : 0u;
+    while (going) {
+      const uint32_t unit = __shfl_sync(kAll, next, 0);
+      if (unit >= a.units) break;
+      if (lane == 0) next = atomicAdd(a.counters, 1u);
+      const UnitOf u = unit_of(a, unit, tiles_k);
+      if (!u.tiles) {
+        const uint32_t strips = u.slab + 1 == a.slabs ? a.strips - u.slab * a.per_slab : a.per_slab;
+        bool ready = true;
+        if (lane == 0) ready = wait_slab(a.counters + 1 + u.slab, strips * tiles_k);
+        going = __shfl_sync(kAll, (int)ready, 0);
+      }
+      const int e = u.strip / tiles_n, col = (u.strip % tiles_n) * kTileCols;
+      const int rows = min(kTileRows, K - (int)u.tile_k * kTileRows);
+      for (int row = 0; going && row < rows; row += kRows) {
+        Desc d;
+        d.kind = u.tiles ? kTile : kCodes;
+        d.entry = 0, d.strip = u.strip, d.tile_k = u.tile_k;
+        d.left = min(kRows, rows - row);
+        d.edge = (row == 0 ? 1 : 0) + (row + kRows >= rows ? 2 : 0);
+        const int k = u.tile_k * kTileRows + row;
+        d.base = ((int64_t)e * K + k) * N + col;
+        going = f.room();
+        if (!going) break;
+        if (lane == 0) {
+          constexpr uint32_t kValues = kStage;
+          f.begin(d, kValues * 4 + (u.tiles ? kValues * ((a.d.g_bf16 ? 2 : 4) + 2 * BITS / 8) : 0));
+          tma_load_3d(f.data(), &a.tm_p, f.full(), col, k, e);
+          if (u.tiles) {
+            tma_load_3d(f.data() + L::kG, &a.tm_g, f.full(), col, k, e);
+            tma_load_3d(f.data() + L::kM, &a.tm_m, f.full(), col, k, e);
+            tma_load_3d(f.data() + L::kV, &a.tm_v, f.full(), col, k, e);
+          }
+        }
+        __syncwarp();
+        const int r = lane % kBlocks < (int)d.left ? lane % kBlocks : 0;
+        f.end(BITS == 8 && u.tiles
+                  ? (lane < kBlocks ? a.d.m_scale : a.d.v_scale) + (d.base >> 7) + (int64_t)r * (N >> 7)
+                  : nullptr);
+      }
+    }
+    if (going) going = f.empty_stage(Desc{});      // kEnd
+    if (!going) f.drain();
+    return;
+  }
+
+  const Rates rates = rates_for(rates_of(a.c), a.c, a.d);
+  float most[4];
+  Columns x;
+  uint32_t joins = 0;
+  for (uint32_t n = 0;; ++n) {
+    const uint32_t at = n % L::kStages;
+    if (!mbar_wait_warp(&s_full[at], (n / L::kStages) & 1, kWhereEpilogue)) return;
+    const Desc& d = s_desc[at];
+    if (d.kind == kEnd) return;
+    const bool tiles = d.kind == kTile;
+    const int col = (d.strip % tiles_n) * kTileCols;
+    const int64_t e = d.strip / tiles_n, base = d.base;
+    const uint32_t edge = d.edge, rows = d.left, tile_k = d.tile_k;
+    const bool in = col + lane * 4 < N;            // N is a multiple of 16
+    const uint8_t* stage = s_data + at * L::kBytes;
+    const uint32_t none[4] = {0, 0, 0, 0};
+    if (tiles) {
+      if (edge & 1) most[0] = most[1] = most[2] = most[3] = 0.0f;
+#pragma unroll 1
+      for (uint32_t row = warp; row < rows; row += kWarps) {
+        const int64_t i = base + (int64_t)row * N;
+        Quad q;
+        take_quad<BITS, true>(stage, row, a.d.g_bf16, none, q);
+        step_quad<BITS>(rates, i + lane * 4, 1, q);
+        if (in) {
+          store_quad<BITS, true>(a.d, i, 128, q);
+#pragma unroll
+          for (int j = 0; j < 4; ++j) most[j] = max_abs(most[j], q.p[j], 0.0f);
+        }
+      }
+    } else {
+      if (edge & 1) columns_of<true>(a.d.most, a.scale, e, col, N, tile_k == 0 && warp == 0, x);
+#pragma unroll
+      for (uint32_t i = 0; i < kRows / kWarps; ++i) {
+        const uint32_t row = i * kWarps + warp;
+        float v[4];
+        lds_f32<true>(stage + row * 512, v);
+        const uint32_t w = codes_of(v, x);
+        if (row < rows && in)
+          __stcs(reinterpret_cast<uint32_t*>(a.codes + base + (int64_t)row * N) + lane, w);
+      }
+    }
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&s_empty[at]);
+    if (!tiles || !(edge & 2)) continue;
+    // a tile is done: its columns' largest magnitudes, then its slab's count
+#pragma unroll
+    for (int j = 0; j < 4; ++j) s_most[warp * kTileCols + lane * 4 + j] = most[j];
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&s_join[0]);
+    if (!mbar_wait_warp(&s_join[0], joins & 1, kWhereEpilogue)) return;
+    const int c = threadIdx.x;
+    if (c < kTileCols && col + c < N) {
+      float m = 0.0f;
+#pragma unroll
+      for (int w = 0; w < kWarps; w += 2)
+        m = max_abs(m, s_most[w * kTileCols + c], s_most[(w + 1) * kTileCols + c]);
+      atomicMax(a.d.most + e * N + col + c, __float_as_uint(m));
+    }
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&s_join[1]);
+    if (!mbar_wait_warp(&s_join[1], joins & 1, kWhereEpilogue)) return;
+    if (threadIdx.x == 0) {
+      const uint32_t strip = e * tiles_n + col / kTileCols;
+      __threadfence();
+      atomicAdd(a.counters + 1 + strip / a.per_slab, 1u);
+    }
+    ++joins;
+  }
+}
+
+// The same limit for every call of a kernel.
+template <typename F>
+cudaError_t allow_ring(F kernel, int bytes) {
+  return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+}
+
+template <int BITS, int kCapacity>
+cudaError_t launch_table(const AdamwCommon& c, const AdamwEntry* at, int num_sms, cudaStream_t s) {
+  static thread_local AdamwTable<kCapacity> t;   // up to 32 KB: not on the stack
   t.c = c;
-  t.c.count = count;
-  for (int i = 0; i < count; ++i) t.at[i] = at[i];
-  adamw_kernel<kCapacity><<<units, kThreads, 0, s>>>(t);
+  for (int i = 0; i < c.count; ++i) t.at[i] = at[i];
+  auto* kernel = adamw_kernel<BITS, kCapacity>;
+  const cudaError_t e = allow_ring(kernel, Layout<BITS>::kAll);
+  if (e != cudaSuccess) return e;
+  const uint32_t most = (uint32_t)num_sms * (BITS == 8 ? kPer8 : kPer32);
+  kernel<<<c.units < most ? c.units : most, kThreads, Layout<BITS>::kAll, s>>>(t);
   return cudaGetLastError();
+}
+
+uint32_t strips_of(int64_t n, int64_t K, int64_t N) {
+  return (uint32_t)(n / (K * N) * ((N + kTileCols - 1) / kTileCols));
+}
+uint32_t strips_per_slab(int64_t K) {
+  const int64_t tiles_k = (K + kTileRows - 1) / kTileRows;
+  return (uint32_t)((kSlabTiles + tiles_k - 1) / tiles_k);
 }
 
 }  // namespace
@@ -437,22 +833,52 @@ cudaError_t launch_table(const AdamwCommon& c, const AdamwEntry* at, int count, 
 
 using namespace fp8moe;
 
+FP8MOE_DEFINE_STATUS_TAKE(fp8moe_status_take_adamw)
+
 uint64_t fp8moe_adamw_units(const AdamwEntry& d) {
-  if (!d.tiles) return (uint64_t)(d.n + kUnit - 1) / kUnit;
-  const uint64_t E = (uint64_t)d.n / ((uint64_t)d.K * d.N);
-  return E * ((d.K + kTileRows - 1) / kTileRows) * ((d.N + kTileCols - 1) / kTileCols);
+  return d.n <= d.head ? 1 : (uint64_t)(d.n - d.head + kUnit - 1) / kUnit;
 }
 
-cudaError_t fp8moe_launch_adamw(const AdamwCommon& common, AdamwEntry* at, int count,
-                                cudaStream_t s) {
+cudaError_t fp8moe_launch_adamw(const AdamwCommon& common, AdamwEntry* at, int count, int bits,
+                                int num_sms, cudaStream_t s) {
+  AdamwCommon c = common;
   uint64_t units = 0;
   for (int i = 0; i < count; ++i) {
     at[i].first_unit = (uint32_t)units;
     units += fp8moe_adamw_units(at[i]);
   }
-  // a table of 16 entries is a launch's usual few KB of parameters, one of 256 nearly all of them
-  return count <= 16 ? launch_table<16>(common, at, count, (uint32_t)units, s)
-                     : launch_table<kAdamwEntries>(common, at, count, (uint32_t)units, s);
+  c.count = count, c.units = (uint32_t)units;
+  // a table of 16 entries is a launch's usual few KB of parameters, the other nearly all of them
+  if (count <= 16)
+    return bits == 8 ? launch_table<8, 16>(c, at, num_sms, s) : launch_table<32, 16>(c, at, num_sms, s);
+  return bits == 8 ? launch_table<8, kAdamwEntries>(c, at, num_sms, s)
+                   : launch_table<32, kAdamwEntries>(c, at, num_sms, s);
+}
+
+uint32_t fp8moe_adamw_slab_counters(int64_t n, int64_t K, int64_t N) {
+  return 1 + (strips_of(n, K, N) + strips_per_slab(K) - 1) / strips_per_slab(K);
+}
+void fp8moe_adamw_tile(int* cols, int* rows) {
+  *cols = kTileCols;
+  *rows = kStage / kTileCols;
+}
+
+cudaError_t fp8moe_launch_adamw_slabs(const AdamwSlabArgs& args, int bits, int num_sms,
+                                      cudaStream_t s) {
+  AdamwSlabArgs a = args;
+  a.strips = strips_of(a.d.n, a.d.K, a.d.N);
+  a.per_slab = strips_per_slab(a.d.K);
+  a.slabs = fp8moe_adamw_slab_counters(a.d.n, a.d.K, a.d.N) - 1;
+  a.units = 2 * a.strips * ((a.d.K + kTileRows - 1) / kTileRows);
+  auto launch = [&](auto* kernel, int per, int bytes) {
+    const cudaError_t e = allow_ring(kernel, bytes);
+    if (e != cudaSuccess) return e;
+    const uint32_t most = (uint32_t)(num_sms * per);
+    kernel<<<a.units < most ? a.units : most, kThreads, bytes, s>>>(a);
+    return cudaGetLastError();
+  };
+  return bits == 8 ? launch(adamw_slab_kernel<8>, kPer8, Layout<8>::kAll)
+                   : launch(adamw_slab_kernel<32>, kPer32, Layout<32>::kAll);
 }
 
 cudaError_t fp8moe_launch_adamw_prepare(AdamwRates* rates, const int64_t* step, int64_t host_step,
@@ -465,12 +891,10 @@ cudaError_t fp8moe_launch_adamw_prepare(AdamwRates* rates, const int64_t* step, 
   return cudaGetLastError();
 }
 
-cudaError_t fp8moe_launch_weight_codes(const float* p, int E, int K, int N, bool vec, bool have_most,
-                                       uint32_t* most, uint8_t* codes, float* scale,
-                                       cudaStream_t s) {
+cudaError_t fp8moe_launch_weight_codes(const float* p, int E, int K, int N, uint32_t* most,
+                                       uint8_t* codes, float* scale, cudaStream_t s) {
   const dim3 grid((N + kTileCols - 1) / kTileCols, (K + kTileRows - 1) / kTileRows, E);
-  if (!have_most) column_max_kernel<<<grid, kThreads, 0, s>>>(p, K, N, most);
-  if (vec) weight_codes_kernel<true><<<grid, kThreads, 0, s>>>(p, K, N, most, codes, scale);
-  else weight_codes_kernel<false><<<grid, kThreads, 0, s>>>(p, K, N, most, codes, scale);
+  column_max_kernel<<<grid, 32 * kWarps, 0, s>>>(p, K, N, most);
+  weight_codes_kernel<<<grid, 32 * kWarps, 0, s>>>(p, K, N, most, codes, scale);
   return cudaGetLastError();
 }

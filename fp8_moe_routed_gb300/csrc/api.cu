@@ -473,18 +473,62 @@ int check_adamw(const fp8moe_adamw_tensor& d) {
   return FP8MOE_OK;
 }
 
-int64_t adamw_columns(const fp8moe_adamw_tensor& d) {
-  return d.n > 0 && d.codes && d.K > 0 ? d.n / d.K : 0;
+// Words of the workspace for weights with codes: of each column, and the units' counters.
+int64_t adamw_columns(const fp8moe_adamw_tensor& d) { return d.n / d.K; }
+int64_t adamw_words(const fp8moe_adamw_tensor& d) {
+  if (d.n <= 0 || !d.codes || d.K < 1 || d.N < 1) return 0;
+  return adamw_columns(d) + fp8moe_adamw_slab_counters(d.n, d.K, d.N);
 }
 
-// The rates of a step on the device lie in front of the columns' largest magnitudes.
+// The first value from which on every array lies on a boundary that wide accesses need (16 bytes
+// for what is copied to shared memory, 8 for the stores of a copy), -1 if there is none: parts of one
+// flat buffer lie alike, wherever they begin. A block of an 8-bit moment begins with the tensor,
+// so that only 0 will do there.
+int adamw_head(const fp8moe_adamw_tensor& d) {
+  auto at = [](const void* p, int64_t bytes) { return reinterpret_cast<uintptr_t>(p) + bytes; };
+  const int g = d.g_type == FP8MOE_TYPE_BF16 ? 2 : 4, state = d.state_bits / 8;
+  for (int h = 0; h < (d.state_bits == 32 ? 8 : 1); ++h)
+    if (at(d.p, 4 * h) % 16 == 0 && at(d.g, g * h) % 16 == 0 && at(d.m, state * h) % 16 == 0 &&
+        at(d.v, state * h) % 16 == 0 && (!d.copy || at(d.copy, 2 * h) % 8 == 0))
+      return h;
+  return -1;
+}
+// Weights whose step goes by tiles, together with the codes. A block of an 8-bit moment has to lie
+// in one row of a tile.
+bool adamw_slabs(const fp8moe_adamw_tensor& d) {
+  return d.n > 0 && d.codes && aligned4(d.codes) && adamw_head(d) == 0 &&
+         (d.state_bits == 32 || d.N % 128 == 0);
+}
+int adamw_tmap(CUtensorMap* m, const void* base, int bytes, const fp8moe_adamw_tensor& d) {
+  int cols, rows;
+  fp8moe_adamw_tile(&cols, &rows);
+  const uint64_t K = (uint64_t)d.K, N = (uint64_t)d.N;
+  const uint64_t dims[3] = {N, K, (uint64_t)d.n / (K * N)};
+  const uint64_t strides[2] = {N * bytes, K * N * bytes};
+  const uint32_t box[3] = {(uint32_t)cols, (uint32_t)rows, 1};
+  return make_tmap(m, bytes == 4 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32
+                      : bytes == 2 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_UINT8,
+                   3, base, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_NONE);
+}
+AdamwEntry adamw_entry(const fp8moe_adamw_tensor& d, int32_t which, double lr) {
+  AdamwEntry w = {};
+  w.p = d.p, w.g = d.g, w.m = d.m, w.v = d.v, w.m_scale = d.m_scale, w.v_scale = d.v_scale;
+  w.copy = d.copy, w.n = d.n, w.weight_decay = d.weight_decay;
+  w.keep = (float)(1.0 - lr * d.weight_decay);
+  w.which = (uint32_t)which;
+  const int head = adamw_head(d);
+  w.g_bf16 = d.g_type == FP8MOE_TYPE_BF16, w.vec = head >= 0, w.head = (uint8_t)(head > 0 ? head : 0);
+  return w;
+}
+
+// The rates of a step on the device lie in front of the words of the weights with codes.
 constexpr size_t kAdamwRatesBytes = 256;
-static_assert(sizeof(AdamwRates) <= kAdamwRatesBytes, "the columns' words begin behind");
+static_assert(sizeof(AdamwRates) <= kAdamwRatesBytes, "the words of the weights with codes begin behind");
 
 size_t adamw_ws_bytes(const fp8moe_adamw_tensor* tensors, int32_t count, bool on_device) {
-  size_t columns = 0;
-  for (int32_t i = 0; i < count; ++i) columns += (size_t)adamw_columns(tensors[i]);
-  return columns || on_device ? kAdamwRatesBytes + round_up(columns * 4, 256) : 0;
+  size_t words = 0;
+  for (int32_t i = 0; i < count; ++i) words += (size_t)adamw_words(tensors[i]);
+  return words || on_device ? kAdamwRatesBytes + round_up(words * 4, 256) : 0;
 }
 
 }  // namespace
@@ -1181,51 +1225,50 @@ int fp8moe_adamw_step(const fp8moe_adamw_tensor* tensors, int32_t count, int64_t
   c.b2 = (float)beta2, c.c2 = (float)(1.0 - beta2);
   c.eps = (float)eps;
 
-  // as many launches as tables: 256 tensors or 2^30 units each
-  AdamwEntry at[kAdamwEntries];
-  int n = 0;
-  uint64_t units = 0;
-  uint32_t* columns = most;
-  for (int32_t i = 0; i < count; ++i) {
-    const fp8moe_adamw_tensor& d = tensors[i];
-    if (d.n == 0) continue;
-    AdamwEntry w = {};
-    w.p = d.p, w.g = d.g, w.m = d.m, w.v = d.v, w.m_scale = d.m_scale, w.v_scale = d.v_scale;
-    w.copy = d.copy, w.n = d.n, w.weight_decay = d.weight_decay;
-    w.keep = (float)(1.0 - lr * d.weight_decay);
-    w.which = (uint32_t)i;
-    w.g_bf16 = d.g_type == FP8MOE_TYPE_BF16, w.bits = (uint8_t)d.state_bits;
-    w.vec = aligned16(d.p) && aligned16(d.g) && aligned16(d.m) && aligned16(d.v) &&
-            aligned16(d.copy);
-    // a block of an 8-bit moment has to lie in one row of a tile
-    w.tiles = d.codes && w.vec && (d.state_bits == 32 || d.N % 128 == 0);
-    if (d.codes) {
-      w.K = (int32_t)d.K, w.N = (int32_t)d.N;
-      w.most = columns;
-      columns += adamw_columns(d);
+  // A launch for each table of tensors (at most 360 of them, or 2^30 units) with moments of the same kind, then
+  // the weights with codes, one after the other.
+  for (int bits = 8; bits <= 32; bits += 24) {
+    AdamwEntry at[kAdamwEntries];
+    int n = 0;
+    uint64_t units = 0;
+    for (int32_t i = 0; i < count; ++i) {
+      const fp8moe_adamw_tensor& d = tensors[i];
+      if (d.n == 0 || d.state_bits != bits || adamw_slabs(d)) continue;
+      const AdamwEntry w = adamw_entry(d, i, lr);
+      const uint64_t more = fp8moe_adamw_units(w);
+      if (n == kAdamwEntries || (n > 0 && units + more > (1u << 30))) {
+        e = fp8moe_launch_adamw(c, at, n, bits, sms, stream);
+        if (e != cudaSuccess) return cuda_fail(e);
+        n = 0, units = 0;
+      }
+      at[n++] = w;
+      units += more;
     }
-    const uint64_t more = fp8moe_adamw_units(w);
-    if (n == kAdamwEntries || (n > 0 && units + more > (1u << 30))) {
-      e = fp8moe_launch_adamw(c, at, n, stream);
-      if (e != cudaSuccess) return cuda_fail(e);
-      n = 0, units = 0;
-    }
-    at[n++] = w;
-    units += more;
+    if (n == 0) continue;
+    e = fp8moe_launch_adamw(c, at, n, bits, sms, stream);
+    if (e != cudaSuccess) return cuda_fail(e);
   }
-  e = fp8moe_launch_adamw(c, at, n, stream);
-  if (e != cudaSuccess) return cuda_fail(e);
-  columns = most;
   for (int32_t i = 0; i < count; ++i) {
     const fp8moe_adamw_tensor& d = tensors[i];
     if (d.n == 0 || !d.codes) continue;
-    const bool vec = aligned16(d.p) && aligned16(d.codes);
-    const bool tiles = aligned16(d.p) && aligned16(d.g) && aligned16(d.m) && aligned16(d.v) &&
-                       aligned16(d.copy) && (d.state_bits == 32 || d.N % 128 == 0);
-    e = fp8moe_launch_weight_codes(d.p, (int)(d.n / (d.K * d.N)), (int)d.K, (int)d.N, vec, tiles,
-                                   columns, d.codes, d.code_scale, stream);
+    if (adamw_slabs(d)) {
+      AdamwSlabArgs w = {};
+      static_cast<AdamwEntry&>(w.d) = adamw_entry(d, i, lr);
+      w.c = c, w.d.K = (int32_t)d.K, w.d.N = (int32_t)d.N, w.d.most = most;
+      w.codes = d.codes, w.scale = d.code_scale, w.counters = most + adamw_columns(d);
+      const int state = d.state_bits / 8;
+      rc = adamw_tmap(&w.tm_p, d.p, 4, d);
+      if (!rc) rc = adamw_tmap(&w.tm_g, d.g, d.g_type == FP8MOE_TYPE_BF16 ? 2 : 4, d);
+      if (!rc) rc = adamw_tmap(&w.tm_m, d.m, state, d);
+      if (!rc) rc = adamw_tmap(&w.tm_v, d.v, state, d);
+      if (rc) return rc;
+      e = fp8moe_launch_adamw_slabs(w, d.state_bits, sms, stream);
+    } else {
+      e = fp8moe_launch_weight_codes(d.p, (int)(d.n / (d.K * d.N)), (int)d.K, (int)d.N, most,
+                                     d.codes, d.code_scale, stream);
+    }
     if (e != cudaSuccess) return cuda_fail(e);
-    columns += adamw_columns(d);
+    most += adamw_words(d);
   }
   return FP8MOE_OK;
 }

@@ -236,14 +236,13 @@ struct AdamwEntry {
   float* m_scale;
   float* v_scale;
   void* copy;               // bf16, or null
-  uint32_t* most;           // tiles: [E, N], the columns' largest magnitudes (by atomicMax)
   int64_t n;
   double weight_decay;
   float keep;               // 1 - lr * weight_decay, unless the rates are on the device
   uint32_t first_unit;      // set by the launcher
   uint32_t which;           // the tensor's number in the call
-  int32_t K, N;             // tiles: weights [E, K, N]
-  uint8_t g_bf16, bits, vec, tiles;
+  uint8_t g_bf16;
+  uint8_t vec, head;        // from the value number `head` on, all arrays lie on 16 bytes
 };
 struct AdamwRates {         // from a step or a rate on the device
   double lr;
@@ -255,17 +254,39 @@ struct AdamwCommon {
   const float* grad_scale;
   float rate, root, b1, c1, b2, c2, eps;
   uint32_t key;
-  int count;
+  int count;                // set by the launcher, as is the next
+  uint32_t units;
 };
-constexpr int kAdamwEntries = 256;
+constexpr int kAdamwEntries = 360;     // of 88 bytes: a launch has 32764 bytes of parameters
 uint64_t fp8moe_adamw_units(const AdamwEntry& d);
-cudaError_t fp8moe_launch_adamw(const AdamwCommon& common, AdamwEntry* at, int count,
-                                cudaStream_t s);
+cudaError_t fp8moe_launch_adamw(const AdamwCommon& common, AdamwEntry* at, int count, int bits,
+                                int num_sms, cudaStream_t s);
+
+// One tensor of expert weights [E, K, N] with its codes; all arrays on 16 bytes, and with 8 bits N
+// a multiple of 128.
+struct AdamwSlabEntry : AdamwEntry {
+  uint32_t* most;           // [E, N], the columns' largest magnitudes: zeros to begin with
+  int32_t K, N;
+};
+struct AdamwSlabArgs {
+  CUtensorMap tm_p, tm_g, tm_m, tm_v;  // [E, K, N] boxes of fp8moe_adamw_tile()
+  AdamwCommon c;
+  AdamwSlabEntry d;
+  uint8_t* codes;
+  float* scale;
+  uint32_t* counters;       // fp8moe_adamw_slab_counters(), zeros to begin with: the next unit,
+                            // then the tiles done of each slab
+  uint32_t strips, per_slab, slabs, units;   // set by the launcher
+};
+uint32_t fp8moe_adamw_slab_counters(int64_t n, int64_t K, int64_t N);
+void fp8moe_adamw_tile(int* cols, int* rows);
+cudaError_t fp8moe_launch_adamw_slabs(const AdamwSlabArgs& args, int bits, int num_sms,
+                                      cudaStream_t s);
 cudaError_t fp8moe_launch_adamw_prepare(AdamwRates* rates, const int64_t* step, int64_t host_step,
                                         const float* lr, double host_lr, double beta1,
                                         double beta2, uint32_t seed, uint32_t* most, int64_t count,
                                         cudaStream_t s);
-// have_most: the step has left the columns' largest magnitudes; else they are taken here.
-cudaError_t fp8moe_launch_weight_codes(const float* p, int E, int K, int N, bool vec, bool have_most,
-                                       uint32_t* most, uint8_t* codes, float* scale,
-                                       cudaStream_t s);
+// The codes of weights that the step went through in order. most: zeros to begin with.
+cudaError_t fp8moe_launch_weight_codes(const float* p, int E, int K, int N, uint32_t* most,
+                                       uint8_t* codes, float* scale, cudaStream_t s);
+cudaError_t fp8moe_status_take_adamw(uint32_t** word);

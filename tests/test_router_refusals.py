@@ -113,7 +113,7 @@ def test_adamw_tensors():
                 {**codes, "n": 32 * 40, "N": 40}):
         assert step(tensor(), tensor(**bad)) == EALIGN, bad
     assert step(tensor(**codes), ws=None) == EWORKSPACE
-    assert step(tensor(**codes), wsb=256 + 4 * 2 * 48 - 1) == EWORKSPACE
+    assert step(tensor(**codes), wsb=256 + 4 * (2 * 48 + 2) - 1) == EWORKSPACE
 
 
 def test_adamw_workspace():
@@ -123,7 +123,7 @@ def test_adamw_workspace():
     assert size() == 0 and size(tensor()) == 0 and size(tensor(), on_device=1) == 256
     codes = dict(codes=16, code_scale=16, n=2 * 32 * 48, K=32, N=48)
     assert size(tensor(**codes)) == 256 + 512
-    assert size(tensor(**codes), tensor(**codes), on_device=1) == 256 + 768
+    assert size(tensor(**codes), tensor(**codes), on_device=1) == 256 + 1024
 
 
 def test_python_side_refuses_what_is_no_cuda_tensor():
