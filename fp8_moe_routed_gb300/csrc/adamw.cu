@@ -15,8 +15,10 @@
 
 #include "fp8moe_status.cuh"
 #include "kernels.h"
+#include "pdl.cuh"
 #include "ptx.cuh"
 #include "quantize.cuh"
+#include "vec16.cuh"
 
 namespace fp8moe {
 namespace {
@@ -67,7 +69,7 @@ struct Quad {
 };
 
 struct Rates {
-  float keep, rate, root, b1, c1, b2, c2, eps, grad;
+  float keep, rate, root, b1, c1, b2, c2, eps, grad, minus_zero;
   uint32_t key;
   double lr;
 };
@@ -287,12 +289,12 @@ __device__ __forceinline__ float block_scale(uint32_t most) {
 }
 
 // |x| as an e4m3 code by chance, in the top byte: |x| / scale * 2^-120 has the code's bits on
-// top of its own (both formats' subnormals included), and the random ones, 16 bits and a one
-// behind them for the middle of their step, decide about the 20 below. The largest of a block is
-// 448 to within 4 units (its scale, the inverse and two products are rounded), where the random
-// bits reach the next code only from 8 units on: 0x7F, a NaN's code, is for spoilt blocks alone.
-__device__ __forceinline__ uint32_t encode(float x, float inverse, uint32_t random24) {
-  const float y = __fmul_rn(__fmul_rn(fabsf(x), inverse), 0x1p-120f);
+// top of its own (both formats' subnormals included; its sign falls out on the left), and the random
+// ones, 16 bits and a one behind them for the middle of their step, decide about the 20 below. The
+// largest of a block is 448 to within 4 units (its scale, the inverse and two products are
+// rounded), where the random bits reach the next code only from 8 units on: 0x7F, a NaN's code, is
+// for spoilt blocks alone.
+__device__ __forceinline__ uint32_t encode(float y, uint32_t random24) {
   return __float_as_uint(y) * 16u + random24;
 }
 __device__ __forceinline__ uint32_t top_bytes(uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
@@ -306,45 +308,114 @@ __device__ __forceinline__ float max_abs(float a, float b, float c) {
   return r;
 }
 
+// A product of its own: what is added to it later can not be joined with it into one rounding, as
+// the compiler does with packed products, and with those of a -0 that it knows.
+__device__ __forceinline__ float2 prod2(float2 a, float2 b, float minus_zero) {
+  return fma2(a, b, both(minus_zero));
+}
+
+__device__ __forceinline__ float rsqrt_approx(float x) {
+  float y;
+  asm("rsqrt.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ float rcp_approx(float x) {
+  float y;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+// Square root and quotient of two values at once by Newton steps whose last takes the exact
+// remainder (Markstein, "Computation of elementary functions on the IBM RISC System/6000
+// processor", 1990): the nearest f32 but for about one in 2^22, where the exact value lies next to
+// the middle of two. x, and a and b with their quotient, well inside the range of normal numbers.
+__device__ __forceinline__ float2 sqrt2(float2 x) {
+  const float2 y = make_float2(rsqrt_approx(x.x), rsqrt_approx(x.y));
+  const float2 s = mul2(x, y);
+  const float2 rest = fma2(s, s, mul2(x, both(-1.0f)));
+  return fma2(rest, mul2(y, both(-0.5f)), s);
+}
+__device__ __forceinline__ float2 inverse2(float2 b, float2 minus_b) {
+  const float2 y = make_float2(rcp_approx(b.x), rcp_approx(b.y));
+  return fma2(y, fma2(minus_b, y, both(1.0f)), y);
+}
+__device__ __forceinline__ float2 div2(float2 a, float2 b) {
+  const float2 minus_b = mul2(b, both(-1.0f));
+  const float2 y = inverse2(b, minus_b);
+  const float2 q = mul2(a, y);
+  return fma2(fma2(minus_b, q, a), y, q);
+}
+
 // place: of the lane's first value in the tensor; apart: between two of its values.
 template <int BITS>
 __device__ __forceinline__ void step_quad(const Rates& r, uint64_t place, uint32_t apart, Quad& q) {
-  float root[4];
   if constexpr (BITS == 8) {
     decode4(q.mc, q.ms, q.m);
     decode4(q.vc, q.vs, q.v);
   }
+  auto prod = [&](float2 a, float b) { return prod2(a, both(b), r.minus_zero); };
+  float2 p[2], m[2], v[2], root[2], step[2];
 #pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    const float g = __fmul_rn(q.g[j], r.grad);
-    const float v = BITS == 8 ? __fmul_rn(q.v[j], q.v[j]) : q.v[j];
-    q.m[j] = __fadd_rn(__fmul_rn(q.m[j], r.b1), __fmul_rn(g, r.c1));
-    q.v[j] = __fadd_rn(__fmul_rn(v, r.b2), __fmul_rn(__fmul_rn(g, r.c2), g));
-    root[j] = __fsqrt_rn(q.v[j]);
-    const float step = __fdiv_rn(q.m[j], __fadd_rn(__fmul_rn(root[j], r.root), r.eps));
-    q.p[j] = __fsub_rn(__fmul_rn(q.p[j], r.keep), __fmul_rn(step, r.rate));
+  for (int h = 0; h < 2; ++h) {
+    const float2 g = mul2(make_float2(q.g[2 * h], q.g[2 * h + 1]), both(r.grad));
+    p[h] = make_float2(q.p[2 * h], q.p[2 * h + 1]);
+    m[h] = make_float2(q.m[2 * h], q.m[2 * h + 1]);
+    v[h] = make_float2(q.v[2 * h], q.v[2 * h + 1]);
+    if constexpr (BITS == 8) v[h] = mul2(v[h], v[h]);
+    m[h] = add2(prod(m[h], r.b1), prod(g, r.c1));
+    v[h] = add2(prod(v[h], r.b2), prod2(mul2(g, both(r.c2)), g, r.minus_zero));
+  }
+  const float low = fminf(fminf(v[0].x, v[0].y), fminf(v[1].x, v[1].y));
+  const float high = fmaxf(fmaxf(v[0].x, v[0].y), fmaxf(v[1].x, v[1].y));
+  if (low >= 0x1p-126f && high <= 0x1p126f) {    // then the divisors are in [2^-63, 2^90]
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      root[h] = sqrt2(v[h]);
+      step[h] = div2(m[h], add2(prod(root[h], r.root), both(r.eps)));
+    }
+  } else {
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      root[h] = make_float2(__fsqrt_rn(v[h].x), __fsqrt_rn(v[h].y));
+      const float2 d = add2(prod(root[h], r.root), both(r.eps));
+      step[h] = make_float2(__fdiv_rn(m[h].x, d.x), __fdiv_rn(m[h].y, d.y));
+    }
+  }
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    p[h] = add2(prod(p[h], r.keep), prod(step[h], -r.rate));
+    q.p[2 * h] = p[h].x, q.p[2 * h + 1] = p[h].y;
+    q.m[2 * h] = m[h].x, q.m[2 * h + 1] = m[h].y;
+    q.v[2 * h] = v[h].x, q.v[2 * h + 1] = v[h].y;
   }
   if constexpr (BITS == 8) {
     // (values that do not exist are zeros, and so are their moments)
-    const float mm = max_abs(max_abs(q.m[0], q.m[1], q.m[2]), q.m[3], 0.0f);
-    const float vm = max_abs(max_abs(root[0], root[1], root[2]), root[3], 0.0f);
+    const float mm = max_abs(max_abs(m[0].x, m[0].y, m[1].x), m[1].y, 0.0f);
+    const float vm = max_abs(max_abs(root[0].x, root[0].y, root[1].x), root[1].y, 0.0f);
     q.ms = block_scale(__reduce_max_sync(kAll, __float_as_uint(mm)));
     q.vs = block_scale(__reduce_max_sync(kAll, __float_as_uint(vm)));
-    const float mi = q.ms != 0.0f ? __frcp_rn(q.ms) : 0.0f;
-    const float vi = q.vs != 0.0f ? __frcp_rn(q.vs) : 0.0f;
+    const float2 scale = make_float2(q.ms, q.vs);
+    float2 inverse = inverse2(scale, mul2(scale, both(-1.0f)));
+    inverse.x = q.ms != 0.0f ? inverse.x : 0.0f;
+    inverse.y = q.vs != 0.0f ? inverse.y : 0.0f;
     const uint32_t least = q.vs != 0.0f ? 0x01000000u : 0u;
     // a block lies on one side of 2^32, as its first place is a multiple of 128
     const uint32_t base = random_place(place, r.key);
     uint32_t mc[4], vc[4];
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const uint32_t bits = random_bits(base + j * apart * kPlace);
-      mc[j] = (__float_as_uint(q.m[j]) & 0x80000000u) |
-              (encode(q.m[j], mi, __byte_perm(bits, 0x80u, 0x7104)) & 0x7fffffffu);
-      // a second moment that is not zero (its root then is at least 2^-75) never becomes zero:
-      // m / eps would follow
-      vc[j] = max(encode(root[j], vi, __byte_perm(bits, 0x80u, 0x7324)),
-                  min(__float_as_uint(root[j]), least));
+    for (int h = 0; h < 2; ++h) {
+      const float2 my = mul2(mul2(m[h], both(inverse.x)), both(0x1p-120f));
+      const float2 vy = mul2(mul2(root[h], both(inverse.y)), both(0x1p-120f));
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const int j = 2 * h + i;
+        const uint32_t bits = random_bits(base + j * apart * kPlace);
+        mc[j] = (__float_as_uint(q.m[j]) & 0x80000000u) |
+                (encode(i ? my.y : my.x, __byte_perm(bits, 0x80u, 0x7104)) & 0x7fffffffu);
+        // a second moment that is not zero (its root then is at least 2^-75) never becomes zero:
+        // m / eps would follow
+        vc[j] = max(encode(i ? vy.y : vy.x, __byte_perm(bits, 0x80u, 0x7324)),
+                    min(__float_as_uint(i ? root[h].y : root[h].x), least));
+      }
     }
     q.mc = top_bytes(mc[0], mc[1], mc[2], mc[3]);
     q.vc = top_bytes(vc[0], vc[1], vc[2], vc[3]);
@@ -411,15 +482,23 @@ __device__ __forceinline__ void linear_stage(const AdamwEntry& d, const Rates& r
     shift[0] = low(d.p, a.base * 4), shift[1] = low(d.g, a.base * (d.g_bf16 ? 2 : 4));
     shift[2] = low(d.m, a.base * (BITS / 8)), shift[3] = low(d.v, a.base * (BITS / 8));
   }
+  if (a.kind == kWide) {
+#pragma unroll
+    for (uint32_t n = 0; n < kBlocks / kWarps; ++n) {
+      const uint32_t block = n * kWarps + warp;
+      const int64_t i = a.base + block * 128;
+      Quad q;
+      take_quad<BITS, true>(stage, block, d.g_bf16, none, q);
+      step_quad<BITS>(r, i + lane * 4, 1, q);
+      store_quad<BITS, true>(d, i, 128, q);
+    }
+    return;
+  }
 #pragma unroll 1
   for (uint32_t block = warp; block < kBlocks; block += kWarps) {
     const int64_t i = a.base + block * 128;
     Quad q;
-    if (a.kind == kWide) {
-      take_quad<BITS, true>(stage, block, d.g_bf16, none, q);
-      step_quad<BITS>(r, i + lane * 4, 1, q);
-      store_quad<BITS, true>(d, i, 128, q);
-    } else {
+    {
       uint32_t left = 128;
       if (a.kind == kNarrow) {
         take_quad<BITS, false>(stage, block, d.g_bf16, shift, q);
@@ -437,6 +516,7 @@ __device__ __forceinline__ void linear_stage(const AdamwEntry& d, const Rates& r
 // What a call's tensors share, and what is a tensor's own.
 __device__ __forceinline__ Rates rates_of(const AdamwCommon& c) {
   Rates r;
+  r.minus_zero = c.minus_zero;
   r.b1 = c.b1, r.c1 = c.c1, r.b2 = c.b2, r.c2 = c.c2, r.eps = c.eps;
   r.grad = c.grad_scale != nullptr ? *c.grad_scale : 1.0f;
   r.rate = c.rate, r.root = c.root, r.key = c.key, r.lr = 0.0;
@@ -500,6 +580,7 @@ __global__ void __launch_bounds__(kThreads, BITS == 32 ? kPer32 : kPer8) adamw_k
     if (!going) f.drain();
     return;
   }
+  if (c.prepared) pdl_wait();                    // the fetching warp needs nothing of it
   const Rates all = rates_of(c);
   for (uint32_t n = 0;; ++n) {
     const uint32_t at = n % L::kStages;
@@ -518,6 +599,7 @@ __global__ void __launch_bounds__(kThreads, BITS == 32 ? kPer32 : kPer8) adamw_k
 __global__ void adamw_prepare_kernel(AdamwRates* rates, const int64_t* step, int64_t host_step,
                                      const float* lr, double host_lr, double beta1, double beta2,
                                      uint32_t seed, uint32_t* most, int64_t count) {
+  pdl_launch_dependents();
   const int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x;
   if (rates != nullptr && i == 0) {
     const int64_t t = step != nullptr ? *step : host_step;
@@ -684,6 +766,7 @@ __global__ void __launch_bounds__(kThreads, BITS == 32 ? kPer32 : kPer8) adamw_s
   if (warp == kWarps) {
     Fetcher<BITS> f = {ring};
     bool going = true;
+    pdl_wait();
     uint32_t next = lane == 0 ? atomicAdd(a.counters, 1u) : 0u;
     while (going) {
       const uint32_t unit = __shfl_sync(kAll, next, 0);
@@ -730,6 +813,7 @@ __global__ void __launch_bounds__(kThreads, BITS == 32 ? kPer32 : kPer8) adamw_s
     return;
   }
 
+  pdl_wait();
   const Rates rates = rates_for(rates_of(a.c), a.c, a.d);
   float most[4];
   Columns x;
@@ -807,6 +891,22 @@ cudaError_t allow_ring(F kernel, int bytes) {
   return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
 }
 
+// behind: may start before the kernel in front of it (adamw_prepare_kernel) has ended.
+template <typename A>
+cudaError_t launch_behind(void (*kernel)(A), uint32_t grid, int bytes, bool behind, const A& args,
+                          cudaStream_t s) {
+  cudaLaunchAttribute attr[1];
+  pdl_attribute(attr[0]);
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(grid);
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = (size_t)bytes;
+  cfg.stream = s;
+  cfg.attrs = attr;
+  cfg.numAttrs = behind ? 1 : 0;
+  return cudaLaunchKernelEx(&cfg, kernel, args);
+}
+
 template <int BITS, int kCapacity>
 cudaError_t launch_table(const AdamwCommon& c, const AdamwEntry* at, int num_sms, cudaStream_t s) {
   static thread_local AdamwTable<kCapacity> t;   // up to 32 KB: not on the stack
@@ -816,8 +916,7 @@ cudaError_t launch_table(const AdamwCommon& c, const AdamwEntry* at, int num_sms
   const cudaError_t e = allow_ring(kernel, Layout<BITS>::kAll);
   if (e != cudaSuccess) return e;
   const uint32_t most = (uint32_t)num_sms * (BITS == 8 ? kPer8 : kPer32);
-  kernel<<<c.units < most ? c.units : most, kThreads, Layout<BITS>::kAll, s>>>(t);
-  return cudaGetLastError();
+  return launch_behind(kernel, c.units < most ? c.units : most, Layout<BITS>::kAll, c.prepared != 0, t, s);
 }
 
 uint32_t strips_of(int64_t n, int64_t K, int64_t N) {
@@ -874,8 +973,7 @@ cudaError_t fp8moe_launch_adamw_slabs(const AdamwSlabArgs& args, int bits, int n
     const cudaError_t e = allow_ring(kernel, bytes);
     if (e != cudaSuccess) return e;
     const uint32_t most = (uint32_t)(num_sms * per);
-    kernel<<<a.units < most ? a.units : most, kThreads, bytes, s>>>(a);
-    return cudaGetLastError();
+    return launch_behind(kernel, a.units < most ? a.units : most, bytes, a.c.prepared != 0, a, s);
   };
   return bits == 8 ? launch(adamw_slab_kernel<8>, kPer8, Layout<8>::kAll)
                    : launch(adamw_slab_kernel<32>, kPer32, Layout<32>::kAll);

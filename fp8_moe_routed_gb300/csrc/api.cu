@@ -1224,6 +1224,8 @@ int fp8moe_adamw_step(const fp8moe_adamw_tensor* tensors, int32_t count, int64_t
   c.b1 = (float)beta1, c.c1 = (float)(1.0 - beta1);
   c.b2 = (float)beta2, c.c2 = (float)(1.0 - beta2);
   c.eps = (float)eps;
+  c.minus_zero = -0.0f;
+  c.prepared = need > 0;
 
   // A launch for each table of tensors (at most 360 of them, or 2^30 units) with moments of the same kind, then
   // the weights with codes, one after the other.
@@ -1239,6 +1241,7 @@ int fp8moe_adamw_step(const fp8moe_adamw_tensor* tensors, int32_t count, int64_t
       if (n == kAdamwEntries || (n > 0 && units + more > (1u << 30))) {
         e = fp8moe_launch_adamw(c, at, n, bits, sms, stream);
         if (e != cudaSuccess) return cuda_fail(e);
+        c.prepared = 0;
         n = 0, units = 0;
       }
       at[n++] = w;
@@ -1247,6 +1250,7 @@ int fp8moe_adamw_step(const fp8moe_adamw_tensor* tensors, int32_t count, int64_t
     if (n == 0) continue;
     e = fp8moe_launch_adamw(c, at, n, bits, sms, stream);
     if (e != cudaSuccess) return cuda_fail(e);
+    c.prepared = 0;
   }
   for (int32_t i = 0; i < count; ++i) {
     const fp8moe_adamw_tensor& d = tensors[i];
@@ -1263,6 +1267,7 @@ int fp8moe_adamw_step(const fp8moe_adamw_tensor* tensors, int32_t count, int64_t
       if (!rc) rc = adamw_tmap(&w.tm_v, d.v, state, d);
       if (rc) return rc;
       e = fp8moe_launch_adamw_slabs(w, d.state_bits, sms, stream);
+      c.prepared = 0;
     } else {
       e = fp8moe_launch_weight_codes(d.p, (int)(d.n / (d.K * d.N)), (int)d.K, (int)d.N, most,
                                      d.codes, d.code_scale, stream);

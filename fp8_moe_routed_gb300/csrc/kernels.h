@@ -253,7 +253,9 @@ struct AdamwCommon {
   const AdamwRates* rates;  // null: the values below
   const float* grad_scale;
   float rate, root, b1, c1, b2, c2, eps;
+  float minus_zero;         // -0, of which the compiler knows nothing
   uint32_t key;
+  int prepared;             // the kernel right in front of this launch is the preparation
   int count;                // set by the launcher, as is the next
   uint32_t units;
 };
