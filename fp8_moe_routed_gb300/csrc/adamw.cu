@@ -109,8 +109,8 @@ struct Fetcher {
   Ring ring;
   uint32_t count = 0;
 
-  // room() is waited for; then lane 0 names the bytes that will come, and every lane enters a
-  // scale, or that it has none
+  // room() is waited for; then lane 0 names the bytes that will come, and every lane ends its part,
+  // which may be a small copy of its own
   __device__ __forceinline__ bool room() {
     const uint32_t round = count / L::kStages;
     return round == 0 ||
@@ -124,21 +124,19 @@ struct Fetcher {
     if (bytes) mbar_arrive_expect_tx(full(), bytes);
     else mbar_arrive(full());
   }
-  __device__ __forceinline__ void end(const float* scale) {
-    if constexpr (BITS == 8) {
-      if (scale != nullptr) {
-        cp_async4(data() + L::kScales + (threadIdx.x & 31) * 4, scale);
-        cp_async_mbar_arrive(full());
-      } else {
-        mbar_arrive(full());
-      }
-    }
+  __device__ __forceinline__ void end() {
+    mbar_arrive(full());
+    ++count;
+  }
+  __device__ __forceinline__ void end_scale(const float* scale) {
+    cp_async4(data() + L::kScales + (threadIdx.x & 31) * 4, scale);
+    cp_async_mbar_arrive(full());
     ++count;
   }
   __device__ __forceinline__ bool empty_stage(const Desc& d) {
     if (!room()) return false;
     if ((threadIdx.x & 31) == 0) begin(d, 0);
-    end(nullptr);
+    end();
     return true;
   }
   // kWide or kNarrow: kStage values from d.base on, whole blocks, all inside of the tensor
@@ -167,9 +165,9 @@ struct Fetcher {
     }
     __syncwarp();
     if constexpr (BITS == 8)
-      end((lane < kBlocks ? e.m_scale : e.v_scale) + (d.base >> 7) + lane % kBlocks);
+      end_scale((lane < kBlocks ? e.m_scale : e.v_scale) + (d.base >> 7) + lane % kBlocks);
     else
-      end(nullptr);
+      end();
     return true;
   }
   // what was on its way when a wait ran out is waited for, so that no copy outlives the CTA
@@ -185,7 +183,7 @@ template <int BITS>
 __device__ __forceinline__ void ring_init(const Ring& r) {
   if (threadIdx.x == 0) {
     for (int i = 0; i < Layout<BITS>::kStages; ++i) {
-      mbar_init(&r.full[i], BITS == 8 ? 33 : 1);
+      mbar_init(&r.full[i], 33);
       mbar_init(&r.empty[i], kWarps);
     }
     fence_mbar_init();
@@ -639,23 +637,15 @@ __global__ void __launch_bounds__(32 * kWarps) column_max_kernel(const float* p,
 }
 
 // codes = e4m3(p / scale), scale = max(column's largest, 1e-12) / 448, both as the library's
-// other quantisers have them (quantize.cuh). A lane's four columns follow each other (WIDE) or are
-// 32 apart.
+// other quantisers have them (quantize.cuh). For four columns of a lane.
 struct Columns {
   float s[4], rl[4], rh[4];
 };
-template <bool WIDE>
-__device__ __forceinline__ void columns_of(const uint32_t* most, float* scale, int64_t e, int col,
-                                           int N, bool first, Columns& x) {
-  const int lane = threadIdx.x & 31;
+__device__ __forceinline__ void columns_of(const float (&top)[4], Columns& x) {
 #pragma unroll
   for (int j = 0; j < 4; ++j) {
-    const int c = col + (WIDE ? lane * 4 + j : j * 32 + lane);
-    float a = c < N ? __uint_as_float(__ldcg(most + e * N + c)) : 1.0f;
-    a = a < kEps ? kEps : a;                     // a NaN stays
-    x.s[j] = __fdiv_rn(a, kE4m3Max);
+    x.s[j] = __fdiv_rn(top[j] < kEps ? kEps : top[j], kE4m3Max);   // a NaN stays
     bracket(x.s[j], x.rl[j], x.rh[j]);
-    if (first && c < N) scale[e * N + c] = x.s[j];
   }
 }
 __device__ __forceinline__ uint32_t codes_of(const float (&v)[4], const Columns& x) {
@@ -673,8 +663,17 @@ __global__ void __launch_bounds__(32 * kWarps) weight_codes_kernel(const float* 
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int col = blockIdx.x * kTileCols, k0 = blockIdx.y * kTileRows;
   const int64_t e = blockIdx.z;
+  float top[4];
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const int c = col + j * 32 + lane;
+    top[j] = c < N ? __uint_as_float(most[e * N + c]) : 0.0f;
+  }
   Columns x;
-  columns_of<false>(most, scale, e, col, N, k0 == 0 && warp == 0, x);
+  columns_of(top, x);
+#pragma unroll
+  for (int j = 0; j < 4; ++j)
+    if (k0 == 0 && warp == 0 && col + j * 32 + lane < N) scale[e * N + col + j * 32 + lane] = x.s[j];
   const int64_t base = (e * K + k0) * N + col;
   for (int row = warp; row < kTileRows && k0 + row < K; row += kWarps) {
     float v[4];
@@ -742,31 +741,40 @@ __device__ __forceinline__ UnitOf unit_of(const AdamwSlabArgs& a, uint32_t unit,
   return u;
 }
 
+// The arrays' warps: kWarps that work, one that fetches, one that closes tiles.
+constexpr int kSlabThreads = kThreads + 32;
 template <int BITS>
-__global__ void __launch_bounds__(kThreads, BITS == 32 ? kPer32 : kPer8) adamw_slab_kernel(
+__global__ void __launch_bounds__(kSlabThreads, BITS == 32 ? kPer32 : kPer8) adamw_slab_kernel(
     const __grid_constant__ AdamwSlabArgs a) {
   using L = Layout<BITS>;
   extern __shared__ __align__(128) uint8_t s_data[];
-  __shared__ uint64_t s_full[L::kStages], s_empty[L::kStages], s_join[2];
+  __shared__ uint64_t s_full[L::kStages], s_empty[L::kStages], s_tile[2], s_closed[2];
   __shared__ Desc s_desc[L::kStages];
-  __shared__ float s_most[kWarps * kTileCols];
+  __shared__ float s_most[2][kWarps * kTileCols];    // of two tiles, in turn
+  __shared__ uint32_t s_strip[2];
+  constexpr uint32_t kNoStrip = 0xffffffffu;
   const Ring ring = {s_full, s_empty, s_desc, s_data};
   if (threadIdx.x == 0) {
-    mbar_init(&s_join[0], kWarps);
-    mbar_init(&s_join[1], kWarps);
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&s_tile[i], kWarps);
+      mbar_init(&s_closed[i], 1);
+    }
   }
   ring_init<BITS>(ring);
   __syncthreads();
+  pdl_wait();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int K = a.d.K, N = a.d.N;
   const uint32_t tiles_k = (K + kTileRows - 1) / kTileRows;
   const uint32_t tiles_n = (N + kTileCols - 1) / kTileCols;
-  constexpr int kRows = kStage / kTileCols;      // of a stage
+  constexpr int kRows = kStage / kTileCols;      // of a box
+  // a stage of codes has two boxes, the second one where the gradients would be, and the columns'
+  // largest magnitudes in the place of the first moments
+  constexpr int kCodesMost = L::kM;
 
   if (warp == kWarps) {
     Fetcher<BITS> f = {ring};
     bool going = true;
-    pdl_wait();
     uint32_t next = lane == 0 ? atomicAdd(a.counters, 1u) : 0u;
     while (going) {
       const uint32_t unit = __shfl_sync(kAll, next, 0);
@@ -781,31 +789,47 @@ __global__ void __launch_bounds__(kThreads, BITS == 32 ? kPer32 : kPer8) adamw_s
       }
       const int e = u.strip / tiles_n, col = (u.strip % tiles_n) * kTileCols;
       const int rows = min(kTileRows, K - (int)u.tile_k * kTileRows);
-      for (int row = 0; going && row < rows; row += kRows) {
+      const int each = u.tiles ? kRows : 2 * kRows;
+      for (int row = 0; going && row < rows; row += each) {
         Desc d;
         d.kind = u.tiles ? kTile : kCodes;
         d.entry = 0, d.strip = u.strip, d.tile_k = u.tile_k;
-        d.left = min(kRows, rows - row);
-        d.edge = (row == 0 ? 1 : 0) + (row + kRows >= rows ? 2 : 0);
+        d.left = min(each, rows - row);
+        d.edge = (row == 0 ? 1 : 0) + (row + each >= rows ? 2 : 0);
         const int k = u.tile_k * kTileRows + row;
         d.base = ((int64_t)e * K + k) * N + col;
         going = f.room();
         if (!going) break;
-        if (lane == 0) {
-          constexpr uint32_t kValues = kStage;
-          f.begin(d, kValues * 4 + (u.tiles ? kValues * ((a.d.g_bf16 ? 2 : 4) + 2 * BITS / 8) : 0));
-          tma_load_3d(f.data(), &a.tm_p, f.full(), col, k, e);
-          if (u.tiles) {
+        if (u.tiles) {
+          if (lane == 0) {
+            f.begin(d, kStage * (4 + (a.d.g_bf16 ? 2 : 4) + 2 * BITS / 8));
+            tma_load_3d(f.data(), &a.tm_p, f.full(), col, k, e);
             tma_load_3d(f.data() + L::kG, &a.tm_g, f.full(), col, k, e);
             tma_load_3d(f.data() + L::kM, &a.tm_m, f.full(), col, k, e);
             tma_load_3d(f.data() + L::kV, &a.tm_v, f.full(), col, k, e);
           }
+          __syncwarp();
+          if constexpr (BITS == 8) {
+            const int r = lane % kBlocks < (int)d.left ? lane % kBlocks : 0;
+            f.end_scale((lane < kBlocks ? a.d.m_scale : a.d.v_scale) + (d.base >> 7) +
+                        (int64_t)r * (N >> 7));
+          } else {
+            f.end();
+          }
+        } else {
+          if (lane == 0) {
+            f.begin(d, 2 * kStage * 4);
+            tma_load_3d(f.data(), &a.tm_p, f.full(), col, k, e);
+            tma_load_3d(f.data() + L::kG, &a.tm_p, f.full(), col, k + kRows, e);
+          }
+          __syncwarp();
+          // 16 bytes of four columns, past the L1; N is a multiple of 16
+          const uint32_t here = (d.edge & 1) && col + lane * 4 < N ? 16 : 0;
+          cp_async16(f.data() + kCodesMost + lane * 16,
+                     a.d.most + (int64_t)e * N + col + (here ? lane * 4 : 0), here);
+          cp_async_mbar_arrive(f.full());
+          ++f.count;
         }
-        __syncwarp();
-        const int r = lane % kBlocks < (int)d.left ? lane % kBlocks : 0;
-        f.end(BITS == 8 && u.tiles
-                  ? (lane < kBlocks ? a.d.m_scale : a.d.v_scale) + (d.base >> 7) + (int64_t)r * (N >> 7)
-                  : nullptr);
       }
     }
     if (going) going = f.empty_stage(Desc{});      // kEnd
@@ -813,75 +837,103 @@ __global__ void __launch_bounds__(kThreads, BITS == 32 ? kPer32 : kPer8) adamw_s
     return;
   }
 
-  pdl_wait();
+  if (warp == kWarps + 1) {
+    // closes tiles: their columns' largest magnitudes, then, when all of a tile's stores can be
+    // seen, its slab's count (the working warps go on meanwhile)
+    for (uint32_t n = 0;; ++n) {
+      if (!mbar_wait_warp(&s_tile[n & 1], (n >> 1) & 1, kWhereDrain)) return;
+      const uint32_t strip = s_strip[n & 1];
+      if (strip == kNoStrip) return;
+      const int64_t e = strip / tiles_n;
+      const int col = (strip % tiles_n) * kTileCols;
+#pragma unroll
+      for (int j = 0; j < kTileCols / 32; ++j) {
+        const int c = j * 32 + lane;
+        float m = 0.0f;
+#pragma unroll
+        for (int w = 0; w < kWarps; w += 2)
+          m = max_abs(m, s_most[n & 1][w * kTileCols + c], s_most[n & 1][(w + 1) * kTileCols + c]);
+        if (col + c < N) atomicMax(a.d.most + e * N + col + c, __float_as_uint(m));
+      }
+      __threadfence();
+      __syncwarp();
+      if (lane == 0) {
+        mbar_arrive(&s_closed[n & 1]);
+        atomicAdd(a.counters + 1 + strip / a.per_slab, 1u);
+      }
+    }
+  }
+
   const Rates rates = rates_for(rates_of(a.c), a.c, a.d);
   float most[4];
   Columns x;
-  uint32_t joins = 0;
+  uint32_t tiles = 0;                                // closed by this warp
   for (uint32_t n = 0;; ++n) {
     const uint32_t at = n % L::kStages;
     if (!mbar_wait_warp(&s_full[at], (n / L::kStages) & 1, kWhereEpilogue)) return;
     const Desc& d = s_desc[at];
-    if (d.kind == kEnd) return;
-    const bool tiles = d.kind == kTile;
-    const int col = (d.strip % tiles_n) * kTileCols;
-    const int64_t e = d.strip / tiles_n, base = d.base;
-    const uint32_t edge = d.edge, rows = d.left, tile_k = d.tile_k;
-    const bool in = col + lane * 4 < N;            // N is a multiple of 16
-    const uint8_t* stage = s_data + at * L::kBytes;
-    const uint32_t none[4] = {0, 0, 0, 0};
-    if (tiles) {
-      if (edge & 1) most[0] = most[1] = most[2] = most[3] = 0.0f;
-#pragma unroll 1
-      for (uint32_t row = warp; row < rows; row += kWarps) {
-        const int64_t i = base + (int64_t)row * N;
-        Quad q;
-        take_quad<BITS, true>(stage, row, a.d.g_bf16, none, q);
-        step_quad<BITS>(rates, i + lane * 4, 1, q);
-        if (in) {
-          store_quad<BITS, true>(a.d, i, 128, q);
+    const Kind kind = d.kind;
+    const uint32_t strip = kind == kEnd ? kNoStrip : d.strip, edge = d.edge, rows = d.left;
+    if (kind == kTile || kind == kCodes) {
+      const int col = (strip % tiles_n) * kTileCols;
+      const int64_t base = d.base;
+      const bool in = col + lane * 4 < N;            // N is a multiple of 16
+      const uint8_t* stage = s_data + at * L::kBytes;
+      const uint32_t none[4] = {0, 0, 0, 0};
+      if (kind == kTile) {
+        if (edge & 1) most[0] = most[1] = most[2] = most[3] = 0.0f;
 #pragma unroll
-          for (int j = 0; j < 4; ++j) most[j] = max_abs(most[j], q.p[j], 0.0f);
+        for (uint32_t i = 0; i < kRows / kWarps; ++i) {
+          const uint32_t row = i * kWarps + warp;
+          if (row >= rows) break;
+          const int64_t first = base + (int64_t)row * N;
+          Quad q;
+          take_quad<BITS, true>(stage, row, a.d.g_bf16, none, q);
+          step_quad<BITS>(rates, first + lane * 4, 1, q);
+          if (in) {
+            store_quad<BITS, true>(a.d, first, 128, q);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) most[j] = max_abs(most[j], q.p[j], 0.0f);
+          }
+        }
+      } else {
+        if (edge & 1) {
+          float top[4];
+          lds_f32<true>(stage + kCodesMost, top);
+          columns_of(top, x);
+          if (d.tile_k == 0 && warp == 0 && in) {
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+              a.scale[(int64_t)(strip / tiles_n) * N + col + lane * 4 + j] = x.s[j];
+          }
+        }
+        uint8_t* codes = a.codes + base + lane * 4;
+#pragma unroll
+        for (uint32_t i = 0; i < 2 * kRows / kWarps; ++i) {
+          const uint32_t row = i * kWarps + warp;
+          float v[4];
+          lds_f32<true>(stage + (i < kRows / kWarps ? row * 512 : L::kG + (row - kRows) * 512), v);
+          const uint32_t w = codes_of(v, x);
+          if (row < rows && in) __stcs(reinterpret_cast<uint32_t*>(codes + (int64_t)row * N), w);
         }
       }
-    } else {
-      if (edge & 1) columns_of<true>(a.d.most, a.scale, e, col, N, tile_k == 0 && warp == 0, x);
-#pragma unroll
-      for (uint32_t i = 0; i < kRows / kWarps; ++i) {
-        const uint32_t row = i * kWarps + warp;
-        float v[4];
-        lds_f32<true>(stage + row * 512, v);
-        const uint32_t w = codes_of(v, x);
-        if (row < rows && in)
-          __stcs(reinterpret_cast<uint32_t*>(a.codes + base + (int64_t)row * N) + lane, w);
-      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&s_empty[at]);
     }
-    __syncwarp();
-    if (lane == 0) mbar_arrive(&s_empty[at]);
-    if (!tiles || !(edge & 2)) continue;
-    // a tile is done: its columns' largest magnitudes, then its slab's count
+    if (kind != kEnd && !(kind == kTile && (edge & 2))) continue;
+    // a tile's last rows, or the end: to the warp that closes tiles, when it is done with the last
+    // but one
+    const uint32_t b = tiles & 1;
+    if (tiles >= 2 && !mbar_wait_warp(&s_closed[b], ((tiles >> 1) - 1) & 1, kWhereEpilogue)) return;
+    if (kind == kTile) {
 #pragma unroll
-    for (int j = 0; j < 4; ++j) s_most[warp * kTileCols + lane * 4 + j] = most[j];
-    __syncwarp();
-    if (lane == 0) mbar_arrive(&s_join[0]);
-    if (!mbar_wait_warp(&s_join[0], joins & 1, kWhereEpilogue)) return;
-    const int c = threadIdx.x;
-    if (c < kTileCols && col + c < N) {
-      float m = 0.0f;
-#pragma unroll
-      for (int w = 0; w < kWarps; w += 2)
-        m = max_abs(m, s_most[w * kTileCols + c], s_most[(w + 1) * kTileCols + c]);
-      atomicMax(a.d.most + e * N + col + c, __float_as_uint(m));
+      for (int j = 0; j < 4; ++j) s_most[b][warp * kTileCols + lane * 4 + j] = most[j];
     }
+    if (threadIdx.x == 0) s_strip[b] = strip;
     __syncwarp();
-    if (lane == 0) mbar_arrive(&s_join[1]);
-    if (!mbar_wait_warp(&s_join[1], joins & 1, kWhereEpilogue)) return;
-    if (threadIdx.x == 0) {
-      const uint32_t strip = e * tiles_n + col / kTileCols;
-      __threadfence();
-      atomicAdd(a.counters + 1 + strip / a.per_slab, 1u);
-    }
-    ++joins;
+    if (lane == 0) mbar_arrive(&s_tile[b]);
+    ++tiles;
+    if (kind == kEnd) return;
   }
 }
 
@@ -893,13 +945,13 @@ cudaError_t allow_ring(F kernel, int bytes) {
 
 // behind: may start before the kernel in front of it (adamw_prepare_kernel) has ended.
 template <typename A>
-cudaError_t launch_behind(void (*kernel)(A), uint32_t grid, int bytes, bool behind, const A& args,
-                          cudaStream_t s) {
+cudaError_t launch_behind(void (*kernel)(A), uint32_t grid, int threads, int bytes, bool behind,
+                          const A& args, cudaStream_t s) {
   cudaLaunchAttribute attr[1];
   pdl_attribute(attr[0]);
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(grid);
-  cfg.blockDim = dim3(kThreads);
+  cfg.blockDim = dim3(threads);
   cfg.dynamicSmemBytes = (size_t)bytes;
   cfg.stream = s;
   cfg.attrs = attr;
@@ -916,7 +968,8 @@ cudaError_t launch_table(const AdamwCommon& c, const AdamwEntry* at, int num_sms
   const cudaError_t e = allow_ring(kernel, Layout<BITS>::kAll);
   if (e != cudaSuccess) return e;
   const uint32_t most = (uint32_t)num_sms * (BITS == 8 ? kPer8 : kPer32);
-  return launch_behind(kernel, c.units < most ? c.units : most, Layout<BITS>::kAll, c.prepared != 0, t, s);
+  return launch_behind(kernel, c.units < most ? c.units : most, kThreads, Layout<BITS>::kAll,
+                       c.prepared != 0, t, s);
 }
 
 uint32_t strips_of(int64_t n, int64_t K, int64_t N) {
@@ -973,7 +1026,8 @@ cudaError_t fp8moe_launch_adamw_slabs(const AdamwSlabArgs& args, int bits, int n
     const cudaError_t e = allow_ring(kernel, bytes);
     if (e != cudaSuccess) return e;
     const uint32_t most = (uint32_t)(num_sms * per);
-    return launch_behind(kernel, a.units < most ? a.units : most, bytes, a.c.prepared != 0, a, s);
+    return launch_behind(kernel, a.units < most ? a.units : most, kSlabThreads, bytes,
+                         a.c.prepared != 0, a, s);
   };
   return bits == 8 ? launch(adamw_slab_kernel<8>, kPer8, Layout<8>::kAll)
                    : launch(adamw_slab_kernel<32>, kPer32, Layout<32>::kAll);

@@ -473,11 +473,12 @@ int check_adamw(const fp8moe_adamw_tensor& d) {
   return FP8MOE_OK;
 }
 
-// Words of the workspace for weights with codes: of each column, and the units' counters.
+// Words of the workspace for weights with codes: of each column, and the units' counters. Each
+// tensor's begin on 256 bytes (columns are copied by 16).
 int64_t adamw_columns(const fp8moe_adamw_tensor& d) { return d.n / d.K; }
 int64_t adamw_words(const fp8moe_adamw_tensor& d) {
   if (d.n <= 0 || !d.codes || d.K < 1 || d.N < 1) return 0;
-  return adamw_columns(d) + fp8moe_adamw_slab_counters(d.n, d.K, d.N);
+  return (adamw_columns(d) + fp8moe_adamw_slab_counters(d.n, d.K, d.N) + 63) / 64 * 64;
 }
 
 // The first value from which on every array lies on a boundary that wide accesses need (16 bytes
@@ -528,7 +529,7 @@ static_assert(sizeof(AdamwRates) <= kAdamwRatesBytes, "the words of the weights 
 size_t adamw_ws_bytes(const fp8moe_adamw_tensor* tensors, int32_t count, bool on_device) {
   size_t words = 0;
   for (int32_t i = 0; i < count; ++i) words += (size_t)adamw_words(tensors[i]);
-  return words || on_device ? kAdamwRatesBytes + round_up(words * 4, 256) : 0;
+  return words || on_device ? kAdamwRatesBytes + words * 4 : 0;
 }
 
 }  // namespace

@@ -267,7 +267,7 @@ cudaError_t fp8moe_launch_adamw(const AdamwCommon& common, AdamwEntry* at, int c
 // One tensor of expert weights [E, K, N] with its codes; all arrays on 16 bytes, and with 8 bits N
 // a multiple of 128.
 struct AdamwSlabEntry : AdamwEntry {
-  uint32_t* most;           // [E, N], the columns' largest magnitudes: zeros to begin with
+  uint32_t* most;           // [E, N] on 16 bytes, the columns' largest magnitudes: zeros first
   int32_t K, N;
 };
 struct AdamwSlabArgs {
