@@ -28,8 +28,9 @@ constexpr int kThreads = 32 * (kWarps + 1);
 constexpr int kStage = 2048;                     // values of a stage: 16 blocks of 128
 constexpr int kBlocks = kStage / 128;
 constexpr int kUnit = 4 * kStage;                // values of a linear unit
-constexpr int kTileRows = 128, kTileCols = 128;  // a unit of weights with codes
-constexpr int kSlabTiles = 608;                  // tiles of a slab, at least
+constexpr int kTileRows = 64, kTileCols = 128;  // a unit of weights with codes
+constexpr int kSlabTiles = 304;                  // tiles of a slab, at least
+constexpr uint32_t kLag = 4;                     // slabs between a tile and its codes
 constexpr int kPer32 = 2, kPer8 = 3;             // CTAs on an SM
 constexpr uint32_t kAll = 0xffffffffu;
 
@@ -89,6 +90,7 @@ struct Desc {
   uint32_t entry;            // the tensor
   uint32_t left;             // kDirect: values; kTile, kCodes: rows
   uint32_t strip, tile_k;    // kTile, kCodes
+  uint32_t expert, col;      // of the strip
   uint32_t edge;             // 1: a tile's first stage, 2: its last
 };
 
@@ -100,6 +102,21 @@ struct Ring {
 
 __device__ __forceinline__ void cp_async4(void* dst, const void* src) {
   asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(smem_u32(dst)), "l"(src) : "memory");
+}
+
+// What is read once goes first when the L2 needs room: the weights of the last slabs stay.
+__device__ __forceinline__ uint64_t read_once() {
+  uint64_t policy;
+  asm("createpolicy.fractional.L2::evict_first.b64 %0, 1.0;" : "=l"(policy));
+  return policy;
+}
+__device__ __forceinline__ void tma_load_3d_hint(void* dst, const void* tmap, uint64_t* bar, int32_t x,
+                                                 int32_t y, int32_t z, uint64_t policy) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes"
+      ".L2::cache_hint [%0], [%1, {%3, %4, %5}], [%2], %6;"
+      ::"r"(smem_u32(dst)), "l"(tmap), "r"(smem_u32(bar)), "r"(x), "r"(y), "r"(z), "l"(policy)
+      : "memory");
 }
 
 // The fetching warp: stages in the order in which it is told, each when its place is free.
@@ -639,21 +656,36 @@ __global__ void __launch_bounds__(32 * kWarps) column_max_kernel(const float* p,
 // codes = e4m3(p / scale), scale = max(column's largest, 1e-12) / 448, both as the library's
 // other quantisers have them (quantize.cuh). For four columns of a lane.
 struct Columns {
-  float s[4], rl[4], rh[4];
+  float s[4];
+  float2 rl[2], rh[2];
 };
+__device__ __forceinline__ uint32_t e4m3x4(float2 a, float2 b) {
+  uint32_t r;
+  asm("{\n\t.reg .b16 l, h;\n\tcvt.rn.satfinite.e4m3x2.f32 l, %2, %1;\n\t"
+      "cvt.rn.satfinite.e4m3x2.f32 h, %4, %3;\n\tmov.b32 %0, {l, h};\n\t}"
+      : "=r"(r) : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return r;
+}
 __device__ __forceinline__ void columns_of(const float (&top)[4], Columns& x) {
 #pragma unroll
   for (int j = 0; j < 4; ++j) {
     x.s[j] = __fdiv_rn(top[j] < kEps ? kEps : top[j], kE4m3Max);   // a NaN stays
-    bracket(x.s[j], x.rl[j], x.rh[j]);
+  }
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    bracket(x.s[2 * h], x.rl[h].x, x.rh[h].x);
+    bracket(x.s[2 * h + 1], x.rl[h].y, x.rh[h].y);
   }
 }
 __device__ __forceinline__ uint32_t codes_of(const float (&v)[4], const Columns& x) {
-  const uint16_t lo =
-      quotient_x2<false>(v[0], v[1], x.s[0], x.s[1], x.rl[0], x.rl[1], x.rh[0], x.rh[1]);
-  const uint16_t hi =
-      quotient_x2<false>(v[2], v[3], x.s[2], x.s[3], x.rl[2], x.rl[3], x.rh[2], x.rh[3]);
-  return (uint32_t)lo | (uint32_t)hi << 16;
+  // the ends of the bracket around each quotient, all four compared at once (quantize.cuh)
+  const float2 v0 = make_float2(v[0], v[1]), v1 = make_float2(v[2], v[3]);
+  uint32_t lo = e4m3x4(mul2(v0, x.rl[0]), mul2(v1, x.rl[1]));
+  const uint32_t hi = e4m3x4(mul2(v0, x.rh[0]), mul2(v1, x.rh[1]));
+  if (lo != hi)
+    lo = e4m3x4(make_float2(__fdiv_rn(v0.x, x.s[0]), __fdiv_rn(v0.y, x.s[1])),
+                make_float2(__fdiv_rn(v1.x, x.s[2]), __fdiv_rn(v1.y, x.s[3])));
+  return lo;
 }
 
 // For weights that the step went through in order.
@@ -713,33 +745,36 @@ __device__ __forceinline__ bool wait_slab(const uint32_t* done, uint32_t tiles) 
   return true;
 }
 
-struct UnitOf {
-  uint32_t slab, strip, tile_k, tiles;           // tiles: 1, codes: 0
-};
-// What the unit with this number is; `units` has the order.
-__device__ __forceinline__ UnitOf unit_of(const AdamwSlabArgs& a, uint32_t unit, uint32_t tiles_k) {
-  const uint32_t whole = a.per_slab * tiles_k;   // units of a slab but the last
-  const uint32_t last = a.slabs - 1, last_strips = a.strips - last * a.per_slab;
-  const uint32_t first = last == 0 ? last_strips * tiles_k : whole;
-  UnitOf u = {0, 0, 0, 1};
-  if (unit >= first) {
-    unit -= first;
-    if (last != 0) {
-      u.slab = min(1 + unit / (2 * whole), last);
-      unit -= (u.slab - 1) * 2 * whole;
-    }
-    const uint32_t n = last == 0 ? 0 : u.slab < last ? whole : last_strips * tiles_k;
-    if (unit >= n) {
-      unit -= n, u.tiles = 0;
-      if (unit < whole && last != 0) --u.slab;
-      else if (last != 0) unit -= whole;
-    }
+// The units in their order: phase j has the tiles of slab j, then the codes of slab j - kLag.
+struct Order {
+  uint32_t whole, rest, last, strips, rest_strips;   // units of a slab, of the last one; its number
+  uint32_t phase = 0, begin = 0;                     // of the unit that was asked for last
+  uint32_t slab, strip, tile_k;
+  bool tiles;
+
+  __device__ __forceinline__ Order(const AdamwSlabArgs& a, uint32_t tiles_k) {
+    last = a.slabs - 1;
+    strips = a.per_slab, rest_strips = a.strips - last * a.per_slab;
+    whole = strips * tiles_k, rest = rest_strips * tiles_k;
   }
-  const uint32_t strips = u.slab == last ? last_strips : a.per_slab;
-  u.strip = u.slab * a.per_slab + unit % strips;
-  u.tile_k = unit / strips;
-  return u;
-}
+  __device__ __forceinline__ uint32_t units(uint32_t s) const {
+    return s < last ? whole : s == last ? rest : 0u;
+  }
+  __device__ __forceinline__ uint32_t codes(uint32_t p) const {
+    return p >= kLag ? units(p - kLag) : 0u;
+  }
+  // ascending units
+  __device__ __forceinline__ void find(uint32_t unit) {
+    while (unit - begin >= units(phase) + codes(phase)) begin += units(phase) + codes(phase), ++phase;
+    unit -= begin;
+    tiles = unit < units(phase);
+    slab = tiles ? phase : phase - kLag;
+    if (!tiles) unit -= units(phase);
+    const uint32_t n = slab == last ? rest_strips : strips;
+    strip = slab * strips + unit % n;
+    tile_k = unit / n;
+  }
+};
 
 // The arrays' warps: kWarps that work, one that fetches, one that closes tiles.
 constexpr int kSlabThreads = kThreads + 32;
@@ -775,16 +810,17 @@ __global__ void __launch_bounds__(kSlabThreads, BITS == 32 ? kPer32 : kPer8) ada
   if (warp == kWarps) {
     Fetcher<BITS> f = {ring};
     bool going = true;
+    const uint64_t once = read_once();
+    Order u(a, tiles_k);
     uint32_t next = lane == 0 ? atomicAdd(a.counters, 1u) : 0u;
     while (going) {
       const uint32_t unit = __shfl_sync(kAll, next, 0);
       if (unit >= a.units) break;
       if (lane == 0) next = atomicAdd(a.counters, 1u);
-      const UnitOf u = unit_of(a, unit, tiles_k);
+      u.find(unit);
       if (!u.tiles) {
-        const uint32_t strips = u.slab + 1 == a.slabs ? a.strips - u.slab * a.per_slab : a.per_slab;
         bool ready = true;
-        if (lane == 0) ready = wait_slab(a.counters + 1 + u.slab, strips * tiles_k);
+        if (lane == 0) ready = wait_slab(a.counters + 1 + u.slab, u.units(u.slab));
         going = __shfl_sync(kAll, (int)ready, 0);
       }
       const int e = u.strip / tiles_n, col = (u.strip % tiles_n) * kTileCols;
@@ -793,7 +829,7 @@ __global__ void __launch_bounds__(kSlabThreads, BITS == 32 ? kPer32 : kPer8) ada
       for (int row = 0; going && row < rows; row += each) {
         Desc d;
         d.kind = u.tiles ? kTile : kCodes;
-        d.entry = 0, d.strip = u.strip, d.tile_k = u.tile_k;
+        d.entry = 0, d.strip = u.strip, d.tile_k = u.tile_k, d.expert = e, d.col = col;
         d.left = min(each, rows - row);
         d.edge = (row == 0 ? 1 : 0) + (row + each >= rows ? 2 : 0);
         const int k = u.tile_k * kTileRows + row;
@@ -803,10 +839,10 @@ __global__ void __launch_bounds__(kSlabThreads, BITS == 32 ? kPer32 : kPer8) ada
         if (u.tiles) {
           if (lane == 0) {
             f.begin(d, kStage * (4 + (a.d.g_bf16 ? 2 : 4) + 2 * BITS / 8));
-            tma_load_3d(f.data(), &a.tm_p, f.full(), col, k, e);
-            tma_load_3d(f.data() + L::kG, &a.tm_g, f.full(), col, k, e);
-            tma_load_3d(f.data() + L::kM, &a.tm_m, f.full(), col, k, e);
-            tma_load_3d(f.data() + L::kV, &a.tm_v, f.full(), col, k, e);
+            tma_load_3d_hint(f.data(), &a.tm_p, f.full(), col, k, e, once);
+            tma_load_3d_hint(f.data() + L::kG, &a.tm_g, f.full(), col, k, e, once);
+            tma_load_3d_hint(f.data() + L::kM, &a.tm_m, f.full(), col, k, e, once);
+            tma_load_3d_hint(f.data() + L::kV, &a.tm_v, f.full(), col, k, e, once);
           }
           __syncwarp();
           if constexpr (BITS == 8) {
@@ -819,8 +855,8 @@ __global__ void __launch_bounds__(kSlabThreads, BITS == 32 ? kPer32 : kPer8) ada
         } else {
           if (lane == 0) {
             f.begin(d, 2 * kStage * 4);
-            tma_load_3d(f.data(), &a.tm_p, f.full(), col, k, e);
-            tma_load_3d(f.data() + L::kG, &a.tm_p, f.full(), col, k + kRows, e);
+            tma_load_3d_hint(f.data(), &a.tm_p, f.full(), col, k, e, once);
+            tma_load_3d_hint(f.data() + L::kG, &a.tm_p, f.full(), col, k + kRows, e, once);
           }
           __syncwarp();
           // 16 bytes of four columns, past the L1; N is a multiple of 16
@@ -875,7 +911,7 @@ __global__ void __launch_bounds__(kSlabThreads, BITS == 32 ? kPer32 : kPer8) ada
     const Kind kind = d.kind;
     const uint32_t strip = kind == kEnd ? kNoStrip : d.strip, edge = d.edge, rows = d.left;
     if (kind == kTile || kind == kCodes) {
-      const int col = (strip % tiles_n) * kTileCols;
+      const int col = d.col;
       const int64_t base = d.base;
       const bool in = col + lane * 4 < N;            // N is a multiple of 16
       const uint8_t* stage = s_data + at * L::kBytes;
@@ -904,7 +940,7 @@ __global__ void __launch_bounds__(kSlabThreads, BITS == 32 ? kPer32 : kPer8) ada
           if (d.tile_k == 0 && warp == 0 && in) {
 #pragma unroll
             for (int j = 0; j < 4; ++j)
-              a.scale[(int64_t)(strip / tiles_n) * N + col + lane * 4 + j] = x.s[j];
+              a.scale[(int64_t)d.expert * N + col + lane * 4 + j] = x.s[j];
           }
         }
         uint8_t* codes = a.codes + base + lane * 4;
