@@ -27,19 +27,18 @@ constexpr int kWarps = 8;                        // that work; one more fetches
 constexpr int kThreads = 32 * (kWarps + 1);
 constexpr int kStage = 2048;                     // values of a stage: 16 blocks of 128
 constexpr int kBlocks = kStage / 128;
-constexpr int kUnit = 4 * kStage;                // values of a linear unit
+constexpr int kUnitStages = 4;                   // of a linear unit, where there are many
 constexpr int kTileRows = 64, kTileCols = 128;  // a unit of weights with codes
 constexpr int kSlabTiles = 304;                  // tiles of a slab, at least
 constexpr uint32_t kLag = 4;                     // slabs between a tile and its codes
-constexpr int kPer32 = 2, kPer8 = 3;             // CTAs on an SM
 constexpr uint32_t kAll = 0xffffffffu;
 
 // A stage in shared memory: the blocks of each array as they lie in memory (with up to 15 bytes
 // in front, where that is not on a boundary of 16), then 8-bit moments' scales. 100 KB or 63 KB
 // for a CTA's ring, so that an SM has about 200 KB on their way.
 constexpr int kRoomWide = kStage * 4 + 128, kRoomCodes = kStage + 128;
-template <int BITS> struct Layout {
-  static constexpr int kStages = 3;
+template <int BITS, int STAGES> struct Layout {
+  static constexpr int kStages = STAGES;
   static constexpr int kG = kRoomWide, kM = 2 * kRoomWide;
   static constexpr int kV = kM + (BITS == 32 ? kRoomWide : kRoomCodes);
   static constexpr int kScales = kV + (BITS == 32 ? kRoomWide : kRoomCodes);
@@ -74,6 +73,15 @@ struct Rates {
   uint32_t key;
   double lr;
 };
+
+// CTAs on an SM, and the stages of each: 200 KB of 32-bit moments' stages, 190 KB of 8-bit ones' in
+// 3 CTAs for tensors in order (addresses of any kind: 210 us against 225 in 2 CTAs, boundaries of
+// 16 bytes: 178 against 175), 169 KB in 2 for tiles, whose CTAs are one warp larger and spill
+// registers as three (1238 against 1278 us).
+template <int BITS> using LinearLayout = Layout<BITS, 3>;
+template <int BITS> using SlabLayout = Layout<BITS, BITS == 32 ? 3 : 4>;
+template <int BITS> constexpr int kLinearPer = BITS == 32 ? 2 : 3;
+constexpr int kSlabPer = 2;
 
 // What a stage holds.
 enum Kind : uint32_t {
@@ -120,9 +128,8 @@ __device__ __forceinline__ void tma_load_3d_hint(void* dst, const void* tmap, ui
 }
 
 // The fetching warp: stages in the order in which it is told, each when its place is free.
-template <int BITS>
+template <int BITS, typename L>
 struct Fetcher {
-  using L = Layout<BITS>;
   Ring ring;
   uint32_t count = 0;
 
@@ -196,10 +203,10 @@ struct Fetcher {
   }
 };
 
-template <int BITS>
+template <int STAGES>
 __device__ __forceinline__ void ring_init(const Ring& r) {
   if (threadIdx.x == 0) {
-    for (int i = 0; i < Layout<BITS>::kStages; ++i) {
+    for (int i = 0; i < STAGES; ++i) {
       mbar_init(&r.full[i], 33);
       mbar_init(&r.empty[i], kWarps);
     }
@@ -246,7 +253,7 @@ __device__ __forceinline__ uint32_t lds_codes(const uint8_t* s) {
 template <int BITS, bool WIDE>
 __device__ __forceinline__ void take_quad(const uint8_t* stage, int block, bool g_bf16,
                                           const uint32_t (&shift)[4], Quad& q) {
-  using L = Layout<BITS>;
+  using L = Layout<BITS, 1>;
   lds_f32<WIDE>(stage + block * 512 + shift[0], q.p);
   if (g_bf16) lds_bf16<WIDE>(stage + L::kG + block * 256 + shift[1], q.g);
   else lds_f32<WIDE>(stage + L::kG + block * 512 + shift[1], q.g);
@@ -556,19 +563,19 @@ struct AdamwTable {
 };
 
 template <int BITS, int kCapacity>
-__global__ void __launch_bounds__(kThreads, BITS == 32 ? kPer32 : kPer8) adamw_kernel(
+__global__ void __launch_bounds__(kThreads, kLinearPer<BITS>) adamw_kernel(
     const __grid_constant__ AdamwTable<kCapacity> table) {
-  using L = Layout<BITS>;
+  using L = LinearLayout<BITS>;
   extern __shared__ __align__(128) uint8_t s_data[];
   __shared__ uint64_t s_full[L::kStages], s_empty[L::kStages];
   __shared__ Desc s_desc[L::kStages];
   const Ring ring = {s_full, s_empty, s_desc, s_data};
-  ring_init<BITS>(ring);
+  ring_init<L::kStages>(ring);
   __syncthreads();
   const AdamwCommon& c = table.c;
 
   if (threadIdx.x >= 32 * kWarps) {
-    Fetcher<BITS> f = {ring};
+    Fetcher<BITS, L> f = {ring};
     bool going = true;
     uint32_t entry = 0;
     for (uint32_t unit = blockIdx.x; going && unit < c.units; unit += gridDim.x) {
@@ -582,8 +589,8 @@ __global__ void __launch_bounds__(kThreads, BITS == 32 ? kPer32 : kPer8) adamw_k
         a.left = (uint32_t)min(d.n, (int64_t)d.head);
         going = f.empty_stage(a);
       }
-      a.base = d.head + (int64_t)number * kUnit;
-      for (int i = 0; going && i < kUnit / kStage && a.base < d.n; ++i, a.base += kStage) {
+      a.base = d.head + (int64_t)number * c.unit_stages * kStage;
+      for (int i = 0; going && i < c.unit_stages && a.base < d.n; ++i, a.base += kStage) {
         const int64_t behind = d.n - a.base - kStage;
         a.left = (uint32_t)min((int64_t)kStage, d.n - a.base);
         a.kind = d.vec && behind >= 0 ? kWide
@@ -779,9 +786,9 @@ struct Order {
 // The arrays' warps: kWarps that work, one that fetches, one that closes tiles.
 constexpr int kSlabThreads = kThreads + 32;
 template <int BITS>
-__global__ void __launch_bounds__(kSlabThreads, BITS == 32 ? kPer32 : kPer8) adamw_slab_kernel(
+__global__ void __launch_bounds__(kSlabThreads, kSlabPer) adamw_slab_kernel(
     const __grid_constant__ AdamwSlabArgs a) {
-  using L = Layout<BITS>;
+  using L = SlabLayout<BITS>;
   extern __shared__ __align__(128) uint8_t s_data[];
   __shared__ uint64_t s_full[L::kStages], s_empty[L::kStages], s_tile[2], s_closed[2];
   __shared__ Desc s_desc[L::kStages];
@@ -795,7 +802,7 @@ __global__ void __launch_bounds__(kSlabThreads, BITS == 32 ? kPer32 : kPer8) ada
       mbar_init(&s_closed[i], 1);
     }
   }
-  ring_init<BITS>(ring);
+  ring_init<L::kStages>(ring);
   __syncthreads();
   pdl_wait();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -808,7 +815,7 @@ __global__ void __launch_bounds__(kSlabThreads, BITS == 32 ? kPer32 : kPer8) ada
   constexpr int kCodesMost = L::kM;
 
   if (warp == kWarps) {
-    Fetcher<BITS> f = {ring};
+    Fetcher<BITS, L> f = {ring};
     bool going = true;
     const uint64_t once = read_once();
     Order u(a, tiles_k);
@@ -1001,10 +1008,10 @@ cudaError_t launch_table(const AdamwCommon& c, const AdamwEntry* at, int num_sms
   t.c = c;
   for (int i = 0; i < c.count; ++i) t.at[i] = at[i];
   auto* kernel = adamw_kernel<BITS, kCapacity>;
-  const cudaError_t e = allow_ring(kernel, Layout<BITS>::kAll);
+  const cudaError_t e = allow_ring(kernel, LinearLayout<BITS>::kAll);
   if (e != cudaSuccess) return e;
-  const uint32_t most = (uint32_t)num_sms * (BITS == 8 ? kPer8 : kPer32);
-  return launch_behind(kernel, c.units < most ? c.units : most, kThreads, Layout<BITS>::kAll,
+  const uint32_t most = (uint32_t)(num_sms * kLinearPer<BITS>);
+  return launch_behind(kernel, c.units < most ? c.units : most, kThreads, LinearLayout<BITS>::kAll,
                        c.prepared != 0, t, s);
 }
 
@@ -1023,17 +1030,22 @@ using namespace fp8moe;
 
 FP8MOE_DEFINE_STATUS_TAKE(fp8moe_status_take_adamw)
 
-uint64_t fp8moe_adamw_units(const AdamwEntry& d) {
-  return d.n <= d.head ? 1 : (uint64_t)(d.n - d.head + kUnit - 1) / kUnit;
+static uint64_t units_of(const AdamwEntry& d, int64_t values) {
+  return d.n <= d.head ? 1 : (uint64_t)((d.n - d.head + values - 1) / values);
 }
+uint64_t fp8moe_adamw_units(const AdamwEntry& d) { return units_of(d, kUnitStages * kStage); }
 
 cudaError_t fp8moe_launch_adamw(const AdamwCommon& common, AdamwEntry* at, int count, int bits,
                                 int num_sms, cudaStream_t s) {
   AdamwCommon c = common;
+  // units of four stages; of one, where that leaves CTAs without work
   uint64_t units = 0;
+  for (int i = 0; i < count; ++i) units += fp8moe_adamw_units(at[i]);
+  c.unit_stages = units < (uint64_t)num_sms ? 1 : kUnitStages;
+  units = 0;
   for (int i = 0; i < count; ++i) {
     at[i].first_unit = (uint32_t)units;
-    units += fp8moe_adamw_units(at[i]);
+    units += units_of(at[i], (int64_t)c.unit_stages * kStage);
   }
   c.count = count, c.units = (uint32_t)units;
   // a table of 16 entries is a launch's usual few KB of parameters, the other nearly all of them
@@ -1058,15 +1070,15 @@ cudaError_t fp8moe_launch_adamw_slabs(const AdamwSlabArgs& args, int bits, int n
   a.per_slab = strips_per_slab(a.d.K);
   a.slabs = fp8moe_adamw_slab_counters(a.d.n, a.d.K, a.d.N) - 1;
   a.units = 2 * a.strips * ((a.d.K + kTileRows - 1) / kTileRows);
-  auto launch = [&](auto* kernel, int per, int bytes) {
+  auto launch = [&](auto* kernel, int bytes) {
     const cudaError_t e = allow_ring(kernel, bytes);
     if (e != cudaSuccess) return e;
-    const uint32_t most = (uint32_t)(num_sms * per);
+    const uint32_t most = (uint32_t)(num_sms * kSlabPer);
     return launch_behind(kernel, a.units < most ? a.units : most, kSlabThreads, bytes,
                          a.c.prepared != 0, a, s);
   };
-  return bits == 8 ? launch(adamw_slab_kernel<8>, kPer8, Layout<8>::kAll)
-                   : launch(adamw_slab_kernel<32>, kPer32, Layout<32>::kAll);
+  return bits == 8 ? launch(adamw_slab_kernel<8>, SlabLayout<8>::kAll)
+                   : launch(adamw_slab_kernel<32>, SlabLayout<32>::kAll);
 }
 
 cudaError_t fp8moe_launch_adamw_prepare(AdamwRates* rates, const int64_t* step, int64_t host_step,

@@ -256,7 +256,7 @@ struct AdamwCommon {
   float minus_zero;         // -0, of which the compiler knows nothing
   uint32_t key;
   int prepared;             // the kernel right in front of this launch is the preparation
-  int count;                // set by the launcher, as is the next
+  int count, unit_stages;   // set by the launcher, as is the next
   uint32_t units;
 };
 constexpr int kAdamwEntries = 360;     // of 88 bytes: a launch has 32764 bytes of parameters
