@@ -10,6 +10,7 @@ Function names follow the C ABI without the ``fp8moe_`` prefix.
 """
 from __future__ import annotations
 
+import array
 import ctypes
 import os
 import threading
@@ -970,15 +971,39 @@ class AdamwPlan:
             if b[0] < a[1]:
                 raise ValueError(f"params {a[2]} and {b[2]} or their states overlap")
         self._addresses = [p.data_ptr() for p in self.params]
+        self._indices = [self.device.index] * count if count else []
+        self._numels = array.array("Q", [p.numel() for p in self.params])
+        self._columns = memoryview(self._table).cast("B").cast("Q") if count else None
+        self._type = None                       # of all gradients in the table
 
     def _enter(self, grads):
         """Writes the gradients' addresses and types into the table."""
         count = len(self.params)
+        if count == 0:
+            return self._table, 0
         if len(grads) != count:
             raise ValueError(f"grads must have one entry for each of the {count} params")
         if [p.data_ptr() for p in self.params] != self._addresses:
             raise ValueError("a param's storage was replaced: make a new plan")
         table, dev = self._table, self.device
+        try:                                    # the usual case, column by column
+            types = [g.dtype for g in grads]
+            if all(t is types[0] for t in types) and types[0] in TYPES \
+                    and [g.shape for g in grads] == self._shapes \
+                    and all([g.is_contiguous() for g in grads]) \
+                    and [g.get_device() for g in grads] == self._indices:
+                words, step = self._columns, ctypes.sizeof(_AdamwTensor) // 8
+                words[_AdamwTensor.g.offset // 8::step] = \
+                    array.array("Q", [g.data_ptr() for g in grads])
+                words[_AdamwTensor.n.offset // 8::step] = self._numels
+                if self._type != types[0]:
+                    for e in table[:count]:
+                        e.g_type = TYPES[types[0]]
+                    self._type = types[0]
+                return table, count
+        except AttributeError:                  # something is no tensor
+            pass
+        self._type = None
         for i, g in enumerate(grads):
             e = table[i]
             if g is None:                       # no gradient: the param is left as it is

@@ -27,12 +27,25 @@ constexpr int kWarps = 8;
 constexpr int kThreads = 32 * kWarps;
 constexpr int kJoinThreads = 1024;
 
+__device__ __forceinline__ uint32_t load_peer(const void* p, int cta) {
+  uint32_t v;
+  asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(mapa_shared(smem_u32(p), cta))
+               : "memory");
+  return v;
+}
+
 // Ascending with the value; a NaN is the largest, -inf is no candidate (0).
 __device__ __forceinline__ uint32_t order_key(float v) {
   if (v != v) return 0xffffffffu;
   const uint32_t u = __float_as_uint(v + 0.0f);              // -0 is 0
   if (u == 0xff800000u) return 0u;
   return u ^ ((uint32_t)((int32_t)u >> 31) | 0x80000000u);
+}
+
+// The smallest value of a key's upper 22 bits.
+__device__ __forceinline__ float key_value(uint32_t key) {
+  const uint32_t o = key & ~1023u;
+  return __uint_as_float(o & 0x80000000u ? o ^ 0x80000000u : ~o);
 }
 
 // What decides the choice, in f32: the logit, or score + bias (-inf stays out either way).
@@ -106,6 +119,24 @@ __device__ __noinline__ int choose_exactly(const T* row, const float* bias, int 
   return mine;
 }
 
+// For lane i: the lane among the first n whose (value, expert) comes at place i, larger values and
+// lower experts first (a NaN value in place of the largest); its own for lanes from n on.
+template <typename F>
+__device__ __forceinline__ int sorted_from(F value, int id, int n) {
+  const int lane = threadIdx.x & 31;
+  if (value != value) value = (F)INFINITY;
+  int rank = 0;
+  for (int i = 0; i < n; ++i) {
+    const F v = __shfl_sync(kAllLanes, value, i);
+    const int e = __shfl_sync(kAllLanes, id, i);
+    rank += v > value || (v == value && e < id);
+  }
+  int from = lane;
+  for (int i = 0; i < n; ++i)
+    if (__shfl_sync(kAllLanes, rank, i) == lane) from = i;
+  return from;
+}
+
 template <typename T, int V, bool VECT, bool GIVEN>
 __global__ void __launch_bounds__(kThreads) router_kernel(const __grid_constant__ RouterArgs a) {
   extern __shared__ float s_mem[];
@@ -129,93 +160,119 @@ __global__ void __launch_bounds__(kThreads) router_kernel(const __grid_constant_
     load_row<T, V, VECT>(row, E, lane, -INFINITY, x);
     int id = -1;
     if (GIVEN && lane < k) id = a.given[t * k + lane];
-    float largest = x[0];
+    auto row_max = [&]() {
+      float m = x[0];
 #pragma unroll
-    for (int j = 1; j < V; ++j) largest = max_nan(largest, x[j]);
-    largest = warp_max(largest);
-    const float top = scale_top(largest, sig);
-    const bool none = largest == -INFINITY;
-
+      for (int j = 1; j < V; ++j) m = max_nan(m, x[j]);
+      return warp_max(m);
+    };
     // the scores, where shares, unnormalised weights or a bias ask for them
-    float n[V], sum = 0.0f;
-    if (balance || (!GIVEN && !sig && (has_bias || !a.normalize))) {
+    float n[V], top = 0.0f, inv_sum = 0.0f;
+    auto scores = [&](float largest) {
+      top = scale_top(largest, sig);
+      float sum = 0.0f;
 #pragma unroll
       for (int j = 0; j < V; ++j) {
-        n[j] = none ? 0.0f : scaled_score(x[j], top, sig);
+        n[j] = largest == -INFINITY ? 0.0f : scaled_score(x[j], top, sig);
         sum += n[j];
       }
-      sum = warp_sum(sum);
-    }
-    const float inv_sum = none ? 0.0f : __frcp_rn(sum);
+      inv_sum = largest == -INFINITY ? 0.0f : __frcp_rn(warp_sum(sum));
+    };
 
-    if constexpr (!GIVEN) {
+    if constexpr (GIVEN) {
+      scores(row_max());
+    } else {
+      float largest = 0.0f;
+      if (has_bias) {
+        largest = row_max();
+        if (!sig || balance) scores(largest);
+      }
       // keys: the value's upper 22 bits of order, then the expert, the lowest first; they
       // differ from each other, so that the largest of a warp names its expert
       uint32_t key[V];
-      float c[V];
 #pragma unroll
       for (int j = 0; j < V; ++j) {
         const int e = lane * V + j;
         const float b = has_bias && e < E ? a.bias[e] : 0.0f;
-        c[j] = choice_value(x[j], b, has_bias, sig, top, inv_sum);
-        const uint32_t o = order_key(c[j]);
+        const uint32_t o = order_key(choice_value(x[j], b, has_bias, sig, top, inv_sum));
         key[j] = o == 0u ? 0u : (o & ~1023u) | (uint32_t)(1023 - e);
       }
-      uint32_t mine = 0;
-      int chosen = 0;
-      for (; chosen < k; ++chosen) {
+      // The topk largest keys, and those behind them whose values may be as large: with the same
+      // upper bits, or, with a bias, within twice the error of a score (8 * 2^-24 of a sigmoid at
+      // most 1; of a softmax score the argument's rounding, at most .4 of the largest score,
+      // and the sum's of 37 terms; the sum with the bias adds half a unit).
+      uint32_t mine = 0, floor = 0;
+      float slack = 0.0f;
+      int found = 0;
+      for (; found <= 32; ++found) {
         uint32_t m = key[0];
 #pragma unroll
         for (int j = 1; j < V; ++j) m = max(m, key[j]);
         m = __reduce_max_sync(kAllLanes, m);
-        if (m == 0u) break;
+        if (m == 0u || (found >= k && m < floor)) break;
 #pragma unroll
         for (int j = 0; j < V; ++j) key[j] = key[j] == m ? 0u : key[j];
-        if (lane == chosen) mine = m;
+        if (lane == found) mine = m;
+        if (found == 0 && has_bias)
+          slack = (sig ? 0x1p-20f : 0x1p-17f * inv_sum) + 0x1p-22f * fabsf(key_value(m));
+        if (found == k - 1) {
+          floor = m & ~1023u;
+          if (has_bias) {
+            slack += 0x1p-22f * fabsf(key_value(m));
+            floor = order_key(key_value(m) - slack) & ~1023u;
+          }
+        }
       }
       if (mine) id = 1023 - (int)(mine & 1023u);
       float xc = id >= 0 ? load_f32(row + id) : -INFINITY;
-
-      // Is the order settled? Values whose upper bits agree, and with a bias those within twice
-      // the error of a score, may stand in the wrong order, or out of place behind the last one.
-      // (With a bias: 8 * 2^-24 of a sigmoid at most 1; of a softmax score the argument's
-      // rounding, at most .4 of the largest score, and the sum's of 37 terms; the sum with
-      // the bias adds half a unit.)
-      const float b = has_bias && id >= 0 ? a.bias[id] : 0.0f;
-      const float cc = id >= 0 ? choice_value(xc, b, has_bias, sig, top, inv_sum) : INFINITY;
-      const float largest_c = fabsf(__shfl_sync(kAllLanes, cc, 0));
-      float least = cc;
-#pragma unroll
-      for (int o = 16; o > 0; o >>= 1) least = fminf(least, __shfl_xor_sync(kAllLanes, least, o));
-      const float slack = !has_bias ? 0.0f
-          : (sig ? 0x1p-20f : 0x1p-17f * inv_sum) + 0x1p-22f * fmaxf(largest_c, fabsf(least));
-      const float next_c = __shfl_down_sync(kAllLanes, cc, 1);
-      const float next_x = __shfl_down_sync(kAllLanes, xc, 1);
-      const float next_b = __shfl_down_sync(kAllLanes, b, 1);
-      bool open = lane + 1 < chosen &&
-                  (has_bias ? !(cc - next_c > slack) && !(xc == next_x && b == next_b)
-                            : cc < next_c);
-      const float cut = least - slack;
-      const int last = __ffs(__ballot_sync(kAllLanes, cc == least)) - 1;   // -1: all NaN
-      const float last_x = __shfl_sync(kAllLanes, xc, last & 31);
-      const float last_b = __shfl_sync(kAllLanes, b, last & 31);
-#pragma unroll
-      for (int j = 0; j < V; ++j) {
-        if (key[j] == 0u) continue;
-        if (!has_bias) open |= c[j] > least;
-        else if (c[j] >= cut) open |= x[j] != last_x || a.bias[lane * V + j] != last_b;
+      if (!has_bias) largest = __shfl_sync(kAllLanes, xc, 0);   // but for equal upper bits
+      if (k > 1 || found > 1) {
+        const float b = has_bias && id >= 0 ? a.bias[id] : 0.0f;
+        float c = id >= 0 ? choice_value(xc, b, has_bias, sig, top, inv_sum) : -INFINITY;
+        // into the order of the whole values
+        float next = __shfl_down_sync(kAllLanes, c, 1);
+        const bool wrong = lane + 1 < found && c < next;
+        if (__any_sync(kAllLanes, wrong) && found <= 32) {
+          const int from = sorted_from(c, id, found);
+          c = __shfl_sync(kAllLanes, c, from);
+          xc = __shfl_sync(kAllLanes, xc, from);
+          id = __shfl_sync(kAllLanes, id, from);
+          next = __shfl_down_sync(kAllLanes, c, 1);
+        }
+        if (!has_bias) largest = __shfl_sync(kAllLanes, xc, 0);
+        bool open = false;
+        if (has_bias) {
+          const float bc = id >= 0 ? a.bias[id] : 0.0f;
+          const float next_x = __shfl_down_sync(kAllLanes, xc, 1);
+          const float next_b = __shfl_down_sync(kAllLanes, bc, 1);
+          open = lane < k && lane + 1 < found && !(c - next > slack) &&
+                 !(xc == next_x && bc == next_b);
+        }
+        open = __any_sync(kAllLanes, open);
+        if (found > 32 || (open && !sig)) {
+          // cut: the last that can belong to the choice
+          const float cut = key_value(__shfl_sync(kAllLanes, mine, k - 1)) - slack;
+          id = choose_exactly(row, a.bias, E, k, sig, top, inv_sum, cut, list);
+          __syncwarp();
+          xc = id >= 0 ? load_f32(row + id) : -INFINITY;
+          if (!has_bias) largest = __shfl_sync(kAllLanes, xc, 0);
+        } else if (open) {
+          const float bc = id >= 0 ? a.bias[id] : 0.0f;
+          const double v = id >= 0 ? choice_value_64(xc, bc, true, true, 0.0f, 0.0)
+                                   : -(double)INFINITY;
+          const int from = sorted_from(v, id, found);
+          xc = __shfl_sync(kAllLanes, xc, from);
+          id = __shfl_sync(kAllLanes, id, from);
+        }
       }
-      if (__any_sync(kAllLanes, open)) {
-        id = choose_exactly(row, a.bias, E, k, sig, top, inv_sum, cut, list);
-        xc = id >= 0 ? load_f32(row + id) : -INFINITY;
-        __syncwarp();
-      }
+      if (lane >= k) id = -1, xc = -INFINITY;
+      if (!has_bias && (balance || (!sig && !a.normalize))) scores(largest);
 
       float w = 0.0f;
       if (a.normalize) {
-        const float most = warp_max(xc);
+        const float most = has_bias ? warp_max(xc) : largest;
         const float nc = id >= 0 ? scaled_score(xc, scale_top(most, sig), sig) : 0.0f;
-        w = nc / warp_sum(nc);
+        w = nc / first_sum(nc, k);
       } else if (id >= 0) {
         w = sig ? sigmoid(xc) : expf(xc - top) * inv_sum;
       }
@@ -301,10 +358,12 @@ __global__ void __launch_bounds__(kThreads) router_kernel(const __grid_constant_
   padding(at, end);
 }
 
-// Adds up a sequence's parts in a fixed order: counts, slope and loss. One CTA a sequence;
-// thread t has column t % width and every (1024 / width)-th part.
+// Adds up a sequence's parts in a fixed order: counts, slope and loss. A cluster a sequence, of
+// one CTA or of eight; CTA r takes the parts r, r + CTAs, ... of a sequence, its thread t column
+// t % width of every (1024 / width)-th of these. (One CTA for the 586 parts of a batch of 65536
+// tokens and 128 experts took 20 us.)
 __global__ void __launch_bounds__(kJoinThreads) balance_join_kernel(const int32_t* offsets, int64_t T,
-                                                         int B, int E, int width, int chunk,
+                                                         int B, int E, int width, int chunk, int ctas,
                                                          const float* part_share,
                                                          const int32_t* part_count,
                                                          const int32_t* part_tokens,
@@ -312,14 +371,15 @@ __global__ void __launch_bounds__(kJoinThreads) balance_join_kernel(const int32_
                                                          float* slope) {
   __shared__ float s_share[kJoinThreads];
   __shared__ int32_t s_count[kJoinThreads];
-  __shared__ int32_t s_chosen[32], s_tokens[32];
+  __shared__ int32_t s_chosen[32], s_tokens[33];
   __shared__ float s_loss[32];
-  const int b = blockIdx.x, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int b = blockIdx.x / ctas, cta = blockIdx.x % ctas;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int e = tid % width, groups = kJoinThreads / width;
   int64_t first = 0, last = T;
   if (offsets != nullptr) {
     const int64_t o0 = offsets[b], o1 = offsets[b + 1];
-    if (tid == 0 && (o0 < 0 || o1 < o0 || o1 > T)) status_set(kStatusBadOffsets);
+    if (tid == 0 && cta == 0 && (o0 < 0 || o1 < o0 || o1 > T)) status_set(kStatusBadOffsets);
     first = min(max(o0, (int64_t)0), T);
     last = min(max(o1, first), T);
   }
@@ -329,26 +389,55 @@ __global__ void __launch_bounds__(kJoinThreads) balance_join_kernel(const int32_
   int32_t count = 0, tokens = 0;
   if (e < E) {
 #pragma unroll 4
-    for (int64_t s = s0 + tid / width; s < s1; s += groups) {
+    for (int64_t s = s0 + cta + (int64_t)(tid / width) * ctas; s < s1; s += groups * ctas) {
       share += part_share[s * E + e];
       count += part_count[s * E + e];
     }
   }
-  for (int64_t s = s0 + tid; s < s1; s += kJoinThreads) tokens += part_tokens[s];
+  for (int64_t s = s0 + cta + (int64_t)tid * ctas; s < s1; s += kJoinThreads * ctas)
+    tokens += part_tokens[s];
   s_share[tid] = share;
   s_count[tid] = count;
-  const int32_t chosen = __reduce_add_sync(kAllLanes, count);
   tokens = __reduce_add_sync(kAllLanes, tokens);
-  if (lane == 0) s_chosen[warp] = chosen, s_tokens[warp] = tokens;
+  if (lane == 0) s_tokens[warp] = tokens;
   __syncthreads();
-  const float C = (float)__reduce_add_sync(kAllLanes, s_chosen[lane]);
-  const float n = (float)__reduce_add_sync(kAllLanes, s_tokens[lane]);
-  float part = 0.0f;
-  if (tid < width && e < E) {
+  // this CTA's sums of the columns in s_share and s_count [width], its tokens in s_tokens[32]
+  if (tid < width) {
     for (int g = 1; g < groups; ++g) {
       share += s_share[g * width + e];
       count += s_count[g * width + e];
     }
+    s_share[tid] = share;
+    s_count[tid] = count;
+  }
+  if (warp == 0) {
+    tokens = __reduce_add_sync(kAllLanes, s_tokens[lane]);
+    if (lane == 0) s_tokens[32] = tokens;
+  }
+  if (ctas > 1) {
+    cluster_sync();
+    if (cta == 0 && tid < width) {
+      for (int r = 1; r < ctas; ++r) {
+        share += __uint_as_float(load_peer(&s_share[tid], r));
+        count += (int32_t)load_peer(&s_count[tid], r);
+      }
+    }
+    tokens = 0;
+    if (cta == 0 && tid < ctas) tokens = (int32_t)load_peer(&s_tokens[32], tid);
+    cluster_sync();
+    if (cta != 0) return;
+    if (warp == 0) {
+      tokens = __reduce_add_sync(kAllLanes, tokens);
+      if (lane == 0) s_tokens[32] = tokens;
+    }
+  }
+  const int32_t chosen = __reduce_add_sync(kAllLanes, tid < width ? count : 0);
+  if (lane == 0) s_chosen[warp] = chosen;
+  __syncthreads();
+  const float C = (float)__reduce_add_sync(kAllLanes, s_chosen[lane]);
+  const float n = (float)s_tokens[32];
+  float part = 0.0f;
+  if (tid < width && e < E) {
     const float d = C > 0.0f ? (float)count * (float)E / C / n : 0.0f;
     counts[(int64_t)b * E + e] = count;
     slope[(int64_t)b * E + e] = d;
@@ -521,15 +610,19 @@ cudaError_t fp8moe_launch_router(const RouterArgs& args, cudaStream_t s) {
   if (e != cudaSuccess || !balance) return e;
   int width = 32;
   while (width < a.E) width *= 2;
+  const int64_t parts = (a.T + a.chunk - 1) / a.chunk;
+  const int ctas = parts / a.B > 16 ? 8 : 1;
   cudaLaunchConfig_t cfg = {};
-  cudaLaunchAttribute attr[1];
-  pdl_attribute(attr[0]);
-  cfg.gridDim = dim3((unsigned)a.B);
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = ctas, attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+  pdl_attribute(attr[1]);
+  cfg.gridDim = dim3((unsigned)(a.B * ctas));
   cfg.blockDim = dim3(kJoinThreads);
   cfg.stream = s;
   cfg.attrs = attr;
-  cfg.numAttrs = a.T > 0 ? 1 : 0;
-  return cudaLaunchKernelEx(&cfg, balance_join_kernel, a.offsets, a.T, a.B, a.E, width, a.chunk,
+  cfg.numAttrs = a.T > 0 ? 2 : 1;
+  return cudaLaunchKernelEx(&cfg, balance_join_kernel, a.offsets, a.T, a.B, a.E, width, a.chunk, ctas,
                             (const float*)a.part_share, (const int32_t*)a.part_count,
                             (const int32_t*)a.part_tokens, a.counts, a.loss, a.slope);
 }

@@ -86,14 +86,16 @@ __device__ __forceinline__ float warp_sum(float v) {
   for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(kAllLanes, v, o);
   return v;
 }
+// Of lanes 0 to n - 1, for these lanes; the others hold 0.
+__device__ __forceinline__ float first_sum(float v, int n) {
+  for (int o = 1; o < n; o *= 2) v += __shfl_xor_sync(kAllLanes, v, o);
+  return v;
+}
 // A NaN anywhere gives NaN.
 __device__ __forceinline__ float warp_max(float v) {
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) {
-    const float w = __shfl_xor_sync(kAllLanes, v, o);
-    asm("max.NaN.f32 %0, %1, %2;" : "=f"(v) : "f"(v), "f"(w));
-  }
-  return v;
+  float r;
+  asm volatile("redux.sync.max.NaN.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(v));
+  return r;
 }
 __device__ __forceinline__ float max_nan(float a, float b) {
   float r;
