@@ -11,6 +11,7 @@
 #include <cmath>
 #include <cstdint>
 #include <type_traits>
+#include <utility>
 #include <cuda_runtime.h>
 #include <cuda_bf16.h>
 
@@ -53,7 +54,7 @@ __device__ __forceinline__ float choice_value(float x, float b, bool has_bias, b
                                               float inv_sum) {
   if (!has_bias) return x;
   if (x == -INFINITY) return x;
-  return __fadd_rn(sig ? sigmoid(x) : __fmul_rn(expf(x - top), inv_sum), b);
+  return __fadd_rn(sig ? sigmoid(x) : __fmul_rn(exp_neg(x - top), inv_sum), b);
 }
 __device__ __forceinline__ double choice_value_64(float x, float b, bool has_bias, bool sig,
                                                   float top, double sum) {
@@ -119,6 +120,34 @@ __device__ __noinline__ int choose_exactly(const T* row, const float* bias, int 
   return mine;
 }
 
+// Descending, by Batcher's odd-even merge sort: its comparisons, written out by the compiler.
+template <int V>
+struct Network {
+  int count = 0, first[192] = {}, second[192] = {};
+  constexpr Network() {
+    for (int p = 1; p < V; p *= 2)
+      for (int d = p; d >= 1; d /= 2)
+        for (int i = 0; i + d < V; ++i)
+          if (i >= d % p && (i - d % p) % (2 * d) < d && i / (2 * p) == (i + d) / (2 * p))
+            first[count] = i, second[count] = i + d, ++count;
+  }
+};
+template <int V> constexpr Network<V> kNetwork{};
+template <int V, size_t... I>
+__device__ __forceinline__ void sort_steps(uint32_t (&key)[V], std::index_sequence<I...>) {
+  auto step = [&](auto i, auto j) {
+    const uint32_t large = max(key[i], key[j]);
+    key[j] = min(key[i], key[j]);
+    key[i] = large;
+  };
+  (step(std::integral_constant<int, kNetwork<V>.first[I]>(),
+        std::integral_constant<int, kNetwork<V>.second[I]>()), ...);
+}
+template <int V>
+__device__ __forceinline__ void sort_keys(uint32_t (&key)[V]) {
+  sort_steps<V>(key, std::make_index_sequence<kNetwork<V>.count>());
+}
+
 // For lane i: the lane among the first n whose (value, expert) comes at place i, larger values and
 // lower experts first (a NaN value in place of the largest); its own for lanes from n on.
 template <typename F>
@@ -170,13 +199,16 @@ __global__ void __launch_bounds__(kThreads) router_kernel(const __grid_constant_
     float n[V], top = 0.0f, inv_sum = 0.0f;
     auto scores = [&](float largest) {
       top = scale_top(largest, sig);
-      float sum = 0.0f;
+      const bool none = largest == -INFINITY;
+      float2 sum = both(0.0f);
 #pragma unroll
-      for (int j = 0; j < V; ++j) {
-        n[j] = largest == -INFINITY ? 0.0f : scaled_score(x[j], top, sig);
-        sum += n[j];
+      for (int j = 0; j < V; j += 2) {
+        const float2 s = none ? both(0.0f)
+                              : scaled_scores(make_float2(x[j], x[j + 1]), top, sig);
+        n[j] = s.x, n[j + 1] = s.y;
+        sum = add2(sum, s);
       }
-      inv_sum = largest == -INFINITY ? 0.0f : __frcp_rn(warp_sum(sum));
+      inv_sum = none ? 0.0f : inverse(warp_sum(sum.x + sum.y));
     };
 
     if constexpr (GIVEN) {
@@ -193,10 +225,17 @@ __global__ void __launch_bounds__(kThreads) router_kernel(const __grid_constant_
 #pragma unroll
       for (int j = 0; j < V; ++j) {
         const int e = lane * V + j;
-        const float b = has_bias && e < E ? a.bias[e] : 0.0f;
-        const uint32_t o = order_key(choice_value(x[j], b, has_bias, sig, top, inv_sum));
+        float c = x[j];
+        if (has_bias && c != -INFINITY) {
+          const float b = e < E ? a.bias[e] : 0.0f;
+          // (with a balance loss the scores are at hand, on their own scale if that is 0's)
+          if (!sig) c = __fadd_rn(__fmul_rn(n[j], inv_sum), b);
+          else c = __fadd_rn(balance && top == 0.0f ? n[j] : sigmoid(c), b);
+        }
+        const uint32_t o = order_key(c);
         key[j] = o == 0u ? 0u : (o & ~1023u) | (uint32_t)(1023 - e);
       }
+      sort_keys(key);
       // The topk largest keys, and those behind them whose values may be as large: with the same
       // upper bits, or, with a bias, within twice the error of a score (8 * 2^-24 of a sigmoid at
       // most 1; of a softmax score the argument's rounding, at most .4 of the largest score,
@@ -205,13 +244,12 @@ __global__ void __launch_bounds__(kThreads) router_kernel(const __grid_constant_
       float slack = 0.0f;
       int found = 0;
       for (; found <= 32; ++found) {
-        uint32_t m = key[0];
-#pragma unroll
-        for (int j = 1; j < V; ++j) m = max(m, key[j]);
-        m = __reduce_max_sync(kAllLanes, m);
+        const uint32_t m = __reduce_max_sync(kAllLanes, key[0]);
         if (m == 0u || (found >= k && m < floor)) break;
+        const bool mine_is = key[0] == m;
 #pragma unroll
-        for (int j = 0; j < V; ++j) key[j] = key[j] == m ? 0u : key[j];
+        for (int j = 0; j + 1 < V; ++j) key[j] = mine_is ? key[j + 1] : key[j];
+        key[V - 1] = mine_is ? 0u : key[V - 1];
         if (lane == found) mine = m;
         if (found == 0 && has_bias)
           slack = (sig ? 0x1p-20f : 0x1p-17f * inv_sum) + 0x1p-22f * fabsf(key_value(m));
@@ -274,7 +312,7 @@ __global__ void __launch_bounds__(kThreads) router_kernel(const __grid_constant_
         const float nc = id >= 0 ? scaled_score(xc, scale_top(most, sig), sig) : 0.0f;
         w = nc / first_sum(nc, k);
       } else if (id >= 0) {
-        w = sig ? sigmoid(xc) : expf(xc - top) * inv_sum;
+        w = sig ? sigmoid(xc) : exp_neg(xc - top) * inv_sum;
       }
       if (largest != largest) w = largest;       // a NaN among the logits, chosen or not
       if (lane < k) {
@@ -291,7 +329,11 @@ __global__ void __launch_bounds__(kThreads) router_kernel(const __grid_constant_
     if (id >= 0) atomicAdd(&s_count[id], 1);
     ++tokens;
 #pragma unroll
-    for (int j = 0; j < V; ++j) acc[j] += n[j] * inv_sum;
+    for (int j = 0; j < V; j += 2) {
+      const float2 s = fma2(make_float2(n[j], n[j + 1]), both(inv_sum),
+                            make_float2(acc[j], acc[j + 1]));
+      acc[j] = s.x, acc[j + 1] = s.y;
+    }
   };
   auto clear = [&]() {
     tokens = 0;
@@ -518,38 +560,45 @@ __global__ void __launch_bounds__(kThreads) router_bwd_kernel(
   }
   __syncwarp();
 
-  float p[V], sum = 0.0f;
+  float2 d[V / 2], q[V / 2], p[V / 2], sum = both(0.0f);
+  const bool shares = a.dloss != nullptr || joins;
 #pragma unroll
-  for (int j = 0; j < V; ++j) {
-    dx[j] = s_row[j * 32 + lane];
-    p[j] = scaled_score(x[j], top, sig);
-    sum += p[j];
-  }
-  if (a.dloss != nullptr || joins) {
-    const float inv_sum = __frcp_rn(warp_sum(sum));
-    float D[V], dot = 0.0f;
-    if (a.dloss != nullptr) {
-      load_row<float, V, VECT>(a.slope + (int64_t)b * E, E, lane, 0.0f, D);
-      const float dl = a.dloss[b];
-#pragma unroll
-      for (int j = 0; j < V; ++j) D[j] *= dl;
-    } else {
-#pragma unroll
-      for (int j = 0; j < V; ++j) D[j] = 0.0f;
+  for (int h = 0; h < V / 2; ++h) {
+    const float2 v = make_float2(x[2 * h], x[2 * h + 1]);
+    d[h] = make_float2(s_row[2 * h * 32 + lane], s_row[(2 * h + 1) * 32 + lane]);
+    if (sig) {
+      sigmoids(v, p[h], q[h]);
+      if (top != 0.0f)                           // every x is below 0: sigmoid(x) = exp(x) q
+        p[h] = mul2(exp_neg(make_float2(v.x - top, v.y - top)), q[h]);
+    } else if (shares) {
+      p[h] = exp_neg(make_float2(v.x - top, v.y - top));
     }
-#pragma unroll
-    for (int j = 0; j < V; ++j) {
-      if (joins) D[j] += dx[j], dx[j] = 0.0f;
-      p[j] *= inv_sum;
-      dot += D[j] * p[j];
-    }
-    dot = warp_sum(dot);
-#pragma unroll
-    for (int j = 0; j < V; ++j) dx[j] += p[j] * (D[j] - dot);
+    if (shares) sum = add2(sum, p[h]);
   }
-  if (sig) {
+  if (shares) {
+    const float inv_sum = inverse(warp_sum(sum.x + sum.y));
+    float D[V];
+    float2 dot = both(0.0f);
+    if (a.dloss != nullptr) load_row<float, V, VECT>(a.slope + (int64_t)b * E, E, lane, 0.0f, D);
+    const float dl = a.dloss != nullptr ? a.dloss[b] : 0.0f;
 #pragma unroll
-    for (int j = 0; j < V; ++j) dx[j] *= sigmoid(-x[j]);
+    for (int h = 0; h < V / 2; ++h) {
+      float2 g = both(0.0f);
+      if (a.dloss != nullptr) g = mul2(make_float2(D[2 * h], D[2 * h + 1]), both(dl));
+      if (joins) g = add2(g, d[h]), d[h] = both(0.0f);
+      p[h] = mul2(p[h], both(inv_sum));
+      dot = fma2(g, p[h], dot);
+      D[2 * h] = g.x, D[2 * h + 1] = g.y;
+    }
+    const float all = warp_sum(dot.x + dot.y);
+#pragma unroll
+    for (int h = 0; h < V / 2; ++h)
+      d[h] = fma2(p[h], make_float2(D[2 * h] - all, D[2 * h + 1] - all), d[h]);
+  }
+#pragma unroll
+  for (int h = 0; h < V / 2; ++h) {
+    if (sig) d[h] = mul2(d[h], q[h]);
+    dx[2 * h] = d[h].x, dx[2 * h + 1] = d[h].y;
   }
   store_row<T, V, VECT>(out, E, lane, dx);
 }

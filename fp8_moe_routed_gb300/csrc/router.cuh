@@ -6,6 +6,7 @@
 #include <cuda_bf16.h>
 
 #include "ptx.cuh"
+#include "vec16.cuh"
 
 namespace fp8moe {
 
@@ -103,24 +104,57 @@ __device__ __forceinline__ float max_nan(float a, float b) {
   return r;
 }
 
-// sigmoid(x) without cancellation, by t = exp(-|x|): 1 / (1 + t) or t / (1 + t). Within
-// 4 * 2^-24 of it (expf 2 units, the sum, the reciprocal and the product half a unit each).
+// exp(x) for x <= 0 (and NaN), two at a time: by the exponential unit (within 2^-22 of itself) on x
+// times log2 e, with what the product's rounding and the constant's lose put back to first order.
+// Within 6 * 2^-24; 0 below 2^-126.
+__device__ __forceinline__ float2 exp_neg(float2 x) {
+  const float hi = 1.4426950216293335f, lo = 1.9259629911266175e-8f, ln2 = 0.6931471805599453f;
+  x = make_float2(max_nan(x.x, -200.0f), max_nan(x.y, -200.0f));
+  const float2 t = mul2(x, both(hi));
+  const float2 rest = fma2(x, both(lo), fma2(x, both(hi), mul2(t, both(-1.0f))));
+  float2 e;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e.x) : "f"(t.x));
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e.y) : "f"(t.y));
+  return fma2(mul2(e, both(ln2)), rest, e);
+}
+__device__ __forceinline__ float exp_neg(float x) { return exp_neg(make_float2(x, x)).x; }
+
+// 1 / d, by a Newton step from the approximate one (within 2^-24 and a little of it).
+__device__ __forceinline__ float2 inverse(float2 d) {
+  float2 y;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y.x) : "f"(d.x));
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y.y) : "f"(d.y));
+  return fma2(y, fma2(mul2(d, both(-1.0f)), y, both(1.0f)), y);
+}
+__device__ __forceinline__ float inverse(float d) { return inverse(make_float2(d, d)).x; }
+
+// s = sigmoid(x) and q = sigmoid(-x) without cancellation, by t = exp(-|x|): 1 / (1 + t) and
+// t / (1 + t). Each within 5 * 2^-24 (of 1), and within 8 * 2^-24 of itself.
+__device__ __forceinline__ void sigmoids(float2 x, float2& s, float2& q) {
+  const float2 t = exp_neg(make_float2(-fabsf(x.x), -fabsf(x.y)));
+  const float2 large = inverse(add2(t, both(1.0f))), small = mul2(t, large);
+  s = make_float2(x.x < 0.0f ? small.x : large.x, x.y < 0.0f ? small.y : large.y);
+  q = make_float2(x.x < 0.0f ? large.x : small.x, x.y < 0.0f ? large.y : small.y);
+}
 __device__ __forceinline__ float sigmoid(float x) {
-  const float t = expf(-fabsf(x));
-  const float r = __frcp_rn(__fadd_rn(1.0f, t));
-  return x >= 0.0f ? r : x < 0.0f ? __fmul_rn(t, r) : x + r;   // NaN stays NaN
+  float2 s, q;
+  sigmoids(make_float2(x, x), s, q);
+  return s.x;
 }
 
 // A score on the row's scale, n(x) = score(x) * exp(-top): top = the largest logit, or, with
 // sigmoid scores, the largest one below zero (0 if there is one above). The scores themselves may
 // all round to zero (sigmoid below -104); their ratios, which is what weights and shares are,
 // do not depend on the scale, and the largest n is at least 1/2. Experts at -inf have 0.
+__device__ __forceinline__ float2 scaled_scores(float2 x, float top, bool sig) {
+  const float2 y = make_float2(x.x - top, x.y - top);
+  if (!sig) return exp_neg(y);
+  float2 s, q;
+  sigmoids(x, s, q);
+  return top == 0.0f ? s : mul2(exp_neg(y), q);   // top < 0, so every x is, and s = exp(x) q
+}
 __device__ __forceinline__ float scaled_score(float x, float top, bool sig) {
-  if (!sig) return expf(x - top);
-  const float t = expf(-fabsf(x));
-  const float r = __frcp_rn(1.0f + t);
-  if (top == 0.0f) return x >= 0.0f ? r : x < 0.0f ? t * r : x + r;
-  return expf(x - top) * r;                  // top < 0, so every x is
+  return scaled_scores(make_float2(x, x), top, sig).x;
 }
 __device__ __forceinline__ float scale_top(float largest, bool sig) {
   return sig && largest > 0.0f ? 0.0f : largest;
