@@ -27,6 +27,7 @@ namespace {
 constexpr int kWarps = 8;
 constexpr int kThreads = 32 * kWarps;
 constexpr int kJoinThreads = 1024;
+constexpr int64_t kManyTokens = 16384;          // from here on eight lanes take a token
 
 __device__ __forceinline__ uint32_t load_peer(const void* p, int cta) {
   uint32_t v;
@@ -61,6 +62,15 @@ __device__ __forceinline__ double choice_value_64(float x, float b, bool has_bia
   if (!has_bias) return (double)x;
   const double s = sig ? 1.0 / (1.0 + exp(-(double)x)) : exp((double)x - (double)top) / sum;
   return s + (double)b;
+}
+
+// Twice the error of a score and of its sum with the bias: 5 * 2^-24 of a sigmoid; of a softmax
+// score the argument's rounding, at most .4 of the largest score, the exponential's and the sum's
+// of 37 terms; half a unit of the sum.
+__device__ __forceinline__ float choice_slack(uint32_t largest, uint32_t least, bool sig,
+                                              float inv_sum) {
+  return (sig ? 0x1p-20f : 0x1p-17f * inv_sum) +
+         0x1p-22f * (fabsf(key_value(largest)) + fabsf(key_value(least)));
 }
 
 // The choice in 64 bits, among the experts whose f32 value is at least `cut`: lane j's j-th
@@ -166,6 +176,39 @@ __device__ __forceinline__ int sorted_from(F value, int id, int n) {
   return from;
 }
 
+// This CTA's chunk of tokens, one run after the other: of each sequence that has a part in it.
+// What lies outside of the sequences is padding.
+template <bool GIVEN, typename Clear, typename Run, typename Flush>
+__device__ __forceinline__ void walk_chunk(const RouterArgs& a, Clear clear, Run run, Flush flush) {
+  const int64_t begin = (int64_t)blockIdx.x * a.chunk;
+  const int64_t end = begin + a.chunk < a.T ? begin + a.chunk : a.T;
+  auto padding = [&](int64_t from, int64_t to) {
+    if constexpr (!GIVEN) {
+      for (int64_t i = from * a.k + threadIdx.x; i < to * a.k; i += kThreads) {
+        a.ids[i] = -1;
+        a.weights[i] = 0.0f;
+      }
+    }
+  };
+  int64_t at = begin;
+  int b = 0;
+  const int B = a.offsets != nullptr ? a.B : 1;
+  if (a.offsets != nullptr) {
+    at = max(begin, min((int64_t)a.offsets[0], end));
+    padding(begin, at);
+    b = at < end ? max(0, find_sequence(a.offsets, B, at)) : B;
+  }
+  for (; at < end && b < B; ++b) {
+    const int64_t stop = a.offsets != nullptr ? min((int64_t)a.offsets[b + 1], end) : end;
+    if (stop <= at) continue;
+    clear();
+    run(at, stop);
+    flush((int64_t)blockIdx.x + b);
+    at = stop;
+  }
+  padding(at, end);
+}
+
 template <typename T, int V, bool VECT, bool GIVEN>
 __global__ void __launch_bounds__(kThreads) router_kernel(const __grid_constant__ RouterArgs a) {
   extern __shared__ float s_mem[];
@@ -237,28 +280,35 @@ __global__ void __launch_bounds__(kThreads) router_kernel(const __grid_constant_
       }
       sort_keys(key);
       // The topk largest keys, and those behind them whose values may be as large: with the same
-      // upper bits, or, with a bias, within twice the error of a score (8 * 2^-24 of a sigmoid at
-      // most 1; of a softmax score the argument's rounding, at most .4 of the largest score,
-      // and the sum's of 37 terms; the sum with the bias adds half a unit).
-      uint32_t mine = 0, floor = 0;
-      float slack = 0.0f;
-      int found = 0;
-      for (; found <= 32; ++found) {
-        const uint32_t m = __reduce_max_sync(kAllLanes, key[0]);
-        if (m == 0u || (found >= k && m < floor)) break;
-        const bool mine_is = key[0] == m;
+      // upper bits, or, with a bias, within the error of two scores.
+      uint32_t mine = 0, m = 0, top_key = 0;
+      auto take = [&](int place) {               // the largest key, out of its lane
+        m = __reduce_max_sync(kAllLanes, key[0]);
+        const bool here = key[0] == m;
 #pragma unroll
-        for (int j = 0; j + 1 < V; ++j) key[j] = mine_is ? key[j + 1] : key[j];
-        key[V - 1] = mine_is ? 0u : key[V - 1];
-        if (lane == found) mine = m;
-        if (found == 0 && has_bias)
-          slack = (sig ? 0x1p-20f : 0x1p-17f * inv_sum) + 0x1p-22f * fabsf(key_value(m));
-        if (found == k - 1) {
-          floor = m & ~1023u;
-          if (has_bias) {
-            slack += 0x1p-22f * fabsf(key_value(m));
-            floor = order_key(key_value(m) - slack) & ~1023u;
-          }
+        for (int j = 0; j + 1 < V; ++j) key[j] = here ? key[j + 1] : key[j];
+        key[V - 1] = here ? 0u : key[V - 1];
+        if (lane == place) mine = m;
+      };
+      take(0);
+      top_key = m;
+#pragma unroll 1
+      for (int r = 1; r < k; ++r) take(r);
+      int found = k;
+      float slack = 0.0f;
+      const uint32_t k_th = m;
+      if (m == 0u) {
+        found = __popc(__ballot_sync(kAllLanes, mine != 0u));
+      } else {
+        uint32_t floor = m & ~1023u;
+        if (has_bias) {
+          slack = choice_slack(top_key, m, sig, inv_sum);
+          floor = order_key(key_value(m) - slack) & ~1023u;
+        }
+        while (found <= 32) {
+          const uint32_t next = __reduce_max_sync(kAllLanes, key[0]);
+          if (next == 0u || next < floor) break;
+          take(found++);
         }
       }
       if (mine) id = 1023 - (int)(mine & 1023u);
@@ -269,8 +319,8 @@ __global__ void __launch_bounds__(kThreads) router_kernel(const __grid_constant_
         float c = id >= 0 ? choice_value(xc, b, has_bias, sig, top, inv_sum) : -INFINITY;
         // into the order of the whole values
         float next = __shfl_down_sync(kAllLanes, c, 1);
-        const bool wrong = lane + 1 < found && c < next;
-        if (__any_sync(kAllLanes, wrong) && found <= 32) {
+        const bool wrong = __any_sync(kAllLanes, lane + 1 < found && c < next);
+        if (wrong && found <= 32) {
           const int from = sorted_from(c, id, found);
           c = __shfl_sync(kAllLanes, c, from);
           xc = __shfl_sync(kAllLanes, xc, from);
@@ -289,7 +339,7 @@ __global__ void __launch_bounds__(kThreads) router_kernel(const __grid_constant_
         open = __any_sync(kAllLanes, open);
         if (found > 32 || (open && !sig)) {
           // cut: the last that can belong to the choice
-          const float cut = key_value(__shfl_sync(kAllLanes, mine, k - 1)) - slack;
+          const float cut = key_value(k_th) - slack;
           id = choose_exactly(row, a.bias, E, k, sig, top, inv_sum, cut, list);
           __syncwarp();
           xc = id >= 0 ? load_f32(row + id) : -INFINITY;
@@ -368,36 +418,250 @@ __global__ void __launch_bounds__(kThreads) router_kernel(const __grid_constant_
     }
     __syncthreads();
   };
-  auto padding = [&](int64_t from, int64_t to) {
-    if constexpr (!GIVEN) {
-      for (int64_t i = from * k + threadIdx.x; i < to * k; i += kThreads) {
-        a.ids[i] = -1;
-        a.weights[i] = 0.0f;
+  walk_chunk<GIVEN>(a, clear, [&](int64_t from, int64_t to) {
+    for (int64_t t = from + warp; t < to; t += kWarps) token(t);
+  }, flush);
+}
+
+// Many tokens and at most 256 experts, of which 8 are chosen: eight lanes take a token, so that an
+// instruction of the choice works for four. Lane l of a group holds experts [l V, l V + V). What
+// is as above is not explained again; a token whose border is not settled by the upper 22 bits
+// (or, with a bias, by f32) is chosen by the whole warp in choose_exactly. (65536 tokens, 128
+// experts, bf16: 632 instructions a token in the kernel above.)
+constexpr int kGroup = 8, kGroups = 4;
+
+template <typename F>
+__device__ __forceinline__ F group_max(F v) {
+#pragma unroll
+  for (int o = 1; o < kGroup; o *= 2) {
+    const F w = __shfl_xor_sync(kAllLanes, v, o);
+    if constexpr (std::is_same<F, float>::value) v = max_nan(v, w);
+    else v = max(v, w);
+  }
+  return v;
+}
+__device__ __forceinline__ float group_sum(float v) {
+#pragma unroll
+  for (int o = 1; o < kGroup; o *= 2) v += __shfl_xor_sync(kAllLanes, v, o);
+  return v;
+}
+
+template <typename T, int V, bool VECT, bool GIVEN>
+__global__ void __launch_bounds__(kThreads) router_group_kernel(
+    const __grid_constant__ RouterArgs a) {
+  constexpr int W = kGroup * V;
+  extern __shared__ float s_mem[];
+  float* s_share = s_mem;                                           // [kWarps][W]
+  int32_t* s_count = reinterpret_cast<int32_t*>(s_mem + kWarps * W);   // [W]
+  __shared__ int32_t s_tokens[kWarps];
+  pdl_launch_dependents();
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int l = lane & (kGroup - 1), g = lane / kGroup;
+  const uint32_t group_lanes = 0xffu << (g * kGroup);
+  const int E = a.E, k = a.k;
+  const bool sig = a.sig, has_bias = !GIVEN && a.bias != nullptr;
+  const T* logits = static_cast<const T*>(a.logits);
+  const bool balance = a.part_share != nullptr;
+  uint16_t* list = reinterpret_cast<uint16_t*>(s_mem) + warp * 2 * W;
+
+  float acc[V];
+  int tokens = 0;
+  auto group_any = [&](bool x) { return (__ballot_sync(kAllLanes, x) & group_lanes) != 0u; };
+
+  // four tokens of the warp; `on`: this group's exists (its lanes go along all the same)
+  auto four = [&](int64_t first, int64_t to) {
+    const bool on = first + g < to;
+    const int64_t t = on ? first + g : first;
+    const T* row = logits + t * E;
+    float x[V];
+    load_row<T, V, VECT>(row, E, l, -INFINITY, x);
+    int id = -1;
+    if (GIVEN && on && l < k) id = a.given[t * k + l];
+    auto row_max = [&]() {
+      float m = x[0];
+#pragma unroll
+      for (int j = 1; j < V; ++j) m = max_nan(m, x[j]);
+      return group_max(m);
+    };
+    float n[V], top = 0.0f, inv_sum = 0.0f;
+    auto scores = [&](float largest) {
+      top = scale_top(largest, sig);
+      const bool none = largest == -INFINITY;
+      float2 sum = both(0.0f);
+#pragma unroll
+      for (int j = 0; j < V; j += 2) {
+        const float2 s = none ? both(0.0f)
+                              : scaled_scores(make_float2(x[j], x[j + 1]), top, sig);
+        n[j] = s.x, n[j + 1] = s.y;
+        sum = add2(sum, s);
+      }
+      const float all = group_sum(sum.x + sum.y);
+      inv_sum = none ? 0.0f : inverse(all);
+    };
+
+    if constexpr (GIVEN) {
+      scores(row_max());
+    } else {
+      float largest = 0.0f;
+      if (has_bias) {
+        largest = row_max();
+        if (!sig || balance) scores(largest);
+      }
+      uint32_t key[V];
+#pragma unroll
+      for (int j = 0; j < V; ++j) {
+        const int e = l * V + j;
+        float c = x[j];
+        if (has_bias && c != -INFINITY) {
+          const float b = e < E ? a.bias[e] : 0.0f;
+          if (!sig) c = __fadd_rn(__fmul_rn(n[j], inv_sum), b);
+          else c = __fadd_rn(balance && top == 0.0f ? n[j] : sigmoid(c), b);
+        }
+        const uint32_t o = order_key(c);
+        key[j] = o == 0u ? 0u : (o & ~1023u) | (uint32_t)(1023 - e);
+      }
+      sort_keys(key);
+      uint32_t mine = 0, m = 0, top_key = 0;
+#pragma unroll 1
+      for (int r = 0; r < k; ++r) {
+        m = group_max(key[0]);
+        const bool here = key[0] == m;
+#pragma unroll
+        for (int j = 0; j + 1 < V; ++j) key[j] = here ? key[j + 1] : key[j];
+        key[V - 1] = here ? 0u : key[V - 1];
+        if (l == r) mine = m;
+        if (r == 0) top_key = m;
+      }
+      const uint32_t next_key = group_max(key[0]);
+      const float slack = has_bias && m != 0u ? choice_slack(top_key, m, sig, inv_sum) : 0.0f;
+      const uint32_t floor = (has_bias ? order_key(key_value(m) - slack) : m) & ~1023u;
+      // (the upper 22 bits are all that a bf16 logit has)
+      bool hard = (has_bias || sizeof(T) == 4) && on && m != 0u && next_key != 0u &&
+                  next_key >= floor;
+
+      if (mine) id = 1023 - (int)(mine & 1023u);
+      float xc = id >= 0 ? load_f32(row + id) : -INFINITY;
+      const float b = has_bias && id >= 0 ? a.bias[id] : 0.0f;
+      float c = id >= 0 ? choice_value(xc, b, has_bias, sig, top, inv_sum) : -INFINITY;
+      float next = __shfl_down_sync(kAllLanes, c, 1);
+      if (__any_sync(kAllLanes, l + 1 < k && c < next)) {
+        // by the whole values; a NaN in place of the largest, those without an expert at the end
+        const float value = c != c ? INFINITY : c;
+        const int order = id >= 0 ? id : 2048 + l;
+        int rank = 0;
+#pragma unroll
+        for (int o = 1; o < kGroup; ++o) {
+          const float v = __shfl_xor_sync(kAllLanes, value, o);
+          const int e = __shfl_xor_sync(kAllLanes, order, o);
+          rank += v > value || (v == value && e < order);
+        }
+        int from = lane;
+#pragma unroll
+        for (int o = 0; o < kGroup; ++o)
+          if (__shfl_xor_sync(kAllLanes, rank, o) == l) from = lane ^ o;
+        c = __shfl_sync(kAllLanes, c, from);
+        xc = __shfl_sync(kAllLanes, xc, from);
+        id = __shfl_sync(kAllLanes, id, from);
+        next = __shfl_down_sync(kAllLanes, c, 1);
+      }
+      if (has_bias) {
+        const float bc = id >= 0 ? a.bias[id] : 0.0f;
+        const float next_x = __shfl_down_sync(kAllLanes, xc, 1);
+        const float next_b = __shfl_down_sync(kAllLanes, bc, 1);
+        const int next_id = __shfl_down_sync(kAllLanes, id, 1);
+        hard |= group_any(on && l + 1 < k && next_id >= 0 && !(c - next > slack) &&
+                          !(xc == next_x && bc == next_b));
+      }
+      const float cut = key_value(m) - slack;
+      for (uint32_t left = __ballot_sync(kAllLanes, hard && l == 0); left != 0u; left &= left - 1u) {
+        const int who = __ffs(left) - 1;
+        const int64_t th = __shfl_sync(kAllLanes, t, who);
+        const int exact = choose_exactly(
+            logits + th * E, a.bias, E, k, sig, __shfl_sync(kAllLanes, top, who),
+            __shfl_sync(kAllLanes, inv_sum, who), __shfl_sync(kAllLanes, cut, who), list);
+        const int found = __shfl_sync(kAllLanes, exact, l);
+        if (g == who / kGroup) id = l < k ? found : -1;
+        __syncwarp();
+      }
+      if (__any_sync(kAllLanes, hard)) xc = id >= 0 ? load_f32(row + id) : -INFINITY;
+
+      if (!has_bias) {
+        largest = __shfl_sync(kAllLanes, xc, g * kGroup);
+        if (balance || (!sig && !a.normalize)) scores(largest);
+      }
+      float w = 0.0f;
+      if (a.normalize) {
+        const float most = has_bias ? group_max(xc) : largest;
+        const float nc = id >= 0 ? scaled_score(xc, scale_top(most, sig), sig) : 0.0f;
+        w = nc / group_sum(nc);
+      } else if (id >= 0) {
+        w = sig ? sigmoid(xc) : exp_neg(xc - top) * inv_sum;
+      }
+      if (largest != largest) w = largest;
+      if (on && l < k) {
+        a.ids[t * k + l] = id;
+        a.weights[t * k + l] = id >= 0 ? a.scale * w : 0.0f;
+      }
+    }
+    if (!balance) return;
+    if (GIVEN && id >= E) {
+      status_set(kStatusBadExpert);
+      id = -1;
+    }
+    const bool chosen = group_any(id >= 0);        // a vote of all lanes: not behind a condition
+    const bool counts = on && chosen;
+    if (counts && id >= 0) atomicAdd(&s_count[id], 1);
+    if (counts) {
+      tokens += l == 0;
+#pragma unroll
+      for (int j = 0; j < V; j += 2) {
+        const float2 s = fma2(make_float2(n[j], n[j + 1]), both(inv_sum),
+                              make_float2(acc[j], acc[j + 1]));
+        acc[j] = s.x, acc[j + 1] = s.y;
       }
     }
   };
-
-  const int64_t begin = (int64_t)blockIdx.x * a.chunk;
-  const int64_t end = begin + a.chunk < a.T ? begin + a.chunk : a.T;
-  if (a.offsets == nullptr) {
-    clear();
-    for (int64_t t = begin + warp; t < end; t += kWarps) token(t);
-    flush(blockIdx.x);
-    return;
-  }
-  int64_t at = max(begin, min((int64_t)a.offsets[0], end));
-  padding(begin, at);
-  // one run of tokens after the other: of each sequence that has a part in this chunk
-  int b = at < end ? max(0, find_sequence(a.offsets, a.B, at)) : a.B;
-  for (; at < end && b < a.B; ++b) {
-    const int64_t stop = min((int64_t)a.offsets[b + 1], end);
-    if (stop <= at) continue;
-    clear();
-    for (int64_t t = at + warp; t < stop; t += kWarps) token(t);
-    flush((int64_t)blockIdx.x + b);
-    at = stop;
-  }
-  padding(at, end);
+  auto clear = [&]() {
+    tokens = 0;
+#pragma unroll
+    for (int j = 0; j < V; ++j) acc[j] = 0.0f;
+    if (balance) {
+      for (int i = threadIdx.x; i < W; i += kThreads) s_count[i] = 0;
+      __syncthreads();
+    }
+  };
+  auto flush = [&](int64_t slot) {
+    if (!balance) return;
+    __syncthreads();
+#pragma unroll
+    for (int j = 0; j < V; ++j) {
+      float s = acc[j];
+      s += __shfl_xor_sync(kAllLanes, s, kGroup);
+      s += __shfl_xor_sync(kAllLanes, s, 2 * kGroup);
+      if (g == 0) s_share[warp * W + j * kGroup + l] = s;
+    }
+    const int all = __reduce_add_sync(kAllLanes, tokens);
+    if (lane == 0) s_tokens[warp] = all;
+    __syncthreads();
+    for (int i = threadIdx.x; i < W; i += kThreads) {
+      const int e = (i % kGroup) * V + i / kGroup;
+      if (e >= E) continue;
+      float sum = 0.0f;
+#pragma unroll
+      for (int w = 0; w < kWarps; ++w) sum += s_share[w * W + i];
+      a.part_share[slot * E + e] = sum;
+      a.part_count[slot * E + e] = s_count[e];
+    }
+    if (threadIdx.x == 0) {
+      int n = 0;
+      for (int w = 0; w < kWarps; ++w) n += s_tokens[w];
+      a.part_tokens[slot] = n;
+    }
+    __syncthreads();
+  };
+  walk_chunk<GIVEN>(a, clear, [&](int64_t from, int64_t to) {
+    for (int64_t t = from + warp * kGroups; t < to; t += kWarps * kGroups) four(t, to);
+  }, flush);
 }
 
 // Adds up a sequence's parts in a fixed order: counts, slope and loss. A cluster a sequence, of
@@ -524,7 +788,8 @@ __global__ void __launch_bounds__(kThreads) router_bwd_kernel(
   for (int j = 1; j < V; ++j) largest = max_nan(largest, x[j]);
   largest = warp_max(largest);
   // nothing was chosen for this token: padding, or no expert was left
-  if (b < 0 || b >= a.B || largest == -INFINITY || !__any_sync(kAllLanes, id >= 0)) {
+  const bool chosen = __any_sync(kAllLanes, id >= 0);
+  if (b < 0 || b >= a.B || largest == -INFINITY || !chosen) {
 #pragma unroll
     for (int j = 0; j < V; ++j) dx[j] = 0.0f;
     store_row<T, V, VECT>(out, E, lane, dx);
@@ -622,6 +887,21 @@ cudaError_t with_width(int E, F f) {
 template <typename T, bool GIVEN>
 cudaError_t launch_router(const RouterArgs& a, cudaStream_t s) {
   const int64_t grid = (a.T + a.chunk - 1) / a.chunk;
+  if (a.T >= kManyTokens && a.E <= 256 && a.k <= kGroup) {
+    auto launch = [&](auto width) {
+      constexpr int V = decltype(width)::value;
+      const size_t smem = (size_t)(kWarps + 1) * kGroup * V * sizeof(float);
+      if (whole_pieces<T>(a.E, V))
+        router_group_kernel<T, V, true, GIVEN><<<(unsigned)grid, kThreads, smem, s>>>(a);
+      else
+        router_group_kernel<T, V, false, GIVEN><<<(unsigned)grid, kThreads, smem, s>>>(a);
+      return cudaGetLastError();
+    };
+    if (a.E <= 32) return launch(std::integral_constant<int, 4>());
+    if (a.E <= 64) return launch(std::integral_constant<int, 8>());
+    if (a.E <= 128) return launch(std::integral_constant<int, 16>());
+    return launch(std::integral_constant<int, 32>());
+  }
   return with_width(a.E, [&](auto width) {
     constexpr int V = decltype(width)::value;
     const size_t smem = (size_t)(kWarps + 1) * 32 * V * sizeof(float);
@@ -641,14 +921,16 @@ using namespace fp8moe;
 FP8MOE_DEFINE_STATUS_TAKE(fp8moe_status_take_router)
 
 int fp8moe_balance_chunk(int64_t T) {
-  const int64_t c = (T / 304 + kWarps - 1) / kWarps * kWarps;
-  return (int)(c < kWarps ? kWarps : c > 128 ? 128 : c);
+  // two CTAs on an SM, in steps of what a CTA's warps take at once
+  const int64_t step = T < kManyTokens ? kWarps : kWarps * kGroups;
+  const int64_t c = (T / 304 + step - 1) / step * step;
+  return (int)(c < step ? step : c > 256 ? 256 : c);
 }
 
 cudaError_t fp8moe_launch_router(const RouterArgs& args, cudaStream_t s) {
   RouterArgs a = args;
   const bool balance = a.part_share != nullptr;
-  a.chunk = balance ? fp8moe_balance_chunk(a.T) : kWarps;
+  a.chunk = balance || a.T >= kManyTokens ? fp8moe_balance_chunk(a.T) : kWarps;
   cudaError_t e = cudaSuccess;
   if (a.T > 0) {
     if (a.given != nullptr)
