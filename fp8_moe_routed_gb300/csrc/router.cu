@@ -36,12 +36,15 @@ __device__ __forceinline__ uint32_t load_peer(const void* p, int cta) {
   return v;
 }
 
-// Ascending with the value; a NaN is the largest, -inf is no candidate (0).
+// Ascending with the value; a NaN is the largest. -inf lies below kNone: it is no candidate.
+constexpr uint32_t kNone = 0x00800000u;
 __device__ __forceinline__ uint32_t order_key(float v) {
-  if (v != v) return 0xffffffffu;
-  const uint32_t u = __float_as_uint(v + 0.0f);              // -0 is 0
-  if (u == 0xff800000u) return 0u;
+  const uint32_t u = __float_as_uint(__fadd_rn(v, 0.0f));    // -0 is 0, a NaN the positive one
   return u ^ ((uint32_t)((int32_t)u >> 31) | 0x80000000u);
+}
+// The upper 22 bits, then the expert, the lowest first.
+__device__ __forceinline__ uint32_t choice_key(float v, int e) {
+  return (order_key(v) & ~1023u) | (uint32_t)(1023 - e);
 }
 
 // The smallest value of a key's upper 22 bits.
@@ -88,7 +91,7 @@ __device__ __noinline__ int choose_exactly(const T* row, const float* bias, int 
     const float b = has_bias && e < E ? bias[e] : 0.0f;
     if (has_bias && !sig && e < E) sum += exp((double)x - (double)top);
     const float c = choice_value(x, b, has_bias, sig, top, inv_sum);
-    const bool in = e < E && order_key(c) != 0u && !(c < cut);
+    const bool in = e < E && order_key(c) >= kNone && !(c < cut);
     const uint32_t who = __ballot_sync(kAllLanes, in);
     if (in) list[n + __popc(who & ((1u << lane) - 1u))] = (uint16_t)e;
     n += __popc(who);
@@ -275,8 +278,7 @@ __global__ void __launch_bounds__(kThreads) router_kernel(const __grid_constant_
           if (!sig) c = __fadd_rn(__fmul_rn(n[j], inv_sum), b);
           else c = __fadd_rn(balance && top == 0.0f ? n[j] : sigmoid(c), b);
         }
-        const uint32_t o = order_key(c);
-        key[j] = o == 0u ? 0u : (o & ~1023u) | (uint32_t)(1023 - e);
+        key[j] = choice_key(c, e);
       }
       sort_keys(key);
       // The topk largest keys, and those behind them whose values may be as large: with the same
@@ -297,8 +299,8 @@ __global__ void __launch_bounds__(kThreads) router_kernel(const __grid_constant_
       int found = k;
       float slack = 0.0f;
       const uint32_t k_th = m;
-      if (m == 0u) {
-        found = __popc(__ballot_sync(kAllLanes, mine != 0u));
+      if (m < kNone) {
+        found = __popc(__ballot_sync(kAllLanes, mine >= kNone));
       } else {
         uint32_t floor = m & ~1023u;
         if (has_bias) {
@@ -307,11 +309,11 @@ __global__ void __launch_bounds__(kThreads) router_kernel(const __grid_constant_
         }
         while (found <= 32) {
           const uint32_t next = __reduce_max_sync(kAllLanes, key[0]);
-          if (next == 0u || next < floor) break;
+          if (next < kNone || next < floor) break;
           take(found++);
         }
       }
-      if (mine) id = 1023 - (int)(mine & 1023u);
+      if (mine >= kNone) id = 1023 - (int)(mine & 1023u);
       float xc = id >= 0 ? load_f32(row + id) : -INFINITY;
       if (!has_bias) largest = __shfl_sync(kAllLanes, xc, 0);   // but for equal upper bits
       if (k > 1 || found > 1) {
@@ -517,8 +519,7 @@ __global__ void __launch_bounds__(kThreads) router_group_kernel(
           if (!sig) c = __fadd_rn(__fmul_rn(n[j], inv_sum), b);
           else c = __fadd_rn(balance && top == 0.0f ? n[j] : sigmoid(c), b);
         }
-        const uint32_t o = order_key(c);
-        key[j] = o == 0u ? 0u : (o & ~1023u) | (uint32_t)(1023 - e);
+        key[j] = choice_key(c, e);
       }
       sort_keys(key);
       uint32_t mine = 0, m = 0, top_key = 0;
@@ -533,13 +534,13 @@ __global__ void __launch_bounds__(kThreads) router_group_kernel(
         if (r == 0) top_key = m;
       }
       const uint32_t next_key = group_max(key[0]);
-      const float slack = has_bias && m != 0u ? choice_slack(top_key, m, sig, inv_sum) : 0.0f;
+      const float slack = has_bias && m >= kNone ? choice_slack(top_key, m, sig, inv_sum) : 0.0f;
       const uint32_t floor = (has_bias ? order_key(key_value(m) - slack) : m) & ~1023u;
       // (the upper 22 bits are all that a bf16 logit has)
-      bool hard = (has_bias || sizeof(T) == 4) && on && m != 0u && next_key != 0u &&
+      bool hard = (has_bias || sizeof(T) == 4) && on && m >= kNone && next_key >= kNone &&
                   next_key >= floor;
 
-      if (mine) id = 1023 - (int)(mine & 1023u);
+      if (mine >= kNone) id = 1023 - (int)(mine & 1023u);
       float xc = id >= 0 ? load_f32(row + id) : -INFINITY;
       const float b = has_bias && id >= 0 ? a.bias[id] : 0.0f;
       float c = id >= 0 ? choice_value(xc, b, has_bias, sig, top, inv_sum) : -INFINITY;
@@ -761,16 +762,32 @@ __global__ void __launch_bounds__(kJoinThreads) balance_join_kernel(const int32_
 // dx = q * (w (dw - sum dw w) + p (D - sum D p)),  q = 1 (softmax) or sigmoid(-x),
 // D = dloss * slope. Weights that are not normalised: of softmax scores their gradient joins
 // D, of sigmoid scores it is dw s.
-template <typename T, int V, bool VECT>
+// Of the G lanes that have a token.
+template <int G>
+__device__ __forceinline__ float lanes_max(float v) {
+  if constexpr (G == 32) return warp_max(v);
+  else return group_max(v);
+}
+template <int G>
+__device__ __forceinline__ float lanes_sum(float v) {
+  if constexpr (G == 32) return warp_sum(v);
+  else return group_sum(v);
+}
+
+template <typename T, int G, int V, bool VECT>
 __global__ void __launch_bounds__(kThreads) router_bwd_kernel(
     const __grid_constant__ RouterBwdArgs a) {
   extern __shared__ float s_mem[];
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  float* s_row = s_mem + warp * 32 * V;
+  const int lane = threadIdx.x % G, warp = threadIdx.x / 32;
+  float* s_row = s_mem + (threadIdx.x / G) * G * V;
   const int E = a.E, k = a.k;
   const bool sig = a.sig;
-  const int64_t t = (int64_t)blockIdx.x * kWarps + warp;
-  if (t >= a.T) return;
+  const int64_t warp_first = ((int64_t)blockIdx.x * kWarps + warp) * (32 / G);
+  if (warp_first >= a.T) return;
+  // the lanes of a group past the last token go along with its work and write nothing
+  const int64_t mine = warp_first + threadIdx.x % 32 / G;
+  const bool on = mine < a.T;
+  const int64_t t = on ? mine : a.T - 1;
   const T* row = static_cast<const T*>(a.logits) + t * E;
   T* out = static_cast<T*>(a.dlogits) + t * E;
   float x[V], dx[V];
@@ -786,35 +803,42 @@ __global__ void __launch_bounds__(kThreads) router_bwd_kernel(
   float largest = x[0];
 #pragma unroll
   for (int j = 1; j < V; ++j) largest = max_nan(largest, x[j]);
-  largest = warp_max(largest);
+  largest = lanes_max<G>(largest);
   // nothing was chosen for this token: padding, or no expert was left
-  const bool chosen = __any_sync(kAllLanes, id >= 0);
-  if (b < 0 || b >= a.B || largest == -INFINITY || !chosen) {
+  const uint32_t whole = G == 32 ? kAllLanes : ((1u << (G & 31)) - 1u) << (threadIdx.x % 32 / G * G);
+  const bool chosen = (__ballot_sync(kAllLanes, id >= 0) & whole) != 0u;
+  const bool none = b < 0 || b >= a.B || largest == -INFINITY || !chosen;
+  if (__all_sync(kAllLanes, none)) {
 #pragma unroll
     for (int j = 0; j < V; ++j) dx[j] = 0.0f;
-    store_row<T, V, VECT>(out, E, lane, dx);
+    if (on) store_row<T, V, VECT>(out, E, lane, dx);
     return;
   }
+  if (none) b = 0;
   const float xc = id >= 0 ? load_f32(row + id) : -INFINITY;
   const float top = scale_top(largest, sig);
 #pragma unroll
-  for (int j = 0; j < V; ++j) s_row[j * 32 + lane] = 0.0f;
+  for (int j = 0; j < V; ++j) s_row[j * G + lane] = 0.0f;
   __syncwarp();
 
   // each choice's part, put to its expert
   float part = 0.0f;
   const bool joins = !a.normalize && !sig;
   if (a.normalize) {
-    const float most = warp_max(xc);
+    const float most = lanes_max<G>(xc);
     const float nc = id >= 0 && xc != -INFINITY ? scaled_score(xc, scale_top(most, sig), sig) : 0.0f;
-    const float total = largest != largest ? largest : warp_sum(nc);
+    const float sum = lanes_sum<G>(nc);
+    const float total = largest != largest ? largest : sum;
     const float w = total > 0.0f || total != total ? nc / total : 0.0f;
-    part = w * (dw - warp_sum(dw * w));
+    part = w * (dw - lanes_sum<G>(dw * w));
   } else {
     part = joins ? dw : dw * sigmoid(xc);
   }
-  const int place = id >= 0 ? (id % V) * 32 + id / V : -1 - lane;
-  const bool alone = __match_any_sync(kAllLanes, place) == (1u << lane);
+  const int place = id >= 0 ? (id % V) * G + id / V : 0;
+  // is an expert among the choices twice?
+  const int self = threadIdx.x % 32;
+  const int key = id >= 0 ? self / G * 1024 + id : -1 - self;
+  const bool alone = __match_any_sync(kAllLanes, key) == (1u << self);
   if (__all_sync(kAllLanes, alone)) {
     if (id >= 0) s_row[place] = part;
   } else {                                    // an expert twice: in the order of the choices
@@ -825,12 +849,12 @@ __global__ void __launch_bounds__(kThreads) router_bwd_kernel(
   }
   __syncwarp();
 
-  float2 d[V / 2], q[V / 2], p[V / 2], sum = both(0.0f);
+  float2 d[V / 2], q[V / 2], p[V / 2], shares_sum = both(0.0f);
   const bool shares = a.dloss != nullptr || joins;
 #pragma unroll
   for (int h = 0; h < V / 2; ++h) {
     const float2 v = make_float2(x[2 * h], x[2 * h + 1]);
-    d[h] = make_float2(s_row[2 * h * 32 + lane], s_row[(2 * h + 1) * 32 + lane]);
+    d[h] = make_float2(s_row[2 * h * G + lane], s_row[(2 * h + 1) * G + lane]);
     if (sig) {
       sigmoids(v, p[h], q[h]);
       if (top != 0.0f)                           // every x is below 0: sigmoid(x) = exp(x) q
@@ -838,10 +862,10 @@ __global__ void __launch_bounds__(kThreads) router_bwd_kernel(
     } else if (shares) {
       p[h] = exp_neg(make_float2(v.x - top, v.y - top));
     }
-    if (shares) sum = add2(sum, p[h]);
+    if (shares) shares_sum = add2(shares_sum, p[h]);
   }
   if (shares) {
-    const float inv_sum = inverse(warp_sum(sum.x + sum.y));
+    const float inv_sum = inverse(lanes_sum<G>(shares_sum.x + shares_sum.y));
     float D[V];
     float2 dot = both(0.0f);
     if (a.dloss != nullptr) load_row<float, V, VECT>(a.slope + (int64_t)b * E, E, lane, 0.0f, D);
@@ -855,7 +879,7 @@ __global__ void __launch_bounds__(kThreads) router_bwd_kernel(
       dot = fma2(g, p[h], dot);
       D[2 * h] = g.x, D[2 * h + 1] = g.y;
     }
-    const float all = warp_sum(dot.x + dot.y);
+    const float all = lanes_sum<G>(dot.x + dot.y);
 #pragma unroll
     for (int h = 0; h < V / 2; ++h)
       d[h] = fma2(p[h], make_float2(D[2 * h] - all, D[2 * h + 1] - all), d[h]);
@@ -863,9 +887,9 @@ __global__ void __launch_bounds__(kThreads) router_bwd_kernel(
 #pragma unroll
   for (int h = 0; h < V / 2; ++h) {
     if (sig) d[h] = mul2(d[h], q[h]);
-    dx[2 * h] = d[h].x, dx[2 * h + 1] = d[h].y;
+    dx[2 * h] = none ? 0.0f : d[h].x, dx[2 * h + 1] = none ? 0.0f : d[h].y;
   }
-  store_row<T, V, VECT>(out, E, lane, dx);
+  if (on) store_row<T, V, VECT>(out, E, lane, dx);
 }
 
 // Rows of whole pieces for 16-byte accesses (load_row); V: experts of a lane.
@@ -959,19 +983,30 @@ cudaError_t fp8moe_launch_router(const RouterArgs& args, cudaStream_t s) {
 }
 
 cudaError_t fp8moe_launch_router_bwd(const RouterBwdArgs& a, cudaStream_t s) {
-  const int64_t grid = (a.T + kWarps - 1) / kWarps;
-  auto launch = [&](auto type) {
+  auto launch = [&](auto type, auto lanes, auto width) {
     using T = decltype(type);
+    constexpr int G = decltype(lanes)::value, V = decltype(width)::value;
+    const int64_t tokens = kWarps * (32 / G);    // of a CTA
+    const unsigned grid = (unsigned)((a.T + tokens - 1) / tokens);
+    const size_t smem = (size_t)tokens * G * V * sizeof(float);
+    // slope rows are f32: their pieces have to be whole, too
+    if (whole_pieces<T>(a.E, V) && whole_pieces<float>(a.E, V))
+      router_bwd_kernel<T, G, V, true><<<grid, kThreads, smem, s>>>(a);
+    else
+      router_bwd_kernel<T, G, V, false><<<grid, kThreads, smem, s>>>(a);
+    return cudaGetLastError();
+  };
+  auto of_type = [&](auto type) {
+    if (a.T >= kManyTokens && a.E <= 256 && a.k <= kGroup) {
+      const std::integral_constant<int, kGroup> lanes;
+      if (a.E <= 32) return launch(type, lanes, std::integral_constant<int, 4>());
+      if (a.E <= 64) return launch(type, lanes, std::integral_constant<int, 8>());
+      if (a.E <= 128) return launch(type, lanes, std::integral_constant<int, 16>());
+      return launch(type, lanes, std::integral_constant<int, 32>());
+    }
     return with_width(a.E, [&](auto width) {
-      constexpr int V = decltype(width)::value;
-      const size_t smem = (size_t)kWarps * 32 * V * sizeof(float);
-      // slope rows are f32: their pieces have to be whole, too
-      if (whole_pieces<T>(a.E, V) && whole_pieces<float>(a.E, V))
-        router_bwd_kernel<T, V, true><<<(unsigned)grid, kThreads, smem, s>>>(a);
-      else
-        router_bwd_kernel<T, V, false><<<(unsigned)grid, kThreads, smem, s>>>(a);
-      return cudaGetLastError();
+      return launch(type, std::integral_constant<int, 32>(), width);
     });
   };
-  return a.f32 ? launch(float()) : launch(__nv_bfloat16());
+  return a.f32 ? of_type(float()) : of_type(__nv_bfloat16());
 }

@@ -104,6 +104,12 @@ __device__ __forceinline__ float max_nan(float a, float b) {
   return r;
 }
 
+__device__ __forceinline__ float clamp_nan(float x, float limit) {
+  float r;
+  asm("min.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(max_nan(x, -limit)), "f"(limit));
+  return r;
+}
+
 // exp(x) for x <= 0 (and NaN), two at a time: by the exponential unit (within 2^-22 of itself) on x
 // times log2 e, with what the product's rounding and the constant's lose put back to first order.
 // Within 6 * 2^-24; 0 below 2^-126.
@@ -136,22 +142,34 @@ __device__ __forceinline__ void sigmoids(float2 x, float2& s, float2& q) {
   s = make_float2(x.x < 0.0f ? small.x : large.x, x.y < 0.0f ? small.y : large.y);
   q = make_float2(x.x < 0.0f ? large.x : small.x, x.y < 0.0f ? large.y : small.y);
 }
-__device__ __forceinline__ float sigmoid(float x) {
-  float2 s, q;
-  sigmoids(make_float2(x, x), s, q);
-  return s.x;
+// sigmoid(x) = 1 / (1 + exp(-x)) alone, in half of the instructions, as precise (the
+// approximate inverse is within 2^-23); 0 below -88, 1 from 17 on, the infinities' too.
+__device__ __forceinline__ float2 sigmoid(float2 x) {
+  const float hi = 1.4426950216293335f, lo = 1.9259629911266175e-8f, ln2 = 0.6931471805599453f;
+  // exp(88.5) has a zero inverse; an infinity would make a NaN of its own rounding
+  x = make_float2(clamp_nan(x.x, 88.5f), clamp_nan(x.y, 88.5f));
+  const float2 t = mul2(x, both(-hi));
+  const float2 rest = fma2(x, both(-lo), fma2(x, both(-hi), mul2(t, both(-1.0f))));
+  float2 e;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e.x) : "f"(t.x));
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e.y) : "f"(t.y));
+  const float2 d = add2(fma2(mul2(e, both(ln2)), rest, e), both(1.0f));
+  float2 s;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(s.x) : "f"(d.x));
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(s.y) : "f"(d.y));
+  return s;
 }
+__device__ __forceinline__ float sigmoid(float x) { return sigmoid(make_float2(x, x)).x; }
 
 // A score on the row's scale, n(x) = score(x) * exp(-top): top = the largest logit, or, with
 // sigmoid scores, the largest one below zero (0 if there is one above). The scores themselves may
 // all round to zero (sigmoid below -104); their ratios, which is what weights and shares are,
 // do not depend on the scale, and the largest n is at least 1/2. Experts at -inf have 0.
 __device__ __forceinline__ float2 scaled_scores(float2 x, float top, bool sig) {
-  const float2 y = make_float2(x.x - top, x.y - top);
+  const float2 y = add2(x, both(-top));
   if (!sig) return exp_neg(y);
-  float2 s, q;
-  sigmoids(x, s, q);
-  return top == 0.0f ? s : mul2(exp_neg(y), q);   // top < 0, so every x is, and s = exp(x) q
+  if (top == 0.0f) return sigmoid(x);
+  return mul2(exp_neg(y), sigmoid(make_float2(-x.x, -x.y)));   // sigmoid(x) = exp(x) sigmoid(-x)
 }
 __device__ __forceinline__ float scaled_score(float x, float top, bool sig) {
   return scaled_scores(make_float2(x, x), top, sig).x;

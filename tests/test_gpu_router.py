@@ -87,6 +87,12 @@ FORWARD = [
     (301, 511, 9, BF16, "softmax", False, True, 2, 0), (600, 512, 8, F32, "sigmoid", True, False, 0, 0),
     (99, 1000, 10, F32, "softmax", True, True, 4, 9), (64, 1023, 32, F32, "sigmoid", False, True, 1, 0),
     (5000, 1024, 2, BF16, "softmax", False, False, 3, 0),
+    # from 16384 tokens on, at most 256 experts, at most 8 chosen: eight lanes a token
+    (16384, 8, 8, F32, "softmax", False, True, 3, 0), (16385, 31, 3, F32, "sigmoid", True, True, 7, 5),
+    (17001, 61, 6, BF16, "sigmoid", False, False, 0, 0), (16900, 128, 8, BF16, "softmax", False, False, 5, 77),
+    (16399, 160, 5, F32, "softmax", True, False, 300, 0), (20011, 256, 8, F32, "sigmoid", True, True, 4, 11),
+    (16500, 255, 1, BF16, "softmax", False, True, 1, 0), (16390, 257, 8, F32, "sigmoid", False, True, 2, 0),
+    (16401, 64, 9, BF16, "softmax", False, True, 2, 0),
 ]
 
 
@@ -339,6 +345,51 @@ def test_gradient_against_differences(score, normalize):
             down[t, e] -= h
             d = (reference_total(up, *args) - reference_total(down, *args)) / (2 * h)
             assert abs(float(d) - float(got[t, e])) <= 2e-6
+
+
+def test_many_tokens_are_chosen_as_few_are():
+    """The rows on which a choice can go wrong, few and repeated in a large batch, which other
+    kernels take: the same experts, weights and gradients to a few roundings."""
+    E, k = 96, 6
+    g = torch.Generator().manual_seed(5)
+    rows = [torch.zeros(4, E), draw(60, E, 3, F32).round(), draw(60, E, 4, F32), draw(30, E, 5, BF16).float(),
+            (2.0 + torch.arange(E) * 2.0 ** -22)[torch.randperm(E, generator=g)][None],
+            (20.0 + torch.arange(E) * 0.01)[torch.randperm(E, generator=g)][None],
+            draw(20, E, 6, F32) - 200, draw(20, E, 7, F32) * 1e-5]
+    x = torch.cat(rows)
+    x[9, 2:] = -INF
+    x[10] = -INF
+    x[11, 3] = float("nan")
+    x[12, ::3] = -INF
+    T = x.shape[0]
+    many = -(-16400 // T)
+    for dtype in (F32, BF16):
+        few = x.to(dtype).cuda()
+        lots = few.repeat(many, 1)
+        for score in ("softmax", "sigmoid"):
+            for bias in (None, torch.zeros(E).cuda(), (torch.randn(E, generator=g) * 0.05).cuda()):
+                for normalize in (True, False):
+                    a = fb.router_fwd(few, k, score=score, bias=bias, normalize=normalize)
+                    b = fb.router_fwd(lots, k, score=score, bias=bias, normalize=normalize)
+                    sound = ~torch.isnan(x).any(1)
+                    ids = b[0].view(many, T, k)
+                    assert torch.equal(ids[:, sound], a[0][sound].expand(many, -1, -1))
+                    torch.testing.assert_close(b[1].view(many, T, k), a[1].expand(many, -1, -1),
+                                               rtol=4e-6, atol=1e-37, equal_nan=True)
+                    if bias is not None:
+                        continue
+                    dw = torch.randn(T, k, generator=g).cuda()
+                    slope = torch.rand(1, E, generator=g).cuda()
+                    dl = torch.ones(1, device="cuda")
+                    d = fb.router_bwd(dw, few, a[0], score=score, normalize=normalize, dloss=dl,
+                                      slope=slope)
+                    e = fb.router_bwd(dw.repeat(many, 1), lots, a[0].repeat(many, 1), score=score,
+                                      normalize=normalize, dloss=dl, slope=slope)
+                    # sums in another order: of 96 terms, relative to the row's largest
+                    top = d.float().abs().amax(1, keepdim=True)
+                    tol = 200 * U * top + torch.finfo(dtype).eps * d.float().abs()
+                    off = (e.view(many, T, E).float() - d.float()).abs()
+                    assert (off <= tol)[:, sound].all()
 
 
 def test_captured_and_on_streams():
