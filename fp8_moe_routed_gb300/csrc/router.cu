@@ -213,7 +213,7 @@ __device__ __forceinline__ void walk_chunk(const RouterArgs& a, Clear clear, Run
 }
 
 template <typename T, int V, bool VECT, bool GIVEN>
-__global__ void __launch_bounds__(kThreads) router_kernel(const __grid_constant__ RouterArgs a) {
+__global__ void __launch_bounds__(kThreads, V <= 16 ? 4 : 1) router_kernel(const __grid_constant__ RouterArgs a) {
   extern __shared__ float s_mem[];
   float* s_share = s_mem;                                           // [kWarps][32 V]
   int32_t* s_count = reinterpret_cast<int32_t*>(s_mem + kWarps * 32 * V);   // [32 V]
@@ -775,7 +775,7 @@ __device__ __forceinline__ float lanes_sum(float v) {
 }
 
 template <typename T, int G, int V, bool VECT>
-__global__ void __launch_bounds__(kThreads) router_bwd_kernel(
+__global__ void __launch_bounds__(kThreads, V <= 16 ? 4 : 1) router_bwd_kernel(
     const __grid_constant__ RouterBwdArgs a) {
   extern __shared__ float s_mem[];
   const int lane = threadIdx.x % G, warp = threadIdx.x / 32;
@@ -908,10 +908,12 @@ cudaError_t with_width(int E, F f) {
   return f(std::integral_constant<int, 32>());
 }
 
+bool by_groups(int64_t T, int E, int k) { return T >= kManyTokens && E <= 256 && k <= kGroup; }
+
 template <typename T, bool GIVEN>
 cudaError_t launch_router(const RouterArgs& a, cudaStream_t s) {
   const int64_t grid = (a.T + a.chunk - 1) / a.chunk;
-  if (a.T >= kManyTokens && a.E <= 256 && a.k <= kGroup) {
+  if (by_groups(a.T, a.E, a.k)) {
     auto launch = [&](auto width) {
       constexpr int V = decltype(width)::value;
       const size_t smem = (size_t)(kWarps + 1) * kGroup * V * sizeof(float);
@@ -944,17 +946,19 @@ using namespace fp8moe;
 
 FP8MOE_DEFINE_STATUS_TAKE(fp8moe_status_take_router)
 
-int fp8moe_balance_chunk(int64_t T) {
-  // two CTAs on an SM, in steps of what a CTA's warps take at once
-  const int64_t step = T < kManyTokens ? kWarps : kWarps * kGroups;
-  const int64_t c = (T / 304 + step - 1) / step * step;
-  return (int)(c < step ? step : c > 256 ? 256 : c);
+static int chunk_of(int64_t T, int ctas, int step, int most) {
+  const int64_t c = (T / ctas + step - 1) / step * step;
+  return (int)(c < step ? step : c > most ? most : c);
 }
+// The smallest there are: four CTAs on an SM, a token for a warp at a time.
+int fp8moe_balance_chunk(int64_t T) { return chunk_of(T, 608, kWarps, 128); }
+// Two CTAs on an SM, four tokens for a warp.
+static int group_chunk(int64_t T) { return chunk_of(T, 304, kWarps * kGroups, 256); }
 
 cudaError_t fp8moe_launch_router(const RouterArgs& args, cudaStream_t s) {
   RouterArgs a = args;
   const bool balance = a.part_share != nullptr;
-  a.chunk = balance || a.T >= kManyTokens ? fp8moe_balance_chunk(a.T) : kWarps;
+  a.chunk = by_groups(a.T, a.E, a.k) ? group_chunk(a.T) : balance ? fp8moe_balance_chunk(a.T) : kWarps;
   cudaError_t e = cudaSuccess;
   if (a.T > 0) {
     if (a.given != nullptr)
@@ -997,7 +1001,7 @@ cudaError_t fp8moe_launch_router_bwd(const RouterBwdArgs& a, cudaStream_t s) {
     return cudaGetLastError();
   };
   auto of_type = [&](auto type) {
-    if (a.T >= kManyTokens && a.E <= 256 && a.k <= kGroup) {
+    if (by_groups(a.T, a.E, a.k)) {
       const std::integral_constant<int, kGroup> lanes;
       if (a.E <= 32) return launch(type, lanes, std::integral_constant<int, 4>());
       if (a.E <= 64) return launch(type, lanes, std::integral_constant<int, 8>());

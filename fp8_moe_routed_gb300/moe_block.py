@@ -6,8 +6,11 @@
     out          = the weighted sum of each token's rows              combine_tokens
     r, h'        = residual sum with the norms after and before       norm_fwd
 
-`forward` and `backward` are the training step on 8-bit weights, `serve` the block on
-4-bit weights. Run as a module for a small demonstration on a GPU:
+`forward` and `backward` are the training pass on 8-bit weights, `serve` the block on
+4-bit weights. `choose` and `choose_backward` are the router in front of it with its balance
+loss (router_fwd, router_bwd), and `Trainer` holds the f32 weights and their moments and turns
+the gradients into the next weights, the experts' as 8-bit codes (adamw_step); `train_step` is
+all of them together. Run as a module for a small demonstration on a GPU:
 
     python -m fp8_moe_routed_gb300.moe_block
 """
@@ -48,6 +51,42 @@ def route(h: torch.Tensor, w_router: torch.Tensor, topk: int):
     return top.indices.to(torch.int32).contiguous(), torch.softmax(top.values, dim=1).contiguous()
 
 
+@dataclasses.dataclass
+class Router:
+    """Weights f32 [H, E] of the logits, an optional bias of the choice (f32 [E]), and the
+    factor of the balance loss (of each sequence) in the total."""
+    w: torch.Tensor
+    topk: int
+    score: str = "softmax"
+    bias: Optional[torch.Tensor] = None
+    weight_scale: float = 1.0
+    balance: float = 1e-3
+
+    def options(self) -> dict:
+        return dict(score=self.score, weight_scale=self.weight_scale)
+
+
+def choose(router: Router, h, seq_offsets=None):
+    """The router's choice for the normalised tokens h [T, H]: (ids, weights, saved), with the
+    balance loss of each sequence and the experts' counts in saved."""
+    logits = h.float() @ router.w
+    ids, weights, counts, loss, slope = fb.router_fwd(
+        logits, router.topk, bias=router.bias, balance=True, seq_offsets=seq_offsets,
+        **router.options())
+    saved: dict[str, Any] = dict(h=h, logits=logits, ids=ids, counts=counts, loss=loss, slope=slope,
+                                 seq_offsets=seq_offsets)
+    return ids, weights, saved
+
+
+def choose_backward(router: Router, saved: dict, dweights):
+    """Gradients for dweights (of the router's weights) and the balance loss's own: (dh, dw)."""
+    dloss = torch.full_like(saved["loss"], router.balance)
+    dlogits = fb.router_bwd(dweights, saved["logits"], saved["ids"], dloss=dloss,
+                            slope=saved["slope"], seq_offsets=saved["seq_offsets"],
+                            **router.options())
+    return dlogits @ router.w.t(), saved["h"].float().t() @ dlogits
+
+
 def forward(p: Params, x, h, ids, weights):
     """x: residual stream, h: its norm (both bf16 [T, H]). Returns (r, h_next, saved)."""
     num_experts = p.wi[0].shape[0]
@@ -77,6 +116,54 @@ def backward(p: Params, saved: dict, dr, dh_next):
     dh = fb.dispatch_tokens_bwd(drows, s["slot_row"])
     return dict(dx=dx, dh=dh, dweights=dweights, dwi=dwi, dwo=dwo, dw_post=dw_post, dw_pre=dw_pre,
                 dgate=dgate)
+
+
+class Trainer:
+    """The f32 weights behind a block and its router, with their moments in 32 or 8 bits. wi
+    [E, H, 2F] and wo [E, F, H] are f32; the block's codes and scales are what they become. The
+    experts and the router's weights decay, the norms and the gate do not."""
+
+    def __init__(self, p: Params, router: Router, wi: torch.Tensor, wo: torch.Tensor, bits: int = 32,
+                 weight_decay: float = 0.1, seed: int = 0):
+        if bits not in (8, 32):
+            raise ValueError(f"bits must be 8 or 32, got {bits}")
+        self.names = ["dwi", "dwo", "dw_router", "dw_post", "dw_pre"]
+        params = [wi, wo, router.w, p.w_post, p.w_pre]
+        if p.gate is not None:
+            self.names.append("dgate")
+            params.append(p.gate)
+        n = len(params)
+        dtype = torch.uint8 if bits == 8 else torch.float32
+        self.m = [torch.zeros(t.shape, dtype=dtype, device=t.device) for t in params]
+        self.v = [torch.zeros_like(t) for t in self.m]
+        scales = [[torch.zeros(fb.adamw_blocks(t.numel()), device=t.device) for t in params]
+                  for _ in range(2)] if bits == 8 else [None, None]
+        none = [None] * (n - 2)
+        self.plan = fb.AdamwPlan(params, self.m, self.v, m_scales=scales[0], v_scales=scales[1],
+                                 codes=[p.wi[0], p.wo[0]] + none,
+                                 code_scales=[p.wi[1], p.wo[1]] + none,
+                                 weight_decay=[weight_decay] * 3 + [0.0] * (n - 3))
+        self.scales, self.seed, self.steps = scales, seed, 0
+
+    def step(self, grads: dict, lr: float, grad_scale=None) -> None:
+        """One AdamW step for the gradients of backward and choose_backward."""
+        self.steps += 1
+        fb.adamw_step(self.plan, [grads[k] for k in self.names], step=self.steps, lr=lr,
+                      grad_scale=grad_scale, seed=self.seed)
+
+
+def train_step(p: Params, router: Router, trainer: Trainer, x, h, dr, dh_next, lr: float,
+               seq_offsets=None):
+    """The whole step for x, h and the gradients of its two results, dr and dh_next: forward,
+    backward and new weights. Returns (r, h_next, losses, grads); grads["dh"] has the router's
+    part, too."""
+    ids, weights, chosen = choose(router, h, seq_offsets)
+    r, h_next, saved = forward(p, x, h, ids, weights)
+    grads = backward(p, saved, dr, dh_next)
+    dh, grads["dw_router"] = choose_backward(router, chosen, grads["dweights"])
+    grads["dh"] = grads["dh"].float() + dh
+    trainer.step(grads, lr)
+    return r, h_next, chosen["loss"], grads
 
 
 def serve(p: Params, x, h, ids, weights):
@@ -113,7 +200,27 @@ def example(T: int = 1000, H: int = 1024, F: int = 512, E: int = 16, topk: int =
     return p8, p4, x, h, ids, weights
 
 
+def training_example(T: int = 1000, H: int = 1024, F: int = 512, E: int = 16, topk: int = 4,
+                     bits: int = 8, seed: int = 0):
+    """A block with a router and a trainer of their own: (p, router, trainer, x, h)."""
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    rand = lambda *shape: torch.randn(*shape, generator=g, device="cuda")
+    wi, wo = rand(E, H, 2 * F) * H ** -0.5, rand(E, F, H) * F ** -0.5
+    p = Params(fp8_weight(wi), fp8_weight(wo), w_post=1 + 0.1 * rand(H), w_pre=1 + 0.1 * rand(H),
+               gate=rand(H))
+    router = Router(rand(H, E) * H ** -0.5, topk, score="sigmoid", bias=0.01 * rand(E))
+    trainer = Trainer(p, router, wi, wo, bits=bits)
+    x = rand(T, H).to(torch.bfloat16)
+    _, h, _, _ = fb.norm_fwd(x, w_pre=torch.ones(H, device="cuda"))
+    return p, router, trainer, x, h
+
+
 def main() -> None:
+    p, router, trainer, x, h = training_example()
+    for _ in range(2):
+        r, h_next, losses, _ = train_step(p, router, trainer, x, h, 1e-3 * torch.randn_like(x),
+                                          1e-3 * torch.randn_like(x), lr=1e-3)
+    print(f"{trainer.steps} training steps, moments in 8 bits: balance loss {float(losses[0]):.4f}")
     p8, p4, x, h, ids, weights = example()
     r, h_next, saved = forward(p8, x, h, ids, weights)
     grads = backward(p8, saved, torch.randn_like(r), torch.randn_like(r))

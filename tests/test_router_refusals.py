@@ -63,8 +63,7 @@ def test_balance_workspace():
     """A part for each chunk of tokens and each sequence: shares and counts of every expert, and
     a number of tokens."""
     for T, B, E in ((0, 1, 8), (1, 1, 1), (4096, 5, 256), (65536, 1, 128)):
-        step = 8 if T < 16384 else 32
-        chunk = min(256, max(step, -(-(T // 304) // step) * step))
+        chunk = min(128, max(8, -(-(T // 608) // 8) * 8))
         slots = -(-T // chunk) + B
         up = lambda n: -(-n // 256) * 256  # noqa: E731
         assert fb.workspace_size(fb.OP_BALANCE, T, 0, B, E) == 2 * up(4 * slots * E) + up(4 * slots)
