@@ -388,7 +388,8 @@ __device__ __forceinline__ void step_quad(const Rates& r, uint64_t place, uint32
   }
   const float low = fminf(fminf(v[0].x, v[0].y), fminf(v[1].x, v[1].y));
   const float high = fmaxf(fmaxf(v[0].x, v[0].y), fmaxf(v[1].x, v[1].y));
-  if (low >= 0x1p-126f && high <= 0x1p126f) {    // then the divisors are in [2^-63, 2^90]
+  // (the remainder of a root is exact from 2^-101 on; the divisors are in [2^-50, 2^90])
+  if (low >= 0x1p-100f && high <= 0x1p126f) {
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
       root[h] = sqrt2(v[h]);

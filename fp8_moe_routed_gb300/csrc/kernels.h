@@ -211,6 +211,8 @@ struct RouterArgs {
 // Tokens of a CTA, whose balance sums are one part for each sequence among them.
 int fp8moe_balance_chunk(int64_t T);
 cudaError_t fp8moe_launch_router(const RouterArgs& a, cudaStream_t s);
+// Many tokens (router_group.cu): without the join of the balance sums.
+cudaError_t fp8moe_launch_router_groups(const RouterArgs& a, cudaStream_t s);
 
 struct RouterBwdArgs {
   const void* logits;
@@ -226,6 +228,8 @@ struct RouterBwdArgs {
 };
 cudaError_t fp8moe_launch_router_bwd(const RouterBwdArgs& a, cudaStream_t s);
 cudaError_t fp8moe_status_take_router(uint32_t** word);
+cudaError_t fp8moe_status_take_router_group(uint32_t** word);
+cudaError_t fp8moe_status_take_router_bwd(uint32_t** word);
 
 // AdamW (adamw.cu): a tensor in a launch's table.
 struct AdamwEntry {

@@ -1,7 +1,9 @@
 // router.cuh -- what the router's choice and its gradient share: a token's logits in a
 // warp's registers, and the experts' scores on a scale on which they cannot all vanish.
 #pragma once
+#include <cmath>
 #include <cstdint>
+#include <type_traits>
 #include <cuda_runtime.h>
 #include <cuda_bf16.h>
 
@@ -11,6 +13,17 @@
 namespace fp8moe {
 
 constexpr uint32_t kAllLanes = 0xffffffffu;
+constexpr int kWarps = 8;
+constexpr int kThreads = 32 * kWarps;
+
+// Many tokens and at most 256 experts, of which 8 are chosen: eight lanes take a token, so that an
+// instruction works for four. (65536 tokens, 128 experts, bf16: 77 us by a warp for a token, 33 by
+// eight lanes; 4096 tokens of 256 experts, whose 1024 warps do not fill the GPU, 17 and 37.)
+constexpr int64_t kManyTokens = 16384;
+constexpr int kGroup = 8, kGroups = 4;
+inline bool by_groups(int64_t T, int E, int k) {
+  return T >= kManyTokens && E <= 256 && k <= kGroup;
+}
 
 __device__ __forceinline__ float load_f32(const float* p) { return *p; }
 __device__ __forceinline__ float load_f32(const __nv_bfloat16* p) { return __bfloat162float(*p); }
@@ -176,6 +189,59 @@ __device__ __forceinline__ float scaled_score(float x, float top, bool sig) {
 }
 __device__ __forceinline__ float scale_top(float largest, bool sig) {
   return sig && largest > 0.0f ? 0.0f : largest;
+}
+
+// Of a token's eight lanes.
+template <typename F>
+__device__ __forceinline__ F group_max(F v) {
+#pragma unroll
+  for (int o = 1; o < kGroup; o *= 2) {
+    const F w = __shfl_xor_sync(kAllLanes, v, o);
+    if constexpr (std::is_same<F, float>::value) v = max_nan(v, w);
+    else v = max(v, w);
+  }
+  return v;
+}
+__device__ __forceinline__ float group_sum(float v) {
+#pragma unroll
+  for (int o = 1; o < kGroup; o *= 2) v += __shfl_xor_sync(kAllLanes, v, o);
+  return v;
+}
+
+// Of the G lanes that have a token.
+template <int G>
+__device__ __forceinline__ float lanes_max(float v) {
+  if constexpr (G == 32) return warp_max(v);
+  else return group_max(v);
+}
+template <int G>
+__device__ __forceinline__ float lanes_sum(float v) {
+  if constexpr (G == 32) return warp_sum(v);
+  else return group_sum(v);
+}
+
+// Rows of whole pieces for 16-byte accesses (load_row); V: experts of a lane.
+template <typename T>
+bool whole_pieces(int E, int V) {
+  const int values = (V * (int)sizeof(T) < 16 ? V * (int)sizeof(T) : 16) / (int)sizeof(T);
+  return E % values == 0;
+}
+template <int N> using Int = std::integral_constant<int, N>;
+// f(experts of a lane), where a warp or where eight lanes have a token.
+template <typename F>
+cudaError_t with_width(int E, F f) {
+  if (E <= 64) return f(Int<2>());
+  if (E <= 128) return f(Int<4>());
+  if (E <= 256) return f(Int<8>());
+  if (E <= 512) return f(Int<16>());
+  return f(Int<32>());
+}
+template <typename F>
+cudaError_t with_group_width(int E, F f) {
+  if (E <= 32) return f(Int<4>());
+  if (E <= 64) return f(Int<8>());
+  if (E <= 128) return f(Int<16>());
+  return f(Int<32>());
 }
 
 // The sequence that token t belongs to, with offsets[b] <= t < offsets[b + 1] (the first b

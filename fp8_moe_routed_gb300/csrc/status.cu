@@ -40,6 +40,7 @@ cudaError_t fp8moe_collect_status(uint32_t* flags, cudaStream_t s) {
       fp8moe_status_take_dlhs, fp8moe_status_take_dlhs_pair, fp8moe_status_take_tgmm,
       fp8moe_status_take_selftest, fp8moe_status_take_route, fp8moe_status_take_norm,
       fp8moe_status_take_mxfp4, fp8moe_status_take_gmm_mxfp4, fp8moe_status_take_router,
+      fp8moe_status_take_router_group, fp8moe_status_take_router_bwd,
       fp8moe_status_take_adamw};
   constexpr int n = sizeof(units) / sizeof(units[0]);
   static_assert(n <= kMaxWords, "a lane for every word");

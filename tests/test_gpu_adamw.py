@@ -274,7 +274,7 @@ def test_infinite_and_nan_gradients(bits):
 
 def test_extreme_values():
     """Moments below the scales' range are zero; huge and tiny gradients stay in line with f32."""
-    for scale in (1e-38, 1e-30, 1e-20, 1e15, 1e18):
+    for scale in (1e-38, 1e-30, 1e-20, 1e-18, 1e-17, 1e-16, 1e-15, 1e-14, 1e-13, 1e9, 1e15, 1e18):
         for bits in (32, 8):
             t = Tensor(2000, bits, zero=True)
             t.g = numbers(2000, 5, 1) * F(scale)
