@@ -12,6 +12,7 @@ from __future__ import annotations
 
 import array
 import ctypes
+import functools
 import os
 import threading
 from typing import Optional
@@ -184,6 +185,7 @@ def _req(t: torch.Tensor, dtype, name: str, ndim: int):
         raise ValueError(f"{name} must be contiguous")
 
 
+@functools.lru_cache(maxsize=1024)
 def workspace_size(op: int, M: int, K: int, N: int, E: int) -> int:
     return int(load().fp8moe_workspace_size(op, M, K, N, E))
 

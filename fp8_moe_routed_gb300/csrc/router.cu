@@ -372,10 +372,11 @@ static int group_chunk(int64_t T) { return chunk_of(T, 304, kWarps * kGroups, 25
 cudaError_t fp8moe_launch_router(const RouterArgs& args, cudaStream_t s) {
   RouterArgs a = args;
   const bool balance = a.part_share != nullptr;
-  a.chunk = by_groups(a.T, a.E, a.k) ? group_chunk(a.T) : balance ? fp8moe_balance_chunk(a.T) : kWarps;
+  const bool groups = by_groups(a.T, a.E, a.k, a.bias != nullptr);
+  a.chunk = groups ? group_chunk(a.T) : balance ? fp8moe_balance_chunk(a.T) : kWarps;
   cudaError_t e = cudaSuccess;
   if (a.T > 0) {
-    if (by_groups(a.T, a.E, a.k))
+    if (groups)
       e = fp8moe_launch_router_groups(a, s);
     else if (a.given != nullptr)
       e = a.f32 ? launch_router<float, true>(a, s) : launch_router<__nv_bfloat16, true>(a, s);

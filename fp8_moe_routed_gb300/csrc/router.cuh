@@ -16,13 +16,15 @@ constexpr uint32_t kAllLanes = 0xffffffffu;
 constexpr int kWarps = 8;
 constexpr int kThreads = 32 * kWarps;
 
-// Many tokens and at most 256 experts, of which 8 are chosen: eight lanes take a token, so that an
-// instruction works for four. (65536 tokens, 128 experts, bf16: 77 us by a warp for a token, 33 by
-// eight lanes; 4096 tokens of 256 experts, whose 1024 warps do not fill the GPU, 17 and 37.)
-constexpr int64_t kManyTokens = 16384;
+// Many tokens, at most 128 experts, at most 8 chosen, and no bias: eight lanes take a token, so that
+// an instruction works for four. A choice (65536 tokens, 128 experts, bf16, with the balance loss)
+// takes 31 us then and 77 by a warp for a token; of 4096 tokens 9.7 and 11.1, of 2048 8.8 both. With
+// a bias more tokens have to be settled one by one (f32, 65536: 66 and 63 us), and 256 experts
+// take so many registers that an SM has one CTA (f32, 32768: 66 and 40; the gradient 57 and 37).
+constexpr int64_t kManyTokens = 4096;
 constexpr int kGroup = 8, kGroups = 4;
-inline bool by_groups(int64_t T, int E, int k) {
-  return T >= kManyTokens && E <= 256 && k <= kGroup;
+inline bool by_groups(int64_t T, int E, int k, bool bias) {
+  return T >= kManyTokens && E <= 128 && k <= kGroup && !bias;
 }
 
 __device__ __forceinline__ float load_f32(const float* p) { return *p; }
@@ -240,8 +242,7 @@ template <typename F>
 cudaError_t with_group_width(int E, F f) {
   if (E <= 32) return f(Int<4>());
   if (E <= 64) return f(Int<8>());
-  if (E <= 128) return f(Int<16>());
-  return f(Int<32>());
+  return f(Int<16>());
 }
 
 // The sequence that token t belongs to, with offsets[b] <= t < offsets[b + 1] (the first b

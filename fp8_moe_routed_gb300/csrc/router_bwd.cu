@@ -159,7 +159,7 @@ cudaError_t fp8moe_launch_router_bwd(const RouterBwdArgs& a, cudaStream_t s) {
     return cudaGetLastError();
   };
   auto of_type = [&](auto type) {
-    if (by_groups(a.T, a.E, a.k))
+    if (by_groups(a.T, a.E, a.k, false))
       return with_group_width(a.E, [&](auto width) { return launch(type, Int<kGroup>(), width); });
     return with_width(a.E, [&](auto width) { return launch(type, Int<32>(), width); });
   };

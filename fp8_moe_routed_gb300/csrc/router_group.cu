@@ -1,7 +1,7 @@
-// router_group.cu -- the router's choice and the balance sums for many tokens (router.cuh): eight
-// lanes take a token, lane l of a group holds experts [l V, l V + V). What is as in router.cu is not
-// explained again; a token whose border is not settled by the upper 22 bits (or, with a bias, by
-// f32) is chosen by the whole warp in choose_exactly.
+// router_group.cu -- the router's choice without a bias, and the balance sums, for many tokens
+// (router.cuh): eight lanes take a token, lane l of a group holds experts [l V, l V + V). What is as
+// in router.cu is not explained again; a token whose border is not settled by the keys' upper 22 bits
+// is chosen by the whole warp in choose_exactly.
 #include <cmath>
 #include <cstdint>
 #include <cuda_runtime.h>
@@ -30,7 +30,7 @@ __global__ void __launch_bounds__(kThreads) router_group_kernel(
   const int l = lane & (kGroup - 1), g = lane / kGroup;
   const uint32_t group_lanes = 0xffu << (g * kGroup);
   const int E = a.E, k = a.k;
-  const bool sig = a.sig, has_bias = !GIVEN && a.bias != nullptr;
+  const bool sig = a.sig;
   const T* logits = static_cast<const T*>(a.logits);
   const bool balance = a.part_share != nullptr;
   uint16_t* list = reinterpret_cast<uint16_t*>(s_mem) + warp * 2 * W;
@@ -73,27 +73,13 @@ __global__ void __launch_bounds__(kThreads) router_group_kernel(
     if constexpr (GIVEN) {
       scores(row_max());
     } else {
-      float largest = 0.0f;
-      if (has_bias) {
-        largest = row_max();
-        if (!sig || balance) scores(largest);
-      }
       uint32_t key[V];
 #pragma unroll
-      for (int j = 0; j < V; ++j) {
-        const int e = l * V + j;
-        float c = x[j];
-        if (has_bias && c != -INFINITY) {
-          const float b = e < E ? a.bias[e] : 0.0f;
-          if (!sig) c = __fadd_rn(__fmul_rn(n[j], inv_sum), b);
-          else c = __fadd_rn(balance && top == 0.0f ? n[j] : sigmoid(c), b);
-        }
-        key[j] = choice_key(c, e);
-      }
+      for (int j = 0; j < V; ++j) key[j] = choice_key(x[j], l * V + j);
       sort_keys(key);
       // a lane's first nine are all that eight choices and the next one can come from
       constexpr int kDepth = V < kGroup + 1 ? V : kGroup + 1;
-      uint32_t mine = 0, m = 0, top_key = 0;
+      uint32_t mine = 0, m = 0;
 #pragma unroll 1
       for (int r = 0; r < k; ++r) {
         m = group_max(key[0]);
@@ -102,23 +88,17 @@ __global__ void __launch_bounds__(kThreads) router_group_kernel(
         for (int j = 0; j + 1 < kDepth; ++j) key[j] = here ? key[j + 1] : key[j];
         key[kDepth - 1] = here ? 0u : key[kDepth - 1];
         if (l == r) mine = m;
-        if (r == 0) top_key = m;
       }
       const uint32_t next_key = group_max(key[0]);
-      const float slack = has_bias && m >= kNone ? choice_slack(top_key, m, sig, inv_sum) : 0.0f;
-      const uint32_t floor = (has_bias ? order_key(key_value(m) - slack) : m) & ~1023u;
       // (the upper 22 bits are all that a bf16 logit has)
-      bool hard = (has_bias || sizeof(T) == 4) && on && m >= kNone && next_key >= kNone &&
-                  next_key >= floor;
+      const bool hard = sizeof(T) == 4 && on && m >= kNone && next_key >= (m & ~1023u);
 
       if (mine >= kNone) id = 1023 - (int)(mine & 1023u);
       float xc = id >= 0 ? load_f32(row + id) : -INFINITY;
-      const float b = has_bias && id >= 0 ? a.bias[id] : 0.0f;
-      float c = id >= 0 ? choice_value(xc, b, has_bias, sig, top, inv_sum) : -INFINITY;
-      float next = __shfl_down_sync(kAllLanes, c, 1);
-      if (__any_sync(kAllLanes, l + 1 < k && c < next)) {
+      const float next = __shfl_down_sync(kAllLanes, xc, 1);
+      if (__any_sync(kAllLanes, l + 1 < k && xc < next)) {
         // by the whole values; a NaN in place of the largest, those without an expert at the end
-        const float value = c != c ? INFINITY : c;
+        const float value = xc != xc ? INFINITY : xc;
         const int order = id >= 0 ? id : 2048 + l;
         int rank = 0;
 #pragma unroll
@@ -131,40 +111,26 @@ __global__ void __launch_bounds__(kThreads) router_group_kernel(
 #pragma unroll
         for (int o = 0; o < kGroup; ++o)
           if (__shfl_xor_sync(kAllLanes, rank, o) == l) from = lane ^ o;
-        c = __shfl_sync(kAllLanes, c, from);
         xc = __shfl_sync(kAllLanes, xc, from);
         id = __shfl_sync(kAllLanes, id, from);
-        next = __shfl_down_sync(kAllLanes, c, 1);
       }
-      if (has_bias) {
-        const float bc = id >= 0 ? a.bias[id] : 0.0f;
-        const float next_x = __shfl_down_sync(kAllLanes, xc, 1);
-        const float next_b = __shfl_down_sync(kAllLanes, bc, 1);
-        const int next_id = __shfl_down_sync(kAllLanes, id, 1);
-        hard |= group_any(on && l + 1 < k && next_id >= 0 && !(c - next > slack) &&
-                          !(xc == next_x && bc == next_b));
-      }
-      const float cut = key_value(m) - slack;
+      const float cut = key_value(m);
       for (uint32_t left = __ballot_sync(kAllLanes, hard && l == 0); left != 0u; left &= left - 1u) {
         const int who = __ffs(left) - 1;
         const int64_t th = __shfl_sync(kAllLanes, t, who);
-        const int exact = choose_exactly(
-            logits + th * E, a.bias, E, k, sig, __shfl_sync(kAllLanes, top, who),
-            __shfl_sync(kAllLanes, inv_sum, who), __shfl_sync(kAllLanes, cut, who), list);
+        const int exact = choose_exactly(logits + th * E, static_cast<const float*>(nullptr), E, k, sig,
+                                         0.0f, 0.0f, __shfl_sync(kAllLanes, cut, who), list);
         const int found = __shfl_sync(kAllLanes, exact, l);
         if (g == who / kGroup) id = l < k ? found : -1;
         __syncwarp();
       }
       if (__any_sync(kAllLanes, hard)) xc = id >= 0 ? load_f32(row + id) : -INFINITY;
 
-      if (!has_bias) {
-        largest = __shfl_sync(kAllLanes, xc, g * kGroup);
-        if (balance || (!sig && !a.normalize)) scores(largest);
-      }
+      const float largest = __shfl_sync(kAllLanes, xc, g * kGroup);
+      if (balance || (!sig && !a.normalize)) scores(largest);
       float w = 0.0f;
       if (a.normalize) {
-        const float most = has_bias ? group_max(xc) : largest;
-        const float nc = id >= 0 ? scaled_score(xc, scale_top(most, sig), sig) : 0.0f;
+        const float nc = id >= 0 ? scaled_score(xc, scale_top(largest, sig), sig) : 0.0f;
         w = nc / group_sum(nc);
       } else if (id >= 0) {
         w = sig ? sigmoid(xc) : exp_neg(xc - top) * inv_sum;

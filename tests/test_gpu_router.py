@@ -87,12 +87,13 @@ FORWARD = [
     (301, 511, 9, BF16, "softmax", False, True, 2, 0), (600, 512, 8, F32, "sigmoid", True, False, 0, 0),
     (99, 1000, 10, F32, "softmax", True, True, 4, 9), (64, 1023, 32, F32, "sigmoid", False, True, 1, 0),
     (5000, 1024, 2, BF16, "softmax", False, False, 3, 0),
-    # from 16384 tokens on, at most 256 experts, at most 8 chosen: eight lanes a token
+    # from 16384 tokens on, at most 128 experts, at most 8 chosen: eight lanes a token
     (16384, 8, 8, F32, "softmax", False, True, 3, 0), (16385, 31, 3, F32, "sigmoid", True, True, 7, 5),
     (17001, 61, 6, BF16, "sigmoid", False, False, 0, 0), (16900, 128, 8, BF16, "softmax", False, False, 5, 77),
     (16399, 160, 5, F32, "softmax", True, False, 300, 0), (20011, 256, 8, F32, "sigmoid", True, True, 4, 11),
     (16500, 255, 1, BF16, "softmax", False, True, 1, 0), (16390, 257, 8, F32, "sigmoid", False, True, 2, 0),
-    (16401, 64, 9, BF16, "softmax", False, True, 2, 0),
+    (16401, 64, 9, BF16, "softmax", False, True, 2, 0), (16390, 100, 8, F32, "sigmoid", True, True, 3, 9),
+    (16500, 127, 7, F32, "softmax", True, True, 2, 0), (16385, 128, 8, F32, "sigmoid", False, False, 40, 0),
 ]
 
 
