@@ -466,7 +466,7 @@ int check_adamw(const fp8moe_adamw_tensor& d) {
       (!eight && (!aligned4(d.m) || !aligned4(d.v))))
     return FP8MOE_EALIGN;
   if (d.codes) {
-    if (d.K < 1 || d.N < 1 || d.K > (1 << 22) || d.N > (1 << 22)) return FP8MOE_EINVAL;
+    if (d.K < 1 || d.N < 1 || d.K > (1 << 21) || d.N > (1 << 21)) return FP8MOE_EINVAL;
     if (d.n % (d.K * d.N) != 0 || d.n / (d.K * d.N) > 1024) return FP8MOE_EINVAL;
     if (d.K % 16 != 0 || d.N % 16 != 0) return FP8MOE_EALIGN;
   }
@@ -477,7 +477,7 @@ int check_adamw(const fp8moe_adamw_tensor& d) {
 // tensor's begin on 256 bytes (columns are copied by 16).
 int64_t adamw_columns(const fp8moe_adamw_tensor& d) { return d.n / d.K; }
 int64_t adamw_words(const fp8moe_adamw_tensor& d) {
-  if (d.n <= 0 || !d.codes || d.K < 1 || d.N < 1) return 0;
+  if (d.n <= 0 || !d.codes || check_adamw(d) != FP8MOE_OK) return 0;
   return (adamw_columns(d) + fp8moe_adamw_slab_counters(d.n, d.K, d.N) + 63) / 64 * 64;
 }
 

@@ -498,8 +498,9 @@ int fp8moe_router_bwd(const float* dweights, const void* logits, const int32_t* 
  * into the next step's weights. For each value, g = grad_scale * g (where one is given):
  *   m = beta1 m + (1 - beta1) g,   v = beta2 v + (1 - beta2) g^2
  *   p = p (1 - lr weight_decay) - lr / (1 - beta1^t) * m / (sqrt(v) / sqrt(1 - beta2^t) + eps)
- * p is f32 (master weights), g bf16 or f32. Every operation is rounded to f32 by itself: a step
- * has one right result, which does not depend on what else is in the call.
+ * p is f32 (master weights), g bf16 or f32. Every operation is rounded to f32 by itself (root and
+ * quotient to the nearest, but for about one in 2^22 that lies next to the middle of two values): a
+ * step has one result, which does not depend on what else is in the call.
  *
  * Moments are f32 (state_bits = 32), or (8) e4m3 codes of m and of sqrt(v) with an f32 scale for
  * each 128 consecutive values (the last block may be shorter): scale = largest magnitude / 448,
@@ -510,9 +511,9 @@ int fp8moe_router_bwd(const float* dweights, const void* logits, const int32_t* 
  * A NaN or an infinity in a block's moments makes the block NaN or infinite in the next step.
  *
  * copy (may be NULL): bf16 of the new p. codes with code_scale (may be NULL): p is expert weights
- * [E, K, N], n = E K N, K and N multiples of 16, and the new weights come as the forward takes
- * them, code_scale f32 [E, N] = max(max_k |p|, 1e-12) / 448, codes u8 [E, K, N] = e4m3(p /
- * code_scale), round to nearest even. */
+ * [E, K, N], n = E K N, E at most 1024, K and N multiples of 16 up to 2^21, and the new weights
+ * come as the forward takes them, code_scale f32 [E, N] = max(max_k |p|, 1e-12) / 448, codes u8
+ * [E, K, N] = e4m3(p / code_scale), round to nearest even. */
 typedef struct fp8moe_adamw_tensor {
   float* p;
   const void* g;
@@ -531,12 +532,12 @@ typedef struct fp8moe_adamw_tensor {
 } fp8moe_adamw_tensor;
 
 /* `tensors` is a HOST array of `count` entries, read during the call (its pointers are device
- * pointers); no two entries may overlap. Values need the alignment of their type only; tensors
- * whose pointers are all 16-byte aligned take wider accesses. t: `step` >= 1, or *step_dev (int64
- * on the device, NULL: `step`); the rate: `lr`, or *lr_dev (f32 on the device, NULL: `lr`): a
- * captured step follows what they hold when it is replayed. grad_scale: f32 on the device or
- * NULL. 0 <= beta < 1, eps >= 0. Workspace: fp8moe_adamw_workspace_size (256-byte aligned), with
- * on_device = 1 if step_dev or lr_dev is given. */
+ * pointers); no two entries may overlap. Values need the alignment of their type only. t: `step`
+ * >= 1, or *step_dev (int64 on the device, NULL: `step`); the rate: `lr`, or *lr_dev (f32 on the
+ * device, NULL: `lr`): a captured step follows what they hold when it is replayed. grad_scale: f32
+ * on the device or NULL. 0 <= beta < 1, eps >= 0 (with 0 a value that never had a gradient becomes
+ * NaN). Workspace: fp8moe_adamw_workspace_size (256-byte aligned), with on_device = 1 if step_dev or
+ * lr_dev is given; calls that overlap on the GPU need one each. */
 size_t fp8moe_adamw_workspace_size(const fp8moe_adamw_tensor* tensors, int32_t count,
                                    int32_t on_device);
 int fp8moe_adamw_step(const fp8moe_adamw_tensor* tensors, int32_t count, int64_t step,

@@ -105,7 +105,8 @@ def test_adamw_tensors():
                 dict(g_type=2), dict(state_bits=16), dict(state_bits=8), dict(m_scale=16),
                 dict(state_bits=8, m_scale=16), dict(weight_decay=float("nan")), dict(codes=16),
                 dict(code_scale=16), {**codes, "n": 2 * 32 * 48 + 1}, {**codes, "K": 0},
-                {**codes, "n": 2000 * 32 * 48}):
+                {**codes, "n": 2000 * 32 * 48}, {**codes, "n": 2 ** 21 * 64, "K": 2 ** 22, "N": 32},
+                {**codes, "K": 2 ** 40, "N": 2 ** 40}):
         assert step(tensor(), tensor(**bad)) == EINVAL, bad
     for bad in (dict(p=2), dict(g=2), dict(m=2), dict(v=2), dict(copy=1),
                 dict(g=1, g_type=0), dict(state_bits=8, m_scale=2, v_scale=16),
@@ -124,6 +125,9 @@ def test_adamw_workspace():
     codes = dict(codes=16, code_scale=16, n=2 * 32 * 48, K=32, N=48)
     assert size(tensor(**codes)) == 256 + 512
     assert size(tensor(**codes), tensor(**codes), on_device=1) == 256 + 1024
+    # what the step refuses needs none
+    assert size(tensor(**{**codes, "K": 2 ** 32, "N": 2 ** 32})) == 0
+    assert size(tensor(**{**codes, "n": -5})) == 0 and size(tensor(**{**codes, "K": 0})) == 0
 
 
 def test_python_side_refuses_what_is_no_cuda_tensor():
