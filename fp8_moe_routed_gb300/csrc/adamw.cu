@@ -933,13 +933,12 @@ __global__ void __launch_bounds__(kSlabThreads, kSlabPer) adamw_slab_kernel(
         if (edge & 1) most[0] = most[1] = most[2] = most[3] = 0.0f;
 #pragma unroll
         for (uint32_t i = 0; i < kRows / kWarps; ++i) {
-          const uint32_t row = i * kWarps + warp;
-          if (row >= rows) break;
+          const uint32_t row = i * kWarps + warp;  // past the last: zeros, worked on for nothing
           const int64_t first = base + (int64_t)row * N;
           Quad q;
           take_quad<BITS, true>(stage, row, a.d.g_bf16, none, q);
           step_quad<BITS>(rates, first + lane * 4, 1, q);
-          if (in) {
+          if (in && row < rows) {
             store_quad<BITS, true>(a.d, first, 128, q);
 #pragma unroll
             for (int j = 0; j < 4; ++j) most[j] = max_abs(most[j], q.p[j], 0.0f);

@@ -60,14 +60,3 @@ def test_no_norm_variant_is_built_that_no_row_reaches():
     with open(report) as f:
         built = set(re.findall(r"norm_(?:fwd|bwd)_kernelI(\w+?)Li(\d+)E", f.read()))
     assert built == {("13__nv_bfloat16", "512"), ("13__nv_bfloat16", "1024"), ("f", "512")}
-
-
-@pytest.mark.parametrize("name", ["router.cu", "router.cuh", "router_choice.cuh", "router_group.cu",
-                                  "router_bwd.cu", "adamw.cu"])
-def test_no_lane_skips_what_its_warp_does_together(name):
-    """A vote, a shuffle or a reduction of all lanes waits for all of them: none stands behind
-    && or ||, whose left side may differ between the lanes."""
-    text = code(os.path.join(CSRC, name))
-    together = r"(?:__any_sync|__all_sync|__ballot_sync|__shfl\w*|__reduce\w*|__match\w*|" \
-               r"group_any|group_max|group_sum|warp_max|warp_sum|first_sum)"
-    assert not re.findall(r"(?:&&|\|\|)\s*\(?\s*!?\s*%s\s*[(<]" % together, text)
