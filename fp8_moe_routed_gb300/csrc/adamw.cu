@@ -931,17 +931,21 @@ __global__ void __launch_bounds__(kSlabThreads, kSlabPer) adamw_slab_kernel(
       const uint32_t none[4] = {0, 0, 0, 0};
       if (kind == kTile) {
         if (edge & 1) most[0] = most[1] = most[2] = most[3] = 0.0f;
+        constexpr int kEach = kRows / kWarps;      // rows past the last: zeros, worked on for nothing
+        Quad q[kEach];
 #pragma unroll
-        for (uint32_t i = 0; i < kRows / kWarps; ++i) {
-          const uint32_t row = i * kWarps + warp;  // past the last: zeros, worked on for nothing
-          const int64_t first = base + (int64_t)row * N;
-          Quad q;
-          take_quad<BITS, true>(stage, row, a.d.g_bf16, none, q);
-          step_quad<BITS>(rates, first + lane * 4, 1, q);
+        for (int i = 0; i < kEach; ++i)
+          take_quad<BITS, true>(stage, i * kWarps + warp, a.d.g_bf16, none, q[i]);
+#pragma unroll
+        for (int i = 0; i < kEach; ++i)
+          step_quad<BITS>(rates, base + (int64_t)(i * kWarps + warp) * N + lane * 4, 1, q[i]);
+#pragma unroll
+        for (int i = 0; i < kEach; ++i) {
+          const uint32_t row = i * kWarps + warp;
           if (in && row < rows) {
-            store_quad<BITS, true>(a.d, first, 128, q);
+            store_quad<BITS, true>(a.d, base + (int64_t)row * N, 128, q[i]);
 #pragma unroll
-            for (int j = 0; j < 4; ++j) most[j] = max_abs(most[j], q.p[j], 0.0f);
+            for (int j = 0; j < 4; ++j) most[j] = max_abs(most[j], q[i].p[j], 0.0f);
           }
         }
       } else {
