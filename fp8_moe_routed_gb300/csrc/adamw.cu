@@ -10,6 +10,7 @@
 // proportion to what is lost: rounded to nearest, a moment whose change in a step is below half
 // a code's spacing (6 %; b2 = 0.999 changes v by 0.1 %) would never move.
 #include <cstdint>
+#include <type_traits>
 #include <cuda_runtime.h>
 #include <cuda_bf16.h>
 
@@ -499,7 +500,6 @@ template <int BITS>
 __device__ __forceinline__ void linear_stage(const AdamwEntry& d, const Rates& r, const Desc& a,
                                              const uint8_t* stage) {
   const uint32_t lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const uint32_t none[4] = {0, 0, 0, 0};
   uint32_t shift[4] = {0, 0, 0, 0};
   if (a.kind == kNarrow) {
     auto low = [](const void* p, int64_t bytes) {
@@ -508,32 +508,27 @@ __device__ __forceinline__ void linear_stage(const AdamwEntry& d, const Rates& r
     shift[0] = low(d.p, a.base * 4), shift[1] = low(d.g, a.base * (d.g_bf16 ? 2 : 4));
     shift[2] = low(d.m, a.base * (BITS / 8)), shift[3] = low(d.v, a.base * (BITS / 8));
   }
-  if (a.kind == kWide) {
+  auto whole = [&](auto is_wide) {
+    constexpr bool kIsWide = decltype(is_wide)::value;
 #pragma unroll
     for (uint32_t n = 0; n < kBlocks / kWarps; ++n) {
       const uint32_t block = n * kWarps + warp;
       const int64_t i = a.base + block * 128;
       Quad q;
-      take_quad<BITS, true>(stage, block, d.g_bf16, none, q);
-      step_quad<BITS>(r, i + lane * 4, 1, q);
-      store_quad<BITS, true>(d, i, 128, q);
+      take_quad<BITS, kIsWide>(stage, block, d.g_bf16, shift, q);
+      step_quad<BITS>(r, i + (kIsWide ? lane * 4 : lane), kIsWide ? 1 : 32, q);
+      store_quad<BITS, kIsWide>(d, i, 128, q);
     }
-    return;
-  }
+  };
+  if (a.kind == kWide) return whole(std::true_type());
+  if (a.kind == kNarrow) return whole(std::false_type());
 #pragma unroll 1
-  for (uint32_t block = warp; block < kBlocks; block += kWarps) {
+  for (uint32_t block = warp; block * 128 < a.left; block += kWarps) {
     const int64_t i = a.base + block * 128;
     Quad q;
-    uint32_t left = 128;
-    if (a.kind == kNarrow) {
-      take_quad<BITS, false>(stage, block, d.g_bf16, shift, q);
-    } else {
-      if (block * 128 >= a.left) break;
-      left = a.left - block * 128;
-      load_quad<BITS>(d, i, left, q);
-    }
+    load_quad<BITS>(d, i, a.left - block * 128, q);
     step_quad<BITS>(r, i + lane, 32, q);
-    store_quad<BITS, false>(d, i, left, q);
+    store_quad<BITS, false>(d, i, a.left - block * 128, q);
   }
 }
 
