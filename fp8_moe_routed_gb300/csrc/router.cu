@@ -23,7 +23,7 @@
 namespace fp8moe {
 namespace {
 
-constexpr int kJoinThreads = 1024;
+constexpr int kJoinThreads = 1024, kJoinCtas = 8;
 
 __device__ __forceinline__ uint32_t load_peer(const void* p, int cta) {
   uint32_t v;
@@ -303,10 +303,17 @@ __global__ void __launch_bounds__(kJoinThreads) balance_join_kernel(const int32_
   }
   if (ctas > 1) {
     cluster_sync();
-    if (cta == 0 && tid < width) {
-      for (int r = 1; r < ctas; ++r) {
-        share += __uint_as_float(load_peer(&s_share[tid], r));
-        count += (int32_t)load_peer(&s_count[tid], r);
+    if (cta == 0 && tid < width) {               // all on their way before the first is added
+      uint32_t shares[kJoinCtas - 1], those[kJoinCtas - 1];
+#pragma unroll
+      for (int r = 1; r < kJoinCtas; ++r) {
+        shares[r - 1] = load_peer(&s_share[tid], r);
+        those[r - 1] = load_peer(&s_count[tid], r);
+      }
+#pragma unroll
+      for (int r = 0; r < kJoinCtas - 1; ++r) {
+        share += __uint_as_float(shares[r]);
+        count += (int32_t)those[r];
       }
     }
     tokens = 0;
@@ -387,7 +394,7 @@ cudaError_t fp8moe_launch_router(const RouterArgs& args, cudaStream_t s) {
   int width = 32;
   while (width < a.E) width *= 2;
   const int64_t parts = (a.T + a.chunk - 1) / a.chunk;
-  const int ctas = parts / a.B > 16 ? 8 : 1;
+  const int ctas = parts / a.B > 64 ? kJoinCtas : 1;
   cudaLaunchConfig_t cfg = {};
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeClusterDimension;
