@@ -927,53 +927,58 @@ class AdamwPlan:
         self.params, self._kept, self._shapes = list(params), [], []
         self.device = None
         self._table = (_AdamwTensor * max(1, count))()
-        f32, u8 = torch.float32, torch.uint8
-        spans = []
+        f32, u8, bf16 = torch.float32, torch.uint8, torch.bfloat16
+        spans, index = [], None
+
+        def enter(e, i, t, field, dtype, shape, name):
+            """Checks a tensor and writes its address down; its memory is kept."""
+            nonlocal index
+            if not (isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape
+                    and t.is_cuda and t.is_contiguous()):
+                _shaped(t, dtype, f"{name} {i}", tuple(shape))
+            if t.get_device() != index:
+                if index is not None:
+                    raise ValueError(f"param {i} and its states must be on {self.device}")
+                self.device, index = t.device, t.get_device()
+            at = t.data_ptr()
+            setattr(e, field, at)
+            spans.append((at, at + t.nbytes, i))
+            self._kept.append(t.untyped_storage())
+
         for i, p in enumerate(self.params):
             if not isinstance(p, torch.Tensor):
                 raise TypeError(f"param {i} must be a tensor")
-            shape, n = tuple(p.shape), p.numel()
-            _req(p, f32, f"param {i}", p.dim())
+            shape, n, e = p.shape, p.numel(), self._table[i]
+            enter(e, i, p, "p", f32, shape, "param")
             eight = m_scales[i] is not None
             if eight != (v_scales[i] is not None):
                 raise ValueError(f"m_scale and v_scale of param {i} go together")
             state = u8 if eight else f32
-            _shaped(m[i], state, f"m of param {i}", shape)
-            _shaped(v[i], state, f"v of param {i}", shape)
+            enter(e, i, m[i], "m", state, shape, "m of param")
+            enter(e, i, v[i], "v", state, shape, "v of param")
             if eight:
-                _shaped(m_scales[i], f32, f"m_scale of param {i}", (adamw_blocks(n),))
-                _shaped(v_scales[i], f32, f"v_scale of param {i}", (adamw_blocks(n),))
+                blocks = (adamw_blocks(n),)
+                enter(e, i, m_scales[i], "m_scale", f32, blocks, "m_scale of param")
+                enter(e, i, v_scales[i], "v_scale", f32, blocks, "v_scale of param")
             if copies[i] is not None:
-                _shaped(copies[i], torch.bfloat16, f"copy of param {i}", shape)
+                enter(e, i, copies[i], "copy", bf16, shape, "copy of param")
             if (codes[i] is None) != (code_scales[i] is None):
                 raise ValueError(f"codes and code_scale of param {i} go together")
-            e = self._table[i]
             if codes[i] is not None:
                 if len(shape) != 3:
-                    raise ValueError(f"param {i} must be [E, K, N] to have codes, got {shape}")
-                _shaped(codes[i], u8, f"codes of param {i}", shape)
-                _shaped(code_scales[i], f32, f"code_scale of param {i}", (shape[0], shape[2]))
+                    raise ValueError(f"param {i} must be [E, K, N] to have codes, got {tuple(shape)}")
+                enter(e, i, codes[i], "codes", u8, shape, "codes of param")
+                enter(e, i, code_scales[i], "code_scale", f32, (shape[0], shape[2]),
+                      "code_scale of param")
                 e.K, e.N = shape[1], shape[2]
-            own = [p, m[i], v[i], m_scales[i], v_scales[i], copies[i], codes[i], code_scales[i]]
-            for t, field in zip(own, ("p", "m", "v", "m_scale", "v_scale", "copy", "codes",
-                                      "code_scale")):
-                if t is None:
-                    continue
-                if self.device is None:
-                    self.device = t.device
-                if t.device != self.device:
-                    raise ValueError(f"param {i} and its states must be on {self.device}")
-                setattr(e, field, t.data_ptr())
-                spans.append((t.data_ptr(), t.data_ptr() + t.numel() * t.element_size(), i))
-                self._kept.append(t.detach())
             e.n, e.weight_decay, e.state_bits = n, float(decay[i]), 8 if eight else 32
-            self._shapes.append(p.shape)
+            self._shapes.append(shape)
         spans = sorted(s for s in spans if s[0] < s[1])
         for a, b in zip(spans, spans[1:]):
             if b[0] < a[1]:
                 raise ValueError(f"params {a[2]} and {b[2]} or their states overlap")
         self._addresses = [p.data_ptr() for p in self.params]
-        self._indices = [self.device.index] * count if count else []
+        self._indices = [index] * count
         self._numels = array.array("Q", [p.numel() for p in self.params])
         self._columns = memoryview(self._table).cast("B").cast("Q") if count else None
         self._type = None                       # of all gradients in the table
