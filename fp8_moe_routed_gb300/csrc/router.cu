@@ -6,8 +6,8 @@
 //   share p_i = s_i / sum s;  for a sequence of n tokens with C choices, c_i of them expert i:
 //   loss = sum_i slope_i * sum_t p_ti,  slope_i = E c_i / (C n)
 //
-// A warp takes a token: lane l holds experts [l V, l V + V) in registers, so that one pass over
-// the logits gives the maximum, the sum, the choice and the shares.
+// A warp takes a token, its logits in registers, so that one pass over them gives the maximum, the
+// sum, the choice and the shares.
 #include <cmath>
 #include <cstdint>
 #include <cuda_runtime.h>
@@ -34,6 +34,7 @@ __device__ __forceinline__ uint32_t load_peer(const void* p, int cta) {
 
 template <typename T, int V, bool VECT, bool GIVEN>
 __global__ void __launch_bounds__(kThreads, V <= 16 ? 4 : 1) router_kernel(const __grid_constant__ RouterArgs a) {
+  using R = Row<32, V, kPiece<T, V, VECT>>;
   extern __shared__ float s_mem[];
   float* s_share = s_mem;                                           // [kWarps][32 V]
   int32_t* s_count = reinterpret_cast<int32_t*>(s_mem + kWarps * 32 * V);   // [32 V]
@@ -52,7 +53,7 @@ __global__ void __launch_bounds__(kThreads, V <= 16 ? 4 : 1) router_kernel(const
   auto token = [&](int64_t t) {
     const T* row = logits + t * E;
     float x[V];
-    load_row<T, V, VECT>(row, E, lane, -INFINITY, x);
+    R::load(row, E, lane, -INFINITY, x);
     int id = -1;
     if (GIVEN && lane < k) id = a.given[t * k + lane];
     auto row_max = [&]() {
@@ -90,7 +91,7 @@ __global__ void __launch_bounds__(kThreads, V <= 16 ? 4 : 1) router_kernel(const
       uint32_t key[V];
 #pragma unroll
       for (int j = 0; j < V; ++j) {
-        const int e = lane * V + j;
+        const int e = R::expert(lane, j);
         float c = x[j];
         if (has_bias && c != -INFINITY) {
           const float b = e < E ? a.bias[e] : 0.0f;
@@ -225,7 +226,7 @@ __global__ void __launch_bounds__(kThreads, V <= 16 ? 4 : 1) router_kernel(const
     if (lane == 0) s_tokens[warp] = tokens;
     __syncthreads();
     for (int i = threadIdx.x; i < 32 * V; i += kThreads) {
-      const int e = (i & 31) * V + (i >> 5);
+      const int e = R::expert(i & 31, i >> 5);
       if (e >= E) continue;
       float sum = 0.0f;
 #pragma unroll
@@ -352,7 +353,7 @@ cudaError_t launch_router(const RouterArgs& a, cudaStream_t s) {
   return with_width(a.E, [&](auto width) {
     constexpr int V = decltype(width)::value;
     const size_t smem = (size_t)(kWarps + 1) * 32 * V * sizeof(float);
-    if (whole_pieces<T>(a.E, V))
+    if (whole_pieces<T, V>(a.E))
       router_kernel<T, V, true, GIVEN><<<(unsigned)grid, kThreads, smem, s>>>(a);
     else
       router_kernel<T, V, false, GIVEN><<<(unsigned)grid, kThreads, smem, s>>>(a);

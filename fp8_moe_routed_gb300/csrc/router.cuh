@@ -30,72 +30,89 @@ inline bool by_groups(int64_t T, int E, int k, bool bias) {
 __device__ __forceinline__ float load_f32(const float* p) { return *p; }
 __device__ __forceinline__ float load_f32(const __nv_bfloat16* p) { return __bfloat162float(*p); }
 
-// Lane l holds experts [l * V, l * V + V): the lowest expert is in the lowest lane. VECT: rows
-// of whole 16-byte pieces (or of whole lanes, where a lane has less). Past E: `fill`.
-template <typename T, int V, bool VECT>
-__device__ __forceinline__ void load_row(const T* row, int E, int lane, float fill, float (&x)[V]) {
-  const int e0 = lane * V;
-  if constexpr (!VECT) {
+// The V experts that a lane of the G of a token holds: pieces of P, which is 16 bytes (or all of a
+// lane's) where rows are whole pieces, so that the lanes' pieces follow each other in memory, and 1
+// where they are not.
+template <int G, int V, int P>
+struct Row {
+  static_assert(V % P == 0, "whole pieces");
+  static __device__ __forceinline__ int expert(int lane, int j) {
+    return (j / P * G + lane) * P + j % P;
+  }
+  // where expert e stands in [V][G] values, in the order of the lanes' registers
+  static __device__ __forceinline__ int place(int e) {
+    return (e / (G * P) * P + e % P) * G + e / P % G;
+  }
+  // past E: `fill`
+  template <typename T>
+  static __device__ __forceinline__ void load(const T* row, int E, int lane, float fill,
+                                              float (&x)[V]) {
+    constexpr int kBytes = P * (int)sizeof(T);
 #pragma unroll
-    for (int j = 0; j < V; ++j) x[j] = e0 + j < E ? load_f32(row + e0 + j) : fill;
-  } else {
-    constexpr int kWords = V * (int)sizeof(T) / 4;          // 32-bit words of a lane
-    constexpr int kPiece = kWords < 4 ? kWords : 4;         // of one load
-    constexpr int kValues = kPiece * 4 / (int)sizeof(T);
-#pragma unroll
-    for (int i = 0; i < kWords / kPiece; ++i) {
-      uint32_t w[kPiece];
-      const bool in = e0 + i * kValues < E;
-      const T* p = row + e0 + i * kValues;
-      if constexpr (kPiece == 4) {
-        const uint4 v = in ? *reinterpret_cast<const uint4*>(p) : make_uint4(0, 0, 0, 0);
-        w[0] = v.x, w[1] = v.y, w[2] = v.z, w[3] = v.w;
-      } else if constexpr (kPiece == 2) {
-        const uint2 v = in ? *reinterpret_cast<const uint2*>(p) : make_uint2(0, 0);
-        w[0] = v.x, w[1] = v.y;
+    for (int i = 0; i < V / P; ++i) {
+      const T* p = row + expert(lane, i * P);
+      const bool in = expert(lane, i * P) < E;
+      float (&y)[P] = *reinterpret_cast<float (*)[P]>(&x[i * P]);
+      if constexpr (P == 1) {
+        y[0] = in ? load_f32(p) : fill;
       } else {
-        w[0] = in ? *reinterpret_cast<const uint32_t*>(p) : 0;
-      }
+        uint32_t w[kBytes / 4];
+        words<kBytes / 4>(p, in, w);
 #pragma unroll
-      for (int j = 0; j < kPiece; ++j) {
-        if constexpr (sizeof(T) == 4) {
-          x[i * kValues + j] = in ? __uint_as_float(w[j]) : fill;
-        } else {
-          x[i * kValues + 2 * j] = in ? bf16lo_to_f32(w[j]) : fill;
-          x[i * kValues + 2 * j + 1] = in ? bf16hi_to_f32(w[j]) : fill;
+        for (int j = 0; j < kBytes / 4; ++j) {
+          if constexpr (sizeof(T) == 4) {
+            y[j] = in ? __uint_as_float(w[j]) : fill;
+          } else {
+            y[2 * j] = in ? bf16lo_to_f32(w[j]) : fill;
+            y[2 * j + 1] = in ? bf16hi_to_f32(w[j]) : fill;
+          }
         }
       }
     }
   }
-}
-
-template <typename T, int V, bool VECT>
-__device__ __forceinline__ void store_row(T* row, int E, int lane, const float (&x)[V]) {
-  const int e0 = lane * V;
-  if constexpr (!VECT) {
+  template <typename T>
+  static __device__ __forceinline__ void store(T* row, int E, int lane, const float (&x)[V]) {
+    constexpr int kWords = P * (int)sizeof(T) / 4;
 #pragma unroll
-    for (int j = 0; j < V; ++j)
-      if (e0 + j < E) row[e0 + j] = T(x[j]);
-  } else {
-    constexpr int kWords = V * (int)sizeof(T) / 4;
-    constexpr int kPiece = kWords < 4 ? kWords : 4;
-    constexpr int kValues = kPiece * 4 / (int)sizeof(T);
+    for (int i = 0; i < V / P; ++i) {
+      T* p = row + expert(lane, i * P);
+      if (expert(lane, i * P) >= E) continue;
+      if constexpr (P == 1) {
+        *p = T(x[i]);
+      } else {
+        uint32_t w[kWords];
 #pragma unroll
-    for (int i = 0; i < kWords / kPiece; ++i) {
-      uint32_t w[kPiece];
-#pragma unroll
-      for (int j = 0; j < kPiece; ++j) {
-        if constexpr (sizeof(T) == 4) w[j] = __float_as_uint(x[i * kValues + j]);
-        else w[j] = f32x2_to_bf16x2(x[i * kValues + 2 * j], x[i * kValues + 2 * j + 1]);
+        for (int j = 0; j < kWords; ++j) {
+          if constexpr (sizeof(T) == 4) w[j] = __float_as_uint(x[i * P + j]);
+          else w[j] = f32x2_to_bf16x2(x[i * P + 2 * j], x[i * P + 2 * j + 1]);
+        }
+        if constexpr (kWords == 4) *reinterpret_cast<uint4*>(p) = make_uint4(w[0], w[1], w[2], w[3]);
+        else if constexpr (kWords == 2) *reinterpret_cast<uint2*>(p) = make_uint2(w[0], w[1]);
+        else *reinterpret_cast<uint32_t*>(p) = w[0];
       }
-      if (e0 + i * kValues >= E) continue;
-      T* p = row + e0 + i * kValues;
-      if constexpr (kPiece == 4) *reinterpret_cast<uint4*>(p) = make_uint4(w[0], w[1], w[2], w[3]);
-      else if constexpr (kPiece == 2) *reinterpret_cast<uint2*>(p) = make_uint2(w[0], w[1]);
-      else *reinterpret_cast<uint32_t*>(p) = w[0];
     }
   }
-}
+
+ private:
+  template <int N>
+  static __device__ __forceinline__ void words(const void* p, bool in, uint32_t (&w)[N]) {
+    if constexpr (N >= 4) {
+#pragma unroll
+      for (int i = 0; i < N / 4; ++i) {
+        const uint4 v = in ? static_cast<const uint4*>(p)[i] : make_uint4(0, 0, 0, 0);
+        w[4 * i] = v.x, w[4 * i + 1] = v.y, w[4 * i + 2] = v.z, w[4 * i + 3] = v.w;
+      }
+    } else if constexpr (N == 2) {
+      const uint2 v = in ? *static_cast<const uint2*>(p) : make_uint2(0, 0);
+      w[0] = v.x, w[1] = v.y;
+    } else {
+      w[0] = in ? *static_cast<const uint32_t*>(p) : 0;
+    }
+  }
+};
+// Values of a piece of a lane's V.
+template <typename T, int V, bool VECT>
+constexpr int kPiece = !VECT ? 1 : V * (int)sizeof(T) < 16 ? V : 16 / (int)sizeof(T);
 
 __device__ __forceinline__ float warp_sum(float v) {
 #pragma unroll
@@ -222,12 +239,8 @@ __device__ __forceinline__ float lanes_sum(float v) {
   else return group_sum(v);
 }
 
-// Rows of whole pieces for 16-byte accesses (load_row); V: experts of a lane.
-template <typename T>
-bool whole_pieces(int E, int V) {
-  const int values = (V * (int)sizeof(T) < 16 ? V * (int)sizeof(T) : 16) / (int)sizeof(T);
-  return E % values == 0;
-}
+template <typename T, int V>
+bool whole_pieces(int E) { return E % kPiece<T, V, true> == 0; }
 template <int N> using Int = std::integral_constant<int, N>;
 // f(experts of a lane), where a warp or where eight lanes have a token.
 template <typename F>

@@ -22,6 +22,7 @@ namespace {
 template <typename T, int G, int V, bool VECT>
 __global__ void __launch_bounds__(kThreads, V <= 16 ? 4 : 1) router_bwd_kernel(
     const __grid_constant__ RouterBwdArgs a) {
+  using R = Row<G, V, kPiece<T, V, VECT>>;
   extern __shared__ float s_mem[];
   const int lane = threadIdx.x % G, warp = threadIdx.x / 32;
   float* s_row = s_mem + (threadIdx.x / G) * G * V;
@@ -36,7 +37,7 @@ __global__ void __launch_bounds__(kThreads, V <= 16 ? 4 : 1) router_bwd_kernel(
   const T* row = static_cast<const T*>(a.logits) + t * E;
   T* out = static_cast<T*>(a.dlogits) + t * E;
   float x[V], dx[V];
-  load_row<T, V, VECT>(row, E, lane, -INFINITY, x);
+  R::load(row, E, lane, -INFINITY, x);
   int id = lane < k ? a.ids[t * k + lane] : -1;
   if (id >= E) {
     status_set(kStatusBadExpert);
@@ -56,7 +57,7 @@ __global__ void __launch_bounds__(kThreads, V <= 16 ? 4 : 1) router_bwd_kernel(
   if (__all_sync(kAllLanes, none)) {
 #pragma unroll
     for (int j = 0; j < V; ++j) dx[j] = 0.0f;
-    if (on) store_row<T, V, VECT>(out, E, lane, dx);
+    if (on) R::store(out, E, lane, dx);
     return;
   }
   if (none) b = 0;
@@ -79,7 +80,7 @@ __global__ void __launch_bounds__(kThreads, V <= 16 ? 4 : 1) router_bwd_kernel(
   } else {
     part = joins ? dw : dw * sigmoid(xc);
   }
-  const int place = id >= 0 ? (id % V) * G + id / V : 0;
+  const int place = id >= 0 ? R::place(id) : 0;
   // is an expert among the choices twice?
   const int self = threadIdx.x % 32;
   const int key = id >= 0 ? self / G * 1024 + id : -1 - self;
@@ -113,7 +114,7 @@ __global__ void __launch_bounds__(kThreads, V <= 16 ? 4 : 1) router_bwd_kernel(
     const float inv_sum = inverse(lanes_sum<G>(shares_sum.x + shares_sum.y));
     float D[V];
     float2 dot = both(0.0f);
-    if (a.dloss != nullptr) load_row<float, V, VECT>(a.slope + (int64_t)b * E, E, lane, 0.0f, D);
+    if (a.dloss != nullptr) R::load(a.slope + (int64_t)b * E, E, lane, 0.0f, D);
     const float dl = a.dloss != nullptr ? a.dloss[b] : 0.0f;
 #pragma unroll
     for (int h = 0; h < V / 2; ++h) {
@@ -134,7 +135,7 @@ __global__ void __launch_bounds__(kThreads, V <= 16 ? 4 : 1) router_bwd_kernel(
     if (sig) d[h] = mul2(d[h], q[h]);
     dx[2 * h] = none ? 0.0f : d[h].x, dx[2 * h + 1] = none ? 0.0f : d[h].y;
   }
-  if (on) store_row<T, V, VECT>(out, E, lane, dx);
+  if (on) R::store(out, E, lane, dx);
 }
 
 }  // namespace
@@ -151,8 +152,7 @@ cudaError_t fp8moe_launch_router_bwd(const RouterBwdArgs& a, cudaStream_t s) {
     const int64_t tokens = kWarps * (32 / G);    // of a CTA
     const unsigned grid = (unsigned)((a.T + tokens - 1) / tokens);
     const size_t smem = (size_t)tokens * G * V * sizeof(float);
-    // slope rows are f32: their pieces have to be whole, too
-    if (whole_pieces<T>(a.E, V) && whole_pieces<float>(a.E, V))
+    if (whole_pieces<T, V>(a.E))
       router_bwd_kernel<T, G, V, true><<<grid, kThreads, smem, s>>>(a);
     else
       router_bwd_kernel<T, G, V, false><<<grid, kThreads, smem, s>>>(a);

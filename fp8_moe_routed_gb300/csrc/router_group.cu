@@ -21,6 +21,7 @@ template <typename T, int V, bool VECT, bool GIVEN>
 __global__ void __launch_bounds__(kThreads) router_group_kernel(
     const __grid_constant__ RouterArgs a) {
   constexpr int W = kGroup * V;
+  using R = Row<kGroup, V, kPiece<T, V, VECT>>;
   extern __shared__ float s_mem[];
   float* s_share = s_mem;                                           // [kWarps][W]
   int32_t* s_count = reinterpret_cast<int32_t*>(s_mem + kWarps * W);   // [W]
@@ -45,7 +46,7 @@ __global__ void __launch_bounds__(kThreads) router_group_kernel(
     const int64_t t = on ? first + g : first;
     const T* row = logits + t * E;
     float x[V];
-    load_row<T, V, VECT>(row, E, l, -INFINITY, x);
+    R::load(row, E, l, -INFINITY, x);
     int id = -1;
     if (GIVEN && on && l < k) id = a.given[t * k + l];
     auto row_max = [&]() {
@@ -75,7 +76,7 @@ __global__ void __launch_bounds__(kThreads) router_group_kernel(
     } else {
       uint32_t key[V];
 #pragma unroll
-      for (int j = 0; j < V; ++j) key[j] = choice_key(x[j], l * V + j);
+      for (int j = 0; j < V; ++j) key[j] = choice_key(x[j], R::expert(l, j));
       sort_keys(key);
       // a lane's first nine are all that eight choices and the next one can come from
       constexpr int kDepth = V < kGroup + 1 ? V : kGroup + 1;
@@ -182,7 +183,7 @@ __global__ void __launch_bounds__(kThreads) router_group_kernel(
     if (lane == 0) s_tokens[warp] = all;
     __syncthreads();
     for (int i = threadIdx.x; i < W; i += kThreads) {
-      const int e = (i % kGroup) * V + i / kGroup;
+      const int e = R::expert(i % kGroup, i / kGroup);
       if (e >= E) continue;
       float sum = 0.0f;
 #pragma unroll
@@ -208,7 +209,7 @@ cudaError_t launch_groups(const RouterArgs& a, cudaStream_t s) {
   return with_group_width(a.E, [&](auto width) {
     constexpr int V = decltype(width)::value;
     const size_t smem = (size_t)(kWarps + 1) * kGroup * V * sizeof(float);
-    if (whole_pieces<T>(a.E, V))
+    if (whole_pieces<T, V>(a.E))
       router_group_kernel<T, V, true, GIVEN><<<(unsigned)grid, kThreads, smem, s>>>(a);
     else
       router_group_kernel<T, V, false, GIVEN><<<(unsigned)grid, kThreads, smem, s>>>(a);
