@@ -33,7 +33,8 @@ __device__ __forceinline__ uint32_t load_peer(const void* p, int cta) {
 }
 
 template <typename T, int V, bool VECT, bool GIVEN>
-__global__ void __launch_bounds__(kThreads, V <= 16 ? 4 : 1) router_kernel(const __grid_constant__ RouterArgs a) {
+__global__ void __launch_bounds__(kThreads, GIVEN ? V <= 16 ? 4 : 3 : V <= 8 ? 4 : 2)
+    router_kernel(const __grid_constant__ RouterArgs a) {
   using R = Row<32, V, kPiece<T, V, VECT>>;
   extern __shared__ float s_mem[];
   float* s_share = s_mem;                                           // [kWarps][32 V]

@@ -20,7 +20,7 @@ namespace fp8moe {
 namespace {
 
 template <typename T, int G, int V, bool VECT>
-__global__ void __launch_bounds__(kThreads, V <= 16 ? 4 : 1) router_bwd_kernel(
+__global__ void __launch_bounds__(kThreads, V <= 16 ? 4 : 2) router_bwd_kernel(
     const __grid_constant__ RouterBwdArgs a) {
   using R = Row<G, V, kPiece<T, V, VECT>>;
   extern __shared__ float s_mem[];
