@@ -773,8 +773,11 @@ SCORES = {"softmax": 0, "sigmoid": 1}
 
 def _router(logits, score: str, topk: int, seq_offsets):
     """Checks what the router's calls share: (type number, score number, B)."""
-    ty = _req_rows(logits, "logits")
-    if score not in SCORES:
+    ty = TYPES.get(logits.dtype) if isinstance(logits, torch.Tensor) else None
+    if ty is None or not logits.is_cuda or logits.dim() != 2 or not logits.is_contiguous():
+        ty = _req_rows(logits, "logits")
+    sc = SCORES.get(score)
+    if sc is None:
         raise ValueError(f"score must be one of {sorted(SCORES)}, got {score!r}")
     B = 1
     if seq_offsets is not None:
@@ -782,16 +785,20 @@ def _router(logits, score: str, topk: int, seq_offsets):
         B = seq_offsets.numel() - 1
         if B < 1:
             raise ValueError("seq_offsets must hold at least one sequence (two offsets)")
-    return ty, SCORES[score], B
+    return ty, sc, B
 
 
-def _one_device(device, **tensors):
-    """Every tensor of a call lies on the current device."""
-    if device.index != torch.cuda.current_device():
+_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+
+
+def _one_device(device, *tensors) -> None:
+    """Every tensor of a call (or None) lies on the current device."""
+    index = device.index
+    for t in tensors:
+        if t is not None and t.get_device() != index:
+            raise ValueError(f"tensors must be on {device}, got one on {t.device}")
+    if index != _current_device():
         raise ValueError(f"tensors must be on the current device, got {device}")
-    for name, t in tensors.items():
-        if t is not None and t.device != device:
-            raise ValueError(f"{name} must be on {device}, got {t.device}")
 
 
 def _balance_outputs(B: int, E: int, device):
@@ -813,7 +820,7 @@ def router_fwd(logits, topk: int, score: str = "softmax", bias=None, normalize: 
     dev = logits.device
     if bias is not None:
         _shaped(bias, torch.float32, "bias", (E,))
-    _one_device(dev, bias=bias, seq_offsets=seq_offsets, workspace=workspace)
+    _one_device(dev, bias, seq_offsets, workspace)
     if topk < 1:
         raise ValueError("topk must be positive")
     ids = torch.empty(T, topk, dtype=torch.int32, device=dev)
@@ -823,10 +830,11 @@ def router_fwd(logits, topk: int, score: str = "softmax", bias=None, normalize: 
     if balance:
         counts, loss, slope = _balance_outputs(B, E, dev)
         ws, wsb = _workspace(OP_BALANCE, T, 0, B, E, dev, workspace)
-    _check(L.fp8moe_router_fwd(_ptr(logits), T, E, ty, sc, _ptr(bias), topk, int(bool(normalize)),
-                               weight_scale, _ptr(seq_offsets), B, _ptr(ids), _ptr(weights),
-                               _ptr(counts), _ptr(loss), _ptr(slope), _ptr(ws), wsb, _stream(dev)),
-           "fp8moe_router_fwd")
+    rc = L.fp8moe_router_fwd(logits.data_ptr(), T, E, ty, sc, _ptr(bias), topk, 1 if normalize else 0,
+                             weight_scale, _ptr(seq_offsets), B, ids.data_ptr(), weights.data_ptr(),
+                             _ptr(counts), _ptr(loss), _ptr(slope), _ptr(ws), wsb, _stream(dev))
+    if rc:
+        _check(rc, "fp8moe_router_fwd")
     return ids, weights, counts, loss, slope
 
 
@@ -842,7 +850,7 @@ def balance_fwd(logits, ids, score: str = "softmax", seq_offsets=None, workspace
     if logits.shape[0] != T:
         raise ValueError("shape mismatch")
     E, dev = logits.shape[1], logits.device
-    _one_device(dev, ids=ids, seq_offsets=seq_offsets, workspace=workspace)
+    _one_device(dev, ids, seq_offsets, workspace)
     counts, loss, slope = _balance_outputs(B, E, dev)
     ws, wsb = _workspace(OP_BALANCE, T, 0, B, E, dev, workspace)
     _check(L.fp8moe_balance_fwd(_ptr(logits), _ptr(ids), T, E, ty, sc, k, _ptr(seq_offsets), B,
@@ -870,8 +878,7 @@ def router_bwd(dweights, logits, ids, score: str = "softmax", normalize: bool = 
     if dloss is not None:
         _shaped(dloss, f32, "dloss", (B,))
         _shaped(slope, f32, "slope", (B, E))
-    _one_device(dev, ids=ids, dweights=dweights, dloss=dloss, slope=slope, seq_offsets=seq_offsets,
-                out=out)
+    _one_device(dev, ids, dweights, dloss, slope, seq_offsets, out)
     out = _like(out, (T, E), logits.dtype, dev, "out")
     _check(L.fp8moe_router_bwd(_ptr(dweights), _ptr(logits), _ptr(ids), T, E, ty, sc, k,
                                int(bool(normalize)), weight_scale, _ptr(dloss), _ptr(slope),
@@ -1051,7 +1058,7 @@ def adamw_step(plan: AdamwPlan, grads, step, lr, beta1: float = 0.9, beta2: floa
         lr, lr_dev = 0.0, lr
     if grad_scale is not None:
         _shaped(grad_scale, torch.float32, "grad_scale", (1,))
-    _one_device(dev, step=step_dev, lr=lr_dev, grad_scale=grad_scale, workspace=workspace)
+    _one_device(dev, step_dev, lr_dev, grad_scale, workspace)
     need = int(L.fp8moe_adamw_workspace_size(table, count,
                                              step_dev is not None or lr_dev is not None))
     if workspace is None and need:
