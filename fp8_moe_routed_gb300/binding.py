@@ -989,12 +989,11 @@ class AdamwPlan:
         self._numels = array.array("Q", [p.numel() for p in self.params])
         self._columns = memoryview(self._table).cast("B").cast("Q") if count else None
         self._type = None                       # of all gradients in the table
+        self._lock = threading.Lock()           # the table is one call's until the library read it
 
     def _enter(self, grads):
         """Writes the gradients' addresses and types into the table."""
         count = len(self.params)
-        if count == 0:
-            return self._table, 0
         if len(grads) != count:
             raise ValueError(f"grads must have one entry for each of the {count} params")
         if [p.data_ptr() for p in self.params] != self._addresses:
@@ -1045,8 +1044,7 @@ def adamw_step(plan: AdamwPlan, grads, step, lr, beta1: float = 0.9, beta2: floa
     a captured step reads when it is replayed). grad_scale: f32 CUDA tensor [1] that every gradient
     is multiplied by, or None. seed: of the rounding of 8-bit moments."""
     L = load()
-    table, count = plan._enter(grads)
-    if count == 0:
+    if not plan.params:
         return
     dev = plan.device
     step_dev = lr_dev = None
@@ -1059,16 +1057,19 @@ def adamw_step(plan: AdamwPlan, grads, step, lr, beta1: float = 0.9, beta2: floa
     if grad_scale is not None:
         _shaped(grad_scale, torch.float32, "grad_scale", (1,))
     _one_device(dev, step_dev, lr_dev, grad_scale, workspace)
-    need = int(L.fp8moe_adamw_workspace_size(table, count,
-                                             step_dev is not None or lr_dev is not None))
-    if workspace is None and need:
-        workspace = torch.empty(need, dtype=torch.uint8, device=dev)
-    elif workspace is not None and not (workspace.is_cuda and workspace.is_contiguous()):
+    if workspace is not None and not (workspace.is_cuda and workspace.is_contiguous()):
         raise ValueError("workspace must be a contiguous CUDA tensor")
-    wsb = workspace.numel() * workspace.element_size() if workspace is not None else 0
-    _check(L.fp8moe_adamw_step(table, count, int(step), _ptr(step_dev), float(lr), _ptr(lr_dev),
-                               beta1, beta2, eps, _ptr(grad_scale), seed & 0xFFFFFFFF,
-                               _ptr(workspace), wsb, _stream(dev)), "fp8moe_adamw_step")
+    with plan._lock:
+        table, count = plan._enter(grads)
+        need = int(L.fp8moe_adamw_workspace_size(table, count,
+                                                 step_dev is not None or lr_dev is not None))
+        if workspace is None and need:
+            workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+        wsb = workspace.numel() * workspace.element_size() if workspace is not None else 0
+        _check(L.fp8moe_adamw_step(table, count, int(step), _ptr(step_dev), float(lr),
+                                   _ptr(lr_dev), beta1, beta2, eps, _ptr(grad_scale),
+                                   seed & 0xFFFFFFFF, _ptr(workspace), wsb, _stream(dev)),
+               "fp8moe_adamw_step")
 
 
 def read_status(device=None) -> int:

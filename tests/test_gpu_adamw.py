@@ -1,5 +1,7 @@
 """The AdamW step: bit for bit against f32 operations rounded one by one, and against the formula
 in 64 bits, on the GPU."""
+import threading
+
 import numpy as np
 import pytest
 import torch
@@ -298,6 +300,32 @@ def test_params_without_a_gradient_stay():
     fb.adamw_step(plan, grads_of(ts) + [None], step=2, **HYPER)
     for i, t in enumerate(ts):
         t.step(i, 2)
+        t.check()
+
+
+def test_two_threads_step_one_plan():
+    """Each thread has the gradients of every other param: a call's gradients stay its own."""
+    ts = [Tensor(50 + i, 8 if i % 4 > 1 else 32, seed=i) for i in range(64)]
+    plan, steps, errors = plan_of(ts), range(1, 21), []
+    torch.cuda.synchronize()
+
+    def work(half):
+        try:
+            grads = [t.d["g"] if i % 2 == half else None for i, t in enumerate(ts)]
+            for s in steps:
+                fb.adamw_step(plan, grads, step=s, **HYPER)
+        except Exception as e:                  # noqa: BLE001 - shown by the assertion below
+            errors.append(e)
+
+    threads = [threading.Thread(target=work, args=(half,)) for half in range(2)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not errors, errors
+    for i, t in enumerate(ts):
+        for s in steps:
+            t.step(i, s)
         t.check()
 
 
