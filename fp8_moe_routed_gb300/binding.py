@@ -996,25 +996,25 @@ class AdamwPlan:
         count = len(self.params)
         if len(grads) != count:
             raise ValueError(f"grads must have one entry for each of the {count} params")
-        if [p.data_ptr() for p in self.params] != self._addresses:
+        if list(map(torch.Tensor.data_ptr, self.params)) != self._addresses:
             raise ValueError("a param's storage was replaced: make a new plan")
         table, dev = self._table, self.device
         try:                                    # the usual case, column by column
             types = [g.dtype for g in grads]
-            if all(t is types[0] for t in types) and types[0] in TYPES \
+            if types.count(types[0]) == count and types[0] in TYPES \
                     and [g.shape for g in grads] == self._shapes \
-                    and all([g.is_contiguous() for g in grads]) \
-                    and [g.get_device() for g in grads] == self._indices:
+                    and all(map(torch.Tensor.is_contiguous, grads)) \
+                    and list(map(torch.Tensor.get_device, grads)) == self._indices:
                 words, step = self._columns, ctypes.sizeof(_AdamwTensor) // 8
                 words[_AdamwTensor.g.offset // 8::step] = \
-                    array.array("Q", [g.data_ptr() for g in grads])
+                    array.array("Q", map(torch.Tensor.data_ptr, grads))
                 words[_AdamwTensor.n.offset // 8::step] = self._numels
                 if self._type != types[0]:
                     for e in table[:count]:
                         e.g_type = TYPES[types[0]]
                     self._type = types[0]
                 return table, count
-        except AttributeError:                  # something is no tensor
+        except (AttributeError, TypeError):     # something is no tensor
             pass
         self._type = None
         for i, g in enumerate(grads):
