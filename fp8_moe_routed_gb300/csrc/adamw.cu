@@ -4,11 +4,13 @@
 //   m = b1 m + (1 - b1) g        v = b2 v + (1 - b2) g g
 //   p = p (1 - lr wd) - lr / (1 - b1^t) * m / (sqrt(v) / sqrt(1 - b2^t) + eps)
 //
-// Every product, sum, root and quotient is rounded by itself to f32 (no contraction), so that a
-// step has one result, however the tensors are cut into units. Moments in 8 bits: e4m3
+// Every product, sum, root and quotient is rounded by itself to f32 (no contraction), and how a root
+// or quotient is found depends on that value alone, so that a step has one result, however the
+// tensors lie and are cut into units. Moments in 8 bits: e4m3
 // codes of m and of sqrt(v), with an f32 scale for 128 values, rounded up or down by chance in
 // proportion to what is lost: rounded to nearest, a moment whose change in a step is below half
 // a code's spacing (6 %; b2 = 0.999 changes v by 0.1 %) would never move.
+#include <cmath>
 #include <cstdint>
 #include <type_traits>
 #include <cuda_runtime.h>
@@ -71,6 +73,7 @@ struct Quad {
 
 struct Rates {
   float keep, rate, root, b1, c1, b2, c2, eps, grad, minus_zero;
+  float low, raised;             // kLeastMoment or more, -rate / kRaise
   uint32_t key;
   double lr;
 };
@@ -331,6 +334,10 @@ __device__ __forceinline__ float max_abs(float a, float b, float c) {
   return r;
 }
 
+__device__ __forceinline__ float largest(const float2 (&x)[2]) {
+  return max_abs(max_abs(x[0].x, x[0].y, x[1].x), x[1].y, 0.0f);
+}
+
 // A product of its own: what is added to it later can not be joined with it into one rounding, as
 // the compiler does with packed products, and with those of a -0 that it knows.
 __device__ __forceinline__ float2 prod2(float2 a, float2 b, float minus_zero) {
@@ -351,6 +358,17 @@ __device__ __forceinline__ float rcp_approx(float x) {
 // remainder (Markstein, "Computation of elementary functions on the IBM RISC System/6000
 // processor", 1990): the nearest f32 but for about one in 2^22, where the exact value lies next to
 // the middle of two. x, and a and b with their quotient, well inside the range of normal numbers.
+//
+// Whether that holds is asked of each value by itself (within()), so that its result does not depend
+// on the values beside it: second moments in [2^-100, 2^36], whose roots' remainders are exact;
+// first moments up to 2^36, raised by 2^40 for the quotient and lowered again by the rate, so that
+// the quotient's remainder is exact for the smallest ones, too (one whose gradient stopped falls
+// below 2^-100 long before its second moment; 2 % of the time of 8-bit moments). The divisors are in [2^-50, 2^46] then (1 / sqrt(1 -
+// b2^t) is at most 2^27, as b2 is a double below 1; kMostEps), the quotients below 2^126.
+constexpr float kLeastMoment = 0x1p-100f, kMostMoment = 0x1p36f, kMostRoot = 0x1p18f;
+constexpr float kMostEps = 0x1p20f;
+constexpr float kRaise = 0x1p40f, kLower = 0x1p-40f;
+constexpr float kLeastRate = 0x1p-60f;           // a smaller one would not be normal when lowered
 __device__ __forceinline__ float2 sqrt2(float2 x) {
   const float2 y = make_float2(rsqrt_approx(x.x), rsqrt_approx(x.y));
   const float2 s = mul2(x, y);
@@ -368,81 +386,114 @@ __device__ __forceinline__ float2 div2(float2 a, float2 b) {
   return fma2(fma2(minus_b, q, a), y, q);
 }
 
-// place: of the lane's first value in the tensor; apart: between two of its values.
-template <int BITS>
-__device__ __forceinline__ void step_quad(const Rates& r, uint64_t place, uint32_t apart, Quad& q) {
-  if constexpr (BITS == 8) {
-    decode4(q.mc, q.ms, q.m);
-    decode4(q.vc, q.vs, q.v);
+// Of one value or of several: the least second moment, the largest root (by sqrt2, whose root of
+// an infinity is a NaN, as that of a NaN is), the largest first moment.
+__device__ __forceinline__ bool within(float second, float root, float first, float least) {
+  return second >= least && root <= kMostRoot && first <= kMostMoment;
+}
+
+__device__ __forceinline__ float2 raised_step(const Rates& r, float2 m, float2 root) {
+  const float2 d = add2(prod2(root, both(r.root), r.minus_zero), both(r.eps));
+  return prod2(div2(mul2(m, both(kRaise)), d), both(r.raised), r.minus_zero);
+}
+// The values that are not within(): by the rounded operations, unless they are all zeros (an expert
+// that got no token: 0 / eps).
+__device__ __forceinline__ void far_step(const Rates& r, float v, float m, float& root, float& step) {
+  if (within(v, root, fabsf(m), r.low)) return;
+  if (v == 0.0f && m == 0.0f && r.eps > 0.0f) {
+    root = v;
+    step = __fmul_rn(m, -r.rate);
+    return;
   }
+  root = __fsqrt_rn(v);
+  const float d = __fadd_rn(__fmul_rn(root, r.root), r.eps);
+  step = __fmul_rn(__fdiv_rn(m, d), -r.rate);
+}
+
+// Steps of COUNT quads, side by side; the few far values are put right behind one branch of all of
+// them (a branch for each quad, in front of the quotient: 1230 us for the experts with 8-bit moments,
+// 1222 so). place: of the lane's first value of each in the tensor;
+// apart: between two of its values.
+template <int BITS, int COUNT>
+__device__ __forceinline__ void step_quads(const Rates& r, const uint64_t (&place)[COUNT],
+                                           uint32_t apart, Quad (&quads)[COUNT]) {
   auto prod = [&](float2 a, float b) { return prod2(a, both(b), r.minus_zero); };
-  float2 p[2], m[2], v[2], root[2], step[2];
+  float2 ms[COUNT][2], vs[COUNT][2], roots[COUNT][2], steps[COUNT][2];
+  bool usual = true;
 #pragma unroll
-  for (int h = 0; h < 2; ++h) {
-    const float2 g = mul2(make_float2(q.g[2 * h], q.g[2 * h + 1]), both(r.grad));
-    p[h] = make_float2(q.p[2 * h], q.p[2 * h + 1]);
-    m[h] = make_float2(q.m[2 * h], q.m[2 * h + 1]);
-    v[h] = make_float2(q.v[2 * h], q.v[2 * h + 1]);
-    if constexpr (BITS == 8) v[h] = mul2(v[h], v[h]);
-    m[h] = add2(prod(m[h], r.b1), prod(g, r.c1));
-    v[h] = add2(prod(v[h], r.b2), prod2(mul2(g, both(r.c2)), g, r.minus_zero));
-  }
-  const float low = fminf(fminf(v[0].x, v[0].y), fminf(v[1].x, v[1].y));
-  const float high = fmaxf(fmaxf(v[0].x, v[0].y), fmaxf(v[1].x, v[1].y));
-  // (the remainder of a root is exact from 2^-101 on; the divisors are in [2^-50, 2^90])
-  if (low >= 0x1p-100f && high <= 0x1p126f) {
+  for (int c = 0; c < COUNT; ++c) {
+    Quad& q = quads[c];
+    float2(&m)[2] = ms[c], (&v)[2] = vs[c], (&root)[2] = roots[c];
+    if constexpr (BITS == 8) {
+      decode4(q.mc, q.ms, q.m);
+      decode4(q.vc, q.vs, q.v);
+    }
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
+      const float2 g = mul2(make_float2(q.g[2 * h], q.g[2 * h + 1]), both(r.grad));
+      m[h] = make_float2(q.m[2 * h], q.m[2 * h + 1]);
+      v[h] = make_float2(q.v[2 * h], q.v[2 * h + 1]);
+      if constexpr (BITS == 8) v[h] = mul2(v[h], v[h]);
+      m[h] = add2(prod(m[h], r.b1), prod(g, r.c1));
+      v[h] = add2(prod(v[h], r.b2), prod2(mul2(g, both(r.c2)), g, r.minus_zero));
       root[h] = sqrt2(v[h]);
-      step[h] = div2(m[h], add2(prod(root[h], r.root), both(r.eps)));
+      steps[c][h] = raised_step(r, m[h], root[h]);
     }
-  } else {
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      root[h] = make_float2(__fsqrt_rn(v[h].x), __fsqrt_rn(v[h].y));
-      const float2 d = add2(prod(root[h], r.root), both(r.eps));
-      step[h] = make_float2(__fdiv_rn(m[h].x, d.x), __fdiv_rn(m[h].y, d.y));
-    }
+    usual &= within(fminf(fminf(v[0].x, v[0].y), fminf(v[1].x, v[1].y)), largest(root), largest(m),
+                    r.low);
   }
+  if (!usual) {
 #pragma unroll
-  for (int h = 0; h < 2; ++h) {
-    p[h] = add2(prod(p[h], r.keep), prod(step[h], -r.rate));
-    q.p[2 * h] = p[h].x, q.p[2 * h + 1] = p[h].y;
-    q.m[2 * h] = m[h].x, q.m[2 * h + 1] = m[h].y;
-    q.v[2 * h] = v[h].x, q.v[2 * h + 1] = v[h].y;
-  }
-  if constexpr (BITS == 8) {
-    // (values that do not exist are zeros, and so are their moments)
-    const float mm = max_abs(max_abs(m[0].x, m[0].y, m[1].x), m[1].y, 0.0f);
-    const float vm = max_abs(max_abs(root[0].x, root[0].y, root[1].x), root[1].y, 0.0f);
-    q.ms = block_scale(__reduce_max_sync(kAll, __float_as_uint(mm)));
-    q.vs = block_scale(__reduce_max_sync(kAll, __float_as_uint(vm)));
-    const float2 scale = make_float2(q.ms, q.vs);
-    float2 inverse = inverse2(scale, mul2(scale, both(-1.0f)));
-    inverse.x = q.ms != 0.0f ? inverse.x : 0.0f;
-    inverse.y = q.vs != 0.0f ? inverse.y : 0.0f;
-    const uint32_t least = q.vs != 0.0f ? 0x01000000u : 0u;
-    // a block lies on one side of 2^32, as its first place is a multiple of 128
-    const uint32_t base = random_place(place, r.key);
-    uint32_t mc[4], vc[4];
+    for (int c = 0; c < COUNT; ++c) {
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      const float2 my = mul2(mul2(m[h], both(inverse.x)), both(0x1p-120f));
-      const float2 vy = mul2(mul2(root[h], both(inverse.y)), both(0x1p-120f));
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const int j = 2 * h + i;
-        const uint32_t bits = random_bits(base + j * apart * kPlace);
-        mc[j] = (__float_as_uint(q.m[j]) & 0x80000000u) |
-                (encode(i ? my.y : my.x, __byte_perm(bits, 0x80u, 0x7104)) & 0x7fffffffu);
-        // a second moment that is not zero (its root then is at least 2^-75) never becomes zero:
-        // m / eps would follow
-        vc[j] = max(encode(i ? vy.y : vy.x, __byte_perm(bits, 0x80u, 0x7324)),
-                    min(__float_as_uint(i ? root[h].y : root[h].x), least));
+      for (int h = 0; h < 2; ++h) {
+        far_step(r, vs[c][h].x, ms[c][h].x, roots[c][h].x, steps[c][h].x);
+        far_step(r, vs[c][h].y, ms[c][h].y, roots[c][h].y, steps[c][h].y);
       }
     }
-    q.mc = top_bytes(mc[0], mc[1], mc[2], mc[3]);
-    q.vc = top_bytes(vc[0], vc[1], vc[2], vc[3]);
+  }
+#pragma unroll
+  for (int c = 0; c < COUNT; ++c) {
+    Quad& q = quads[c];
+    float2(&m)[2] = ms[c], (&v)[2] = vs[c], (&root)[2] = roots[c];
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const float2 p = add2(prod(make_float2(q.p[2 * h], q.p[2 * h + 1]), r.keep), steps[c][h]);
+      q.p[2 * h] = p.x, q.p[2 * h + 1] = p.y;
+      q.m[2 * h] = m[h].x, q.m[2 * h + 1] = m[h].y;
+      q.v[2 * h] = v[h].x, q.v[2 * h + 1] = v[h].y;
+    }
+    if constexpr (BITS == 8) {
+      // (values that do not exist are zeros, and so are their moments)
+      q.ms = block_scale(__reduce_max_sync(kAll, __float_as_uint(largest(m))));
+      q.vs = block_scale(__reduce_max_sync(kAll, __float_as_uint(largest(root))));
+      const float2 scale = make_float2(q.ms, q.vs);
+      float2 inverse = inverse2(scale, mul2(scale, both(-1.0f)));
+      inverse.x = q.ms != 0.0f ? inverse.x : 0.0f;
+      inverse.y = q.vs != 0.0f ? inverse.y : 0.0f;
+      const uint32_t least = q.vs != 0.0f ? 0x01000000u : 0u;
+      // a block lies on one side of 2^32, as its first place is a multiple of 128
+      const uint32_t base = random_place(place[c], r.key);
+      uint32_t mc[4], vc[4];
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const float2 my = mul2(mul2(m[h], both(inverse.x)), both(0x1p-120f));
+        const float2 vy = mul2(mul2(root[h], both(inverse.y)), both(0x1p-120f));
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const int j = 2 * h + i;
+          const uint32_t bits = random_bits(base + j * apart * kPlace);
+          mc[j] = (__float_as_uint(q.m[j]) & 0x80000000u) |
+                  (encode(i ? my.y : my.x, __byte_perm(bits, 0x80u, 0x7104)) & 0x7fffffffu);
+          // a second moment that is not zero (its root then is at least 2^-75) never becomes zero:
+          // m / eps would follow
+          vc[j] = max(encode(i ? vy.y : vy.x, __byte_perm(bits, 0x80u, 0x7324)),
+                      min(__float_as_uint(i ? root[h].y : root[h].x), least));
+        }
+      }
+      q.mc = top_bytes(mc[0], mc[1], mc[2], mc[3]);
+      q.vc = top_bytes(vc[0], vc[1], vc[2], vc[3]);
+    }
   }
 }
 
@@ -514,10 +565,10 @@ __device__ __forceinline__ void linear_stage(const AdamwEntry& d, const Rates& r
     for (uint32_t n = 0; n < kBlocks / kWarps; ++n) {
       const uint32_t block = n * kWarps + warp;
       const int64_t i = a.base + block * 128;
-      Quad q;
-      take_quad<BITS, kIsWide>(stage, block, d.g_bf16, shift, q);
-      step_quad<BITS>(r, i + (kIsWide ? lane * 4 : lane), kIsWide ? 1 : 32, q);
-      store_quad<BITS, kIsWide>(d, i, 128, q);
+      Quad q[1];
+      take_quad<BITS, kIsWide>(stage, block, d.g_bf16, shift, q[0]);
+      step_quads<BITS, 1>(r, {(uint64_t)i + (kIsWide ? lane * 4 : lane)}, kIsWide ? 1 : 32, q);
+      store_quad<BITS, kIsWide>(d, i, 128, q[0]);
     }
   };
   if (a.kind == kWide) return whole(std::true_type());
@@ -525,10 +576,10 @@ __device__ __forceinline__ void linear_stage(const AdamwEntry& d, const Rates& r
 #pragma unroll 1
   for (uint32_t block = warp; block * 128 < a.left; block += kWarps) {
     const int64_t i = a.base + block * 128;
-    Quad q;
-    load_quad<BITS>(d, i, a.left - block * 128, q);
-    step_quad<BITS>(r, i + lane, 32, q);
-    store_quad<BITS, false>(d, i, a.left - block * 128, q);
+    Quad q[1];
+    load_quad<BITS>(d, i, a.left - block * 128, q[0]);
+    step_quads<BITS, 1>(r, {(uint64_t)i + lane}, 32, q);
+    store_quad<BITS, false>(d, i, a.left - block * 128, q[0]);
   }
 }
 
@@ -543,6 +594,9 @@ __device__ __forceinline__ Rates rates_of(const AdamwCommon& c) {
     r.rate = c.rates->rate, r.root = c.rates->root, r.key = c.rates->key, r.lr = c.rates->lr;
   }
   r.keep = 1.0f;
+  const bool usual = r.eps <= kMostEps && (r.rate == 0.0f || fabsf(r.rate) >= kLeastRate);
+  r.low = usual ? kLeastMoment : INFINITY;
+  r.raised = -r.rate * kLower;
   return r;
 }
 __device__ __forceinline__ Rates rates_for(const Rates& all, const AdamwCommon& c,
@@ -928,12 +982,13 @@ __global__ void __launch_bounds__(kSlabThreads, kSlabPer) adamw_slab_kernel(
         if (edge & 1) most[0] = most[1] = most[2] = most[3] = 0.0f;
         constexpr int kEach = kRows / kWarps;      // rows past the last: zeros, worked on for nothing
         Quad q[kEach];
+        uint64_t place[kEach];
 #pragma unroll
-        for (int i = 0; i < kEach; ++i)
+        for (int i = 0; i < kEach; ++i) {
           take_quad<BITS, true>(stage, i * kWarps + warp, a.d.g_bf16, none, q[i]);
-#pragma unroll
-        for (int i = 0; i < kEach; ++i)
-          step_quad<BITS>(rates, base + (int64_t)(i * kWarps + warp) * N + lane * 4, 1, q[i]);
+          place[i] = base + (int64_t)(i * kWarps + warp) * N + lane * 4;
+        }
+        step_quads<BITS, kEach>(rates, place, 1, q);
 #pragma unroll
         for (int i = 0; i < kEach; ++i) {
           const uint32_t row = i * kWarps + warp;

@@ -499,8 +499,10 @@ int fp8moe_router_bwd(const float* dweights, const void* logits, const int32_t* 
  *   m = beta1 m + (1 - beta1) g,   v = beta2 v + (1 - beta2) g^2
  *   p = p (1 - lr weight_decay) - lr / (1 - beta1^t) * m / (sqrt(v) / sqrt(1 - beta2^t) + eps)
  * p is f32 (master weights), g bf16 or f32. Every operation is rounded to f32 by itself (root and
- * quotient to the nearest, but for about one in 2^22 that lies next to the middle of two values): a
- * step has one result, which does not depend on what else is in the call.
+ * quotient to the nearest, but for about one in 2^22 that lies next to the middle of two values; a
+ * quotient below 2^-126 may keep more bits than f32 has there): a step has one result for a value,
+ * which depends neither on its neighbours (but for those in the block of an 8-bit moment), nor on
+ * where its tensor lies, nor on what else is in the call.
  *
  * Moments are f32 (state_bits = 32), or (8) e4m3 codes of m and of sqrt(v) with an f32 scale for
  * each 128 consecutive values (the last block may be shorter): scale = largest magnitude / 448,
