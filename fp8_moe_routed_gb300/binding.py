@@ -917,7 +917,7 @@ class AdamwPlan:
     [E, K, N]. Each is a list as long as params, with None where a param has none, or None.
     weight_decay: a number or one for each param. The plan keeps the tensors' memory: where one of
     them has other memory than it had (its data replaced, or grown), adamw_step refuses the plan;
-    a new one takes 3 to 7 us a param."""
+    a new one takes 4 to 10 us a param."""
 
     def __init__(self, params, m, v, m_scales=None, v_scales=None, copies=None, codes=None,
                  code_scales=None, weight_decay=0.0):
@@ -999,11 +999,19 @@ class AdamwPlan:
         self._indices = [index] * count
         self._numels = array.array("Q", [p.numel() for p in self.params])
         self._columns = memoryview(self._table).cast("B").cast("Q") if count else None
+        # what a backward pass may have kept, and autograd is told of: weights and what is made of
+        # them, by the tensors whose version counters they share, one for a tensor's views
+        made = [[p, copies[i], codes[i], code_scales[i]] for i, p in enumerate(self.params)]
+        made = [[t if t._base is None else t._base for t in ts
+                 if t is not None and not t.is_inference()] for ts in made]
+        self._made = made
+        self._all_made = list({id(t): t for ts in made for t in ts}.values())
         self._type = None                       # of all gradients in the table
         self._lock = threading.Lock()           # the table is one call's until the library read it
 
     def _enter(self, grads):
-        """Writes the gradients' addresses and types into the table."""
+        """Writes the gradients' addresses and types into the table; returns it, its length, and
+        the tensors whose versions the step raises."""
         count = len(self.params)
         if len(grads) != count:
             raise ValueError(f"grads must have one entry for each of the {count} params")
@@ -1026,10 +1034,11 @@ class AdamwPlan:
                     for e in table[:count]:
                         e.g_type = TYPES[types[0]]
                     self._type = types[0]
-                return table, count
+                return table, count, self._all_made
         except (AttributeError, TypeError):     # something is no tensor
             pass
         self._type = None
+        made = {}
         for i, g in enumerate(grads):
             e = table[i]
             if g is None:                       # no gradient: the param is left as it is
@@ -1046,7 +1055,8 @@ class AdamwPlan:
                 _shaped(g, g.dtype, f"gradient {i}", tuple(self._shapes[i]))
                 raise ValueError(f"gradient {i} must be on {dev}, got {g.device}")
             e.g, e.g_type, e.n = g.data_ptr(), ty, g.numel()
-        return table, count
+            made.update((id(t), t) for t in self._made[i])
+        return table, count, list(made.values())
 
 
 def adamw_step(plan: AdamwPlan, grads, step, lr, beta1: float = 0.9, beta2: float = 0.999,
@@ -1055,7 +1065,8 @@ def adamw_step(plan: AdamwPlan, grads, step, lr, beta1: float = 0.9, beta2: floa
     None leaves the param and its states as they are) (see fp8moe_adamw_step). step: the number
     of this step, from 1, or an int64 CUDA tensor [1]; lr: a number or an f32 CUDA tensor [1] (what
     a captured step reads when it is replayed). grad_scale: f32 CUDA tensor [1] that every gradient
-    is multiplied by, or None. seed: of the rounding of 8-bit moments."""
+    is multiplied by, or None. seed: of the rounding of 8-bit moments. Autograd sees params, copies
+    and codes as changed in place."""
     L = load()
     if not plan.params:
         return
@@ -1073,7 +1084,7 @@ def adamw_step(plan: AdamwPlan, grads, step, lr, beta1: float = 0.9, beta2: floa
     if workspace is not None and not (workspace.is_cuda and workspace.is_contiguous()):
         raise ValueError("workspace must be a contiguous CUDA tensor")
     with plan._lock:
-        table, count = plan._enter(grads)
+        table, count, made = plan._enter(grads)
         need = int(L.fp8moe_adamw_workspace_size(table, count,
                                                  step_dev is not None or lr_dev is not None))
         if workspace is None and need:
@@ -1083,6 +1094,7 @@ def adamw_step(plan: AdamwPlan, grads, step, lr, beta1: float = 0.9, beta2: floa
                                    _ptr(lr_dev), beta1, beta2, eps, _ptr(grad_scale),
                                    seed & 0xFFFFFFFF, _ptr(workspace), wsb, _stream(dev)),
                "fp8moe_adamw_step")
+        torch.autograd.graph.increment_version(made)
 
 
 def read_status(device=None) -> int:

@@ -1,4 +1,5 @@
-"""What a plan of the AdamW step notices: memory that a tensor of its list no longer has."""
+"""What a plan of the AdamW step notices: memory that a tensor of its list no longer has; and what
+autograd notices of a step."""
 import pytest
 import torch
 
@@ -58,3 +59,69 @@ def test_memory_that_was_replaced_is_refused(name, how):
         fb.adamw_step(plan, [grads()[0], None], step=2, lr=1e-3)
     for k, x in t.items():
         assert torch.equal(x, before[k]), k
+
+
+def test_autograd_sees_that_weights_changed():
+    """A weight, copy or codes that a backward pass still needs: the pass ends in an error, as it
+    does after any other change in place, not in the gradient of other weights."""
+    t = tensors()
+    plan = plan_of(t)
+    p = t["p"].requires_grad_()
+    x = torch.randn(K, N, device="cuda", requires_grad=True)
+
+    class Scaled(torch.autograd.Function):
+        @staticmethod
+        def forward(ctx, x, w):
+            ctx.save_for_backward(w)
+            return x * w.float()[0]
+
+        @staticmethod
+        def backward(ctx, d):
+            w, = ctx.saved_tensors
+            return d * w.float()[0], None
+
+    for make in (lambda: (x * p[0]).sum(), lambda: Scaled.apply(x, t["copies"]).sum(),
+                 lambda: Scaled.apply(x, t["codes"]).sum(),
+                 lambda: Scaled.apply(x[0], t["code_scales"]).sum()):
+        loss = make()
+        fb.adamw_step(plan, grads(), step=1, lr=1e-3)
+        with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+            loss.backward()
+        make().backward()                          # and a new pass is fine
+
+
+def test_what_a_step_leaves_alone_keeps_its_version():
+    """A param without a gradient is not changed, and a refused step changes nothing."""
+    t = tensors()
+    plan = plan_of(t)
+    before = {k: x._version for k, x in t.items()}
+    fb.adamw_step(plan, [None, grads()[1]], step=1, lr=1e-3)
+    with pytest.raises(ValueError):
+        fb.adamw_step(plan, grads()[:1], step=1, lr=1e-3)
+    with pytest.raises(fb.Fp8MoeError):
+        fb.adamw_step(plan, grads(), step=0, lr=1e-3)
+    assert {k: x._version for k, x in t.items()} == before
+    fb.adamw_step(plan, [grads()[0], None], step=1, lr=1e-3)
+    assert all(t[k]._version > before[k] for k in ("p", "copies", "codes", "code_scales"))
+
+
+def test_parts_of_one_buffer():
+    """Params that are views of one tensor share its version; a step in inference mode has none."""
+    flat = torch.ones(30, device="cuda", requires_grad=True)
+    with torch.no_grad():
+        parts = list(torch.split(flat, [10, 20]))
+    zeros = lambda: [torch.zeros(n, device="cuda") for n in (10, 20)]  # noqa: E731
+    plan = fb.AdamwPlan(parts, zeros(), zeros())
+    loss = (flat * flat).sum()
+    before = flat._version
+    fb.adamw_step(plan, zeros(), step=1, lr=1e-3)
+    assert flat._version == before + 1
+    with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+        loss.backward()
+    with torch.inference_mode():
+        p = torch.ones(10, device="cuda")
+        plan = fb.AdamwPlan([p], [torch.zeros_like(p)], [torch.zeros_like(p)], weight_decay=0.5)
+        fb.adamw_step(plan, [torch.zeros_like(p)], step=1, lr=1.0)
+        assert p.tolist() == [0.5] * 10
+    fb.adamw_step(plan, [torch.zeros(10, device="cuda")], step=2, lr=1.0)
+    assert p.tolist() == [0.25] * 10
