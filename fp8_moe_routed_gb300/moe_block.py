@@ -146,10 +146,11 @@ class Trainer:
         self.scales, self.seed, self.steps = scales, seed, 0
 
     def step(self, grads: dict, lr: float, grad_scale=None) -> None:
-        """One AdamW step for the gradients of backward and choose_backward."""
-        self.steps += 1
-        fb.adamw_step(self.plan, [grads[k] for k in self.names], step=self.steps, lr=lr,
+        """One AdamW step for the gradients of backward and choose_backward. A step that is refused
+        is not counted."""
+        fb.adamw_step(self.plan, [grads[k] for k in self.names], step=self.steps + 1, lr=lr,
                       grad_scale=grad_scale, seed=self.seed)
+        self.steps += 1
 
 
 def train_step(p: Params, router: Router, trainer: Trainer, x, h, dr, dh_next, lr: float,
