@@ -144,10 +144,22 @@ class Trainer:
                                  code_scales=[p.wi[1], p.wo[1]] + none,
                                  weight_decay=[weight_decay] * 3 + [0.0] * (n - 3))
         self.scales, self.seed, self.steps = scales, seed, 0
+        self.p, self.router, self.held = p, router, self._weights(p, router)
+
+    @staticmethod
+    def _weights(p: Params, router: Router) -> dict:
+        """What the block and its router take, by name."""
+        return {"wi": p.wi[0], "the scales of wi": p.wi[1], "wo": p.wo[0],
+                "the scales of wo": p.wo[1], "w_post": p.w_post, "w_pre": p.w_pre, "gate": p.gate,
+                "the router's w": router.w}
 
     def step(self, grads: dict, lr: float, grad_scale=None) -> None:
         """One AdamW step for the gradients of backward and choose_backward. A step that is refused
-        is not counted."""
+        is not counted; one is refused if the block or its router have other weights than at the
+        start, as they would stay as they are."""
+        for name, t in self._weights(self.p, self.router).items():
+            if t is not self.held[name]:
+                raise ValueError(f"{name} was replaced: make a new Trainer")
         fb.adamw_step(self.plan, [grads[k] for k in self.names], step=self.steps + 1, lr=lr,
                       grad_scale=grad_scale, seed=self.seed)
         self.steps += 1

@@ -1,4 +1,4 @@
-"""The block's trainer around a step that is refused."""
+"""The block's trainer around a step that is refused, and around weights that were replaced."""
 import pytest
 import torch
 
@@ -45,3 +45,36 @@ def test_a_refused_step_is_not_counted(made, monkeypatch):
     assert trainer.steps == 1
     trainer.step(grads, lr=1e-3)
     assert calls == [1, 2] and trainer.steps == 2
+
+
+@pytest.mark.parametrize("name", ["wi", "wo", "w_post", "w_pre", "gate", "router"])
+def test_replaced_weights_are_refused(made, name):
+    """Weights that the block takes from now on and that the trainer does not hold would stay as
+    they are while it steps others."""
+    p, router, trainer, grads, calls = made
+    if name == "router":
+        router.w = router.w.clone()
+    elif name in ("wi", "wo"):
+        setattr(p, name, mb.fp8_weight(torch.randn(getattr(p, name)[0].shape)))
+    else:
+        setattr(p, name, getattr(p, name).clone())
+    with pytest.raises(ValueError, match="replaced"):
+        trainer.step(grads, lr=1e-3)
+    assert trainer.steps == 0 and not calls
+
+
+def test_a_gate_that_is_gone_is_refused(made):
+    p, router, trainer, grads, calls = made
+    p.gate = None
+    with pytest.raises(ValueError, match="gate was replaced"):
+        trainer.step(grads, lr=1e-3)
+    assert not calls
+
+
+def test_the_same_weights_in_a_new_pair(made):
+    """A pair is only a pair: its tensors are what counts, and a bias of the choice is no weight."""
+    p, router, trainer, grads, calls = made
+    p.wi = (p.wi[0], p.wi[1])
+    router.bias = torch.ones_like(router.bias)
+    trainer.step(grads, lr=1e-3)
+    assert calls == [1]
