@@ -961,7 +961,7 @@ class AdamwPlan:
             self._kept.append(t.untyped_storage())
             self._tensors.append(t)
             self._addresses.append(at)
-            self._names.append(f"{name} {i}")
+            self._names.append((name, i))
 
         for i, p in enumerate(self.params):
             if not isinstance(p, torch.Tensor):
@@ -1001,11 +1001,13 @@ class AdamwPlan:
         self._columns = memoryview(self._table).cast("B").cast("Q") if count else None
         # what a backward pass may have kept, and autograd is told of: weights and what is made of
         # them, by the tensors whose version counters they share, one for a tensor's views
-        made = [[p, copies[i], codes[i], code_scales[i]] for i, p in enumerate(self.params)]
-        made = [[t if t._base is None else t._base for t in ts
-                 if t is not None and not t.is_inference()] for ts in made]
-        self._made = made
-        self._all_made = list({id(t): t for ts in made for t in ts}.values())
+        self._made = [[t if (base := t._base) is None else base for t in ts if t is not None]
+                      for ts in zip(self.params, copies, codes, code_scales)]
+        made = {id(t): t for ts in self._made for t in ts}
+        if any(map(torch.Tensor.is_inference, made.values())):      # these have no counters
+            self._made = [[t for t in ts if not t.is_inference()] for ts in self._made]
+            made = {id(t): t for ts in self._made for t in ts}
+        self._all_made = list(made.values())
         self._type = None                       # of all gradients in the table
         self._lock = threading.Lock()           # the table is one call's until the library read it
 
@@ -1016,9 +1018,9 @@ class AdamwPlan:
         if len(grads) != count:
             raise ValueError(f"grads must have one entry for each of the {count} params")
         if not _addresses_equal(self._tensors, self._addresses, self._places):
-            for t, at, name in zip(self._tensors, self._addresses, self._names):
+            for t, at, (name, i) in zip(self._tensors, self._addresses, self._names):
                 if t.data_ptr() != at:
-                    raise ValueError(f"the storage of {name} was replaced: make a new plan")
+                    raise ValueError(f"the storage of {name} {i} was replaced: make a new plan")
         table, dev = self._table, self.device
         try:                                    # the usual case, column by column
             types = [g.dtype for g in grads]
