@@ -544,9 +544,9 @@ __device__ __forceinline__ void store_quad(const AdamwEntry& d, int64_t i, uint3
 }
 
 // A working warp's blocks of a stage of a linear unit. 60 million values with a bf16 copy: f32
-// gradients and 8-bit moments in one tensor 178 us (0.90 of the copy rate), in 300 tensors at odd
-// addresses 202 (0.79: byte and word accesses, 73 % of the issue slots); bf16 gradients and 32-bit
-// moments in 300 tensors 269 (0.92). With loads straight into registers these took 465, 465 and 372.
+// gradients and 8-bit moments in one tensor 175 us (0.92 of the copy rate), in 300 tensors at odd
+// addresses 208 (0.77: byte and word accesses, 68 % of the issue slots); bf16 gradients and 32-bit
+// moments in 300 tensors 271 (0.92). With loads straight into registers these took 465, 465 and 372.
 template <int BITS>
 __device__ __forceinline__ void linear_stage(const AdamwEntry& d, const Rates& r, const Desc& a,
                                              const uint8_t* stage) {
@@ -685,7 +685,11 @@ __global__ void adamw_prepare_kernel(AdamwRates* rates, const int64_t* step, int
   for (int64_t j = i; j < count; j += (int64_t)gridDim.x * blockDim.x) most[j] = 0u;
 }
 
-// The columns' largest magnitudes of weights [E, K, N], where the step's units are not tiles.
+// The columns' largest magnitudes of weights [E, K, N], where the step's units are not tiles: 8-bit
+// moments whose blocks cross rows (N no multiple of 128), or arrays off 16 bytes. This kernel and the
+// next but one read the weights again, value by value: 16 x 2880 x 2880 weights with 8-bit moments
+// 586 us (0.57 of the copy rate for the bytes that have to move), 16 x 2880 x 2944 by tiles 477
+// (0.72); off 16 bytes 633 and 644, with 32-bit moments 787 for 601.
 __global__ void __launch_bounds__(32 * kWarps) column_max_kernel(const float* p, int K, int N,
                                                               uint32_t* most) {
   __shared__ uint32_t s_most[kWarps * kTileCols];
@@ -787,7 +791,7 @@ __global__ void __launch_bounds__(32 * kWarps) weight_codes_kernel(const float* 
 // whatever else runs, and as two slabs have as many tiles as CTAs can have taken, it hardly ever
 // begins. 8 x 7168 x 4096 and 8 x 2048 x 7168 weights, 32-bit moments: 1607 us (6.36 TB/s of the
 // bytes that have to move), bound by memory; two kernels one after the other, 1796; slabs by a
-// launch each, 1701. 8-bit moments: 1201 us, bound by instructions (97 a value, 69 % of the issue
+// launch each, 1701. 8-bit moments: 1224 us, bound by instructions (96 a value, 65 % of the issue
 // slots); 2153 at first, with the same arithmetic one value at a time.
 // Waits until a slab's tiles are done; false (and a status bit) after two seconds.
 __device__ __forceinline__ bool wait_slab(const uint32_t* done, uint32_t tiles) {

@@ -8,9 +8,10 @@
 //
 // A warp takes a token, its logits in registers, so that one pass over them gives the maximum, the
 // sum, the choice and the shares. Bytes are nothing to it: 4096 tokens of 256 f32 logits with a bias
-// (0.66 us of bytes) take 9.7 us for the choice and 16.1 with the balance loss, which is a token's
-// chain of dependent steps and about 900 instructions; one token takes 4.1 us, most of it the
-// launch's. 32768 tokens of 512 logits with given choices 21.7 us (3.1 TB/s), bound by the
+// (0.66 us of bytes) take 9.7 us for the choice and 16.3 with the balance loss: one wave, so that it
+// is the chain of a token's dependent steps (about 900 instructions; k rounds of a maximum over the
+// lanes; with the 64 registers of four CTAs, 176 bytes of spills) and the join. One token takes
+// 4.1 us, most of it the launch's. 32768 tokens of 512 logits with given choices 21.7 us (3.1 TB/s), bound by the
 // instructions of the scores.
 #include <cmath>
 #include <cstdint>

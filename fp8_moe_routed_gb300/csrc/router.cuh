@@ -17,10 +17,11 @@ constexpr int kWarps = 8;
 constexpr int kThreads = 32 * kWarps;
 
 // Many tokens, at most 128 experts, at most 8 chosen, and no bias: eight lanes take a token, so that
-// an instruction works for four. A choice (65536 tokens, 128 experts, bf16, with the balance loss)
-// takes 31 us then and 77 by a warp for a token; of 4096 tokens 9.7 and 11.1, of 2048 8.8 both. With
-// a bias more tokens have to be settled one by one (f32, 65536: 66 and 63 us), and 256 experts
-// take so many registers that an SM has one CTA (f32, 32768: 66 and 40; the gradient 57 and 37).
+// an instruction works for four. A choice of 65536 tokens (128 experts, bf16, with the balance loss)
+// takes 25.0 us then and 46.8 by a warp for a token, of 4096 tokens 7.8 and 10.5, of 2048 7.4 and
+// 8.0; its gradient 16.5 and 25.0, 4.1 and 4.3, and 3.9 and 3.5. Versions of this kernel with a bias
+// had more tokens to settle one by one (f32, 32768 tokens: 51 us, by a warp 36), and with 256 experts
+// so many registers that an SM had one CTA (f32, 32768: 66 and 40; the gradient 57 and 37).
 constexpr int64_t kManyTokens = 4096;
 constexpr int kGroup = 8, kGroups = 4;
 inline bool by_groups(int64_t T, int E, int k, bool bias) {
@@ -143,7 +144,8 @@ __device__ __forceinline__ float clamp_nan(float x, float limit) {
 }
 
 // exp(x) for x <= 0 (and NaN), two at a time: by the exponential unit (within 2^-22 of itself) on x
-// times log2 e, with what the product's rounding and the constant's lose put back to first order.
+// times log2 e, with what the product's rounding and the constant's lose put back to first order:
+// hi is the f32 nearest to log2 e, lo the one nearest to log2 e - hi.
 // Within 6 * 2^-24; 0 below 2^-126.
 __device__ __forceinline__ float2 exp_neg(float2 x) {
   const float hi = 1.4426950216293335f, lo = 1.9259629911266175e-8f, ln2 = 0.6931471805599453f;

@@ -1,8 +1,10 @@
 // router_group.cu -- the router's choice without a bias, and the balance sums, for many tokens
-// (router.cuh): eight lanes take a token, lane l of a group holds experts [l V, l V + V). What is as
-// in router.cu is not explained again; a token whose border is not settled by the keys' upper 22 bits
-// is chosen by the whole warp in choose_exactly. 65536 tokens of 128 bf16 logits: 19.5 us for the
-// choice, 25.0 with the balance loss (0.8 TB/s), bound by instructions: 194 a token, 630 by a warp.
+// (router.cuh): eight lanes take a token, each of them pieces of a row that follow the other lanes'
+// (Row::expert). What is as in router.cu is not explained again; a token whose border is not settled
+// by the keys' upper 22 bits is chosen by the whole warp in choose_exactly. 65536 tokens of 128 bf16
+// logits: 19.5 us for the choice, 25.0 with the balance loss (0.8 TB/s), at half of the issue slots
+// (194 instructions a token, 630 by a warp): eight rounds of three dependent shuffles, with 16 warps
+// on an SM to hide them.
 #include <cmath>
 #include <cstdint>
 #include <cuda_runtime.h>

@@ -534,12 +534,12 @@ typedef struct fp8moe_adamw_tensor {
 } fp8moe_adamw_tensor;
 
 /* `tensors` is a HOST array of `count` entries, read during the call (its pointers are device
- * pointers); no two entries may overlap. Values need the alignment of their type only. t: `step`
- * >= 1, or *step_dev (int64 on the device, NULL: `step`); the rate: `lr`, or *lr_dev (f32 on the
- * device, NULL: `lr`): a captured step follows what they hold when it is replayed. grad_scale: f32
- * on the device or NULL. 0 <= beta < 1, eps >= 0 (with 0 a value that never had a gradient becomes
- * NaN). Workspace: fp8moe_adamw_workspace_size (256-byte aligned), with on_device = 1 if step_dev or
- * lr_dev is given; calls that overlap on the GPU need one each. */
+ * pointers); no two entries may overlap, nor may a gradient overlap what a step writes. Values need
+ * the alignment of their type only. t: `step` >= 1, or *step_dev (int64 on the device, NULL: `step`);
+ * the rate: `lr`, or *lr_dev (f32 on the device, NULL: `lr`): a captured step follows what they hold
+ * when it is replayed. grad_scale: f32 on the device or NULL. 0 <= beta < 1, eps >= 0 (with 0 a value
+ * that never had a gradient becomes NaN). Workspace: fp8moe_adamw_workspace_size (256-byte aligned),
+ * with on_device = 1 if step_dev or lr_dev is given; calls that overlap on the GPU need one each. */
 size_t fp8moe_adamw_workspace_size(const fp8moe_adamw_tensor* tensors, int32_t count,
                                    int32_t on_device);
 int fp8moe_adamw_step(const fp8moe_adamw_tensor* tensors, int32_t count, int64_t step,
