@@ -363,10 +363,12 @@ __device__ __forceinline__ float rcp_approx(float x) {
 // on the values beside it: second moments in [2^-100, 2^36], whose roots' remainders are exact;
 // first moments up to 2^36, raised by 2^40 for the quotient and lowered again by the rate, so that
 // the quotient's remainder is exact for the smallest ones, too (one whose gradient stopped falls
-// below 2^-100 long before its second moment; 2 % of the time of 8-bit moments). The divisors are in [2^-50, 2^46] then (1 / sqrt(1 -
-// b2^t) is at most 2^27, as b2 is a double below 1; kMostEps), the quotients below 2^126.
+// below 2^-100 long before its second moment; 2 % of the time of 8-bit moments). The divisors are in
+// [2^-50, 2^46] then (kMostFactor, kMostEps), the quotients below 2^126.
 constexpr float kLeastMoment = 0x1p-100f, kMostMoment = 0x1p36f, kMostRoot = 0x1p18f;
 constexpr float kMostEps = 0x1p20f;
+// 1 / sqrt(1 - b2^t) for any b2 below 1, unless the power comes out as 1
+constexpr float kMostFactor = 0x1p27f;
 constexpr float kRaise = 0x1p40f, kLower = 0x1p-40f;
 constexpr float kLeastRate = 0x1p-60f;           // a smaller one would not be normal when lowered
 __device__ __forceinline__ float2 sqrt2(float2 x) {
@@ -594,7 +596,8 @@ __device__ __forceinline__ Rates rates_of(const AdamwCommon& c) {
     r.rate = c.rates->rate, r.root = c.rates->root, r.key = c.rates->key, r.lr = c.rates->lr;
   }
   r.keep = 1.0f;
-  const bool usual = r.eps <= kMostEps && (r.rate == 0.0f || fabsf(r.rate) >= kLeastRate);
+  const bool usual = r.eps <= kMostEps && r.root <= kMostFactor &&
+                     (r.rate == 0.0f || fabsf(r.rate) >= kLeastRate);
   r.low = usual ? kLeastMoment : INFINITY;
   r.raised = -r.rate * kLower;
   return r;

@@ -65,16 +65,17 @@ def test_one_result_wherever_a_tensor_lies(bits):
             assert differ(a, b) == 0, (place, name, differ(a, b))
 
 
-def step_of(m, v, g=None, **hyper):
+def step_of(m, v, g=None, step=1000, on_device=False, **hyper):
     """New weights and moments of weights of zero, on the GPU and by the reference."""
     n = len(m)
     h = {**HYPER, **hyper}
     g = np.zeros(n, F) if g is None else g
     t = [torch.from_numpy(a.copy()).cuda() for a in (np.zeros(n, F), g, m, v)]
     plan = fb.AdamwPlan([t[0]], [t[2]], [t[3]])
-    fb.adamw_step(plan, [t[1]], step=1000, **h)
+    at = torch.tensor([step], device="cuda") if on_device else step
+    fb.adamw_step(plan, [t[1]], step=at, **h)
     with np.errstate(all="ignore"):
-        want = ref.adamw(np.zeros(n, F), g, m, v, 1000, decay=0.0, **h)
+        want = ref.adamw(np.zeros(n, F), g, m, v, step, decay=0.0, **h)
     return [x.cpu().numpy() for x in (t[0], t[2], t[3])], want
 
 
@@ -103,6 +104,34 @@ def test_large_eps(eps):
     v = np.square(rng.uniform(1e-4, 1e-2, n)).astype(F)
     got, want = step_of(m, v, eps=eps)
     assert off(got[0], want[0]) == 0
+
+
+@pytest.mark.parametrize("on_device", [False, True])
+@pytest.mark.parametrize("hyper", [dict(lr=1e-30), dict(lr=0.0), dict(lr=-3e-4), dict(lr=1e30),
+                                   dict(beta1=0.0), dict(beta2=0.0), dict(eps=0.0),
+                                   dict(beta2=1 - 2.0 ** -40, step=1), dict(beta1=1 - 2.0 ** -20, step=1)])
+def test_rates_at_their_ends(hyper, on_device):
+    """Rates that vanish or are huge, factors of a moment's correction at the ends of their range."""
+    n = 2 ** 12
+    rng = np.random.default_rng(4)
+    m, g = (rng.standard_normal(n) * 1e-3).astype(F), (rng.standard_normal(n) * 1e-2).astype(F)
+    v = np.square(rng.uniform(1e-4, 1e-2, n)).astype(F)
+    got, want = step_of(m, v, g, on_device=on_device, **hyper)
+    # a power in 64 bits, within two units of itself on the GPU, is the whole of 1 - b^t's error
+    if on_device and "step" in hyper:
+        rel = 4 * 2.0 ** -53 / (1 - hyper.get("beta1", hyper.get("beta2"))) + 8 * 2.0 ** -24
+        assert (np.abs(got[0] - want[0]) <= rel * np.abs(want[0])).all()
+    else:
+        assert off(got[0], want[0]) == 0
+    assert off(got[1], want[1]) == off(got[2], want[2]) == 0
+
+
+def test_a_correction_without_end():
+    """A beta2 whose power is 1 to 64 bits, or next to it: finite weights, whatever pow() says."""
+    m, v = np.full(256, 1e-3, F), np.full(256, 1e-4, F)
+    for on_device in (False, True):
+        got, _ = step_of(m, v, on_device=on_device, step=1, beta2=1 - 2.0 ** -53)
+        assert np.isfinite(got[0]).all()
 
 
 def test_far_values_among_ordinary_ones():
