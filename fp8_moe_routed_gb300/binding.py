@@ -917,7 +917,7 @@ class AdamwPlan:
     [E, K, N]. Each is a list as long as params, with None where a param has none, or None.
     weight_decay: a number or one for each param. The plan keeps the tensors' memory: where one of
     them has other memory than it had (its data replaced, or grown), adamw_step refuses the plan;
-    a new one takes 4 to 10 us a param."""
+    a new one takes 4 to 8 us a param."""
 
     def __init__(self, params, m, v, m_scales=None, v_scales=None, copies=None, codes=None,
                  code_scales=None, weight_decay=0.0):
